@@ -66,6 +66,28 @@ SIGNATURES = {
     "fmpq_plan_layout": (_I32, [_I32, _P, _I32, _P, _P]),
     "fmpq_plan_layout_budget": (_I32, [_I32, _P, _P, _I64, _I64, ctypes.c_double, _P, _P, _P, _P]),
     "fmpq_outlier_blocks": (_I32, [_I32, ctypes.c_double]),
+    "fp8_layer_create": (_I32, [_I32, _I32, _I32, _I32, ctypes.POINTER(_P)]),
+    "fp8_layer_destroy": (None, [_P]),
+    "fp8_device_status": (_I32, [_P, ctypes.POINTER(_I32), _I32]),
+    "fp8_packed_w_bytes": (_SZ, [_P]),
+    "fp8_weight_scale_count": (_SZ, [_P]),
+    "fp8_packed_a_bytes": (_SZ, [_P, _I64]),
+    "fp8_a_scale_count": (_SZ, [_P, _I64]),
+    "fp8_pack_weights": (_I32, [_P, _I32, _P, _I32, _I64, _P, _P, _P]),
+    "fp8_pack_codes": (_I32, [_P, _I32, _P, _I64, _P, _P]),
+    "fp8_unpack_weights": (_I32, [_P, _I32, _P, _P, _P, _P]),
+    "fp8_quantize": (_I32, [_P, _P, _I32, _I64, _I64, _P, _P, _P]),
+    "fp8_gemm_workspace_bytes": (_SZ, [_P, _I64]),
+    "fp8_gemm": (_I32, [_P, _P, _P, _P, _P, _I64, _P, _I32, _I64, _P, _SZ, _P]),
+    "fp8_quantize_gemm": (_I32, [_P, _P, _I32, _I64, _I64, _P, _P, _P, _P, _P, _I64, _P, _SZ, _P]),
+    "moe_route": (_I32, [_P, _I32, _I64, _I64, _I32, _I32, _I32, _P, _I32, _I32, _I32, _I32, ctypes.c_float, _P, _P, _P]),
+    "moe_rows": (_I64, [_I64, _I32, _I32]),
+    "moe_plan_bytes": (_SZ, [_I64, _I32, _I32]),
+    "moe_plan": (_I32, [_P, _I64, _I32, _I32, _P, _P]),
+    "moe_quantize": (_I32, [_P, _P, _I64, _I32, _P, _I32, _I64, _P, _P, _P]),
+    "moe_up": (_I32, [_P, _P, _I64, _I32, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_down": (_I32, [_P, _P, _I64, _I32, _P, _P, _P, _P, _P, _P, _I32, _I64, _P]),
+    "moe_combine": (_I32, [_P, _I32, _I64, _P, _I64, _I32, _I32, _I32, _P, _I64, _P]),
     "fmpq_status_string": (ctypes.c_char_p, [_I32]),
     "fmpq_version": (_I32, []),
 }
@@ -551,3 +573,336 @@ def qoq_gemm_partials(layout: Layout, A_packed, W_packed, M: int, N: int, m0: in
     _check("qoq_gemm_partials", layout._lib.qoq_gemm_partials(layout.handle, _ptr(A_packed), _ptr(W_packed), M, N,
                                                                 m0, mcount, n0, ncount, _ptr(P), _stream(stream)))
     return P
+
+
+# ---- E4M3 linear layers: a scale for each block of 128 ------------------------------------
+
+def _dtype_code(t) -> int:
+    import torch
+    codes = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+    if t not in codes:
+        raise ValueError(f"unsupported dtype {t}")
+    return codes[t]
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _rows16(X, what: str):
+    """A 16-bit CUDA matrix whose rows are contiguous (any row stride)."""
+    import torch
+    _need(X.is_cuda and X.dim() == 2 and X.dtype in (torch.float16, torch.bfloat16),
+          f"{what} must be a 2-D fp16 or bf16 CUDA tensor")
+    _need(X.shape[1] <= 1 or X.stride(1) == 1, f"{what} must have contiguous rows")
+
+
+def _ld(X) -> int:
+    """Row stride in elements (a single row may have any)."""
+    return max(X.stride(0), X.shape[1]) if X.shape[0] > 1 else X.shape[1]
+
+
+class Fp8Layer:
+    """Owns an fp8_layer*: `experts` E4M3 weight matrices [N, K] with 128 x 128 block scales (one: a
+    linear layer); gated: N = 2F rows, F gate rows then F up rows (for moe_up)."""
+
+    def __init__(self, K: int, N: int, experts: int = 1, gated: bool = False):
+        lib = load_library()
+        h = ctypes.c_void_p()
+        _check("fp8_layer_create", lib.fp8_layer_create(K, N, experts, int(gated), ctypes.byref(h)))
+        self._h = h
+        self._lib = lib
+        self.K, self.N, self.experts, self.gated = K, N, experts, bool(gated)
+        self.nb = -(-K // BLOCK)
+        self.scale_rows = 2 * -(-(N // 2) // BLOCK) if gated else -(-N // BLOCK)
+        self._workspaces = {}
+
+    @property
+    def handle(self):
+        return self._h
+
+    def close(self):
+        if getattr(self, "_h", None) is not None and self._h.value:
+            self._lib.fp8_layer_destroy(self._h)
+            self._h = ctypes.c_void_p()
+        self._workspaces = {}
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def packed_w_bytes(self) -> int:
+        return int(self._lib.fp8_packed_w_bytes(self._h))
+
+    def activations(self, rows: int, device):
+        """Buffers for `rows` rows of quantized activations: codes uint8 [nb, rows, 128] (swizzled) and
+        scales fp32 [nb, rows rounded up to 4]."""
+        import torch
+        return (torch.empty((self.nb, rows, BLOCK), dtype=torch.uint8, device=device),
+                torch.empty((self.nb, (rows + 3) // 4 * 4), dtype=torch.float32, device=device))
+
+    def workspace(self, M: int, stream=None):
+        """fp8_gemm's workspace for M rows: zeroed, reused by later calls on the same stream; one that a
+        stream capture creates belongs to that graph alone."""
+        import torch
+        nbytes = int(self._lib.fp8_gemm_workspace_bytes(self._h, M))
+        if nbytes == 0:
+            return None
+        if torch.cuda.is_current_stream_capturing():
+            return torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
+        key = (nbytes, _stream(stream).value)
+        ws = self._workspaces.get(key)
+        if ws is None:
+            ws = torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
+            if stream is not None:
+                torch.cuda.current_stream().synchronize()   # zeroed before another stream uses it
+            self._workspaces[key] = ws
+        return ws
+
+
+def fp8_pack_weights(layer: Fp8Layer, W, stream=None):
+    """Quantize W (fp16 or bf16, [N, K], or [experts, N, K]) per 128 x 128 block. Returns (W_packed u8,
+    w_scales fp32 [experts, scale rows, nb])."""
+    import torch
+    W3 = W if W.dim() == 3 else W[None]
+    _need(W3.shape == (layer.experts, layer.N, layer.K), "W must be [experts, N, K] (or [N, K])")
+    Wp = torch.empty(layer.packed_w_bytes(), dtype=torch.uint8, device=W.device)
+    ws = torch.empty((layer.experts, layer.scale_rows, layer.nb), dtype=torch.float32, device=W.device)
+    for e in range(layer.experts):
+        _rows16(W3[e], "W")
+        _check("fp8_pack_weights", layer._lib.fp8_pack_weights(layer.handle, e, _ptr(W3[e]), _dtype_code(W.dtype),
+                                                               _ld(W3[e]), _ptr(Wp), _ptr(ws), _stream(stream)))
+    return Wp, ws
+
+
+def fp8_pack_codes(layer: Fp8Layer, codes, scales, stream=None):
+    """Lay out an E4M3 checkpoint: codes float8_e4m3fn (or its bytes) [experts, N, K] or [N, K], scales
+    fp32 [experts, scale rows, nb] or [scale rows, nb] (value = code * scale). Returns (W_packed u8,
+    w_scales)."""
+    import torch
+    C = codes if codes.dim() == 3 else codes[None]
+    S = scales if scales.dim() == 3 else scales[None]
+    _need(codes.dtype in (torch.float8_e4m3fn, torch.uint8) and codes.is_cuda, "codes must be float8_e4m3fn on the GPU")
+    _need(C.shape == (layer.experts, layer.N, layer.K), "codes must be [experts, N, K] (or [N, K])")
+    _need(S.shape == (layer.experts, layer.scale_rows, layer.nb) and S.dtype == torch.float32 and S.is_cuda,
+          "scales must be fp32 [experts, scale rows, blocks of K]")
+    _need(C.shape[2] <= 1 or C.stride(2) == 1, "codes must have contiguous rows")
+    Wp = torch.empty(layer.packed_w_bytes(), dtype=torch.uint8, device=codes.device)
+    for e in range(layer.experts):
+        _check("fp8_pack_codes", layer._lib.fp8_pack_codes(layer.handle, e, _ptr(C[e]), _ld(C[e]), _ptr(Wp),
+                                                           _stream(stream)))
+    return Wp, S.contiguous()
+
+
+def fp8_unpack_weights(layer: Fp8Layer, W_packed, w_scales, expert: int = 0, stream=None):
+    import torch
+    W = torch.empty((layer.N, layer.K), dtype=torch.float32, device=W_packed.device)
+    _check("fp8_unpack_weights", layer._lib.fp8_unpack_weights(layer.handle, expert, _ptr(W_packed), _ptr(w_scales),
+                                                               _ptr(W), _stream(stream)))
+    return W
+
+
+def fp8_quantize(layer: Fp8Layer, X, A_packed=None, a_scales=None, stream=None):
+    """X fp16 or bf16 [M, K], any row stride. Returns (A_packed u8, a_scales fp32), see
+    Fp8Layer.activations."""
+    _rows16(X, "X")
+    _need(X.shape[1] == layer.K, "X must be [M, K]")
+    M = X.shape[0]
+    if A_packed is None or a_scales is None:
+        A, s = layer.activations(M, X.device)
+        A_packed, a_scales = A if A_packed is None else A_packed, s if a_scales is None else a_scales
+    _check("fp8_quantize", layer._lib.fp8_quantize(layer.handle, _ptr(X), _dtype_code(X.dtype), _ld(X), M,
+                                                   _ptr(A_packed), _ptr(a_scales), _stream(stream)))
+    return A_packed, a_scales
+
+
+def _workspace_of(layer: Fp8Layer, M: int, workspace, stream):
+    if workspace is None:
+        workspace = layer.workspace(M, stream)
+    return workspace, workspace.numel() if workspace is not None else 0
+
+
+def fp8_gemm(layer: Fp8Layer, A_packed, a_scales, W_packed, w_scales, M: int, dtype=None, Y=None, workspace=None,
+             stream=None):
+    """Y [M, N] (fp16 by default) of quantized activations and packed weights."""
+    import torch
+    if Y is None:
+        Y = torch.empty((M, layer.N), dtype=dtype or torch.float16, device=A_packed.device)
+    _rows16(Y, "Y")
+    _need(Y.shape == (M, layer.N), "Y must be [M, N]")
+    workspace, nbytes = _workspace_of(layer, M, workspace, stream)
+    _check("fp8_gemm", layer._lib.fp8_gemm(layer.handle, _ptr(A_packed), _ptr(a_scales), _ptr(W_packed), _ptr(w_scales), M,
+                                           _ptr(Y), _dtype_code(Y.dtype), _ld(Y), _ptr(workspace), nbytes,
+                                           _stream(stream)))
+    return Y
+
+
+def fp8_quantize_gemm(layer: Fp8Layer, X, W_packed, w_scales, A_packed=None, a_scales=None, Y=None, workspace=None,
+                      stream=None):
+    """The layer on X (fp16 or bf16 [M, K]) in one call: Y [M, N] of X's type."""
+    import torch
+    _rows16(X, "X")
+    _need(X.shape[1] == layer.K, "X must be [M, K]")
+    M = X.shape[0]
+    if A_packed is None or a_scales is None:
+        A, s = layer.activations(M, X.device)
+        A_packed, a_scales = A if A_packed is None else A_packed, s if a_scales is None else a_scales
+    if Y is None:
+        Y = torch.empty((M, layer.N), dtype=X.dtype, device=X.device)
+    _rows16(Y, "Y")
+    _need(Y.shape == (M, layer.N) and Y.dtype == X.dtype, "Y must be [M, N] of X's type")
+    workspace, nbytes = _workspace_of(layer, M, workspace, stream)
+    _check("fp8_quantize_gemm", layer._lib.fp8_quantize_gemm(
+        layer.handle, _ptr(X), _dtype_code(X.dtype), _ld(X), M, _ptr(A_packed), _ptr(a_scales), _ptr(W_packed),
+        _ptr(w_scales), _ptr(Y), _ld(Y), _ptr(workspace), nbytes, _stream(stream)))
+    return Y
+
+
+def fp8_device_status(layer: Fp8Layer, clear: bool = True) -> int:
+    code = ctypes.c_int32(0)
+    _check("fp8_device_status", layer._lib.fp8_device_status(layer.handle, ctypes.byref(code), int(clear)))
+    return int(code.value)
+
+
+# ---- routing to experts -------------------------------------------------------------------
+
+def moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1,
+              group_top: int = 1, renormalize: bool = True, scale: float = 1.0, ids=None, weights=None, stream=None):
+    """The top-k experts of each token from the router's logits [T, E] (fp32, fp16 or bf16): ids int32
+    [T, k] (by falling key, -1: none) and weights fp32 [T, k]. score: "softmax" or "sigmoid"; bias: fp32
+    [E], added for the choice only; groups: keep the top_groups runs of E / groups experts with the
+    largest sum of their group_top best keys; renormalize: weights sum to `scale`."""
+    import torch
+    _need(score in ("softmax", "sigmoid"), "score must be 'softmax' or 'sigmoid'")
+    _need(logits.is_cuda and logits.dim() == 2, "logits must be a 2-D CUDA tensor")
+    T, E = logits.shape
+    _need(E <= 1 or logits.stride(1) == 1, "logits must have contiguous rows")
+    if bias is not None:
+        _need(bias.is_cuda and bias.dtype == torch.float32 and bias.shape == (E,) and (E == 1 or bias.stride(0) == 1),
+              "bias must be a contiguous fp32 CUDA tensor [E]")
+    ids = torch.empty((T, k), dtype=torch.int32, device=logits.device) if ids is None else ids
+    weights = torch.empty((T, k), dtype=torch.float32, device=logits.device) if weights is None else weights
+    for t, d in ((ids, torch.int32), (weights, torch.float32)):
+        _need(t.shape == (T, k) and t.dtype == d and t.is_contiguous(), "ids int32 and weights fp32 must be [T, k]")
+    _check("moe_route", load_library().moe_route(
+        _ptr(logits), _dtype_code(logits.dtype), _ld(logits), T, E, k, int(score == "sigmoid"), _ptr(bias), groups,
+        top_groups, group_top, int(renormalize), ctypes.c_float(scale), _ptr(ids), _ptr(weights), _stream(stream)))
+    return ids, weights
+
+
+class MoePlan:
+    """The (token, slot) pairs sorted by expert (moe_plan): sizes and the device buffer."""
+
+    def __init__(self, T: int, k: int, experts: int, device):
+        import torch
+        lib = load_library()
+        nbytes = int(lib.moe_plan_bytes(T, k, experts))
+        if nbytes == 0:
+            raise FmpqError("moe_plan_bytes", 2)
+        self.T, self.k, self.experts = T, k, experts
+        self.rows = int(lib.moe_rows(T, k, experts))
+        self.buffer = torch.empty(nbytes // 4, dtype=torch.int32, device=device)
+
+    @property
+    def start(self):
+        return self.buffer[:self.experts]
+
+    @property
+    def count(self):
+        return self.buffer[self.experts:2 * self.experts]
+
+    @property
+    def row_of(self):
+        return self.buffer[2 * self.experts:2 * self.experts + self.T * self.k].view(self.T, self.k)
+
+
+def moe_plan(ids, experts: int, plan=None, stream=None) -> MoePlan:
+    """Sort the pairs of ids (int32 [T, k]) by expert; ids outside [0, experts) belong to none."""
+    import torch
+    _need(ids.is_cuda and ids.dim() == 2 and ids.dtype == torch.int32 and ids.is_contiguous(),
+          "ids must be a contiguous int32 CUDA tensor [T, k]")
+    T, k = ids.shape
+    plan = MoePlan(T, k, experts, ids.device) if plan is None else plan
+    _need((plan.T, plan.k, plan.experts) == (T, k, experts), "the plan was made for other sizes")
+    _check("moe_plan", load_library().moe_plan(_ptr(ids), T, k, experts, _ptr(plan.buffer), _stream(stream)))
+    return plan
+
+
+def moe_quantize(layer: Fp8Layer, plan: MoePlan, X, A_packed=None, a_scales=None, stream=None):
+    """Quantize each token of X [T, K] once into its experts' rows."""
+    _rows16(X, "X")
+    _need(X.shape == (plan.T, layer.K) and plan.experts == layer.experts, "X must be [T, K], the plan the layer's")
+    if A_packed is None or a_scales is None:
+        A, s = layer.activations(plan.rows, X.device)
+        A_packed, a_scales = A if A_packed is None else A_packed, s if a_scales is None else a_scales
+    _check("moe_quantize", layer._lib.moe_quantize(layer.handle, _ptr(plan.buffer), plan.T, plan.k, _ptr(X),
+                                                   _dtype_code(X.dtype), _ld(X), _ptr(A_packed), _ptr(a_scales),
+                                                   _stream(stream)))
+    return A_packed, a_scales
+
+
+def moe_up(layer: Fp8Layer, plan: MoePlan, A_packed, a_scales, W_packed, w_scales, H_packed=None, h_scales=None,
+           stream=None):
+    """SwiGLU of the gated layer's products, quantized: codes uint8 [F / 128, rows, 128] and scales."""
+    import torch
+    _need(layer.gated and plan.experts == layer.experts, "moe_up needs a gated layer and its plan")
+    fb = -(-(layer.N // 2) // BLOCK)
+    if H_packed is None:
+        H_packed = torch.empty((fb, plan.rows, BLOCK), dtype=torch.uint8, device=A_packed.device)
+    if h_scales is None:
+        h_scales = torch.empty((fb, (plan.rows + 3) // 4 * 4), dtype=torch.float32, device=A_packed.device)
+    _check("moe_up", layer._lib.moe_up(layer.handle, _ptr(plan.buffer), plan.T, plan.k, _ptr(A_packed), _ptr(a_scales),
+                                       _ptr(W_packed), _ptr(w_scales), _ptr(H_packed), _ptr(h_scales), _stream(stream)))
+    return H_packed, h_scales
+
+
+def moe_down(layer: Fp8Layer, plan: MoePlan, A_packed, a_scales, W_packed, w_scales, weights=None, dtype=None, D=None,
+             stream=None):
+    """Every row's product with its expert, times its pair's weight: D [plan.rows, N] (fp16 by default)."""
+    import torch
+    _need(plan.experts == layer.experts and not layer.gated, "moe_down needs a plain layer and its plan")
+    if weights is not None:
+        _need(weights.is_cuda and weights.dtype == torch.float32 and weights.shape == (plan.T, plan.k) and
+              weights.is_contiguous(), "weights must be contiguous fp32 [T, k]")
+    if D is None:
+        D = torch.empty((plan.rows, layer.N), dtype=dtype or torch.float16, device=A_packed.device)
+    _rows16(D, "D")
+    _need(D.shape == (plan.rows, layer.N), "D must be [rows, N]")
+    _check("moe_down", layer._lib.moe_down(layer.handle, _ptr(plan.buffer), plan.T, plan.k, _ptr(weights), _ptr(A_packed),
+                                           _ptr(a_scales), _ptr(W_packed), _ptr(w_scales), _ptr(D), _dtype_code(D.dtype),
+                                           _ld(D), _stream(stream)))
+    return D
+
+
+def moe_combine(D, plan: MoePlan, Y=None, stream=None):
+    """Y [T, N]: the sum of D's rows of each token."""
+    import torch
+    _rows16(D, "D")
+    _need(D.shape[0] == plan.rows, "D must be [rows, N]")
+    if Y is None:
+        Y = torch.empty((plan.T, D.shape[1]), dtype=D.dtype, device=D.device)
+    _rows16(Y, "Y")
+    _need(Y.shape == (plan.T, D.shape[1]) and Y.dtype == D.dtype, "Y must be [T, N] of D's type")
+    _check("moe_combine", load_library().moe_combine(_ptr(D), _dtype_code(D.dtype), _ld(D), _ptr(plan.buffer), plan.T,
+                                                     plan.k, plan.experts, D.shape[1], _ptr(Y), _ld(Y), _stream(stream)))
+    return Y
+
+
+def moe_experts(up: Fp8Layer, down: Fp8Layer, X, ids, weights, W_up, s_up, W_down, s_down, stream=None):
+    """The routed feed-forward on X [T, K]: for each token the sum over its slots of weights[t, j] *
+    down(silu(gate(x)) * up(x)) with expert ids[t, j] (-1: none). up: a gated layer [2F, K]; down: [N, F]
+    with the same experts. ids and weights as moe_route returns them. Y [T, N] of X's type."""
+    import torch
+    _need(up.gated and not down.gated and up.experts == down.experts and up.N == 2 * down.K,
+          "up must be the gated layer [2F, K] and down the plain layer [N, F] of the same experts")
+    _need(weights.dtype == torch.float32 and weights.shape == ids.shape and weights.is_contiguous(),
+          "weights must be contiguous fp32 [T, k]")
+    _need(X.dim() == 2 and ids.dim() == 2 and X.shape[0] == ids.shape[0], "ids must be [T, k] for X [T, K]")
+    plan = moe_plan(ids, up.experts, stream=stream)
+    A, sa = moe_quantize(up, plan, X, stream=stream)
+    H, sh = moe_up(up, plan, A, sa, W_up, s_up, stream=stream)
+    D = moe_down(down, plan, H, sh, W_down, s_down, weights=weights, dtype=X.dtype, stream=stream)
+    return moe_combine(D, plan, stream=stream)

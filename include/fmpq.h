@@ -19,7 +19,8 @@
  * the quantizer fused with RMSNorm (fmpq_rmsnorm_quantize) or SwiGLU (fmpq_swiglu_quantize), QUIK's FP16 outlier split
  * (fmpq_layout_create_select, fmpq_outlier_gemm_fp16), QUIK asymmetric activations
  * (fmpq_quantize_asym, w4ax_gemm_asym) and QoQ progressive group quantization with W4A8
- * GEMMs (qoq_pack_weights, qoq_quantize, qoq_gemm).
+ * GEMMs (qoq_pack_weights, qoq_quantize, qoq_gemm). E4M3 layers with a scale for each block of
+ * 128 (fp8_*), and layers of routed experts on them (moe_*).
  *
  * Conventions for every call:
  *   - Pointers are DEVICE pointers unless the parameter name ends in "_host".
@@ -33,7 +34,8 @@
  *     A CUDA launch failure returns FMPQ_ERR_CUDA. A device-side wait that gives up (a
  *     bounded wait, never a hang) records FMPQ_ERR_TIMEOUT in the layout's device status
  *     word, read by fmpq_device_status. The library never aborts, traps or prints.
- *   - All data buffers must be 16-byte aligned (FMPQ_ERR_MISALIGNED otherwise).
+ *   - All data buffers must be 16-byte aligned (FMPQ_ERR_MISALIGNED otherwise); the fp8_* and moe_*
+ *     calls take their 16-bit and fp32 inputs and outputs at any alignment of an element.
  *   - Inputs must be finite (no NaN/Inf); results for non-finite inputs are unspecified.
  */
 #ifndef FMPQ_H
@@ -424,6 +426,125 @@ FMPQ_API fmpq_status qoq_gemm_partials(const fmpq_layout* layout, const void* A_
 /* Read (and, if clear != 0, reset) the layout's device status word. Synchronizes the
  * device. *code = FMPQ_OK or the first error a kernel recorded (e.g. FMPQ_ERR_TIMEOUT). */
 FMPQ_API fmpq_status fmpq_device_status(const fmpq_layout* layout, int32_t* code, int32_t clear);
+
+/* ======================================================================================
+ * E4M3 linear layers: a scale for each block of 128
+ *
+ *   activations  per token m and block b of 128 channels (the last block may be partial):
+ *                s = fl32(max|x| / 448), code = e4m3(fl32(x / s)); s = 0 gives codes 0
+ *   weights      per 128 x 128 block, the same rule; or an E4M3 checkpoint's own codes and scales
+ *   product      Y[m][n] = sum_b a_scales[b][m] * w_scales[n / 128][b] * P[m][n][b], P the FP32
+ *                dot products of the block's codes on the tensor cores; FP32 sums; Y rounded once
+ * Any K, N and M; inputs finite. Divisions and conversions round to nearest even.
+ * These calls are forward only, like the rest of the library.
+ * ====================================================================================== */
+
+typedef enum fmpq_dtype { FMPQ_DTYPE_F16 = 0, FMPQ_DTYPE_BF16 = 1, FMPQ_DTYPE_F32 = 2 } fmpq_dtype;
+
+#define FP8_MAX_K 65536
+#define FP8_MAX_N 1048576
+
+/* Opaque, library-owned description of a layer of `experts` weight matrices [N][K] (1: a linear
+ * layer). gated = 1: the N = 2F rows of a matrix are F gate rows, then F up rows (moe_up).
+ * N >= 1, 1 <= K <= FP8_MAX_K, 1 <= experts <= 1024. Synchronous; allocates a status word. */
+typedef struct fp8_layer fp8_layer;
+FMPQ_API fmpq_status fp8_layer_create(int32_t K, int32_t N, int32_t experts, int32_t gated, fp8_layer** out);
+FMPQ_API void fp8_layer_destroy(fp8_layer* layer);
+/* As fmpq_device_status, for this layer's calls. */
+FMPQ_API fmpq_status fp8_device_status(const fp8_layer* layer, int32_t* status_host, int32_t clear);
+
+/* Bytes of the packed weights of all experts: per expert ceil(N/256) (gated: ceil(F/128)) pairs of
+ * tiles of 128 rows, every tile ceil(K/128) swizzled blocks of 16 KB. The format is
+ * implementation-defined; fp8_unpack_weights decodes it. */
+FMPQ_API size_t fp8_packed_w_bytes(const fp8_layer* layer);
+/* Weight scales, fp32 [experts][rows][ceil(K/128)]: rows = ceil(N/128); gated: ceil(F/128) of the
+ * gate, then ceil(F/128) of the up rows. This is their count. */
+FMPQ_API size_t fp8_weight_scale_count(const fp8_layer* layer);
+/* Bytes of `rows` rows of packed activations: codes [ceil(K/128)][rows][128], the 16-byte chunk c
+ * of row r at position c XOR (r mod 8), channels past K zero. */
+FMPQ_API size_t fp8_packed_a_bytes(const fp8_layer* layer, int64_t rows);
+/* Activation scales, fp32 [ceil(K/128)][stride], stride = rows rounded up to 4. Their count. */
+FMPQ_API size_t fp8_a_scale_count(const fp8_layer* layer, int64_t rows);
+
+/* Quantize one expert's weights W [N][ldw] (FMPQ_DTYPE_F16 or _BF16) into the layer's buffers. */
+FMPQ_API fmpq_status fp8_pack_weights(const fp8_layer* layer, int32_t expert, const void* W, int32_t dtype, int64_t ldw,
+                                      void* W_packed, void* w_scales, void* stream);
+/* Lay out one expert's E4M3 codes [N][ldw] (bytes; no NaN codes). Its scales are used as they are. */
+FMPQ_API fmpq_status fp8_pack_codes(const fp8_layer* layer, int32_t expert, const void* codes, int64_t ldw,
+                                    void* W_packed, void* stream);
+/* Debug/test: the values one expert's packed weights stand for, fp32 [N][K]. */
+FMPQ_API fmpq_status fp8_unpack_weights(const fp8_layer* layer, int32_t expert, const void* W_packed,
+                                        const void* w_scales, void* W, void* stream);
+
+/* Quantize X [M][ldx] (16 bits; any alignment of its elements, 16-byte rows are faster). */
+FMPQ_API fmpq_status fp8_quantize(const fp8_layer* layer, const void* X, int32_t dtype, int64_t ldx, int64_t M,
+                                  void* A_packed, void* a_scales, void* stream);
+/* Bytes of workspace fp8_gemm needs for M rows (0: none). Zero it once; every call leaves it fit
+ * for the next. Calls that may run at the same time need one each. */
+FMPQ_API size_t fp8_gemm_workspace_bytes(const fp8_layer* layer, int64_t M);
+/* Y [M][ldy] (16 bits) of a layer with experts = 1, gated = 0. */
+FMPQ_API fmpq_status fp8_gemm(const fp8_layer* layer, const void* A_packed, const void* a_scales, const void* W_packed,
+                              const void* w_scales, int64_t M, void* Y, int32_t dtype, int64_t ldy, void* workspace,
+                              size_t workspace_bytes, void* stream);
+/* fp8_quantize then fp8_gemm as one call; Y has X's type. A_packed and a_scales are written. */
+FMPQ_API fmpq_status fp8_quantize_gemm(const fp8_layer* layer, const void* X, int32_t dtype, int64_t ldx, int64_t M,
+                                       void* A_packed, void* a_scales, const void* W_packed, const void* w_scales,
+                                       void* Y, int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ======================================================================================
+ * Routing to experts, and the experts' products
+ * ====================================================================================== */
+
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+
+/* The k experts of each token and their weights from the router's logits [T][ldl] (any
+ * fmpq_dtype), 1 <= E <= 512, 1 <= k <= min(32, E).
+ *   score     softmax over the E logits, or the sigmoid of each.
+ *   key       what experts are chosen by: the logit itself where no bias and no sum over a group
+ *             is asked for (both scores grow with it), else score + bias[e] (fp32 [E]; NULL: 0),
+ *             compared as if in 64 bits: where FP32 cannot tell two keys apart, the token is decided
+ *             again in FP64. Equal keys: the lowest expert.
+ *   groups    > 1: the experts form `groups` (<= 32, dividing E) equal runs; a run's value is the sum of its
+ *             group_top (1 or 2) largest keys, and only the top_groups best runs (the lowest among
+ *             equals) stay. k <= top_groups * E / groups.
+ *   masked    logits of -inf or NaN, and biases of -inf or NaN, take their expert out of the choice; a
+ *             run's missing keys add nothing and a run without any is never chosen. A token with
+ *             fewer than k experts left gets id -1 and weight 0 in its last slots.
+ *   ids       int32 [T][k], by falling key; weights fp32 [T][k]: the scores (without bias); renormalize =
+ *             1: divided by their sum over the k (0 stays 0); times scale. A logit of +inf takes all of
+ *             the softmax (shared among several). */
+FMPQ_API fmpq_status moe_route(const void* logits, int32_t dtype, int64_t ldl, int64_t T, int32_t E, int32_t k,
+                               int32_t score, const void* bias, int32_t groups, int32_t top_groups, int32_t group_top,
+                               int32_t renormalize, float scale, void* ids, void* weights, void* stream);
+
+/* The (token, slot) pairs sorted by expert, in pair order inside an expert: ids int32 [T][k], those
+ * outside [0, E) belong to no expert. E <= 1024, k <= 32, T * k <= 2^22. Each expert's rows start at a
+ * multiple of 8; moe_rows is the number of rows that the experts' buffers have. The plan is
+ * int32 [E] first rows, [E] row counts, [T][k] row of each pair (-1: none), [moe_rows] pair of each
+ * row (defined for rows in use), then scratch; moe_plan_bytes in all. The same ids give the same
+ * plan. Both queries return 0 for sizes outside these limits. */
+FMPQ_API int64_t moe_rows(int64_t T, int32_t k, int32_t E);
+FMPQ_API size_t moe_plan_bytes(int64_t T, int32_t k, int32_t E);
+FMPQ_API fmpq_status moe_plan(const void* ids, int64_t T, int32_t k, int32_t E, void* plan, void* stream);
+
+/* Quantize X [T][ldx] once and write each token to its experts' rows (A_packed, a_scales: moe_rows
+ * rows of the layer). Rows of no pair are not written. */
+FMPQ_API fmpq_status moe_quantize(const fp8_layer* layer, const void* plan, int64_t T, int32_t k, const void* X,
+                                  int32_t dtype, int64_t ldx, void* A_packed, void* a_scales, void* stream);
+/* A gated layer's products, the SwiGLU h = silu(gate) * up in FP32, and its E4M3 codes and scales
+ * (the activations of a layer with K = F), every row with its expert's weights. */
+FMPQ_API fmpq_status moe_up(const fp8_layer* layer, const void* plan, int64_t T, int32_t k, const void* A_packed,
+                            const void* a_scales, const void* W_packed, const void* w_scales, void* H_packed,
+                            void* h_scales, void* stream);
+/* D[row][n] = weights[pair of row] * (the row's product with its expert), 16 bits, [moe_rows][ldd];
+ * weights fp32 [T][k], NULL: 1. */
+FMPQ_API fmpq_status moe_down(const fp8_layer* layer, const void* plan, int64_t T, int32_t k, const void* weights,
+                              const void* A_packed, const void* a_scales, const void* W_packed, const void* w_scales,
+                              void* D, int32_t dtype, int64_t ldd, void* stream);
+/* Y[t] = the sum of D over the token's rows, in slot order, FP32 sums, rounded once; a token without
+ * experts gets zeros. */
+FMPQ_API fmpq_status moe_combine(const void* D, int32_t dtype, int64_t ldd, const void* plan, int64_t T, int32_t k,
+                                 int32_t E, int32_t N, void* Y, int64_t ldy, void* stream);
 
 /* Static description of a status code. */
 FMPQ_API const char* fmpq_status_string(fmpq_status status);
