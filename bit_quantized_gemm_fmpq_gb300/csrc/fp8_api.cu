@@ -9,7 +9,7 @@
 
 namespace {
 
-constexpr int64_t kMaxRows = INT64_C(1) << 30;
+constexpr int64_t kMaxRows = INT64_C(1) << 24;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxRouteExperts = 512;
 constexpr int64_t kMaxPairs = INT64_C(1) << 22;

@@ -435,7 +435,7 @@ FMPQ_API fmpq_status fmpq_device_status(const fmpq_layout* layout, int32_t* code
  *   weights      per 128 x 128 block, the same rule; or an E4M3 checkpoint's own codes and scales
  *   product      Y[m][n] = sum_b a_scales[b][m] * w_scales[n / 128][b] * P[m][n][b], P the FP32
  *                dot products of the block's codes on the tensor cores; FP32 sums; Y rounded once
- * Any K, N and M; inputs finite. Divisions and conversions round to nearest even.
+ * Any K, N and M <= 2^24; inputs finite. Divisions and conversions round to nearest even.
  * These calls are forward only, like the rest of the library.
  * ====================================================================================== */
 
@@ -480,7 +480,8 @@ FMPQ_API fmpq_status fp8_unpack_weights(const fp8_layer* layer, int32_t expert, 
 FMPQ_API fmpq_status fp8_quantize(const fp8_layer* layer, const void* X, int32_t dtype, int64_t ldx, int64_t M,
                                   void* A_packed, void* a_scales, void* stream);
 /* Bytes of workspace fp8_gemm needs for M rows (0: none). Zero it once; every call leaves it fit
- * for the next. Calls that may run at the same time need one each. */
+ * for the next (zero it again after FMPQ_ERR_TIMEOUT). Calls that may run at the same time need one
+ * each. */
 FMPQ_API size_t fp8_gemm_workspace_bytes(const fp8_layer* layer, int64_t M);
 /* Y [M][ldy] (16 bits) of a layer with experts = 1, gated = 0. */
 FMPQ_API fmpq_status fp8_gemm(const fp8_layer* layer, const void* A_packed, const void* a_scales, const void* W_packed,
