@@ -10,8 +10,7 @@
 namespace {
 
 constexpr int64_t kMaxRows = INT64_C(1) << 24;
-constexpr int kMaxExperts = 1024;
-constexpr int kMaxRouteExperts = 512;
+constexpr int kMaxPlanExperts = 1024;
 constexpr int64_t kMaxPairs = INT64_C(1) << 22;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -33,7 +32,7 @@ cudaStream_t st(void* stream) { return static_cast<cudaStream_t>(stream); }
 
 // T tokens of k slots over E experts: what the plan and the experts' calls take.
 bool routing_ok(int64_t T, int32_t k, int32_t E) {
-    return T >= 1 && k >= 1 && k <= 32 && E >= 1 && E <= kMaxExperts && T <= kMaxPairs && T * k <= kMaxPairs;
+    return T >= 1 && k >= 1 && k <= 32 && E >= 1 && E <= kMaxPlanExperts && T <= kMaxPairs && T * k <= kMaxPairs;
 }
 
 }  // namespace
@@ -44,7 +43,7 @@ fmpq_status fp8_layer_create(int32_t K, int32_t N, int32_t experts, int32_t gate
     if (out == nullptr) return FMPQ_ERR_INVALID_ARG;
     *out = nullptr;
     if (gated != 0 && gated != 1) return FMPQ_ERR_INVALID_ARG;
-    if (K < 1 || K > FP8_MAX_K || N < 1 || N > FP8_MAX_N || experts < 1 || experts > kMaxExperts || (gated && N % 2 != 0))
+    if (K < 1 || K > FP8_MAX_K || N < 1 || N > FP8_MAX_N || experts < 1 || experts > fmpq::kMaxFp8Experts || (gated && N % 2 != 0))
         return FMPQ_ERR_UNSUPPORTED_SHAPE;
     int dev = -1, major = 0, minor = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -206,7 +205,7 @@ fmpq_status moe_route(const void* logits, int32_t dtype, int64_t ldl, int64_t T,
         (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) || (group_top != 1 && group_top != 2) ||
         (renormalize != 0 && renormalize != 1) || !std::isfinite(scale))
         return FMPQ_ERR_INVALID_ARG;
-    if (T < 1 || T > kMaxRows || E < 1 || E > kMaxRouteExperts || k < 1 || k > 32 || k > E || ldl < E || groups < 1 ||
+    if (T < 1 || T > kMaxRows || E < 1 || E > fmpq::kMaxFp8Experts || k < 1 || k > 32 || k > E || ldl < E || groups < 1 ||
         groups > 32 || E % groups != 0 || top_groups < 1 || top_groups > groups || k > top_groups * (E / groups))
         return FMPQ_ERR_UNSUPPORTED_SHAPE;
     if (!element_aligned(logits, dtype) || !element_aligned(bias, FMPQ_DTYPE_F32) ||

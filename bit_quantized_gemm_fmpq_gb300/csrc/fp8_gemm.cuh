@@ -1,0 +1,172 @@
+// What the two E4M3 product kernels share: parameters, the tiles and their order, epilogue pieces.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "fmpq_device.cuh"
+#include "fmpq_internal.h"
+#include "fp8_internal.h"
+
+namespace fmpq {
+namespace fp8 {
+
+constexpr int kStages = 6;      // operand blocks in flight
+constexpr int kScChunk = 4;     // blocks of token scales per copy
+constexpr int kScSlots = 3;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 384;   // 4 warps of other roles, 8 of the epilogue
+constexpr int kGroupM = 8;      // dense order: bands of 8 token tiles, weight tiles inside a band
+constexpr uint32_t kTmemCols = 512;
+
+struct Params {
+    const uint8_t* A;
+    const uint8_t* W;
+    const float* w_scales;
+    const int32_t* start;      // experts (nullptr: dense)
+    const int32_t* count;
+    const int32_t* pair_of;
+    const float* pair_weight;
+    int64_t rows, sstride;
+    uint16_t* Y;
+    int64_t ldy;
+    int bf16;                  // output type
+    int vec;                   // 16-byte output stores allowed
+    uint8_t* H;
+    float* h_scales;
+    int M, N, nb, pairs, scale_rows, experts, splits;
+    float* partial;            // split-K: [tile][split][CTA][warp][vector][lane] FP32 sums
+    int32_t* arrivals;         // [tile][CTA]
+    int32_t* status;
+};
+
+// The experts' tiles, staged in shared memory: units before each expert's, its first row and tokens.
+struct Tables {
+    int32_t first_unit[kMaxFp8Experts + 1], start[kMaxFp8Experts], count[kMaxFp8Experts];
+};
+
+// A unit of work: the 256 packed weight rows `pair` of expert e, `n` tokens from row `row0`, blocks
+// [b0, b1).
+struct Unit {
+    int e, pair, n, b0, b1, tile, split;
+    int64_t row0;
+};
+
+// One warp fills the tables (kT tokens a tile): lane l sums the run of experts [l * run, l * run + run).
+template <int kT>
+__device__ __forceinline__ void fill_tables(const Params& p, Tables& s, int lane) {
+    for (int e = lane; e < p.experts; e += 32) {
+        s.start[e] = p.start[e];
+        s.count[e] = p.count[e];
+    }
+    __syncwarp();
+    const int run = (p.experts + 31) / 32;
+    auto units_of = [&](int e) { return e < p.experts ? (s.count[e] + kT - 1) / kT * p.pairs : 0; };
+    int sum = 0;
+    for (int i = 0; i < run; ++i) sum += units_of(lane * run + i);
+    int before = sum;
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, before, d);
+        if (lane >= d) before += o;
+    }
+    before -= sum;
+    for (int i = 0; i < run; ++i) {
+        const int e = lane * run + i;
+        if (e <= p.experts) s.first_unit[e] = before;
+        before += units_of(e);
+    }
+    if (lane == 31 && p.experts == 32 * run) s.first_unit[p.experts] = before;
+}
+
+template <int kT>
+__device__ __forceinline__ int unit_count(const Params& p, const Tables& s) {
+    if (p.start != nullptr) return s.first_unit[p.experts];
+    return p.pairs * ((p.M + kT - 1) / kT) * p.splits;
+}
+
+// kEven: an expert's (or the layer's) tokens in tiles of about the same size, multiples of 32; else
+// full tiles and a rest.
+template <int kT, bool kEven>
+__device__ __forceinline__ Unit unit_of(const Params& p, const Tables& s, int u) {
+    Unit r;
+    int tokens = p.M, tiles, t;
+    int64_t row = 0;
+    r.e = 0;
+    r.split = 0;
+    r.b0 = 0;
+    r.b1 = p.nb;
+    if (p.start != nullptr) {
+        int lo = 0, hi = p.experts;   // the expert with first_unit[e] <= u < first_unit[e + 1]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s.first_unit[mid] <= u) lo = mid;
+            else hi = mid;
+        }
+        r.e = lo;
+        tokens = s.count[lo];
+        row = s.start[lo];
+        tiles = (tokens + kT - 1) / kT;
+        const int i = u - s.first_unit[lo];
+        t = i % tiles;
+        r.pair = i / tiles;
+        r.tile = u;
+    } else {
+        tiles = (p.M + kT - 1) / kT;
+        r.tile = u / p.splits;
+        r.split = u % p.splits;
+        const int band = r.tile / (kGroupM * p.pairs), in_band = r.tile - band * kGroupM * p.pairs;
+        const int gm = min(kGroupM, tiles - band * kGroupM);
+        t = band * kGroupM + in_band % gm;
+        r.pair = in_band / gm;
+        r.b0 = static_cast<int>(static_cast<int64_t>(r.split) * p.nb / p.splits);
+        r.b1 = static_cast<int>(static_cast<int64_t>(r.split + 1) * p.nb / p.splits);
+    }
+    const int size = kEven ? ((tokens + tiles - 1) / tiles + 31) & ~31 : kT;
+    r.row0 = row + t * size;
+    r.n = min(size, tokens - t * size);
+    return r;
+}
+
+__device__ __forceinline__ void fail(const Params& p, volatile int* abort_flag) {
+    *abort_flag = 1;
+    dev::report(p.status, dev::kStatusTimeout);
+}
+
+__device__ __forceinline__ const uint8_t* weight_block(const Params& p, const Unit& t, uint32_t rank) {
+    return p.W + ((static_cast<int64_t>(t.e) * p.pairs * 2 + 2 * t.pair + rank) * p.nb + t.b0) * kTileBytes;
+}
+
+// true in one lane of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xFFFFFFFF;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
+}
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool bf16) {
+    if (bf16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float silu_times(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+}  // namespace fp8
+
+// The token scales as a 2-D tensor [nb][rows]: boxes of kScChunk blocks x `tokens` rows.
+bool encode_scale_map(CUtensorMap* map, const float* scales, int64_t sstride, int nb, int tokens);
+// More than this many tokens a tile go to the kernel with the tokens on the tensor core's M side.
+cudaError_t launch_fp8_wide(const fp8_layer& L, const fp8::Params& p, const float* a_scales, int64_t tiles,
+                            cudaStream_t stream);
+// Pairs of CTAs that are resident at once (one CTA per SM).
+int fp8_resident_pairs(const fp8_layer& L);
+
+}  // namespace fmpq

@@ -1,0 +1,441 @@
+// E4M3 product with a scale for each block of 128, for many tokens (sm_103a).
+//
+// A pair of CTAs computes 256 tokens x 256 packed weight rows. The tokens are on the tensor core's M
+// side, so an epilogue thread owns one token: per block of 128 channels its partial sums P (FP32, in
+// TMEM) take one factor, a_scale[b][m] * w_scale[.][b] (a gated layer: two), and cost nothing but a
+// TMEM read and a packed multiply-add for two of them. With the weights on the M side (fp8_gemm.cu)
+// every pair of sums needs its own factor from shared memory.
+//
+// Per block and CTA: 4 MMAs of 128 clk, 128 KB of TMEM reads, 32 K multiply-adds (256 clk of the FP32
+// pipe), 32 KB of operands from L2 (about 40 bytes a clk and SM with all SMs reading: 820 clk).
+//
+// Warp roles (384 threads, one CTA per SM, pairs persistent over tiles):
+//   warp 0      producer: token codes and weight block, token scales (a chunk of blocks at a time)
+//   warp 1      even CTA: MMA issuer; odd CTA: reports its operands to the even one
+//   warp 2      allocates and frees TMEM; warp 3 fills the experts' tables
+//   warps 4-11  epilogue: TMEM lane quarter warp % 4 (32 tokens), 128 of the 256 columns each
+#include "fp8_gemm.cuh"
+
+namespace fmpq {
+namespace fp8 {
+namespace {
+
+constexpr int kT = 256;      // tokens of a tile, 128 a CTA
+constexpr int kAcc = 2;      // accumulators of 256 columns
+constexpr int kRing = 8;     // blocks whose readiness may be in flight (> kStages)
+
+struct __align__(1024) Smem {
+    uint8_t x[kStages][kTileBytes];   // token codes: this CTA's 128 rows
+    uint8_t w[kStages][kTileBytes];   // weight block: this CTA's tile, half of the pair's columns
+    float sx[kScSlots][kScChunk][128];
+    float amax[2][2][128];            // gated: absmax of each half of a token's 128 hidden channels (units in turn)
+    // ready[b % kRing], even CTA: block b's operands have landed in both CTAs and its accumulator has
+    // been read (by both CTAs' epilogue warps). Odd CTA: its operands have landed.
+    uint64_t ready[kRing], empty[kStages];
+    uint64_t acc_full[kAcc];
+    uint64_t sc_full[kScSlots], sc_empty[kScSlots];
+    uint64_t mma_done;
+    uint32_t tmem_base;
+    int abort_flag;
+    int fixup_last;
+    Tables tables;
+};
+
+__device__ __forceinline__ Unit unit(const Params& p, const Smem& s, int u) { return unit_of<kT, false>(p, s.tables, u); }
+
+__device__ __forceinline__ void producer(const Params& p, const CUtensorMap* scales, Smem& s, uint32_t rank,
+                                         volatile int* abort_flag) {
+    const int units = unit_count<kT>(p, s.tables);
+    uint32_t it = 0, ch = 0;
+    bool ok = true;
+    for (int u = blockIdx.x >> 1; ok && u < units; u += gridDim.x >> 1) {
+        const Unit t = unit(p, s, u);
+        const int local = static_cast<int>(rank) * 128;
+        const uint32_t xbytes = static_cast<uint32_t>(max(0, min(128, t.n - local))) * 128u;
+        const uint8_t* w = weight_block(p, t, rank);
+        const uint8_t* x = p.A + (t.row0 + local + t.b0 * p.rows) * 128;
+        for (int b = t.b0; b < t.b1; ++b, ++it) {
+            if ((b - t.b0) % kScChunk == 0) {
+                const int sl = ch % kScSlots;
+                ok = dev::mbar_wait(&s.sc_empty[sl], ((ch / kScSlots) & 1) ^ 1, abort_flag);
+                if (!ok) break;
+                dev::mbar_arrive_expect_tx(&s.sc_full[sl], sizeof(s.sx[0]));
+                dev::tma_load_2d(s.sx[sl], scales, static_cast<int>(t.row0) + local, b, &s.sc_full[sl]);
+                ++ch;
+            }
+            const int st = it % kStages;
+            ok = dev::mbar_wait(&s.empty[st], ((it / kStages) & 1) ^ 1, abort_flag);
+            if (!ok) break;
+            uint64_t* bar = &s.ready[it % kRing];
+            dev::mbar_arrive_expect_tx(bar, kTileBytes + xbytes);
+            dev::bulk_g2s(s.w[st], w, kTileBytes, bar);
+            if (xbytes > 0) dev::bulk_g2s(s.x[st], x, xbytes, bar);
+            w += kTileBytes;
+            x += p.rows * 128;
+        }
+    }
+    if (!ok) fail(p, abort_flag);
+    // the copies in flight must land before the CTA's shared memory is given up (after an abort the
+    // even CTA's readiness may never be complete: a short bound, far longer than a copy)
+    for (uint32_t k = 0; k < kStages && k < it; ++k) {
+        const uint32_t i = it - 1 - k;
+        dev::mbar_wait(&s.ready[i % kRing], (i / kRing) & 1, nullptr, ok ? dev::kMaxPolls : 1u << 16);
+    }
+    for (uint32_t k = 0; k < kScSlots && k < ch; ++k) {
+        const uint32_t i = ch - 1 - k;
+        dev::mbar_wait(&s.sc_full[i % kScSlots], (i / kScSlots) & 1, nullptr);
+    }
+}
+
+__device__ __forceinline__ void mma_issuer(const Params& p, Smem& s, uint32_t rank, uint32_t tmem,
+                                           volatile int* abort_flag) {
+    const int units = unit_count<kT>(p, s.tables);
+    constexpr uint32_t kIdesc = dev::idesc_e4m3_f32(256, 256);
+    const uint32_t leader = dev::mapa(&s.ready[0], 0);
+    const uint64_t x0 = dev::sdesc_k_sw128(dev::smem_u32(s.x[0])), w0 = dev::sdesc_k_sw128(dev::smem_u32(s.w[0]));
+    uint32_t it = 0, st = 0;
+    bool ok = true;
+    for (int u = blockIdx.x >> 1; ok && u < units; u += gridDim.x >> 1) {
+        const Unit t = unit(p, s, u);
+        for (int b = t.b0; b < t.b1; ++b, ++it) {
+            ok = __all_sync(0xFFFFFFFFu, dev::mbar_wait(&s.ready[it % kRing], (it / kRing) & 1, abort_flag));
+            if (!ok) break;
+            if (rank != 0) {
+                if (elect_one()) dev::mbar_arrive_remote(leader + (it % kRing) * 8u);
+                continue;
+            }
+            dev::tc_fence_after();
+            // (a descriptor's address field counts 16 bytes)
+            const uint64_t ad = x0 + st * (kTileBytes / 16), bd = w0 + st * (kTileBytes / 16);
+            const uint32_t d = tmem + (it % kAcc) * 256u;
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) dev::mma_e4m3_pair(d, ad + 2 * k, bd + 2 * k, kIdesc, k > 0 ? 1u : 0u);
+                dev::mma_commit_pair(&s.acc_full[it % kAcc]);
+                dev::mma_commit_pair(&s.empty[st]);
+            }
+            __syncwarp();
+            if (++st == kStages) st = 0;
+        }
+    }
+    if (elect_one()) {
+        if (!ok) fail(p, abort_flag);
+        if (rank == 0) {   // every MMA must finish before TMEM is released
+            dev::mma_commit_pair(&s.mma_done);
+            dev::mbar_wait(&s.mma_done, 0, nullptr);
+        }
+    }
+    __syncwarp();
+}
+
+// acc += d * f for 32 columns, the first 16 with f0 and the others with f1.
+__device__ __forceinline__ void accumulate(const uint32_t (&d)[32], float f0, float f1, float2 (&acc)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float f = i < 8 ? f0 : f1;
+        acc[i] = dev::ffma2(make_float2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1])), make_float2(f, f), acc[i]);
+    }
+}
+
+// Thread: token 32 (warp % 4) + lane of this CTA's 128, columns 128 h .. + 127 (packed weight rows of
+// tile 2 pair + h): acc[c][i] holds columns 32c + 2i and + 1. The blocks of a unit run straight-line
+// (a TMEM load under a condition makes the compiler move its 32 registers at every join), the next
+// load always in flight during the arithmetic of this one.
+template <bool kGated>
+__device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank, int warp, int lane, uint32_t tmem,
+                                         volatile int* abort_flag) {
+    const int units = unit_count<kT>(p, s.tables);
+    const int q = warp & 3, h = (warp - 4) >> 2;
+    const int local = 32 * q + lane;
+    const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16) + 128u * h;
+    const uint32_t leader_ready = dev::mapa(&s.ready[0], 0);
+    uint32_t v = 0, ch = 0, nu = 0;
+    bool ok = true;
+    auto acc_ready = [&](uint32_t n) {
+        const bool there = dev::mbar_wait(&s.acc_full[n % kAcc], (n / kAcc) & 1, abort_flag);
+        const bool all = __all_sync(0xFFFFFFFFu, there);
+        dev::tc_fence_after();
+        return all;
+    };
+    for (int u = blockIdx.x >> 1; u < units; u += gridDim.x >> 1) {
+        const Unit t = unit(p, s, u);
+        float2 acc[4][16];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[c][i] = make_float2(0.0f, 0.0f);
+        // weight scales of 32 blocks, one a lane: the tile's, or gate and up
+        const int srow = kGated ? t.pair : 2 * t.pair + h;
+        const float* ws0 = p.w_scales + (static_cast<int64_t>(t.e) * p.scale_rows + min(srow, p.scale_rows - 1)) * p.nb;
+        const float* ws1 = kGated ? ws0 + static_cast<int64_t>(p.scale_rows / 2) * p.nb : ws0;
+        auto scale_of = [&](const float* w, int b) { return b < t.b1 ? __ldg(w + b) : 0.0f; };
+        float next0 = scale_of(ws0, t.b0 + lane), next1 = kGated ? scale_of(ws1, t.b0 + lane) : 0.0f;
+        float cur0 = 0.0f, cur1 = 0.0f;
+
+        uint32_t d0[32], d1[32];
+        if (ok && (ok = acc_ready(v))) {
+            dev::tmem_ld32(base + (v % kAcc) * 256u, d0);
+            for (int b = t.b0;; ++v) {
+                const int i = b - t.b0, i32 = i & 31, in_chunk = i % kScChunk, sl = ch % kScSlots;
+                if (i32 == 0) {
+                    cur0 = next0;
+                    cur1 = next1;
+                    next0 = scale_of(ws0, b + 32 + lane);
+                    if (kGated) next1 = scale_of(ws1, b + 32 + lane);
+                }
+                if (in_chunk == 0 && !__all_sync(0xFFFFFFFFu, dev::mbar_wait(&s.sc_full[sl], (ch / kScSlots) & 1, abort_flag))) {
+                    ok = false;
+                    break;
+                }
+                const float sx = s.sx[sl][in_chunk][local];
+                const float f0 = sx * __shfl_sync(0xFFFFFFFFu, cur0, i32);
+                const float f1 = kGated ? sx * __shfl_sync(0xFFFFFFFFu, cur1, i32) : f0;
+                const uint32_t at = base + (v % kAcc) * 256u;
+                dev::tmem_ld_wait32(d0);
+                dev::tmem_ld32(at + 32u, d1);
+                accumulate(d0, f0, f1, acc[0]);
+                dev::tmem_ld_wait32(d1);
+                dev::tmem_ld32(at + 64u, d0);
+                accumulate(d1, f0, f1, acc[1]);
+                dev::tmem_ld_wait32(d0);
+                dev::tmem_ld32(at + 96u, d1);
+                accumulate(d0, f0, f1, acc[2]);
+                dev::tmem_ld_wait32(d1);
+                // all of it is in registers: the accumulator is free for block v + kAcc
+                dev::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) dev::mbar_arrive_remote(leader_ready + ((v + kAcc) % kRing) * 8u);
+                if (in_chunk == kScChunk - 1 || b + 1 == t.b1) {
+                    if (lane == 0) dev::mbar_arrive(&s.sc_empty[sl]);
+                    ++ch;
+                }
+                if (++b == t.b1) {
+                    accumulate(d1, f0, f1, acc[3]);
+                    ++v;
+                    break;
+                }
+                if (!acc_ready(v + 1)) {
+                    ok = false;
+                    break;
+                }
+                dev::tmem_ld32(base + ((v + 1) % kAcc) * 256u, d0);
+                accumulate(d1, f0, f1, acc[3]);
+            }
+        }
+
+        const int tok = static_cast<int>(rank) * 128 + local;
+        const bool mine = ok && tok < t.n;
+        const int64_t row = t.row0 + tok;
+        if constexpr (kGated) {
+            // acc[c][0..7] gates and acc[c][8..15] ups of 16 hidden channels: h = silu(gate) * up, kept
+            // in the gates' place
+            float top = 0.0f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float2& g = acc[c][i];
+                    g = make_float2(silu_times(g.x, acc[c][i + 8].x), silu_times(g.y, acc[c][i + 8].y));
+                    top = fmaxf(top, fmaxf(fabsf(g.x), fabsf(g.y)));
+                }
+            // the other half of the block's channels is with the same lane of the other column warp; a
+            // warp two units ahead has seen the other arrive for the unit between, after its reads
+            const int par = nu++ & 1;
+            s.amax[par][h][local] = top;
+            dev::named_bar_sync(2 + q, 64);
+            const float scale = __fdiv_rn(fmaxf(s.amax[par][0][local], s.amax[par][1][local]), 448.0f);
+            if (mine) {
+                uint8_t* out = p.H + (static_cast<int64_t>(t.pair) * p.rows + row) * 128;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[4] = {0u, 0u, 0u, 0u};
+                    if (scale > 0.0f) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 g = acc[c][i];
+                            o[i >> 1] |= e4m3x2(__fdiv_rn(g.x, scale), __fdiv_rn(g.y, scale)) << (16 * (i & 1));
+                        }
+                    }
+                    *reinterpret_cast<uint4*>(out + (((4 * h + c) ^ static_cast<int>(row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+                if (h == 0) p.h_scales[t.pair * p.sstride + row] = scale;
+            }
+        } else {
+            auto store = [&]() {
+                if (!mine) return;
+                const float w = p.pair_weight != nullptr ? __ldg(p.pair_weight + p.pair_of[row]) : 1.0f;
+                const int n0 = 256 * t.pair + 128 * h;
+                uint16_t* y = p.Y + row * p.ldy + n0;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int n = 32 * c + 8 * k;
+                        uint32_t o[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 f = acc[c][4 * k + i];
+                            o[i] = pack16(f.x * w, f.y * w, p.bf16);
+                        }
+                        if (p.vec && n0 + n + 8 <= p.N) {
+                            *reinterpret_cast<uint4*>(y + n) = make_uint4(o[0], o[1], o[2], o[3]);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                if (n0 + n + j < p.N) y[n + j] = static_cast<uint16_t>(o[j >> 1] >> (16 * (j & 1)));
+                        }
+                    }
+            };
+            if (p.splits == 1) {
+                store();
+            } else {
+                // publish this split's sums; the last split to arrive adds all of them in split order
+                auto slot_of = [&](int sp) {
+                    return reinterpret_cast<float4*>(p.partial) +
+                           (((static_cast<int64_t>(t.tile) * p.splits + sp) * 2 + rank) * kEpiWarps + (warp - 4)) * (32 * 32) + lane;
+                };
+                float4* out = slot_of(t.split);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        __stcg(out + (8 * c + i) * 32, make_float4(acc[c][2 * i].x, acc[c][2 * i].y, acc[c][2 * i + 1].x, acc[c][2 * i + 1].y));
+                __threadfence();
+                dev::named_bar_sync(1, kEpiWarps * 32);
+                if (warp == 4 && lane == 0) {
+                    int32_t* cnt = p.arrivals + t.tile * 2 + static_cast<int>(rank);
+                    const int last = atomicAdd(cnt, 1) == p.splits - 1;
+                    if (last) *cnt = 0;   // ready for the next call
+                    s.fixup_last = last;
+                }
+                dev::named_bar_sync(1, kEpiWarps * 32);
+                if (s.fixup_last) {
+                    __threadfence();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            for (int sp = 0; sp < p.splits; ++sp) {
+                                const float4 f = __ldcg(slot_of(sp) + (8 * c + i) * 32);
+                                sum.x += f.x;
+                                sum.y += f.y;
+                                sum.z += f.z;
+                                sum.w += f.w;
+                            }
+                            acc[c][2 * i] = make_float2(sum.x, sum.y);
+                            acc[c][2 * i + 1] = make_float2(sum.z, sum.w);
+                        }
+                    store();
+                }
+            }
+        }
+    }
+    if (!ok) {
+        dev::tmem_ld_wait();   // none in flight when TMEM is freed
+        if (lane == 0) fail(p, abort_flag);
+    }
+}
+
+template <bool kGated>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+fp8_wide_kernel(const Params p, const __grid_constant__ CUtensorMap scales) {
+    extern __shared__ uint8_t smem_raw[];
+    Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = dev::cluster_ctarank();
+    if (threadIdx.x == 0) {
+        dev::tma_prefetch_map(&scales);
+        for (int i = 0; i < kRing; ++i) dev::mbar_init(&s.ready[i], rank == 0 ? 2 + 2 * kEpiWarps : 1);
+        for (int i = 0; i < kStages; ++i) dev::mbar_init(&s.empty[i], 1);
+        for (int i = 0; i < kAcc; ++i) dev::mbar_init(&s.acc_full[i], 1);
+        for (int i = 0; i < kScSlots; ++i) {
+            dev::mbar_init(&s.sc_full[i], 1);
+            dev::mbar_init(&s.sc_empty[i], kEpiWarps);
+        }
+        dev::mbar_init(&s.mma_done, 1);
+        s.abort_flag = 0;
+        if (rank == 0)   // the first blocks find their accumulators free
+            for (int i = 0; i < kAcc; ++i)
+                for (int k = 0; k < 2 * kEpiWarps; ++k) dev::mbar_arrive(&s.ready[i]);
+        dev::fence_barrier_init();
+    }
+    if (warp == 2) dev::tmem_alloc_pair(&s.tmem_base, kTmemCols);
+    if (warp == 3 && p.start != nullptr) fill_tables<kT>(p, s.tables, lane);
+    dev::tc_fence_before();
+    __syncthreads();
+    dev::cluster_sync();   // both CTAs' barriers and TMEM exist before any traffic between them
+    dev::tc_fence_after();
+    const uint32_t tmem = s.tmem_base;
+    volatile int* abort_flag = &s.abort_flag;
+
+    if (warp < 4) {
+        dev::setmaxnreg_dec<72>();
+        if (warp == 0) {
+            if (lane == 0) producer(p, &scales, s, rank, abort_flag);
+        } else if (warp == 1) {
+            mma_issuer(p, s, rank, tmem, abort_flag);
+        }
+        __syncwarp();
+    } else {
+        dev::setmaxnreg_inc<216>();   // 128 x 72 + 256 x 216 = the 384 x 168 of the launch
+        epilogue<kGated>(p, s, rank, warp, lane, tmem, abort_flag);
+    }
+    dev::tc_fence_before();
+    __syncthreads();
+    dev::cluster_sync();   // the peer's MMAs, commits and arrivals on this CTA are done
+    if (warp == 2) {
+        dev::tc_fence_after();
+        dev::tmem_dealloc_pair(tmem, kTmemCols);
+    }
+}
+
+constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory exceeds the 227 KB a CTA may use");
+
+}  // namespace
+}  // namespace fp8
+
+// The persistent grids never launch more pairs than can be resident; asked once per device.
+int fp8_resident_pairs(const fp8_layer& L) {
+    static int cached[64] = {};
+    if (L.device >= 0 && L.device < 64 && cached[L.device] > 0) return cached[L.device];
+    int pairs = L.num_sms / 2 > 0 ? L.num_sms / 2 : 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+    cfg.blockDim = dim3(fp8::kThreads);
+    cfg.dynamicSmemBytes = fp8::kSmemBytes;
+    int clusters = 0;
+    if (ensure_smem_limit(reinterpret_cast<const void*>(fp8::fp8_wide_kernel<false>), static_cast<int>(fp8::kSmemBytes)) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&clusters, fp8::fp8_wide_kernel<false>, &cfg) == cudaSuccess && clusters > 0 && clusters < pairs)
+        pairs = clusters;
+    cudaGetLastError();   // a failed query leaves no error behind
+    if (L.device >= 0 && L.device < 64) cached[L.device] = pairs;
+    return pairs;
+}
+
+bool encode_scale_map(CUtensorMap* map, const float* scales, int64_t sstride, int nb, int tokens) {
+    const EncodeTiledFn encode = encode_tiled();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(sstride), static_cast<cuuint64_t>(nb)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(sstride) * sizeof(float)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(tokens), fp8::kScChunk}, step[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float*>(scales), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_fp8_wide(const fp8_layer& L, const fp8::Params& p, const float* a_scales, int64_t tiles,
+                            cudaStream_t stream) {
+    CUtensorMap map;
+    if (!encode_scale_map(&map, a_scales, p.sstride, L.nb, 128)) return cudaErrorInvalidValue;
+    auto fn = L.gated ? fp8::fp8_wide_kernel<true> : fp8::fp8_wide_kernel<false>;
+    const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), static_cast<int>(fp8::kSmemBytes));
+    if (e != cudaSuccess) return e;
+    const int64_t units = tiles * L.pairs * p.splits;
+    const int grid = 2 * static_cast<int>(units < fp8_resident_pairs(L) ? units : fp8_resident_pairs(L));
+    fn<<<grid, fp8::kThreads, fp8::kSmemBytes, stream>>>(p, map);
+    return cudaGetLastError();
+}
+
+}  // namespace fmpq

@@ -20,29 +20,21 @@ namespace fmpq {
 
 constexpr int kFp8Block = 128;
 constexpr int kTileBytes = 128 * 128;   // one operand tile: 128 rows of 128 codes
+constexpr int kMaxFp8Experts = 512;
 
 // ---------------------------------------------------------------- the packed weight layout
 // A pair tile is two tiles of 128 weight rows, one for each CTA of a pair; its blocks follow one
 // another: tile t of an expert holds [nb][128 rows][128 codes], the 16-byte chunk c of row r at
 // position c ^ (r % 8) (the 128-byte-swizzled K-major operand tile, one bulk copy of 16 KB).
-// The order of the rows inside a tile is the one in which the tensor core's accumulator lanes
-// fall to a thread with consecutive output channels (see the product's epilogue):
-//   plain layer: row 32q + 8g + 2c + j of tile t is channel 128t + 32q + 8c + 2g + j;
-//   gated layer: rows 32q .. 32q + 15 are gate rows and 32q + 16 .. 32q + 31 the up rows of the
-//   same 16 hidden channels: row 32q + 16u + 8g + 2c + j of tile t is hidden channel
-//   64t + 16q + 4c + 2g + j, so the two tiles of a pair cover one block of 128 of them.
+// Plain layer: row p of tile t is channel 128t + p. Gated layer: rows 32q .. 32q + 15 are gate rows
+// and rows 32q + 16 .. 32q + 31 the up rows of the hidden channels 64t + 16q .. + 15, so a warp of
+// the product's epilogue holds both of a channel and the two tiles of a pair cover a block of 128.
 // Returns the weight row (of N) held by row `p` of tile `t`, or -1 past the last one.
 __host__ __device__ inline int fp8_source_row(int t, int p, int N, int gated) {
-    const int q = p >> 5, l = p & 31;
-    const int c = (l & 7) >> 1, j = l & 1;
-    if (!gated) {
-        const int n = 128 * t + 32 * q + 8 * c + 2 * (l >> 3) + j;
-        return n < N ? n : -1;
-    }
-    const int F = N / 2;
-    const int f = 64 * t + 16 * q + 4 * c + 2 * ((l >> 3) & 1) + j;
+    if (!gated) return 128 * t + p < N ? 128 * t + p : -1;
+    const int F = N / 2, f = 64 * t + 16 * (p >> 5) + (p & 15);
     if (f >= F) return -1;
-    return (l >> 4) ? F + f : f;
+    return (p & 16) ? F + f : f;
 }
 // Row of the weight scales that weight row n belongs to.
 __host__ __device__ inline int fp8_scale_row(int n, int N, int gated) {

@@ -446,7 +446,7 @@ typedef enum fmpq_dtype { FMPQ_DTYPE_F16 = 0, FMPQ_DTYPE_BF16 = 1, FMPQ_DTYPE_F3
 
 /* Opaque, library-owned description of a layer of `experts` weight matrices [N][K] (1: a linear
  * layer). gated = 1: the N = 2F rows of a matrix are F gate rows, then F up rows (moe_up).
- * N >= 1, 1 <= K <= FP8_MAX_K, 1 <= experts <= 1024. Synchronous; allocates a status word. */
+ * N >= 1, 1 <= K <= FP8_MAX_K, 1 <= experts <= 512. Synchronous; allocates a status word. */
 typedef struct fp8_layer fp8_layer;
 FMPQ_API fmpq_status fp8_layer_create(int32_t K, int32_t N, int32_t experts, int32_t gated, fp8_layer** out);
 FMPQ_API void fp8_layer_destroy(fp8_layer* layer);
