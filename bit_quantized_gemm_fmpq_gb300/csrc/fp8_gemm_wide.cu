@@ -9,11 +9,11 @@
 // Per block and CTA: 4 MMAs of 128 clk, 128 KB of TMEM reads, 32 K multiply-adds (256 clk of the FP32
 // pipe), 32 KB of operands from L2 (about 40 bytes a clk and SM with all SMs reading: 820 clk).
 //
-// Warp roles (384 threads, one CTA per SM, pairs persistent over tiles):
+// Warp roles (640 threads, one CTA per SM, pairs persistent over tiles):
 //   warp 0      producer: token codes and weight block, token scales (a chunk of blocks at a time)
 //   warp 1      even CTA: MMA issuer; odd CTA: reports its operands to the even one
 //   warp 2      allocates and frees TMEM; warp 3 fills the experts' tables
-//   warps 4-11  epilogue: TMEM lane quarter warp % 4 (32 tokens), 128 of the 256 columns each
+//   warps 4-19  epilogue: TMEM lane quarter warp % 4 (32 tokens), 64 of the 256 columns each
 #include "fp8_gemm.cuh"
 
 namespace fmpq {
@@ -22,13 +22,16 @@ namespace {
 
 constexpr int kT = 256;      // tokens of a tile, 128 a CTA
 constexpr int kAcc = 2;      // accumulators of 256 columns
+constexpr int kWideEpi = 16; // epilogue warps
+constexpr int kWideThreads = 640;
 constexpr int kRing = 8;     // blocks whose readiness may be in flight (> kStages)
 
 struct __align__(1024) Smem {
     uint8_t x[kStages][kTileBytes];   // token codes: this CTA's 128 rows
     uint8_t w[kStages][kTileBytes];   // weight block: this CTA's tile, half of the pair's columns
     float sx[kScSlots][kScChunk][128];
-    float amax[2][2][128];            // gated: absmax of each half of a token's 128 hidden channels (units in turn)
+    float amax[2][4][128];            // gated: absmax of each quarter of a token's 128 hidden channels (units in turn)
+    uint4 out[kWideEpi][32 * 2];      // a warp's 32 tokens x 16 columns of 16-bit outputs
     // ready[b % kRing], even CTA: block b's operands have landed in both CTAs and its accumulator has
     // been read (by both CTAs' epilogue warps). Odd CTA: its operands have landed.
     uint64_t ready[kRing], empty[kStages];
@@ -137,117 +140,99 @@ __device__ __forceinline__ void accumulate(const uint32_t (&d)[32], float f0, fl
     }
 }
 
-// Thread: token 32 (warp % 4) + lane of this CTA's 128, columns 128 h .. + 127 (packed weight rows of
-// tile 2 pair + h): acc[c][i] holds columns 32c + 2i and + 1. The blocks of a unit run straight-line
-// (a TMEM load under a condition makes the compiler move its 32 registers at every join), the next
-// load always in flight during the arithmetic of this one.
+// Thread: token 32 (warp % 4) + lane of this CTA's 128, columns 64 h .. + 63 (packed weight rows of
+// tile 2 pair + h / 2): acc[c][i] holds columns 32c + 2i and + 1. A warp has one TMEM load in flight
+// (a wait covers all of a warp's loads), so four warps a scheduler hide them for each other. The
+// blocks of a unit run straight-line: a TMEM load under a condition makes the compiler move its 32
+// registers at every join. A wait that gives up is remembered, and the unit's outputs are not stored.
 template <bool kGated>
 __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank, int warp, int lane, uint32_t tmem,
                                          volatile int* abort_flag) {
     const int units = unit_count<kT>(p, s.tables);
     const int q = warp & 3, h = (warp - 4) >> 2;
     const int local = 32 * q + lane;
-    const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16) + 128u * h;
+    const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16) + 64u * h;
     const uint32_t leader_ready = dev::mapa(&s.ready[0], 0);
     uint32_t v = 0, ch = 0, nu = 0;
     bool ok = true;
-    auto acc_ready = [&](uint32_t n) {
-        const bool there = dev::mbar_wait(&s.acc_full[n % kAcc], (n / kAcc) & 1, abort_flag);
-        const bool all = __all_sync(0xFFFFFFFFu, there);
-        dev::tc_fence_after();
-        return all;
-    };
     for (int u = blockIdx.x >> 1; u < units; u += gridDim.x >> 1) {
         const Unit t = unit(p, s, u);
-        float2 acc[4][16];
+        const int tok = static_cast<int>(rank) * 128 + local;
+        const int64_t row = t.row0 + tok;
+        float weight = 1.0f;   // of this thread's token
+        if (!kGated && p.pair_weight != nullptr && tok < t.n) weight = __ldg(p.pair_weight + p.pair_of[row]);
+        float2 acc[2][16];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[c][i] = make_float2(0.0f, 0.0f);
         // weight scales of 32 blocks, one a lane: the tile's, or gate and up
-        const int srow = kGated ? t.pair : 2 * t.pair + h;
-        const float* ws0 = p.w_scales + (static_cast<int64_t>(t.e) * p.scale_rows + min(srow, p.scale_rows - 1)) * p.nb;
-        const float* ws1 = kGated ? ws0 + static_cast<int64_t>(p.scale_rows / 2) * p.nb : ws0;
-        auto scale_of = [&](const float* w, int b) { return b < t.b1 ? __ldg(w + b) : 0.0f; };
-        float next0 = scale_of(ws0, t.b0 + lane), next1 = kGated ? scale_of(ws1, t.b0 + lane) : 0.0f;
+        const int srow = kGated ? t.pair : 2 * t.pair + (h >> 1);
+        const float* ws0 = p.w_scales + (static_cast<int64_t>(t.e) * p.scale_rows + min(srow, p.scale_rows - 1)) * p.nb + lane;
+        const int up = kGated ? p.scale_rows / 2 * p.nb : 0;   // the up scales from the gate's
+        const int blocks = t.b1 - t.b0;
+        auto scale_of = [&](int i, int off) { return i + lane < blocks ? __ldg(ws0 + t.b0 + i + off) : 0.0f; };
+        float next0 = scale_of(0, 0), next1 = kGated ? scale_of(0, up) : 0.0f;
         float cur0 = 0.0f, cur1 = 0.0f;
-
-        uint32_t d0[32], d1[32];
-        if (ok && (ok = acc_ready(v))) {
-            dev::tmem_ld32(base + (v % kAcc) * 256u, d0);
-            for (int b = t.b0;; ++v) {
-                const int i = b - t.b0, i32 = i & 31, in_chunk = i % kScChunk, sl = ch % kScSlots;
-                if (i32 == 0) {
-                    cur0 = next0;
-                    cur1 = next1;
-                    next0 = scale_of(ws0, b + 32 + lane);
-                    if (kGated) next1 = scale_of(ws1, b + 32 + lane);
-                }
-                if (in_chunk == 0 && !__all_sync(0xFFFFFFFFu, dev::mbar_wait(&s.sc_full[sl], (ch / kScSlots) & 1, abort_flag))) {
-                    ok = false;
-                    break;
-                }
-                const float sx = s.sx[sl][in_chunk][local];
-                const float f0 = sx * __shfl_sync(0xFFFFFFFFu, cur0, i32);
-                const float f1 = kGated ? sx * __shfl_sync(0xFFFFFFFFu, cur1, i32) : f0;
-                const uint32_t at = base + (v % kAcc) * 256u;
-                dev::tmem_ld_wait32(d0);
-                dev::tmem_ld32(at + 32u, d1);
-                accumulate(d0, f0, f1, acc[0]);
-                dev::tmem_ld_wait32(d1);
-                dev::tmem_ld32(at + 64u, d0);
-                accumulate(d1, f0, f1, acc[1]);
-                dev::tmem_ld_wait32(d0);
-                dev::tmem_ld32(at + 96u, d1);
-                accumulate(d0, f0, f1, acc[2]);
-                dev::tmem_ld_wait32(d1);
-                // all of it is in registers: the accumulator is free for block v + kAcc
-                dev::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) dev::mbar_arrive_remote(leader_ready + ((v + kAcc) % kRing) * 8u);
-                if (in_chunk == kScChunk - 1 || b + 1 == t.b1) {
-                    if (lane == 0) dev::mbar_arrive(&s.sc_empty[sl]);
-                    ++ch;
-                }
-                if (++b == t.b1) {
-                    accumulate(d1, f0, f1, acc[3]);
-                    ++v;
-                    break;
-                }
-                if (!acc_ready(v + 1)) {
-                    ok = false;
-                    break;
-                }
-                dev::tmem_ld32(base + ((v + 1) % kAcc) * 256u, d0);
-                accumulate(d1, f0, f1, acc[3]);
+#pragma unroll 1
+        for (int i = 0; i < blocks; ++i, ++v) {
+            const int in_chunk = i % kScChunk, sl = ch % kScSlots;
+            if ((i & 31) == 0) {
+                cur0 = next0;
+                cur1 = next1;
+                next0 = scale_of(i + 32, 0);
+                if (kGated) next1 = scale_of(i + 32, up);
             }
+            if (in_chunk == 0) ok &= dev::mbar_wait(&s.sc_full[sl], (ch / kScSlots) & 1, abort_flag);
+            const float sx = s.sx[sl][in_chunk][local];
+            const float f0 = sx * __shfl_sync(0xFFFFFFFFu, cur0, i & 31);
+            const float f1 = kGated ? sx * __shfl_sync(0xFFFFFFFFu, cur1, i & 31) : f0;
+            ok &= dev::mbar_wait(&s.acc_full[v % kAcc], (v / kAcc) & 1, abort_flag);
+            __syncwarp();
+            dev::tc_fence_after();
+            const uint32_t at = base + (v % kAcc) * 256u;
+            uint32_t d[32];
+            dev::tmem_ld32(at, d);
+            dev::tmem_ld_wait32(d);
+            accumulate(d, f0, f1, acc[0]);
+            dev::tmem_ld32(at + 32u, d);
+            dev::tmem_ld_wait32(d);
+            // all of it is in registers: the accumulator is free for block v + kAcc
+            dev::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) dev::mbar_arrive_remote(leader_ready + ((v + kAcc) % kRing) * 8u);
+            if (in_chunk == kScChunk - 1 || i + 1 == blocks) {
+                if (lane == 0) dev::mbar_arrive(&s.sc_empty[sl]);
+                ++ch;
+            }
+            accumulate(d, f0, f1, acc[1]);
         }
+        ok = __all_sync(0xFFFFFFFFu, ok);
 
-        const int tok = static_cast<int>(rank) * 128 + local;
         const bool mine = ok && tok < t.n;
-        const int64_t row = t.row0 + tok;
         if constexpr (kGated) {
             // acc[c][0..7] gates and acc[c][8..15] ups of 16 hidden channels: h = silu(gate) * up, kept
             // in the gates' place
             float top = 0.0f;
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     float2& g = acc[c][i];
                     g = make_float2(silu_times(g.x, acc[c][i + 8].x), silu_times(g.y, acc[c][i + 8].y));
                     top = fmaxf(top, fmaxf(fabsf(g.x), fabsf(g.y)));
                 }
-            // the other half of the block's channels is with the same lane of the other column warp; a
-            // warp two units ahead has seen the other arrive for the unit between, after its reads
+            // the block's other channels are with the same lane of the other three column warps; a warp
+            // two units ahead has seen the others arrive for the unit between, after their reads
             const int par = nu++ & 1;
             s.amax[par][h][local] = top;
-            dev::named_bar_sync(2 + q, 64);
-            const float scale = __fdiv_rn(fmaxf(s.amax[par][0][local], s.amax[par][1][local]), 448.0f);
+            dev::named_bar_sync(2 + q, 128);
+            const float scale = __fdiv_rn(fmaxf(fmaxf(s.amax[par][0][local], s.amax[par][1][local]),
+                                                fmaxf(s.amax[par][2][local], s.amax[par][3][local])), 448.0f);
             if (mine) {
                 uint8_t* out = p.H + (static_cast<int64_t>(t.pair) * p.rows + row) * 128;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 2; ++c) {
                     uint32_t o[4] = {0u, 0u, 0u, 0u};
                     if (scale > 0.0f) {
 #pragma unroll
@@ -256,35 +241,47 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
                             o[i >> 1] |= e4m3x2(__fdiv_rn(g.x, scale), __fdiv_rn(g.y, scale)) << (16 * (i & 1));
                         }
                     }
-                    *reinterpret_cast<uint4*>(out + (((4 * h + c) ^ static_cast<int>(row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4*>(out + (((2 * h + c) ^ static_cast<int>(row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
                 if (h == 0) p.h_scales[t.pair * p.sstride + row] = scale;
             }
         } else {
+            // 32 tokens x 16 columns at a time through shared memory (the 16-byte piece k of token l at
+            // k ^ (l / 4 % 2): no bank conflicts either way), so that a store covers whole sectors
             auto store = [&]() {
-                if (!mine) return;
-                const float w = p.pair_weight != nullptr ? __ldg(p.pair_weight + p.pair_of[row]) : 1.0f;
-                const int n0 = 256 * t.pair + 128 * h;
-                uint16_t* y = p.Y + row * p.ldy + n0;
+                uint4* stage = s.out[warp - 4];
+                const int first = static_cast<int>(rank) * 128 + 32 * q;   // token of the warp's lane 0
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 4; ++c) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int n = 32 * c + 8 * k;
+                    for (int k = 0; k < 2; ++k) {
                         uint32_t o[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float2 f = acc[c][4 * k + i];
-                            o[i] = pack16(f.x * w, f.y * w, p.bf16);
+                            const float2 f = acc[c >> 1][8 * (c & 1) + 4 * k + i];
+                            o[i] = pack16(f.x * weight, f.y * weight, p.bf16);
                         }
-                        if (p.vec && n0 + n + 8 <= p.N) {
-                            *reinterpret_cast<uint4*>(y + n) = make_uint4(o[0], o[1], o[2], o[3]);
-                        } else {
+                        stage[lane * 2 + (k ^ ((lane >> 2) & 1))] = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                    __syncwarp();
+                    const int n0 = 256 * t.pair + 64 * h + 16 * c;
+                    uint16_t* y = p.Y + (t.row0 + first) * p.ldy + n0;
+                    if (p.vec && n0 + 16 <= p.N) {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                if (n0 + n + j < p.N) y[n + j] = static_cast<uint16_t>(o[j >> 1] >> (16 * (j & 1)));
+                        for (int j = 0; j < 2; ++j) {
+                            const int l = 16 * j + (lane >> 1), k = lane & 1;
+                            if (ok && first + l < t.n)
+                                *reinterpret_cast<uint4*>(y + l * p.ldy + 8 * k) = stage[l * 2 + (k ^ ((l >> 2) & 1))];
+                        }
+                    } else {
+                        for (int j = 0; j < 16; ++j) {
+                            const int l = 2 * j + (lane >> 4), n = lane & 15;
+                            const uint16_t val = reinterpret_cast<const uint16_t*>(&stage[l * 2 + ((n >> 3) ^ ((l >> 2) & 1))])[n & 7];
+                            if (ok && first + l < t.n && n0 + n < p.N) y[l * p.ldy + n] = val;
                         }
                     }
+                    __syncwarp();
+                }
             };
             if (p.splits == 1) {
                 store();
@@ -292,27 +289,27 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
                 // publish this split's sums; the last split to arrive adds all of them in split order
                 auto slot_of = [&](int sp) {
                     return reinterpret_cast<float4*>(p.partial) +
-                           (((static_cast<int64_t>(t.tile) * p.splits + sp) * 2 + rank) * kEpiWarps + (warp - 4)) * (32 * 32) + lane;
+                           (((static_cast<int64_t>(t.tile) * p.splits + sp) * 2 + rank) * kWideEpi + (warp - 4)) * (16 * 32) + lane;
                 };
                 float4* out = slot_of(t.split);
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 2; ++c)
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         __stcg(out + (8 * c + i) * 32, make_float4(acc[c][2 * i].x, acc[c][2 * i].y, acc[c][2 * i + 1].x, acc[c][2 * i + 1].y));
                 __threadfence();
-                dev::named_bar_sync(1, kEpiWarps * 32);
+                dev::named_bar_sync(1, kWideEpi * 32);
                 if (warp == 4 && lane == 0) {
                     int32_t* cnt = p.arrivals + t.tile * 2 + static_cast<int>(rank);
                     const int last = atomicAdd(cnt, 1) == p.splits - 1;
                     if (last) *cnt = 0;   // ready for the next call
                     s.fixup_last = last;
                 }
-                dev::named_bar_sync(1, kEpiWarps * 32);
+                dev::named_bar_sync(1, kWideEpi * 32);
                 if (s.fixup_last) {
                     __threadfence();
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < 2; ++c)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -331,14 +328,11 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
             }
         }
     }
-    if (!ok) {
-        dev::tmem_ld_wait();   // none in flight when TMEM is freed
-        if (lane == 0) fail(p, abort_flag);
-    }
+    if (!ok && lane == 0) fail(p, abort_flag);
 }
 
 template <bool kGated>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
 fp8_wide_kernel(const Params p, const __grid_constant__ CUtensorMap scales) {
     extern __shared__ uint8_t smem_raw[];
     Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -346,18 +340,18 @@ fp8_wide_kernel(const Params p, const __grid_constant__ CUtensorMap scales) {
     const uint32_t rank = dev::cluster_ctarank();
     if (threadIdx.x == 0) {
         dev::tma_prefetch_map(&scales);
-        for (int i = 0; i < kRing; ++i) dev::mbar_init(&s.ready[i], rank == 0 ? 2 + 2 * kEpiWarps : 1);
+        for (int i = 0; i < kRing; ++i) dev::mbar_init(&s.ready[i], rank == 0 ? 2 + 2 * kWideEpi : 1);
         for (int i = 0; i < kStages; ++i) dev::mbar_init(&s.empty[i], 1);
         for (int i = 0; i < kAcc; ++i) dev::mbar_init(&s.acc_full[i], 1);
         for (int i = 0; i < kScSlots; ++i) {
             dev::mbar_init(&s.sc_full[i], 1);
-            dev::mbar_init(&s.sc_empty[i], kEpiWarps);
+            dev::mbar_init(&s.sc_empty[i], kWideEpi);
         }
         dev::mbar_init(&s.mma_done, 1);
         s.abort_flag = 0;
         if (rank == 0)   // the first blocks find their accumulators free
             for (int i = 0; i < kAcc; ++i)
-                for (int k = 0; k < 2 * kEpiWarps; ++k) dev::mbar_arrive(&s.ready[i]);
+                for (int k = 0; k < 2 * kWideEpi; ++k) dev::mbar_arrive(&s.ready[i]);
         dev::fence_barrier_init();
     }
     if (warp == 2) dev::tmem_alloc_pair(&s.tmem_base, kTmemCols);
@@ -370,7 +364,7 @@ fp8_wide_kernel(const Params p, const __grid_constant__ CUtensorMap scales) {
     volatile int* abort_flag = &s.abort_flag;
 
     if (warp < 4) {
-        dev::setmaxnreg_dec<72>();
+        dev::setmaxnreg_dec<32>();
         if (warp == 0) {
             if (lane == 0) producer(p, &scales, s, rank, abort_flag);
         } else if (warp == 1) {
@@ -378,7 +372,7 @@ fp8_wide_kernel(const Params p, const __grid_constant__ CUtensorMap scales) {
         }
         __syncwarp();
     } else {
-        dev::setmaxnreg_inc<216>();   // 128 x 72 + 256 x 216 = the 384 x 168 of the launch
+        dev::setmaxnreg_inc<112>();   // 128 x 32 + 512 x 112 = the 640 x 96 of the launch
         epilogue<kGated>(p, s, rank, warp, lane, tmem, abort_flag);
     }
     dev::tc_fence_before();
@@ -403,7 +397,7 @@ int fp8_resident_pairs(const fp8_layer& L) {
     int pairs = L.num_sms / 2 > 0 ? L.num_sms / 2 : 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
-    cfg.blockDim = dim3(fp8::kThreads);
+    cfg.blockDim = dim3(fp8::kWideThreads);
     cfg.dynamicSmemBytes = fp8::kSmemBytes;
     int clusters = 0;
     if (ensure_smem_limit(reinterpret_cast<const void*>(fp8::fp8_wide_kernel<false>), static_cast<int>(fp8::kSmemBytes)) == cudaSuccess &&
@@ -434,7 +428,7 @@ cudaError_t launch_fp8_wide(const fp8_layer& L, const fp8::Params& p, const floa
     if (e != cudaSuccess) return e;
     const int64_t units = tiles * L.pairs * p.splits;
     const int grid = 2 * static_cast<int>(units < fp8_resident_pairs(L) ? units : fp8_resident_pairs(L));
-    fn<<<grid, fp8::kThreads, fp8::kSmemBytes, stream>>>(p, map);
+    fn<<<grid, fp8::kWideThreads, fp8::kSmemBytes, stream>>>(p, map);
     return cudaGetLastError();
 }
 
