@@ -323,4 +323,63 @@ fmpq_status moe_combine(const void* D, int32_t dtype, int64_t ldd, const void* p
     return launched(fmpq::launch_moe_combine(D, dtype, ldd, p.row_of, T, k, N, Y, ldy, st(stream)));
 }
 
+namespace {
+
+// The parts of moe_experts' scratch buffer: byte offsets.
+struct Scratch {
+    size_t plan, codes, scales, h_codes, h_scales, d, end;
+};
+bool experts_ok(const fp8_layer* up, const fp8_layer* down) {
+    return up != nullptr && down != nullptr && up->gated && !down->gated && up->experts == down->experts &&
+           up->N == 2 * down->K && up->device == down->device;
+}
+Scratch scratch_parts(const fp8_layer* up, const fp8_layer* down, int64_t T, int32_t k) {
+    const int64_t rows = fmpq::moe_rows_of(T, k, up->experts);
+    auto after = [](size_t at, size_t bytes) { return (at + bytes + 255) & ~size_t(255); };
+    Scratch s{};
+    s.plan = 0;
+    s.codes = after(s.plan, moe_plan_bytes(T, k, up->experts));
+    s.scales = after(s.codes, fp8_packed_a_bytes(up, rows));
+    s.h_codes = after(s.scales, fp8_a_scale_count(up, rows) * sizeof(float));
+    s.h_scales = after(s.h_codes, fp8_packed_a_bytes(down, rows));
+    s.d = after(s.h_scales, fp8_a_scale_count(down, rows) * sizeof(float));
+    s.end = after(s.d, static_cast<size_t>(rows) * ((down->N + 7) / 8 * 8) * 2);
+    return s;
+}
+
+}  // namespace
+
+size_t moe_experts_bytes(const fp8_layer* up, const fp8_layer* down, int64_t T, int32_t k) {
+    return experts_ok(up, down) && routing_ok(T, k, up->experts) ? scratch_parts(up, down, T, k).end : 0;
+}
+
+fmpq_status moe_experts(const fp8_layer* up, const fp8_layer* down, const void* X, int32_t dtype, int64_t ldx, int64_t T,
+                        int32_t k, const void* ids, const void* weights, const void* W_up, const void* s_up,
+                        const void* W_down, const void* s_down, void* Y, int64_t ldy, void* scratch, size_t scratch_bytes,
+                        void* stream) {
+    // every step's checks first, so that a refusal launches nothing
+    if (!experts_ok(up, down) || X == nullptr || ids == nullptr || weights == nullptr || W_up == nullptr ||
+        s_up == nullptr || W_down == nullptr || s_down == nullptr || Y == nullptr || !sixteen_bits(dtype))
+        return FMPQ_ERR_INVALID_ARG;
+    if (!routing_ok(T, k, up->experts) || ldx < up->K || ldy < down->N) return FMPQ_ERR_UNSUPPORTED_SHAPE;
+    if (!all_aligned16(W_up, s_up, W_down, s_down) || !element_aligned(X, dtype) || !element_aligned(Y, dtype) ||
+        !element_aligned(ids, FMPQ_DTYPE_F32) || !element_aligned(weights, FMPQ_DTYPE_F32))
+        return FMPQ_ERR_MISALIGNED;
+    const Scratch at = scratch_parts(up, down, T, k);
+    if (scratch == nullptr || scratch_bytes < at.end) return FMPQ_ERR_WORKSPACE;
+    if (!aligned16(scratch)) return FMPQ_ERR_MISALIGNED;
+    if (fmpq_status s = check_device(up)) return s;
+    uint8_t* b = static_cast<uint8_t*>(scratch);
+    const int64_t ldd = (down->N + 7) / 8 * 8;   // 16-byte rows, whatever N is
+    if (fmpq_status s = moe_plan(ids, T, k, up->experts, b + at.plan, stream)) return s;
+    if (fmpq_status s = moe_quantize(up, b + at.plan, T, k, X, dtype, ldx, b + at.codes, b + at.scales, stream)) return s;
+    if (fmpq_status s = moe_up(up, b + at.plan, T, k, b + at.codes, b + at.scales, W_up, s_up, b + at.h_codes,
+                               b + at.h_scales, stream))
+        return s;
+    if (fmpq_status s = moe_down(down, b + at.plan, T, k, weights, b + at.h_codes, b + at.h_scales, W_down, s_down, b + at.d,
+                                 dtype, ldd, stream))
+        return s;
+    return moe_combine(b + at.d, dtype, ldd, b + at.plan, T, k, up->experts, down->N, Y, ldy, stream);
+}
+
 }  // extern "C"

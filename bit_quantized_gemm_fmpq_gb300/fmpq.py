@@ -87,6 +87,8 @@ SIGNATURES = {
     "moe_quantize": (_I32, [_P, _P, _I64, _I32, _P, _I32, _I64, _P, _P, _P]),
     "moe_up": (_I32, [_P, _P, _I64, _I32, _P, _P, _P, _P, _P, _P, _P]),
     "moe_down": (_I32, [_P, _P, _I64, _I32, _P, _P, _P, _P, _P, _P, _I32, _I64, _P]),
+    "moe_experts_bytes": (_SZ, [_P, _P, _I64, _I32]),
+    "moe_experts": (_I32, [_P, _P, _P, _I32, _I64, _I64, _I32, _P, _P, _P, _P, _P, _P, _P, _I64, _P, _SZ, _P]),
     "moe_combine": (_I32, [_P, _I32, _I64, _P, _I64, _I32, _I32, _I32, _P, _I64, _P]),
     "fmpq_status_string": (ctypes.c_char_p, [_I32]),
     "fmpq_version": (_I32, []),
@@ -577,12 +579,17 @@ def qoq_gemm_partials(layout: Layout, A_packed, W_packed, M: int, N: int, m0: in
 
 # ---- E4M3 linear layers: a scale for each block of 128 ------------------------------------
 
+_DTYPES = {}
+
+
 def _dtype_code(t) -> int:
-    import torch
-    codes = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
-    if t not in codes:
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float16: 0, torch.bfloat16: 1, torch.float32: 2})
+    code = _DTYPES.get(t)
+    if code is None:
         raise ValueError(f"unsupported dtype {t}")
-    return codes[t]
+    return code
 
 
 def _need(ok: bool, what: str):
@@ -590,17 +597,27 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _rows16(X, what: str):
-    """A 16-bit CUDA matrix whose rows are contiguous (any row stride)."""
-    import torch
-    _need(X.is_cuda and X.dim() == 2 and X.dtype in (torch.float16, torch.bfloat16),
-          f"{what} must be a 2-D fp16 or bf16 CUDA tensor")
-    _need(X.shape[1] <= 1 or X.stride(1) == 1, f"{what} must have contiguous rows")
+def _rows16(X, what: str) -> int:
+    """A 16-bit CUDA matrix whose rows are contiguous (any row stride). Returns its dtype code."""
+    code = _dtype_code(X.dtype)
+    if not (X.is_cuda and X.dim() == 2 and code < 2):
+        raise ValueError(f"{what} must be a 2-D fp16 or bf16 CUDA tensor")
+    if X.shape[1] > 1 and X.stride(1) != 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    return code
 
 
 def _ld(X) -> int:
     """Row stride in elements (a single row may have any)."""
     return max(X.stride(0), X.shape[1]) if X.shape[0] > 1 else X.shape[1]
+
+
+def _on(X, stream) -> int:
+    """The stream to launch on: the given one, or torch's current one for X's device."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(X.device.index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 class Fp8Layer:
@@ -617,6 +634,7 @@ class Fp8Layer:
         self.nb = -(-K // BLOCK)
         self.scale_rows = 2 * -(-(N // 2) // BLOCK) if gated else -(-N // BLOCK)
         self._workspaces = {}
+        self._workspace_bytes = {}
 
     @property
     def handle(self):
@@ -648,12 +666,15 @@ class Fp8Layer:
         """fp8_gemm's workspace for M rows: zeroed, reused by later calls on the same stream; one that a
         stream capture creates belongs to that graph alone."""
         import torch
-        nbytes = int(self._lib.fp8_gemm_workspace_bytes(self._h, M))
+        nbytes = self._workspace_bytes.get(M)
+        if nbytes is None:
+            nbytes = self._workspace_bytes[M] = int(self._lib.fp8_gemm_workspace_bytes(self._h, M))
         if nbytes == 0:
             return None
         if torch.cuda.is_current_stream_capturing():
             return torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
-        key = (nbytes, _stream(stream).value)
+        key = (nbytes, torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None
+               else stream if isinstance(stream, int) else stream.cuda_stream)
         ws = self._workspaces.get(key)
         if ws is None:
             ws = torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
@@ -744,20 +765,29 @@ def fp8_quantize_gemm(layer: Fp8Layer, X, W_packed, w_scales, A_packed=None, a_s
                       stream=None):
     """The layer on X (fp16 or bf16 [M, K]) in one call: Y [M, N] of X's type."""
     import torch
-    _rows16(X, "X")
-    _need(X.shape[1] == layer.K, "X must be [M, K]")
-    M = X.shape[0]
+    code = _rows16(X, "X")
+    M, K = X.shape
+    _need(K == layer.K, "X must be [M, K]")
     if A_packed is None or a_scales is None:
-        A, s = layer.activations(M, X.device)
-        A_packed, a_scales = A if A_packed is None else A_packed, s if a_scales is None else a_scales
+        # one scratch buffer: codes, then scales
+        codes = layer.nb * M * BLOCK
+        scratch = torch.empty(codes + layer.nb * ((M + 3) // 4 * 16), dtype=torch.uint8, device=X.device)
+        a_ptr = scratch.data_ptr()
+        s_ptr = a_ptr + codes
+    if A_packed is not None:
+        a_ptr = A_packed.data_ptr()
+    if a_scales is not None:
+        s_ptr = a_scales.data_ptr()
     if Y is None:
         Y = torch.empty((M, layer.N), dtype=X.dtype, device=X.device)
-    _rows16(Y, "Y")
-    _need(Y.shape == (M, layer.N) and Y.dtype == X.dtype, "Y must be [M, N] of X's type")
-    workspace, nbytes = _workspace_of(layer, M, workspace, stream)
+    else:
+        _need(_rows16(Y, "Y") == code and Y.shape == (M, layer.N), "Y must be [M, N] of X's type")
+    if workspace is None:
+        workspace = layer.workspace(M, stream)
+    w_ptr, w_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     _check("fp8_quantize_gemm", layer._lib.fp8_quantize_gemm(
-        layer.handle, _ptr(X), _dtype_code(X.dtype), _ld(X), M, _ptr(A_packed), _ptr(a_scales), _ptr(W_packed),
-        _ptr(w_scales), _ptr(Y), _ld(Y), _ptr(workspace), nbytes, _stream(stream)))
+        layer._h, X.data_ptr(), code, _ld(X), M, a_ptr, s_ptr, W_packed.data_ptr(), w_scales.data_ptr(), Y.data_ptr(),
+        _ld(Y), w_ptr, w_bytes, _on(X, stream)))
     return Y
 
 
@@ -769,6 +799,9 @@ def fp8_device_status(layer: Fp8Layer, clear: bool = True) -> int:
 
 # ---- routing to experts -------------------------------------------------------------------
 
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
 def moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1,
               group_top: int = 1, renormalize: bool = True, scale: float = 1.0, ids=None, weights=None, stream=None):
     """The top-k experts of each token from the router's logits [T, E] (fp32, fp16 or bf16): ids int32
@@ -776,20 +809,28 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1
     [E], added for the choice only; groups: keep the top_groups runs of E / groups experts with the
     largest sum of their group_top best keys; renormalize: weights sum to `scale`."""
     import torch
-    _need(score in ("softmax", "sigmoid"), "score must be 'softmax' or 'sigmoid'")
+    sigmoid = _SCORES.get(score)
+    _need(sigmoid is not None, "score must be 'softmax' or 'sigmoid'")
     _need(logits.is_cuda and logits.dim() == 2, "logits must be a 2-D CUDA tensor")
     T, E = logits.shape
     _need(E <= 1 or logits.stride(1) == 1, "logits must have contiguous rows")
+    b_ptr = None
     if bias is not None:
         _need(bias.is_cuda and bias.dtype == torch.float32 and bias.shape == (E,) and (E == 1 or bias.stride(0) == 1),
               "bias must be a contiguous fp32 CUDA tensor [E]")
-    ids = torch.empty((T, k), dtype=torch.int32, device=logits.device) if ids is None else ids
-    weights = torch.empty((T, k), dtype=torch.float32, device=logits.device) if weights is None else weights
-    for t, d in ((ids, torch.int32), (weights, torch.float32)):
-        _need(t.shape == (T, k) and t.dtype == d and t.is_contiguous(), "ids int32 and weights fp32 must be [T, k]")
-    _check("moe_route", load_library().moe_route(
-        _ptr(logits), _dtype_code(logits.dtype), _ld(logits), T, E, k, int(score == "sigmoid"), _ptr(bias), groups,
-        top_groups, group_top, int(renormalize), ctypes.c_float(scale), _ptr(ids), _ptr(weights), _stream(stream)))
+        b_ptr = bias.data_ptr()
+    if ids is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+    else:
+        _need(ids.shape == (T, k) and ids.dtype == torch.int32 and ids.is_contiguous(), "ids must be int32 [T, k]")
+    if weights is None:
+        weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    else:
+        _need(weights.shape == (T, k) and weights.dtype == torch.float32 and weights.is_contiguous(),
+              "weights must be fp32 [T, k]")
+    _check("moe_route", (_lib or load_library()).moe_route(
+        logits.data_ptr(), _dtype_code(logits.dtype), _ld(logits), T, E, k, sigmoid, b_ptr, groups, top_groups, group_top,
+        1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(), _on(logits, stream)))
     return ids, weights
 
 
@@ -898,11 +939,24 @@ def moe_experts(up: Fp8Layer, down: Fp8Layer, X, ids, weights, W_up, s_up, W_dow
     import torch
     _need(up.gated and not down.gated and up.experts == down.experts and up.N == 2 * down.K,
           "up must be the gated layer [2F, K] and down the plain layer [N, F] of the same experts")
-    _need(weights.dtype == torch.float32 and weights.shape == ids.shape and weights.is_contiguous(),
+    code = _rows16(X, "X")
+    T, K = X.shape
+    _need(ids.is_cuda and ids.dim() == 2 and ids.dtype == torch.int32 and ids.is_contiguous() and ids.shape[0] == T and
+          K == up.K, "ids must be a contiguous int32 CUDA tensor [T, k] for X [T, K]")
+    _need(weights.is_cuda and weights.dtype == torch.float32 and weights.shape == ids.shape and weights.is_contiguous(),
           "weights must be contiguous fp32 [T, k]")
-    _need(X.dim() == 2 and ids.dim() == 2 and X.shape[0] == ids.shape[0], "ids must be [T, k] for X [T, K]")
-    plan = moe_plan(ids, up.experts, stream=stream)
-    A, sa = moe_quantize(up, plan, X, stream=stream)
-    H, sh = moe_up(up, plan, A, sa, W_up, s_up, stream=stream)
-    D = moe_down(down, plan, H, sh, W_down, s_down, weights=weights, dtype=X.dtype, stream=stream)
-    return moe_combine(D, plan, stream=stream)
+    k = ids.shape[1]
+    sizes = up._workspace_bytes
+    nbytes = sizes.get((T, k, down))
+    if nbytes is None:
+        nbytes = sizes[(T, k, down)] = int(up._lib.moe_experts_bytes(up._h, down._h, T, k))
+        if nbytes == 0:
+            del sizes[(T, k, down)]
+            raise FmpqError("moe_experts", 2)
+    scratch = torch.empty(nbytes, dtype=torch.uint8, device=X.device)
+    Y = torch.empty((T, down.N), dtype=X.dtype, device=X.device)
+    _check("moe_experts", up._lib.moe_experts(
+        up._h, down._h, X.data_ptr(), code, _ld(X), T, k, ids.data_ptr(), weights.data_ptr(), W_up.data_ptr(),
+        s_up.data_ptr(), W_down.data_ptr(), s_down.data_ptr(), Y.data_ptr(), down.N, scratch.data_ptr(), nbytes,
+        _on(X, stream)))
+    return Y

@@ -547,6 +547,15 @@ FMPQ_API fmpq_status moe_down(const fp8_layer* layer, const void* plan, int64_t 
 FMPQ_API fmpq_status moe_combine(const void* D, int32_t dtype, int64_t ldd, const void* plan, int64_t T, int32_t k,
                                  int32_t E, int32_t N, void* Y, int64_t ldy, void* stream);
 
+/* The routed feed-forward in one call, its steps above in order on `stream`: moe_plan of ids, moe_quantize
+ * of X, moe_up, moe_down with the weights, moe_combine into Y [T][ldy] of X's type. up: gated, [2F][K];
+ * down: [N][F] with the same experts. scratch: moe_experts_bytes, not read before it is written. */
+FMPQ_API size_t moe_experts_bytes(const fp8_layer* up, const fp8_layer* down, int64_t T, int32_t k);
+FMPQ_API fmpq_status moe_experts(const fp8_layer* up, const fp8_layer* down, const void* X, int32_t dtype, int64_t ldx,
+                                 int64_t T, int32_t k, const void* ids, const void* weights, const void* W_up,
+                                 const void* s_up, const void* W_down, const void* s_down, void* Y, int64_t ldy,
+                                 void* scratch, size_t scratch_bytes, void* stream);
+
 /* Static description of a status code. */
 FMPQ_API const char* fmpq_status_string(fmpq_status status);
 
