@@ -45,20 +45,57 @@ __device__ __forceinline__ double warp_sum(double v) {
 
 struct Rules {
     int E, k, groups, top_groups, group_top;
+    bool lanes;   // every group is a power of two of whole lanes
 };
 
-// Two keys computed in FP32 may be closer than their errors: each is within 8 half steps of its
-// value (an exponential, a sum, a quotient and the bias), a group's sum of two within 16.
-__device__ __forceinline__ bool close_call(float hi, float lo) {
-    return hi - lo <= 1.9073486e-6f * fmaxf(1.0f, fmaxf(fabsf(hi), fabsf(lo)));   // 2^-19
+// Two keys computed in FP32 may be closer than their errors. A key's is at most 8e-7 max(1, |key|): the
+// fast exponential and quotient leave 5e-7 of a score (at most 1), adding the bias rounds once.
+__device__ __forceinline__ bool close_call(float hi, float lo, float step) {
+    return hi - lo <= step * fmaxf(1.0f, fmaxf(fabsf(hi), fabsf(lo)));
 }
-__device__ __forceinline__ bool close_call(double, double) { return false; }
+constexpr float kKeyStep = 1.9073486e-6f;     // 2^-19: two keys
+constexpr float kGroupStep = 3.8146973e-6f;   // 2^-18: two sums of two
+__device__ __forceinline__ bool close_call(double, double, float) { return false; }
 
 // Drop the experts outside the best groups: keys of the others become -inf. Lane L holds the
-// experts L * NI .. L * NI + NI - 1. Returns whether a close call decided.
+// experts L * NI .. L * NI + NI - 1. Returns whether a close call decided (check only).
 template <int NI, typename V>
 __device__ __forceinline__ bool keep_best_groups(V (&key)[NI], const Rules& r, int lane, bool check) {
     const int per = r.E / r.groups;
+    if (r.lanes) {
+        // the two best keys of a lane, then of the lanes of its group
+        V b1 = V(kNone), b2 = V(kNone);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const V v = key[i];
+            b2 = v > b1 ? b1 : (v > b2 ? v : b2);
+            b1 = v > b1 ? v : b1;
+        }
+        const int width = per / NI;
+        for (int d = 1; d < width; d <<= 1) {
+            const V o1 = __shfl_xor_sync(kAll, b1, d), o2 = __shfl_xor_sync(kAll, b2, d);
+            const V low = b1 > o1 ? o1 : b1, second = b2 > o2 ? b2 : o2;
+            b2 = low > second ? low : second;
+            b1 = b1 > o1 ? b1 : o1;
+        }
+        const V value = r.group_top == 2 && b2 > V(kNone) ? b1 + b2 : b1;
+        // its place among the groups: the number of better ones, the lower index first among equals
+        const int mine = lane / width;
+        int place = 0;
+        for (int g = 0; g < r.groups; ++g) {
+            const V o = __shfl_sync(kAll, value, g * width);
+            place += (o > value || (o == value && g < mine)) ? 1 : 0;
+        }
+        const bool keep = place < r.top_groups && value > V(kNone);
+        bool close = false;
+        if (check && r.top_groups < r.groups) {
+            const V worst = -warp_max(keep ? -value : V(kNone)), next = warp_max(keep ? V(kNone) : value);
+            close = next > V(kNone) && close_call(worst, next, kGroupStep);
+        }
+#pragma unroll
+        for (int i = 0; i < NI; ++i) key[i] = keep ? key[i] : V(kNone);
+        return close;
+    }
     V mine = V(kNone);   // lane g: the value of group g
     for (int g = 0; g < r.groups; ++g) {
         const int lo = g * per - lane * NI, hi = lo + per;
@@ -93,7 +130,7 @@ __device__ __forceinline__ bool keep_best_groups(V (&key)[NI], const Rules& r, i
     bool close = false;
     if (check) {
         const V next = warp_max(mine);
-        close = next > V(kNone) && close_call(last, next);
+        close = next > V(kNone) && close_call(last, next, kGroupStep);
     }
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
@@ -103,165 +140,228 @@ __device__ __forceinline__ bool keep_best_groups(V (&key)[NI], const Rules& r, i
     return close;
 }
 
-// The k largest keys, the lowest index first among equals: lane j receives the j-th expert and its
-// item's score. `logit` and `bias` tell a true tie (both equal) from a close call.
-template <int NI, typename V>
-__device__ __forceinline__ bool take_top(V (&key)[NI], const float (&score)[NI], const float (&logit)[NI],
-                                         const float* bias, const Rules& r, int lane, bool check, int& my_id,
-                                         float& my_score) {
-    bool close = false;
-    V last = V(kNone);
-    float last_logit = 0.0f, last_bias = 0.0f;
-    const int rounds = check && r.k < r.E ? r.k + 1 : r.k;
-    for (int j = 0; j < rounds; ++j) {
-        V best = key[0];
-        int at = 0;
+// A lane's keys as sorted 64-bit words, largest first: the ordered key above the item's number
+// counted from the end, so that the lowest index comes first among equals (a masked key is the
+// smallest word of all). Odd-even merge sort.
+template <int NI>
+__device__ __forceinline__ void sort_items(const float (&key)[NI], uint64_t (&item)[NI]) {
 #pragma unroll
-        for (int i = 1; i < NI; ++i)
-            if (key[i] > best) { best = key[i]; at = i; }
-        const V m = warp_max(best);
-        if (!(m > V(kNone))) break;
-        const int w = __ffs(__ballot_sync(kAll, best == m)) - 1;
-        at = __shfl_sync(kAll, at, w);
-        float sc = 0.0f, lg = 0.0f;
+    for (int i = 0; i < NI; ++i)
+        item[i] = (static_cast<uint64_t>(key[i] > kNone ? ordered(key[i]) : 0u) << 32) | static_cast<uint32_t>(NI - 1 - i);
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
-            if (i == at) {
-                sc = score[i];
-                lg = logit[i];
-                if (lane == w) key[i] = V(kNone);
-            }
-        const int id = w * NI + at;
-        if (check) {
-            lg = __shfl_sync(kAll, lg, w);
-            const float bs = bias != nullptr ? bias[id] : 0.0f;
-            if (j > 0 && close_call(last, m) && !(lg == last_logit && bs == last_bias)) close = true;
-            last = m;
-            last_logit = lg;
-            last_bias = bs;
-        }
-        sc = __shfl_sync(kAll, sc, w);
-        if (lane == j && j < r.k) {
-            my_id = id;
-            my_score = sc;
-        }
-    }
-    return close;
+    for (int p = 1; p < NI; p <<= 1)
+#pragma unroll
+        for (int q = p; q >= 1; q >>= 1)
+#pragma unroll
+            for (int j = q % p; j + q < NI; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i)
+                    if (i + j + q < NI && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+                        const uint64_t x = item[i + j], y = item[i + j + q];
+                        const bool swap = x < y;
+                        item[i + j] = swap ? y : x;
+                        item[i + j + q] = swap ? x : y;
+                    }
 }
 
-// The same choice with keys in 64 bits, for the tokens where FP32 cannot tell.
+// The k largest keys, the lowest index first among equals: lane j receives the j-th expert.
 template <int NI>
-__device__ __noinline__ void choose_in_64(const float* logit, const float* score, const float* bias, int sigmoid, float top,
-                                          const Rules r, int lane, int* id_out, float* score_out) {
+__device__ __forceinline__ void take_top(const double (&key)[NI], const Rules& r, int lane, int& my_id) {
+    unsigned left = (1u << NI) - 1u;   // this lane's items not taken
+    for (int j = 0; j < r.k; ++j) {
+        double best = static_cast<double>(kNone);
+        int at = 0;
+#pragma unroll 1
+        for (int i = 0; i < NI; ++i)
+            if (((left >> i) & 1u) && key[i] > best) { best = key[i]; at = i; }
+        const double m = warp_max(best);
+        if (!(m > static_cast<double>(kNone))) break;
+        const int w = __ffs(__ballot_sync(kAll, best == m)) - 1;
+        at = __shfl_sync(kAll, at, w);
+        if (lane == w) left &= ~(1u << at);
+        if (lane == j) my_id = w * NI + at;
+    }
+}
+
+// The choice with keys in 64 bits, for the tokens where FP32 cannot tell.
+template <typename T, int NI>
+__device__ __noinline__ int choose_in_64(const T* row, const float* bias, int sigmoid, float top, const Rules r, int lane) {
     double key[NI];
-    float lg[NI], sc[NI];
     double total = 0.0;
 #pragma unroll 1
     for (int i = 0; i < NI; ++i) {
-        lg[i] = logit[i];
-        sc[i] = score[i];
-        const double x = static_cast<double>(lg[i]);
-        double v = 0.0;
-        if (lg[i] > kNone) v = sigmoid ? 1.0 / (1.0 + exp(-x)) : (lg[i] == top ? 1.0 : exp(x - static_cast<double>(top)));
-        key[i] = v;
-        total += v;
-    }
-    if (!sigmoid) {
-        total = warp_sum(total);
-        if (!(total > 0.0)) total = 1.0;
-    } else {
-        total = 1.0;
-    }
-#pragma unroll 1
-    for (int i = 0; i < NI; ++i) {
         const int e = lane * NI + i;
-        double v = key[i] / total;
-        if (e < r.E && bias != nullptr) v += static_cast<double>(bias[e]);
-        key[i] = (lg[i] > kNone && v > kNone) ? v : static_cast<double>(kNone);
+        const float x = e < r.E ? as_float(row[e]) : kNone;
+        double v = static_cast<double>(kNone);
+        if (x > kNone) {
+            v = sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(x)))
+                        : (x == top ? 1.0 : exp(static_cast<double>(x) - static_cast<double>(top)));
+            total += v;
+        }
+        key[i] = v;
     }
+    total = sigmoid ? 1.0 : warp_sum(total);
+#pragma unroll 1
+    for (int i = 0; i < NI; ++i)
+        if (key[i] > static_cast<double>(kNone)) {
+            double v = key[i] / total;
+            if (bias != nullptr) v += static_cast<double>(bias[lane * NI + i]);
+            key[i] = v > static_cast<double>(kNone) ? v : static_cast<double>(kNone);
+        }
     if (r.groups > 1) keep_best_groups<NI, double>(key, r, lane, false);
-    take_top<NI, double>(key, sc, lg, bias, r, lane, false, *id_out, *score_out);
+    int id = -1;
+    take_top<NI>(key, r, lane, id);
+    return id;
+}
+
+// A lane's NI consecutive logits.
+template <typename T, int NI, bool kVec>
+__device__ __forceinline__ void load_logits(const T* row, int E, int lane, float (&logit)[NI]) {
+    if constexpr (kVec) {
+        constexpr int kBytes = NI * static_cast<int>(sizeof(T));
+        constexpr int kWidth = kBytes < 16 ? kBytes : 16;
+        struct alignas(kWidth) Piece {
+            T v[kWidth / sizeof(T)];
+        };
+#pragma unroll
+        for (int i = 0; i < kBytes / kWidth; ++i) {
+            const Piece w = reinterpret_cast<const Piece*>(row + lane * NI)[i];
+#pragma unroll
+            for (int j = 0; j < kWidth / static_cast<int>(sizeof(T)); ++j) logit[i * (kWidth / sizeof(T)) + j] = as_float(w.v[j]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) logit[i] = lane * NI + i < E ? as_float(row[lane * NI + i]) : kNone;
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) logit[i] = logit[i] > kNone ? logit[i] : kNone;   // NaN counts as masked
 }
 
 // A warp a token. NI experts a lane (E <= 32 * NI), in order, so that the lowest lane holds the
-// lowest index.
-template <typename T, int NI>
-__global__ void __launch_bounds__(128) route_kernel(const RouteArgs p) {
+// lowest index. Each lane sorts its items once; a round then takes the largest head (one integer
+// reduction and one ballot). Keys use the fast exponential; a chosen expert's weight is computed
+// again, accurately, by the lane that keeps it.
+template <typename T, int NI, bool kVec>
+__global__ void __launch_bounds__(128) route_kernel(const RouteArgs p, const Rules r) {
     const int lane = threadIdx.x & 31;
-    const Rules r{p.E, p.k, p.groups, p.top_groups, p.group_top};
     const bool by_logit = p.bias == nullptr && (p.groups == 1 || p.group_top == 1);
+    float bias[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) bias[i] = p.bias != nullptr && lane * NI + i < p.E ? p.bias[lane * NI + i] : 0.0f;
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5); t < p.T;
          t += static_cast<int64_t>(gridDim.x) * 4) {
         const T* row = static_cast<const T*>(p.logits) + t * p.ldl;
-        float logit[NI], score[NI], key[NI];
-        float top = kNone;
+        float key[NI];
+        load_logits<T, NI, kVec>(row, p.E, lane, key);
+        float top = kNone, total = 1.0f;
+        if (!p.sigmoid) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int e = lane * NI + i;
-            float v = e < p.E ? as_float(row[e]) : kNone;
-            if (!(v > kNone)) v = kNone;   // NaN counts as masked
-            logit[i] = v;
-            top = fmaxf(top, v);
+            for (int i = 0; i < NI; ++i) top = fmaxf(top, key[i]);
+            top = warp_max(top);
         }
-        top = warp_max(top);
-        if (p.sigmoid) {
+        if (!by_logit || (!p.sigmoid && !p.renormalize)) {
+            float score[NI];
+            if (p.sigmoid) {
 #pragma unroll
-            for (int i = 0; i < NI; ++i) score[i] = logit[i] > kNone ? 1.0f / (1.0f + expf(-logit[i])) : 0.0f;
-        } else {
-            float total = 0.0f;
+                for (int i = 0; i < NI; ++i) score[i] = __fdividef(1.0f, 1.0f + __expf(-key[i]));
+            } else {
+                total = 0.0f;
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                // (an infinite top: it takes all)
-                score[i] = logit[i] > kNone ? (logit[i] == top ? 1.0f : expf(logit[i] - top)) : 0.0f;
-                total += score[i];
+                for (int i = 0; i < NI; ++i) {
+                    // (an infinite top takes all; equal ones share)
+                    score[i] = key[i] == top ? 1.0f : __expf(key[i] - top);
+                    score[i] = key[i] > kNone ? score[i] : 0.0f;
+                    total += score[i];
+                }
+                total = warp_sum(total);
+                total = total > 0.0f ? total : 1.0f;
+                const float inv = 1.0f / total;
+#pragma unroll
+                for (int i = 0; i < NI; ++i) score[i] *= inv;
             }
-            total = warp_sum(total);
-            const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+            if (!by_logit) {
 #pragma unroll
-            for (int i = 0; i < NI; ++i) score[i] *= inv;
-        }
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int e = lane * NI + i;
-            float v = logit[i];
-            if (!by_logit && v > kNone) {
-                v = score[i];
-                if (p.bias != nullptr) v += p.bias[e];
-                if (!(v > kNone)) v = kNone;
+                for (int i = 0; i < NI; ++i) {
+                    const float v = score[i] + bias[i];
+                    key[i] = key[i] > kNone && v > kNone ? v : kNone;
+                }
             }
-            key[i] = v;
         }
-        int id = -1;
-        float sc = 0.0f;
         bool close = false;
         if (p.groups > 1) close = keep_best_groups<NI, float>(key, r, lane, !by_logit);
-        close |= take_top<NI, float>(key, score, logit, p.bias, r, lane, !by_logit, id, sc);
-        if (close) {
-            id = -1;
-            sc = 0.0f;
-            choose_in_64<NI>(logit, score, p.bias, p.sigmoid, top, r, lane, &id, &sc);
+        uint64_t item[NI];
+        sort_items<NI>(key, item);
+        int id = -1;
+        uint32_t mine = 0u;   // lane j: the j-th largest key
+        const int rounds = by_logit || p.k == p.E ? p.k : min(p.k + 1, 32);
+        for (int j = 0; j < rounds; ++j) {
+            const uint32_t head = static_cast<uint32_t>(item[0] >> 32);
+            const uint32_t m = __reduce_max_sync(kAll, head);
+            if (m == 0u) break;
+            const int w = __ffs(__ballot_sync(kAll, head == m)) - 1;
+            const int e = __shfl_sync(kAll, lane * NI + NI - 1 - static_cast<int>(static_cast<uint32_t>(item[0])), w);
+            if (lane == w) {
+#pragma unroll
+                for (int i = 0; i + 1 < NI; ++i) item[i] = item[i + 1];
+                item[NI - 1] = 0u;
+            }
+            if (lane == j) {
+                mine = m;
+                id = e;
+            }
+        }
+        float x = id >= 0 ? as_float(row[id]) : kNone;
+        if (!by_logit) {
+            // neighbours too close for FP32, unless their logits and biases are equal (a true tie)
+            const uint32_t next = __shfl_down_sync(kAll, mine, 1);
+            const float next_x = __shfl_down_sync(kAll, x, 1);
+            const float b = id >= 0 && p.bias != nullptr ? p.bias[id] : 0.0f, next_b = __shfl_down_sync(kAll, b, 1);
+            const bool tight = lane < 31 && mine != 0u && next != 0u && close_call(unordered(mine), unordered(next), kKeyStep) &&
+                               !(x == next_x && b == next_b);
+            // (with k = 32 the 33rd key was not taken: decided in 64 bits)
+            if (__any_sync(kAll, tight) || close || (p.k == 32 && p.E > 32)) {
+                id = choose_in_64<T, NI>(row, p.bias, p.sigmoid, top, r, lane);
+                x = id >= 0 ? as_float(row[id]) : kNone;
+            }
+        }
+        if (lane >= p.k) id = -1;
+        float weight = 0.0f;
+        if (id >= 0) {
+            if (p.sigmoid) weight = 1.0f / (1.0f + expf(-x));
+            else weight = (x == top ? 1.0f : expf(x - top)) / total;
         }
         if (p.renormalize) {
-            const float total = warp_sum(sc);
-            sc = total > 0.0f ? sc / total : 0.0f;
+            const float sum = warp_sum(weight);
+            weight = sum > 0.0f ? weight / sum : 0.0f;
         }
         if (lane < p.k) {
             p.ids[t * p.k + lane] = id;
-            p.weights[t * p.k + lane] = sc * p.scale;
+            p.weights[t * p.k + lane] = weight * p.scale;
         }
     }
+}
+
+template <typename T, int NI>
+cudaError_t route_as(const RouteArgs& a, cudaStream_t stream) {
+    const int per = a.E / a.groups, width = per / NI;
+    const Rules r{a.E, a.k, a.groups, a.top_groups, a.group_top,
+                  a.E == 32 * NI && per % NI == 0 && (width & (width - 1)) == 0};
+    const bool vec = a.E == 32 * NI && a.ldl * static_cast<int64_t>(sizeof(T)) % 16 == 0 &&
+                     (reinterpret_cast<uintptr_t>(a.logits) & 15u) == 0;
+    const int64_t ctas = (a.T + 3) / 4;
+    const int grid = static_cast<int>(ctas < 65535 ? ctas : 65535);
+    if (vec) route_kernel<T, NI, true><<<grid, 128, 0, stream>>>(a, r);
+    else route_kernel<T, NI, false><<<grid, 128, 0, stream>>>(a, r);
+    return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t route_as(const RouteArgs& a, cudaStream_t stream) {
-    const int64_t ctas = (a.T + 3) / 4;
-    const int grid = static_cast<int>(ctas < 65535 ? ctas : 65535);
-    if (a.E <= 32) route_kernel<T, 1><<<grid, 128, 0, stream>>>(a);
-    else if (a.E <= 64) route_kernel<T, 2><<<grid, 128, 0, stream>>>(a);
-    else if (a.E <= 128) route_kernel<T, 4><<<grid, 128, 0, stream>>>(a);
-    else if (a.E <= 256) route_kernel<T, 8><<<grid, 128, 0, stream>>>(a);
-    else route_kernel<T, 16><<<grid, 128, 0, stream>>>(a);
-    return cudaGetLastError();
+    if (a.E <= 32) return route_as<T, 1>(a, stream);
+    if (a.E <= 64) return route_as<T, 2>(a, stream);
+    if (a.E <= 128) return route_as<T, 4>(a, stream);
+    if (a.E <= 256) return route_as<T, 8>(a, stream);
+    return route_as<T, 16>(a, stream);
 }
 
 // ---------------------------------------------------------------- the plan
