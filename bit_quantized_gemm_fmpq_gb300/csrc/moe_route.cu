@@ -49,12 +49,12 @@ struct Rules {
 };
 
 // Two keys computed in FP32 may be closer than their errors. A key's is at most 8e-7 max(1, |key|): the
-// fast exponential and quotient leave 5e-7 of a score (at most 1), adding the bias rounds once.
+// fast exponential and quotient leave 5e-7 of a score (at most 1), adding the bias rounds once. Packing
+// (pack_items) takes the last 4 bits, 1.8e-6 of a key at most.
 __device__ __forceinline__ bool close_call(float hi, float lo, float step) {
     return hi - lo <= step * fmaxf(1.0f, fmaxf(fabsf(hi), fabsf(lo)));
 }
-constexpr float kKeyStep = 1.9073486e-6f;     // 2^-19: two keys
-constexpr float kGroupStep = 3.8146973e-6f;   // 2^-18: two sums of two
+constexpr float kStep = 3.8146973e-6f;   // 2^-18: two packed keys, or two sums of two keys
 __device__ __forceinline__ bool close_call(double, double, float) { return false; }
 
 // Drop the experts outside the best groups: keys of the others become -inf. Lane L holds the
@@ -90,7 +90,7 @@ __device__ __forceinline__ bool keep_best_groups(V (&key)[NI], const Rules& r, i
         bool close = false;
         if (check && r.top_groups < r.groups) {
             const V worst = -warp_max(keep ? -value : V(kNone)), next = warp_max(keep ? V(kNone) : value);
-            close = next > V(kNone) && close_call(worst, next, kGroupStep);
+            close = next > V(kNone) && close_call(worst, next, kStep);
         }
 #pragma unroll
         for (int i = 0; i < NI; ++i) key[i] = keep ? key[i] : V(kNone);
@@ -130,7 +130,7 @@ __device__ __forceinline__ bool keep_best_groups(V (&key)[NI], const Rules& r, i
     bool close = false;
     if (check) {
         const V next = warp_max(mine);
-        close = next > V(kNone) && close_call(last, next, kGroupStep);
+        close = next > V(kNone) && close_call(last, next, kStep);
     }
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
@@ -140,14 +140,14 @@ __device__ __forceinline__ bool keep_best_groups(V (&key)[NI], const Rules& r, i
     return close;
 }
 
-// A lane's keys as sorted 64-bit words, largest first: the ordered key above the item's number
-// counted from the end, so that the lowest index comes first among equals (a masked key is the
-// smallest word of all). Odd-even merge sort.
+// A lane's keys as sorted integers, largest first: the ordered key with its last bits replaced by the
+// item's number counted from the end (the lowest index first among keys that agree in the rest; a
+// masked key is 0). Odd-even merge sort: a comparison is one minimum and one maximum.
 template <int NI>
-__device__ __forceinline__ void sort_items(const float (&key)[NI], uint64_t (&item)[NI]) {
+__device__ __forceinline__ void pack_items(const float (&key)[NI], uint32_t (&item)[NI]) {
 #pragma unroll
     for (int i = 0; i < NI; ++i)
-        item[i] = (static_cast<uint64_t>(key[i] > kNone ? ordered(key[i]) : 0u) << 32) | static_cast<uint32_t>(NI - 1 - i);
+        item[i] = key[i] > kNone ? (ordered(key[i]) & ~static_cast<uint32_t>(NI - 1)) | static_cast<uint32_t>(NI - 1 - i) : 0u;
 #pragma unroll
     for (int p = 1; p < NI; p <<= 1)
 #pragma unroll
@@ -157,10 +157,9 @@ __device__ __forceinline__ void sort_items(const float (&key)[NI], uint64_t (&it
 #pragma unroll
                 for (int i = 0; i < q; ++i)
                     if (i + j + q < NI && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
-                        const uint64_t x = item[i + j], y = item[i + j + q];
-                        const bool swap = x < y;
-                        item[i + j] = swap ? y : x;
-                        item[i + j + q] = swap ? x : y;
+                        const uint32_t x = item[i + j], y = item[i + j + q];
+                        item[i + j] = max(x, y);
+                        item[i + j + q] = min(x, y);
                     }
 }
 
@@ -185,7 +184,8 @@ __device__ __forceinline__ void take_top(const double (&key)[NI], const Rules& r
 
 // The choice with keys in 64 bits, for the tokens where FP32 cannot tell.
 template <typename T, int NI>
-__device__ __noinline__ int choose_in_64(const T* row, const float* bias, int sigmoid, float top, const Rules r, int lane) {
+__device__ __noinline__ int choose_in_64(const T* row, const float* bias, int sigmoid, bool by_logit, float top,
+                                         const Rules r, int lane) {
     double key[NI];
     double total = 0.0;
 #pragma unroll 1
@@ -193,14 +193,16 @@ __device__ __noinline__ int choose_in_64(const T* row, const float* bias, int si
         const int e = lane * NI + i;
         const float x = e < r.E ? as_float(row[e]) : kNone;
         double v = static_cast<double>(kNone);
-        if (x > kNone) {
+        if (x > kNone && by_logit) {
+            v = static_cast<double>(x);
+        } else if (x > kNone) {
             v = sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(x)))
                         : (x == top ? 1.0 : exp(static_cast<double>(x) - static_cast<double>(top)));
             total += v;
         }
         key[i] = v;
     }
-    total = sigmoid ? 1.0 : warp_sum(total);
+    total = sigmoid || by_logit ? 1.0 : warp_sum(total);
 #pragma unroll 1
     for (int i = 0; i < NI; ++i)
         if (key[i] > static_cast<double>(kNone)) {
@@ -212,6 +214,25 @@ __device__ __noinline__ int choose_in_64(const T* row, const float* bias, int si
     int id = -1;
     take_top<NI>(key, r, lane, id);
     return id;
+}
+
+// Lanes 0 .. n - 1 hold experts, their logits x and biases: sort them by the logits, or by the sigmoid keys
+// in 64 bits, the lowest index first among equals.
+__device__ __noinline__ void order_in_64(float x, float b, bool by_logit, int n, int lane, int& id) {
+    double key = static_cast<double>(x);
+    if (!by_logit) key = 1.0 / (1.0 + exp(-key)) + static_cast<double>(b);
+    if (lane >= n) key = static_cast<double>(kNone);
+    int place = 0, from = lane;
+    for (int i = 0; i < n; ++i) {
+        const double o = __shfl_sync(kAll, key, i);
+        const int other = __shfl_sync(kAll, id, i);
+        place += (o > key || (o == key && other < id)) ? 1 : 0;
+    }
+    for (int i = 0; i < n; ++i) {
+        const unsigned who = __ballot_sync(kAll, lane < n && place == i);
+        if (lane == i) from = __ffs(who) - 1;
+    }
+    id = __shfl_sync(kAll, id, from);
 }
 
 // A lane's NI consecutive logits.
@@ -245,6 +266,8 @@ template <typename T, int NI, bool kVec>
 __global__ void __launch_bounds__(128) route_kernel(const RouteArgs p, const Rules r) {
     const int lane = threadIdx.x & 31;
     const bool by_logit = p.bias == nullptr && (p.groups == 1 || p.group_top == 1);
+    // 16-bit logits keep their order when packed: their last bits are the same for all
+    const bool exact = by_logit && sizeof(T) == 2;
     float bias[NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i) bias[i] = p.bias != nullptr && lane * NI + i < p.E ? p.bias[lane * NI + i] : 0.0f;
@@ -289,38 +312,45 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs p, const Rul
         }
         bool close = false;
         if (p.groups > 1) close = keep_best_groups<NI, float>(key, r, lane, !by_logit);
-        uint64_t item[NI];
-        sort_items<NI>(key, item);
+        uint32_t item[NI];
+        pack_items<NI>(key, item);
         int id = -1;
-        uint32_t mine = 0u;   // lane j: the j-th largest key
-        const int rounds = by_logit || p.k == p.E ? p.k : min(p.k + 1, 32);
-        for (int j = 0; j < rounds; ++j) {
-            const uint32_t head = static_cast<uint32_t>(item[0] >> 32);
+        uint32_t mine = 0u, last = 0u;   // lane j: the j-th largest key
+        int taken = 0;
+        for (; taken < 32; ++taken) {
+            const uint32_t head = item[0] & ~static_cast<uint32_t>(NI - 1);
             const uint32_t m = __reduce_max_sync(kAll, head);
             if (m == 0u) break;
-            const int w = __ffs(__ballot_sync(kAll, head == m)) - 1;
-            const int e = __shfl_sync(kAll, lane * NI + NI - 1 - static_cast<int>(static_cast<uint32_t>(item[0])), w);
+            // past the k-th: only while it may be one of them
+            if (taken >= p.k && (exact || !close_call(unordered(last), unordered(m), kStep))) break;
+            last = m;
+            const int w = __ffs(__ballot_sync(kAll, head == m)) - 1;   // the lowest lane with it
+            const uint32_t from_end = __shfl_sync(kAll, item[0], w) & static_cast<uint32_t>(NI - 1);
             if (lane == w) {
 #pragma unroll
                 for (int i = 0; i + 1 < NI; ++i) item[i] = item[i + 1];
                 item[NI - 1] = 0u;
             }
-            if (lane == j) {
+            if (lane == taken) {
                 mine = m;
-                id = e;
+                id = w * NI + NI - 1 - static_cast<int>(from_end);
             }
         }
         float x = id >= 0 ? as_float(row[id]) : kNone;
-        if (!by_logit) {
-            // neighbours too close for FP32, unless their logits and biases are equal (a true tie)
+        if (!exact) {
+            // neighbours too close to tell, unless their logits and biases are equal (a true tie)
             const uint32_t next = __shfl_down_sync(kAll, mine, 1);
             const float next_x = __shfl_down_sync(kAll, x, 1);
             const float b = id >= 0 && p.bias != nullptr ? p.bias[id] : 0.0f, next_b = __shfl_down_sync(kAll, b, 1);
-            const bool tight = lane < 31 && mine != 0u && next != 0u && close_call(unordered(mine), unordered(next), kKeyStep) &&
+            const bool tight = lane < 31 && mine != 0u && next != 0u && close_call(unordered(mine), unordered(next), kStep) &&
                                !(x == next_x && b == next_b);
-            // (with k = 32 the 33rd key was not taken: decided in 64 bits)
-            if (__any_sync(kAll, tight) || close || (p.k == 32 && p.E > 32)) {
-                id = choose_in_64<T, NI>(row, p.bias, p.sigmoid, top, r, lane);
+            const bool any = __any_sync(kAll, tight);
+            if (any && !close && (p.sigmoid || by_logit) && taken < 32) {
+                // every expert that may be among the k is in a lane: put them in the order of their keys in 64 bits
+                order_in_64(x, b, by_logit, taken, lane, id);
+                x = id >= 0 ? as_float(row[id]) : kNone;
+            } else if (any || close) {
+                id = choose_in_64<T, NI>(row, p.bias, p.sigmoid, by_logit, top, r, lane);
                 x = id >= 0 ? as_float(row[id]) : kNone;
             }
         }
@@ -349,7 +379,7 @@ cudaError_t route_as(const RouteArgs& a, cudaStream_t stream) {
     const bool vec = a.E == 32 * NI && a.ldl * static_cast<int64_t>(sizeof(T)) % 16 == 0 &&
                      (reinterpret_cast<uintptr_t>(a.logits) & 15u) == 0;
     const int64_t ctas = (a.T + 3) / 4;
-    const int grid = static_cast<int>(ctas < 65535 ? ctas : 65535);
+    const int grid = static_cast<int>(ctas < 1216 ? ctas : 1216);   // 8 CTAs an SM: a warp keeps its biases
     if (vec) route_kernel<T, NI, true><<<grid, 128, 0, stream>>>(a, r);
     else route_kernel<T, NI, false><<<grid, 128, 0, stream>>>(a, r);
     return cudaGetLastError();
