@@ -57,6 +57,32 @@ __device__ __forceinline__ bool close_call(float hi, float lo, float step) {
 constexpr float kStep = 3.8146973e-6f;   // 2^-18: two packed keys, or two sums of two keys
 __device__ __forceinline__ bool close_call(double, double, float) { return false; }
 
+// Whether this lane's group is among the best, from the two best keys of each lane; b2 becomes the
+// group's second best. Groups are runs of `width` lanes.
+template <typename V>
+__device__ __forceinline__ bool keep_group(V b1, V& b2, const Rules& r, int width, int lane, bool check, bool& close) {
+    for (int d = 1; d < width; d <<= 1) {
+        const V o1 = __shfl_xor_sync(kAll, b1, d), o2 = __shfl_xor_sync(kAll, b2, d);
+        const V low = b1 > o1 ? o1 : b1, second = b2 > o2 ? b2 : o2;
+        b2 = low > second ? low : second;
+        b1 = b1 > o1 ? b1 : o1;
+    }
+    const V value = r.group_top == 2 && b2 > V(kNone) ? b1 + b2 : b1;
+    // its place among the groups: the number of better ones, the lower index first among equals
+    const int mine = lane / width;
+    int place = 0;
+    for (int g = 0; g < r.groups; ++g) {
+        const V o = __shfl_sync(kAll, value, g * width);
+        place += (o > value || (o == value && g < mine)) ? 1 : 0;
+    }
+    const bool keep = place < r.top_groups && value > V(kNone);
+    if (check && r.top_groups < r.groups) {
+        const V worst = -warp_max(keep ? -value : V(kNone)), next = warp_max(keep ? V(kNone) : value);
+        close = next > V(kNone) && close_call(worst, next, kStep);
+    }
+    return keep;
+}
+
 // Drop the experts outside the best groups: keys of the others become -inf. Lane L holds the
 // experts L * NI .. L * NI + NI - 1. Returns whether a close call decided (check only).
 template <int NI, typename V>
@@ -71,27 +97,8 @@ __device__ __forceinline__ bool keep_best_groups(V (&key)[NI], const Rules& r, i
             b2 = v > b1 ? b1 : (v > b2 ? v : b2);
             b1 = v > b1 ? v : b1;
         }
-        const int width = per / NI;
-        for (int d = 1; d < width; d <<= 1) {
-            const V o1 = __shfl_xor_sync(kAll, b1, d), o2 = __shfl_xor_sync(kAll, b2, d);
-            const V low = b1 > o1 ? o1 : b1, second = b2 > o2 ? b2 : o2;
-            b2 = low > second ? low : second;
-            b1 = b1 > o1 ? b1 : o1;
-        }
-        const V value = r.group_top == 2 && b2 > V(kNone) ? b1 + b2 : b1;
-        // its place among the groups: the number of better ones, the lower index first among equals
-        const int mine = lane / width;
-        int place = 0;
-        for (int g = 0; g < r.groups; ++g) {
-            const V o = __shfl_sync(kAll, value, g * width);
-            place += (o > value || (o == value && g < mine)) ? 1 : 0;
-        }
-        const bool keep = place < r.top_groups && value > V(kNone);
         bool close = false;
-        if (check && r.top_groups < r.groups) {
-            const V worst = -warp_max(keep ? -value : V(kNone)), next = warp_max(keep ? V(kNone) : value);
-            close = next > V(kNone) && close_call(worst, next, kStep);
-        }
+        const bool keep = keep_group<V>(b1, b2, r, per / NI, lane, check, close);
 #pragma unroll
         for (int i = 0; i < NI; ++i) key[i] = keep ? key[i] : V(kNone);
         return close;
@@ -216,6 +223,26 @@ __device__ __noinline__ int choose_in_64(const T* row, const float* bias, int si
     return id;
 }
 
+// keep_group with sigmoid keys in 64 bits of the lane's items in `need` (those that may be among a
+// group's two best).
+template <typename T, int NI>
+__device__ __noinline__ bool keep_group_in_64(const T* row, const float* bias, unsigned need, const Rules r, int lane) {
+    double b1 = static_cast<double>(kNone), b2 = b1;
+    while (__any_sync(kAll, need != 0u)) {
+        if (need != 0u) {
+            const int e = lane * NI + __ffs(need) - 1;
+            double v = 1.0 / (1.0 + exp(-static_cast<double>(as_float(row[e]))));
+            if (bias != nullptr) v += static_cast<double>(bias[e]);
+            b2 = v > b1 ? b1 : (v > b2 ? v : b2);
+            b1 = v > b1 ? v : b1;
+            need &= need - 1u;
+        }
+        __syncwarp();
+    }
+    bool close = false;
+    return keep_group<double>(b1, b2, r, r.E / r.groups / NI, lane, false, close);
+}
+
 // Lanes 0 .. n - 1 hold experts, their logits x and biases: sort them by the logits, or by the sigmoid keys
 // in 64 bits, the lowest index first among equals.
 __device__ __noinline__ void order_in_64(float x, float b, bool by_logit, int n, int lane, int& id) {
@@ -233,6 +260,14 @@ __device__ __noinline__ void order_in_64(float x, float b, bool by_logit, int n,
         if (lane == i) from = __ffs(who) - 1;
     }
     id = __shfl_sync(kAll, id, from);
+}
+
+// Within 5e-7 of the sigmoid (results below the smallest normal number become 0).
+__device__ __forceinline__ float fast_sigmoid(float x) {
+    float e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+    return s;
 }
 
 // A lane's NI consecutive logits.
@@ -286,7 +321,7 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs p, const Rul
             float score[NI];
             if (p.sigmoid) {
 #pragma unroll
-                for (int i = 0; i < NI; ++i) score[i] = __fdividef(1.0f, 1.0f + __expf(-key[i]));
+                for (int i = 0; i < NI; ++i) score[i] = fast_sigmoid(key[i]);
             } else {
                 total = 0.0f;
 #pragma unroll
@@ -311,7 +346,27 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs p, const Rul
             }
         }
         bool close = false;
-        if (p.groups > 1) close = keep_best_groups<NI, float>(key, r, lane, !by_logit);
+        if (p.groups > 1 && r.lanes) {
+            float b1 = kNone, b2 = kNone;   // the lane's two best keys
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                b2 = fmaxf(b2, fminf(b1, key[i]));
+                b1 = fmaxf(b1, key[i]);
+            }
+            bool keep = keep_group<float>(b1, b2, r, p.E / p.groups / NI, lane, !by_logit, close);
+            if (close && p.sigmoid) {
+                unsigned need = 0u;
+#pragma unroll
+                for (int i = 0; i < NI; ++i)
+                    if (key[i] > kNone && (key[i] >= b2 || close_call(b2, key[i], kStep))) need |= 1u << i;
+                keep = keep_group_in_64<T, NI>(row, p.bias, need, r, lane);
+                close = false;
+            }
+#pragma unroll
+            for (int i = 0; i < NI; ++i) key[i] = keep ? key[i] : kNone;
+        } else if (p.groups > 1) {
+            close = keep_best_groups<NI, float>(key, r, lane, !by_logit);
+        }
         uint32_t item[NI];
         pack_items<NI>(key, item);
         int id = -1;
