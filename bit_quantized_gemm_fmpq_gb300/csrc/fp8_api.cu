@@ -146,16 +146,26 @@ fmpq_status fp8_quantize(const fp8_layer* L, const void* X, int32_t dtype, int64
     if (!all_aligned16(A_packed, a_scales) || !element_aligned(X, dtype)) return FMPQ_ERR_MISALIGNED;
     if (fmpq_status s = check_device(L)) return s;
     return launched(fmpq::launch_fp8_quantize(X, dtype, ldx, M, L->K, nullptr, 1, M, A_packed,
-                                              static_cast<float*>(a_scales), L->num_sms, st(stream)));
+                                              static_cast<float*>(a_scales), L->num_sms, false, st(stream)));
 }
 
 size_t fp8_gemm_workspace_bytes(const fp8_layer* L, int64_t M) {
     return L && M > 0 ? fmpq::fp8_gemm_workspace(*L, M) : 0;
 }
 
+static fmpq_status gemm_after(const fp8_layer* L, const void* A_packed, const void* a_scales, const void* W_packed,
+                              const void* w_scales, int64_t M, void* Y, int32_t dtype, int64_t ldy, void* workspace,
+                              size_t workspace_bytes, bool pdl, void* stream);
+
 fmpq_status fp8_gemm(const fp8_layer* L, const void* A_packed, const void* a_scales, const void* W_packed,
                      const void* w_scales, int64_t M, void* Y, int32_t dtype, int64_t ldy, void* workspace,
                      size_t workspace_bytes, void* stream) {
+    return gemm_after(L, A_packed, a_scales, W_packed, w_scales, M, Y, dtype, ldy, workspace, workspace_bytes, false, stream);
+}
+
+static fmpq_status gemm_after(const fp8_layer* L, const void* A_packed, const void* a_scales, const void* W_packed,
+                              const void* w_scales, int64_t M, void* Y, int32_t dtype, int64_t ldy, void* workspace,
+                              size_t workspace_bytes, bool pdl, void* stream) {
     if (L == nullptr || A_packed == nullptr || a_scales == nullptr || W_packed == nullptr || w_scales == nullptr ||
         Y == nullptr || !sixteen_bits(dtype) || L->gated || L->experts != 1)
         return FMPQ_ERR_INVALID_ARG;
@@ -176,6 +186,7 @@ fmpq_status fp8_gemm(const fp8_layer* L, const void* A_packed, const void* a_sca
     a.dtype = dtype;
     a.ldy = ldy;
     a.workspace = need > 0 ? workspace : nullptr;
+    a.pdl = pdl;
     return launched(fmpq::launch_fp8_gemm(*L, a, st(stream)));
 }
 
@@ -193,7 +204,7 @@ fmpq_status fp8_quantize_gemm(const fp8_layer* L, const void* X, int32_t dtype, 
     if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return FMPQ_ERR_WORKSPACE;
     if (need > 0 && !aligned16(workspace)) return FMPQ_ERR_MISALIGNED;
     if (fmpq_status s = fp8_quantize(L, X, dtype, ldx, M, A_packed, a_scales, stream)) return s;
-    return fp8_gemm(L, A_packed, a_scales, W_packed, w_scales, M, Y, dtype, ldy, workspace, workspace_bytes, stream);
+    return gemm_after(L, A_packed, a_scales, W_packed, w_scales, M, Y, dtype, ldy, workspace, workspace_bytes, true, stream);
 }
 
 // ---------------------------------------------------------------- routing and experts
@@ -249,8 +260,8 @@ fmpq_status moe_plan(const void* ids, int64_t T, int32_t k, int32_t E, void* pla
                                           p + 2 * E + T * k + fmpq::moe_rows_of(T, k, E), st(stream)));
 }
 
-fmpq_status moe_quantize(const fp8_layer* L, const void* plan, int64_t T, int32_t k, const void* X, int32_t dtype,
-                         int64_t ldx, void* A_packed, void* a_scales, void* stream) {
+static fmpq_status quantize_after(const fp8_layer* L, const void* plan, int64_t T, int32_t k, const void* X, int32_t dtype,
+                         int64_t ldx, void* A_packed, void* a_scales, bool pdl, void* stream) {
     if (L == nullptr || plan == nullptr || X == nullptr || A_packed == nullptr || a_scales == nullptr || !sixteen_bits(dtype))
         return FMPQ_ERR_INVALID_ARG;
     if (!routing_ok(T, k, L->experts) || ldx < L->K) return FMPQ_ERR_UNSUPPORTED_SHAPE;
@@ -258,11 +269,15 @@ fmpq_status moe_quantize(const fp8_layer* L, const void* plan, int64_t T, int32_
     if (fmpq_status s = check_device(L)) return s;
     const fmpq::MoePlan p = fmpq::moe_plan_parts(plan, T, k, L->experts);
     return launched(fmpq::launch_fp8_quantize(X, dtype, ldx, T, L->K, p.row_of, k, fmpq::moe_rows_of(T, k, L->experts),
-                                              A_packed, static_cast<float*>(a_scales), L->num_sms, st(stream)));
+                                              A_packed, static_cast<float*>(a_scales), L->num_sms, pdl, st(stream)));
+}
+fmpq_status moe_quantize(const fp8_layer* L, const void* plan, int64_t T, int32_t k, const void* X, int32_t dtype,
+                         int64_t ldx, void* A_packed, void* a_scales, void* stream) {
+    return quantize_after(L, plan, T, k, X, dtype, ldx, A_packed, a_scales, false, stream);
 }
 
-fmpq_status moe_up(const fp8_layer* L, const void* plan, int64_t T, int32_t k, const void* A_packed, const void* a_scales,
-                   const void* W_packed, const void* w_scales, void* H_packed, void* h_scales, void* stream) {
+static fmpq_status up_after(const fp8_layer* L, const void* plan, int64_t T, int32_t k, const void* A_packed, const void* a_scales,
+                   const void* W_packed, const void* w_scales, void* H_packed, void* h_scales, bool pdl, void* stream) {
     if (L == nullptr || plan == nullptr || A_packed == nullptr || a_scales == nullptr || W_packed == nullptr ||
         w_scales == nullptr || H_packed == nullptr || h_scales == nullptr || !L->gated)
         return FMPQ_ERR_INVALID_ARG;
@@ -282,12 +297,17 @@ fmpq_status moe_up(const fp8_layer* L, const void* plan, int64_t T, int32_t k, c
     a.pairs_routed = T * k;
     a.H = H_packed;
     a.h_scales = static_cast<float*>(h_scales);
+    a.pdl = pdl;
     return launched(fmpq::launch_fp8_gemm(*L, a, st(stream)));
 }
+fmpq_status moe_up(const fp8_layer* L, const void* plan, int64_t T, int32_t k, const void* A_packed, const void* a_scales,
+                   const void* W_packed, const void* w_scales, void* H_packed, void* h_scales, void* stream) {
+    return up_after(L, plan, T, k, A_packed, a_scales, W_packed, w_scales, H_packed, h_scales, false, stream);
+}
 
-fmpq_status moe_down(const fp8_layer* L, const void* plan, int64_t T, int32_t k, const void* weights, const void* A_packed,
+static fmpq_status down_after(const fp8_layer* L, const void* plan, int64_t T, int32_t k, const void* weights, const void* A_packed,
                      const void* a_scales, const void* W_packed, const void* w_scales, void* D, int32_t dtype, int64_t ldd,
-                     void* stream) {
+                     bool pdl, void* stream) {
     if (L == nullptr || plan == nullptr || A_packed == nullptr || a_scales == nullptr || W_packed == nullptr ||
         w_scales == nullptr || D == nullptr || !sixteen_bits(dtype) || L->gated)
         return FMPQ_ERR_INVALID_ARG;
@@ -311,16 +331,26 @@ fmpq_status moe_down(const fp8_layer* L, const void* plan, int64_t T, int32_t k,
     a.Y = D;
     a.dtype = dtype;
     a.ldy = ldd;
+    a.pdl = pdl;
     return launched(fmpq::launch_fp8_gemm(*L, a, st(stream)));
 }
+fmpq_status moe_down(const fp8_layer* L, const void* plan, int64_t T, int32_t k, const void* weights, const void* A_packed,
+                     const void* a_scales, const void* W_packed, const void* w_scales, void* D, int32_t dtype, int64_t ldd,
+                     void* stream) {
+    return down_after(L, plan, T, k, weights, A_packed, a_scales, W_packed, w_scales, D, dtype, ldd, false, stream);
+}
 
-fmpq_status moe_combine(const void* D, int32_t dtype, int64_t ldd, const void* plan, int64_t T, int32_t k, int32_t E,
-                        int32_t N, void* Y, int64_t ldy, void* stream) {
+static fmpq_status combine_after(const void* D, int32_t dtype, int64_t ldd, const void* plan, int64_t T, int32_t k, int32_t E,
+                        int32_t N, void* Y, int64_t ldy, bool pdl, void* stream) {
     if (D == nullptr || plan == nullptr || Y == nullptr || !sixteen_bits(dtype)) return FMPQ_ERR_INVALID_ARG;
     if (!routing_ok(T, k, E) || N < 1 || N > FP8_MAX_N || ldd < N || ldy < N) return FMPQ_ERR_UNSUPPORTED_SHAPE;
     if (!aligned16(plan) || !element_aligned(D, dtype) || !element_aligned(Y, dtype)) return FMPQ_ERR_MISALIGNED;
     const fmpq::MoePlan p = fmpq::moe_plan_parts(plan, T, k, E);
-    return launched(fmpq::launch_moe_combine(D, dtype, ldd, p.row_of, T, k, N, Y, ldy, st(stream)));
+    return launched(fmpq::launch_moe_combine(D, dtype, ldd, p.row_of, T, k, N, Y, ldy, pdl, st(stream)));
+}
+fmpq_status moe_combine(const void* D, int32_t dtype, int64_t ldd, const void* plan, int64_t T, int32_t k, int32_t E,
+                        int32_t N, void* Y, int64_t ldy, void* stream) {
+    return combine_after(D, dtype, ldd, plan, T, k, E, N, Y, ldy, false, stream);
 }
 
 namespace {
@@ -372,14 +402,14 @@ fmpq_status moe_experts(const fp8_layer* up, const fp8_layer* down, const void* 
     uint8_t* b = static_cast<uint8_t*>(scratch);
     const int64_t ldd = (down->N + 7) / 8 * 8;   // 16-byte rows, whatever N is
     if (fmpq_status s = moe_plan(ids, T, k, up->experts, b + at.plan, stream)) return s;
-    if (fmpq_status s = moe_quantize(up, b + at.plan, T, k, X, dtype, ldx, b + at.codes, b + at.scales, stream)) return s;
-    if (fmpq_status s = moe_up(up, b + at.plan, T, k, b + at.codes, b + at.scales, W_up, s_up, b + at.h_codes,
-                               b + at.h_scales, stream))
+    if (fmpq_status s = quantize_after(up, b + at.plan, T, k, X, dtype, ldx, b + at.codes, b + at.scales, true, stream)) return s;
+    if (fmpq_status s = up_after(up, b + at.plan, T, k, b + at.codes, b + at.scales, W_up, s_up, b + at.h_codes,
+                               b + at.h_scales, true, stream))
         return s;
-    if (fmpq_status s = moe_down(down, b + at.plan, T, k, weights, b + at.h_codes, b + at.h_scales, W_down, s_down, b + at.d,
-                                 dtype, ldd, stream))
+    if (fmpq_status s = down_after(down, b + at.plan, T, k, weights, b + at.h_codes, b + at.h_scales, W_down, s_down, b + at.d,
+                                 dtype, ldd, true, stream))
         return s;
-    return moe_combine(b + at.d, dtype, ldd, b + at.plan, T, k, up->experts, down->N, Y, ldy, stream);
+    return combine_after(b + at.d, dtype, ldd, b + at.plan, T, k, up->experts, down->N, Y, ldy, true, stream);
 }
 
 }  // extern "C"

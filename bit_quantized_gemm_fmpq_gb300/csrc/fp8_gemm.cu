@@ -11,17 +11,18 @@
 // 256 x 256 pair tile of long prompts reads each operand byte half as often as two single CTAs.
 //   * P is an FP32 accumulator tile in TMEM for one block of 128 (4 MMAs); 2, 4 or 8 of them, so that
 //     the next blocks' MMAs run while the epilogue scales this one into FP32 registers.
-//   * An epilogue thread owns one weight row (a TMEM lane) and half of the tile's tokens. Two scaler
-//     warps multiply the block's token scales by its weight scale beforehand, so that a pair of
+//   * An epilogue thread owns one weight row (a TMEM lane) and half of the tile's tokens. A scaler
+//     warp multiplies the block's token scales by its weight scale beforehand, so that a pair of
 //     sums costs one packed multiply-add and half a broadcast shared load.
 //   * A gated layer's rows are packed so that a warp holds the gate and the up rows of the same 16
 //     hidden channels in its two halves: SwiGLU and the E4M3 quantization of the hidden vector
 //     happen in registers, with one absmax per token exchanged inside the pair.
 //
 // Warp roles (384 threads, one CTA per SM, pairs persistent over tiles):
-//   warp 0      producer: weight block, token codes, token scales (a chunk of blocks at a time)
+//   warp 0      weight producer (a 16 KB block a copy)
 //   warp 1      even CTA: MMA issuer; odd CTA: reports its operands to the even one
-//   warps 2-3   scalers (blocks in turn); warp 2 also allocates and frees TMEM
+//   warp 2      scaler; also allocates and frees TMEM
+//   warp 3      token producer: codes and scales of four blocks at a time
 //   warps 4-11  epilogue: TMEM lane quarter warp % 4, half of the tile's tokens each
 #include "fp8_gemm.cuh"
 
@@ -37,23 +38,27 @@ constexpr int kMaxAcc = 8;
 template <int kC>
 struct Shape {
     static constexpr int kTokens = 64 * kC;
-    static constexpr int kAcc = kC == 1 ? 8 : 4;   // accumulators of kTokens columns in 512
+    static constexpr int kAcc = kC == 1 ? 8 : 4;      // accumulators of kTokens columns in 512
+    static constexpr int kStages = kC == 1 ? 8 : 6;   // weight blocks in flight
 };
 
 template <int kC>
 struct __align__(1024) Smem {
     static constexpr int kT = Shape<kC>::kTokens;
-    uint8_t w[kStages][kTileBytes];   // weight block: this CTA's 128 rows
-    uint8_t x[kStages][kT * 64];      // token codes: this CTA's half of the tile
-    float sx[kScSlots][kScChunk][kT]; // token scales
+    static constexpr int kStages = Shape<kC>::kStages;
+    uint8_t w[kStages][kTileBytes];              // weight block: this CTA's 128 rows
+    uint8_t x[kScSlots][kScChunk][kT * 64];      // token codes of a chunk of blocks: this CTA's half of the tile
+    float sx[kScSlots][kScChunk][kT];            // token scales of the chunk
     // token scales times the block's weight scale; gated: [0] gate, [1] up (the 16-byte skew keeps
     // the two halves of a warp in different banks)
     float prod[kProd][2][kT + 4];
     // gated: absmax of 16 hidden channels (a quarter's), of this CTA's 64 and the peer's 64, the
     // tokens' scales
     float amax[4][kT], amax_peer[2][kT], hscale[kT];
-    // ready[b % kRing], even CTA: block b's operands have landed in both CTAs and its accumulator has
-    // been read (by both CTAs' epilogue warps). Odd CTA: its operands have landed.
+    // ready[b % kRing], even CTA: block b's weights have landed in both CTAs, the odd one's token codes
+    // too, and its accumulator has been read (by both CTAs' epilogue warps). Odd CTA: its weights have
+    // landed. sc_full: a chunk's token codes and scales have landed here; sc_empty: the scaler has read the
+    // scales and the chunk's MMAs are done.
     uint64_t ready[kRing];
     uint64_t empty[kStages];
     uint64_t acc_full[kMaxAcc];
@@ -74,84 +79,110 @@ __device__ __forceinline__ Unit unit(const Params& p, const Smem<kC>& s, int u) 
 // Columns of a tile's MMAs: its tokens rounded up to 32.
 __device__ __forceinline__ int columns(const Unit& t) { return max(32, (t.n + 31) & ~31); }
 
-// ---------------------------------------------------------------- producer (warp 0, one thread)
+// ---------------------------------------------------------------- producers (warps 0 and 3)
+// Whole warps, one elected lane issuing: with one lane alone in the loop the addresses leave the uniform
+// registers and a block took about 600 clk of issue. Warp 0 streams the weights, which no earlier kernel
+// writes, from the start.
 template <int kC>
-__device__ __forceinline__ void producer(const Params& p, const CUtensorMap* scales, Smem<kC>& s, uint32_t rank,
-                                         volatile int* abort_flag) {
+__device__ __forceinline__ void weight_producer(const Params& p, Smem<kC>& s, uint32_t rank, volatile int* abort_flag) {
+    constexpr int kStages = Shape<kC>::kStages;
     const int units = unit_count<Shape<kC>::kTokens>(p, s.tables);
-    uint32_t it = 0, ch = 0;
+    uint32_t it = 0;
     bool ok = true;
     for (int u = blockIdx.x >> 1; ok && u < units; u += gridDim.x >> 1) {
         const Unit t = unit<kC>(p, s, u);
-        const int half = columns(t) >> 1, local = static_cast<int>(rank) * half;
-        const uint32_t xbytes = static_cast<uint32_t>(max(0, min(half, t.n - local))) * 128u;
         const uint8_t* w = weight_block(p, t, rank);
-        const uint8_t* x = p.A + (t.row0 + local + t.b0 * p.rows) * 128;
-        for (int b = t.b0; b < t.b1; ++b, ++it) {
-            if ((b - t.b0) % kScChunk == 0) {
-                const int sl = ch % kScSlots;
-                ok = dev::mbar_wait(&s.sc_empty[sl], ((ch / kScSlots) & 1) ^ 1, abort_flag);
-                if (!ok) break;
-                dev::mbar_arrive_expect_tx(&s.sc_full[sl], sizeof(s.sx[0]));
-                dev::tma_load_2d(s.sx[sl], scales, static_cast<int>(t.row0), b, &s.sc_full[sl]);
-                ++ch;
-            }
+        for (int b = t.b0; b < t.b1; ++b, ++it, w += kTileBytes) {
             const int st = it % kStages;
-            ok = dev::mbar_wait(&s.empty[st], ((it / kStages) & 1) ^ 1, abort_flag);
+            ok = __all_sync(0xFFFFFFFFu, dev::mbar_wait(&s.empty[st], ((it / kStages) & 1) ^ 1, abort_flag));
             if (!ok) break;
-            uint64_t* bar = &s.ready[it % kRing];
-            dev::mbar_arrive_expect_tx(bar, kTileBytes + xbytes);
-            dev::bulk_g2s(s.w[st], w, kTileBytes, bar);
-            if (xbytes > 0) dev::bulk_g2s(s.x[st], x, xbytes, bar);
-            w += kTileBytes;
-            x += p.rows * 128;
+            if (elect_one()) {
+                uint64_t* bar = &s.ready[it % kRing];
+                dev::mbar_arrive_expect_tx(bar, kTileBytes);
+                dev::bulk_g2s(s.w[st], w, kTileBytes, bar);
+            }
+            __syncwarp();
         }
     }
-    if (!ok) fail(p, abort_flag);
+    if (!ok && elect_one()) fail(p, abort_flag);
     // the copies in flight must land before the CTA's shared memory is given up (after an abort the
     // even CTA's readiness may never be complete: a short bound, far longer than a copy)
     for (uint32_t k = 0; k < kStages && k < it; ++k) {
         const uint32_t i = it - 1 - k;
         dev::mbar_wait(&s.ready[i % kRing], (i / kRing) & 1, nullptr, ok ? dev::kMaxPolls : 1u << 16);
     }
+}
+
+// Warp 3: the token codes and scales of kScChunk blocks at a time, one box each.
+template <int kC>
+__device__ __forceinline__ void token_producer(const Params& p, const CUtensorMap* codes, const CUtensorMap* scales,
+                                               Smem<kC>& s, uint32_t rank, volatile int* abort_flag) {
+    const int units = unit_count<Shape<kC>::kTokens>(p, s.tables);
+    uint32_t ch = 0;
+    bool ok = true;
+    dev::pdl_wait();                // the codes and scales come from the kernel before
+    dev::pdl_launch_dependents();   // (after the wait: see Fp8GemmArgs::pdl)
+    for (int u = blockIdx.x >> 1; ok && u < units; u += gridDim.x >> 1) {
+        const Unit t = unit<kC>(p, s, u);
+        const int row = static_cast<int>(t.row0), mine = row + static_cast<int>(rank) * (columns(t) >> 1);
+        for (int b = t.b0; b < t.b1; b += kScChunk, ++ch) {
+            const int sl = ch % kScSlots;
+            ok = __all_sync(0xFFFFFFFFu, dev::mbar_wait(&s.sc_empty[sl], ((ch / kScSlots) & 1) ^ 1, abort_flag));
+            if (!ok) break;
+            if (elect_one()) {
+                dev::mbar_arrive_expect_tx(&s.sc_full[sl], sizeof(s.sx[0]) + sizeof(s.x[0]));
+                dev::tma_load_3d(s.x[sl], codes, 0, mine, b, &s.sc_full[sl]);
+                dev::tma_load_2d(s.sx[sl], scales, row, b, &s.sc_full[sl]);
+            }
+            __syncwarp();
+        }
+    }
+    if (!ok && elect_one()) fail(p, abort_flag);
     for (uint32_t k = 0; k < kScSlots && k < ch; ++k) {
         const uint32_t i = ch - 1 - k;
         dev::mbar_wait(&s.sc_full[i % kScSlots], (i / kScSlots) & 1, nullptr);
     }
 }
 
-// ---------------------------------------------------------------- MMA (warp 1, one thread)
+// ---------------------------------------------------------------- MMA (warp 1)
 template <int kC>
 __device__ __forceinline__ void mma_issuer(const Params& p, Smem<kC>& s, uint32_t rank, uint32_t tmem,
                                            volatile int* abort_flag) {
     constexpr int kAcc = Shape<kC>::kAcc;
     const int units = unit_count<Shape<kC>::kTokens>(p, s.tables);
     const uint32_t leader = dev::mapa(&s.ready[0], 0);
-    const uint64_t w0 = dev::sdesc_k_sw128(dev::smem_u32(s.w[0])), x0 = dev::sdesc_k_sw128(dev::smem_u32(s.x[0]));
-    uint32_t it = 0, st = 0;
+    const uint64_t w0 = dev::sdesc_k_sw128(dev::smem_u32(s.w[0])), x0 = dev::sdesc_k_sw128(dev::smem_u32(s.x[0][0]));
+    uint32_t it = 0, st = 0, ch = 0;
     bool ok = true;
     for (int u = blockIdx.x >> 1; ok && u < units; u += gridDim.x >> 1) {
         const Unit t = unit<kC>(p, s, u);
         const uint32_t idesc = dev::idesc_e4m3_f32(256, static_cast<uint32_t>(columns(t)));
         for (int b = t.b0; b < t.b1; ++b, ++it) {
-            ok = __all_sync(0xFFFFFFFFu, dev::mbar_wait(&s.ready[it % kRing], (it / kRing) & 1, abort_flag));
+            const int in_chunk = (b - t.b0) % kScChunk, sl = ch % kScSlots;
+            const bool chunk_ends = in_chunk == kScChunk - 1 || b + 1 == t.b1;
+            bool there = in_chunk != 0 || dev::mbar_wait(&s.sc_full[sl], (ch / kScSlots) & 1, abort_flag);
+            there = there && dev::mbar_wait(&s.ready[it % kRing], (it / kRing) & 1, abort_flag);
+            ok = __all_sync(0xFFFFFFFFu, there);
             if (!ok) break;
+            if (chunk_ends) ++ch;
             if (rank != 0) {
                 if (elect_one()) dev::mbar_arrive_remote(leader + (it % kRing) * 8u);
+                __syncwarp();
                 continue;
             }
             dev::tc_fence_after();
             // (a descriptor's address field counts 16 bytes)
-            const uint64_t ad = w0 + st * (kTileBytes / 16), bd = x0 + st * (Shape<kC>::kTokens * 4);
+            const uint64_t ad = w0 + st * (kTileBytes / 16), bd = x0 + (sl * kScChunk + in_chunk) * (Shape<kC>::kTokens * 4);
             const uint32_t d = tmem + (it % kAcc) * Shape<kC>::kTokens;
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) dev::mma_e4m3_pair(d, ad + 2 * k, bd + 2 * k, idesc, k > 0 ? 1u : 0u);
                 dev::mma_commit_pair(&s.acc_full[it % kAcc]);
                 dev::mma_commit_pair(&s.empty[st]);
+                if (chunk_ends) dev::mma_commit_pair(&s.sc_empty[sl]);
             }
             __syncwarp();
-            if (++st == kStages) st = 0;
+            if (++st == Shape<kC>::kStages) st = 0;
         }
     }
     if (elect_one()) {
@@ -164,11 +195,11 @@ __device__ __forceinline__ void mma_issuer(const Params& p, Smem<kC>& s, uint32_
     __syncwarp();
 }
 
-// ---------------------------------------------------------------- scalers (warps 2 and 3, blocks in turn)
+// ---------------------------------------------------------------- scaler (warp 2)
 template <int kC, bool kGated>
-__device__ __forceinline__ void scaler(const Params& p, Smem<kC>& s, uint32_t rank, int turn, int lane,
+__device__ __forceinline__ void scaler(const Params& p, Smem<kC>& s, uint32_t rank, int lane,
                                        volatile int* abort_flag) {
-    constexpr int kPer = Shape<kC>::kTokens / 32;   // tokens a lane: 2, 4 or 8
+    constexpr int kPer = Shape<kC>::kTokens / 32;   // tokens a lane: 2 or 4
     const int units = unit_count<Shape<kC>::kTokens>(p, s.tables);
     uint32_t v = 0, ch = 0;
     bool ok = true;
@@ -192,24 +223,23 @@ __device__ __forceinline__ void scaler(const Params& p, Smem<kC>& s, uint32_t ra
             }
             const float w0 = __shfl_sync(0xFFFFFFFFu, cur0, i32);
             const float w1 = kGated ? __shfl_sync(0xFFFFFFFFu, cur1, i32) : 0.0f;
-            if (in_chunk == 0) ok = dev::mbar_wait(&s.sc_full[sl], (ch / kScSlots) & 1, abort_flag);
-            if (static_cast<int>(v & 1) == turn) {
-                const int slot = v % kProd;
-                ok = __all_sync(0xFFFFFFFFu, ok && dev::mbar_wait(&s.prod_empty[slot], ((v / kProd) & 1) ^ 1, abort_flag));
-                if (!ok) break;
-                float x[kPer];
+            const int slot = v % kProd;
+            bool there = in_chunk != 0 || dev::mbar_wait(&s.sc_full[sl], (ch / kScSlots) & 1, abort_flag);
+            there = there && dev::mbar_wait(&s.prod_empty[slot], ((v / kProd) & 1) ^ 1, abort_flag);
+            ok = __all_sync(0xFFFFFFFFu, there);
+            if (!ok) break;
+            float x[kPer];
 #pragma unroll
-                for (int j = 0; j < kPer; j += 2)
-                    *reinterpret_cast<float2*>(x + j) = *reinterpret_cast<const float2*>(&s.sx[sl][in_chunk][lane * kPer + j]);
+            for (int j = 0; j < kPer; j += 2)
+                *reinterpret_cast<float2*>(x + j) = *reinterpret_cast<const float2*>(&s.sx[sl][in_chunk][lane * kPer + j]);
 #pragma unroll
-                for (int j = 0; j < kPer; j += 2) {
-                    *reinterpret_cast<float2*>(&s.prod[slot][0][lane * kPer + j]) = make_float2(x[j] * w0, x[j + 1] * w0);
-                    if (kGated)
-                        *reinterpret_cast<float2*>(&s.prod[slot][1][lane * kPer + j]) = make_float2(x[j] * w1, x[j + 1] * w1);
-                }
-                __syncwarp();
-                if (lane == 0) dev::mbar_arrive(&s.prod_full[slot]);
+            for (int j = 0; j < kPer; j += 2) {
+                *reinterpret_cast<float2*>(&s.prod[slot][0][lane * kPer + j]) = make_float2(x[j] * w0, x[j + 1] * w0);
+                if (kGated)
+                    *reinterpret_cast<float2*>(&s.prod[slot][1][lane * kPer + j]) = make_float2(x[j] * w1, x[j + 1] * w1);
             }
+            __syncwarp();
+            if (lane == 0) dev::mbar_arrive(&s.prod_full[slot]);
             if (in_chunk == kScChunk - 1 || b + 1 == t.b1) {
                 __syncwarp();
                 if (lane == 0) dev::mbar_arrive(&s.sc_empty[sl]);
@@ -359,16 +389,17 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem<kC>& s, uint32_t 
             auto store = [&]() {
 #pragma unroll
                 for (int c = 0; c < kC; ++c) {
-                    if (c >= chunks) break;
+                    if (32 * c >= min(half, t.n - c0)) break;
                     float weight = 1.0f;   // of token c0 + 32c + lane
                     const int mine = c0 + 32 * c + lane;
                     if (p.pair_weight != nullptr && mine < t.n) weight = __ldg(p.pair_weight + p.pair_of[t.row0 + mine]);
                     uint16_t* y = p.Y + (t.row0 + c0 + 32 * c) * p.ldy + n;
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        const float w = __shfl_sync(0xFFFFFFFFu, weight, i);
                         const int col = c0 + 32 * c + i;
-                        if (ok && 32 * c + i < half && col < t.n && n < p.N) {
+                        if (32 * c + i >= half || col >= t.n) break;   // (the same for the whole warp)
+                        const float w = __shfl_sync(0xFFFFFFFFu, weight, i);
+                        if (ok && n < p.N) {
                             const float f = ((i & 1) ? acc[c][i >> 1].y : acc[c][i >> 1].x) * w;
                             *y = p.bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(f)) : __half_as_ushort(__float2half_rn(f));
                         }
@@ -385,13 +416,13 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem<kC>& s, uint32_t 
                            (((static_cast<int64_t>(t.tile) * p.splits + sp) * 2 + rank) * kEpiWarps + ew) * (kC * 8 * 32) + lane;
                 };
                 float4* out = slot_of(t.split);
+                const int mine = min(half, t.n - c0);   // tokens of this warp (<= 0: none)
 #pragma unroll
-                for (int c = 0; c < kC; ++c) {
-                    if (c >= chunks) break;
+                for (int c = 0; c < kC; ++c)
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        __stcg(out + (8 * c + i) * 32, make_float4(acc[c][2 * i].x, acc[c][2 * i].y, acc[c][2 * i + 1].x, acc[c][2 * i + 1].y));
-                }
+                        if (32 * c + 4 * i < mine)
+                            __stcg(out + (8 * c + i) * 32, make_float4(acc[c][2 * i].x, acc[c][2 * i].y, acc[c][2 * i + 1].x, acc[c][2 * i + 1].y));
                 __threadfence();
                 dev::named_bar_sync(1, kEpiWarps * 32);
                 if (ew == 0 && lane == 0) {
@@ -404,21 +435,27 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem<kC>& s, uint32_t 
                 if (s.fixup_last) {
                     __threadfence();
 #pragma unroll
-                    for (int c = 0; c < kC; ++c) {
-                        if (c >= chunks) break;
+                    for (int c = 0; c < kC; ++c)
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                            for (int sp = 0; sp < p.splits; ++sp) {
-                                const float4 f = __ldcg(slot_of(sp) + (8 * c + i) * 32);
-                                sum.x += f.x;
-                                sum.y += f.y;
-                                sum.z += f.z;
-                                sum.w += f.w;
-                            }
-                            acc[c][2 * i] = make_float2(sum.x, sum.y);
-                            acc[c][2 * i + 1] = make_float2(sum.z, sum.w);
-                        }
+                        for (int i = 0; i < 16; ++i) acc[c][i] = make_float2(0.0f, 0.0f);
+                    for (int sp = 0; sp < p.splits; ++sp) {
+                        const float4* in = slot_of(sp);
+                        float4 f[kC][8];
+#pragma unroll
+                        for (int c = 0; c < kC; ++c)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (32 * c + 4 * i < mine) f[c][i] = __ldcg(in + (8 * c + i) * 32);
+#pragma unroll
+                        for (int c = 0; c < kC; ++c)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (32 * c + 4 * i < mine) {
+                                    acc[c][2 * i].x += f[c][i].x;
+                                    acc[c][2 * i].y += f[c][i].y;
+                                    acc[c][2 * i + 1].x += f[c][i].z;
+                                    acc[c][2 * i + 1].y += f[c][i].w;
+                                }
                     }
                     store();
                 }
@@ -433,19 +470,20 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem<kC>& s, uint32_t 
 
 template <int kC, bool kGated>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-fp8_few_kernel(const Params p, const __grid_constant__ CUtensorMap scales) {
+fp8_few_kernel(const Params p, const __grid_constant__ CUtensorMap codes, const __grid_constant__ CUtensorMap scales) {
     extern __shared__ uint8_t smem_raw[];
     Smem<kC>& s = *reinterpret_cast<Smem<kC>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = dev::cluster_ctarank();
     if (threadIdx.x == 0) {
+        dev::tma_prefetch_map(&codes);
         dev::tma_prefetch_map(&scales);
         for (int i = 0; i < kRing; ++i) dev::mbar_init(&s.ready[i], rank == 0 ? 2 + 2 * kEpiWarps : 1);
-        for (int i = 0; i < kStages; ++i) dev::mbar_init(&s.empty[i], 1);
+        for (int i = 0; i < Shape<kC>::kStages; ++i) dev::mbar_init(&s.empty[i], 1);
         for (int i = 0; i < kMaxAcc; ++i) dev::mbar_init(&s.acc_full[i], 1);
         for (int i = 0; i < kScSlots; ++i) {
             dev::mbar_init(&s.sc_full[i], 1);
-            dev::mbar_init(&s.sc_empty[i], 2);
+            dev::mbar_init(&s.sc_empty[i], 2);   // the scaler and the MMAs
         }
         for (int i = 0; i < kProd; ++i) {
             dev::mbar_init(&s.prod_full[i], 1);
@@ -460,7 +498,7 @@ fp8_few_kernel(const Params p, const __grid_constant__ CUtensorMap scales) {
         dev::fence_barrier_init();
     }
     if (warp == 2) dev::tmem_alloc_pair(&s.tmem_base, kTmemCols);
-    if (warp == 3 && p.start != nullptr) fill_tables<Shape<kC>::kTokens>(p, s.tables, lane);
+    if (p.start != nullptr) fill_tables<Shape<kC>::kTokens>(p, s.tables, warp, lane);
     dev::tc_fence_before();
     __syncthreads();
     dev::cluster_sync();   // both CTAs' barriers and TMEM exist before any traffic between them
@@ -471,11 +509,13 @@ fp8_few_kernel(const Params p, const __grid_constant__ CUtensorMap scales) {
     if (warp < 4) {
         dev::setmaxnreg_dec<72>();
         if (warp == 0) {
-            if (lane == 0) producer<kC>(p, &scales, s, rank, abort_flag);
+            weight_producer<kC>(p, s, rank, abort_flag);
         } else if (warp == 1) {
             mma_issuer<kC>(p, s, rank, tmem, abort_flag);
+        } else if (warp == 2) {
+            scaler<kC, kGated>(p, s, rank, lane, abort_flag);
         } else {
-            scaler<kC, kGated>(p, s, rank, warp - 2, lane, abort_flag);
+            token_producer<kC>(p, &codes, &scales, s, rank, abort_flag);
         }
         __syncwarp();
     } else {
@@ -496,11 +536,8 @@ constexpr size_t smem_bytes() { return sizeof(Smem<kC>) + 1024; }
 static_assert(smem_bytes<2>() <= 232448, "shared memory exceeds the 227 KB a CTA may use");
 
 template <int kC, bool kGated>
-cudaError_t launch_as(const Params& p, int grid, const CUtensorMap& map, cudaStream_t stream) {
-    const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fp8_few_kernel<kC, kGated>), static_cast<int>(smem_bytes<kC>()));
-    if (e != cudaSuccess) return e;
-    fp8_few_kernel<kC, kGated><<<grid, kThreads, smem_bytes<kC>(), stream>>>(p, map);
-    return cudaGetLastError();
+cudaError_t launch_as(const Params& p, int grid, const CUtensorMap& codes, const CUtensorMap& scales, bool pdl, cudaStream_t stream) {
+    return launch_pairs(fp8_few_kernel<kC, kGated>, grid, kThreads, smem_bytes<kC>(), pdl, stream, p, codes, scales);
 }
 
 // Tokens of a tile: 64 or 128 with the weights on the tensor core's M side, 256 with the tokens there:
@@ -574,13 +611,17 @@ cudaError_t launch_fp8_gemm(const fp8_layer& L, const Fp8GemmArgs& a, cudaStream
     // an upper bound of the token tiles: a partial one per expert in use
     const int64_t experts_used = routed ? (L.experts < a.pairs_routed ? L.experts : a.pairs_routed) : 0;
     const int64_t tiles = routed ? experts_used + a.pairs_routed / most : (a.rows + most - 1) / most;
-    if (most == 256) return launch_fp8_wide(L, p, a.a_scales, tiles, stream);
-    CUtensorMap map;
-    if (!encode_scale_map(&map, a.a_scales, p.sstride, L.nb, most)) return cudaErrorInvalidValue;
+    if (most == 256) return launch_fp8_wide(L, p, a.a_scales, tiles, a.pdl, stream);
+    CUtensorMap codes, scales;
+    if (!encode_code_map(&codes, a.A, a.rows, L.nb, most / 2) || !encode_scale_map(&scales, a.a_scales, p.sstride, L.nb, most))
+        return cudaErrorInvalidValue;
     const int64_t units = tiles * L.pairs * p.splits;
     const int grid = 2 * static_cast<int>(units < fp8_resident_pairs(L) ? units : fp8_resident_pairs(L));
-    if (L.gated) return most == 64 ? fp8::launch_as<1, true>(p, grid, map, stream) : fp8::launch_as<2, true>(p, grid, map, stream);
-    return most == 64 ? fp8::launch_as<1, false>(p, grid, map, stream) : fp8::launch_as<2, false>(p, grid, map, stream);
+    if (L.gated)
+        return most == 64 ? fp8::launch_as<1, true>(p, grid, codes, scales, a.pdl, stream)
+                          : fp8::launch_as<2, true>(p, grid, codes, scales, a.pdl, stream);
+    return most == 64 ? fp8::launch_as<1, false>(p, grid, codes, scales, a.pdl, stream)
+                      : fp8::launch_as<2, false>(p, grid, codes, scales, a.pdl, stream);
 }
 
 }  // namespace fmpq

@@ -12,7 +12,6 @@
 namespace fmpq {
 namespace fp8 {
 
-constexpr int kStages = 6;      // operand blocks in flight
 constexpr int kScChunk = 4;     // blocks of token scales per copy
 constexpr int kScSlots = 3;
 constexpr int kEpiWarps = 8;
@@ -53,14 +52,16 @@ struct Unit {
     int64_t row0;
 };
 
-// One warp fills the tables (kT tokens a tile): lane l sums the run of experts [l * run, l * run + run).
+// Every thread calls it; a barrier must follow. All threads load, then warp 3 sums up the units (kT tokens
+// a tile): lane l those of the run of experts [l * run, l * run + run).
 template <int kT>
-__device__ __forceinline__ void fill_tables(const Params& p, Tables& s, int lane) {
-    for (int e = lane; e < p.experts; e += 32) {
+__device__ __forceinline__ void fill_tables(const Params& p, Tables& s, int warp, int lane) {
+    for (int e = threadIdx.x; e < p.experts; e += blockDim.x) {
         s.start[e] = p.start[e];
         s.count[e] = p.count[e];
     }
-    __syncwarp();
+    __syncthreads();
+    if (warp != 3) return;
     const int run = (p.experts + 31) / 32;
     auto units_of = [&](int e) { return e < p.experts ? (s.count[e] + kT - 1) / kT * p.pairs : 0; };
     int sum = 0;
@@ -161,10 +162,21 @@ __device__ __forceinline__ float silu_times(float g, float u) { return g / (1.0f
 
 }  // namespace fp8
 
-// The token scales as a 2-D tensor [nb][rows]: boxes of kScChunk blocks x `tokens` rows.
+// The token scales as a 2-D tensor [nb][rows]: boxes of kScChunk blocks x `tokens` rows. The codes as a
+// 3-D one [nb][rows][128 bytes], boxes of kScChunk blocks x `tokens` rows.
 bool encode_scale_map(CUtensorMap* map, const float* scales, int64_t sstride, int nb, int tokens);
+bool encode_code_map(CUtensorMap* map, const void* codes, int64_t rows, int nb, int tokens);
+
+// Launch a kernel of CTA pairs; pdl: as the programmatic dependent of the launch before it.
+template <typename... P, typename... A>
+cudaError_t launch_pairs(void (*fn)(P...), int grid, int threads, size_t smem, bool pdl, cudaStream_t stream, const A&... args) {
+    const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    return launch_after(fn, dim3(static_cast<unsigned>(grid)), threads, smem, pdl, stream, args...);
+}
+
 // More than this many tokens a tile go to the kernel with the tokens on the tensor core's M side.
-cudaError_t launch_fp8_wide(const fp8_layer& L, const fp8::Params& p, const float* a_scales, int64_t tiles,
+cudaError_t launch_fp8_wide(const fp8_layer& L, const fp8::Params& p, const float* a_scales, int64_t tiles, bool pdl,
                             cudaStream_t stream);
 // Pairs of CTAs that are resident at once (one CTA per SM).
 int fp8_resident_pairs(const fp8_layer& L);

@@ -21,6 +21,7 @@ namespace fp8 {
 namespace {
 
 constexpr int kT = 256;      // tokens of a tile, 128 a CTA
+constexpr int kStages = 6;   // operand blocks in flight
 constexpr int kAcc = 2;      // accumulators of 256 columns
 constexpr int kWideEpi = 16; // epilogue warps
 constexpr int kWideThreads = 640;
@@ -51,6 +52,8 @@ __device__ __forceinline__ void producer(const Params& p, const CUtensorMap* sca
     const int units = unit_count<kT>(p, s.tables);
     uint32_t it = 0, ch = 0;
     bool ok = true;
+    dev::pdl_wait();                // the codes and scales come from the kernel before
+    dev::pdl_launch_dependents();   // (after the wait: see Fp8GemmArgs::pdl)
     for (int u = blockIdx.x >> 1; ok && u < units; u += gridDim.x >> 1) {
         const Unit t = unit(p, s, u);
         const int local = static_cast<int>(rank) * 128;
@@ -355,7 +358,7 @@ fp8_wide_kernel(const Params p, const __grid_constant__ CUtensorMap scales) {
         dev::fence_barrier_init();
     }
     if (warp == 2) dev::tmem_alloc_pair(&s.tmem_base, kTmemCols);
-    if (warp == 3 && p.start != nullptr) fill_tables<kT>(p, s.tables, lane);
+    if (p.start != nullptr) fill_tables<kT>(p, s.tables, warp, lane);
     dev::tc_fence_before();
     __syncthreads();
     dev::cluster_sync();   // both CTAs' barriers and TMEM exist before any traffic between them
@@ -408,6 +411,17 @@ int fp8_resident_pairs(const fp8_layer& L) {
     return pairs;
 }
 
+bool encode_code_map(CUtensorMap* map, const void* codes, int64_t rows, int nb, int tokens) {
+    const EncodeTiledFn encode = encode_tiled();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(nb)};
+    const cuuint64_t strides[2] = {128, static_cast<cuuint64_t>(rows) * 128};
+    const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(tokens), fp8::kScChunk}, step[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(codes), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool encode_scale_map(CUtensorMap* map, const float* scales, int64_t sstride, int nb, int tokens) {
     const EncodeTiledFn encode = encode_tiled();
     if (encode == nullptr) return false;
@@ -419,17 +433,14 @@ bool encode_scale_map(CUtensorMap* map, const float* scales, int64_t sstride, in
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaError_t launch_fp8_wide(const fp8_layer& L, const fp8::Params& p, const float* a_scales, int64_t tiles,
+cudaError_t launch_fp8_wide(const fp8_layer& L, const fp8::Params& p, const float* a_scales, int64_t tiles, bool pdl,
                             cudaStream_t stream) {
     CUtensorMap map;
     if (!encode_scale_map(&map, a_scales, p.sstride, L.nb, 128)) return cudaErrorInvalidValue;
-    auto fn = L.gated ? fp8::fp8_wide_kernel<true> : fp8::fp8_wide_kernel<false>;
-    const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), static_cast<int>(fp8::kSmemBytes));
-    if (e != cudaSuccess) return e;
     const int64_t units = tiles * L.pairs * p.splits;
     const int grid = 2 * static_cast<int>(units < fp8_resident_pairs(L) ? units : fp8_resident_pairs(L));
-    fn<<<grid, fp8::kWideThreads, fp8::kSmemBytes, stream>>>(p, map);
-    return cudaGetLastError();
+    auto fn = L.gated ? fp8::fp8_wide_kernel<true> : fp8::fp8_wide_kernel<false>;
+    return launch_pairs(fn, grid, fp8::kWideThreads, fp8::kSmemBytes, pdl, stream, p, map);
 }
 
 }  // namespace fmpq

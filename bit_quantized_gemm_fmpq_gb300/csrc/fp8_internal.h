@@ -70,7 +70,8 @@ enum { kF16 = 0, kBF16 = 1, kF32 = 2 };
 // rows/positions: nullptr writes token m to row m; otherwise token m goes to the rows
 // positions[m * slots .. + slots) that are not negative.
 cudaError_t launch_fp8_quantize(const void* X, int dtype, int64_t ldx, int64_t M, int K, const int32_t* positions,
-                                int slots, int64_t rows, void* A, float* scales, int num_sms, cudaStream_t stream);
+                                int slots, int64_t rows, void* A, float* scales, int num_sms, bool pdl,
+                                cudaStream_t stream);
 cudaError_t launch_fp8_pack_weights(const fp8_layer& L, int expert, const void* W, int dtype, int64_t ldw, void* Wp,
                                     float* scales, cudaStream_t stream);
 cudaError_t launch_fp8_pack_codes(const fp8_layer& L, int expert, const void* codes, int64_t ldw, void* Wp,
@@ -96,6 +97,11 @@ struct Fp8GemmArgs {
     void* H;                  // gated layer: E4M3 codes [F/128][rows][128] and scales
     float* h_scales;
     void* workspace;
+    // Launched as the programmatic dependent of this library's kernel before it: its prologue, and the
+    // weights' stream, start while that one runs; only its codes and scales are waited for. Every kernel
+    // launched so lets its own dependent start after its wait, so what was written two launches
+    // before (the plan) is complete from the start.
+    bool pdl;
 };
 cudaError_t launch_fp8_gemm(const fp8_layer& L, const Fp8GemmArgs& a, cudaStream_t stream);
 // Workspace of a dense product of M rows (0: none needed), zero before its first use.
@@ -115,6 +121,22 @@ cudaError_t launch_moe_route(const RouteArgs& a, cudaStream_t stream);
 cudaError_t launch_moe_plan(const int32_t* ids, int64_t T, int k, int E, int32_t* plan, int32_t* counts,
                             cudaStream_t stream);
 cudaError_t launch_moe_combine(const void* D, int dtype, int64_t ldd, const int32_t* row_of, int64_t T, int k, int N,
-                               void* Y, int64_t ldy, cudaStream_t stream);
+                               void* Y, int64_t ldy, bool pdl, cudaStream_t stream);
+
+// Launch; pdl: as the programmatic dependent of the launch before it.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*fn)(P...), dim3 grid, int threads, size_t smem, bool pdl, cudaStream_t stream, const A&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, fn, P(args)...);
+}
 
 }  // namespace fmpq

@@ -7,6 +7,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "fmpq_device.cuh"
 #include "fp8_internal.h"
 
 namespace fmpq {
@@ -45,6 +46,8 @@ __global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ X, 
                                                        float* __restrict__ scales) {
     const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
     const int64_t tasks = M * ((nb + 1) / 2);
+    dev::pdl_wait();
+    dev::pdl_launch_dependents();
     for (int64_t task = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); task < tasks;
          task += static_cast<int64_t>(gridDim.x) * 8) {
         const int64_t m = task % M;
@@ -173,23 +176,22 @@ __global__ void __launch_bounds__(256) unpack_kernel(const uint8_t* __restrict__
 
 template <typename T>
 cudaError_t quantize_as(const void* X, int64_t ldx, int64_t M, int K, const int32_t* positions, int slots, int64_t rows,
-                        void* A, float* scales, int num_sms, cudaStream_t stream) {
+                        void* A, float* scales, int num_sms, bool pdl, cudaStream_t stream) {
     const int nb = (K + 127) / 128;
     const int64_t tasks = M * ((nb + 1) / 2), ctas = (tasks + 7) / 8;
     const int grid = static_cast<int>(ctas < num_sms * 64LL ? ctas : num_sms * 64LL);
     const bool vec = ldx % 8 == 0 && (reinterpret_cast<uintptr_t>(X) & 15u) == 0;
     auto fn = vec ? quantize_kernel<T, true> : quantize_kernel<T, false>;
-    fn<<<grid, 256, 0, stream>>>(static_cast<const T*>(X), ldx, M, K, nb, positions, positions != nullptr ? slots : 1, rows,
-                                 scale_stride(rows), static_cast<uint8_t*>(A), scales);
-    return cudaGetLastError();
+    return launch_after(fn, dim3(static_cast<unsigned>(grid)), 256, 0, pdl, stream, static_cast<const T*>(X), ldx, M, K, nb,
+                        positions, positions != nullptr ? slots : 1, rows, scale_stride(rows), static_cast<uint8_t*>(A), scales);
 }
 
 }  // namespace
 
 cudaError_t launch_fp8_quantize(const void* X, int dtype, int64_t ldx, int64_t M, int K, const int32_t* positions,
-                                int slots, int64_t rows, void* A, float* scales, int num_sms, cudaStream_t stream) {
-    return dtype == kF16 ? quantize_as<__half>(X, ldx, M, K, positions, slots, rows, A, scales, num_sms, stream)
-                         : quantize_as<__nv_bfloat16>(X, ldx, M, K, positions, slots, rows, A, scales, num_sms, stream);
+                                int slots, int64_t rows, void* A, float* scales, int num_sms, bool pdl, cudaStream_t stream) {
+    return dtype == kF16 ? quantize_as<__half>(X, ldx, M, K, positions, slots, rows, A, scales, num_sms, pdl, stream)
+                         : quantize_as<__nv_bfloat16>(X, ldx, M, K, positions, slots, rows, A, scales, num_sms, pdl, stream);
 }
 
 cudaError_t launch_fp8_pack_weights(const fp8_layer& L, int expert, const void* W, int dtype, int64_t ldw, void* Wp,

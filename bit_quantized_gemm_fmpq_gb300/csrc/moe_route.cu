@@ -3,6 +3,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "fmpq_device.cuh"
 #include "fp8_internal.h"
 
 namespace fmpq {
@@ -478,6 +479,7 @@ __global__ void __launch_bounds__(kChunk) plan_place_kernel(const int32_t* __res
     uint16_t* per_warp = reinterpret_cast<uint16_t*>(sm + 2 * E);
     __shared__ int32_t carry[32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    dev::pdl_launch_dependents();   // (the quantizer after it waits for all of it)
     for (int i = threadIdx.x; i < 32 * E; i += kChunk) per_warp[i] = 0;
     __syncthreads();
     // ranks inside the warp, counts of the warp
@@ -551,6 +553,8 @@ template <typename T, bool kVec>
 __global__ void __launch_bounds__(256) combine_kernel(const T* __restrict__ D, int64_t ldd, const int32_t* __restrict__ row_of,
                                                       int64_t tokens, int k, int N, T* __restrict__ Y, int64_t ldy) {
     const int per_row = (N + 7) / 8;
+    dev::pdl_wait();
+    dev::pdl_launch_dependents();
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < tokens * per_row;
          i += static_cast<int64_t>(gridDim.x) * 256) {
         const int64_t t = i / per_row;
@@ -586,14 +590,14 @@ __global__ void __launch_bounds__(256) combine_kernel(const T* __restrict__ D, i
 
 template <typename T>
 cudaError_t combine_as(const void* D, int64_t ldd, const int32_t* row_of, int64_t tokens, int k, int N, void* Y, int64_t ldy,
-                       cudaStream_t stream) {
+                       bool pdl, cudaStream_t stream) {
     const int64_t ctas = (tokens * ((N + 7) / 8) + 255) / 256;
     const int grid = static_cast<int>(ctas < 1 << 20 ? ctas : 1 << 20);
     const bool vec = ldd % 8 == 0 && ldy % 8 == 0 &&
                      ((reinterpret_cast<uintptr_t>(D) | reinterpret_cast<uintptr_t>(Y)) & 15u) == 0;
     auto fn = vec ? combine_kernel<T, true> : combine_kernel<T, false>;
-    fn<<<grid, 256, 0, stream>>>(static_cast<const T*>(D), ldd, row_of, tokens, k, N, static_cast<T*>(Y), ldy);
-    return cudaGetLastError();
+    return launch_after(fn, dim3(static_cast<unsigned>(grid)), 256, 0, pdl, stream, static_cast<const T*>(D), ldd, row_of, tokens, k, N,
+                        static_cast<T*>(Y), ldy);
 }
 
 }  // namespace
@@ -616,9 +620,9 @@ cudaError_t launch_moe_plan(const int32_t* ids, int64_t T, int k, int E, int32_t
 }
 
 cudaError_t launch_moe_combine(const void* D, int dtype, int64_t ldd, const int32_t* row_of, int64_t T, int k, int N,
-                               void* Y, int64_t ldy, cudaStream_t stream) {
-    return dtype == kF16 ? combine_as<__half>(D, ldd, row_of, T, k, N, Y, ldy, stream)
-                         : combine_as<__nv_bfloat16>(D, ldd, row_of, T, k, N, Y, ldy, stream);
+                               void* Y, int64_t ldy, bool pdl, cudaStream_t stream) {
+    return dtype == kF16 ? combine_as<__half>(D, ldd, row_of, T, k, N, Y, ldy, pdl, stream)
+                         : combine_as<__nv_bfloat16>(D, ldd, row_of, T, k, N, Y, ldy, pdl, stream);
 }
 
 }  // namespace fmpq
