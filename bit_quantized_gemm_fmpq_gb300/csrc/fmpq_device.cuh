@@ -95,6 +95,11 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// The same, `count` arrivals at once.
+__device__ __forceinline__ void mbar_arrive_remote_n(uint32_t cluster_addr, uint32_t count) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr), "r"(count) : "memory");
+}
+
 // Arrive on an mbarrier of any CTA of the cluster with release semantics at cluster scope
 // (the peer reads, after its acquire, data this thread's CTA wrote or freed).
 __device__ __forceinline__ void mbar_arrive_remote_release(uint32_t cluster_addr) {
@@ -136,6 +141,10 @@ __device__ __forceinline__ void cluster_sync() {
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t count) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
 }
 
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t bytes) {

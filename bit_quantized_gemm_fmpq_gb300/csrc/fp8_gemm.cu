@@ -55,6 +55,7 @@ struct __align__(1024) Smem {
     // gated: absmax of 16 hidden channels (a quarter's), of this CTA's 64 and the peer's 64, the
     // tokens' scales
     float amax[4][kT], amax_peer[2][kT], hscale[kT];
+    float2 other_turn[kC == 1 ? 16 : 1][128];    // up to 32 tokens: the sums of every second block
     // ready[b % kRing], even CTA: block b's weights have landed in both CTAs, the odd one's token codes
     // too, and its accumulator has been read (by both CTAs' epilogue warps). Odd CTA: its weights have
     // landed. sc_full: a chunk's token codes and scales have landed here; sc_empty: the scaler has read the
@@ -266,13 +267,16 @@ __device__ __forceinline__ void accumulate(const uint32_t (&d)[32], const float*
 // The blocks of a unit for one epilogue warp whose half tile has kCh chunks of 32 tokens: P of block
 // b from TMEM, times the scale products, into acc. Straight-line inside a block: a TMEM load's 32
 // registers are one fixed run, and a load under a condition makes the compiler move all 32 of them
-// at every join. Returns false when a wait gave up. v counts the blocks of this CTA.
-template <int kC, int kCh>
+// at every join. Returns false when a wait gave up. v counts the blocks of this CTA. kTurns: the warp takes
+// every second block (v % 2 == turn) and arrives for the warp that takes the others.
+template <int kC, int kCh, bool kTurns>
 __device__ __forceinline__ bool sum_blocks(Smem<kC>& s, uint32_t base, const float* prod0, uint32_t leader_ready, int blocks,
-                                           int lane, uint32_t& v, float2 (&acc)[kC][16], volatile int* abort_flag) {
+                                           int lane, int turn, uint32_t& v, float2 (&acc)[kC][16], volatile int* abort_flag) {
     using S = Shape<kC>;
+    constexpr uint32_t kArrivals = kTurns ? 2 : 1;
     constexpr int kProdFloats = sizeof(s.prod[0]) / sizeof(float);
     for (int left = blocks; left > 0; --left, ++v) {
+        if (kTurns && static_cast<int>(v & 1) != turn) continue;
         const uint32_t slot = v % kProd;
         const bool there = dev::mbar_wait(&s.acc_full[v % S::kAcc], (v / S::kAcc) & 1, abort_flag);
         if (!__all_sync(0xFFFFFFFFu, there)) return false;
@@ -288,11 +292,11 @@ __device__ __forceinline__ bool sum_blocks(Smem<kC>& s, uint32_t base, const flo
         // all of it is in registers: the accumulator is free for block v + kAcc
         dev::tc_fence_before();
         __syncwarp();
-        if (lane == 0) dev::mbar_arrive_remote(leader_ready + ((v + S::kAcc) % kRing) * 8u);
+        if (lane == 0) dev::mbar_arrive_remote_n(leader_ready + ((v + S::kAcc) % kRing) * 8u, kArrivals);
         accumulate(d0, prod, acc[0]);
         if constexpr (kCh == 2) accumulate(d1, prod + 32, acc[kC - 1]);
         __syncwarp();
-        if (lane == 0) dev::mbar_arrive(&s.prod_empty[slot]);
+        if (lane == 0) dev::mbar_arrive_n(&s.prod_empty[slot], kArrivals);
     }
     return true;
 }
@@ -310,10 +314,20 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem<kC>& s, uint32_t 
     bool ok = true;
     for (int u = blockIdx.x >> 1; u < units; u += gridDim.x >> 1) {
         const Unit t = unit<kC>(p, s, u);
-        const int half = columns(t) >> 1, c0 = h * half;
+        // up to 32 tokens: the two warps of a quarter take the blocks in turn, each with all the columns
+        const bool turns = kC == 1 && columns(t) == 32;
+        const int half = turns ? 32 : columns(t) >> 1, c0 = turns ? 0 : h * half;
+        const int own = turns && h == 1 ? 0 : max(0, min(half, t.n - c0));   // tokens that this warp puts out
         const int chunks = (half + 31) >> 5;
         const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(c0);
         const float* prod0 = &s.prod[0][kGated ? lane >> 4 : 0][c0];
+        float weight[kC];   // of token c0 + 32c + lane
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            weight[c] = 1.0f;
+            if (!kGated && p.pair_weight != nullptr && 32 * c + lane < own)
+                weight[c] = __ldg(p.pair_weight + p.pair_of[t.row0 + c0 + 32 * c + lane]);
+        }
         float2 acc[kC][16];
 #pragma unroll
         for (int c = 0; c < kC; ++c)
@@ -322,8 +336,26 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem<kC>& s, uint32_t 
 
         if (ok) {
             const int blocks = t.b1 - t.b0;
-            if (kC == 1 || chunks == 1) ok = sum_blocks<kC, 1>(s, base, prod0, leader_ready, blocks, lane, v, acc, abort_flag);
-            else ok = sum_blocks<kC, kC>(s, base, prod0, leader_ready, blocks, lane, v, acc, abort_flag);
+            if (turns) ok = sum_blocks<kC, 1, true>(s, base, prod0, leader_ready, blocks, lane, h, v, acc, abort_flag);
+            else if (kC == 1 || chunks == 1) ok = sum_blocks<kC, 1, false>(s, base, prod0, leader_ready, blocks, lane, 0, v, acc, abort_flag);
+            else ok = sum_blocks<kC, kC, false>(s, base, prod0, leader_ready, blocks, lane, 0, v, acc, abort_flag);
+        }
+        if (turns) {
+            if (h == 1) {
+#pragma unroll
+                for (int i = 0; i < (kC == 1 ? 16 : 1); ++i)
+                    if (2 * i < t.n) s.other_turn[i][32 * q + lane] = acc[0][i];
+            }
+            dev::named_bar_sync(4 + q, 64);
+            if (h == 0) {
+#pragma unroll
+                for (int i = 0; i < (kC == 1 ? 16 : 1); ++i)
+                    if (2 * i < t.n) {
+                        const float2 f = s.other_turn[i][32 * q + lane];
+                        acc[0][i] = make_float2(acc[0][i].x + f.x, acc[0][i].y + f.y);
+                    }
+            }
+            dev::named_bar_sync(4 + q, 64);   // read before the next unit's sums come
         }
 
         if constexpr (kGated) {
@@ -339,6 +371,7 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem<kC>& s, uint32_t 
                 float top = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
+                    if (32 * c + 2 * i >= own) break;   // (the same for the whole warp)
                     const float2 f = acc[c][i];
                     const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? f.x : f.y, 16);
                     const float g = odd ? got : f.x, up = odd ? f.y : got;
@@ -348,11 +381,11 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem<kC>& s, uint32_t 
                     if (l16 == i) top = m;
                 }
                 // token of this lane's maximum: 2 l16 (+ 1) of the 32
-                if (32 * c + 2 * l16 < half) s.amax[q][c0 + 32 * c + 2 * l16 + (odd ? 1 : 0)] = top;
+                if (32 * c + 2 * l16 < own) s.amax[q][c0 + 32 * c + 2 * l16 + (odd ? 1 : 0)] = top;
             }
             dev::named_bar_sync(2 + h, 128);
             // the four quarters' maximum of a token to the peer; warp q takes a quarter of the tokens
-            for (int j = lane; j < half; j += 32) {
+            for (int j = lane; j < own; j += 32) {
                 if (((j >> 5) & 3) != q) continue;
                 const int col = c0 + j;
                 const float m = fmaxf(fmaxf(s.amax[0][col], s.amax[1][col]), fmaxf(s.amax[2][col], s.amax[3][col]));
@@ -363,7 +396,7 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem<kC>& s, uint32_t 
             if (lane == 0) dev::mbar_arrive_remote_release(dev::mapa(&s.amax_full[par], rank ^ 1u));
             if (ok) ok = dev::mbar_wait_cluster(&s.amax_full[par], (nu >> 1) & 1);
             ok = __all_sync(0xFFFFFFFFu, ok);
-            for (int j = lane; j < half; j += 32) {
+            for (int j = lane; j < own; j += 32) {
                 if (((j >> 5) & 3) != q) continue;
                 const int col = c0 + j;
                 const float sc = __fdiv_rn(fmaxf(s.hscale[col], s.amax_peer[par][col]), 448.0f);
@@ -378,7 +411,8 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem<kC>& s, uint32_t 
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int col = c0 + 32 * c + 2 * i + (odd ? 1 : 0);
-                    if (!ok || 32 * c + 2 * i >= half || col >= t.n) continue;
+                    if (32 * c + 2 * i >= own) break;
+                    if (!ok || col >= t.n) continue;
                     const float sc = s.hscale[col];
                     const uint32_t code = e4m3x2(sc > 0.0f ? __fdiv_rn(acc[c][i].x, sc) : 0.0f, 0.0f);
                     out[static_cast<int64_t>(col) * 128 + ((chunk16 ^ static_cast<int>((t.row0 + col) & 7)) << 4)] = static_cast<uint8_t>(code);
@@ -389,16 +423,12 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem<kC>& s, uint32_t 
             auto store = [&]() {
 #pragma unroll
                 for (int c = 0; c < kC; ++c) {
-                    if (32 * c >= min(half, t.n - c0)) break;
-                    float weight = 1.0f;   // of token c0 + 32c + lane
-                    const int mine = c0 + 32 * c + lane;
-                    if (p.pair_weight != nullptr && mine < t.n) weight = __ldg(p.pair_weight + p.pair_of[t.row0 + mine]);
+                    if (32 * c >= own) break;
                     uint16_t* y = p.Y + (t.row0 + c0 + 32 * c) * p.ldy + n;
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        const int col = c0 + 32 * c + i;
-                        if (32 * c + i >= half || col >= t.n) break;   // (the same for the whole warp)
-                        const float w = __shfl_sync(0xFFFFFFFFu, weight, i);
+                        if (32 * c + i >= own) break;   // (the same for the whole warp)
+                        const float w = __shfl_sync(0xFFFFFFFFu, weight[c], i);
                         if (ok && n < p.N) {
                             const float f = ((i & 1) ? acc[c][i >> 1].y : acc[c][i >> 1].x) * w;
                             *y = p.bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(f)) : __half_as_ushort(__float2half_rn(f));
@@ -416,12 +446,11 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem<kC>& s, uint32_t 
                            (((static_cast<int64_t>(t.tile) * p.splits + sp) * 2 + rank) * kEpiWarps + ew) * (kC * 8 * 32) + lane;
                 };
                 float4* out = slot_of(t.split);
-                const int mine = min(half, t.n - c0);   // tokens of this warp (<= 0: none)
 #pragma unroll
                 for (int c = 0; c < kC; ++c)
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        if (32 * c + 4 * i < mine)
+                        if (32 * c + 4 * i < own)
                             __stcg(out + (8 * c + i) * 32, make_float4(acc[c][2 * i].x, acc[c][2 * i].y, acc[c][2 * i + 1].x, acc[c][2 * i + 1].y));
                 __threadfence();
                 dev::named_bar_sync(1, kEpiWarps * 32);
@@ -445,12 +474,12 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem<kC>& s, uint32_t 
                         for (int c = 0; c < kC; ++c)
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
-                                if (32 * c + 4 * i < mine) f[c][i] = __ldcg(in + (8 * c + i) * 32);
+                                if (32 * c + 4 * i < own) f[c][i] = __ldcg(in + (8 * c + i) * 32);
 #pragma unroll
                         for (int c = 0; c < kC; ++c)
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
-                                if (32 * c + 4 * i < mine) {
+                                if (32 * c + 4 * i < own) {
                                     acc[c][2 * i].x += f[c][i].x;
                                     acc[c][2 * i].y += f[c][i].y;
                                     acc[c][2 * i + 1].x += f[c][i].z;
