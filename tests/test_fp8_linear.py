@@ -199,6 +199,8 @@ def test_weights_pack_and_unpack(fmpq_mod, N, K, gated):
     (1, 1, 1), (1, 8192, 256), (2, 300, 130), (16, 512, 512), (17, 128, 4004), (31, 2868, 100), (32, 1024, 300),
     (33, 640, 264), (64, 4096, 520), (65, 129, 257), (100, 2000, 1000), (129, 384, 768), (255, 256, 136), (256, 1024, 256),
     (257, 640, 513), (300, 1536, 1300), (515, 2868, 404), (1000, 512, 2304),
+    # more tiles than pairs of CTAs
+    (64, 200, 20500), (130, 384, 20500), (1000, 256, 5001),
 ])
 @pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
 def test_product(fmpq_mod, M, K, N, dtype):

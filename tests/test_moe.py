@@ -266,6 +266,8 @@ CASES = [
     (40, 2, 6, 300, 140, 260, 1.0, 0.1), (17, 1, 2, 512, 256, 384, 0.0, 0.0), (200, 3, 4, 129, 127, 256, 1.0, 0.1),
     (700, 2, 3, 256, 200, 264, 1.0, 0.0), (600, 1, 1, 128, 130, 72, 0.0, 0.0), (30, 2, 4, 256, 128, 128, 0.0, 1.0),
     (130, 8, 32, 384, 384, 512, 0.5, 0.0),
+    # more tiles than pairs of CTAs: several a pair, for many tokens an expert and for few
+    (700, 2, 3, 256, 2560, 5200, 0.0, 0.0), (64, 4, 16, 256, 1280, 2600, 0.5, 0.1),
 ]
 
 
