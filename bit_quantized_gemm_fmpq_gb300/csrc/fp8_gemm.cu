@@ -642,7 +642,7 @@ cudaError_t launch_fp8_gemm(const fp8_layer& L, const Fp8GemmArgs& a, cudaStream
     const int64_t tiles = routed ? experts_used + a.pairs_routed / most : (a.rows + most - 1) / most;
     if (most == 256) return launch_fp8_wide(L, p, a.a_scales, tiles, a.pdl, stream);
     CUtensorMap codes, scales;
-    if (!encode_code_map(&codes, a.A, a.rows, L.nb, most / 2) || !encode_scale_map(&scales, a.a_scales, p.sstride, L.nb, most))
+    if (!encode_code_map(&codes, a.A, a.rows, L.nb, most / 2) || !encode_scale_map(&scales, a.a_scales, p.sstride, L.nb, most, fp8::kScChunk))
         return cudaErrorInvalidValue;
     const int64_t units = tiles * L.pairs * p.splits;
     const int grid = 2 * static_cast<int>(units < fp8_resident_pairs(L) ? units : fp8_resident_pairs(L));

@@ -129,6 +129,25 @@ __device__ __forceinline__ Unit unit_of(const Params& p, const Tables& s, int u)
     return r;
 }
 
+// dev::mbar_wait on a shared-memory address.
+__device__ __forceinline__ bool wait_at(uint32_t bar, uint32_t parity, const volatile int* abort) {
+    for (uint32_t i = 0; i < dev::kMaxPolls; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n"
+            ".reg .pred p;\n"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+            "selp.u32 %0, 1, 0, p;\n"
+            "}\n"
+            : "=r"(done)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (done) return true;
+        if ((i & 255u) == 255u && *abort) return false;
+    }
+    return false;
+}
+
 __device__ __forceinline__ void fail(const Params& p, volatile int* abort_flag) {
     *abort_flag = 1;
     dev::report(p.status, dev::kStatusTimeout);
@@ -170,9 +189,9 @@ __device__ __forceinline__ float silu_times(float g, float u) {
 
 }  // namespace fp8
 
-// The token scales as a 2-D tensor [nb][rows]: boxes of kScChunk blocks x `tokens` rows. The codes as a
+// The token scales as a 2-D tensor [nb][rows]: boxes of `blocks` blocks x `tokens` rows. The codes as a
 // 3-D one [nb][rows][128 bytes], boxes of kScChunk blocks x `tokens` rows.
-bool encode_scale_map(CUtensorMap* map, const float* scales, int64_t sstride, int nb, int tokens);
+bool encode_scale_map(CUtensorMap* map, const float* scales, int64_t sstride, int nb, int tokens, int blocks);
 bool encode_code_map(CUtensorMap* map, const void* codes, int64_t rows, int nb, int tokens);
 
 // Launch a kernel of CTA pairs; pdl: as the programmatic dependent of the launch before it.

@@ -12,7 +12,8 @@
 // Warp roles (640 threads, one CTA per SM, pairs persistent over tiles):
 //   warp 0      producer: token codes and weight block, token scales (a chunk of blocks at a time)
 //   warp 1      even CTA: MMA issuer; odd CTA: reports its operands to the even one
-//   warp 2      allocates and frees TMEM; warp 3 fills the experts' tables
+//   warp 2      scaler: a chunk's token scales times its weight scales; also allocates and frees TMEM
+//   warp 3      sums up the experts' tiles at the start
 //   warps 4-19  epilogue: TMEM lane quarter warp % 4 (32 tokens), 64 of the 256 columns each
 #include "fp8_gemm.cuh"
 
@@ -25,19 +26,22 @@ constexpr int kStages = 6;   // operand blocks in flight
 constexpr int kAcc = 2;      // accumulators of 256 columns
 constexpr int kWideEpi = 16; // epilogue warps
 constexpr int kWideThreads = 640;
+constexpr int kChunk = 2;    // blocks of token scales per copy
+constexpr int kSlots = 2;    // chunks of scales, and of factors
 constexpr int kRing = 8;     // blocks whose readiness may be in flight (> kStages)
 
 struct __align__(1024) Smem {
     uint8_t x[kStages][kTileBytes];   // token codes: this CTA's 128 rows
     uint8_t w[kStages][kTileBytes];   // weight block: this CTA's tile, half of the pair's columns
-    float sx[kScSlots][kScChunk][128];
+    float sx[kSlots][kChunk][128];        // token scales
+    float factor[kSlots][kChunk][2][128]; // times the weight scales: of the pair's two tiles, or gate and up
     float amax[2][4][128];            // gated: absmax of each quarter of a token's 128 hidden channels (units in turn)
     uint4 out[kWideEpi][32 * 2];      // a warp's 32 tokens x 16 columns of 16-bit outputs
     // ready[b % kRing], even CTA: block b's operands have landed in both CTAs and its accumulator has
     // been read (by both CTAs' epilogue warps). Odd CTA: its operands have landed.
     uint64_t ready[kRing], empty[kStages];
     uint64_t acc_full[kAcc];
-    uint64_t sc_full[kScSlots], sc_empty[kScSlots];
+    uint64_t sc_full[kSlots], sc_empty[kSlots], factor_full[kSlots], factor_empty[kSlots];
     uint64_t mma_done;
     uint32_t tmem_base;
     int abort_flag;
@@ -61,9 +65,9 @@ __device__ __forceinline__ void producer(const Params& p, const CUtensorMap* sca
         const uint8_t* w = weight_block(p, t, rank);
         const uint8_t* x = p.A + (t.row0 + local + t.b0 * p.rows) * 128;
         for (int b = t.b0; b < t.b1; ++b, ++it) {
-            if ((b - t.b0) % kScChunk == 0) {
-                const int sl = ch % kScSlots;
-                ok = dev::mbar_wait(&s.sc_empty[sl], ((ch / kScSlots) & 1) ^ 1, abort_flag);
+            if ((b - t.b0) % kChunk == 0) {
+                const int sl = ch % kSlots;
+                ok = dev::mbar_wait(&s.sc_empty[sl], ((ch / kSlots) & 1) ^ 1, abort_flag);
                 if (!ok) break;
                 dev::mbar_arrive_expect_tx(&s.sc_full[sl], sizeof(s.sx[0]));
                 dev::tma_load_2d(s.sx[sl], scales, static_cast<int>(t.row0) + local, b, &s.sc_full[sl]);
@@ -87,9 +91,9 @@ __device__ __forceinline__ void producer(const Params& p, const CUtensorMap* sca
         const uint32_t i = it - 1 - k;
         dev::mbar_wait(&s.ready[i % kRing], (i / kRing) & 1, nullptr, ok ? dev::kMaxPolls : 1u << 16);
     }
-    for (uint32_t k = 0; k < kScSlots && k < ch; ++k) {
+    for (uint32_t k = 0; k < kSlots && k < ch; ++k) {
         const uint32_t i = ch - 1 - k;
-        dev::mbar_wait(&s.sc_full[i % kScSlots], (i / kScSlots) & 1, nullptr);
+        dev::mbar_wait(&s.sc_full[i % kSlots], (i / kSlots) & 1, nullptr);
     }
 }
 
@@ -134,6 +138,50 @@ __device__ __forceinline__ void mma_issuer(const Params& p, Smem& s, uint32_t ra
     __syncwarp();
 }
 
+// ---------------------------------------------------------------- scaler (warp 2)
+template <bool kGated>
+__device__ __forceinline__ void scaler(const Params& p, Smem& s, int lane, volatile int* abort_flag) {
+    const int units = unit_count<kT>(p, s.tables);
+    uint32_t ch = 0;
+    bool ok = true;
+    for (int u = blockIdx.x >> 1; ok && u < units; u += gridDim.x >> 1) {
+        const Unit t = unit(p, s, u);
+        // weight scales of 32 blocks, one a lane, of the pair's two tiles, or of gate and up
+        const int srow = kGated ? t.pair : 2 * t.pair;
+        const float* ws0 = p.w_scales + (static_cast<int64_t>(t.e) * p.scale_rows + srow) * p.nb + t.b0 + lane;
+        const int to1 = kGated ? p.scale_rows / 2 * p.nb : (srow + 1 < p.scale_rows ? p.nb : 0);
+        const int blocks = t.b1 - t.b0;
+        auto scale_of = [&](int i, int off) { return i + lane < blocks ? __ldg(ws0 + i + off) : 0.0f; };
+        float next0 = scale_of(0, 0), next1 = scale_of(0, to1), cur0 = 0.0f, cur1 = 0.0f;
+        for (int i = 0; i < blocks; i += kChunk, ++ch) {
+            const int sl = ch % kSlots;
+            const uint32_t phase = (ch / kSlots) & 1;
+            if ((i & 31) == 0) {
+                cur0 = next0;
+                cur1 = next1;
+                next0 = scale_of(i + 32, 0);
+                next1 = scale_of(i + 32, to1);
+            }
+            ok = dev::mbar_wait(&s.sc_full[sl], phase, abort_flag) && dev::mbar_wait(&s.factor_empty[sl], phase ^ 1, abort_flag);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+#pragma unroll
+            for (int j = 0; j < kChunk; ++j) {
+                const float w0 = __shfl_sync(0xFFFFFFFFu, cur0, (i + j) & 31), w1 = __shfl_sync(0xFFFFFFFFu, cur1, (i + j) & 31);
+                const float4 x = *reinterpret_cast<const float4*>(&s.sx[sl][j][4 * lane]);
+                *reinterpret_cast<float4*>(&s.factor[sl][j][0][4 * lane]) = make_float4(x.x * w0, x.y * w0, x.z * w0, x.w * w0);
+                *reinterpret_cast<float4*>(&s.factor[sl][j][1][4 * lane]) = make_float4(x.x * w1, x.y * w1, x.z * w1, x.w * w1);
+            }
+            __syncwarp();
+            if (lane == 0) {
+                dev::mbar_arrive(&s.factor_full[sl]);
+                dev::mbar_arrive(&s.sc_empty[sl]);
+            }
+        }
+    }
+    if (!ok && lane == 0) fail(p, abort_flag);
+}
+
 // acc += d * f for 32 columns, the first 16 with f0 and the others with f1.
 __device__ __forceinline__ void accumulate(const uint32_t (&d)[32], float f0, float f1, float2 (&acc)[16]) {
 #pragma unroll
@@ -156,7 +204,12 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
     const int local = 32 * q + lane;
     const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16) + 64u * h;
     const uint32_t leader_ready = dev::mapa(&s.ready[0], 0);
-    uint32_t v = 0, ch = 0, nu = 0;
+    const uint32_t acc_full = dev::smem_u32(&s.acc_full[0]), factor_full = dev::smem_u32(&s.factor_full[0]);
+    const float* factors = &s.factor[0][0][kGated ? 0 : h >> 1][local];
+    uint32_t slot = 0, phase = 0;     // of the next block's accumulator
+    uint32_t after = kAcc;            // the place in the ring of the block that takes the accumulator next
+    uint32_t chunk = 0, chunk_phase = 0;
+    uint32_t nu = 0;
     bool ok = true;
     for (int u = blockIdx.x >> 1; u < units; u += gridDim.x >> 1) {
         const Unit t = unit(p, s, u);
@@ -169,45 +222,37 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
         for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[c][i] = make_float2(0.0f, 0.0f);
-        // weight scales of 32 blocks, one a lane: the tile's, or gate and up
-        const int srow = kGated ? t.pair : 2 * t.pair + (h >> 1);
-        const float* ws0 = p.w_scales + (static_cast<int64_t>(t.e) * p.scale_rows + min(srow, p.scale_rows - 1)) * p.nb + lane;
-        const int up = kGated ? p.scale_rows / 2 * p.nb : 0;   // the up scales from the gate's
         const int blocks = t.b1 - t.b0;
-        auto scale_of = [&](int i, int off) { return i + lane < blocks ? __ldg(ws0 + t.b0 + i + off) : 0.0f; };
-        float next0 = scale_of(0, 0), next1 = kGated ? scale_of(0, up) : 0.0f;
-        float cur0 = 0.0f, cur1 = 0.0f;
+        // (little besides the loads and the arithmetic: with the scales and the rings' index arithmetic in
+        // it, this loop's own instructions took most of a block's time)
 #pragma unroll 1
-        for (int i = 0; i < blocks; ++i, ++v) {
-            const int in_chunk = i % kScChunk, sl = ch % kScSlots;
-            if ((i & 31) == 0) {
-                cur0 = next0;
-                cur1 = next1;
-                next0 = scale_of(i + 32, 0);
-                if (kGated) next1 = scale_of(i + 32, up);
-            }
-            if (in_chunk == 0) ok &= dev::mbar_wait(&s.sc_full[sl], (ch / kScSlots) & 1, abort_flag);
-            const float sx = s.sx[sl][in_chunk][local];
-            const float f0 = sx * __shfl_sync(0xFFFFFFFFu, cur0, i & 31);
-            const float f1 = kGated ? sx * __shfl_sync(0xFFFFFFFFu, cur1, i & 31) : f0;
-            ok &= dev::mbar_wait(&s.acc_full[v % kAcc], (v / kAcc) & 1, abort_flag);
+        for (int i = 0; i < blocks; ++i) {
+            const int j = i % kChunk;
+            if (j == 0) ok &= wait_at(factor_full + chunk * 8u, chunk_phase, abort_flag);
+            const float* f = factors + (chunk * kChunk + j) * 256;
+            const float f0 = f[0], f1 = kGated ? f[128] : f0;
+            ok &= wait_at(acc_full + slot * 8u, phase, abort_flag);
             __syncwarp();
             dev::tc_fence_after();
-            const uint32_t at = base + (v % kAcc) * 256u;
+            const uint32_t at = base + slot * 256u;
             uint32_t d[32];
             dev::tmem_ld32(at, d);
             dev::tmem_ld_wait32(d);
             accumulate(d, f0, f1, acc[0]);
             dev::tmem_ld32(at + 32u, d);
             dev::tmem_ld_wait32(d);
-            // all of it is in registers: the accumulator is free for block v + kAcc
+            // all of it is in registers: the accumulator is free
             dev::tc_fence_before();
             __syncwarp();
-            if (lane == 0) dev::mbar_arrive_remote(leader_ready + ((v + kAcc) % kRing) * 8u);
-            if (in_chunk == kScChunk - 1 || i + 1 == blocks) {
-                if (lane == 0) dev::mbar_arrive(&s.sc_empty[sl]);
-                ++ch;
+            if (lane == 0) dev::mbar_arrive_remote(leader_ready + after * 8u);
+            if (j == kChunk - 1 || i + 1 == blocks) {
+                if (lane == 0) dev::mbar_arrive(&s.factor_empty[chunk]);
+                chunk ^= 1;
+                chunk_phase ^= chunk ^ 1;
             }
+            slot ^= 1;
+            phase ^= slot ^ 1;
+            after = (after + 1) % kRing;
             accumulate(d, f0, f1, acc[1]);
         }
         ok = __all_sync(0xFFFFFFFFu, ok);
@@ -346,9 +391,11 @@ fp8_wide_kernel(const Params p, const __grid_constant__ CUtensorMap scales) {
         for (int i = 0; i < kRing; ++i) dev::mbar_init(&s.ready[i], rank == 0 ? 2 + 2 * kWideEpi : 1);
         for (int i = 0; i < kStages; ++i) dev::mbar_init(&s.empty[i], 1);
         for (int i = 0; i < kAcc; ++i) dev::mbar_init(&s.acc_full[i], 1);
-        for (int i = 0; i < kScSlots; ++i) {
+        for (int i = 0; i < kSlots; ++i) {
             dev::mbar_init(&s.sc_full[i], 1);
-            dev::mbar_init(&s.sc_empty[i], kWideEpi);
+            dev::mbar_init(&s.sc_empty[i], 1);
+            dev::mbar_init(&s.factor_full[i], 1);
+            dev::mbar_init(&s.factor_empty[i], kWideEpi);
         }
         dev::mbar_init(&s.mma_done, 1);
         s.abort_flag = 0;
@@ -372,6 +419,8 @@ fp8_wide_kernel(const Params p, const __grid_constant__ CUtensorMap scales) {
             if (lane == 0) producer(p, &scales, s, rank, abort_flag);
         } else if (warp == 1) {
             mma_issuer(p, s, rank, tmem, abort_flag);
+        } else if (warp == 2) {
+            scaler<kGated>(p, s, lane, abort_flag);
         }
         __syncwarp();
     } else {
@@ -422,12 +471,12 @@ bool encode_code_map(CUtensorMap* map, const void* codes, int64_t rows, int nb, 
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool encode_scale_map(CUtensorMap* map, const float* scales, int64_t sstride, int nb, int tokens) {
+bool encode_scale_map(CUtensorMap* map, const float* scales, int64_t sstride, int nb, int tokens, int blocks) {
     const EncodeTiledFn encode = encode_tiled();
     if (encode == nullptr) return false;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(sstride), static_cast<cuuint64_t>(nb)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(sstride) * sizeof(float)};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(tokens), fp8::kScChunk}, step[2] = {1, 1};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(tokens), static_cast<cuuint32_t>(blocks)}, step[2] = {1, 1};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float*>(scales), dims, strides, box, step,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -436,7 +485,7 @@ bool encode_scale_map(CUtensorMap* map, const float* scales, int64_t sstride, in
 cudaError_t launch_fp8_wide(const fp8_layer& L, const fp8::Params& p, const float* a_scales, int64_t tiles, bool pdl,
                             cudaStream_t stream) {
     CUtensorMap map;
-    if (!encode_scale_map(&map, a_scales, p.sstride, L.nb, 128)) return cudaErrorInvalidValue;
+    if (!encode_scale_map(&map, a_scales, p.sstride, L.nb, 128, fp8::kChunk)) return cudaErrorInvalidValue;
     const int64_t units = tiles * L.pairs * p.splits;
     const int grid = 2 * static_cast<int>(units < fp8_resident_pairs(L) ? units : fp8_resident_pairs(L));
     auto fn = L.gated ? fp8::fp8_wide_kernel<true> : fp8::fp8_wide_kernel<false>;
