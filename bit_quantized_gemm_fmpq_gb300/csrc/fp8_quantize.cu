@@ -36,22 +36,19 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
     return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xFFFFu)));
 }
 
-// A warp takes one token's 256 channels at a time: 16 lanes a block, 8 channels a lane (one
-// 16-byte load, 8 bytes of codes). Tokens vary fastest over the warps, so that a CTA's stores of
-// a block's codes (128 bytes a row) and scales are contiguous.
+// A warp takes 256 channels of a token, 16 lanes a block, 8 channels a lane (one 16-byte load, 8 bytes
+// of codes); blockIdx.y chooses the channels, so that a CTA's stores of a block's codes (128 bytes a
+// row) and scales are contiguous.
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ X, int64_t ldx, int64_t M, int K, int nb,
                                                        const int32_t* __restrict__ positions, int slots, int64_t rows,
                                                        int64_t sstride, uint8_t* __restrict__ A,
                                                        float* __restrict__ scales) {
     const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
-    const int64_t tasks = M * ((nb + 1) / 2);
     dev::pdl_wait();
     dev::pdl_launch_dependents();
-    for (int64_t task = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); task < tasks;
-         task += static_cast<int64_t>(gridDim.x) * 8) {
-        const int64_t m = task % M;
-        const int b = static_cast<int>(task / M) * 2 + half;
+    const int b = static_cast<int>(blockIdx.y) * 2 + half;
+    for (int64_t m = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); m < M; m += static_cast<int64_t>(gridDim.x) * 8) {
         const int k0 = b * 128 + l * 8;
         const T* x = X + m * ldx + k0;
         float v[8];
@@ -178,11 +175,12 @@ template <typename T>
 cudaError_t quantize_as(const void* X, int64_t ldx, int64_t M, int K, const int32_t* positions, int slots, int64_t rows,
                         void* A, float* scales, int num_sms, bool pdl, cudaStream_t stream) {
     const int nb = (K + 127) / 128;
-    const int64_t tasks = M * ((nb + 1) / 2), ctas = (tasks + 7) / 8;
-    const int grid = static_cast<int>(ctas < num_sms * 64LL ? ctas : num_sms * 64LL);
+    const int pairs = (nb + 1) / 2;
+    const int64_t ctas = (M + 7) / 8, most = (num_sms * 64LL + pairs - 1) / pairs;
+    const dim3 grid(static_cast<unsigned>(ctas < most ? ctas : most), static_cast<unsigned>(pairs));
     const bool vec = ldx % 8 == 0 && (reinterpret_cast<uintptr_t>(X) & 15u) == 0;
     auto fn = vec ? quantize_kernel<T, true> : quantize_kernel<T, false>;
-    return launch_after(fn, dim3(static_cast<unsigned>(grid)), 256, 0, pdl, stream, static_cast<const T*>(X), ldx, M, K, nb,
+    return launch_after(fn, grid, 256, 0, pdl, stream, static_cast<const T*>(X), ldx, M, K, nb,
                         positions, positions != nullptr ? slots : 1, rows, scale_stride(rows), static_cast<uint8_t*>(A), scales);
 }
 

@@ -552,27 +552,33 @@ __global__ void __launch_bounds__(kChunk) plan_place_kernel(const int32_t* __res
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(256) combine_kernel(const T* __restrict__ D, int64_t ldd, const int32_t* __restrict__ row_of,
                                                       int64_t tokens, int k, int N, T* __restrict__ Y, int64_t ldy) {
-    const int per_row = (N + 7) / 8;
     dev::pdl_wait();
     dev::pdl_launch_dependents();
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < tokens * per_row;
-         i += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t t = i / per_row;
-        const int n = static_cast<int>(i % per_row) * 8;
+    const int n = static_cast<int>(blockIdx.x * 256 + threadIdx.x) * 8;
+    if (n >= N) return;
+    for (int64_t t = blockIdx.y; t < tokens; t += gridDim.y) {
         float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         const bool whole = kVec && n + 8 <= N;
-        for (int j = 0; j < k; ++j) {
-            const int32_t r = row_of[t * k + j];
-            if (r < 0) continue;
-            const T* d = D + r * ldd + n;
-            if (whole) {
-                T v[8];
-                *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(d);
+        for (int j0 = 0; j0 < k; j0 += 4) {   // four rows in flight
+            int32_t r[4];
+            uint4 raw[4];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) acc[c] += as_float(v[c]);
+            for (int j = 0; j < 4; ++j) r[j] = j0 + j < k ? row_of[t * k + j0 + j] : -1;
+            if (whole) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (r[j] >= 0) raw[j] = *reinterpret_cast<const uint4*>(D + r[j] * ldd + n);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (r[j] >= 0) {
+                        const T* v = reinterpret_cast<const T*>(&raw[j]);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) acc[c] += as_float(v[c]);
+                    }
             } else {
-                for (int c = 0; c < 8; ++c)
-                    if (n + c < N) acc[c] += as_float(d[c]);
+                for (int j = 0; j < 4; ++j)
+                    for (int c = 0; c < 8; ++c)
+                        if (r[j] >= 0 && n + c < N) acc[c] += as_float(D[r[j] * ldd + n + c]);
             }
         }
         T o[8];
@@ -591,12 +597,11 @@ __global__ void __launch_bounds__(256) combine_kernel(const T* __restrict__ D, i
 template <typename T>
 cudaError_t combine_as(const void* D, int64_t ldd, const int32_t* row_of, int64_t tokens, int k, int N, void* Y, int64_t ldy,
                        bool pdl, cudaStream_t stream) {
-    const int64_t ctas = (tokens * ((N + 7) / 8) + 255) / 256;
-    const int grid = static_cast<int>(ctas < 1 << 20 ? ctas : 1 << 20);
+    const dim3 grid(static_cast<unsigned>(((N + 7) / 8 + 255) / 256), static_cast<unsigned>(tokens < 65535 ? tokens : 65535));
     const bool vec = ldd % 8 == 0 && ldy % 8 == 0 &&
                      ((reinterpret_cast<uintptr_t>(D) | reinterpret_cast<uintptr_t>(Y)) & 15u) == 0;
     auto fn = vec ? combine_kernel<T, true> : combine_kernel<T, false>;
-    return launch_after(fn, dim3(static_cast<unsigned>(grid)), 256, 0, pdl, stream, static_cast<const T*>(D), ldd, row_of, tokens, k, N,
+    return launch_after(fn, grid, 256, 0, pdl, stream, static_cast<const T*>(D), ldd, row_of, tokens, k, N,
                         static_cast<T*>(Y), ldy);
 }
 
