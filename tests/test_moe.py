@@ -268,6 +268,7 @@ CASES = [
     (130, 8, 32, 384, 384, 512, 0.5, 0.0),
     # more tiles than pairs of CTAs: several a pair, for many tokens an expert and for few
     (700, 2, 3, 256, 2560, 5200, 0.0, 0.0), (64, 4, 16, 256, 1280, 2600, 0.5, 0.1),
+    (160, 2, 4, 256, 200, 264, 0.0, 0.0), (150, 4, 7, 200, 1300, 2500, 0.3, 0.1),
 ]
 
 
@@ -378,3 +379,11 @@ def test_experts_binding_refusals(fmpq_mod):
         fmpq_mod.moe_route(X[0], 1)
     with pytest.raises(fmpq_mod.FmpqError):
         fmpq_mod.moe_route(X, 200)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tokens", [1, 40, 700])
+def test_example_step(fmpq_mod, tokens):
+    """The example's captured step: two bf16 roundings and flipped codes (see the head of this file)."""
+    from examples import routed_experts
+    assert routed_experts.main(tokens) <= 2.0 ** -7 + 2.8e-3
