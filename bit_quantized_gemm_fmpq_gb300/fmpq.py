@@ -9,6 +9,7 @@ fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -578,6 +579,20 @@ def qoq_gemm_partials(layout: Layout, A_packed, W_packed, M: int, N: int, m0: in
 
 
 # ---- E4M3 linear layers: a scale for each block of 128 ------------------------------------
+# Every call below also takes stream=: it then runs, and allocates, as under torch.cuda.stream(stream).
+
+def _on_stream(call):
+    """Run a call under its `stream` argument (a torch stream or a raw handle), so that its buffers come from
+    that stream's memory and are not given to other work before it is done."""
+    @functools.wraps(call)
+    def wrapped(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        import torch
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+            return call(*args, **kw)
+    return wrapped
+
 
 _DTYPES = {}
 
@@ -612,12 +627,10 @@ def _ld(X) -> int:
     return max(X.stride(0), X.shape[1]) if X.shape[0] > 1 else X.shape[1]
 
 
-def _on(X, stream) -> int:
-    """The stream to launch on: the given one, or torch's current one for X's device."""
-    if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(X.device.index)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+def _on(X) -> int:
+    """torch's current stream for X's device."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(X.device.index)
 
 
 class Fp8Layer:
@@ -662,7 +675,7 @@ class Fp8Layer:
         return (torch.empty((self.nb, rows, BLOCK), dtype=torch.uint8, device=device),
                 torch.empty((self.nb, (rows + 3) // 4 * 4), dtype=torch.float32, device=device))
 
-    def workspace(self, M: int, stream=None):
+    def workspace(self, M: int):
         """fp8_gemm's workspace for M rows: zeroed, reused by later calls on the same stream; one that a
         stream capture creates belongs to that graph alone."""
         import torch
@@ -673,18 +686,15 @@ class Fp8Layer:
             return None
         if torch.cuda.is_current_stream_capturing():
             return torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
-        key = (nbytes, torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None
-               else stream if isinstance(stream, int) else stream.cuda_stream)
+        key = (nbytes, torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
         ws = self._workspaces.get(key)
         if ws is None:
-            ws = torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
-            if stream is not None:
-                torch.cuda.current_stream().synchronize()   # zeroed before another stream uses it
-            self._workspaces[key] = ws
+            ws = self._workspaces[key] = torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
         return ws
 
 
-def fp8_pack_weights(layer: Fp8Layer, W, stream=None):
+@_on_stream
+def fp8_pack_weights(layer: Fp8Layer, W):
     """Quantize W (fp16 or bf16, [N, K], or [experts, N, K]) per 128 x 128 block. Returns (W_packed u8,
     w_scales fp32 [experts, scale rows, nb])."""
     import torch
@@ -695,11 +705,12 @@ def fp8_pack_weights(layer: Fp8Layer, W, stream=None):
     for e in range(layer.experts):
         _rows16(W3[e], "W")
         _check("fp8_pack_weights", layer._lib.fp8_pack_weights(layer.handle, e, _ptr(W3[e]), _dtype_code(W.dtype),
-                                                               _ld(W3[e]), _ptr(Wp), _ptr(ws), _stream(stream)))
+                                                               _ld(W3[e]), _ptr(Wp), _ptr(ws), _stream(None)))
     return Wp, ws
 
 
-def fp8_pack_codes(layer: Fp8Layer, codes, scales, stream=None):
+@_on_stream
+def fp8_pack_codes(layer: Fp8Layer, codes, scales):
     """Lay out an E4M3 checkpoint: codes float8_e4m3fn (or its bytes) [experts, N, K] or [N, K], scales
     fp32 [experts, scale rows, nb] or [scale rows, nb] (value = code * scale). Returns (W_packed u8,
     w_scales)."""
@@ -714,19 +725,21 @@ def fp8_pack_codes(layer: Fp8Layer, codes, scales, stream=None):
     Wp = torch.empty(layer.packed_w_bytes(), dtype=torch.uint8, device=codes.device)
     for e in range(layer.experts):
         _check("fp8_pack_codes", layer._lib.fp8_pack_codes(layer.handle, e, _ptr(C[e]), _ld(C[e]), _ptr(Wp),
-                                                           _stream(stream)))
+                                                           _stream(None)))
     return Wp, S.contiguous()
 
 
-def fp8_unpack_weights(layer: Fp8Layer, W_packed, w_scales, expert: int = 0, stream=None):
+@_on_stream
+def fp8_unpack_weights(layer: Fp8Layer, W_packed, w_scales, expert: int = 0):
     import torch
     W = torch.empty((layer.N, layer.K), dtype=torch.float32, device=W_packed.device)
     _check("fp8_unpack_weights", layer._lib.fp8_unpack_weights(layer.handle, expert, _ptr(W_packed), _ptr(w_scales),
-                                                               _ptr(W), _stream(stream)))
+                                                               _ptr(W), _stream(None)))
     return W
 
 
-def fp8_quantize(layer: Fp8Layer, X, A_packed=None, a_scales=None, stream=None):
+@_on_stream
+def fp8_quantize(layer: Fp8Layer, X, A_packed=None, a_scales=None):
     """X fp16 or bf16 [M, K], any row stride. Returns (A_packed u8, a_scales fp32), see
     Fp8Layer.activations."""
     _rows16(X, "X")
@@ -736,33 +749,33 @@ def fp8_quantize(layer: Fp8Layer, X, A_packed=None, a_scales=None, stream=None):
         A, s = layer.activations(M, X.device)
         A_packed, a_scales = A if A_packed is None else A_packed, s if a_scales is None else a_scales
     _check("fp8_quantize", layer._lib.fp8_quantize(layer.handle, _ptr(X), _dtype_code(X.dtype), _ld(X), M,
-                                                   _ptr(A_packed), _ptr(a_scales), _stream(stream)))
+                                                   _ptr(A_packed), _ptr(a_scales), _stream(None)))
     return A_packed, a_scales
 
 
-def _workspace_of(layer: Fp8Layer, M: int, workspace, stream):
+def _workspace_of(layer: Fp8Layer, M: int, workspace):
     if workspace is None:
-        workspace = layer.workspace(M, stream)
+        workspace = layer.workspace(M)
     return workspace, workspace.numel() if workspace is not None else 0
 
 
-def fp8_gemm(layer: Fp8Layer, A_packed, a_scales, W_packed, w_scales, M: int, dtype=None, Y=None, workspace=None,
-             stream=None):
+@_on_stream
+def fp8_gemm(layer: Fp8Layer, A_packed, a_scales, W_packed, w_scales, M: int, dtype=None, Y=None, workspace=None):
     """Y [M, N] (fp16 by default) of quantized activations and packed weights."""
     import torch
     if Y is None:
         Y = torch.empty((M, layer.N), dtype=dtype or torch.float16, device=A_packed.device)
     _rows16(Y, "Y")
     _need(Y.shape == (M, layer.N), "Y must be [M, N]")
-    workspace, nbytes = _workspace_of(layer, M, workspace, stream)
+    workspace, nbytes = _workspace_of(layer, M, workspace)
     _check("fp8_gemm", layer._lib.fp8_gemm(layer.handle, _ptr(A_packed), _ptr(a_scales), _ptr(W_packed), _ptr(w_scales), M,
                                            _ptr(Y), _dtype_code(Y.dtype), _ld(Y), _ptr(workspace), nbytes,
-                                           _stream(stream)))
+                                           _stream(None)))
     return Y
 
 
-def fp8_quantize_gemm(layer: Fp8Layer, X, W_packed, w_scales, A_packed=None, a_scales=None, Y=None, workspace=None,
-                      stream=None):
+@_on_stream
+def fp8_quantize_gemm(layer: Fp8Layer, X, W_packed, w_scales, A_packed=None, a_scales=None, Y=None, workspace=None):
     """The layer on X (fp16 or bf16 [M, K]) in one call: Y [M, N] of X's type."""
     import torch
     code = _rows16(X, "X")
@@ -783,11 +796,11 @@ def fp8_quantize_gemm(layer: Fp8Layer, X, W_packed, w_scales, A_packed=None, a_s
     else:
         _need(_rows16(Y, "Y") == code and Y.shape == (M, layer.N), "Y must be [M, N] of X's type")
     if workspace is None:
-        workspace = layer.workspace(M, stream)
+        workspace = layer.workspace(M)
     w_ptr, w_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     _check("fp8_quantize_gemm", layer._lib.fp8_quantize_gemm(
         layer._h, X.data_ptr(), code, _ld(X), M, a_ptr, s_ptr, W_packed.data_ptr(), w_scales.data_ptr(), Y.data_ptr(),
-        _ld(Y), w_ptr, w_bytes, _on(X, stream)))
+        _ld(Y), w_ptr, w_bytes, _on(X)))
     return Y
 
 
@@ -802,8 +815,9 @@ def fp8_device_status(layer: Fp8Layer, clear: bool = True) -> int:
 _SCORES = {"softmax": 0, "sigmoid": 1}
 
 
+@_on_stream
 def moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1,
-              group_top: int = 1, renormalize: bool = True, scale: float = 1.0, ids=None, weights=None, stream=None):
+              group_top: int = 1, renormalize: bool = True, scale: float = 1.0, ids=None, weights=None):
     """The top-k experts of each token from the router's logits [T, E] (fp32, fp16 or bf16): ids int32
     [T, k] (by falling key, -1: none) and weights fp32 [T, k]. score: "softmax" or "sigmoid"; bias: fp32
     [E], added for the choice only; groups: keep the top_groups runs of E / groups experts with the
@@ -830,7 +844,7 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1
               "weights must be fp32 [T, k]")
     _check("moe_route", (_lib or load_library()).moe_route(
         logits.data_ptr(), _dtype_code(logits.dtype), _ld(logits), T, E, k, sigmoid, b_ptr, groups, top_groups, group_top,
-        1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(), _on(logits, stream)))
+        1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(), _on(logits)))
     return ids, weights
 
 
@@ -860,7 +874,8 @@ class MoePlan:
         return self.buffer[2 * self.experts:2 * self.experts + self.T * self.k].view(self.T, self.k)
 
 
-def moe_plan(ids, experts: int, plan=None, stream=None) -> MoePlan:
+@_on_stream
+def moe_plan(ids, experts: int, plan=None) -> MoePlan:
     """Sort the pairs of ids (int32 [T, k]) by expert; ids outside [0, experts) belong to none."""
     import torch
     _need(ids.is_cuda and ids.dim() == 2 and ids.dtype == torch.int32 and ids.is_contiguous(),
@@ -868,11 +883,12 @@ def moe_plan(ids, experts: int, plan=None, stream=None) -> MoePlan:
     T, k = ids.shape
     plan = MoePlan(T, k, experts, ids.device) if plan is None else plan
     _need((plan.T, plan.k, plan.experts) == (T, k, experts), "the plan was made for other sizes")
-    _check("moe_plan", load_library().moe_plan(_ptr(ids), T, k, experts, _ptr(plan.buffer), _stream(stream)))
+    _check("moe_plan", load_library().moe_plan(_ptr(ids), T, k, experts, _ptr(plan.buffer), _stream(None)))
     return plan
 
 
-def moe_quantize(layer: Fp8Layer, plan: MoePlan, X, A_packed=None, a_scales=None, stream=None):
+@_on_stream
+def moe_quantize(layer: Fp8Layer, plan: MoePlan, X, A_packed=None, a_scales=None):
     """Quantize each token of X [T, K] once into its experts' rows."""
     _rows16(X, "X")
     _need(X.shape == (plan.T, layer.K) and plan.experts == layer.experts, "X must be [T, K], the plan the layer's")
@@ -881,12 +897,12 @@ def moe_quantize(layer: Fp8Layer, plan: MoePlan, X, A_packed=None, a_scales=None
         A_packed, a_scales = A if A_packed is None else A_packed, s if a_scales is None else a_scales
     _check("moe_quantize", layer._lib.moe_quantize(layer.handle, _ptr(plan.buffer), plan.T, plan.k, _ptr(X),
                                                    _dtype_code(X.dtype), _ld(X), _ptr(A_packed), _ptr(a_scales),
-                                                   _stream(stream)))
+                                                   _stream(None)))
     return A_packed, a_scales
 
 
-def moe_up(layer: Fp8Layer, plan: MoePlan, A_packed, a_scales, W_packed, w_scales, H_packed=None, h_scales=None,
-           stream=None):
+@_on_stream
+def moe_up(layer: Fp8Layer, plan: MoePlan, A_packed, a_scales, W_packed, w_scales, H_packed=None, h_scales=None):
     """SwiGLU of the gated layer's products, quantized: codes uint8 [F / 128, rows, 128] and scales."""
     import torch
     _need(layer.gated and plan.experts == layer.experts, "moe_up needs a gated layer and its plan")
@@ -896,12 +912,12 @@ def moe_up(layer: Fp8Layer, plan: MoePlan, A_packed, a_scales, W_packed, w_scale
     if h_scales is None:
         h_scales = torch.empty((fb, (plan.rows + 3) // 4 * 4), dtype=torch.float32, device=A_packed.device)
     _check("moe_up", layer._lib.moe_up(layer.handle, _ptr(plan.buffer), plan.T, plan.k, _ptr(A_packed), _ptr(a_scales),
-                                       _ptr(W_packed), _ptr(w_scales), _ptr(H_packed), _ptr(h_scales), _stream(stream)))
+                                       _ptr(W_packed), _ptr(w_scales), _ptr(H_packed), _ptr(h_scales), _stream(None)))
     return H_packed, h_scales
 
 
-def moe_down(layer: Fp8Layer, plan: MoePlan, A_packed, a_scales, W_packed, w_scales, weights=None, dtype=None, D=None,
-             stream=None):
+@_on_stream
+def moe_down(layer: Fp8Layer, plan: MoePlan, A_packed, a_scales, W_packed, w_scales, weights=None, dtype=None, D=None):
     """Every row's product with its expert, times its pair's weight: D [plan.rows, N] (fp16 by default)."""
     import torch
     _need(plan.experts == layer.experts and not layer.gated, "moe_down needs a plain layer and its plan")
@@ -914,11 +930,12 @@ def moe_down(layer: Fp8Layer, plan: MoePlan, A_packed, a_scales, W_packed, w_sca
     _need(D.shape == (plan.rows, layer.N), "D must be [rows, N]")
     _check("moe_down", layer._lib.moe_down(layer.handle, _ptr(plan.buffer), plan.T, plan.k, _ptr(weights), _ptr(A_packed),
                                            _ptr(a_scales), _ptr(W_packed), _ptr(w_scales), _ptr(D), _dtype_code(D.dtype),
-                                           _ld(D), _stream(stream)))
+                                           _ld(D), _stream(None)))
     return D
 
 
-def moe_combine(D, plan: MoePlan, Y=None, stream=None):
+@_on_stream
+def moe_combine(D, plan: MoePlan, Y=None):
     """Y [T, N]: the sum of D's rows of each token."""
     import torch
     _rows16(D, "D")
@@ -928,11 +945,12 @@ def moe_combine(D, plan: MoePlan, Y=None, stream=None):
     _rows16(Y, "Y")
     _need(Y.shape == (plan.T, D.shape[1]) and Y.dtype == D.dtype, "Y must be [T, N] of D's type")
     _check("moe_combine", load_library().moe_combine(_ptr(D), _dtype_code(D.dtype), _ld(D), _ptr(plan.buffer), plan.T,
-                                                     plan.k, plan.experts, D.shape[1], _ptr(Y), _ld(Y), _stream(stream)))
+                                                     plan.k, plan.experts, D.shape[1], _ptr(Y), _ld(Y), _stream(None)))
     return Y
 
 
-def moe_experts(up: Fp8Layer, down: Fp8Layer, X, ids, weights, W_up, s_up, W_down, s_down, stream=None):
+@_on_stream
+def moe_experts(up: Fp8Layer, down: Fp8Layer, X, ids, weights, W_up, s_up, W_down, s_down):
     """The routed feed-forward on X [T, K]: for each token the sum over its slots of weights[t, j] *
     down(silu(gate(x)) * up(x)) with expert ids[t, j] (-1: none). up: a gated layer [2F, K]; down: [N, F]
     with the same experts. ids and weights as moe_route returns them. Y [T, N] of X's type."""
@@ -947,16 +965,16 @@ def moe_experts(up: Fp8Layer, down: Fp8Layer, X, ids, weights, W_up, s_up, W_dow
           "weights must be contiguous fp32 [T, k]")
     k = ids.shape[1]
     sizes = up._workspace_bytes
-    nbytes = sizes.get((T, k, down))
+    nbytes = sizes.get((T, k, down.N))
     if nbytes is None:
-        nbytes = sizes[(T, k, down)] = int(up._lib.moe_experts_bytes(up._h, down._h, T, k))
+        nbytes = sizes[(T, k, down.N)] = int(up._lib.moe_experts_bytes(up._h, down._h, T, k))
         if nbytes == 0:
-            del sizes[(T, k, down)]
+            del sizes[(T, k, down.N)]
             raise FmpqError("moe_experts", 2)
     scratch = torch.empty(nbytes, dtype=torch.uint8, device=X.device)
     Y = torch.empty((T, down.N), dtype=X.dtype, device=X.device)
     _check("moe_experts", up._lib.moe_experts(
         up._h, down._h, X.data_ptr(), code, _ld(X), T, k, ids.data_ptr(), weights.data_ptr(), W_up.data_ptr(),
         s_up.data_ptr(), W_down.data_ptr(), s_down.data_ptr(), Y.data_ptr(), down.N, scratch.data_ptr(), nbytes,
-        _on(X, stream)))
+        _on(X)))
     return Y

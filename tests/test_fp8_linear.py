@@ -246,6 +246,26 @@ def test_product_on_streams_and_in_a_graph(fmpq_mod):
 
 
 @pytest.mark.gpu
+def test_stream_argument(fmpq_mod):
+    """stream= (a torch stream or its handle) runs and allocates there: scratch is not reused early."""
+    import torch
+    layer = fmpq_mod.Fp8Layer(4096, 1024)
+    w = (torch.randn(1024, 4096, generator=torch.Generator().manual_seed(2)) * 0.02).to(torch.bfloat16)
+    Wp, s = fmpq_mod.fp8_pack_weights(layer, w.cuda())
+    xs = [draw(m, 4096, torch.bfloat16, m) for m in (3, 200, 1500)]
+    want = [fmpq_mod.fp8_quantize_gemm(layer, x, Wp, s) for x in xs]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = []
+    for i in range(6):
+        x = xs[i % 3]
+        got.append(fmpq_mod.fp8_quantize_gemm(layer, x, Wp, s, stream=side if i < 3 else side.cuda_stream))
+        junk = torch.full((1 << 22,), float(i), device="cuda")      # work on the current stream meanwhile
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i % 3]) for i, y in enumerate(got)) and float(junk[0]) == 5.0
+
+
+@pytest.mark.gpu
 def test_binding_refusals(fmpq_mod):
     import torch
     layer = fmpq_mod.Fp8Layer(256, 128)
