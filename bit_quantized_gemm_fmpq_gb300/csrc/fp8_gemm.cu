@@ -4,65 +4,63 @@
 //   Y[m][n] = sum_b a_scale[b][m] * w_scale[n / 128][b] * P[m][n][b],
 //   P[m][n][b] = sum over the 128 channels of block b of a_code * w_code.
 //
-// One kernel serves one token and thousands. The tensor core's M side is the weights: a pair of
-// CTAs covers 256 packed weight rows (128 each, a 16 KB bulk copy a block), its N side the tokens
-// of a tile, 32 to 256 of them in steps of 32. So a tile costs tensor time in proportion to its tokens
-// (an expert's 150 tokens cost 160 columns, not 256), few tokens leave a pure weight stream, and the
-// 256 x 256 pair tile of long prompts reads each operand byte half as often as two single CTAs.
-//   * P is an FP32 accumulator tile in TMEM for one block of 128 (4 MMAs); 2, 4 or 8 of them, so that
-//     the next blocks' MMAs run while the epilogue scales this one into FP32 registers.
-//   * An epilogue thread owns one weight row (a TMEM lane) and half of the tile's tokens. A scaler
-//     warp multiplies the block's token scales by its weight scale beforehand, so that a pair of
-//     sums costs one packed multiply-add and half a broadcast shared load.
+// This file: few tokens a matrix (a decode step, an expert's share of one), and the choice between this
+// kernel and the one for many (fp8_gemm_wide.cu). Reading the weights bounds it. The tensor core's M
+// side is the weights: a pair of CTAs covers 256 packed weight rows (128 each, a 16 KB bulk copy a
+// block, 128 KB in flight per SM); its N side is a tile of 32 or 64 tokens.
+//   * P is an FP32 accumulator tile in TMEM for one block of 128 (4 MMAs), eight of them, so that the
+//     next blocks' MMAs run while the epilogue scales this one into FP32 registers.
+//   * An epilogue thread owns one weight row (a TMEM lane) and 32 tokens. A scaler warp multiplies the
+//     block's token scales by its weight scale beforehand, so that a pair of sums costs one packed
+//     multiply-add and half a broadcast shared load. Up to 32 tokens, the two warps of a lane quarter
+//     take the blocks in turn: the chain of a block through one warp (wait, TMEM load, arithmetic,
+//     release: about 650 clk) is as long as a 16 KB copy takes at the HBM's rate.
 //   * A gated layer's rows are packed so that a warp holds the gate and the up rows of the same 16
 //     hidden channels in its two halves: SwiGLU and the E4M3 quantization of the hidden vector
 //     happen in registers, with one absmax per token exchanged inside the pair.
+//   * The weights' stream starts before the codes are there (the kernel is launched as the quantizer's
+//     programmatic dependent); token codes come four blocks a box, one copy per block being what the
+//     copy engine and the issuing warp keep up with.
+// Measured (quantizer included): one token of 8192 x 8192 21.1 us, 67.1 MB = 3.2 TB/s (a stream this short does
+// not reach the copy rate); 64 tokens through 8 of 128 experts of 4096 x 1024, 1.59 GB in 272 us = 5.8 TB/s, 86% of
+// the measured copy rate.
 //
 // Warp roles (384 threads, one CTA per SM, pairs persistent over tiles):
 //   warp 0      weight producer (a 16 KB block a copy)
 //   warp 1      even CTA: MMA issuer; odd CTA: reports its operands to the even one
 //   warp 2      scaler; also allocates and frees TMEM
 //   warp 3      token producer: codes and scales of four blocks at a time
-//   warps 4-11  epilogue: TMEM lane quarter warp % 4, half of the tile's tokens each
+//   warps 4-11  epilogue: TMEM lane quarter warp % 4, half of the tile's tokens (or of the blocks) each
 #include "fp8_gemm.cuh"
 
 namespace fmpq {
 namespace fp8 {
 namespace {
 
-constexpr int kRing = 16;   // blocks whose readiness may be in flight (> kStages, > 2 kMaxAcc - 1)
-constexpr int kProd = 4;    // blocks of scale products
-constexpr int kMaxAcc = 8;
+constexpr int kRing = 16;      // blocks whose readiness may be in flight (> kStages, > 2 kAcc - 1)
+constexpr int kProd = 4;       // blocks of scale products
+constexpr int kTokens = 64;    // of a tile, at most
+constexpr int kAcc = 8;        // accumulators of kTokens columns in 512
+constexpr int kStages = 8;     // weight blocks in flight
 
-// Token tiles of up to 64 kC tokens (kC = 1, 2): kC loads of 32 TMEM columns an epilogue warp.
-template <int kC>
-struct Shape {
-    static constexpr int kTokens = 64 * kC;
-    static constexpr int kAcc = kC == 1 ? 8 : 4;      // accumulators of kTokens columns in 512
-    static constexpr int kStages = kC == 1 ? 8 : 6;   // weight blocks in flight
-};
-
-template <int kC>
 struct __align__(1024) Smem {
-    static constexpr int kT = Shape<kC>::kTokens;
-    static constexpr int kStages = Shape<kC>::kStages;
-    uint8_t w[kStages][kTileBytes];              // weight block: this CTA's 128 rows
-    uint8_t x[kScSlots][kScChunk][kT * 64];      // token codes of a chunk of blocks: this CTA's half of the tile
-    float sx[kScSlots][kScChunk][kT];            // token scales of the chunk
+    uint8_t w[kStages][kTileBytes];                // weight block: this CTA's 128 rows
+    uint8_t x[kScSlots][kScChunk][kTokens * 64];   // token codes of a chunk of blocks: this CTA's half of the tile
+    float sx[kScSlots][kScChunk][kTokens];         // token scales of the chunk
     // token scales times the block's weight scale; gated: [0] gate, [1] up (the 16-byte skew keeps
     // the two halves of a warp in different banks)
-    float prod[kProd][2][kT + 4];
+    float prod[kProd][2][kTokens + 4];
     // gated: absmax of 16 hidden channels (a quarter's), of this CTA's 64 and the peer's 64, the
     // tokens' scales
-    float amax[4][kT], amax_peer[2][kT], hscale[kT];
-    float2 other_turn[kC == 1 ? 16 : 1][128];    // up to 32 tokens: the sums of every second block
+    float amax[4][kTokens], amax_peer[2][kTokens], hscale[kTokens];
+    float2 other_turn[16][128];   // up to 32 tokens: the sums of every second block
     // ready[b % kRing], even CTA: block b's weights have landed in both CTAs, the odd one's token codes
     // too, and its accumulator has been read (by both CTAs' epilogue warps). Odd CTA: its weights have
     // landed. sc_full: a chunk's token codes and scales have landed here; sc_empty: the scaler has read the
     // scales and the chunk's MMAs are done.
     uint64_t ready[kRing];
     uint64_t empty[kStages];
-    uint64_t acc_full[kMaxAcc];
+    uint64_t acc_full[kAcc];
     uint64_t sc_full[kScSlots], sc_empty[kScSlots];
     uint64_t prod_full[kProd], prod_empty[kProd];
     uint64_t amax_full[2];
@@ -73,9 +71,8 @@ struct __align__(1024) Smem {
     Tables tables;
 };
 
-template <int kC>
-__device__ __forceinline__ Unit unit(const Params& p, const Smem<kC>& s, int u) {
-    return unit_of<Shape<kC>::kTokens, true>(p, s.tables, u);
+__device__ __forceinline__ Unit unit(const Params& p, const Smem& s, int u) {
+    return unit_of<kTokens>(p, s.tables, u);
 }
 // Columns of a tile's MMAs: its tokens rounded up to 32.
 __device__ __forceinline__ int columns(const Unit& t) { return max(32, (t.n + 31) & ~31); }
@@ -84,14 +81,12 @@ __device__ __forceinline__ int columns(const Unit& t) { return max(32, (t.n + 31
 // Whole warps, one elected lane issuing: with one lane alone in the loop the addresses leave the uniform
 // registers and a block took about 600 clk of issue. Warp 0 streams the weights, which no earlier kernel
 // writes, from the start.
-template <int kC>
-__device__ __forceinline__ void weight_producer(const Params& p, Smem<kC>& s, uint32_t rank, volatile int* abort_flag) {
-    constexpr int kStages = Shape<kC>::kStages;
-    const int units = unit_count<Shape<kC>::kTokens>(p, s.tables);
+__device__ __forceinline__ void weight_producer(const Params& p, Smem& s, uint32_t rank, volatile int* abort_flag) {
+    const int units = unit_count<kTokens>(p, s.tables);
     uint32_t it = 0;
     bool ok = true;
     for (int u = blockIdx.x >> 1; ok && u < units; u += gridDim.x >> 1) {
-        const Unit t = unit<kC>(p, s, u);
+        const Unit t = unit(p, s, u);
         const uint8_t* w = weight_block(p, t, rank);
         for (int b = t.b0; b < t.b1; ++b, ++it, w += kTileBytes) {
             const int st = it % kStages;
@@ -115,16 +110,15 @@ __device__ __forceinline__ void weight_producer(const Params& p, Smem<kC>& s, ui
 }
 
 // Warp 3: the token codes and scales of kScChunk blocks at a time, one box each.
-template <int kC>
 __device__ __forceinline__ void token_producer(const Params& p, const CUtensorMap* codes, const CUtensorMap* scales,
-                                               Smem<kC>& s, uint32_t rank, volatile int* abort_flag) {
-    const int units = unit_count<Shape<kC>::kTokens>(p, s.tables);
+                                               Smem& s, uint32_t rank, volatile int* abort_flag) {
+    const int units = unit_count<kTokens>(p, s.tables);
     uint32_t ch = 0;
     bool ok = true;
     dev::pdl_wait();                // the codes and scales come from the kernel before
     dev::pdl_launch_dependents();   // (after the wait: see Fp8GemmArgs::pdl)
     for (int u = blockIdx.x >> 1; ok && u < units; u += gridDim.x >> 1) {
-        const Unit t = unit<kC>(p, s, u);
+        const Unit t = unit(p, s, u);
         const int row = static_cast<int>(t.row0), mine = row + static_cast<int>(rank) * (columns(t) >> 1);
         for (int b = t.b0; b < t.b1; b += kScChunk, ++ch) {
             const int sl = ch % kScSlots;
@@ -146,17 +140,15 @@ __device__ __forceinline__ void token_producer(const Params& p, const CUtensorMa
 }
 
 // ---------------------------------------------------------------- MMA (warp 1)
-template <int kC>
-__device__ __forceinline__ void mma_issuer(const Params& p, Smem<kC>& s, uint32_t rank, uint32_t tmem,
+__device__ __forceinline__ void mma_issuer(const Params& p, Smem& s, uint32_t rank, uint32_t tmem,
                                            volatile int* abort_flag) {
-    constexpr int kAcc = Shape<kC>::kAcc;
-    const int units = unit_count<Shape<kC>::kTokens>(p, s.tables);
+    const int units = unit_count<kTokens>(p, s.tables);
     const uint32_t leader = dev::mapa(&s.ready[0], 0);
     const uint64_t w0 = dev::sdesc_k_sw128(dev::smem_u32(s.w[0])), x0 = dev::sdesc_k_sw128(dev::smem_u32(s.x[0][0]));
     uint32_t it = 0, st = 0, ch = 0;
     bool ok = true;
     for (int u = blockIdx.x >> 1; ok && u < units; u += gridDim.x >> 1) {
-        const Unit t = unit<kC>(p, s, u);
+        const Unit t = unit(p, s, u);
         const uint32_t idesc = dev::idesc_e4m3_f32(256, static_cast<uint32_t>(columns(t)));
         for (int b = t.b0; b < t.b1; ++b, ++it) {
             const int in_chunk = (b - t.b0) % kScChunk, sl = ch % kScSlots;
@@ -173,8 +165,8 @@ __device__ __forceinline__ void mma_issuer(const Params& p, Smem<kC>& s, uint32_
             }
             dev::tc_fence_after();
             // (a descriptor's address field counts 16 bytes)
-            const uint64_t ad = w0 + st * (kTileBytes / 16), bd = x0 + (sl * kScChunk + in_chunk) * (Shape<kC>::kTokens * 4);
-            const uint32_t d = tmem + (it % kAcc) * Shape<kC>::kTokens;
+            const uint64_t ad = w0 + st * (kTileBytes / 16), bd = x0 + (sl * kScChunk + in_chunk) * (kTokens * 4);
+            const uint32_t d = tmem + (it % kAcc) * kTokens;
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) dev::mma_e4m3_pair(d, ad + 2 * k, bd + 2 * k, idesc, k > 0 ? 1u : 0u);
@@ -183,7 +175,7 @@ __device__ __forceinline__ void mma_issuer(const Params& p, Smem<kC>& s, uint32_
                 if (chunk_ends) dev::mma_commit_pair(&s.sc_empty[sl]);
             }
             __syncwarp();
-            if (++st == Shape<kC>::kStages) st = 0;
+            if (++st == kStages) st = 0;
         }
     }
     if (elect_one()) {
@@ -197,15 +189,15 @@ __device__ __forceinline__ void mma_issuer(const Params& p, Smem<kC>& s, uint32_
 }
 
 // ---------------------------------------------------------------- scaler (warp 2)
-template <int kC, bool kGated>
-__device__ __forceinline__ void scaler(const Params& p, Smem<kC>& s, uint32_t rank, int lane,
+template <bool kGated>
+__device__ __forceinline__ void scaler(const Params& p, Smem& s, uint32_t rank, int lane,
                                        volatile int* abort_flag) {
-    constexpr int kPer = Shape<kC>::kTokens / 32;   // tokens a lane: 2 or 4
-    const int units = unit_count<Shape<kC>::kTokens>(p, s.tables);
+    constexpr int kPer = kTokens / 32;   // tokens a lane: 2 or 4
+    const int units = unit_count<kTokens>(p, s.tables);
     uint32_t v = 0, ch = 0;
     bool ok = true;
     for (int u = blockIdx.x >> 1; ok && u < units; u += gridDim.x >> 1) {
-        const Unit t = unit<kC>(p, s, u);
+        const Unit t = unit(p, s, u);
         // weight scales of 32 blocks, one a lane: this CTA's 128 channels, or gate and up
         const int srow = kGated ? t.pair : 2 * t.pair + static_cast<int>(rank);
         const float* ws = p.w_scales + static_cast<int64_t>(t.e) * p.scale_rows * p.nb;
@@ -252,7 +244,6 @@ __device__ __forceinline__ void scaler(const Params& p, Smem<kC>& s, uint32_t ra
 }
 
 // ---------------------------------------------------------------- epilogue (warps 4-11)
-__device__ __forceinline__ void wait_cols(uint32_t (&d)[32]) { dev::tmem_ld_wait32(d); }
 
 // acc[c] += d * (scale product) for 32 tokens.
 __device__ __forceinline__ void accumulate(const uint32_t (&d)[32], const float* prod, float2 (&acc)[16]) {
@@ -264,37 +255,31 @@ __device__ __forceinline__ void accumulate(const uint32_t (&d)[32], const float*
     }
 }
 
-// The blocks of a unit for one epilogue warp whose half tile has kCh chunks of 32 tokens: P of block
-// b from TMEM, times the scale products, into acc. Straight-line inside a block: a TMEM load's 32
-// registers are one fixed run, and a load under a condition makes the compiler move all 32 of them
-// at every join. Returns false when a wait gave up. v counts the blocks of this CTA. kTurns: the warp takes
-// every second block (v % 2 == turn) and arrives for the warp that takes the others.
-template <int kC, int kCh, bool kTurns>
-__device__ __forceinline__ bool sum_blocks(Smem<kC>& s, uint32_t base, const float* prod0, uint32_t leader_ready, int blocks,
-                                           int lane, int turn, uint32_t& v, float2 (&acc)[kC][16], volatile int* abort_flag) {
-    using S = Shape<kC>;
+// The blocks of a unit for one epilogue warp: P of 32 tokens from TMEM, times the scale products, into
+// acc. Straight-line inside a block: a TMEM load's 32 registers are one fixed run, and a load under a
+// condition makes the compiler move all 32 of them at every join. Returns false when a wait gave up. v
+// counts the blocks of this CTA. kTurns: the warp takes every second block (v % 2 == turn) and arrives
+// for the warp that takes the others.
+template <bool kTurns>
+__device__ __forceinline__ bool sum_blocks(Smem& s, uint32_t base, const float* prod0, uint32_t leader_ready, int blocks,
+                                           int lane, int turn, uint32_t& v, float2 (&acc)[16], volatile int* abort_flag) {
     constexpr uint32_t kArrivals = kTurns ? 2 : 1;
     constexpr int kProdFloats = sizeof(s.prod[0]) / sizeof(float);
     for (int left = blocks; left > 0; --left, ++v) {
         if (kTurns && static_cast<int>(v & 1) != turn) continue;
         const uint32_t slot = v % kProd;
-        const bool there = dev::mbar_wait(&s.acc_full[v % S::kAcc], (v / S::kAcc) & 1, abort_flag);
+        const bool there = dev::mbar_wait(&s.acc_full[v % kAcc], (v / kAcc) & 1, abort_flag);
         if (!__all_sync(0xFFFFFFFFu, there)) return false;
         dev::tc_fence_after();
-        const uint32_t at = base + (v % S::kAcc) * S::kTokens;
-        uint32_t d0[32], d1[32];
-        dev::tmem_ld32(at, d0);
-        if constexpr (kCh == 2) dev::tmem_ld32(at + 32u, d1);
+        uint32_t d[32];
+        dev::tmem_ld32(base + (v % kAcc) * kTokens, d);
         if (!__all_sync(0xFFFFFFFFu, dev::mbar_wait(&s.prod_full[slot], (v / kProd) & 1, abort_flag))) return false;
-        const float* prod = prod0 + slot * kProdFloats;
-        wait_cols(d0);
-        if constexpr (kCh == 2) wait_cols(d1);
+        dev::tmem_ld_wait32(d);
         // all of it is in registers: the accumulator is free for block v + kAcc
         dev::tc_fence_before();
         __syncwarp();
-        if (lane == 0) dev::mbar_arrive_remote_n(leader_ready + ((v + S::kAcc) % kRing) * 8u, kArrivals);
-        accumulate(d0, prod, acc[0]);
-        if constexpr (kCh == 2) accumulate(d1, prod + 32, acc[kC - 1]);
+        if (lane == 0) dev::mbar_arrive_remote_n(leader_ready + ((v + kAcc) % kRing) * 8u, kArrivals);
+        accumulate(d, prod0 + slot * kProdFloats, acc);
         __syncwarp();
         if (lane == 0) dev::mbar_arrive_n(&s.prod_empty[slot], kArrivals);
     }
@@ -302,57 +287,47 @@ __device__ __forceinline__ bool sum_blocks(Smem<kC>& s, uint32_t base, const flo
 }
 
 // Warp w covers TMEM lanes 32 (w % 4) .. + 31, one packed weight row a thread, and half of the
-// tile's tokens: acc[c][i] holds tokens c0 + 32c + 2i and + 1.
-template <int kC, bool kGated>
-__device__ __forceinline__ void epilogue(const Params& p, Smem<kC>& s, uint32_t rank, int warp, int lane, uint32_t tmem,
+// tile's tokens (up to 32): acc[i] holds tokens c0 + 2i and + 1.
+template <bool kGated>
+__device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank, int warp, int lane, uint32_t tmem,
                                          volatile int* abort_flag) {
-    using S = Shape<kC>;
-    const int units = unit_count<Shape<kC>::kTokens>(p, s.tables);
+    const int units = unit_count<kTokens>(p, s.tables);
     const int ew = warp - 4, q = warp & 3, h = ew >> 2;
     const uint32_t leader_ready = dev::mapa(&s.ready[0], 0);
     uint32_t v = 0, nu = 0;
     bool ok = true;
     for (int u = blockIdx.x >> 1; u < units; u += gridDim.x >> 1) {
-        const Unit t = unit<kC>(p, s, u);
+        const Unit t = unit(p, s, u);
         // up to 32 tokens: the two warps of a quarter take the blocks in turn, each with all the columns
-        const bool turns = kC == 1 && columns(t) == 32;
+        const bool turns = columns(t) == 32;
         const int half = turns ? 32 : columns(t) >> 1, c0 = turns ? 0 : h * half;
         const int own = turns && h == 1 ? 0 : max(0, min(half, t.n - c0));   // tokens that this warp puts out
-        const int chunks = (half + 31) >> 5;
         const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(c0);
         const float* prod0 = &s.prod[0][kGated ? lane >> 4 : 0][c0];
-        float weight[kC];   // of token c0 + 32c + lane
+        float weight = 1.0f;   // of token c0 + lane
+        if (!kGated && p.pair_weight != nullptr && lane < own) weight = __ldg(p.pair_weight + p.pair_of[t.row0 + c0 + lane]);
+        float2 acc[16];
 #pragma unroll
-        for (int c = 0; c < kC; ++c) {
-            weight[c] = 1.0f;
-            if (!kGated && p.pair_weight != nullptr && 32 * c + lane < own)
-                weight[c] = __ldg(p.pair_weight + p.pair_of[t.row0 + c0 + 32 * c + lane]);
-        }
-        float2 acc[kC][16];
-#pragma unroll
-        for (int c = 0; c < kC; ++c)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[c][i] = make_float2(0.0f, 0.0f);
+        for (int i = 0; i < 16; ++i) acc[i] = make_float2(0.0f, 0.0f);
 
         if (ok) {
             const int blocks = t.b1 - t.b0;
-            if (turns) ok = sum_blocks<kC, 1, true>(s, base, prod0, leader_ready, blocks, lane, h, v, acc, abort_flag);
-            else if (kC == 1 || chunks == 1) ok = sum_blocks<kC, 1, false>(s, base, prod0, leader_ready, blocks, lane, 0, v, acc, abort_flag);
-            else ok = sum_blocks<kC, kC, false>(s, base, prod0, leader_ready, blocks, lane, 0, v, acc, abort_flag);
+            if (turns) ok = sum_blocks<true>(s, base, prod0, leader_ready, blocks, lane, h, v, acc, abort_flag);
+            else ok = sum_blocks<false>(s, base, prod0, leader_ready, blocks, lane, 0, v, acc, abort_flag);
         }
         if (turns) {
             if (h == 1) {
 #pragma unroll
-                for (int i = 0; i < (kC == 1 ? 16 : 1); ++i)
-                    if (2 * i < t.n) s.other_turn[i][32 * q + lane] = acc[0][i];
+                for (int i = 0; i < 16; ++i)
+                    if (2 * i < t.n) s.other_turn[i][32 * q + lane] = acc[i];
             }
             dev::named_bar_sync(4 + q, 64);
             if (h == 0) {
 #pragma unroll
-                for (int i = 0; i < (kC == 1 ? 16 : 1); ++i)
+                for (int i = 0; i < 16; ++i)
                     if (2 * i < t.n) {
                         const float2 f = s.other_turn[i][32 * q + lane];
-                        acc[0][i] = make_float2(acc[0][i].x + f.x, acc[0][i].y + f.y);
+                        acc[i] = make_float2(acc[i].x + f.x, acc[i].y + f.y);
                     }
             }
             dev::named_bar_sync(4 + q, 64);   // read before the next unit's sums come
@@ -361,33 +336,29 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem<kC>& s, uint32_t 
         if constexpr (kGated) {
             // Lanes 0-15 hold the gate rows and lanes 16-31 the up rows of the same hidden channels. A
             // lane of the first half takes the even token of each pair, one of the second half the odd
-            // one: h = silu(gate) * up for 16 tokens of each 32, kept in acc[c][i].x.
+            // one: h = silu(gate) * up for 16 tokens, kept in acc[i].x.
             const int l16 = lane & 15;
             const bool odd = lane >= 16;
             const unsigned mine = odd ? 0xFFFF0000u : 0x0000FFFFu;
             const int par = nu & 1;
+            float top = 0.0f;
 #pragma unroll
-            for (int c = 0; c < kC; ++c) {
-                float top = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    if (32 * c + 2 * i >= own) break;   // (the same for the whole warp)
-                    const float2 f = acc[c][i];
-                    const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? f.x : f.y, 16);
-                    const float g = odd ? got : f.x, up = odd ? f.y : got;
-                    const float hv = silu_times(g, up);
-                    acc[c][i].x = hv;
-                    const float m = __uint_as_float(__reduce_max_sync(mine, __float_as_uint(fabsf(hv))));
-                    if (l16 == i) top = m;
-                }
-                // token of this lane's maximum: 2 l16 (+ 1) of the 32
-                if (32 * c + 2 * l16 < own) s.amax[q][c0 + 32 * c + 2 * l16 + (odd ? 1 : 0)] = top;
+            for (int i = 0; i < 16; ++i) {
+                if (2 * i >= own) break;   // (the same for the whole warp)
+                const float2 f = acc[i];
+                const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? f.x : f.y, 16);
+                const float g = odd ? got : f.x, up = odd ? f.y : got;
+                const float hv = silu_times(g, up);
+                acc[i].x = hv;
+                const float m = __uint_as_float(__reduce_max_sync(mine, __float_as_uint(fabsf(hv))));
+                if (l16 == i) top = m;
             }
+            // this lane's maximum is of token 2 l16 (+ 1)
+            if (2 * l16 < own) s.amax[q][c0 + 2 * l16 + (odd ? 1 : 0)] = top;
             dev::named_bar_sync(2 + h, 128);
-            // the four quarters' maximum of a token to the peer; warp q takes a quarter of the tokens
-            for (int j = lane; j < own; j += 32) {
-                if (((j >> 5) & 3) != q) continue;
-                const int col = c0 + j;
+            // the four quarters' maximum of a token to the peer
+            const int col = c0 + lane;
+            if (q == 0 && lane < own) {
                 const float m = fmaxf(fmaxf(s.amax[0][col], s.amax[1][col]), fmaxf(s.amax[2][col], s.amax[3][col]));
                 s.hscale[col] = m;
                 asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dev::mapa(&s.amax_peer[par][col], rank ^ 1u)), "f"(m) : "memory");
@@ -396,9 +367,7 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem<kC>& s, uint32_t 
             if (lane == 0) dev::mbar_arrive_remote_release(dev::mapa(&s.amax_full[par], rank ^ 1u));
             if (ok) ok = dev::mbar_wait_cluster(&s.amax_full[par], (nu >> 1) & 1);
             ok = __all_sync(0xFFFFFFFFu, ok);
-            for (int j = lane; j < own; j += 32) {
-                if (((j >> 5) & 3) != q) continue;
-                const int col = c0 + j;
+            if (q == 0 && lane < own) {
                 const float sc = __fdiv_rn(fmaxf(s.hscale[col], s.amax_peer[par][col]), 448.0f);
                 s.hscale[col] = sc;
                 if (ok && rank == 0 && col < t.n) p.h_scales[t.pair * p.sstride + t.row0 + col] = sc;
@@ -407,34 +376,28 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem<kC>& s, uint32_t 
             const int chunk16 = static_cast<int>(rank) * 4 + q;
             uint8_t* out = p.H + (static_cast<int64_t>(t.pair) * p.rows + t.row0) * 128 + l16;
 #pragma unroll
-            for (int c = 0; c < kC; ++c)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int col = c0 + 32 * c + 2 * i + (odd ? 1 : 0);
-                    if (32 * c + 2 * i >= own) break;
-                    if (!ok || col >= t.n) continue;
-                    const float sc = s.hscale[col];
-                    const uint32_t code = e4m3x2(sc > 0.0f ? __fdiv_rn(acc[c][i].x, sc) : 0.0f, 0.0f);
-                    out[static_cast<int64_t>(col) * 128 + ((chunk16 ^ static_cast<int>((t.row0 + col) & 7)) << 4)] = static_cast<uint8_t>(code);
-                }
+            for (int i = 0; i < 16; ++i) {
+                if (2 * i >= own) break;
+                const int tok = c0 + 2 * i + (odd ? 1 : 0);
+                if (!ok || tok >= t.n) continue;
+                const float sc = s.hscale[tok];
+                const uint32_t code = e4m3x2(sc > 0.0f ? __fdiv_rn(acc[i].x, sc) : 0.0f, 0.0f);
+                out[static_cast<int64_t>(tok) * 128 + ((chunk16 ^ static_cast<int>((t.row0 + tok) & 7)) << 4)] = static_cast<uint8_t>(code);
+            }
             ++nu;
         } else {
             const int n = 256 * t.pair + 128 * static_cast<int>(rank) + 32 * q + lane;
             auto store = [&]() {
+                uint16_t* y = p.Y + (t.row0 + c0) * p.ldy + n;
 #pragma unroll
-                for (int c = 0; c < kC; ++c) {
-                    if (32 * c >= own) break;
-                    uint16_t* y = p.Y + (t.row0 + c0 + 32 * c) * p.ldy + n;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        if (32 * c + i >= own) break;   // (the same for the whole warp)
-                        const float w = __shfl_sync(0xFFFFFFFFu, weight[c], i);
-                        if (ok && n < p.N) {
-                            const float f = ((i & 1) ? acc[c][i >> 1].y : acc[c][i >> 1].x) * w;
-                            *y = p.bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(f)) : __half_as_ushort(__float2half_rn(f));
-                        }
-                        y += p.ldy;
+                for (int i = 0; i < 32; ++i) {
+                    if (i >= own) break;   // (the same for the whole warp)
+                    const float w = __shfl_sync(0xFFFFFFFFu, weight, i);
+                    if (ok && n < p.N) {
+                        const float f = ((i & 1) ? acc[i >> 1].y : acc[i >> 1].x) * w;
+                        *y = p.bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(f)) : __half_as_ushort(__float2half_rn(f));
                     }
+                    y += p.ldy;
                 }
             };
             if (p.splits == 1) {
@@ -443,15 +406,13 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem<kC>& s, uint32_t 
                 // publish this split's sums; the last split to arrive adds all of them in split order
                 auto slot_of = [&](int sp) {
                     return reinterpret_cast<float4*>(p.partial) +
-                           (((static_cast<int64_t>(t.tile) * p.splits + sp) * 2 + rank) * kEpiWarps + ew) * (kC * 8 * 32) + lane;
+                           (((static_cast<int64_t>(t.tile) * p.splits + sp) * 2 + rank) * kEpiWarps + ew) * (8 * 32) + lane;
                 };
                 float4* out = slot_of(t.split);
 #pragma unroll
-                for (int c = 0; c < kC; ++c)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (32 * c + 4 * i < own)
-                            __stcg(out + (8 * c + i) * 32, make_float4(acc[c][2 * i].x, acc[c][2 * i].y, acc[c][2 * i + 1].x, acc[c][2 * i + 1].y));
+                for (int i = 0; i < 8; ++i)
+                    if (4 * i < own)
+                        __stcg(out + i * 32, make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y));
                 __threadfence();
                 dev::named_bar_sync(1, kEpiWarps * 32);
                 if (ew == 0 && lane == 0) {
@@ -464,27 +425,21 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem<kC>& s, uint32_t 
                 if (s.fixup_last) {
                     __threadfence();
 #pragma unroll
-                    for (int c = 0; c < kC; ++c)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) acc[c][i] = make_float2(0.0f, 0.0f);
+                    for (int i = 0; i < 16; ++i) acc[i] = make_float2(0.0f, 0.0f);
                     for (int sp = 0; sp < p.splits; ++sp) {
                         const float4* in = slot_of(sp);
-                        float4 f[kC][8];
+                        float4 f[8];
 #pragma unroll
-                        for (int c = 0; c < kC; ++c)
+                        for (int i = 0; i < 8; ++i)
+                            if (4 * i < own) f[i] = __ldcg(in + i * 32);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                if (32 * c + 4 * i < own) f[c][i] = __ldcg(in + (8 * c + i) * 32);
-#pragma unroll
-                        for (int c = 0; c < kC; ++c)
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                if (32 * c + 4 * i < own) {
-                                    acc[c][2 * i].x += f[c][i].x;
-                                    acc[c][2 * i].y += f[c][i].y;
-                                    acc[c][2 * i + 1].x += f[c][i].z;
-                                    acc[c][2 * i + 1].y += f[c][i].w;
-                                }
+                        for (int i = 0; i < 8; ++i)
+                            if (4 * i < own) {
+                                acc[2 * i].x += f[i].x;
+                                acc[2 * i].y += f[i].y;
+                                acc[2 * i + 1].x += f[i].z;
+                                acc[2 * i + 1].y += f[i].w;
+                            }
                     }
                     store();
                 }
@@ -497,19 +452,19 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem<kC>& s, uint32_t 
     }
 }
 
-template <int kC, bool kGated>
+template <bool kGated>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 fp8_few_kernel(const Params p, const __grid_constant__ CUtensorMap codes, const __grid_constant__ CUtensorMap scales) {
     extern __shared__ uint8_t smem_raw[];
-    Smem<kC>& s = *reinterpret_cast<Smem<kC>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = dev::cluster_ctarank();
     if (threadIdx.x == 0) {
         dev::tma_prefetch_map(&codes);
         dev::tma_prefetch_map(&scales);
         for (int i = 0; i < kRing; ++i) dev::mbar_init(&s.ready[i], rank == 0 ? 2 + 2 * kEpiWarps : 1);
-        for (int i = 0; i < Shape<kC>::kStages; ++i) dev::mbar_init(&s.empty[i], 1);
-        for (int i = 0; i < kMaxAcc; ++i) dev::mbar_init(&s.acc_full[i], 1);
+        for (int i = 0; i < kStages; ++i) dev::mbar_init(&s.empty[i], 1);
+        for (int i = 0; i < kAcc; ++i) dev::mbar_init(&s.acc_full[i], 1);
         for (int i = 0; i < kScSlots; ++i) {
             dev::mbar_init(&s.sc_full[i], 1);
             dev::mbar_init(&s.sc_empty[i], 2);   // the scaler and the MMAs
@@ -522,12 +477,12 @@ fp8_few_kernel(const Params p, const __grid_constant__ CUtensorMap codes, const 
         dev::mbar_init(&s.mma_done, 1);
         s.abort_flag = 0;
         if (rank == 0)   // the first blocks find their accumulators free
-            for (int i = 0; i < Shape<kC>::kAcc; ++i)
+            for (int i = 0; i < kAcc; ++i)
                 for (int k = 0; k < 2 * kEpiWarps; ++k) dev::mbar_arrive(&s.ready[i]);
         dev::fence_barrier_init();
     }
     if (warp == 2) dev::tmem_alloc_pair(&s.tmem_base, kTmemCols);
-    if (p.start != nullptr) fill_tables<Shape<kC>::kTokens>(p, s.tables, warp, lane);
+    if (p.start != nullptr) fill_tables<kTokens>(p, s.tables, warp, lane);
     dev::tc_fence_before();
     __syncthreads();
     dev::cluster_sync();   // both CTAs' barriers and TMEM exist before any traffic between them
@@ -536,20 +491,18 @@ fp8_few_kernel(const Params p, const __grid_constant__ CUtensorMap codes, const 
     volatile int* abort_flag = &s.abort_flag;
 
     if (warp < 4) {
-        dev::setmaxnreg_dec<72>();
         if (warp == 0) {
-            weight_producer<kC>(p, s, rank, abort_flag);
+            weight_producer(p, s, rank, abort_flag);
         } else if (warp == 1) {
-            mma_issuer<kC>(p, s, rank, tmem, abort_flag);
+            mma_issuer(p, s, rank, tmem, abort_flag);
         } else if (warp == 2) {
-            scaler<kC, kGated>(p, s, rank, lane, abort_flag);
+            scaler<kGated>(p, s, rank, lane, abort_flag);
         } else {
-            token_producer<kC>(p, &codes, &scales, s, rank, abort_flag);
+            token_producer(p, &codes, &scales, s, rank, abort_flag);
         }
         __syncwarp();
     } else {
-        dev::setmaxnreg_inc<216>();   // 128 x 72 + 256 x 216 = the 384 x 168 of the launch
-        epilogue<kC, kGated>(p, s, rank, warp, lane, tmem, abort_flag);
+        epilogue<kGated>(p, s, rank, warp, lane, tmem, abort_flag);
     }
     dev::tc_fence_before();
     __syncthreads();
@@ -560,31 +513,34 @@ fp8_few_kernel(const Params p, const __grid_constant__ CUtensorMap codes, const 
     }
 }
 
-template <int kC>
-constexpr size_t smem_bytes() { return sizeof(Smem<kC>) + 1024; }
-static_assert(smem_bytes<2>() <= 232448, "shared memory exceeds the 227 KB a CTA may use");
+constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory exceeds the 227 KB a CTA may use");
 
-template <int kC, bool kGated>
-cudaError_t launch_as(const Params& p, int grid, const CUtensorMap& codes, const CUtensorMap& scales, bool pdl, cudaStream_t stream) {
-    return launch_pairs(fp8_few_kernel<kC, kGated>, grid, kThreads, smem_bytes<kC>(), pdl, stream, p, codes, scales);
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Which kernel, from the rounds of tiles over the resident pairs of CTAs. A round of 256-token tiles takes 1.8
+// to 1.9 times as long as one of 64-token tiles (a block about 1,080 against 600 clk), so these are taken
+// while they need at most 1.8 times the rounds. Measured, quantizer included: 128 tokens of 8192 x 8192 (one
+// round each) 27.7 against 45.3 us, 256 tokens (two against one) 48.3 against 46.6; 64 experts of 2048 x 1024 with 48
+// tokens each 140 against 161 us, with 64 (some have two small tiles) 181 against 164. 128-token tiles, tried
+// between the two, were slower than the better of them everywhere. Experts: their mean load, and a
+// sixth more for its spread.
+bool few_tokens(const fp8_layer& L, int64_t tokens, bool routed) {
+    int64_t tiles64 = ceil_div(tokens, kTokens), tiles256 = ceil_div(tokens, 256);
+    if (routed) {
+        const int64_t used = tokens < L.experts ? tokens : L.experts, load = ceil_div(tokens * 7, used * 6);
+        tiles64 = used * ceil_div(load, kTokens);
+        tiles256 = used * ceil_div(load, 256);
+    }
+    const int pairs = fp8_resident_pairs(L);
+    return 5 * ceil_div(tiles64 * L.pairs, pairs) <= 9 * ceil_div(tiles256 * L.pairs, pairs);
 }
 
-// Tokens of a tile: 64 or 128 with the weights on the tensor core's M side, 256 with the tokens there:
-// the smallest that holds a dense layer's tokens, or an expert's share of them with room for an
-// uneven load.
-int tile_tokens(int64_t tokens, int experts) {
-    const int64_t share = experts > 1 ? (tokens * 4 / 3 + experts - 1) / experts : tokens;
-    return share <= 64 ? 64 : share <= 128 ? 128 : 256;
-}
-int64_t dense_tiles(const fp8_layer& L, int64_t M) {
-    const int most = tile_tokens(M, 1);
-    return L.pairs * ((M + most - 1) / most);
-}
-
-// Dense tiles too few for the pairs: K is split, at least 4 blocks a split.
+// Dense tiles too few for the pairs: K is split, at least 4 blocks a split and at most 8 splits. Measured at
+// 32 tokens: 1024 x 8192 in 1, 4, 8 and 16 splits 23.5, 16.5, 16.8 and 21.4 us; 8192 x 8192 in 1 and 2 25.3 and 23.5.
 int splits_for(const fp8_layer& L, int64_t M) {
-    if (L.experts > 1 || L.gated) return 1;
-    const int64_t tiles = dense_tiles(L, M);
+    if (L.experts > 1 || L.gated || !few_tokens(L, M, false)) return 1;
+    const int64_t tiles = L.pairs * ceil_div(M, kTokens);
     const int pairs = fp8_resident_pairs(L);
     if (tiles * 2 > pairs) return 1;
     int64_t s = pairs / tiles;
@@ -602,13 +558,12 @@ size_t counter_bytes(const fp8_layer& L) { return (static_cast<size_t>(L.num_sms
 size_t fp8_gemm_workspace(const fp8_layer& L, int64_t M) {
     const int splits = fp8::splits_for(L, M);
     if (splits == 1) return 0;
-    const size_t sums = static_cast<size_t>(fp8::tile_tokens(M, 1)) * 256 * sizeof(float);   // of a tile
-    return fp8::counter_bytes(L) + static_cast<size_t>(fp8::dense_tiles(L, M)) * splits * sums;
+    const size_t tile_bytes = fp8::kTokens * 256 * sizeof(float);
+    return fp8::counter_bytes(L) + static_cast<size_t>(L.pairs) * fp8::ceil_div(M, fp8::kTokens) * splits * tile_bytes;
 }
 
 cudaError_t launch_fp8_gemm(const fp8_layer& L, const Fp8GemmArgs& a, cudaStream_t stream) {
     const bool routed = a.start != nullptr;
-    const int most = fp8::tile_tokens(a.pairs_routed, routed ? L.experts : 1);
     fp8::Params p{};
     p.A = static_cast<const uint8_t*>(a.A);
     p.W = static_cast<const uint8_t*>(a.W);
@@ -638,19 +593,18 @@ cudaError_t launch_fp8_gemm(const fp8_layer& L, const Fp8GemmArgs& a, cudaStream
         p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + fp8::counter_bytes(L));
     }
     // an upper bound of the token tiles: a partial one per expert in use
-    const int64_t experts_used = routed ? (L.experts < a.pairs_routed ? L.experts : a.pairs_routed) : 0;
-    const int64_t tiles = routed ? experts_used + a.pairs_routed / most : (a.rows + most - 1) / most;
-    if (most == 256) return launch_fp8_wide(L, p, a.a_scales, tiles, a.pdl, stream);
+    const bool few = fp8::few_tokens(L, a.pairs_routed, routed);
+    const int most = few ? fp8::kTokens : 256;
+    const int64_t used = routed ? (L.experts < a.pairs_routed ? L.experts : a.pairs_routed) : 0;
+    const int64_t tiles = routed ? used + a.pairs_routed / most : fp8::ceil_div(a.rows, most);
+    if (!few) return launch_fp8_wide(L, p, a.a_scales, tiles, a.pdl, stream);
     CUtensorMap codes, scales;
     if (!encode_code_map(&codes, a.A, a.rows, L.nb, most / 2) || !encode_scale_map(&scales, a.a_scales, p.sstride, L.nb, most, fp8::kScChunk))
         return cudaErrorInvalidValue;
     const int64_t units = tiles * L.pairs * p.splits;
     const int grid = 2 * static_cast<int>(units < fp8_resident_pairs(L) ? units : fp8_resident_pairs(L));
-    if (L.gated)
-        return most == 64 ? fp8::launch_as<1, true>(p, grid, codes, scales, a.pdl, stream)
-                          : fp8::launch_as<2, true>(p, grid, codes, scales, a.pdl, stream);
-    return most == 64 ? fp8::launch_as<1, false>(p, grid, codes, scales, a.pdl, stream)
-                      : fp8::launch_as<2, false>(p, grid, codes, scales, a.pdl, stream);
+    auto fn = L.gated ? fp8::fp8_few_kernel<true> : fp8::fp8_few_kernel<false>;
+    return launch_pairs(fn, grid, fp8::kThreads, fp8::kSmemBytes, a.pdl, stream, p, codes, scales);
 }
 
 }  // namespace fmpq

@@ -86,9 +86,8 @@ __device__ __forceinline__ int unit_count(const Params& p, const Tables& s) {
     return p.pairs * ((p.M + kT - 1) / kT) * p.splits;
 }
 
-// kEven: an expert's (or the layer's) tokens in tiles of about the same size, multiples of 32; else
-// full tiles and a rest.
-template <int kT, bool kEven>
+// An expert's (or the layer's) tokens in full tiles and a rest.
+template <int kT>
 __device__ __forceinline__ Unit unit_of(const Params& p, const Tables& s, int u) {
     Unit r;
     int tokens = p.M, tiles, t;
@@ -123,9 +122,8 @@ __device__ __forceinline__ Unit unit_of(const Params& p, const Tables& s, int u)
         r.b0 = static_cast<int>(static_cast<int64_t>(r.split) * p.nb / p.splits);
         r.b1 = static_cast<int>(static_cast<int64_t>(r.split + 1) * p.nb / p.splits);
     }
-    const int size = kEven ? ((tokens + tiles - 1) / tiles + 31) & ~31 : kT;
-    r.row0 = row + t * size;
-    r.n = min(size, tokens - t * size);
+    r.row0 = row + t * kT;
+    r.n = min(kT, tokens - t * kT);
     return r;
 }
 

@@ -45,11 +45,10 @@ struct __align__(1024) Smem {
     uint64_t mma_done;
     uint32_t tmem_base;
     int abort_flag;
-    int fixup_last;
     Tables tables;
 };
 
-__device__ __forceinline__ Unit unit(const Params& p, const Smem& s, int u) { return unit_of<kT, false>(p, s.tables, u); }
+__device__ __forceinline__ Unit unit(const Params& p, const Smem& s, int u) { return unit_of<kT>(p, s.tables, u); }
 
 __device__ __forceinline__ void producer(const Params& p, const CUtensorMap* scales, Smem& s, uint32_t rank,
                                          volatile int* abort_flag) {
@@ -296,7 +295,7 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
         } else {
             // 32 tokens x 16 columns at a time through shared memory (the 16-byte piece k of token l at
             // k ^ (l / 4 % 2): no bank conflicts either way), so that a store covers whole sectors
-            auto store = [&]() {
+            {
                 uint4* stage = s.out[warp - 4];
                 const int first = static_cast<int>(rank) * 128 + 32 * q;   // token of the warp's lane 0
 #pragma unroll
@@ -329,49 +328,6 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
                         }
                     }
                     __syncwarp();
-                }
-            };
-            if (p.splits == 1) {
-                store();
-            } else {
-                // publish this split's sums; the last split to arrive adds all of them in split order
-                auto slot_of = [&](int sp) {
-                    return reinterpret_cast<float4*>(p.partial) +
-                           (((static_cast<int64_t>(t.tile) * p.splits + sp) * 2 + rank) * kWideEpi + (warp - 4)) * (16 * 32) + lane;
-                };
-                float4* out = slot_of(t.split);
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        __stcg(out + (8 * c + i) * 32, make_float4(acc[c][2 * i].x, acc[c][2 * i].y, acc[c][2 * i + 1].x, acc[c][2 * i + 1].y));
-                __threadfence();
-                dev::named_bar_sync(1, kWideEpi * 32);
-                if (warp == 4 && lane == 0) {
-                    int32_t* cnt = p.arrivals + t.tile * 2 + static_cast<int>(rank);
-                    const int last = atomicAdd(cnt, 1) == p.splits - 1;
-                    if (last) *cnt = 0;   // ready for the next call
-                    s.fixup_last = last;
-                }
-                dev::named_bar_sync(1, kWideEpi * 32);
-                if (s.fixup_last) {
-                    __threadfence();
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                            for (int sp = 0; sp < p.splits; ++sp) {
-                                const float4 f = __ldcg(slot_of(sp) + (8 * c + i) * 32);
-                                sum.x += f.x;
-                                sum.y += f.y;
-                                sum.z += f.z;
-                                sum.w += f.w;
-                            }
-                            acc[c][2 * i] = make_float2(sum.x, sum.y);
-                            acc[c][2 * i + 1] = make_float2(sum.z, sum.w);
-                        }
-                    store();
                 }
             }
         }
@@ -486,7 +442,7 @@ cudaError_t launch_fp8_wide(const fp8_layer& L, const fp8::Params& p, const floa
                             cudaStream_t stream) {
     CUtensorMap map;
     if (!encode_scale_map(&map, a_scales, p.sstride, L.nb, 128, fp8::kChunk)) return cudaErrorInvalidValue;
-    const int64_t units = tiles * L.pairs * p.splits;
+    const int64_t units = tiles * L.pairs;
     const int grid = 2 * static_cast<int>(units < fp8_resident_pairs(L) ? units : fp8_resident_pairs(L));
     auto fn = L.gated ? fp8::fp8_wide_kernel<true> : fp8::fp8_wide_kernel<false>;
     return launch_pairs(fn, grid, fp8::kWideThreads, fp8::kSmemBytes, pdl, stream, p, map);
