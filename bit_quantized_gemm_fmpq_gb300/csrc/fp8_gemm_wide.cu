@@ -4,16 +4,21 @@
 // side, so an epilogue thread owns one token: per block of 128 channels its partial sums P (FP32, in
 // TMEM) take one factor, a_scale[b][m] * w_scale[.][b] (a gated layer: two), and cost nothing but a
 // TMEM read and a packed multiply-add for two of them. With the weights on the M side (fp8_gemm.cu)
-// every pair of sums needs its own factor from shared memory.
+// every pair of sums needs its own factor from shared memory: 1.45 ms at 4096 x 28672 x 8192 against 0.90 here.
 //
 // Per block and CTA: 4 MMAs of 128 clk, 128 KB of TMEM reads, 32 K multiply-adds (256 clk of the FP32
-// pipe), 32 KB of operands from L2 (about 40 bytes a clk and SM with all SMs reading: 820 clk).
+// pipe), 32 KB of operands from L2. Measured there: 0.90 ms with the quantizer (0.86 ms without), 2.24
+// PFLOP/s, 1,070 clk a block, of which the tensor pipe works 512. With parts of the kernel left out (copies kept):
+// without the multiply-adds 0.68 ms, without TMEM reads either 0.65, without copies 0.89, with a quarter of the MMAs 0.92:
+// the per-block work of the epilogue bounds it, not the copies or the tensor pipe, and at this rate the
+// card runs at its power limit (1,370 of 1,400 W, 1.95 of 2.07 GHz). Tried and no faster: single-CTA MMAs with the weights
+// multicast to both CTAs (0.96 ms: 0.93 then), 8 warps of 128 sums (0.97), 16-column loads (the same), the sums kept as
+// packed pairs (1.02).
 //
 // Warp roles (640 threads, one CTA per SM, pairs persistent over tiles):
 //   warp 0      producer: token codes and weight block, token scales (a chunk of blocks at a time)
-//   warp 1      even CTA: MMA issuer; odd CTA: reports its operands to the even one
+//   warps 1, 3  even CTA: MMA issuers of one half of the columns each; odd CTA: warp 1 reports its operands
 //   warp 2      scaler: a chunk's token scales times its weight scales; also allocates and frees TMEM
-//   warp 3      sums up the experts' tiles at the start
 //   warps 4-19  epilogue: TMEM lane quarter warp % 4 (32 tokens), 64 of the 256 columns each
 #include "fp8_gemm.cuh"
 
@@ -23,12 +28,11 @@ namespace {
 
 constexpr int kT = 256;      // tokens of a tile, 128 a CTA
 constexpr int kStages = 6;   // operand blocks in flight
-constexpr int kAcc = 2;      // accumulators of 256 columns
+constexpr int kAcc = 2;      // blocks with accumulators, two halves of 128 columns each
 constexpr int kWideEpi = 16; // epilogue warps
 constexpr int kWideThreads = 640;
 constexpr int kChunk = 2;    // blocks of token scales per copy
 constexpr int kSlots = 2;    // chunks of scales, and of factors
-constexpr int kRing = 8;     // blocks whose readiness may be in flight (> kStages)
 
 struct __align__(1024) Smem {
     uint8_t x[kStages][kTileBytes];   // token codes: this CTA's 128 rows
@@ -37,12 +41,12 @@ struct __align__(1024) Smem {
     float factor[kSlots][kChunk][2][128]; // times the weight scales: of the pair's two tiles, or gate and up
     float amax[2][4][128];            // gated: absmax of each quarter of a token's 128 hidden channels (units in turn)
     uint4 out[kWideEpi][32 * 2];      // a warp's 32 tokens x 16 columns of 16-bit outputs
-    // ready[b % kRing], even CTA: block b's operands have landed in both CTAs and its accumulator has
-    // been read (by both CTAs' epilogue warps). Odd CTA: its operands have landed.
-    uint64_t ready[kRing], empty[kStages];
-    uint64_t acc_full[kAcc];
+    // full: a stage's operands have landed (even CTA: in both CTAs). empty: both halves' MMAs have read it.
+    uint64_t full[kStages], empty[kStages];
+    // [2 (b % kAcc) + half] of block b's accumulator: summed up; read by both CTAs' warps (even CTA)
+    uint64_t acc_full[2 * kAcc], acc_free[2 * kAcc];
     uint64_t sc_full[kSlots], sc_empty[kSlots], factor_full[kSlots], factor_empty[kSlots];
-    uint64_t mma_done;
+    uint64_t mma_done[2];
     uint32_t tmem_base;
     int abort_flag;
     Tables tables;
@@ -75,7 +79,7 @@ __device__ __forceinline__ void producer(const Params& p, const CUtensorMap* sca
             const int st = it % kStages;
             ok = dev::mbar_wait(&s.empty[st], ((it / kStages) & 1) ^ 1, abort_flag);
             if (!ok) break;
-            uint64_t* bar = &s.ready[it % kRing];
+            uint64_t* bar = &s.full[st];
             dev::mbar_arrive_expect_tx(bar, kTileBytes + xbytes);
             dev::bulk_g2s(s.w[st], w, kTileBytes, bar);
             if (xbytes > 0) dev::bulk_g2s(s.x[st], x, xbytes, bar);
@@ -88,7 +92,7 @@ __device__ __forceinline__ void producer(const Params& p, const CUtensorMap* sca
     // even CTA's readiness may never be complete: a short bound, far longer than a copy)
     for (uint32_t k = 0; k < kStages && k < it; ++k) {
         const uint32_t i = it - 1 - k;
-        dev::mbar_wait(&s.ready[i % kRing], (i / kRing) & 1, nullptr, ok ? dev::kMaxPolls : 1u << 16);
+        dev::mbar_wait(&s.full[i % kStages], (i / kStages) & 1, nullptr, ok ? dev::kMaxPolls : 1u << 16);
     }
     for (uint32_t k = 0; k < kSlots && k < ch; ++k) {
         const uint32_t i = ch - 1 - k;
@@ -96,42 +100,50 @@ __device__ __forceinline__ void producer(const Params& p, const CUtensorMap* sca
     }
 }
 
-__device__ __forceinline__ void mma_issuer(const Params& p, Smem& s, uint32_t rank, uint32_t tmem,
+// Even CTA: warps 1 and 3 issue the MMAs of one half of the columns each (weight rows 0-63 and 64-127 of both
+// tiles), as its operands and its accumulator allow. Odd CTA: warp 1 reports its operands.
+__device__ __forceinline__ void mma_issuer(const Params& p, Smem& s, uint32_t rank, int half, uint32_t tmem,
                                            volatile int* abort_flag) {
     const int units = unit_count<kT>(p, s.tables);
-    constexpr uint32_t kIdesc = dev::idesc_e4m3_f32(256, 256);
-    const uint32_t leader = dev::mapa(&s.ready[0], 0);
-    const uint64_t x0 = dev::sdesc_k_sw128(dev::smem_u32(s.x[0])), w0 = dev::sdesc_k_sw128(dev::smem_u32(s.w[0]));
-    uint32_t it = 0, st = 0;
+    constexpr uint32_t kIdesc = dev::idesc_e4m3_f32(256, 128);
+    const uint32_t leader = dev::mapa(&s.full[0], 0);
+    // (a descriptor's address field counts 16 bytes; 64 weight rows are 8 KB)
+    const uint64_t x0 = dev::sdesc_k_sw128(dev::smem_u32(s.x[0])), w0 = dev::sdesc_k_sw128(dev::smem_u32(s.w[0])) + half * 512;
+    uint32_t it = 0, st = 0, phase = 0;
     bool ok = true;
     for (int u = blockIdx.x >> 1; ok && u < units; u += gridDim.x >> 1) {
         const Unit t = unit(p, s, u);
         for (int b = t.b0; b < t.b1; ++b, ++it) {
-            ok = __all_sync(0xFFFFFFFFu, dev::mbar_wait(&s.ready[it % kRing], (it / kRing) & 1, abort_flag));
+            bool there = dev::mbar_wait(&s.full[st], phase, abort_flag);
+            const uint32_t acc = 2 * (it % kAcc) + half;
+            if (rank == 0) there = there && dev::mbar_wait(&s.acc_free[acc], ((it / kAcc) & 1) ^ 1, abort_flag);
+            ok = __all_sync(0xFFFFFFFFu, there);
             if (!ok) break;
             if (rank != 0) {
-                if (elect_one()) dev::mbar_arrive_remote(leader + (it % kRing) * 8u);
-                continue;
-            }
-            dev::tc_fence_after();
-            // (a descriptor's address field counts 16 bytes)
-            const uint64_t ad = x0 + st * (kTileBytes / 16), bd = w0 + st * (kTileBytes / 16);
-            const uint32_t d = tmem + (it % kAcc) * 256u;
-            if (elect_one()) {
+                if (elect_one()) dev::mbar_arrive_remote(leader + st * 8u);
+            } else {
+                dev::tc_fence_after();
+                const uint64_t ad = x0 + st * (kTileBytes / 16), bd = w0 + st * (kTileBytes / 16);
+                const uint32_t d = tmem + acc * 128u;
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) dev::mma_e4m3_pair(d, ad + 2 * k, bd + 2 * k, kIdesc, k > 0 ? 1u : 0u);
-                dev::mma_commit_pair(&s.acc_full[it % kAcc]);
-                dev::mma_commit_pair(&s.empty[st]);
+                    for (int k = 0; k < 4; ++k) dev::mma_e4m3_pair(d, ad + 2 * k, bd + 2 * k, kIdesc, k > 0 ? 1u : 0u);
+                    dev::mma_commit_pair(&s.acc_full[acc]);
+                    dev::mma_commit_pair(&s.empty[st]);
+                }
             }
             __syncwarp();
-            if (++st == kStages) st = 0;
+            if (++st == kStages) {
+                st = 0;
+                phase ^= 1;
+            }
         }
     }
     if (elect_one()) {
         if (!ok) fail(p, abort_flag);
         if (rank == 0) {   // every MMA must finish before TMEM is released
-            dev::mma_commit_pair(&s.mma_done);
-            dev::mbar_wait(&s.mma_done, 0, nullptr);
+            dev::mma_commit_pair(&s.mma_done[half]);
+            dev::mbar_wait(&s.mma_done[half], 0, nullptr);
         }
     }
     __syncwarp();
@@ -190,23 +202,25 @@ __device__ __forceinline__ void accumulate(const uint32_t (&d)[32], float f0, fl
     }
 }
 
-// Thread: token 32 (warp % 4) + lane of this CTA's 128, columns 64 h .. + 63 (packed weight rows of
-// tile 2 pair + h / 2): acc[c][i] holds columns 32c + 2i and + 1. A warp has one TMEM load in flight
-// (a wait covers all of a warp's loads), so four warps a scheduler hide them for each other. The
-// blocks of a unit run straight-line: a TMEM load under a condition makes the compiler move its 32
-// registers at every join. A wait that gives up is remembered, and the unit's outputs are not stored.
+// Thread: token 32 (warp % 4) + lane of this CTA's 128; columns 64 h .. + 63 of the accumulator: packed rows
+// 64 (h / 2) .. + 63 of tile 2 pair + h % 2, acc[c][i] rows 32c + 2i and + 1 of them. The columns' halves have
+// accumulators, barriers and MMAs of their own, so one half's arithmetic runs while the other waits
+// for its MMAs. A warp has one TMEM load in flight (a wait covers all of a warp's loads), so four warps
+// a scheduler hide them for each other. The blocks of a unit run straight-line: a TMEM load under a
+// condition makes the compiler move its 32 registers at every join. A wait that gives up is remembered,
+// and the unit's outputs are not stored.
 template <bool kGated>
 __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank, int warp, int lane, uint32_t tmem,
                                          volatile int* abort_flag) {
     const int units = unit_count<kT>(p, s.tables);
     const int q = warp & 3, h = (warp - 4) >> 2;
     const int local = 32 * q + lane;
+    const int half = h >> 1, sub = h & 1;
     const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16) + 64u * h;
-    const uint32_t leader_ready = dev::mapa(&s.ready[0], 0);
-    const uint32_t acc_full = dev::smem_u32(&s.acc_full[0]), factor_full = dev::smem_u32(&s.factor_full[0]);
-    const float* factors = &s.factor[0][0][kGated ? 0 : h >> 1][local];
+    const uint32_t leader_free = dev::mapa(&s.acc_free[half], 0);
+    const uint32_t acc_full = dev::smem_u32(&s.acc_full[half]), factor_full = dev::smem_u32(&s.factor_full[0]);
+    const float* factors = &s.factor[0][0][kGated ? 0 : sub][local];
     uint32_t slot = 0, phase = 0;     // of the next block's accumulator
-    uint32_t after = kAcc;            // the place in the ring of the block that takes the accumulator next
     uint32_t chunk = 0, chunk_phase = 0;
     uint32_t nu = 0;
     bool ok = true;
@@ -230,7 +244,7 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
             if (j == 0) ok &= wait_at(factor_full + chunk * 8u, chunk_phase, abort_flag);
             const float* f = factors + (chunk * kChunk + j) * 256;
             const float f0 = f[0], f1 = kGated ? f[128] : f0;
-            ok &= wait_at(acc_full + slot * 8u, phase, abort_flag);
+            ok &= wait_at(acc_full + slot * 16u, phase, abort_flag);
             __syncwarp();
             dev::tc_fence_after();
             const uint32_t at = base + slot * 256u;
@@ -243,7 +257,7 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
             // all of it is in registers: the accumulator is free
             dev::tc_fence_before();
             __syncwarp();
-            if (lane == 0) dev::mbar_arrive_remote(leader_ready + after * 8u);
+            if (lane == 0) dev::mbar_arrive_remote(leader_free + slot * 16u);
             if (j == kChunk - 1 || i + 1 == blocks) {
                 if (lane == 0) dev::mbar_arrive(&s.factor_empty[chunk]);
                 chunk ^= 1;
@@ -251,7 +265,6 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
             }
             slot ^= 1;
             phase ^= slot ^ 1;
-            after = (after + 1) % kRing;
             accumulate(d, f0, f1, acc[1]);
         }
         ok = __all_sync(0xFFFFFFFFu, ok);
@@ -288,7 +301,7 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
                             o[i >> 1] |= e4m3x2(__fdiv_rn(g.x, scale), __fdiv_rn(g.y, scale)) << (16 * (i & 1));
                         }
                     }
-                    *reinterpret_cast<uint4*>(out + (((2 * h + c) ^ static_cast<int>(row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4*>(out + (((4 * sub + 2 * half + c) ^ static_cast<int>(row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
                 if (h == 0) p.h_scales[t.pair * p.sstride + row] = scale;
             }
@@ -311,7 +324,7 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
                         stage[lane * 2 + (k ^ ((lane >> 2) & 1))] = make_uint4(o[0], o[1], o[2], o[3]);
                     }
                     __syncwarp();
-                    const int n0 = 256 * t.pair + 64 * h + 16 * c;
+                    const int n0 = 256 * t.pair + 128 * sub + 64 * half + 16 * c;
                     uint16_t* y = p.Y + (t.row0 + first) * p.ldy + n0;
                     if (p.vec && n0 + 16 <= p.N) {
 #pragma unroll
@@ -344,20 +357,22 @@ fp8_wide_kernel(const Params p, const __grid_constant__ CUtensorMap scales) {
     const uint32_t rank = dev::cluster_ctarank();
     if (threadIdx.x == 0) {
         dev::tma_prefetch_map(&scales);
-        for (int i = 0; i < kRing; ++i) dev::mbar_init(&s.ready[i], rank == 0 ? 2 + 2 * kWideEpi : 1);
-        for (int i = 0; i < kStages; ++i) dev::mbar_init(&s.empty[i], 1);
-        for (int i = 0; i < kAcc; ++i) dev::mbar_init(&s.acc_full[i], 1);
+        for (int i = 0; i < kStages; ++i) {
+            dev::mbar_init(&s.full[i], rank == 0 ? 2 : 1);
+            dev::mbar_init(&s.empty[i], 2);
+        }
+        for (int i = 0; i < 2 * kAcc; ++i) {
+            dev::mbar_init(&s.acc_full[i], 1);
+            dev::mbar_init(&s.acc_free[i], kWideEpi);   // half the warps of both CTAs
+        }
         for (int i = 0; i < kSlots; ++i) {
             dev::mbar_init(&s.sc_full[i], 1);
             dev::mbar_init(&s.sc_empty[i], 1);
             dev::mbar_init(&s.factor_full[i], 1);
             dev::mbar_init(&s.factor_empty[i], kWideEpi);
         }
-        dev::mbar_init(&s.mma_done, 1);
+        for (int i = 0; i < 2; ++i) dev::mbar_init(&s.mma_done[i], 1);
         s.abort_flag = 0;
-        if (rank == 0)   // the first blocks find their accumulators free
-            for (int i = 0; i < kAcc; ++i)
-                for (int k = 0; k < 2 * kWideEpi; ++k) dev::mbar_arrive(&s.ready[i]);
         dev::fence_barrier_init();
     }
     if (warp == 2) dev::tmem_alloc_pair(&s.tmem_base, kTmemCols);
@@ -374,9 +389,11 @@ fp8_wide_kernel(const Params p, const __grid_constant__ CUtensorMap scales) {
         if (warp == 0) {
             if (lane == 0) producer(p, &scales, s, rank, abort_flag);
         } else if (warp == 1) {
-            mma_issuer(p, s, rank, tmem, abort_flag);
+            mma_issuer(p, s, rank, 0, tmem, abort_flag);
         } else if (warp == 2) {
             scaler<kGated>(p, s, lane, abort_flag);
+        } else if (rank == 0) {
+            mma_issuer(p, s, rank, 1, tmem, abort_flag);
         }
         __syncwarp();
     } else {
