@@ -648,6 +648,8 @@ class Fp8Layer:
         self.scale_rows = 2 * -(-(N // 2) // BLOCK) if gated else -(-N // BLOCK)
         self._workspaces = {}
         self._workspace_bytes = {}
+        self._w_bytes = int(lib.fp8_packed_w_bytes(h))
+        self._w_scales = int(lib.fp8_weight_scale_count(h))
 
     @property
     def handle(self):
@@ -666,7 +668,15 @@ class Fp8Layer:
             pass
 
     def packed_w_bytes(self) -> int:
-        return int(self._lib.fp8_packed_w_bytes(self._h))
+        return self._w_bytes
+
+    def check_weights(self, W_packed, w_scales):
+        _need(W_packed.numel() == self._w_bytes and w_scales.numel() == self._w_scales and w_scales.is_contiguous(),
+              "W_packed and w_scales must be this layer's (fp8_pack_weights, fp8_pack_codes)")
+
+    def check_activations(self, A_packed, a_scales, rows: int):
+        _need(A_packed.is_contiguous() and a_scales.is_contiguous() and A_packed.numel() >= self.nb * rows * BLOCK and
+              a_scales.numel() >= self.nb * ((rows + 3) // 4 * 4), "A_packed and a_scales are too small for the rows")
 
     def activations(self, rows: int, device):
         """Buffers for `rows` rows of quantized activations: codes uint8 [nb, rows, 128] (swizzled) and
@@ -767,6 +777,9 @@ def fp8_gemm(layer: Fp8Layer, A_packed, a_scales, W_packed, w_scales, M: int, dt
         Y = torch.empty((M, layer.N), dtype=dtype or torch.float16, device=A_packed.device)
     _rows16(Y, "Y")
     _need(Y.shape == (M, layer.N), "Y must be [M, N]")
+    if not layer.gated:  # the library refuses a gated one
+        layer.check_weights(W_packed, w_scales)
+        layer.check_activations(A_packed, a_scales, M)
     workspace, nbytes = _workspace_of(layer, M, workspace)
     _check("fp8_gemm", layer._lib.fp8_gemm(layer.handle, _ptr(A_packed), _ptr(a_scales), _ptr(W_packed), _ptr(w_scales), M,
                                            _ptr(Y), _dtype_code(Y.dtype), _ld(Y), _ptr(workspace), nbytes,
@@ -781,16 +794,17 @@ def fp8_quantize_gemm(layer: Fp8Layer, X, W_packed, w_scales, A_packed=None, a_s
     code = _rows16(X, "X")
     M, K = X.shape
     _need(K == layer.K, "X must be [M, K]")
-    if A_packed is None or a_scales is None:
+    layer.check_weights(W_packed, w_scales)
+    _need((A_packed is None) == (a_scales is None), "pass both A_packed and a_scales, or neither")
+    if A_packed is not None:
+        layer.check_activations(A_packed, a_scales, M)
+        a_ptr, s_ptr = A_packed.data_ptr(), a_scales.data_ptr()
+    else:
         # one scratch buffer: codes, then scales
         codes = layer.nb * M * BLOCK
         scratch = torch.empty(codes + layer.nb * ((M + 3) // 4 * 16), dtype=torch.uint8, device=X.device)
         a_ptr = scratch.data_ptr()
         s_ptr = a_ptr + codes
-    if A_packed is not None:
-        a_ptr = A_packed.data_ptr()
-    if a_scales is not None:
-        s_ptr = a_scales.data_ptr()
     if Y is None:
         Y = torch.empty((M, layer.N), dtype=X.dtype, device=X.device)
     else:
@@ -906,6 +920,8 @@ def moe_up(layer: Fp8Layer, plan: MoePlan, A_packed, a_scales, W_packed, w_scale
     """SwiGLU of the gated layer's products, quantized: codes uint8 [F / 128, rows, 128] and scales."""
     import torch
     _need(layer.gated and plan.experts == layer.experts, "moe_up needs a gated layer and its plan")
+    layer.check_weights(W_packed, w_scales)
+    layer.check_activations(A_packed, a_scales, plan.rows)
     fb = -(-(layer.N // 2) // BLOCK)
     if H_packed is None:
         H_packed = torch.empty((fb, plan.rows, BLOCK), dtype=torch.uint8, device=A_packed.device)
@@ -921,6 +937,8 @@ def moe_down(layer: Fp8Layer, plan: MoePlan, A_packed, a_scales, W_packed, w_sca
     """Every row's product with its expert, times its pair's weight: D [plan.rows, N] (fp16 by default)."""
     import torch
     _need(plan.experts == layer.experts and not layer.gated, "moe_down needs a plain layer and its plan")
+    layer.check_weights(W_packed, w_scales)
+    layer.check_activations(A_packed, a_scales, plan.rows)
     if weights is not None:
         _need(weights.is_cuda and weights.dtype == torch.float32 and weights.shape == (plan.T, plan.k) and
               weights.is_contiguous(), "weights must be contiguous fp32 [T, k]")
@@ -963,6 +981,8 @@ def moe_experts(up: Fp8Layer, down: Fp8Layer, X, ids, weights, W_up, s_up, W_dow
           K == up.K, "ids must be a contiguous int32 CUDA tensor [T, k] for X [T, K]")
     _need(weights.is_cuda and weights.dtype == torch.float32 and weights.shape == ids.shape and weights.is_contiguous(),
           "weights must be contiguous fp32 [T, k]")
+    up.check_weights(W_up, s_up)
+    down.check_weights(W_down, s_down)
     k = ids.shape[1]
     sizes = up._workspace_bytes
     nbytes = sizes.get((T, k, down.N))

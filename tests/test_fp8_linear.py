@@ -280,6 +280,11 @@ def test_binding_refusals(fmpq_mod):
         fmpq_mod.fp8_pack_codes(layer, torch.zeros(128, 256, device="cuda"), s)
     with pytest.raises(fmpq_mod.FmpqError):
         fmpq_mod.fp8_quantize_gemm(layer, X[:0], Wp, s)
+    for kw in (dict(W_packed=Wp[:-16], w_scales=s), dict(W_packed=Wp, w_scales=s[:, :, :1]),
+               dict(W_packed=Wp, w_scales=s, A_packed=torch.empty(4, dtype=torch.uint8, device="cuda"), a_scales=s),
+               dict(W_packed=Wp, w_scales=s, A_packed=torch.empty(4096, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(ValueError):
+            fmpq_mod.fp8_quantize_gemm(layer, X, **kw)
     gated = fmpq_mod.Fp8Layer(256, 256, gated=True)
     with pytest.raises(fmpq_mod.FmpqError):
         fmpq_mod.fp8_gemm(gated, *fmpq_mod.fp8_quantize(gated, X), Wp, s, 4)
