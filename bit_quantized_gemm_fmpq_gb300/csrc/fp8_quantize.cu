@@ -38,7 +38,9 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
 
 // A warp takes 256 channels of a token, 16 lanes a block, 8 channels a lane (one 16-byte load, 8 bytes
 // of codes); blockIdx.y chooses the channels, so that a CTA's stores of a block's codes (128 bytes a
-// row) and scales are contiguous.
+// row) and scales are contiguous. 4096 x 8192 bf16: 33.6 us, 102 MB = 3.0 TB/s, 45% of the copy rate: its instructions
+// bound it (218 a warp for 256 values, most of them the 8 divisions a lane that round to nearest). A product with the
+// reciprocal, checked and divided again where it might round differently, and four rows a warp in flight gave the same.
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ X, int64_t ldx, int64_t M, int K, int nb,
                                                        const int32_t* __restrict__ positions, int slots, int64_t rows,
