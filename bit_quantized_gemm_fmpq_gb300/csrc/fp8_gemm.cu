@@ -115,7 +115,10 @@ __device__ __forceinline__ void token_producer(const Params& p, const CUtensorMa
     const int units = unit_count<kTokens>(p, s.tables);
     uint32_t ch = 0;
     bool ok = true;
-    dev::pdl_wait();                // the codes and scales come from the kernel before
+    // The codes and scales come from the kernel before. The launch for the small rests follows the one for
+    // the tiles, whose CTAs let it start once they had waited for them: it waits at its end, so that its own
+    // dependent finds both launches complete.
+    if (p.part != kSmallRests) dev::pdl_wait();
     dev::pdl_launch_dependents();   // (after the wait: see Fp8GemmArgs::pdl)
     for (int u = blockIdx.x >> 1; ok && u < units; u += gridDim.x >> 1) {
         const Unit t = unit(p, s, u);
@@ -137,6 +140,7 @@ __device__ __forceinline__ void token_producer(const Params& p, const CUtensorMa
         const uint32_t i = ch - 1 - k;
         dev::mbar_wait(&s.sc_full[i % kScSlots], (i / kScSlots) & 1, nullptr);
     }
+    if (p.part == kSmallRests) dev::pdl_wait();
 }
 
 // ---------------------------------------------------------------- MMA (warp 1)
@@ -536,6 +540,14 @@ bool few_tokens(const fp8_layer& L, int64_t tokens, bool routed) {
     return 5 * ceil_div(tiles64 * L.pairs, pairs) <= 9 * ceil_div(tiles256 * L.pairs, pairs);
 }
 
+// Whether an expert's rest of at most 64 rows past its tiles of 256 goes to a second launch, of this file's
+// kernel: there a block takes 0.3 us of a pair of CTAs, not 0.55. The second launch fills the SMs that the first
+// one leaves, but costs 3.5 us, so the products of one tile of every expert must take long enough (16384
+// blocks: 120 us). Measured, both products: 128 experts of 4096 x 1024 with 256 uniform tokens each 765 against 856 us,
+// with 192 594 against 593, with 384 of uneven load 1079 against 1099; below the bound, 16 experts of 4096 x 2048
+// with 128 164 against 157, with 288 252 against 256.
+bool split_rests(const fp8_layer& L, int64_t experts_used) { return experts_used * L.pairs * L.nb >= 16384; }
+
 // Dense tiles too few for the pairs: K is split, at least 4 blocks a split and at most 8 splits. Measured at
 // 32 tokens: 1024 x 8192 in 1, 4, 8 and 16 splits 23.5, 16.5, 16.8 and 21.4 us; 8192 x 8192 in 1 and 2 25.3 and 23.5.
 int splits_for(const fp8_layer& L, int64_t M) {
@@ -597,14 +609,21 @@ cudaError_t launch_fp8_gemm(const fp8_layer& L, const Fp8GemmArgs& a, cudaStream
     const int most = few ? fp8::kTokens : 256;
     const int64_t used = routed ? (L.experts < a.pairs_routed ? L.experts : a.pairs_routed) : 0;
     const int64_t tiles = routed ? used + a.pairs_routed / most : fp8::ceil_div(a.rows, most);
-    if (!few) return launch_fp8_wide(L, p, a.a_scales, tiles, a.pdl, stream);
+    if (!few) {
+        const bool split = fp8::split_rests(L, used);   // (no expert of a dense layer is in use)
+        p.part = split ? fp8::kTiles : fp8::kAllRows;
+        const cudaError_t e = launch_fp8_wide(L, p, a.a_scales, tiles, a.pdl, stream);
+        if (!split || e != cudaSuccess) return e;
+        p.part = fp8::kSmallRests;
+    }
     CUtensorMap codes, scales;
-    if (!encode_code_map(&codes, a.A, a.rows, L.nb, most / 2) || !encode_scale_map(&scales, a.a_scales, p.sstride, L.nb, most, fp8::kScChunk))
+    if (!encode_code_map(&codes, a.A, a.rows, L.nb, fp8::kTokens / 2) ||
+        !encode_scale_map(&scales, a.a_scales, p.sstride, L.nb, fp8::kTokens, fp8::kScChunk))
         return cudaErrorInvalidValue;
-    const int64_t units = tiles * L.pairs * p.splits;
+    const int64_t units = (few ? tiles : used) * L.pairs * p.splits;
     const int grid = 2 * static_cast<int>(units < fp8_resident_pairs(L) ? units : fp8_resident_pairs(L));
     auto fn = L.gated ? fp8::fp8_few_kernel<true> : fp8::fp8_few_kernel<false>;
-    return launch_pairs(fn, grid, fp8::kThreads, fp8::kSmemBytes, a.pdl, stream, p, codes, scales);
+    return launch_pairs(fn, grid, fp8::kThreads, fp8::kSmemBytes, a.pdl || !few, stream, p, codes, scales);
 }
 
 }  // namespace fmpq

@@ -332,6 +332,67 @@ def test_experts_step_by_step(fmpq_mod, T, k, E, H, F, N, skew, dropped, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("turn", [0, 5])
+def test_experts_tiles_and_small_rests(fmpq_mod, turn):
+    """Products long enough that the rests of at most 64 rows past an expert's tiles of 256 go to a second
+    launch: every kind of rest, most experts with one, and (turned) the last experts with none."""
+    import torch
+    E, H, F, N = 512, 1024, 512, 2048
+    shares = [0, 1, 40, 64, 65, 130, 255, 256, 257, 300, 320, 321, 513, 600]
+    share = [shares[(e + turn) % len(shares)] for e in range(E)]
+    g = torch.Generator(device="cuda").manual_seed(turn)
+    ids = torch.repeat_interleave(torch.arange(E), torch.tensor(share))
+    T = ids.numel()
+    ids = ids[torch.randperm(T, generator=torch.Generator().manual_seed(turn))].int().cuda()[:, None]
+    X = torch.randn(T, H, device="cuda", generator=g).half()
+    w = torch.rand(T, 1, device="cuda", generator=g) + 0.1
+
+    def weights(layer, rows, cols):
+        codes = torch.randn(E, rows, cols, device="cuda", generator=g).mul_(100).clamp_(-448, 448).to(torch.float8_e4m3fn)
+        scales = (torch.rand(E, rows // BLOCK, cols // BLOCK, device="cuda", generator=g) + 0.5) / (100 * cols ** 0.5)
+        return codes, scales, fmpq_mod.fp8_pack_codes(layer, codes, scales)
+    Lu, Ld = fmpq_mod.Fp8Layer(H, 2 * F, experts=E, gated=True), fmpq_mod.Fp8Layer(F, N, experts=E)
+    cu, su, Wu = weights(Lu, 2 * F, H)
+    cd, sd, Wd = weights(Ld, N, F)
+    plan = fmpq_mod.moe_plan(ids, E)
+    A, sa = fmpq_mod.moe_quantize(Lu, plan, X)
+    Hq, sh = fmpq_mod.moe_up(Lu, plan, A, sa, *Wu)
+    D = fmpq_mod.moe_down(Ld, plan, Hq, sh, *Wd, weights=w, dtype=torch.float16)
+    Y = fmpq_mod.moe_combine(D, plan)
+    assert fmpq_mod.fp8_device_status(Lu) == 0 and fmpq_mod.fp8_device_status(Ld) == 0
+    again = fmpq_mod.moe_experts(Lu, Ld, X, ids, w, *Wu, *Wd)
+    assert torch.equal(Y, again)
+
+    def decoded(codes, scales, channels):
+        v = decode_activations(codes, plan.rows, channels).cuda()
+        return v, scales.double()[:, :plan.rows].t().repeat_interleave(BLOCK, 1)
+
+    def matrix(codes, scales):
+        return codes.double() * scales.double().repeat_interleave(BLOCK, 0).repeat_interleave(BLOCK, 1)
+    (a, a_scale), (h_codes, h_scale) = decoded(A, sa, H), decoded(Hq, sh, F)
+    row_of = plan.row_of.long()[:, 0]
+    assert torch.equal(Y.cpu(), (D[row_of].float() + 0.0).half().cpu())   # one expert a token
+    slack, eps = (H + 2 * (H // BLOCK) + 8) * 2.0 ** -23, torch.finfo(torch.float16).eps / 2
+    for e in range(E):
+        t = (ids[:, 0] == e).nonzero()[:, 0]
+        assert t.numel() == share[e]
+        r = row_of[t]
+        x = a[r] * a_scale[r]
+        wg, wu = matrix(cu[e], su[e]).split(F)
+        u, gate = x @ wu.t(), x @ wg.t()
+        dg, du = slack * (x.abs() @ wg.abs().t()), slack * (x.abs() @ wu.abs().t())
+        h = gate * torch.sigmoid(gate) * u
+        fp32 = 1.1 * dg * (u.abs() + du) + gate.abs() * du + 2.0 ** -20 * h.abs()
+        hq = h_codes[r] * h_scale[r]
+        bound = h.abs() * 2.0 ** -4 * (1 + 2.0 ** -20) + 2.0 ** -10 * h_scale[r] + 1.1 * fp32 + 1e-300
+        assert bool(((hq - h).abs() <= bound).all()), (e, share[e])
+        x, wd = hq * w[t].double(), matrix(cd[e], sd[e])
+        ref, size = x @ wd.t(), x.abs() @ wd.abs().t()
+        bound = ref.abs() * eps + 2.0 ** -25 + (F + 2 * (F // BLOCK) + 2) * 2.0 ** -23 * size
+        assert bool(((D[r].double() - ref).abs() <= bound).all()), (e, share[e])
+
+
+@pytest.mark.gpu
 def test_experts_in_a_graph_and_on_a_stream(fmpq_mod):
     import torch
     X, up, down, ids, w = experts_case(50, 2, 6, 256, 256, 256, torch.bfloat16, 3)
