@@ -21,8 +21,8 @@
 //   * The weights' stream starts before the codes are there (the kernel is launched as the quantizer's
 //     programmatic dependent); token codes come four blocks a box, one copy per block being what the
 //     copy engine and the issuing warp keep up with.
-// Measured (quantizer included): one token of 8192 x 8192 21.1 us, 67.1 MB = 3.2 TB/s (a stream this short does
-// not reach the copy rate); 64 tokens through 8 of 128 experts of 4096 x 1024, 1.59 GB in 272 us = 5.8 TB/s, 86% of
+// Measured (quantizer included): one token of 8192 x 8192 21.8 us, 67.1 MB = 3.1 TB/s (a stream this short does
+// not reach the copy rate); 64 tokens through 8 of 128 experts of 4096 x 1024, 1.59 GB in 270 us = 5.9 TB/s, 87% of
 // the measured copy rate.
 //
 // Warp roles (384 threads, one CTA per SM, pairs persistent over tiles):
