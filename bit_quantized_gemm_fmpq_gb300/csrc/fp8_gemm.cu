@@ -589,7 +589,8 @@ cudaError_t launch_fp8_gemm(const fp8_layer& L, const Fp8GemmArgs& a, cudaStream
     p.Y = static_cast<uint16_t*>(a.Y);
     p.ldy = a.ldy;
     p.bf16 = a.dtype == kBF16;
-    p.vec = a.ldy % 8 == 0 && (reinterpret_cast<uintptr_t>(a.Y) & 15u) == 0;
+    const uintptr_t y = reinterpret_cast<uintptr_t>(a.Y);
+    p.vec = a.ldy % 8 == 0 && (y & 15u) == 0 ? 8 : a.ldy % 4 == 0 && (y & 7u) == 0 ? 4 : 1;
     p.H = static_cast<uint8_t*>(a.H);
     p.h_scales = a.h_scales;
     p.M = static_cast<int>(a.rows);

@@ -36,7 +36,7 @@ struct Params {
     uint16_t* Y;
     int64_t ldy;
     int bf16;                  // output type
-    int vec;                   // 16-byte output stores allowed
+    int vec;                   // columns a store may write at once: 8, 4 or 1
     uint8_t* H;
     float* h_scales;
     int M, N, nb, pairs, scale_rows, experts, splits;

@@ -40,7 +40,7 @@ struct __align__(1024) Smem {
     float sx[kSlots][kChunk][128];        // token scales
     float factor[kSlots][kChunk][2][128]; // times the weight scales: of the pair's two tiles, or gate and up
     float amax[2][4][128];            // gated: absmax of each quarter of a token's 128 hidden channels (units in turn)
-    uint4 out[kWideEpi][32 * 2];      // a warp's 32 tokens x 16 columns of 16-bit outputs
+    uint4 out[kWideEpi][8 * 8];       // 8 of a warp's tokens x its 64 columns of 16-bit outputs
     // full: a stage's operands have landed (even CTA: in both CTAs). empty: both halves' MMAs have read it.
     uint64_t full[kStages], empty[kStages];
     // [2 (b % kAcc) + half] of block b's accumulator: summed up; read by both CTAs' warps (even CTA)
@@ -202,6 +202,46 @@ __device__ __forceinline__ void accumulate(const uint32_t (&d)[32], float f0, fl
     }
 }
 
+// A warp's 32 tokens x 64 columns to memory, 8 tokens at a time through shared memory (the 16-byte piece k of
+// token l at k ^ l: no bank conflicts either way), so that a store instruction covers whole lines of 128 bytes. kW
+// columns a lane and store. TIMES
+template <int kW>
+__device__ __forceinline__ void store_tile(const Params& p, uint4* stage, int lane, const float2 (&acc)[2][16], float weight,
+                                           uint16_t* y, int tokens, int columns) {
+    struct alignas(2 * kW) Piece {
+        uint16_t v[kW];
+    };
+    uint32_t o[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const float2 f = acc[i >> 4][i & 15];
+        o[i] = pack16(f.x * weight, f.y * weight, p.bf16);
+    }
+#pragma unroll
+    for (int pass = 0; pass < 4; ++pass) {
+        if ((lane >> 3) == pass)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                stage[(lane & 7) * 8 + (k ^ (lane & 7))] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 16 / kW; ++j) {
+            const int l = (32 * j + lane) / (64 / kW), n = (32 * j + lane) % (64 / kW) * kW;
+            const Piece v = *reinterpret_cast<const Piece*>(reinterpret_cast<const uint16_t*>(&stage[l * 8 + ((n >> 3) ^ l)]) + (n & 7));
+            if (8 * pass + l >= tokens) continue;
+            uint16_t* to = y + (8 * pass + l) * p.ldy + n;
+            if (n + kW <= columns) {
+                *reinterpret_cast<Piece*>(to) = v;
+            } else {
+#pragma unroll
+                for (int i = 0; i < kW; ++i)
+                    if (n + i < columns) to[i] = v.v[i];
+            }
+        }
+        __syncwarp();
+    }
+}
+
 // Thread: token 32 (warp % 4) + lane of this CTA's 128; columns 64 h .. + 63 of the accumulator: packed rows
 // 64 (h / 2) .. + 63 of tile 2 pair + h % 2, acc[c][i] rows 32c + 2i and + 1 of them. The columns' halves have
 // accumulators, barriers and MMAs of their own, so one half's arithmetic runs while the other waits
@@ -306,43 +346,13 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
                 if (h == 0) p.h_scales[t.pair * p.sstride + row] = scale;
             }
         } else {
-            // 32 tokens x 16 columns at a time through shared memory (the 16-byte piece k of token l at
-            // k ^ (l / 4 % 2): no bank conflicts either way), so that a store covers whole sectors
-            {
-                uint4* stage = s.out[warp - 4];
-                const int first = static_cast<int>(rank) * 128 + 32 * q;   // token of the warp's lane 0
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        uint32_t o[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 f = acc[c >> 1][8 * (c & 1) + 4 * k + i];
-                            o[i] = pack16(f.x * weight, f.y * weight, p.bf16);
-                        }
-                        stage[lane * 2 + (k ^ ((lane >> 2) & 1))] = make_uint4(o[0], o[1], o[2], o[3]);
-                    }
-                    __syncwarp();
-                    const int n0 = 256 * t.pair + 128 * sub + 64 * half + 16 * c;
-                    uint16_t* y = p.Y + (t.row0 + first) * p.ldy + n0;
-                    if (p.vec && n0 + 16 <= p.N) {
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const int l = 16 * j + (lane >> 1), k = lane & 1;
-                            if (ok && first + l < t.n)
-                                *reinterpret_cast<uint4*>(y + l * p.ldy + 8 * k) = stage[l * 2 + (k ^ ((l >> 2) & 1))];
-                        }
-                    } else {
-                        for (int j = 0; j < 16; ++j) {
-                            const int l = 2 * j + (lane >> 4), n = lane & 15;
-                            const uint16_t val = reinterpret_cast<const uint16_t*>(&stage[l * 2 + ((n >> 3) ^ ((l >> 2) & 1))])[n & 7];
-                            if (ok && first + l < t.n && n0 + n < p.N) y[l * p.ldy + n] = val;
-                        }
-                    }
-                    __syncwarp();
-                }
-            }
+            const int first = static_cast<int>(rank) * 128 + 32 * q;   // token of the warp's lane 0
+            const int n0 = 256 * t.pair + 128 * sub + 64 * half;
+            uint16_t* y = p.Y + (t.row0 + first) * p.ldy + n0;
+            const int tokens = ok ? t.n - first : 0, columns = p.N - n0;
+            if (p.vec == 8) store_tile<8>(p, s.out[warp - 4], lane, acc, weight, y, tokens, columns);
+            else if (p.vec == 4) store_tile<4>(p, s.out[warp - 4], lane, acc, weight, y, tokens, columns);
+            else store_tile<1>(p, s.out[warp - 4], lane, acc, weight, y, tokens, columns);
         }
     }
     if (!ok && lane == 0) fail(p, abort_flag);
