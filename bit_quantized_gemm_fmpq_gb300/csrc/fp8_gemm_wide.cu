@@ -27,11 +27,11 @@ namespace fp8 {
 namespace {
 
 constexpr int kT = 256;      // tokens of a tile, 128 a CTA
-constexpr int kStages = 6;   // operand blocks in flight
+constexpr int kStages = 5;   // operand blocks in flight
 constexpr int kAcc = 2;      // blocks with accumulators, two halves of 128 columns each
 constexpr int kWideEpi = 16; // epilogue warps
 constexpr int kWideThreads = 640;
-constexpr int kChunk = 2;    // blocks of token scales per copy
+constexpr int kChunk = 8;    // blocks of token scales per copy
 constexpr int kSlots = 2;    // chunks of scales, and of factors
 
 struct __align__(1024) Smem {
@@ -39,8 +39,10 @@ struct __align__(1024) Smem {
     uint8_t w[kStages][kTileBytes];   // weight block: this CTA's tile, half of the pair's columns
     float sx[kSlots][kChunk][128];        // token scales
     float factor[kSlots][kChunk][2][128]; // times the weight scales: of the pair's two tiles, or gate and up
-    float amax[2][4][128];            // gated: absmax of each quarter of a token's 128 hidden channels (units in turn)
-    uint4 out[kWideEpi][8 * 8];       // 8 of a warp's tokens x its 64 columns of 16-bit outputs
+    union {
+        float amax[2][4][128];        // gated: absmax of each quarter of a token's 128 hidden channels (units in turn)
+        uint4 out[kWideEpi][16 * 8];  // 16 of a warp's 32 tokens x 64 columns of 16-bit outputs
+    };
     // full: a stage's operands have landed (even CTA: in both CTAs). empty: both halves' MMAs have read it.
     uint64_t full[kStages], empty[kStages];
     // [2 (b % kAcc) + half] of block b's accumulator: summed up; read by both CTAs' warps (even CTA)
@@ -202,9 +204,9 @@ __device__ __forceinline__ void accumulate(const uint32_t (&d)[32], float f0, fl
     }
 }
 
-// A warp's 32 tokens x 64 columns to memory, 8 tokens at a time through shared memory (the 16-byte piece k of
-// token l at k ^ l: no bank conflicts either way), so that a store instruction covers whole lines of 128 bytes. kW
-// columns a lane and store. TIMES
+// A warp's 32 tokens x 64 columns to memory through shared memory (the 16-byte piece k of token l at k ^ (l % 8):
+// no bank conflicts either way), so that a store instruction covers whole lines of 128 bytes; kW columns a
+// lane and store. Pieces of 32 bytes of 16 rows cost 1.8 us a tile of 256 x 256 more.
 template <int kW>
 __device__ __forceinline__ void store_tile(const Params& p, uint4* stage, int lane, const float2 (&acc)[2][16], float weight,
                                            uint16_t* y, int tokens, int columns) {
@@ -212,24 +214,26 @@ __device__ __forceinline__ void store_tile(const Params& p, uint4* stage, int la
         uint16_t v[kW];
     };
     uint32_t o[32];
+    if (p.bf16) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const float2 f = acc[i >> 4][i & 15];
-        o[i] = pack16(f.x * weight, f.y * weight, p.bf16);
+        for (int i = 0; i < 32; ++i) o[i] = pack16(acc[i >> 4][i & 15].x * weight, acc[i >> 4][i & 15].y * weight, true);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = pack16(acc[i >> 4][i & 15].x * weight, acc[i >> 4][i & 15].y * weight, false);
     }
 #pragma unroll
-    for (int pass = 0; pass < 4; ++pass) {
-        if ((lane >> 3) == pass)
+    for (int pass = 0; pass < 2; ++pass) {
+        if ((lane >> 4) == pass)
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                stage[(lane & 7) * 8 + (k ^ (lane & 7))] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                stage[(lane & 15) * 8 + (k ^ (lane & 7))] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 16 / kW; ++j) {
+#pragma unroll 4
+        for (int j = 0; j < 32 / kW; ++j) {
             const int l = (32 * j + lane) / (64 / kW), n = (32 * j + lane) % (64 / kW) * kW;
-            const Piece v = *reinterpret_cast<const Piece*>(reinterpret_cast<const uint16_t*>(&stage[l * 8 + ((n >> 3) ^ l)]) + (n & 7));
-            if (8 * pass + l >= tokens) continue;
-            uint16_t* to = y + (8 * pass + l) * p.ldy + n;
+            const Piece v = *reinterpret_cast<const Piece*>(reinterpret_cast<const uint16_t*>(&stage[l * 8 + ((n >> 3) ^ (l & 7))]) + (n & 7));
+            if (16 * pass + l >= tokens) continue;
+            uint16_t* to = y + (16 * pass + l) * p.ldy + n;
             if (n + kW <= columns) {
                 *reinterpret_cast<Piece*>(to) = v;
             } else {
