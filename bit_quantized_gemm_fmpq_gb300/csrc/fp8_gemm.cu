@@ -522,13 +522,13 @@ static_assert(kSmemBytes <= 232448, "shared memory exceeds the 227 KB a CTA may 
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Which kernel, from the rounds of tiles over the resident pairs of CTAs. A round of 256-token tiles takes 1.8
-// to 1.9 times as long as one of 64-token tiles (a block about 1,080 against 600 clk), so these are taken
-// while they need at most 1.8 times the rounds. Measured, quantizer included: 128 tokens of 8192 x 8192 (one
-// round each) 27.7 against 45.3 us, 256 tokens (two against one) 48.3 against 46.6; 64 experts of 2048 x 1024 with 48
-// tokens each 140 against 161 us, with 64 (some have two small tiles) 181 against 164. 128-token tiles, tried
-// between the two, were slower than the better of them everywhere. Experts: their mean load, and a
-// sixth more for its spread.
+// Which kernel, from the rounds of tiles over the resident pairs of CTAs. A round of 256-token tiles takes 1.3
+// to 1.5 times as long as one of 64-token tiles, so these are taken while they need less than 1.5 times the
+// rounds. Measured, quantizer included: 128 tokens of 8192 x 8192 (one round each) 27.7 against 35.7 us, 256 tokens (two
+// against one) 48.1 against 37.2; 16 experts of 4096 x 2048 with 56 tokens each (4 rounds each) 112 against
+// 134 us, with 96 (7 against 4) 176 against 141; 10 of 2012 x 1404 with 96 (3 against 2) 84 against 60.
+// 128-token tiles, tried between the two, were slower than the better of them everywhere. Experts: their mean load,
+// and a sixth more for its spread.
 bool few_tokens(const fp8_layer& L, int64_t tokens, bool routed) {
     int64_t tiles64 = ceil_div(tokens, kTokens), tiles256 = ceil_div(tokens, 256);
     if (routed) {
@@ -537,15 +537,15 @@ bool few_tokens(const fp8_layer& L, int64_t tokens, bool routed) {
         tiles256 = used * ceil_div(load, 256);
     }
     const int pairs = fp8_resident_pairs(L);
-    return 5 * ceil_div(tiles64 * L.pairs, pairs) <= 9 * ceil_div(tiles256 * L.pairs, pairs);
+    return 2 * ceil_div(tiles64 * L.pairs, pairs) < 3 * ceil_div(tiles256 * L.pairs, pairs);
 }
 
 // Whether an expert's rest of at most 64 rows past its tiles of 256 goes to a second launch, of this file's
-// kernel: there a block takes 0.3 us of a pair of CTAs, not 0.55. The second launch fills the SMs that the first
+// kernel, where a block takes 0.3 us of a pair of CTAs, not 0.43. The second launch fills the SMs that the first
 // one leaves, but costs 3.5 us, so the products of one tile of every expert must take long enough (16384
-// blocks: 120 us). Measured, both products: 128 experts of 4096 x 1024 with 256 uniform tokens each 765 against 856 us,
-// with 192 594 against 593, with 384 of uneven load 1079 against 1099; below the bound, 16 experts of 4096 x 2048
-// with 128 164 against 157, with 288 252 against 256.
+// blocks: 95 us). Measured, both products: 128 experts of 4096 x 1024 with 256 uniform tokens each 722 against 763 us, with
+// 288 895 against 945, with 128 518 against 513, with 64 of uneven load 433 against 468; below the bound, 16 experts
+// of 4096 x 2048 with 128 154 against 146, with 288 244 against 230.
 bool split_rests(const fp8_layer& L, int64_t experts_used) { return experts_used * L.pairs * L.nb >= 16384; }
 
 // Dense tiles too few for the pairs: K is split, at least 4 blocks a split and at most 8 splits. Measured at

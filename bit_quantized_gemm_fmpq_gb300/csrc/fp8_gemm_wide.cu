@@ -4,16 +4,16 @@
 // side, so an epilogue thread owns one token: per block of 128 channels its partial sums P (FP32, in
 // TMEM) take one factor, a_scale[b][m] * w_scale[.][b] (a gated layer: two), and cost nothing but a
 // TMEM read and a packed multiply-add for two of them. With the weights on the M side (fp8_gemm.cu)
-// every pair of sums needs its own factor from shared memory: 1.45 ms at 4096 x 28672 x 8192 against 0.90 here.
+// every pair of sums needs its own factor from shared memory: 1.45 ms at 4096 x 28672 x 8192 against 0.75 here.
 //
 // Per block and CTA: 4 MMAs of 128 clk, 128 KB of TMEM reads, 32 K multiply-adds (256 clk of the FP32
-// pipe), 32 KB of operands from L2. Measured there: 0.90 ms with the quantizer (0.86 ms without), 2.24
-// PFLOP/s, 1,070 clk a block, of which the tensor pipe works 512. With parts of the kernel left out (copies kept):
-// without the multiply-adds 0.68 ms, without TMEM reads either 0.65, without copies 0.89, with a quarter of the MMAs 0.92:
-// the per-block work of the epilogue bounds it, not the copies or the tensor pipe, and at this rate the
-// card runs at its power limit (1,370 of 1,400 W, 1.95 of 2.07 GHz). Tried and no faster: single-CTA MMAs with the weights
-// multicast to both CTAs (0.96 ms: 0.93 then), 8 warps of 128 sums (0.97), 16-column loads (the same), the sums kept as
-// packed pairs (1.02).
+// pipe), 32 KB of operands from L2. Measured there: 0.75 ms with the quantizer (0.72 ms without), 2.57
+// PFLOP/s, 840 clk a block, of which the tensor pipe works 512. With parts of the kernel left out: without the
+// multiply-adds 0.63 ms, without TMEM reads either 0.61, with a quarter of the MMAs 0.73: the per-block work of the
+// epilogue bounds it, not the tensor pipe. Tried and no faster: single-CTA MMAs with the weights multicast to both
+// CTAs, 8 warps of 128 sums, 16-column loads, the sums kept as packed pairs, 2 blocks a loop iteration. Factors by
+// chunks of 8 blocks, not 2 (a wait and an arrival less for each warp and block): 0.83 to 0.75 ms; 5 operand stages cost
+// nothing against 6, 3 cost 2%. A tile's output takes 0.9 us of stores and 1.2 of conversion and staging.
 //
 // Warp roles (640 threads, one CTA per SM, pairs persistent over tiles):
 //   warp 0      producer: token codes and weight block, token scales (a chunk of blocks at a time)
