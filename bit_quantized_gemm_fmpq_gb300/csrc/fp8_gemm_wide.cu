@@ -51,6 +51,7 @@ struct __align__(1024) Smem {
     uint64_t mma_done[2];
     uint32_t tmem_base;
     int abort_flag;
+    int4 unit[2];        // first row, tokens and pair tile of the epilogue's units (in turn), with their first factors
     Tables tables;
 };
 
@@ -114,8 +115,7 @@ __device__ __forceinline__ void mma_issuer(const Params& p, Smem& s, uint32_t ra
     uint32_t it = 0, st = 0, phase = 0;
     bool ok = true;
     for (int u = blockIdx.x >> 1; ok && u < units; u += gridDim.x >> 1) {
-        const Unit t = unit(p, s, u);
-        for (int b = t.b0; b < t.b1; ++b, ++it) {
+        for (int b = 0; b < p.nb; ++b, ++it) {
             bool there = dev::mbar_wait(&s.full[st], phase, abort_flag);
             const uint32_t acc = 2 * (it % kAcc) + half;
             if (rank == 0) there = there && dev::mbar_wait(&s.acc_free[acc], ((it / kAcc) & 1) ^ 1, abort_flag);
@@ -155,9 +155,9 @@ __device__ __forceinline__ void mma_issuer(const Params& p, Smem& s, uint32_t ra
 template <bool kGated>
 __device__ __forceinline__ void scaler(const Params& p, Smem& s, int lane, volatile int* abort_flag) {
     const int units = unit_count<kT>(p, s.tables);
-    uint32_t ch = 0;
+    uint32_t ch = 0, nu = 0;
     bool ok = true;
-    for (int u = blockIdx.x >> 1; ok && u < units; u += gridDim.x >> 1) {
+    for (int u = blockIdx.x >> 1; ok && u < units; u += gridDim.x >> 1, ++nu) {
         const Unit t = unit(p, s, u);
         // weight scales of 32 blocks, one a lane, of the pair's two tiles, or of gate and up
         const int srow = kGated ? t.pair : 2 * t.pair;
@@ -187,6 +187,8 @@ __device__ __forceinline__ void scaler(const Params& p, Smem& s, int lane, volat
             }
             __syncwarp();
             if (lane == 0) {
+                // (the unit two before has been read: its first factors have)
+                if (i == 0) s.unit[nu & 1] = make_int4(static_cast<int>(t.row0), t.n, t.pair, 0);
                 dev::mbar_arrive(&s.factor_full[sl]);
                 dev::mbar_arrive(&s.sc_empty[sl]);
             }
@@ -269,21 +271,22 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
     uint32_t nu = 0;
     bool ok = true;
     for (int u = blockIdx.x >> 1; u < units; u += gridDim.x >> 1) {
-        const Unit t = unit(p, s, u);
+        ok &= wait_at(factor_full + chunk * 8u, chunk_phase, abort_flag);
+        const int4 info = s.unit[nu++ & 1];
+        const int row0 = info.x, n = info.y, pair = info.z;
         const int tok = static_cast<int>(rank) * 128 + local;
-        const int64_t row = t.row0 + tok;
+        const int64_t row = row0 + tok;
         float weight = 1.0f;   // of this thread's token
-        if (!kGated && p.pair_weight != nullptr && tok < t.n) weight = __ldg(p.pair_weight + p.pair_of[row]);
+        if (!kGated && ok && p.pair_weight != nullptr && tok < n) weight = __ldg(p.pair_weight + p.pair_of[row]);
         float2 acc[2][16];
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[c][i] = make_float2(0.0f, 0.0f);
-        const int blocks = t.b1 - t.b0;
         // (little besides the loads and the arithmetic: with the scales and the rings' index arithmetic in
         // it, this loop's own instructions took most of a block's time)
 #pragma unroll 1
-        for (int i = 0; i < blocks; ++i) {
+        for (int i = 0; i < p.nb; ++i) {
             const int j = i % kChunk;
             if (j == 0) ok &= wait_at(factor_full + chunk * 8u, chunk_phase, abort_flag);
             const float* f = factors + (chunk * kChunk + j) * 256;
@@ -302,7 +305,7 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
             dev::tc_fence_before();
             __syncwarp();
             if (lane == 0) dev::mbar_arrive_remote(leader_free + slot * 16u);
-            if (j == kChunk - 1 || i + 1 == blocks) {
+            if (j == kChunk - 1 || i + 1 == p.nb) {
                 if (lane == 0) dev::mbar_arrive(&s.factor_empty[chunk]);
                 chunk ^= 1;
                 chunk_phase ^= chunk ^ 1;
@@ -313,7 +316,7 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
         }
         ok = __all_sync(0xFFFFFFFFu, ok);
 
-        const bool mine = ok && tok < t.n;
+        const bool mine = ok && tok < n;
         if constexpr (kGated) {
             // acc[c][0..7] gates and acc[c][8..15] ups of 16 hidden channels: h = silu(gate) * up, kept
             // in the gates' place
@@ -328,13 +331,13 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
                 }
             // the block's other channels are with the same lane of the other three column warps; a warp
             // two units ahead has seen the others arrive for the unit between, after their reads
-            const int par = nu++ & 1;
+            const int par = nu & 1;
             s.amax[par][h][local] = top;
             dev::named_bar_sync(2 + q, 128);
             const float scale = __fdiv_rn(fmaxf(fmaxf(s.amax[par][0][local], s.amax[par][1][local]),
                                                 fmaxf(s.amax[par][2][local], s.amax[par][3][local])), 448.0f);
             if (mine) {
-                uint8_t* out = p.H + (static_cast<int64_t>(t.pair) * p.rows + row) * 128;
+                uint8_t* out = p.H + (static_cast<int64_t>(pair) * p.rows + row) * 128;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     uint32_t o[4] = {0u, 0u, 0u, 0u};
@@ -347,13 +350,13 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
                     }
                     *reinterpret_cast<uint4*>(out + (((4 * sub + 2 * half + c) ^ static_cast<int>(row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
-                if (h == 0) p.h_scales[t.pair * p.sstride + row] = scale;
+                if (h == 0) p.h_scales[pair * p.sstride + row] = scale;
             }
         } else {
             const int first = static_cast<int>(rank) * 128 + 32 * q;   // token of the warp's lane 0
-            const int n0 = 256 * t.pair + 128 * sub + 64 * half;
-            uint16_t* y = p.Y + (t.row0 + first) * p.ldy + n0;
-            const int tokens = ok ? t.n - first : 0, columns = p.N - n0;
+            const int n0 = 256 * pair + 128 * sub + 64 * half;
+            uint16_t* y = p.Y + (static_cast<int64_t>(row0) + first) * p.ldy + n0;
+            const int tokens = ok ? n - first : 0, columns = p.N - n0;
             if (p.vec == 8) store_tile<8>(p, s.out[warp - 4], lane, acc, weight, y, tokens, columns);
             else if (p.vec == 4) store_tile<4>(p, s.out[warp - 4], lane, acc, weight, y, tokens, columns);
             else store_tile<1>(p, s.out[warp - 4], lane, acc, weight, y, tokens, columns);
