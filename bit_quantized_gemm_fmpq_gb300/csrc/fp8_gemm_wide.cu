@@ -248,6 +248,13 @@ __device__ __forceinline__ void store_tile(const Params& p, uint4* stage, int la
     }
 }
 
+// (behind the waits of this thread: volatile)
+__device__ __forceinline__ float load_shared(uint32_t address) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(address) : "memory");
+    return v;
+}
+
 // Thread: token 32 (warp % 4) + lane of this CTA's 128; columns 64 h .. + 63 of the accumulator: packed rows
 // 64 (h / 2) .. + 63 of tile 2 pair + h % 2, acc[c][i] rows 32c + 2i and + 1 of them. The columns' halves have
 // accumulators, barriers and MMAs of their own, so one half's arithmetic runs while the other waits
@@ -265,7 +272,7 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
     const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16) + 64u * h;
     const uint32_t leader_free = dev::mapa(&s.acc_free[half], 0);
     const uint32_t acc_full = dev::smem_u32(&s.acc_full[half]), factor_full = dev::smem_u32(&s.factor_full[0]);
-    const float* factors = &s.factor[0][0][kGated ? 0 : sub][local];
+    const uint32_t factors = dev::smem_u32(&s.factor[0][0][kGated ? 0 : sub][local]);
     uint32_t slot = 0, phase = 0;     // of the next block's accumulator
     uint32_t chunk = 0, chunk_phase = 0;
     uint32_t nu = 0;
@@ -289,8 +296,8 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
         for (int i = 0; i < p.nb; ++i) {
             const int j = i % kChunk;
             if (j == 0) ok &= wait_at(factor_full + chunk * 8u, chunk_phase, abort_flag);
-            const float* f = factors + (chunk * kChunk + j) * 256;
-            const float f0 = f[0], f1 = kGated ? f[128] : f0;
+            const uint32_t f = factors + (chunk * kChunk + j) * static_cast<uint32_t>(sizeof(s.factor[0][0]));
+            const float f0 = load_shared(f), f1 = kGated ? load_shared(f + sizeof(s.factor[0][0][0])) : f0;
             ok &= wait_at(acc_full + slot * 16u, phase, abort_flag);
             __syncwarp();
             dev::tc_fence_after();
