@@ -36,12 +36,57 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
     return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xFFFFu)));
 }
 
+// The codes of eight values, e4m3(fl32(v / s)). Products with s's reciprocal, made 2^-21 smaller and larger,
+// enclose the quotient (the reciprocal is good to 2^-23, each product rounds by 2^-24): where both round to the same
+// code it is the quotient's, and elsewhere (one value in 2^17) the division decides.
+__device__ __forceinline__ uint2 codes_of(const float (&v)[8], float s) {
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    const float lo = inv * (1.0f - 4.76837158e-7f), hi = inv * (1.0f + 4.76837158e-7f);
+    uint2 code, other;
+    code.x = e4m3x2(v[0] * lo, v[1] * lo) | (e4m3x2(v[2] * lo, v[3] * lo) << 16);
+    code.y = e4m3x2(v[4] * lo, v[5] * lo) | (e4m3x2(v[6] * lo, v[7] * lo) << 16);
+    other.x = e4m3x2(v[0] * hi, v[1] * hi) | (e4m3x2(v[2] * hi, v[3] * hi) << 16);
+    other.y = e4m3x2(v[4] * hi, v[5] * hi) | (e4m3x2(v[6] * hi, v[7] * hi) << 16);
+    if (s >= 1.17549435e-38f && s <= 1e37f && code.x == other.x && code.y == other.y) return code;
+    if (!(s > 0.0f)) return make_uint2(0u, 0u);
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(v[i], s);
+    return make_uint2(e4m3x2(q[0], q[1]) | (e4m3x2(q[2], q[3]) << 16), e4m3x2(q[4], q[5]) | (e4m3x2(q[6], q[7]) << 16));
+}
+
+// The codes of eight values, e4m3(fl32(v / s)). Products with s's reciprocal, made 2^-21 smaller and larger,
+// enclose the quotient (the reciprocal is good to 2^-23, each product rounds by 2^-24): where both round to the same
+// code it is the quotient's, and elsewhere (one value in 2^17) the division decides.
+__device__ __forceinline__ uint2 codes_of(const float (&v)[8], float s) {
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    const float lo = inv * (1.0f - 4.76837158e-7f), hi = inv * (1.0f + 4.76837158e-7f);
+    uint2 code, other;
+    code.x = e4m3x2(v[0] * lo, v[1] * lo) | (e4m3x2(v[2] * lo, v[3] * lo) << 16);
+    code.y = e4m3x2(v[4] * lo, v[5] * lo) | (e4m3x2(v[6] * lo, v[7] * lo) << 16);
+    other.x = e4m3x2(v[0] * hi, v[1] * hi) | (e4m3x2(v[2] * hi, v[3] * hi) << 16);
+    other.y = e4m3x2(v[4] * hi, v[5] * hi) | (e4m3x2(v[6] * hi, v[7] * hi) << 16);
+    if (s >= 1.17549435e-38f && s <= 1e37f && code.x == other.x && code.y == other.y) return code;
+    if (!(s > 0.0f)) return make_uint2(0u, 0u);
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(v[i], s);
+    return make_uint2(e4m3x2(q[0], q[1]) | (e4m3x2(q[2], q[3]) << 16), e4m3x2(q[4], q[5]) | (e4m3x2(q[6], q[7]) << 16));
+}
+
 // A warp takes 256 channels of a token, 16 lanes a block, 8 channels a lane (one 16-byte load, 8 bytes
 // of codes); blockIdx.y chooses the channels, so that a CTA's stores of a block's codes (128 bytes a
 // row) and scales are contiguous. 4096 x 8192 bf16: 33.6 us, 102 MB = 3.0 TB/s, 45% of the copy rate: its instructions
 // bound it (218 a warp for 256 values, most of them the 8 divisions a lane that round to nearest). A product with the
 // reciprocal, checked and divided again where it might round differently, and four rows a warp in flight gave the same.
-template <typename T, bool kVec>
+// A warp takes 256 channels of a token, 16 lanes a block, 8 channels a lane (one 16-byte load, 8 bytes
+// of codes); blockIdx.y chooses the channels, so that a CTA's stores of a block's codes (128 bytes a
+// row) and scales are contiguous. kRows tokens a warp are in flight. 4096 x 8192 bf16: 29.4 us, 102 MB = 3.5 TB/s, 51%
+// of the copy rate: its instructions bound it. With 8 rounded divisions a lane it took 32.6, with one token in
+// flight or with four 31.3.
+template <typename T, bool kVec, int kRows>
 __global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ X, int64_t ldx, int64_t M, int K, int nb,
                                                        const int32_t* __restrict__ positions, int slots, int64_t rows,
                                                        int64_t sstride, uint8_t* __restrict__ A,
@@ -50,43 +95,47 @@ __global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ X, 
     dev::pdl_wait();
     dev::pdl_launch_dependents();
     const int b = static_cast<int>(blockIdx.y) * 2 + half;
-    for (int64_t m = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); m < M; m += static_cast<int64_t>(gridDim.x) * 8) {
-        const int k0 = b * 128 + l * 8;
-        const T* x = X + m * ldx + k0;
-        float v[8];
-        if (kVec && k0 + 8 <= K) {
-            const uint4 w = __ldcs(reinterpret_cast<const uint4*>(x));
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    const int k0 = b * 128 + l * 8;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * 8 * kRows;
+    for (int64_t m0 = (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * kRows; m0 < M; m0 += step) {
+        const T* x = X + m0 * ldx + k0;
+        const bool whole = kVec && k0 + 8 <= K;
+        uint4 raw[kRows];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = unpack2(u[i], x);
-                v[2 * i] = f.x;
-                v[2 * i + 1] = f.y;
+        for (int i = 0; i < kRows; ++i)
+            if (whole && m0 + i < M) raw[i] = __ldcs(reinterpret_cast<const uint4*>(x + i * ldx));
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int64_t m = m0 + i;
+            if (m >= M) break;
+            float v[8];
+            if (whole) {
+                const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float2 f = unpack2(u[c], x);
+                    v[2 * c] = f.x;
+                    v[2 * c + 1] = f.y;
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) v[c] = k0 + c < K ? load_as_float(x + i * ldx + c) : 0.0f;
             }
-        } else {
+            float amax = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = k0 + i < K ? load_as_float(x + i) : 0.0f;
-        }
-        float amax = 0.0f;
+            for (int c = 0; c < 8; ++c) amax = fmaxf(amax, fabsf(v[c]));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
-#pragma unroll
-        for (int d = 8; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-        const float s = __fdiv_rn(amax, kQMax);
-        uint2 code = make_uint2(0u, 0u);
-        if (s > 0.0f) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __fdiv_rn(v[i], s);
-            code.x = e4m3x2(v[0], v[1]) | (e4m3x2(v[2], v[3]) << 16);
-            code.y = e4m3x2(v[4], v[5]) | (e4m3x2(v[6], v[7]) << 16);
-        }
-        if (b >= nb) continue;
-        for (int j = 0; j < slots; ++j) {
-            const int64_t r = positions != nullptr ? positions[m * slots + j] : m;
-            if (r < 0) continue;
-            uint8_t* row = A + (static_cast<int64_t>(b) * rows + r) * 128;
-            *reinterpret_cast<uint2*>(row + (((l >> 1) ^ static_cast<int>(r & 7)) << 4) + (l & 1) * 8) = code;
-            if (l == 0) scales[b * sstride + r] = s;
+            for (int d = 8; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+            const float s = __fdiv_rn(amax, kQMax);
+            const uint2 code = codes_of(v, s);
+            if (b >= nb) continue;
+            for (int j = 0; j < slots; ++j) {
+                const int64_t r = positions != nullptr ? positions[m * slots + j] : m;
+                if (r < 0) continue;
+                uint8_t* row = A + (static_cast<int64_t>(b) * rows + r) * 128;
+                *reinterpret_cast<uint2*>(row + (((l >> 1) ^ static_cast<int>(r & 7)) << 4) + (l & 1) * 8) = code;
+                if (l == 0) scales[b * sstride + r] = s;
+            }
         }
     }
 }
@@ -178,10 +227,12 @@ cudaError_t quantize_as(const void* X, int64_t ldx, int64_t M, int K, const int3
                         void* A, float* scales, int num_sms, bool pdl, cudaStream_t stream) {
     const int nb = (K + 127) / 128;
     const int pairs = (nb + 1) / 2;
-    const int64_t ctas = (M + 7) / 8, most = (num_sms * 64LL + pairs - 1) / pairs;
-    const dim3 grid(static_cast<unsigned>(ctas < most ? ctas : most), static_cast<unsigned>(pairs));
     const bool vec = ldx % 8 == 0 && (reinterpret_cast<uintptr_t>(X) & 15u) == 0;
-    auto fn = vec ? quantize_kernel<T, true> : quantize_kernel<T, false>;
+    // two tokens a warp once every warp has several: 2048 x 4096 9.1 against 9.7 us, 1024 x 4096 6.0 either way
+    const bool deep = vec && M * pairs >= num_sms * 128LL;
+    const int64_t per = deep ? 8 * 2 : 8, ctas = (M + per - 1) / per, most = (num_sms * 64LL + pairs - 1) / pairs;
+    const dim3 grid(static_cast<unsigned>(ctas < most ? ctas : most), static_cast<unsigned>(pairs));
+    auto fn = !vec ? quantize_kernel<T, false, 1> : deep ? quantize_kernel<T, true, 2> : quantize_kernel<T, true, 1>;
     return launch_after(fn, grid, 256, 0, pdl, stream, static_cast<const T*>(X), ldx, M, K, nb,
                         positions, positions != nullptr ? slots : 1, rows, scale_stride(rows), static_cast<uint8_t*>(A), scales);
 }
