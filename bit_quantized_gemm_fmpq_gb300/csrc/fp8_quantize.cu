@@ -56,31 +56,6 @@ __device__ __forceinline__ uint2 codes_of(const float (&v)[8], float s) {
     return make_uint2(e4m3x2(q[0], q[1]) | (e4m3x2(q[2], q[3]) << 16), e4m3x2(q[4], q[5]) | (e4m3x2(q[6], q[7]) << 16));
 }
 
-// The codes of eight values, e4m3(fl32(v / s)). Products with s's reciprocal, made 2^-21 smaller and larger,
-// enclose the quotient (the reciprocal is good to 2^-23, each product rounds by 2^-24): where both round to the same
-// code it is the quotient's, and elsewhere (one value in 2^17) the division decides.
-__device__ __forceinline__ uint2 codes_of(const float (&v)[8], float s) {
-    float inv;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
-    const float lo = inv * (1.0f - 4.76837158e-7f), hi = inv * (1.0f + 4.76837158e-7f);
-    uint2 code, other;
-    code.x = e4m3x2(v[0] * lo, v[1] * lo) | (e4m3x2(v[2] * lo, v[3] * lo) << 16);
-    code.y = e4m3x2(v[4] * lo, v[5] * lo) | (e4m3x2(v[6] * lo, v[7] * lo) << 16);
-    other.x = e4m3x2(v[0] * hi, v[1] * hi) | (e4m3x2(v[2] * hi, v[3] * hi) << 16);
-    other.y = e4m3x2(v[4] * hi, v[5] * hi) | (e4m3x2(v[6] * hi, v[7] * hi) << 16);
-    if (s >= 1.17549435e-38f && s <= 1e37f && code.x == other.x && code.y == other.y) return code;
-    if (!(s > 0.0f)) return make_uint2(0u, 0u);
-    float q[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(v[i], s);
-    return make_uint2(e4m3x2(q[0], q[1]) | (e4m3x2(q[2], q[3]) << 16), e4m3x2(q[4], q[5]) | (e4m3x2(q[6], q[7]) << 16));
-}
-
-// A warp takes 256 channels of a token, 16 lanes a block, 8 channels a lane (one 16-byte load, 8 bytes
-// of codes); blockIdx.y chooses the channels, so that a CTA's stores of a block's codes (128 bytes a
-// row) and scales are contiguous. 4096 x 8192 bf16: 33.6 us, 102 MB = 3.0 TB/s, 45% of the copy rate: its instructions
-// bound it (218 a warp for 256 values, most of them the 8 divisions a lane that round to nearest). A product with the
-// reciprocal, checked and divided again where it might round differently, and four rows a warp in flight gave the same.
 // A warp takes 256 channels of a token, 16 lanes a block, 8 channels a lane (one 16-byte load, 8 bytes
 // of codes); blockIdx.y chooses the channels, so that a CTA's stores of a block's codes (128 bytes a
 // row) and scales are contiguous. kRows tokens a warp are in flight. 4096 x 8192 bf16: 29.4 us, 102 MB = 3.5 TB/s, 51%
