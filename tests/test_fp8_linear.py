@@ -162,6 +162,30 @@ def test_quantize_exact(fmpq_mod, M, K, pad, offset, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("M,K", [(9, 128), (640, 8192)])
+def test_quantize_values_between_two_codes(fmpq_mod, M, K, dtype):
+    """Every block holds its absmax and the 126 midpoints of neighbouring codes times its scale, rounded to the
+    type, and the values next to them."""
+    import torch
+    dtype = getattr(torch, dtype)
+    g = torch.Generator().manual_seed(M)
+    codes = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).float()
+    middles = (codes[1:] + codes[:-1]) / 2
+    amax = torch.exp(torch.empty(M, K // BLOCK, 1).uniform_(-6, 6, generator=g)).to(dtype)
+    x = ((amax.float() / 448) * middles).to(dtype)
+    bits = x.view(torch.int16)       # (a zero has no neighbour below)
+    x = (bits + torch.randint(-1, 2, x.shape, generator=g, dtype=torch.int16)).clamp(min=0).view(dtype)
+    x = x * (torch.randint(0, 2, x.shape, generator=g) * 2 - 1).to(dtype)
+    x = torch.minimum(torch.maximum(x, -amax), amax)
+    X = torch.cat([amax, torch.zeros_like(amax), x], 2).reshape(M, K)
+    A, s = fmpq_mod.fp8_quantize(fmpq_mod.Fp8Layer(K, 128), X.cuda())
+    q, sr = quantized(X)
+    assert torch.equal(s.cpu()[:, :M].t(), sr)
+    assert torch.equal(decode_activations(A, M, K), q)
+
+
+@pytest.mark.gpu
 def test_quantize_tiny_and_large_values(fmpq_mod):
     import torch
     X = torch.zeros(8, 256, dtype=torch.bfloat16, device="cuda")
