@@ -460,7 +460,8 @@ template <bool kGated>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 fp8_few_kernel(const Params p, const __grid_constant__ CUtensorMap codes, const __grid_constant__ CUtensorMap scales) {
     extern __shared__ uint8_t smem_raw[];
-    Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // (an offset from the array, so that the compiler still knows the accesses to be shared memory's)
+    Smem& s = *reinterpret_cast<Smem*>(smem_raw + ((1024u - (dev::smem_u32(smem_raw) & 1023u)) & 1023u));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = dev::cluster_ctarank();
     if (threadIdx.x == 0) {
