@@ -115,10 +115,7 @@ __device__ __forceinline__ void token_producer(const Params& p, const CUtensorMa
     const int units = unit_count<kTokens>(p, s.tables);
     uint32_t ch = 0;
     bool ok = true;
-    // The codes and scales come from the kernel before. The launch for the small rests follows the one for
-    // the tiles, whose CTAs let it start once they had waited for them: it waits at its end, so that its own
-    // dependent finds both launches complete.
-    if (p.part != kSmallRests) dev::pdl_wait();
+    dev::pdl_wait();                // the codes and scales come from the kernel before
     dev::pdl_launch_dependents();   // (after the wait: see Fp8GemmArgs::pdl)
     for (int u = blockIdx.x >> 1; ok && u < units; u += gridDim.x >> 1) {
         const Unit t = unit(p, s, u);
@@ -140,7 +137,6 @@ __device__ __forceinline__ void token_producer(const Params& p, const CUtensorMa
         const uint32_t i = ch - 1 - k;
         dev::mbar_wait(&s.sc_full[i % kScSlots], (i / kScSlots) & 1, nullptr);
     }
-    if (p.part == kSmallRests) dev::pdl_wait();
 }
 
 // ---------------------------------------------------------------- MMA (warp 1)
@@ -523,13 +519,14 @@ static_assert(kSmemBytes <= 232448, "shared memory exceeds the 227 KB a CTA may 
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Which kernel, from the rounds of tiles over the resident pairs of CTAs. A round of 256-token tiles takes 1.3
-// to 1.5 times as long as one of 64-token tiles, so these are taken while they need less than 1.5 times the
-// rounds. Measured, quantizer included: 128 tokens of 8192 x 8192 (one round each) 27.7 against 35.7 us, 256 tokens (two
-// against one) 48.1 against 37.2; 16 experts of 4096 x 2048 with 56 tokens each (4 rounds each) 112 against
-// 134 us, with 96 (7 against 4) 176 against 141; 10 of 2012 x 1404 with 96 (3 against 2) 84 against 60.
-// 128-token tiles, tried between the two, were slower than the better of them everywhere. Experts: their mean load,
-// and a sixth more for its spread.
+// Which kernel, from the rounds of tiles over the resident pairs of CTAs. A round of 256-token tiles takes 1.2
+// to 1.4 times as long as one of 64-token tiles, so these are taken while they need less than 1.5 times the
+// rounds. Measured, quantizer included: 128 tokens of 8192 x 8192 (one round each) 27.2 against 32.3 us, 256 tokens (two
+// against one) 46.3 against 33.2; 16 experts of 4096 x 2048 with 48 tokens each (4 rounds each) 109 against
+// 115 us, with 96 (7 against 4) 168 against 123; 10 of 2012 x 1404 with 96 (3 against 2) 82 against 54.
+// 128-token tiles, tried between the two, were slower than the better of them everywhere, and the last few tokens of an
+// expert in a second launch of small tiles gained or lost 2%. Experts: their mean load, and a sixth more for its
+// spread.
 bool few_tokens(const fp8_layer& L, int64_t tokens, bool routed) {
     int64_t tiles64 = ceil_div(tokens, kTokens), tiles256 = ceil_div(tokens, 256);
     if (routed) {
@@ -540,14 +537,6 @@ bool few_tokens(const fp8_layer& L, int64_t tokens, bool routed) {
     const int pairs = fp8_resident_pairs(L);
     return 2 * ceil_div(tiles64 * L.pairs, pairs) < 3 * ceil_div(tiles256 * L.pairs, pairs);
 }
-
-// Whether an expert's rest of at most 64 rows past its tiles of 256 goes to a second launch, of this file's
-// kernel, where a block takes 0.3 us of a pair of CTAs, not 0.43. The second launch fills the SMs that the first
-// one leaves, but costs 3.5 us, so the products of one tile of every expert must take long enough (16384
-// blocks: 95 us). Measured, both products: 128 experts of 4096 x 1024 with 256 uniform tokens each 722 against 763 us, with
-// 288 895 against 945, with 128 518 against 513, with 64 of uneven load 433 against 468; below the bound, 16 experts
-// of 4096 x 2048 with 128 154 against 146, with 288 244 against 230.
-bool split_rests(const fp8_layer& L, int64_t experts_used) { return experts_used * L.pairs * L.nb >= 16384; }
 
 // Dense tiles too few for the pairs: K is split, at least 4 blocks a split and at most 8 splits. Measured at
 // 32 tokens: 1024 x 8192 in 1, 4, 8 and 16 splits 23.5, 16.5, 16.8 and 21.4 us; 8192 x 8192 in 1 and 2 25.3 and 23.5.
@@ -611,21 +600,15 @@ cudaError_t launch_fp8_gemm(const fp8_layer& L, const Fp8GemmArgs& a, cudaStream
     const int most = few ? fp8::kTokens : 256;
     const int64_t used = routed ? (L.experts < a.pairs_routed ? L.experts : a.pairs_routed) : 0;
     const int64_t tiles = routed ? used + a.pairs_routed / most : fp8::ceil_div(a.rows, most);
-    if (!few) {
-        const bool split = fp8::split_rests(L, used);   // (no expert of a dense layer is in use)
-        p.part = split ? fp8::kTiles : fp8::kAllRows;
-        const cudaError_t e = launch_fp8_wide(L, p, a.a_scales, tiles, a.pdl, stream);
-        if (!split || e != cudaSuccess) return e;
-        p.part = fp8::kSmallRests;
-    }
+    if (!few) return launch_fp8_wide(L, p, a.a_scales, tiles, a.pdl, stream);
     CUtensorMap codes, scales;
     if (!encode_code_map(&codes, a.A, a.rows, L.nb, fp8::kTokens / 2) ||
         !encode_scale_map(&scales, a.a_scales, p.sstride, L.nb, fp8::kTokens, fp8::kScChunk))
         return cudaErrorInvalidValue;
-    const int64_t units = (few ? tiles : used) * L.pairs * p.splits;
+    const int64_t units = tiles * L.pairs * p.splits;
     const int grid = 2 * static_cast<int>(units < fp8_resident_pairs(L) ? units : fp8_resident_pairs(L));
     auto fn = L.gated ? fp8::fp8_few_kernel<true> : fp8::fp8_few_kernel<false>;
-    return launch_pairs(fn, grid, fp8::kThreads, fp8::kSmemBytes, a.pdl || !few, stream, p, codes, scales);
+    return launch_pairs(fn, grid, fp8::kThreads, fp8::kSmemBytes, a.pdl, stream, p, codes, scales);
 }
 
 }  // namespace fmpq

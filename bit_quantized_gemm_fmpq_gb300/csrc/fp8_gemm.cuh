@@ -19,11 +19,6 @@ constexpr int kThreads = 384;   // 4 warps of other roles, 8 of the epilogue
 constexpr int kGroupM = 8;      // dense order: bands of 8 token tiles, weight tiles inside a band
 constexpr uint32_t kTmemCols = 512;
 
-// Which of an expert's rows a launch takes: all, or in two launches the tiles of 256 rows (with the rest, if
-// it is larger than kSmallRest), and the small rests.
-enum { kAllRows = 0, kTiles = 1, kSmallRests = 2 };
-constexpr int kSmallRest = 64;
-
 struct Params {
     const uint8_t* A;
     const uint8_t* W;
@@ -40,7 +35,6 @@ struct Params {
     uint8_t* H;
     float* h_scales;
     int M, N, nb, pairs, scale_rows, experts, splits;
-    int part;                  // kAllRows, kTiles or kSmallRests
     float* partial;            // split-K: [tile][split][CTA][warp][vector][lane] FP32 sums
     int32_t* arrivals;         // [tile][CTA]
     int32_t* status;
@@ -63,15 +57,8 @@ struct Unit {
 template <int kT>
 __device__ __forceinline__ void fill_tables(const Params& p, Tables& s, int warp, int lane) {
     for (int e = threadIdx.x; e < p.experts; e += blockDim.x) {
-        int start = p.start[e], count = p.count[e];
-        const int rest = count % 256;
-        if (p.part == kTiles && rest <= kSmallRest) count -= rest;
-        if (p.part == kSmallRests) {
-            start += count - rest;
-            count = rest <= kSmallRest ? rest : 0;
-        }
-        s.start[e] = start;
-        s.count[e] = count;
+        s.start[e] = p.start[e];
+        s.count[e] = p.count[e];
     }
     __syncthreads();
     if (warp != 3) return;

@@ -4,16 +4,15 @@
 // side, so an epilogue thread owns one token: per block of 128 channels its partial sums P (FP32, in
 // TMEM) take one factor, a_scale[b][m] * w_scale[.][b] (a gated layer: two), and cost nothing but a
 // TMEM read and a packed multiply-add for two of them. With the weights on the M side (fp8_gemm.cu)
-// every pair of sums needs its own factor from shared memory: 1.45 ms at 4096 x 28672 x 8192 against 0.75 here.
+// every pair of sums needs its own factor from shared memory, and costs twice as much.
 //
 // Per block and CTA: 4 MMAs of 128 clk, 128 KB of TMEM reads, 32 K multiply-adds (256 clk of the FP32
-// pipe), 32 KB of operands from L2. Measured there: 0.75 ms with the quantizer (0.72 ms without), 2.57
-// PFLOP/s, 840 clk a block, of which the tensor pipe works 512. With parts of the kernel left out: without the
-// multiply-adds 0.63 ms, without TMEM reads either 0.61, with a quarter of the MMAs 0.73: the per-block work of the
-// epilogue bounds it, not the tensor pipe. Tried and no faster: single-CTA MMAs with the weights multicast to both
-// CTAs, 8 warps of 128 sums, 16-column loads, the sums kept as packed pairs, 2 blocks a loop iteration. Factors by
-// chunks of 8 blocks, not 2 (a wait and an arrival less for each warp and block): 0.83 to 0.75 ms; 5 operand stages cost
-// nothing against 6, 3 cost 2%. A tile's output takes 0.9 us of stores and 1.2 of conversion and staging.
+// pipe), 32 KB of operands from L2. Measured at 4096 x 28672 x 8192: 0.68 ms with the quantizer, 2.8 PFLOP/s, 750 clk a
+// block, of which the tensor pipe works 512; back to back the card reaches its power limit. The per-block work
+// of the epilogue bounds it, not the tensor pipe or the copies. Tried and no faster: single-CTA MMAs with the weights
+// multicast to both CTAs, 8 warps of 128 sums, 16-column loads, the sums kept as packed pairs, 2 blocks a loop iteration
+// (it spills), waits with a time hint. Factors by chunks of 8 blocks, not 2: 0.83 to 0.75 ms; shared memory reached
+// without generic addresses: 0.73 to 0.68; 5 operand stages cost nothing against 6, 3 cost 2%.
 //
 // Warp roles (640 threads, one CTA per SM, pairs persistent over tiles):
 //   warp 0      producer: token codes and weight block, token scales (a chunk of blocks at a time)

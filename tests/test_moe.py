@@ -334,8 +334,7 @@ def test_experts_step_by_step(fmpq_mod, T, k, E, H, F, N, skew, dropped, dtype):
 @pytest.mark.gpu
 @pytest.mark.parametrize("turn", [0, 5])
 def test_experts_tiles_and_small_rests(fmpq_mod, turn):
-    """Products long enough that the rests of at most 64 rows past an expert's tiles of 256 go to a second
-    launch: every kind of rest, most experts with one, and (turned) the last experts with none."""
+    """Tiles of 256 rows and every kind of rest, for many experts, the last of them with and without any."""
     import torch
     E, H, F, N = 512, 1024, 512, 2048
     shares = [0, 1, 40, 64, 65, 130, 255, 256, 257, 300, 320, 321, 513, 600]
