@@ -388,16 +388,17 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
         } else {
             const int n = 256 * t.pair + 128 * static_cast<int>(rank) + 32 * q + lane;
             auto store = [&]() {
-                uint16_t* y = p.Y + (t.row0 + c0) * p.ldy + n;
+                int64_t at = (t.row0 + c0) * p.ldy + n;
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     if (i >= own) break;   // (the same for the whole warp)
                     const float w = __shfl_sync(0xFFFFFFFFu, weight, i);
                     if (ok && n < p.N) {
                         const float f = ((i & 1) ? acc[i >> 1].y : acc[i >> 1].x) * w;
-                        *y = p.bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(f)) : __half_as_ushort(__float2half_rn(f));
+                        if (p.f32) static_cast<float*>(p.Y)[at] = f;
+                        else static_cast<uint16_t*>(p.Y)[at] = p.bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(f)) : __half_as_ushort(__float2half_rn(f));
                     }
-                    y += p.ldy;
+                    at += p.ldy;
                 }
             };
             if (p.splits == 1) {
@@ -576,11 +577,13 @@ cudaError_t launch_fp8_gemm(const fp8_layer& L, const Fp8GemmArgs& a, cudaStream
     p.pair_weight = a.pair_weight;
     p.rows = a.rows;
     p.sstride = scale_stride(a.rows);
-    p.Y = static_cast<uint16_t*>(a.Y);
+    p.Y = a.Y;
     p.ldy = a.ldy;
     p.bf16 = a.dtype == kBF16;
+    p.f32 = a.dtype == kF32;
     const uintptr_t y = reinterpret_cast<uintptr_t>(a.Y);
-    p.vec = a.ldy % 8 == 0 && (y & 15u) == 0 ? 8 : a.ldy % 4 == 0 && (y & 7u) == 0 ? 4 : 1;
+    if (p.f32) p.vec = a.ldy % 4 == 0 && (y & 15u) == 0 ? 4 : 1;
+    else p.vec = a.ldy % 8 == 0 && (y & 15u) == 0 ? 8 : a.ldy % 4 == 0 && (y & 7u) == 0 ? 4 : 1;
     p.H = static_cast<uint8_t*>(a.H);
     p.h_scales = a.h_scales;
     p.M = static_cast<int>(a.rows);

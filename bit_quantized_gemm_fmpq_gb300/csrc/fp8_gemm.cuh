@@ -28,10 +28,10 @@ struct Params {
     const int32_t* pair_of;
     const float* pair_weight;
     int64_t rows, sstride;
-    uint16_t* Y;
+    void* Y;
     int64_t ldy;
-    int bf16;                  // output type
-    int vec;                   // columns a store may write at once: 8, 4 or 1
+    int bf16, f32;             // output type (neither: fp16)
+    int vec;                   // columns a store may write at once: 8 (16 bits), 4 or 1
     uint8_t* H;
     float* h_scales;
     int M, N, nb, pairs, scale_rows, experts, splits;

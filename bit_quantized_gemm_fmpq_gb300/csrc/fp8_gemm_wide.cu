@@ -40,7 +40,7 @@ struct __align__(1024) Smem {
     float factor[kSlots][kChunk][2][128]; // times the weight scales: of the pair's two tiles, or gate and up
     union {
         float amax[2][4][128];        // gated: absmax of each quarter of a token's 128 hidden channels (units in turn)
-        uint4 out[kWideEpi][16 * 8];  // 16 of a warp's 32 tokens x 64 columns of 16-bit outputs
+        uint4 out[kWideEpi][16 * 8];  // 16 of a warp's 32 tokens x 64 columns of 16-bit outputs, or 8 of FP32
     };
     // full: a stage's operands have landed (even CTA: in both CTAs). empty: both halves' MMAs have read it.
     uint64_t full[kStages], empty[kStages];
@@ -247,6 +247,41 @@ __device__ __forceinline__ void store_tile(const Params& p, uint4* stage, int la
     }
 }
 
+// The same for FP32 outputs, 8 tokens at a time (a routed product whose rows are still to be summed); kW 4 or 1.
+template <int kW>
+__device__ __forceinline__ void store_tile_f32(const Params& p, uint4* stage, int lane, const float2 (&acc)[2][16], float weight,
+                                               float* y, int tokens, int columns) {
+    struct alignas(4 * kW) Piece {
+        float v[kW];
+    };
+#pragma unroll 1
+    for (int pass = 0; pass < 4; ++pass) {
+        if ((lane >> 3) == pass)
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const float2 a = acc[k >> 3][2 * (k & 7)], b = acc[k >> 3][2 * (k & 7) + 1];
+                stage[(lane & 7) * 16 + (k ^ (lane & 7))] =
+                    make_uint4(__float_as_uint(a.x * weight), __float_as_uint(a.y * weight), __float_as_uint(b.x * weight), __float_as_uint(b.y * weight));
+            }
+        __syncwarp();
+#pragma unroll 4
+        for (int j = 0; j < 16 / kW; ++j) {
+            const int l = (32 * j + lane) / (64 / kW), n = (32 * j + lane) % (64 / kW) * kW;
+            const Piece v = *reinterpret_cast<const Piece*>(reinterpret_cast<const float*>(&stage[l * 16 + ((n >> 2) ^ l)]) + (n & 3));
+            if (8 * pass + l >= tokens) continue;
+            float* to = y + (8 * pass + l) * p.ldy + n;
+            if (n + kW <= columns) {
+                *reinterpret_cast<Piece*>(to) = v;
+            } else {
+#pragma unroll
+                for (int i = 0; i < kW; ++i)
+                    if (n + i < columns) to[i] = v.v[i];
+            }
+        }
+        __syncwarp();
+    }
+}
+
 // (behind the waits of this thread: volatile)
 __device__ __forceinline__ float load_shared(uint32_t address) {
     float v;
@@ -361,9 +396,14 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
         } else {
             const int first = static_cast<int>(rank) * 128 + 32 * q;   // token of the warp's lane 0
             const int n0 = 256 * pair + 128 * sub + 64 * half;
-            uint16_t* y = p.Y + (static_cast<int64_t>(row0) + first) * p.ldy + n0;
+            const int64_t at = (static_cast<int64_t>(row0) + first) * p.ldy + n0;
+            uint16_t* y = static_cast<uint16_t*>(p.Y) + at;
             const int tokens = ok ? n - first : 0, columns = p.N - n0;
-            if (p.vec == 8) store_tile<8>(p, s.out[warp - 4], lane, acc, weight, y, tokens, columns);
+            if (p.f32) {
+                float* yf = static_cast<float*>(p.Y) + at;
+                if (p.vec == 4) store_tile_f32<4>(p, s.out[warp - 4], lane, acc, weight, yf, tokens, columns);
+                else store_tile_f32<1>(p, s.out[warp - 4], lane, acc, weight, yf, tokens, columns);
+            } else if (p.vec == 8) store_tile<8>(p, s.out[warp - 4], lane, acc, weight, y, tokens, columns);
             else if (p.vec == 4) store_tile<4>(p, s.out[warp - 4], lane, acc, weight, y, tokens, columns);
             else store_tile<1>(p, s.out[warp - 4], lane, acc, weight, y, tokens, columns);
         }

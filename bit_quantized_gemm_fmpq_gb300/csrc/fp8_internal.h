@@ -91,7 +91,7 @@ struct Fp8GemmArgs {
     const int32_t* pair_of;
     const float* pair_weight; // scales a row's outputs (nullptr: 1)
     int64_t pairs_routed;     // T * k, an upper bound of the rows in use (dense: rows)
-    void* Y;                  // plain layer: 16-bit output
+    void* Y;                  // plain layer: output of type dtype (FP32: experts only)
     int dtype;
     int64_t ldy;
     void* H;                  // gated layer: E4M3 codes [F/128][rows][128] and scales
@@ -120,8 +120,8 @@ struct RouteArgs {
 cudaError_t launch_moe_route(const RouteArgs& a, cudaStream_t stream);
 cudaError_t launch_moe_plan(const int32_t* ids, int64_t T, int k, int E, int32_t* plan, int32_t* counts,
                             cudaStream_t stream);
-cudaError_t launch_moe_combine(const void* D, int dtype, int64_t ldd, const int32_t* row_of, int64_t T, int k, int N,
-                               void* Y, int64_t ldy, bool pdl, cudaStream_t stream);
+cudaError_t launch_moe_combine(const void* D, int d_dtype, int64_t ldd, const int32_t* row_of, int64_t T, int k, int N,
+                               void* Y, int dtype, int64_t ldy, bool pdl, cudaStream_t stream);
 
 // Launch; pdl: as the programmatic dependent of the launch before it.
 template <typename... P, typename... A>

@@ -553,10 +553,23 @@ __global__ void __launch_bounds__(kChunk) plan_place_kernel(const int32_t* __res
 }
 
 // ---------------------------------------------------------------- the sum over a token's experts
-// Eight columns a thread, the slots in order, FP32 sums. DRAM bounds it: 4096 tokens of 8 rows of 4096 16-bit values,
-// 302 MB (44.5 us at the copy rate) in 49.7 us. Four rows in flight: one at a time, each waited for its row's number too.
-template <typename T, bool kVec>
-__global__ void __launch_bounds__(256) combine_kernel(const T* __restrict__ D, int64_t ldd, const int32_t* __restrict__ row_of,
+__device__ __forceinline__ void load8(const float* d, float (&v)[8]) {
+    const float4 a = reinterpret_cast<const float4*>(d)[0], b = reinterpret_cast<const float4*>(d)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T* d, float (&v)[8]) {
+    const uint4 raw = *reinterpret_cast<const uint4*>(d);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v[c] = as_float(reinterpret_cast<const T*>(&raw)[c]);
+}
+
+// Eight columns a thread, the slots in order, FP32 sums, rounded once to T. DRAM bounds it: 4096 tokens of 8 rows of 4096
+// 16-bit values, 302 MB (44.5 us at the copy rate) in 49.7 us. Four rows in flight: one at a time, each waited for its
+// row's number too.
+template <typename S, typename T, bool kVec>
+__global__ void __launch_bounds__(256) combine_kernel(const S* __restrict__ D, int64_t ldd, const int32_t* __restrict__ row_of,
                                                       int64_t tokens, int k, int N, T* __restrict__ Y, int64_t ldy) {
     dev::pdl_wait();
     dev::pdl_launch_dependents();
@@ -567,19 +580,18 @@ __global__ void __launch_bounds__(256) combine_kernel(const T* __restrict__ D, i
         const bool whole = kVec && n + 8 <= N;
         for (int j0 = 0; j0 < k; j0 += 4) {   // four rows in flight
             int32_t r[4];
-            uint4 raw[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) r[j] = j0 + j < k ? row_of[t * k + j0 + j] : -1;
             if (whole) {
+                float v[4][8];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (r[j] >= 0) raw[j] = *reinterpret_cast<const uint4*>(D + r[j] * ldd + n);
+                    if (r[j] >= 0) load8(D + r[j] * ldd + n, v[j]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     if (r[j] >= 0) {
-                        const T* v = reinterpret_cast<const T*>(&raw[j]);
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) acc[c] += as_float(v[c]);
+                        for (int c = 0; c < 8; ++c) acc[c] += v[j][c];
                     }
             } else {
                 for (int j = 0; j < 4; ++j)
@@ -600,14 +612,14 @@ __global__ void __launch_bounds__(256) combine_kernel(const T* __restrict__ D, i
     }
 }
 
-template <typename T>
+template <typename S, typename T>
 cudaError_t combine_as(const void* D, int64_t ldd, const int32_t* row_of, int64_t tokens, int k, int N, void* Y, int64_t ldy,
                        bool pdl, cudaStream_t stream) {
     const dim3 grid(static_cast<unsigned>(((N + 7) / 8 + 255) / 256), static_cast<unsigned>(tokens < 65535 ? tokens : 65535));
-    const bool vec = ldd % 8 == 0 && ldy % 8 == 0 &&
+    const bool vec = ldd * static_cast<int64_t>(sizeof(S)) % 16 == 0 && ldy % 8 == 0 &&
                      ((reinterpret_cast<uintptr_t>(D) | reinterpret_cast<uintptr_t>(Y)) & 15u) == 0;
-    auto fn = vec ? combine_kernel<T, true> : combine_kernel<T, false>;
-    return launch_after(fn, grid, 256, 0, pdl, stream, static_cast<const T*>(D), ldd, row_of, tokens, k, N,
+    auto fn = vec ? combine_kernel<S, T, true> : combine_kernel<S, T, false>;
+    return launch_after(fn, grid, 256, 0, pdl, stream, static_cast<const S*>(D), ldd, row_of, tokens, k, N,
                         static_cast<T*>(Y), ldy);
 }
 
@@ -630,10 +642,11 @@ cudaError_t launch_moe_plan(const int32_t* ids, int64_t T, int k, int E, int32_t
     return cudaGetLastError();
 }
 
-cudaError_t launch_moe_combine(const void* D, int dtype, int64_t ldd, const int32_t* row_of, int64_t T, int k, int N,
-                               void* Y, int64_t ldy, bool pdl, cudaStream_t stream) {
-    return dtype == kF16 ? combine_as<__half>(D, ldd, row_of, T, k, N, Y, ldy, pdl, stream)
-                         : combine_as<__nv_bfloat16>(D, ldd, row_of, T, k, N, Y, ldy, pdl, stream);
+cudaError_t launch_moe_combine(const void* D, int d_dtype, int64_t ldd, const int32_t* row_of, int64_t T, int k, int N,
+                               void* Y, int dtype, int64_t ldy, bool pdl, cudaStream_t stream) {
+    auto fn = d_dtype == kF32 ? (dtype == kF16 ? combine_as<float, __half> : combine_as<float, __nv_bfloat16>)
+                              : (dtype == kF16 ? combine_as<__half, __half> : combine_as<__nv_bfloat16, __nv_bfloat16>);
+    return fn(D, ldd, row_of, T, k, N, Y, ldy, pdl, stream);
 }
 
 }  // namespace fmpq

@@ -90,6 +90,7 @@ SIGNATURES = {
     "moe_down": (_I32, [_P, _P, _I64, _I32, _P, _P, _P, _P, _P, _P, _I32, _I64, _P]),
     "moe_experts_bytes": (_SZ, [_P, _P, _I64, _I32]),
     "moe_experts": (_I32, [_P, _P, _P, _I32, _I64, _I64, _I32, _P, _P, _P, _P, _P, _P, _P, _I64, _P, _SZ, _P]),
+    "moe_combine_f32": (_I32, [_P, _I64, _P, _I64, _I32, _I32, _I32, _P, _I32, _I64, _P]),
     "moe_combine": (_I32, [_P, _I32, _I64, _P, _I64, _I32, _I32, _I32, _P, _I64, _P]),
     "fmpq_status_string": (ctypes.c_char_p, [_I32]),
     "fmpq_version": (_I32, []),
@@ -612,11 +613,11 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _rows16(X, what: str) -> int:
-    """A 16-bit CUDA matrix whose rows are contiguous (any row stride). Returns its dtype code."""
+def _rows16(X, what: str, fp32: bool = False) -> int:
+    """A 16-bit (fp32: or FP32) CUDA matrix whose rows are contiguous (any row stride). Returns its dtype code."""
     code = _dtype_code(X.dtype)
-    if not (X.is_cuda and X.dim() == 2 and code < 2):
-        raise ValueError(f"{what} must be a 2-D fp16 or bf16 CUDA tensor")
+    if not (X.is_cuda and X.dim() == 2 and (code < 2 or fp32)):
+        raise ValueError(f"{what} must be a 2-D {'fp32, ' if fp32 else ''}fp16 or bf16 CUDA tensor")
     if X.shape[1] > 1 and X.stride(1) != 1:
         raise ValueError(f"{what} must have contiguous rows")
     return code
@@ -863,7 +864,8 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1
 
 
 class MoePlan:
-    """The (token, slot) pairs sorted by expert (moe_plan): sizes and the device buffer."""
+    """The (token, slot) pairs sorted by expert (moe_plan): sizes, the device buffer, and the type of the sums over a
+    token's slots (moe_down's dtype)."""
 
     def __init__(self, T: int, k: int, experts: int, device):
         import torch
@@ -872,6 +874,7 @@ class MoePlan:
         if nbytes == 0:
             raise FmpqError("moe_plan_bytes", 2)
         self.T, self.k, self.experts = T, k, experts
+        self.dtype = torch.float16
         self.rows = int(lib.moe_rows(T, k, experts))
         self.buffer = torch.empty(nbytes // 4, dtype=torch.int32, device=device)
 
@@ -934,7 +937,9 @@ def moe_up(layer: Fp8Layer, plan: MoePlan, A_packed, a_scales, W_packed, w_scale
 
 @_on_stream
 def moe_down(layer: Fp8Layer, plan: MoePlan, A_packed, a_scales, W_packed, w_scales, weights=None, dtype=None, D=None):
-    """Every row's product with its expert, times its pair's weight: D [plan.rows, N] (fp16 by default)."""
+    """Every row's product with its expert, times its pair's weight: D [plan.rows, N] in FP32, for moe_combine to sum
+    and to round to dtype (fp16 by default). A D that is passed may have 16 bits: each row is then rounded, which halves
+    the bytes and costs a rounding a slot."""
     import torch
     _need(plan.experts == layer.experts and not layer.gated, "moe_down needs a plain layer and its plan")
     layer.check_weights(W_packed, w_scales)
@@ -943,9 +948,12 @@ def moe_down(layer: Fp8Layer, plan: MoePlan, A_packed, a_scales, W_packed, w_sca
         _need(weights.is_cuda and weights.dtype == torch.float32 and weights.shape == (plan.T, plan.k) and
               weights.is_contiguous(), "weights must be contiguous fp32 [T, k]")
     if D is None:
-        D = torch.empty((plan.rows, layer.N), dtype=dtype or torch.float16, device=A_packed.device)
-    _rows16(D, "D")
+        D = torch.empty((plan.rows, layer.N), dtype=torch.float32, device=A_packed.device)
+    _rows16(D, "D", fp32=True)
     _need(D.shape == (plan.rows, layer.N), "D must be [rows, N]")
+    dtype = dtype or (D.dtype if D.dtype != torch.float32 else torch.float16)
+    _need(_dtype_code(dtype) < 2 and D.dtype in (torch.float32, dtype), "dtype must be fp16 or bf16, and a 16-bit D of it")
+    plan.dtype = dtype
     _check("moe_down", layer._lib.moe_down(layer.handle, _ptr(plan.buffer), plan.T, plan.k, _ptr(weights), _ptr(A_packed),
                                            _ptr(a_scales), _ptr(W_packed), _ptr(w_scales), _ptr(D), _dtype_code(D.dtype),
                                            _ld(D), _stream(None)))
@@ -954,16 +962,19 @@ def moe_down(layer: Fp8Layer, plan: MoePlan, A_packed, a_scales, W_packed, w_sca
 
 @_on_stream
 def moe_combine(D, plan: MoePlan, Y=None):
-    """Y [T, N]: the sum of D's rows of each token."""
+    """Y [T, N]: the sum of D's rows of each token, rounded once; of moe_down's dtype (or of a 16-bit D's)."""
     import torch
-    _rows16(D, "D")
+    code = _rows16(D, "D", fp32=True)
     _need(D.shape[0] == plan.rows, "D must be [rows, N]")
     if Y is None:
-        Y = torch.empty((plan.T, D.shape[1]), dtype=D.dtype, device=D.device)
-    _rows16(Y, "Y")
-    _need(Y.shape == (plan.T, D.shape[1]) and Y.dtype == D.dtype, "Y must be [T, N] of D's type")
-    _check("moe_combine", load_library().moe_combine(_ptr(D), _dtype_code(D.dtype), _ld(D), _ptr(plan.buffer), plan.T,
-                                                     plan.k, plan.experts, D.shape[1], _ptr(Y), _ld(Y), _stream(None)))
+        Y = torch.empty((plan.T, D.shape[1]), dtype=plan.dtype if code == 2 else D.dtype, device=D.device)
+    y_code = _rows16(Y, "Y")
+    _need(Y.shape == (plan.T, D.shape[1]) and (code == 2 or y_code == code), "Y must be [T, N], of a 16-bit D's type")
+    sizes = (_ptr(plan.buffer), plan.T, plan.k, plan.experts, D.shape[1])
+    if code == 2:
+        _check("moe_combine_f32", load_library().moe_combine_f32(_ptr(D), _ld(D), *sizes, _ptr(Y), y_code, _ld(Y), _stream(None)))
+    else:
+        _check("moe_combine", load_library().moe_combine(_ptr(D), code, _ld(D), *sizes, _ptr(Y), _ld(Y), _stream(None)))
     return Y
 
 

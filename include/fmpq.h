@@ -537,18 +537,21 @@ FMPQ_API fmpq_status moe_quantize(const fp8_layer* layer, const void* plan, int6
 FMPQ_API fmpq_status moe_up(const fp8_layer* layer, const void* plan, int64_t T, int32_t k, const void* A_packed,
                             const void* a_scales, const void* W_packed, const void* w_scales, void* H_packed,
                             void* h_scales, void* stream);
-/* D[row][n] = weights[pair of row] * (the row's product with its expert), 16 bits, [moe_rows][ldd];
- * weights fp32 [T][k], NULL: 1. */
+/* D[row][n] = weights[pair of row] * (the row's product with its expert), of any fmpq_dtype, [moe_rows][ldd];
+ * weights fp32 [T][k], NULL: 1. FP32 keeps what moe_combine_f32 sums; 16 bits halve the bytes, at one
+ * rounding a row more. */
 FMPQ_API fmpq_status moe_down(const fp8_layer* layer, const void* plan, int64_t T, int32_t k, const void* weights,
                               const void* A_packed, const void* a_scales, const void* W_packed, const void* w_scales,
                               void* D, int32_t dtype, int64_t ldd, void* stream);
 /* Y[t] = the sum of D over the token's rows, in slot order, FP32 sums, rounded once; a token without
- * experts gets zeros. */
+ * experts gets zeros. moe_combine: D and Y of the same 16 bits; moe_combine_f32: FP32 D, Y of 16 bits. */
 FMPQ_API fmpq_status moe_combine(const void* D, int32_t dtype, int64_t ldd, const void* plan, int64_t T, int32_t k,
                                  int32_t E, int32_t N, void* Y, int64_t ldy, void* stream);
+FMPQ_API fmpq_status moe_combine_f32(const float* D, int64_t ldd, const void* plan, int64_t T, int32_t k, int32_t E,
+                                     int32_t N, void* Y, int32_t dtype, int64_t ldy, void* stream);
 
 /* The routed feed-forward in one call, its steps above in order on `stream`: moe_plan of ids, moe_quantize
- * of X, moe_up, moe_down with the weights, moe_combine into Y [T][ldy] of X's type. up: gated, [2F][K];
+ * of X, moe_up, moe_down (FP32) with the weights, moe_combine_f32 into Y [T][ldy] of X's type. up: gated, [2F][K];
  * down: [N][F] with the same experts. scratch: moe_experts_bytes, not read before it is written. */
 FMPQ_API size_t moe_experts_bytes(const fp8_layer* up, const fp8_layer* down, int64_t T, int32_t k);
 FMPQ_API fmpq_status moe_experts(const fp8_layer* up, const fp8_layer* down, const void* X, int32_t dtype, int64_t ldx,
