@@ -175,15 +175,12 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi, bool bf16) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
-// silu(g) * u = g u / (1 + e^-g), with the approximate exponential and reciprocal: within about
-// (4 + 2 |g|) 2^-23 of it, far below the E4M3 rounding that follows. (2^x overflows to inf and the reciprocal
-// to 0 where silu(g) is below 1e-36 in magnitude.)
-__device__ __forceinline__ float silu_times(float g, float u) {
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-    return g * r * u;
-}
+// silu(g) * u = g u / (1 + e^-g): the exponential and the quotient to 2 of their last places, the value and the scale
+// made of it within 4 steps of 2^-23 for every g. The E4M3 codes that follow change where the value crosses the middle
+// between two codes, so the hardware's exponential, whose error grows with |g| (15 steps at 49), is not used: it saves
+// 19 of 798 us for 4096 tokens through 8 of 128 experts of 4096 x 1024. A rounded division costs 48 more. (Where
+// 1 + e^-g passes 2^126, silu(g) is below 1e-36 in magnitude, the quotient is 0.)
+__device__ __forceinline__ float silu_times(float g, float u) { return __fdividef(g, 1.0f + expf(-g)) * u; }
 
 }  // namespace fp8
 

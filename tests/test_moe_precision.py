@@ -1,8 +1,10 @@
-"""The routed experts' outputs are summed in FP32 and rounded once.
+"""The routed experts' outputs are summed in FP32 and rounded once; SwiGLU is good to a few FP32 roundings.
 
 Tolerances. Y against the 64-bit sum over a token's slots of w down(h), h the values of the hidden codes: half a
 step of the type (finfo.eps / 2 of the value, or half the smallest fp16 number), and (F + 2 nb + k + 2) steps of 2^-23
-of the absolute products for the FP32 sums, each addition and scaling one step at worst.
+of the absolute products for the FP32 sums, each addition and scaling one step at worst. The hidden scale where gate
+and up are exact: the exponential 2 steps of 2^-23, the sum in the denominator, the quotient, the product and the
+division by 448 half a step each: 4 steps of 2^-23.
 """
 import pytest
 
@@ -74,6 +76,31 @@ def test_slots_past_the_types_range_may_cancel(fmpq_mod, T):  # noqa: F811
     Y, h, row_of = run_steps(fmpq_mod, X, up, down, ids, w)
     assert float((h[row_of[:, 0]] @ down[0].double().t()).min()) > 65504     # a slot alone
     check_sum(Y, h, row_of, down, ids, w)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [128, 6000])   # tiles of 64 and of 256 tokens
+@pytest.mark.parametrize("sign", [1, -1])
+def test_swiglu_scale(fmpq_mod, T, sign):  # noqa: F811
+    """Tokens with one channel and weights in one row make gate and up exact: the hidden scale is
+    fl32(|silu(g) u| / 448) to 4 steps of 2^-23, for gates up to 49 in size."""
+    import torch
+    channel = torch.arange(T) % 128
+    X = torch.zeros(T, 128)
+    X[torch.arange(T), channel] = 448.0
+    up = torch.zeros(1, 256, 128)
+    codes = torch.arange(128, dtype=torch.uint8).clamp(max=126).view(torch.float8_e4m3fn).float()
+    gates = sign * codes.flip(0) * 2.0 ** -12      # a block of E4M3 codes with the scale 2^-12
+    up[0, 0] = gates
+    up[0, 128] = 448 * 2.0 ** -12
+    layer = fmpq_mod.Fp8Layer(128, 256, gated=True)
+    W = fmpq_mod.fp8_pack_weights(layer, up.half().cuda())
+    plan = fmpq_mod.moe_plan(torch.zeros(T, 1, dtype=torch.int32, device="cuda"), 1)
+    _, scales = fmpq_mod.moe_up(layer, plan, *fmpq_mod.moe_quantize(layer, plan, X.bfloat16().cuda()), *W)
+    gate, lin = (448.0 * gates).double()[channel], 49.0
+    ref = (gate * torch.sigmoid(gate) * lin).abs() / 448
+    got = scales[0].cpu().double()[plan.row_of.cpu().long()[:, 0]]
+    assert bool(((got - ref).abs() <= ref * 4 * 2.0 ** -23 + 2.0 ** -149).all()), float(((got - ref).abs() / ref.clamp_min(1e-300)).max() * 2 ** 23)
 
 
 @pytest.mark.gpu
