@@ -396,6 +396,12 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs p, const Rul
                 id = w * NI + NI - 1 - static_cast<int>(from_end);
             }
         }
+        // all 32 lanes taken: the next key may still be one of the k
+        bool more = false;
+        if (!exact && taken == 32) {
+            const uint32_t m = __reduce_max_sync(kAll, item[0] & ~static_cast<uint32_t>(NI - 1));
+            more = m != 0u && close_call(unordered(last), unordered(m), kStep);
+        }
         float x = id >= 0 ? as_float(row[id]) : kNone;
         if (!exact) {
             // neighbours too close to tell, unless their logits and biases are equal (a true tie)
@@ -405,11 +411,11 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs p, const Rul
             const bool tight = lane < 31 && mine != 0u && next != 0u && close_call(unordered(mine), unordered(next), kStep) &&
                                !(x == next_x && b == next_b);
             const bool any = __any_sync(kAll, tight);
-            if (any && !close && (p.sigmoid || by_logit) && taken < 32) {
+            if (any && !close && !more && (p.sigmoid || by_logit)) {
                 // every expert that may be among the k is in a lane: put them in the order of their keys in 64 bits
                 order_in_64(x, b, by_logit, taken, lane, id);
                 x = id >= 0 ? as_float(row[id]) : kNone;
-            } else if (any || close) {
+            } else if (any || close || more) {
                 id = choose_in_64<T, NI>(row, p.bias, p.sigmoid, by_logit, top, r, lane);
                 x = id >= 0 ? as_float(row[id]) : kNone;
             }
