@@ -624,8 +624,15 @@ def _rows16(X, what: str, fp32: bool = False) -> int:
 
 
 def _ld(X) -> int:
-    """Row stride in elements (a single row may have any)."""
-    return max(X.stride(0), X.shape[1]) if X.shape[0] > 1 else X.shape[1]
+    """Row stride in elements (a single row may have any). Rows that share storage (an expanded tensor, windows that
+    overlap) are refused: the kernels take rows one after another."""
+    rows, width = X.shape
+    if rows <= 1:
+        return width
+    ld = X.stride(0)
+    if ld < width:
+        raise ValueError("the rows of a matrix must not overlap (an expanded tensor needs .contiguous())")
+    return ld
 
 
 def _on(X) -> int:

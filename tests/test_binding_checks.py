@@ -1,0 +1,109 @@
+"""What the Python binding of the E4M3 layers and the routed experts refuses before the library sees a pointer. No GPU:
+CPU tensors that claim to be on one stand in for the arguments, and a library that must not be called for the real one."""
+import pytest
+import torch
+
+from bit_quantized_gemm_fmpq_gb300 import fmpq
+
+
+class OnGpu(torch.Tensor):
+    is_cuda = True
+
+
+def on_gpu(t):
+    return t.as_subclass(OnGpu)
+
+
+class NoLibrary:
+    def __getattr__(self, name):
+        def call(*args):
+            if name.endswith("_bytes"):    # a size, computed on the host
+                return 64
+            raise AssertionError(f"{name} was reached")
+        return call
+
+
+def layer_of(K, N, experts=1, gated=False):
+    layer = object.__new__(fmpq.Fp8Layer)
+    layer._lib, layer._h = NoLibrary(), None
+    layer.K, layer.N, layer.experts, layer.gated = K, N, experts, gated
+    layer.nb = -(-K // 128)
+    layer.scale_rows = 2 * -(-(N // 2) // 128) if gated else -(-N // 128)
+    pairs = -(-(N // 2) // 128) if gated else -(-N // 256)
+    layer._w_bytes, layer._w_scales = experts * pairs * 2 * layer.nb * 128 * 128, experts * layer.scale_rows * layer.nb
+    layer._workspaces, layer._workspace_bytes = {}, {}
+    return layer
+
+
+def weights_of(layer):
+    return (on_gpu(torch.zeros(layer._w_bytes, dtype=torch.uint8)),
+            on_gpu(torch.zeros(layer.experts, layer.scale_rows, layer.nb)))
+
+
+def plan_of(T, k, experts, rows):
+    plan = object.__new__(fmpq.MoePlan)
+    plan.T, plan.k, plan.experts, plan.rows, plan.dtype = T, k, experts, rows, torch.float16
+    plan.buffer = on_gpu(torch.zeros(2 * experts + T * k + rows, dtype=torch.int32))
+    return plan
+
+
+@pytest.fixture(autouse=True)
+def no_library(monkeypatch):
+    monkeypatch.setattr(fmpq, "load_library", NoLibrary)
+    monkeypatch.setattr(fmpq, "_lib", NoLibrary())
+    monkeypatch.setattr(fmpq, "_on", lambda X: 0)
+    monkeypatch.setattr(fmpq, "_stream", lambda s: 0)
+
+
+def half(*shape):
+    return on_gpu(torch.zeros(*shape, dtype=torch.float16))
+
+
+def overlapping(M, K):
+    """M rows of K that share storage: one row repeated, and windows one element apart."""
+    return [half(1, K).expand(M, K), half(M + K).as_strided((M, K), (1, 1)), half(M * K).as_strided((M, K), (K - 1, 1))]
+
+
+# ---- rows that overlap ------------------------------------------------------------------------
+
+def test_row_stride():
+    assert fmpq._ld(half(4, 8)) == 8 and fmpq._ld(half(4, 8)[:, :5]) == 8
+    assert fmpq._ld(half(8, 6)[::2]) == 12 and fmpq._ld(half(1, 8).expand(1, 8)) == 8
+    assert fmpq._ld(half(9)[2:].as_strided((1, 7), (3, 1))) == 7      # one row: any stride
+    for X in overlapping(3, 8):
+        with pytest.raises(ValueError):
+            fmpq._ld(X)
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_overlapping_rows_are_refused(which):
+    layer, M = layer_of(256, 128), 5
+    W, s = weights_of(layer)
+    X = overlapping(M, 256)[which]
+    A, a = on_gpu(torch.zeros(2, M, 128, dtype=torch.uint8)), on_gpu(torch.zeros(2, 8))
+    calls = [
+        lambda: fmpq.fp8_quantize(layer, X, A, a),
+        lambda: fmpq.fp8_quantize_gemm(layer, X, W, s, A, a, Y=half(M, 128), workspace=half(8)),
+        lambda: fmpq.fp8_quantize_gemm(layer, half(M, 256), W, s, A, a, Y=overlapping(M, 128)[which], workspace=half(8)),
+        lambda: fmpq.fp8_gemm(layer, A, a, W, s, M, Y=overlapping(M, 128)[which], workspace=half(8)),
+        lambda: fmpq.fp8_pack_weights(layer, overlapping(128, 256)[which]),
+        lambda: fmpq.fp8_pack_codes(layer, on_gpu(torch.zeros(1, 256, dtype=torch.uint8)).expand(128, 256), s),
+        lambda: fmpq.moe_route(X, 2),
+    ]
+    for call in calls:
+        with pytest.raises(ValueError):
+            call()
+    up, down, T, k = layer_of(256, 256, 3, True), layer_of(128, 256, 3), M, 2
+    plan = plan_of(T, k, 3, 40)
+    H, h = on_gpu(torch.zeros(1, 40, 128, dtype=torch.uint8)), on_gpu(torch.zeros(1, 40))
+    ids, w = on_gpu(torch.zeros(T, k, dtype=torch.int32)), on_gpu(torch.zeros(T, k))
+    calls = [
+        lambda: fmpq.moe_quantize(up, plan, X, on_gpu(torch.zeros(2, 40, 128, dtype=torch.uint8)), on_gpu(torch.zeros(2, 40))),
+        lambda: fmpq.moe_experts(up, down, X, ids, w, *weights_of(up), *weights_of(down)),
+        lambda: fmpq.moe_down(down, plan, H, h, *weights_of(down), D=overlapping(40, 256)[which]),
+        lambda: fmpq.moe_combine(overlapping(40, 256)[which], plan),
+        lambda: fmpq.moe_combine(half(40, 256), plan, Y=overlapping(T, 256)[which]),
+    ]
+    for call in calls:
+        with pytest.raises(ValueError):
+            call()
