@@ -613,6 +613,12 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
+def _need_activations(codes, scales, nb: int, rows: int, what: str):
+    """Codes [nb, rows, 128] and scales [nb, rows rounded up to 4], or larger."""
+    _need(codes.is_contiguous() and scales.is_contiguous() and codes.numel() >= nb * rows * BLOCK and
+          scales.numel() >= nb * ((rows + 3) // 4 * 4), f"{what} are too small for the rows")
+
+
 def _rows16(X, what: str, fp32: bool = False) -> int:
     """A 16-bit (fp32: or FP32) CUDA matrix whose rows are contiguous (any row stride). Returns its dtype code."""
     code = _dtype_code(X.dtype)
@@ -683,8 +689,7 @@ class Fp8Layer:
               "W_packed and w_scales must be this layer's (fp8_pack_weights, fp8_pack_codes)")
 
     def check_activations(self, A_packed, a_scales, rows: int):
-        _need(A_packed.is_contiguous() and a_scales.is_contiguous() and A_packed.numel() >= self.nb * rows * BLOCK and
-              a_scales.numel() >= self.nb * ((rows + 3) // 4 * 4), "A_packed and a_scales are too small for the rows")
+        _need_activations(A_packed, a_scales, self.nb, rows, "A_packed and a_scales")
 
     def activations(self, rows: int, device):
         """Buffers for `rows` rows of quantized activations: codes uint8 [nb, rows, 128] (swizzled) and
@@ -766,6 +771,7 @@ def fp8_quantize(layer: Fp8Layer, X, A_packed=None, a_scales=None):
     if A_packed is None or a_scales is None:
         A, s = layer.activations(M, X.device)
         A_packed, a_scales = A if A_packed is None else A_packed, s if a_scales is None else a_scales
+    layer.check_activations(A_packed, a_scales, M)
     _check("fp8_quantize", layer._lib.fp8_quantize(layer.handle, _ptr(X), _dtype_code(X.dtype), _ld(X), M,
                                                    _ptr(A_packed), _ptr(a_scales), _stream(None)))
     return A_packed, a_scales
@@ -919,6 +925,7 @@ def moe_quantize(layer: Fp8Layer, plan: MoePlan, X, A_packed=None, a_scales=None
     if A_packed is None or a_scales is None:
         A, s = layer.activations(plan.rows, X.device)
         A_packed, a_scales = A if A_packed is None else A_packed, s if a_scales is None else a_scales
+    layer.check_activations(A_packed, a_scales, plan.rows)
     _check("moe_quantize", layer._lib.moe_quantize(layer.handle, _ptr(plan.buffer), plan.T, plan.k, _ptr(X),
                                                    _dtype_code(X.dtype), _ld(X), _ptr(A_packed), _ptr(a_scales),
                                                    _stream(None)))
@@ -937,6 +944,7 @@ def moe_up(layer: Fp8Layer, plan: MoePlan, A_packed, a_scales, W_packed, w_scale
         H_packed = torch.empty((fb, plan.rows, BLOCK), dtype=torch.uint8, device=A_packed.device)
     if h_scales is None:
         h_scales = torch.empty((fb, (plan.rows + 3) // 4 * 4), dtype=torch.float32, device=A_packed.device)
+    _need_activations(H_packed, h_scales, fb, plan.rows, "H_packed and h_scales")
     _check("moe_up", layer._lib.moe_up(layer.handle, _ptr(plan.buffer), plan.T, plan.k, _ptr(A_packed), _ptr(a_scales),
                                        _ptr(W_packed), _ptr(w_scales), _ptr(H_packed), _ptr(h_scales), _stream(None)))
     return H_packed, h_scales

@@ -107,3 +107,35 @@ def test_overlapping_rows_are_refused(which):
     for call in calls:
         with pytest.raises(ValueError):
             call()
+
+
+# ---- buffers that the caller passes -----------------------------------------------------------
+
+def u8(*shape):
+    return on_gpu(torch.zeros(*shape, dtype=torch.uint8))
+
+
+def f32(*shape):
+    return on_gpu(torch.zeros(*shape))
+
+
+@pytest.mark.parametrize("bad", [
+    (u8(1, 5, 128), f32(2, 8)), (u8(2, 5, 128)[:, :, :127], f32(2, 8)), (u8(2, 5, 128), f32(2, 5)), (u8(2, 5, 128), f32(1, 8)),
+    (u8(2, 5, 128), f32(8, 2).t()), (u8(5, 2, 128).transpose(0, 1), f32(2, 8)),
+    (None, f32(2, 4)), (u8(4), None),
+])
+def test_buffers_of_the_quantizers_are_large_enough(bad):
+    layer = layer_of(256, 128)
+    with pytest.raises(ValueError):
+        fmpq.fp8_quantize(layer, half(5, 256), *bad)
+    up = layer_of(256, 256, 3, True)
+    with pytest.raises(ValueError):
+        fmpq.moe_quantize(up, plan_of(2, 1, 3, 5), half(2, 256), *bad)
+
+
+@pytest.mark.parametrize("bad", [(u8(1, 40, 128), None), (None, f32(1, 40)), (u8(2, 39, 128), None), (None, f32(2, 39)),
+                                 (u8(40, 2, 128).transpose(0, 1), f32(2, 40))])
+def test_buffers_of_the_hidden_vectors_are_large_enough(bad):
+    up, plan = layer_of(128, 300, 3, True), plan_of(5, 2, 3, 40)     # 150 hidden channels: two blocks
+    with pytest.raises(ValueError):
+        fmpq.moe_up(up, plan, u8(1, 40, 128), f32(1, 40), *weights_of(up), *bad)
