@@ -613,10 +613,16 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
+def _codes_and_scales(codes, scales) -> bool:
+    import torch
+    return (codes.is_cuda and scales.is_cuda and codes.element_size() == 1 and scales.dtype == torch.float32 and
+            codes.is_contiguous() and scales.is_contiguous())
+
+
 def _need_activations(codes, scales, nb: int, rows: int, what: str):
     """Codes [nb, rows, 128] and scales [nb, rows rounded up to 4], or larger."""
-    _need(codes.is_contiguous() and scales.is_contiguous() and codes.numel() >= nb * rows * BLOCK and
-          scales.numel() >= nb * ((rows + 3) // 4 * 4), f"{what} are too small for the rows")
+    _need(_codes_and_scales(codes, scales) and codes.numel() >= nb * rows * BLOCK and
+          scales.numel() >= nb * ((rows + 3) // 4 * 4), f"{what} must be contiguous bytes and fp32 CUDA tensors, large enough for the rows")
 
 
 def _rows16(X, what: str, fp32: bool = False) -> int:
@@ -685,7 +691,7 @@ class Fp8Layer:
         return self._w_bytes
 
     def check_weights(self, W_packed, w_scales):
-        _need(W_packed.numel() == self._w_bytes and w_scales.numel() == self._w_scales and w_scales.is_contiguous(),
+        _need(_codes_and_scales(W_packed, w_scales) and W_packed.numel() == self._w_bytes and w_scales.numel() == self._w_scales,
               "W_packed and w_scales must be this layer's (fp8_pack_weights, fp8_pack_codes)")
 
     def check_activations(self, A_packed, a_scales, rows: int):
@@ -755,6 +761,7 @@ def fp8_pack_codes(layer: Fp8Layer, codes, scales):
 @_on_stream
 def fp8_unpack_weights(layer: Fp8Layer, W_packed, w_scales, expert: int = 0):
     import torch
+    layer.check_weights(W_packed, w_scales)
     W = torch.empty((layer.N, layer.K), dtype=torch.float32, device=W_packed.device)
     _check("fp8_unpack_weights", layer._lib.fp8_unpack_weights(layer.handle, expert, _ptr(W_packed), _ptr(w_scales),
                                                                _ptr(W), _stream(None)))
@@ -778,9 +785,13 @@ def fp8_quantize(layer: Fp8Layer, X, A_packed=None, a_scales=None):
 
 
 def _workspace_of(layer: Fp8Layer, M: int, workspace):
+    """The pointer and the bytes of the workspace passed, or of the layer's own."""
     if workspace is None:
         workspace = layer.workspace(M)
-    return workspace, workspace.numel() if workspace is not None else 0
+        if workspace is None:
+            return None, 0
+    _need(workspace.is_cuda and workspace.is_contiguous(), "workspace must be a contiguous CUDA tensor")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 @_on_stream
@@ -794,9 +805,9 @@ def fp8_gemm(layer: Fp8Layer, A_packed, a_scales, W_packed, w_scales, M: int, dt
     if not layer.gated:  # the library refuses a gated one
         layer.check_weights(W_packed, w_scales)
         layer.check_activations(A_packed, a_scales, M)
-    workspace, nbytes = _workspace_of(layer, M, workspace)
+    w_ptr, w_bytes = _workspace_of(layer, M, workspace)
     _check("fp8_gemm", layer._lib.fp8_gemm(layer.handle, _ptr(A_packed), _ptr(a_scales), _ptr(W_packed), _ptr(w_scales), M,
-                                           _ptr(Y), _dtype_code(Y.dtype), _ld(Y), _ptr(workspace), nbytes,
+                                           _ptr(Y), _dtype_code(Y.dtype), _ld(Y), w_ptr, w_bytes,
                                            _stream(None)))
     return Y
 
@@ -823,9 +834,7 @@ def fp8_quantize_gemm(layer: Fp8Layer, X, W_packed, w_scales, A_packed=None, a_s
         Y = torch.empty((M, layer.N), dtype=X.dtype, device=X.device)
     else:
         _need(_rows16(Y, "Y") == code and Y.shape == (M, layer.N), "Y must be [M, N] of X's type")
-    if workspace is None:
-        workspace = layer.workspace(M)
-    w_ptr, w_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    w_ptr, w_bytes = _workspace_of(layer, M, workspace)
     _check("fp8_quantize_gemm", layer._lib.fp8_quantize_gemm(
         layer._h, X.data_ptr(), code, _ld(X), M, a_ptr, s_ptr, W_packed.data_ptr(), w_scales.data_ptr(), Y.data_ptr(),
         _ld(Y), w_ptr, w_bytes, _on(X)))
@@ -864,12 +873,13 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1
     if ids is None:
         ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
     else:
-        _need(ids.shape == (T, k) and ids.dtype == torch.int32 and ids.is_contiguous(), "ids must be int32 [T, k]")
+        _need(ids.is_cuda and ids.shape == (T, k) and ids.dtype == torch.int32 and ids.is_contiguous(),
+              "ids must be a contiguous int32 CUDA tensor [T, k]")
     if weights is None:
         weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
     else:
-        _need(weights.shape == (T, k) and weights.dtype == torch.float32 and weights.is_contiguous(),
-              "weights must be fp32 [T, k]")
+        _need(weights.is_cuda and weights.shape == (T, k) and weights.dtype == torch.float32 and weights.is_contiguous(),
+              "weights must be a contiguous fp32 CUDA tensor [T, k]")
     _check("moe_route", (_lib or load_library()).moe_route(
         logits.data_ptr(), _dtype_code(logits.dtype), _ld(logits), T, E, k, sigmoid, b_ptr, groups, top_groups, group_top,
         1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(), _on(logits)))

@@ -139,3 +139,66 @@ def test_buffers_of_the_hidden_vectors_are_large_enough(bad):
     up, plan = layer_of(128, 300, 3, True), plan_of(5, 2, 3, 40)     # 150 hidden channels: two blocks
     with pytest.raises(ValueError):
         fmpq.moe_up(up, plan, u8(1, 40, 128), f32(1, 40), *weights_of(up), *bad)
+
+
+# ---- types, and tensors that are not on the GPU -----------------------------------------------
+
+def calls_with_weights(W, s):
+    """Every call that reads packed weights, each with W and s made for its own layer."""
+    plain, down, up = layer_of(256, 128), layer_of(256, 128, 3), layer_of(256, 256, 3, True)
+    A, a = u8(2, 40, 128), f32(2, 40)
+    plan, ids, w = plan_of(5, 2, 3, 40), on_gpu(torch.zeros(5, 2, dtype=torch.int32)), f32(5, 2)
+    square = layer_of(128, 256, 3)
+    return [lambda: fmpq.fp8_unpack_weights(plain, W(plain), s(plain)),
+            lambda: fmpq.fp8_gemm(plain, A, a, W(plain), s(plain), 5),
+            lambda: fmpq.fp8_quantize_gemm(plain, half(5, 256), W(plain), s(plain)),
+            lambda: fmpq.moe_up(up, plan, A, a, W(up), s(up)),
+            lambda: fmpq.moe_down(down, plan, A, a, W(down), s(down)),
+            lambda: fmpq.moe_experts(up, square, half(5, 256), ids, w, *weights_of(up), W(square), s(square)),
+            lambda: fmpq.moe_experts(up, square, half(5, 256), ids, w, W(up), s(up), *weights_of(square))]
+
+
+@pytest.mark.parametrize("W,s", [
+    (lambda L: weights_of(L)[0], lambda L: weights_of(L)[1].half()),                       # fp16 scales of the right count
+    (lambda L: weights_of(L)[0], lambda L: weights_of(L)[1].as_subclass(torch.Tensor)),    # on the host
+    (lambda L: weights_of(L)[0].as_subclass(torch.Tensor), lambda L: weights_of(L)[1]),
+    (lambda L: on_gpu(torch.zeros(2 * L._w_bytes, dtype=torch.uint8))[::2], lambda L: weights_of(L)[1]),
+    (lambda L: on_gpu(torch.zeros(L._w_bytes, dtype=torch.int16)), lambda L: weights_of(L)[1]),
+    (lambda L: weights_of(L)[0][16:], lambda L: weights_of(L)[1]),
+    (lambda L: weights_of(L)[0], lambda L: f32(L.experts, L.scale_rows, L.nb + 1)),
+])
+def test_weights_are_of_the_layers_types(W, s):
+    for call in calls_with_weights(W, s):
+        with pytest.raises(ValueError):
+            call()
+
+
+@pytest.mark.parametrize("bad", [
+    (u8(2, 40, 128), f32(2, 40).half()), (on_gpu(torch.zeros(2, 40, 128, dtype=torch.int16)), f32(2, 40)),
+    (torch.zeros(2, 40, 128, dtype=torch.uint8), f32(2, 40)), (u8(2, 40, 128), torch.zeros(2, 40)),
+])
+def test_activations_are_of_the_layers_types(bad):
+    plain, down, up = layer_of(256, 128), layer_of(256, 128, 3), layer_of(256, 300, 3, True)
+    plan = plan_of(5, 2, 3, 40)
+    for call in (lambda: fmpq.fp8_quantize(plain, half(40, 256), *bad), lambda: fmpq.moe_quantize(up, plan, half(5, 256), *bad),
+                 lambda: fmpq.fp8_gemm(plain, *bad, *weights_of(plain), 40),
+                 lambda: fmpq.fp8_quantize_gemm(plain, half(40, 256), *weights_of(plain), *bad),
+                 lambda: fmpq.moe_up(up, plan, *bad, *weights_of(up)),
+                 lambda: fmpq.moe_up(up, plan, u8(2, 40, 128), f32(2, 40), *weights_of(up), *bad),
+                 lambda: fmpq.moe_down(down, plan, *bad, *weights_of(down))):
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_outputs_and_workspaces_on_the_host_are_refused():
+    with pytest.raises(ValueError):
+        fmpq.moe_route(f32(5, 8), 2, ids=torch.zeros(5, 2, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        fmpq.moe_route(f32(5, 8), 2, weights=torch.zeros(5, 2))
+    plain = layer_of(256, 128)
+    W, s = weights_of(plain)
+    for ws in (torch.zeros(64, dtype=torch.uint8), on_gpu(torch.zeros(128, dtype=torch.uint8))[::2]):
+        with pytest.raises(ValueError):
+            fmpq.fp8_gemm(plain, u8(2, 5, 128), f32(2, 8), W, s, 5, workspace=ws)
+        with pytest.raises(ValueError):
+            fmpq.fp8_quantize_gemm(plain, half(5, 256), W, s, workspace=ws)
