@@ -581,6 +581,7 @@ def qoq_gemm_partials(layout: Layout, A_packed, W_packed, M: int, N: int, m0: in
 
 # ---- E4M3 linear layers: a scale for each block of 128 ------------------------------------
 # Every call below also takes stream=: it then runs, and allocates, as under torch.cuda.stream(stream).
+# Tensors are on torch's current GPU, which is the layer's.
 
 def _on_stream(call):
     """Run a call under its `stream` argument (a torch stream or a raw handle), so that its buffers come from
@@ -613,23 +614,36 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _codes_and_scales(codes, scales) -> bool:
+def _device() -> int:
     import torch
-    return (codes.is_cuda and scales.is_cuda and codes.element_size() == 1 and scales.dtype == torch.float32 and
+    return torch._C._cuda_getDevice()
+
+
+def _here(*tensors) -> bool:
+    """Whether the tensors are on the current GPU (a host tensor's device is -1)."""
+    device = _device()
+    for t in tensors:
+        if t.get_device() != device:
+            return False
+    return True
+
+
+def _codes_and_scales(codes, scales) -> bool:
+    return (_here(codes, scales) and codes.element_size() == 1 and _dtype_code(scales.dtype) == 2 and
             codes.is_contiguous() and scales.is_contiguous())
 
 
 def _need_activations(codes, scales, nb: int, rows: int, what: str):
     """Codes [nb, rows, 128] and scales [nb, rows rounded up to 4], or larger."""
     _need(_codes_and_scales(codes, scales) and codes.numel() >= nb * rows * BLOCK and
-          scales.numel() >= nb * ((rows + 3) // 4 * 4), f"{what} must be contiguous bytes and fp32 CUDA tensors, large enough for the rows")
+          scales.numel() >= nb * ((rows + 3) // 4 * 4), f"{what} must be contiguous bytes and fp32 on the current GPU, large enough for the rows")
 
 
 def _rows16(X, what: str, fp32: bool = False) -> int:
     """A 16-bit (fp32: or FP32) CUDA matrix whose rows are contiguous (any row stride). Returns its dtype code."""
     code = _dtype_code(X.dtype)
-    if not (X.is_cuda and X.dim() == 2 and (code < 2 or fp32)):
-        raise ValueError(f"{what} must be a 2-D {'fp32, ' if fp32 else ''}fp16 or bf16 CUDA tensor")
+    if not (X.dim() == 2 and (code < 2 or fp32) and _here(X)):
+        raise ValueError(f"{what} must be a 2-D {'fp32, ' if fp32 else ''}fp16 or bf16 tensor on the current GPU")
     if X.shape[1] > 1 and X.stride(1) != 1:
         raise ValueError(f"{what} must have contiguous rows")
     return code
@@ -746,10 +760,10 @@ def fp8_pack_codes(layer: Fp8Layer, codes, scales):
     import torch
     C = codes if codes.dim() == 3 else codes[None]
     S = scales if scales.dim() == 3 else scales[None]
-    _need(codes.dtype in (torch.float8_e4m3fn, torch.uint8) and codes.is_cuda, "codes must be float8_e4m3fn on the GPU")
+    _need(codes.dtype in (torch.float8_e4m3fn, torch.uint8) and _here(codes), "codes must be float8_e4m3fn on the current GPU")
     _need(C.shape == (layer.experts, layer.N, layer.K), "codes must be [experts, N, K] (or [N, K])")
-    _need(S.shape == (layer.experts, layer.scale_rows, layer.nb) and S.dtype == torch.float32 and S.is_cuda,
-          "scales must be fp32 [experts, scale rows, blocks of K]")
+    _need(S.shape == (layer.experts, layer.scale_rows, layer.nb) and S.dtype == torch.float32 and _here(S),
+          "scales must be fp32 on the current GPU, [experts, scale rows, blocks of K]")
     _need(C.shape[2] <= 1 or C.stride(2) == 1, "codes must have contiguous rows")
     Wp = torch.empty(layer.packed_w_bytes(), dtype=torch.uint8, device=codes.device)
     for e in range(layer.experts):
@@ -790,7 +804,7 @@ def _workspace_of(layer: Fp8Layer, M: int, workspace):
         workspace = layer.workspace(M)
         if workspace is None:
             return None, 0
-    _need(workspace.is_cuda and workspace.is_contiguous(), "workspace must be a contiguous CUDA tensor")
+    _need(_here(workspace) and workspace.is_contiguous(), "workspace must be a contiguous tensor on the current GPU")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -862,24 +876,24 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1
     import torch
     sigmoid = _SCORES.get(score)
     _need(sigmoid is not None, "score must be 'softmax' or 'sigmoid'")
-    _need(logits.is_cuda and logits.dim() == 2, "logits must be a 2-D CUDA tensor")
+    _need(logits.dim() == 2 and _here(logits), "logits must be a 2-D tensor on the current GPU")
     T, E = logits.shape
     _need(E <= 1 or logits.stride(1) == 1, "logits must have contiguous rows")
     b_ptr = None
     if bias is not None:
-        _need(bias.is_cuda and bias.dtype == torch.float32 and bias.shape == (E,) and (E == 1 or bias.stride(0) == 1),
-              "bias must be a contiguous fp32 CUDA tensor [E]")
+        _need(_here(bias) and bias.dtype == torch.float32 and bias.shape == (E,) and (E == 1 or bias.stride(0) == 1),
+              "bias must be a contiguous fp32 tensor [E] on the current GPU")
         b_ptr = bias.data_ptr()
     if ids is None:
         ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
     else:
-        _need(ids.is_cuda and ids.shape == (T, k) and ids.dtype == torch.int32 and ids.is_contiguous(),
-              "ids must be a contiguous int32 CUDA tensor [T, k]")
+        _need(_here(ids) and ids.shape == (T, k) and ids.dtype == torch.int32 and ids.is_contiguous(),
+              "ids must be a contiguous int32 tensor [T, k] on the current GPU")
     if weights is None:
         weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
     else:
-        _need(weights.is_cuda and weights.shape == (T, k) and weights.dtype == torch.float32 and weights.is_contiguous(),
-              "weights must be a contiguous fp32 CUDA tensor [T, k]")
+        _need(_here(weights) and weights.shape == (T, k) and weights.dtype == torch.float32 and weights.is_contiguous(),
+              "weights must be a contiguous fp32 tensor [T, k] on the current GPU")
     _check("moe_route", (_lib or load_library()).moe_route(
         logits.data_ptr(), _dtype_code(logits.dtype), _ld(logits), T, E, k, sigmoid, b_ptr, groups, top_groups, group_top,
         1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(), _on(logits)))
@@ -918,11 +932,11 @@ class MoePlan:
 def moe_plan(ids, experts: int, plan=None) -> MoePlan:
     """Sort the pairs of ids (int32 [T, k]) by expert; ids outside [0, experts) belong to none."""
     import torch
-    _need(ids.is_cuda and ids.dim() == 2 and ids.dtype == torch.int32 and ids.is_contiguous(),
-          "ids must be a contiguous int32 CUDA tensor [T, k]")
+    _need(_here(ids) and ids.dim() == 2 and ids.dtype == torch.int32 and ids.is_contiguous(),
+          "ids must be a contiguous int32 tensor [T, k] on the current GPU")
     T, k = ids.shape
     plan = MoePlan(T, k, experts, ids.device) if plan is None else plan
-    _need((plan.T, plan.k, plan.experts) == (T, k, experts), "the plan was made for other sizes")
+    _need((plan.T, plan.k, plan.experts) == (T, k, experts) and _here(plan.buffer), "the plan was made for other sizes, or on another GPU")
     _check("moe_plan", load_library().moe_plan(_ptr(ids), T, k, experts, _ptr(plan.buffer), _stream(None)))
     return plan
 
@@ -931,7 +945,7 @@ def moe_plan(ids, experts: int, plan=None) -> MoePlan:
 def moe_quantize(layer: Fp8Layer, plan: MoePlan, X, A_packed=None, a_scales=None):
     """Quantize each token of X [T, K] once into its experts' rows."""
     _rows16(X, "X")
-    _need(X.shape == (plan.T, layer.K) and plan.experts == layer.experts, "X must be [T, K], the plan the layer's")
+    _need(X.shape == (plan.T, layer.K) and plan.experts == layer.experts and _here(plan.buffer), "X must be [T, K], the plan the layer's")
     if A_packed is None or a_scales is None:
         A, s = layer.activations(plan.rows, X.device)
         A_packed, a_scales = A if A_packed is None else A_packed, s if a_scales is None else a_scales
@@ -946,7 +960,7 @@ def moe_quantize(layer: Fp8Layer, plan: MoePlan, X, A_packed=None, a_scales=None
 def moe_up(layer: Fp8Layer, plan: MoePlan, A_packed, a_scales, W_packed, w_scales, H_packed=None, h_scales=None):
     """SwiGLU of the gated layer's products, quantized: codes uint8 [F / 128, rows, 128] and scales."""
     import torch
-    _need(layer.gated and plan.experts == layer.experts, "moe_up needs a gated layer and its plan")
+    _need(layer.gated and plan.experts == layer.experts and _here(plan.buffer), "moe_up needs a gated layer and its plan")
     layer.check_weights(W_packed, w_scales)
     layer.check_activations(A_packed, a_scales, plan.rows)
     fb = -(-(layer.N // 2) // BLOCK)
@@ -966,12 +980,12 @@ def moe_down(layer: Fp8Layer, plan: MoePlan, A_packed, a_scales, W_packed, w_sca
     and to round to dtype (fp16 by default). A D that is passed may have 16 bits: each row is then rounded, which halves
     the bytes and costs a rounding a slot."""
     import torch
-    _need(plan.experts == layer.experts and not layer.gated, "moe_down needs a plain layer and its plan")
+    _need(plan.experts == layer.experts and not layer.gated and _here(plan.buffer), "moe_down needs a plain layer and its plan")
     layer.check_weights(W_packed, w_scales)
     layer.check_activations(A_packed, a_scales, plan.rows)
     if weights is not None:
-        _need(weights.is_cuda and weights.dtype == torch.float32 and weights.shape == (plan.T, plan.k) and
-              weights.is_contiguous(), "weights must be contiguous fp32 [T, k]")
+        _need(_here(weights) and weights.dtype == torch.float32 and weights.shape == (plan.T, plan.k) and
+              weights.is_contiguous(), "weights must be contiguous fp32 [T, k] on the current GPU")
     if D is None:
         D = torch.empty((plan.rows, layer.N), dtype=torch.float32, device=A_packed.device)
     _rows16(D, "D", fp32=True)
@@ -990,7 +1004,7 @@ def moe_combine(D, plan: MoePlan, Y=None):
     """Y [T, N]: the sum of D's rows of each token, rounded once; of moe_down's dtype (or of a 16-bit D's)."""
     import torch
     code = _rows16(D, "D", fp32=True)
-    _need(D.shape[0] == plan.rows, "D must be [rows, N]")
+    _need(D.shape[0] == plan.rows and _here(plan.buffer), "D must be [rows, N], the plan on its GPU")
     if Y is None:
         Y = torch.empty((plan.T, D.shape[1]), dtype=plan.dtype if code == 2 else D.dtype, device=D.device)
     y_code = _rows16(Y, "Y")
@@ -1013,9 +1027,9 @@ def moe_experts(up: Fp8Layer, down: Fp8Layer, X, ids, weights, W_up, s_up, W_dow
           "up must be the gated layer [2F, K] and down the plain layer [N, F] of the same experts")
     code = _rows16(X, "X")
     T, K = X.shape
-    _need(ids.is_cuda and ids.dim() == 2 and ids.dtype == torch.int32 and ids.is_contiguous() and ids.shape[0] == T and
-          K == up.K, "ids must be a contiguous int32 CUDA tensor [T, k] for X [T, K]")
-    _need(weights.is_cuda and weights.dtype == torch.float32 and weights.shape == ids.shape and weights.is_contiguous(),
+    _need(_here(ids, weights) and ids.dim() == 2 and ids.dtype == torch.int32 and ids.is_contiguous() and ids.shape[0] == T and
+          K == up.K, "ids must be a contiguous int32 tensor [T, k] for X [T, K], ids and weights on the current GPU")
+    _need(weights.dtype == torch.float32 and weights.shape == ids.shape and weights.is_contiguous(),
           "weights must be contiguous fp32 [T, k]")
     up.check_weights(W_up, s_up)
     down.check_weights(W_down, s_down)

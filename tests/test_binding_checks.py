@@ -9,6 +9,16 @@ from bit_quantized_gemm_fmpq_gb300 import fmpq
 class OnGpu(torch.Tensor):
     is_cuda = True
 
+    def get_device(self):
+        return 0
+
+
+class OnAnother(torch.Tensor):
+    is_cuda = True
+
+    def get_device(self):
+        return 1
+
 
 def on_gpu(t):
     return t.as_subclass(OnGpu)
@@ -52,6 +62,7 @@ def no_library(monkeypatch):
     monkeypatch.setattr(fmpq, "load_library", NoLibrary)
     monkeypatch.setattr(fmpq, "_lib", NoLibrary())
     monkeypatch.setattr(fmpq, "_on", lambda X: 0)
+    monkeypatch.setattr(fmpq, "_device", lambda: 0, raising=False)
     monkeypatch.setattr(fmpq, "_stream", lambda s: 0)
 
 
@@ -202,3 +213,66 @@ def test_outputs_and_workspaces_on_the_host_are_refused():
             fmpq.fp8_gemm(plain, u8(2, 5, 128), f32(2, 8), W, s, 5, workspace=ws)
         with pytest.raises(ValueError):
             fmpq.fp8_quantize_gemm(plain, half(5, 256), W, s, workspace=ws)
+
+
+# ---- tensors of another GPU than the current one ----------------------------------------------
+
+def elsewhere(t):
+    return t.as_subclass(OnAnother)
+
+
+def test_tensors_of_another_gpu_are_refused():
+    plain, down, up = layer_of(256, 128), layer_of(128, 256, 3), layer_of(256, 256, 3, True)
+    plan, ids, w = plan_of(5, 2, 3, 40), on_gpu(torch.zeros(5, 2, dtype=torch.int32)), f32(5, 2)
+    A, a, H, h = u8(2, 40, 128), f32(2, 40), u8(1, 40, 128), f32(1, 40)
+    W, X = weights_of, half(5, 256)
+    far = lambda L: (elsewhere(weights_of(L)[0]), weights_of(L)[1])     # noqa: E731
+    far_X, far_ids, far_w = elsewhere(half(5, 256)), elsewhere(ids), elsewhere(f32(5, 2))
+    codes = on_gpu(torch.zeros(128, 256, dtype=torch.uint8))
+    scales = f32(1, 2)
+    calls = [
+        lambda: fmpq.fp8_pack_weights(plain, elsewhere(half(128, 256))),
+        lambda: fmpq.fp8_pack_codes(plain, elsewhere(codes), scales),
+        lambda: fmpq.fp8_pack_codes(plain, codes, elsewhere(f32(1, 2))),
+        lambda: fmpq.fp8_unpack_weights(plain, *far(plain)),
+        lambda: fmpq.fp8_quantize(plain, far_X, A, a),
+        lambda: fmpq.fp8_quantize(plain, X, elsewhere(u8(2, 40, 128)), a),
+        lambda: fmpq.fp8_gemm(plain, A, a, *far(plain), 5),
+        lambda: fmpq.fp8_gemm(plain, A, elsewhere(f32(2, 40)), *W(plain), 5),
+        lambda: fmpq.fp8_gemm(plain, A, a, *W(plain), 5, Y=elsewhere(half(5, 128))),
+        lambda: fmpq.fp8_gemm(plain, A, a, *W(plain), 5, workspace=elsewhere(u8(64))),
+        lambda: fmpq.fp8_quantize_gemm(plain, far_X, *W(plain)),
+        lambda: fmpq.fp8_quantize_gemm(plain, X, *far(plain)),
+        lambda: fmpq.moe_route(elsewhere(f32(5, 8)), 2),
+        lambda: fmpq.moe_route(f32(5, 8), 2, bias=elsewhere(f32(8))),
+        lambda: fmpq.moe_route(f32(5, 8), 2, ids=far_ids),
+        lambda: fmpq.moe_route(f32(5, 8), 2, weights=far_w),
+        lambda: fmpq.moe_plan(far_ids, 3, plan),
+        lambda: fmpq.moe_quantize(up, plan, far_X, A, a),
+        lambda: fmpq.moe_up(up, plan, A, a, *far(up)),
+        lambda: fmpq.moe_down(down, plan, H, h, *W(down), weights=far_w),
+        lambda: fmpq.moe_down(down, plan, elsewhere(u8(1, 40, 128)), h, *W(down)),
+        lambda: fmpq.moe_combine(elsewhere(half(40, 256)), plan),
+        lambda: fmpq.moe_combine(half(40, 256), plan, Y=elsewhere(half(5, 256))),
+        lambda: fmpq.moe_experts(up, down, far_X, ids, w, *W(up), *W(down)),
+        lambda: fmpq.moe_experts(up, down, X, far_ids, w, *W(up), *W(down)),
+        lambda: fmpq.moe_experts(up, down, X, ids, far_w, *W(up), *W(down)),
+        lambda: fmpq.moe_experts(up, down, X, ids, w, *far(up), *W(down)),
+    ]
+    for i, call in enumerate(calls):
+        with pytest.raises(ValueError):
+            call()
+            raise AssertionError(f"call {i} was not refused")
+
+
+def test_a_plan_of_another_gpu_is_refused():
+    plan = plan_of(5, 2, 3, 40)
+    plan.buffer = elsewhere(plan.buffer)
+    up, down = layer_of(256, 256, 3, True), layer_of(128, 256, 3)
+    for call in (lambda: fmpq.moe_quantize(up, plan, half(5, 256), u8(2, 40, 128), f32(2, 40)),
+                 lambda: fmpq.moe_up(up, plan, u8(2, 40, 128), f32(2, 40), *weights_of(up)),
+                 lambda: fmpq.moe_down(down, plan, u8(1, 40, 128), f32(1, 40), *weights_of(down)),
+                 lambda: fmpq.moe_plan(on_gpu(torch.zeros(5, 2, dtype=torch.int32)), 3, plan),
+                 lambda: fmpq.moe_combine(half(40, 256), plan)):
+        with pytest.raises(ValueError):
+            call()
