@@ -52,12 +52,15 @@ struct Rules {
 
 // Two keys computed in FP32 may be closer than their errors. A key's is at most 8e-7 max(1, |key|): the
 // fast exponential and quotient leave 5e-7 of a score (at most 1), adding the bias rounds once. Packing
-// (pack_items) takes the last 4 bits, 1.8e-6 of a key at most.
-__device__ __forceinline__ bool close_call(float hi, float lo, float step) {
-    return hi - lo <= step * fmaxf(1.0f, fmaxf(fabsf(hi), fabsf(lo)));
+// (pack_items) takes the last 4 bits, 1.8e-6 of a key at most. Sums of two keys err by the keys' size, which may be far
+// above the sum's: `size` is the largest key's. (Sums past FP32's range, whose difference is not a number, are close.)
+__device__ __forceinline__ bool close_call(float hi, float lo, float step, float size = 1.0f) {
+    return !(hi - lo > step * fmaxf(fmaxf(1.0f, size), fmaxf(fabsf(hi), fabsf(lo))));
 }
+__device__ __forceinline__ float size_of(float key) { return key > kNone ? fabsf(key) : 0.0f; }
+__device__ __forceinline__ float size_of(double) { return 0.0f; }
 constexpr float kStep = 3.8146973e-6f;   // 2^-18: two packed keys, or two sums of two keys
-__device__ __forceinline__ bool close_call(double, double, float) { return false; }
+__device__ __forceinline__ bool close_call(double, double, float, float = 1.0f) { return false; }
 
 // Whether this lane's group is among the best, from the two best keys of each lane; b2 becomes the
 // group's second best. Groups are runs of `width` lanes.
@@ -80,7 +83,8 @@ __device__ __forceinline__ bool keep_group(V b1, V& b2, const Rules& r, int widt
     const bool keep = place < r.top_groups && value > V(kNone);
     if (check && r.top_groups < r.groups) {
         const V worst = -warp_max(keep ? -value : V(kNone)), next = warp_max(keep ? V(kNone) : value);
-        close = next > V(kNone) && close_call(worst, next, kStep);
+        const float size = warp_max(fmaxf(size_of(b1), r.group_top == 2 ? size_of(b2) : 0.0f));
+        close = next > V(kNone) && close_call(worst, next, kStep, size);
     }
     return keep;
 }
@@ -106,6 +110,7 @@ __device__ __forceinline__ bool keep_best_groups(V (&key)[NI], const Rules& r, i
         return close;
     }
     V mine = V(kNone);   // lane g: the value of group g
+    float size = 0.0f;
     for (int g = 0; g < r.groups; ++g) {
         const int lo = g * per - lane * NI, hi = lo + per;
         V b1 = V(kNone), b2 = V(kNone);
@@ -118,11 +123,13 @@ __device__ __forceinline__ bool keep_best_groups(V (&key)[NI], const Rules& r, i
             }
         const V m1 = warp_max(b1);
         V value = m1;
+        size = fmaxf(size, size_of(m1));
         if (r.group_top == 2) {
             const unsigned who = __ballot_sync(kAll, b1 == m1);
             if (lane == __ffs(who) - 1) b1 = b2;
             const V m2 = warp_max(b1);
             if (m2 > V(kNone)) value += m2;
+            size = fmaxf(size, size_of(m2));
         }
         if (lane == g) mine = value;
     }
@@ -139,7 +146,7 @@ __device__ __forceinline__ bool keep_best_groups(V (&key)[NI], const Rules& r, i
     bool close = false;
     if (check) {
         const V next = warp_max(mine);
-        close = next > V(kNone) && close_call(last, next, kStep);
+        close = next > V(kNone) && close_call(last, next, kStep, size);
     }
 #pragma unroll
     for (int i = 0; i < NI; ++i) {

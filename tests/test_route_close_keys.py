@@ -1,5 +1,6 @@
-"""Routing where keys are closer than FP32 can tell: rows of ties, the last slot's border. Ids are exact, weights to
-the bound of tests/test_moe.py (an exponential, a sum, quotients and the scale, the exponential's argument)."""
+"""Routing where keys are closer than FP32 can tell: rows of ties, the last slot's border, sums of large keys
+that cancel. Ids are exact, weights to the bound of tests/test_moe.py (an exponential, a sum, quotients and the scale,
+the exponential's argument)."""
 import numpy as np
 import pytest
 
@@ -59,3 +60,32 @@ def test_border_of_the_last_of_32_slots(fmpq_mod, E, score):  # noqa: F811
         x[t, lo], x[t, hi] = (1.0, above(1.0)) if t % 2 == 0 else (above(1.0), 1.0)
     check_route(fmpq_mod, x.cuda(), 32, score=score)
     check_route(fmpq_mod, x.cuda(), 32, score=score, bias=torch.zeros(E).cuda())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,groups", [(64, 8), (256, 32), (256, 4), (60, 5), (96, 6)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size,spread", [(1000.0, 1.0), (3e7, 1.0), (1000.0, 1e-4), (1e5, 1e-2), (1e5, 1.0)])
+def test_groups_whose_best_keys_cancel(fmpq_mod, E, groups, score, size, spread):  # noqa: F811
+    """A bias of +size beside one of -size: a group's sum is the two scores', about or far below a step of FP32 at
+    `size` apart from the next group's."""
+    import torch
+    per = E // groups
+    g = torch.Generator().manual_seed(E)
+    x = torch.full((12, E), float("-inf"))
+    x[:, 0::per] = torch.randn(12, groups, generator=g) * spread
+    x[:, 1::per] = torch.randn(12, groups, generator=g) * spread
+    bias = torch.zeros(E)
+    bias[0::per], bias[1::per] = size, -size
+    check_route(fmpq_mod, x.cuda(), 3, score=score, bias=bias.cuda(), groups=groups, top_groups=2, group_top=2)
+
+
+@pytest.mark.gpu
+def test_group_sums_past_the_range_of_fp32(fmpq_mod):  # noqa: F811
+    import torch
+    x = torch.zeros(2, 64)
+    bias = torch.full((64,), -1.0)
+    bias[0:8], bias[16:24], bias[40:48] = 2e38, 3e38, 2.5e38
+    for score in ("softmax", "sigmoid"):
+        check_route(fmpq_mod, x.cuda(), 6, score=score, bias=bias.cuda(), groups=8, top_groups=1, group_top=2)
+        check_route(fmpq_mod, x[:, :60].cuda(), 6, score=score, bias=bias[:60].cuda(), groups=5, top_groups=1, group_top=2)
