@@ -434,7 +434,16 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs p, const Rul
             else weight = (x == top ? 1.0f : expf(x - top)) / total;
         }
         if (p.renormalize) {
-            const float sum = warp_sum(weight);
+            float sum = warp_sum(weight);
+            if (sum < 1e-30f) {
+                // scores about or below FP32's smallest: both kinds are e^x times the same factor there, so the largest
+                // is taken out of it (scores that are 0 in 64 bits too, below e^-745, stay 0)
+                const float best = warp_max(id >= 0 ? x : kNone), depth = (p.sigmoid ? 0.0f : top) - best;
+                if (depth < 745.0f) {
+                    weight = id >= 0 ? expf(x - best) : 0.0f;
+                    sum = warp_sum(weight);
+                }
+            }
             weight = sum > 0.0f ? weight / sum : 0.0f;
         }
         if (lane < p.k) {

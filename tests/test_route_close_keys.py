@@ -1,6 +1,6 @@
 """Routing where keys are closer than FP32 can tell: rows of ties, the last slot's border, sums of large keys
-that cancel. Ids are exact, weights to the bound of tests/test_moe.py (an exponential, a sum, quotients and the scale,
-the exponential's argument)."""
+that cancel; and weights of scores below FP32's range. Ids are exact, weights to the bound of tests/test_moe.py (an
+exponential, a sum, quotients and the scale, the exponential's argument)."""
 import numpy as np
 import pytest
 
@@ -89,3 +89,28 @@ def test_group_sums_past_the_range_of_fp32(fmpq_mod):  # noqa: F811
     for score in ("softmax", "sigmoid"):
         check_route(fmpq_mod, x.cuda(), 6, score=score, bias=bias.cuda(), groups=8, top_groups=1, group_top=2)
         check_route(fmpq_mod, x[:, :60].cuda(), 6, score=score, bias=bias[:60].cuda(), groups=5, top_groups=1, group_top=2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E", [8, 60, 256])
+def test_renormalized_weights_of_tiny_scores(fmpq_mod, E):  # noqa: F811
+    """Scores below FP32's range still have a sum in 64 bits, so their weights are their ratios."""
+    import torch
+    g = torch.Generator().manual_seed(E)
+    lowest = torch.full((2, E), torch.finfo(torch.float32).min)     # masked by the lowest value: a score of 0
+    lowest[0, 0] = 1.0
+    bias = torch.linspace(0, 1, E)
+    x = torch.randn(3, E, generator=g) - 100.0      # sigmoid: about 1e-44
+    x[1] -= 300.0
+    x[2] = -87.5 + torch.rand(E, generator=g)       # the subnormal border
+    for logits in (x, lowest):
+        check_route(fmpq_mod, logits.cuda(), 4, score="sigmoid", renormalize=True)
+        check_route(fmpq_mod, logits.cuda(), 4, score="sigmoid", renormalize=True, bias=bias.cuda(), scale=2.5)
+    # softmax: the biases keep the expert out that holds nearly all of the scores
+    bias[0] = -5.0
+    y = torch.randn(2, E, generator=g)
+    y[0, 0], y[1, 0] = 150.0, 500.0
+    infinite = torch.randn(1, E, generator=g)
+    infinite[0, 0] = float("inf")
+    for logits in (y, lowest, infinite):
+        check_route(fmpq_mod, logits.cuda(), 4, renormalize=True, bias=bias.cuda())
