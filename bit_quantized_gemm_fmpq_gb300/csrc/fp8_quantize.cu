@@ -96,12 +96,13 @@ __global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ X, 
 #pragma unroll
                 for (int c = 0; c < 8; ++c) v[c] = k0 + c < K ? load_as_float(x + i * ldx + c) : 0.0f;
             }
-            float amax = 0.0f;
+            // as bits, NaN is above every number: a block with one gets the scale NaN
+            uint32_t amax = 0u;
 #pragma unroll
-            for (int c = 0; c < 8; ++c) amax = fmaxf(amax, fabsf(v[c]));
+            for (int c = 0; c < 8; ++c) amax = max(amax, __float_as_uint(fabsf(v[c])));
 #pragma unroll
-            for (int d = 8; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-            const float s = __fdiv_rn(amax, kQMax);
+            for (int d = 8; d > 0; d >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+            const float s = __fdiv_rn(__uint_as_float(amax), kQMax);
             const uint2 code = codes_of(v, s);
             if (b >= nb) continue;
             for (int j = 0; j < slots; ++j) {
@@ -147,7 +148,11 @@ __global__ void __launch_bounds__(256) pack_weights_kernel(const T* __restrict__
         const bool pad = n < 0 && (gated ? sr < fb : (sr & 1) == 0);
         if (!mine && !pad) continue;
         float q = 0.0f;
-        if (mine && k < K && s > 0.0f) q = __fdiv_rn(load_as_float(W + static_cast<int64_t>(n) * ldw + k), s);
+        if (mine && k < K) {
+            const float w = load_as_float(W + static_cast<int64_t>(n) * ldw + k);
+            if (s > 0.0f) q = __fdiv_rn(w, s);
+            else if (isnan(w)) q = w;   // the block's other weights are 0, or NaN too
+        }
         const int r = p & 127, kk = threadIdx.x & 127;
         Wp[(static_cast<int64_t>(t) * nb + b) * kTileBytes + r * 128 + (((kk >> 4) ^ (r & 7)) << 4) + (kk & 15)] =
             static_cast<uint8_t>(e4m3x2(q, 0.0f) & 0xFFu);

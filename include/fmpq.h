@@ -435,7 +435,9 @@ FMPQ_API fmpq_status fmpq_device_status(const fmpq_layout* layout, int32_t* code
  *   weights      per 128 x 128 block, the same rule; or an E4M3 checkpoint's own codes and scales
  *   product      Y[m][n] = sum_b a_scales[b][m] * w_scales[n / 128][b] * P[m][n][b], P the FP32
  *                dot products of the block's codes on the tensor cores; FP32 sums; Y rounded once
- * Any K, N and M <= 2^24; inputs finite. Divisions and conversions round to nearest even.
+ * Any K, N and M <= 2^24. Divisions and conversions round to nearest even. A NaN makes every output
+ * that it takes part in NaN (max|x| of a token's block with one is NaN; a NaN weight keeps the NaN
+ * code), and so does an infinity, whose scale is infinite.
  * These calls are forward only, like the rest of the library.
  * ====================================================================================== */
 
