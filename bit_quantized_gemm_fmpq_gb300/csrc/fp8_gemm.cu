@@ -359,7 +359,7 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
             // the four quarters' maximum of a token to the peer
             const int col = c0 + lane;
             if (q == 0 && lane < own) {
-                const float m = fmaxf(fmaxf(s.amax[0][col], s.amax[1][col]), fmaxf(s.amax[2][col], s.amax[3][col]));
+                const float m = max_magnitude(max_magnitude(s.amax[0][col], s.amax[1][col]), max_magnitude(s.amax[2][col], s.amax[3][col]));
                 s.hscale[col] = m;
                 asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dev::mapa(&s.amax_peer[par][col], rank ^ 1u)), "f"(m) : "memory");
             }
@@ -368,7 +368,7 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
             if (ok) ok = dev::mbar_wait_cluster(&s.amax_full[par], (nu >> 1) & 1);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (q == 0 && lane < own) {
-                const float sc = __fdiv_rn(fmaxf(s.hscale[col], s.amax_peer[par][col]), 448.0f);
+                const float sc = __fdiv_rn(max_magnitude(s.hscale[col], s.amax_peer[par][col]), 448.0f);
                 s.hscale[col] = sc;
                 if (ok && rank == 0 && col < t.n) p.h_scales[t.pair * p.sstride + t.row0 + col] = sc;
             }

@@ -175,6 +175,10 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi, bool bf16) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
+// The larger of two magnitudes, compared as bits: NaN is above every number, so a block's scale does not lose it.
+__device__ __forceinline__ float max_magnitude(float a, float b) {
+    return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
+}
 // silu(g) * u = g u / (1 + e^-g): the exponential and the quotient to 2 of their last places, the value and the scale
 // made of it within 4 steps of 2^-23 for every g. The E4M3 codes that follow change where the value crosses the middle
 // between two codes, so the hardware's exponential, whose error grows with |g| (15 steps at 49), is not used: it saves

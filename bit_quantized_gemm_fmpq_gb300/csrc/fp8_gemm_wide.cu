@@ -368,15 +368,15 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
                 for (int i = 0; i < 8; ++i) {
                     float2& g = acc[c][i];
                     g = make_float2(silu_times(g.x, acc[c][i + 8].x), silu_times(g.y, acc[c][i + 8].y));
-                    top = fmaxf(top, fmaxf(fabsf(g.x), fabsf(g.y)));
+                    top = max_magnitude(top, max_magnitude(fabsf(g.x), fabsf(g.y)));
                 }
             // the block's other channels are with the same lane of the other three column warps; a warp
             // two units ahead has seen the others arrive for the unit between, after their reads
             const int par = nu & 1;
             s.amax[par][h][local] = top;
             dev::named_bar_sync(2 + q, 128);
-            const float scale = __fdiv_rn(fmaxf(fmaxf(s.amax[par][0][local], s.amax[par][1][local]),
-                                                fmaxf(s.amax[par][2][local], s.amax[par][3][local])), 448.0f);
+            const float scale = __fdiv_rn(max_magnitude(max_magnitude(s.amax[par][0][local], s.amax[par][1][local]),
+                                                        max_magnitude(s.amax[par][2][local], s.amax[par][3][local])), 448.0f);
             if (mine) {
                 uint8_t* out = p.H + (static_cast<int64_t>(pair) * p.rows + row) * 128;
 #pragma unroll
