@@ -856,8 +856,12 @@ def fp8_quantize_gemm(layer: Fp8Layer, X, W_packed, w_scales, A_packed=None, a_s
 
 
 def fp8_device_status(layer: Fp8Layer, clear: bool = True) -> int:
+    """The layer's status word (0, or 5 after a wait that gave up). After an error the layer's own workspaces are
+    dropped, new ones being zeroed; one that the caller passes has to be zeroed by the caller."""
     code = ctypes.c_int32(0)
     _check("fp8_device_status", layer._lib.fp8_device_status(layer.handle, ctypes.byref(code), int(clear)))
+    if code.value != 0:
+        layer._workspaces = {}
     return int(code.value)
 
 

@@ -276,3 +276,21 @@ def test_a_plan_of_another_gpu_is_refused():
                  lambda: fmpq.moe_combine(half(40, 256), plan)):
         with pytest.raises(ValueError):
             call()
+
+
+# ---- after a timeout --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("code,kept", [(0, True), (5, False)])
+@pytest.mark.parametrize("clear", [False, True])
+def test_workspaces_are_not_reused_after_an_error(code, kept, clear):
+    """A product that gave up leaves counters in its workspace that the next one would take for its own."""
+    class Library:
+        def fp8_device_status(self, handle, status, do_clear):
+            status._obj.value = code
+            return 0
+
+    layer = layer_of(8192, 256)
+    layer._lib = Library()
+    layer._workspaces = {(64, 0): u8(64)}
+    assert fmpq.fp8_device_status(layer, clear) == code
+    assert bool(layer._workspaces) == kept
