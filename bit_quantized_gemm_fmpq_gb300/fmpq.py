@@ -614,18 +614,21 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
+_current_device = None
+
+
 def _device() -> int:
-    import torch
-    return torch._C._cuda_getDevice()
+    global _current_device
+    if _current_device is None:
+        import torch
+        _current_device = torch._C._cuda_getDevice
+    return _current_device()
 
 
-def _here(*tensors) -> bool:
+def _here(a, b=None) -> bool:
     """Whether the tensors are on the current GPU (a host tensor's device is -1)."""
     device = _device()
-    for t in tensors:
-        if t.get_device() != device:
-            return False
-    return True
+    return a.get_device() == device and (b is None or b.get_device() == device)
 
 
 def _codes_and_scales(codes, scales) -> bool:
@@ -664,7 +667,7 @@ def _ld(X) -> int:
 def _on(X) -> int:
     """torch's current stream for X's device."""
     import torch
-    return torch._C._cuda_getCurrentRawStream(X.device.index)
+    return torch._C._cuda_getCurrentRawStream(X.get_device())
 
 
 class Fp8Layer:
@@ -802,8 +805,7 @@ def _workspace_of(layer: Fp8Layer, M: int, workspace):
     """The pointer and the bytes of the workspace passed, or of the layer's own."""
     if workspace is None:
         workspace = layer.workspace(M)
-        if workspace is None:
-            return None, 0
+        return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     _need(_here(workspace) and workspace.is_contiguous(), "workspace must be a contiguous tensor on the current GPU")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
