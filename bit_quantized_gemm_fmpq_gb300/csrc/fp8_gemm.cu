@@ -22,7 +22,7 @@
 //     programmatic dependent); token codes come four blocks a box, one copy per block being what the
 //     copy engine and the issuing warp keep up with.
 // Measured (quantizer included): one token of 8192 x 8192 21.8 us, 67.1 MB = 3.1 TB/s (a stream this short does
-// not reach the copy rate); 64 tokens through 8 of 128 experts of 4096 x 1024, 1.59 GB in 270 us = 5.9 TB/s, 87% of
+// not reach the copy rate); 64 tokens through 8 of 128 experts of 4096 x 1024, 1.59 GB in 272 us = 5.8 TB/s, 86% of
 // the measured copy rate.
 //
 // Warp roles (384 threads, one CTA per SM, pairs persistent over tiles):
@@ -31,6 +31,8 @@
 //   warp 2      scaler; also allocates and frees TMEM
 //   warp 3      token producer: codes and scales of four blocks at a time
 //   warps 4-11  epilogue: TMEM lane quarter warp % 4, half of the tile's tokens (or of the blocks) each
+#include <type_traits>
+
 #include "fp8_gemm.cuh"
 
 namespace fmpq {
@@ -192,7 +194,7 @@ __device__ __forceinline__ void mma_issuer(const Params& p, Smem& s, uint32_t ra
 template <bool kGated>
 __device__ __forceinline__ void scaler(const Params& p, Smem& s, uint32_t rank, int lane,
                                        volatile int* abort_flag) {
-    constexpr int kPer = kTokens / 32;   // tokens a lane: 2 or 4
+    constexpr int kPer = kTokens / 32;   // tokens a lane
     const int units = unit_count<kTokens>(p, s.tables);
     uint32_t v = 0, ch = 0;
     bool ok = true;
@@ -387,7 +389,7 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
             ++nu;
         } else {
             const int n = 256 * t.pair + 128 * static_cast<int>(rank) + 32 * q + lane;
-            auto store = [&]() {
+            auto store = [&](auto f32) {   // (FP32 outputs are the experts', whose K is not split)
                 int64_t at = (t.row0 + c0) * p.ldy + n;
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
@@ -395,14 +397,16 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
                     const float w = __shfl_sync(0xFFFFFFFFu, weight, i);
                     if (ok && n < p.N) {
                         const float f = ((i & 1) ? acc[i >> 1].y : acc[i >> 1].x) * w;
-                        if (p.f32) static_cast<float*>(p.Y)[at] = f;
+                        if constexpr (f32.value) static_cast<float*>(p.Y)[at] = f;
                         else static_cast<uint16_t*>(p.Y)[at] = p.bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(f)) : __half_as_ushort(__float2half_rn(f));
                     }
                     at += p.ldy;
                 }
             };
-            if (p.splits == 1) {
-                store();
+            if (p.splits == 1 && p.f32) {
+                store(std::true_type{});
+            } else if (p.splits == 1) {
+                store(std::false_type{});
             } else {
                 // publish this split's sums; the last split to arrive adds all of them in split order
                 auto slot_of = [&](int sp) {
@@ -442,7 +446,7 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
                                 acc[2 * i + 1].y += f[i].w;
                             }
                     }
-                    store();
+                    store(std::false_type{});
                 }
             }
         }
@@ -522,9 +526,9 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Which kernel, from the rounds of tiles over the resident pairs of CTAs. A round of 256-token tiles takes 1.2
 // to 1.4 times as long as one of 64-token tiles, so these are taken while they need less than 1.5 times the
-// rounds. Measured, quantizer included: 128 tokens of 8192 x 8192 (one round each) 27.2 against 32.3 us, 256 tokens (two
-// against one) 46.3 against 33.2; 16 experts of 4096 x 2048 with 48 tokens each (4 rounds each) 109 against
-// 115 us, with 96 (7 against 4) 168 against 123; 10 of 2012 x 1404 with 96 (3 against 2) 82 against 54.
+// rounds. Measured, quantizer included: 128 tokens of 8192 x 8192 (one round each) 27.6 against 32.6 us, 256 tokens (two
+// against one) 46.9 against 33.7; all of a routed feed-forward, 16 experts of 4096 x 2048 with 48 tokens each (4 rounds
+// each) 111 against 120 us, with 96 (7 against 4) 170 against 131; 10 of 2012 x 1404 with 96 (3 against 2) 86 against 62.
 // 128-token tiles, tried between the two, were slower than the better of them everywhere, and the last few tokens of an
 // expert in a second launch of small tiles gained or lost 2%. Experts: their mean load, and a sixth more for its
 // spread.
