@@ -201,7 +201,7 @@ cudaError_t launch_pairs(void (*fn)(P...), int grid, int threads, size_t smem, b
     return launch_after(fn, dim3(static_cast<unsigned>(grid)), threads, smem, pdl, stream, args...);
 }
 
-// More than this many tokens a tile go to the kernel with the tokens on the tensor core's M side.
+// The kernel for many tokens, with the tokens on the tensor core's M side (few_tokens chooses).
 cudaError_t launch_fp8_wide(const fp8_layer& L, const fp8::Params& p, const float* a_scales, int64_t tiles, bool pdl,
                             cudaStream_t stream);
 // Pairs of CTAs that are resident at once (one CTA per SM).

@@ -12,7 +12,8 @@
 // of the epilogue bounds it, not the tensor pipe or the copies. Tried and no faster: single-CTA MMAs with the weights
 // multicast to both CTAs, 8 warps of 128 sums, 16-column loads, the sums kept as packed pairs, 2 blocks a loop iteration
 // (it spills), waits with a time hint. Factors by chunks of 8 blocks, not 2: 0.83 to 0.75 ms; shared memory reached
-// without generic addresses: 0.73 to 0.68; 5 operand stages cost nothing against 6, 3 cost 2%.
+// without generic addresses: 0.73 to 0.68; 5 operand stages cost nothing against 6, 3 cost 2%. The compiler spills 76
+// bytes a thread in either form (96 registers at launch, before the roles take their shares).
 //
 // Warp roles (640 threads, one CTA per SM, pairs persistent over tiles):
 //   warp 0      producer: token codes and weight block, token scales (a chunk of blocks at a time)

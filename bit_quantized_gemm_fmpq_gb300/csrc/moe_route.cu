@@ -307,7 +307,7 @@ __device__ __forceinline__ void load_logits(const T* row, int E, int lane, float
 // reduction and one ballot). Keys use the fast exponential; a chosen expert's weight is computed
 // again, accurately, by the lane that keeps it.
 // Its instructions bound it, not its bytes (16384 x 256 FP32 logits: 16.8 MB are 2.5 us at the copy rate). Measured
-// there with sigmoid keys, biases, the best 4 of 8 groups and k = 8: 25 us, about 990 warp instructions a token;
+// there with sigmoid keys, biases, the best 4 of 8 groups and k = 8: 25 us, about 1020 warp instructions a token;
 // 4099 x 60 of bf16, softmax, k = 4: 6.2 us; one token: 4.2 us, most of it the launch.
 template <typename T, int NI, bool kVec>
 __global__ void __launch_bounds__(128) route_kernel(const RouteArgs p, const Rules r) {
@@ -588,8 +588,8 @@ __device__ __forceinline__ void load8(const T* d, float (&v)[8]) {
 }
 
 // Eight columns a thread, the slots in order, FP32 sums, rounded once to T. DRAM bounds it: 4096 tokens of 8 rows of 4096
-// 16-bit values, 302 MB (44.5 us at the copy rate) in 49.7 us. Four rows in flight: one at a time, each waited for its
-// row's number too.
+// FP32 values, 570 MB (84 us at the copy rate) in 83.5 us; of 16-bit values, 302 MB (44.5 us) in 49.7. Four rows in
+// flight: one at a time, each waited for its row's number too.
 template <typename S, typename T, bool kVec>
 __global__ void __launch_bounds__(256) combine_kernel(const S* __restrict__ D, int64_t ldd, const int32_t* __restrict__ row_of,
                                                       int64_t tokens, int k, int N, T* __restrict__ Y, int64_t ldy) {
