@@ -2,6 +2,7 @@
 // validation, layer handles, and kernel launches on the caller's stream.
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 #include <new>
 
 #include "../../include/fmpq.h"
@@ -206,6 +207,68 @@ fmpq_status fp8_quantize_gemm(const fp8_layer* L, const void* X, int32_t dtype, 
     if (need > 0 && !aligned16(workspace)) return FMPQ_ERR_MISALIGNED;
     if (fmpq_status s = fp8_quantize(L, X, dtype, ldx, M, A_packed, a_scales, stream)) return s;
     return gemm_after(L, A_packed, a_scales, W_packed, w_scales, M, Y, dtype, ldy, workspace, workspace_bytes, true, stream);
+}
+
+// ---------------------------------------------------------------- between two blocks
+
+fmpq_status fmpq_block_norm(const fmpq_block_norm_args* args, void* stream) {
+    if (args == nullptr) return FMPQ_ERR_INVALID_ARG;
+    const fmpq_block_norm_args& a = *args;
+    auto flag = [](int32_t v) { return v == 0 || v == 1; };
+    auto param_type = [&](int32_t t) { return t == a.dtype || t == FMPQ_DTYPE_F32; };
+    const bool codes = a.A_packed != nullptr || a.a_scales != nullptr;
+    if (a.X == nullptr || !sixteen_bits(a.dtype) || !param_type(a.param_dtype) || (a.gate != nullptr && !param_type(a.gate_dtype)) ||
+        (a.kind != FMPQ_NORM_RMS && a.kind != FMPQ_NORM_LAYER) || !flag(a.post_norm) || !flag(a.pre_norm) ||
+        !(a.eps > 0.0f) || !std::isfinite(a.eps) || !std::isfinite(a.residual_scale) || !std::isfinite(a.weight_offset) ||
+        (codes && (a.A_packed == nullptr || a.a_scales == nullptr)) || (a.R == nullptr && a.Y == nullptr && !codes) ||
+        ((a.Y != nullptr || codes) != (a.pre_norm != 0)) ||
+        (!a.pre_norm && (a.weight != nullptr || a.bias != nullptr)) ||
+        (!a.post_norm && (a.post_weight != nullptr || a.post_bias != nullptr)))
+        return FMPQ_ERR_INVALID_ARG;
+    if (a.M < 1 || a.M > kMaxRows || a.K < 1 || a.K > FP8_MAX_K || a.ldx < a.K || (a.residual != nullptr && a.ldr < a.K) ||
+        (a.gate != nullptr && (a.gate_tokens < 1 || (a.gate_tokens < a.M && a.ldg < a.K))) ||
+        (a.R != nullptr && a.ldo < a.K) || (a.Y != nullptr && a.ldy < a.K))
+        return FMPQ_ERR_UNSUPPORTED_SHAPE;
+    for (const void* p : {a.X, a.residual, static_cast<const void*>(a.R), static_cast<const void*>(a.Y)})
+        if (!element_aligned(p, a.dtype)) return FMPQ_ERR_MISALIGNED;
+    for (const void* p : {a.post_weight, a.post_bias, a.weight, a.bias})
+        if (!element_aligned(p, a.param_dtype)) return FMPQ_ERR_MISALIGNED;
+    if (!element_aligned(a.gate, a.gate_dtype) || !all_aligned16(a.A_packed, a.a_scales)) return FMPQ_ERR_MISALIGNED;
+    int dev = -1, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return FMPQ_ERR_CUDA;
+    fmpq::BlockNormArgs p{};
+    p.X = a.X;
+    p.ldx = a.ldx;
+    p.residual = a.residual;
+    p.ldr = a.residual != nullptr ? a.ldr : 0;
+    p.gate = a.gate;
+    p.gate_tokens = a.gate_tokens;
+    p.ldg = a.gate != nullptr && a.gate_tokens < a.M ? a.ldg : 0;
+    p.post_weight = a.post_weight;
+    p.post_bias = a.post_bias;
+    p.weight = a.weight;
+    p.bias = a.bias;
+    p.R = a.R;
+    p.ldo = a.R != nullptr ? a.ldo : 0;
+    p.Y = a.Y;
+    p.ldy = a.Y != nullptr ? a.ldy : 0;
+    p.A = static_cast<uint8_t*>(a.A_packed);
+    p.a_scales = static_cast<float*>(a.a_scales);
+    p.M = a.M;
+    p.sstride = fmpq::scale_stride(a.M);
+    p.K = a.K;
+    p.nb = (a.K + 127) / 128;
+    p.dtype = a.dtype;
+    p.layer_norm = a.kind == FMPQ_NORM_LAYER;
+    p.post_norm = a.post_norm;
+    p.pre_norm = a.pre_norm;
+    p.param_f32 = a.param_dtype == FMPQ_DTYPE_F32;
+    p.gate_f32 = a.gate_dtype == FMPQ_DTYPE_F32;
+    p.eps = a.eps;
+    p.residual_scale = a.residual_scale;
+    p.weight_offset = a.weight_offset;
+    return launched(fmpq::launch_block_norm(p, sms, st(stream)));
 }
 
 // ---------------------------------------------------------------- routing and experts

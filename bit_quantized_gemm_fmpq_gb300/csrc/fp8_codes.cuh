@@ -1,0 +1,47 @@
+// 16-bit values to floats, and floats to E4M3 codes: what the kernels that quantize share.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace fmpq {
+namespace {
+
+constexpr float kQMax = 448.0f;   // the largest E4M3 value
+
+__device__ __forceinline__ float load_as_float(const __half* p) { return __half2float(*p); }
+__device__ __forceinline__ float load_as_float(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float2 unpack2(uint32_t v, const __half*) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+__device__ __forceinline__ float2 unpack2(uint32_t v, const __nv_bfloat16*) {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+// two values to two E4M3 bytes (lo in bits 0-7), to nearest, at most +-448
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// The codes of eight values, e4m3(fl32(v / s)). Products with s's reciprocal, made 2^-21 smaller and larger,
+// enclose the quotient (the reciprocal is good to 2^-23, each product rounds by 2^-24): where both round to the same
+// code it is the quotient's, and elsewhere (one value in 2^17) the division decides.
+__device__ __forceinline__ uint2 codes_of(const float (&v)[8], float s) {
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    const float lo = inv * (1.0f - 4.76837158e-7f), hi = inv * (1.0f + 4.76837158e-7f);
+    uint2 code, other;
+    code.x = e4m3x2(v[0] * lo, v[1] * lo) | (e4m3x2(v[2] * lo, v[3] * lo) << 16);
+    code.y = e4m3x2(v[4] * lo, v[5] * lo) | (e4m3x2(v[6] * lo, v[7] * lo) << 16);
+    other.x = e4m3x2(v[0] * hi, v[1] * hi) | (e4m3x2(v[2] * hi, v[3] * hi) << 16);
+    other.y = e4m3x2(v[4] * hi, v[5] * hi) | (e4m3x2(v[6] * hi, v[7] * hi) << 16);
+    if (s >= 1.17549435e-38f && s <= 1e37f && code.x == other.x && code.y == other.y) return code;
+    if (!(s > 0.0f)) return make_uint2(0u, 0u);
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(v[i], s);
+    return make_uint2(e4m3x2(q[0], q[1]) | (e4m3x2(q[2], q[3]) << 16), e4m3x2(q[4], q[5]) | (e4m3x2(q[6], q[7]) << 16));
+}
+
+}  // namespace
+}  // namespace fmpq

@@ -107,6 +107,19 @@ cudaError_t launch_fp8_gemm(const fp8_layer& L, const Fp8GemmArgs& a, cudaStream
 // Workspace of a dense product of M rows (0: none needed), zero before its first use.
 size_t fp8_gemm_workspace(const fp8_layer& L, int64_t M);
 
+// The norms between two blocks (block_norm.cu); a missing tensor is nullptr with leading dimension 0.
+struct BlockNormArgs {
+    const void *X, *residual, *gate, *post_weight, *post_bias, *weight, *bias;
+    void *R, *Y;
+    uint8_t* A;
+    float* a_scales;
+    int64_t ldx, ldr, ldg, ldo, ldy, M, gate_tokens, sstride;
+    int K, nb, dtype;
+    int layer_norm, post_norm, pre_norm, param_f32, gate_f32;
+    float eps, residual_scale, weight_offset;
+};
+cudaError_t launch_block_norm(const BlockNormArgs& p, int num_sms, cudaStream_t stream);
+
 struct RouteArgs {
     const void* logits;
     int dtype;

@@ -12,6 +12,7 @@ import ctypes
 import functools
 import os
 import threading
+from typing import NamedTuple
 
 import numpy as np
 
@@ -81,6 +82,7 @@ SIGNATURES = {
     "fp8_gemm_workspace_bytes": (_SZ, [_P, _I64]),
     "fp8_gemm": (_I32, [_P, _P, _P, _P, _P, _I64, _P, _I32, _I64, _P, _SZ, _P]),
     "fp8_quantize_gemm": (_I32, [_P, _P, _I32, _I64, _I64, _P, _P, _P, _P, _P, _I64, _P, _SZ, _P]),
+    "fmpq_block_norm": (_I32, [_P, _P]),
     "moe_route": (_I32, [_P, _I32, _I64, _I64, _I32, _I32, _I32, _P, _I32, _I32, _I32, _I32, ctypes.c_float, _P, _P, _P]),
     "moe_rows": (_I64, [_I64, _I32, _I32]),
     "moe_plan_bytes": (_SZ, [_I64, _I32, _I32]),
@@ -865,6 +867,136 @@ def fp8_device_status(layer: Fp8Layer, clear: bool = True) -> int:
     if code.value != 0:
         layer._workspaces = {}
     return int(code.value)
+
+
+# ---- between two blocks: norms, gate, residual sum, quantizer -----------------------------
+
+class BlockNormArgs(ctypes.Structure):
+    """fmpq_block_norm_args of include/fmpq.h."""
+    _fields_ = [("X", _P), ("ldx", _I64), ("residual", _P), ("ldr", _I64), ("gate", _P), ("ldg", _I64), ("gate_tokens", _I64),
+                ("post_weight", _P), ("post_bias", _P), ("weight", _P), ("bias", _P), ("R", _P), ("ldo", _I64), ("Y", _P),
+                ("ldy", _I64), ("A_packed", _P), ("a_scales", _P), ("M", _I64), ("K", _I32), ("dtype", _I32),
+                ("param_dtype", _I32), ("gate_dtype", _I32), ("kind", _I32), ("post_norm", _I32), ("pre_norm", _I32),
+                ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float), ("weight_offset", ctypes.c_float)]
+
+
+class BlockNorm(NamedTuple):
+    """What block_norm wrote (None: not asked for)."""
+    R: object
+    Y: object
+    A_packed: object
+    a_scales: object
+
+
+_NORMS = {"rms": 0, "layer": 1}
+
+
+def _extent(t):
+    """First and last byte address of a matrix, exclusive."""
+    at, size = t.data_ptr(), t.element_size()
+    return at, at + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * size
+
+
+def _apart(out, what: str, *inputs, same=()):
+    """Refuse an output that shares memory with an input, unless it is in `same` and has its very rows. Column ranges of
+    one buffer are apart."""
+    lo, hi = _extent(out)
+    for t in inputs:
+        if t is None:
+            continue
+        a, b = _extent(t)
+        if hi <= a or b <= lo:
+            continue
+        rows = out.shape[0] <= 1 or out.stride(0) == t.stride(0)
+        if lo == a and rows and out.dtype == t.dtype and any(t is x for x in same):
+            continue
+        if rows and t.dim() == out.dim() == 2 and out.element_size() == t.element_size() and out.shape[0] > 1:
+            ld = out.stride(0) * out.element_size()
+            gap = (a - lo) % ld     # t's columns start this many bytes behind out's, and end before out's next row
+            if gap >= out.shape[1] * out.element_size() and gap + t.shape[1] * t.element_size() <= ld:
+                continue
+        raise ValueError(f"{what} must not overlap an input")
+
+
+def _vector(v, K: int, what: str):
+    """A contiguous vector [K] on the current GPU, or None. Returns its dtype code (None without one)."""
+    if v is None:
+        return None
+    _need(v.dim() == 1 and v.shape[0] == K and (K == 1 or v.stride(0) == 1) and _here(v),
+          f"{what} must be a contiguous tensor [K] on the current GPU")
+    return _dtype_code(v.dtype)
+
+
+@_on_stream
+def block_norm(X, residual=None, kind: str = "rms", eps: float = 1e-6, post_norm: bool = False, post_weight=None,
+               post_bias=None, gate=None, residual_scale: float = 1.0, pre_norm: bool = True, weight=None, bias=None,
+               weight_offset: float = 0.0, layer: "Fp8Layer" = None, R=None, Y=None, A_packed=None,
+               a_scales=None) -> BlockNorm:
+    """The norms between two blocks, fused with the gate, the residual sum and the E4M3 quantizer, for X [M, K] (fp16
+    or bf16): u = X, or its norm (post_norm); r = residual_scale * residual + gate * u; y = norm(r) of the unrounded r
+    (pre_norm). kind: "rms" or "layer". gate: [K], or [G, K] with G dividing M, each row for M / G rows of X. Weights
+    and biases [K]: all of X's type or all fp32; a norm multiplies by weight_offset + weight.
+
+    Returns (R, Y, A_packed, a_scales). R is r (None where r is X itself and no R is passed). With a layer y comes as the
+    codes and scales that fp8_gemm takes for that layer, and as Y only where a Y is passed; without one it comes as Y.
+    R may be residual or X, Y may be X or residual."""
+    import torch
+    code = _rows16(X, "X")
+    M, K = X.shape
+    norm = _NORMS.get(kind)
+    _need(norm is not None, "kind must be 'rms' or 'layer'")
+    _need(post_norm or (post_weight is None and post_bias is None), "post_weight and post_bias need post_norm")
+    _need(pre_norm or (weight is None and bias is None and layer is None and Y is None),
+          "weight, bias, layer and Y need pre_norm")
+    params = [_vector(v, K, what) for v, what in ((post_weight, "post_weight"), (post_bias, "post_bias"),
+                                                  (weight, "weight"), (bias, "bias"))]
+    types = {t for t in params if t is not None}
+    _need(len(types) <= 1 and types <= {code, 2}, "weights and biases must all be of X's type, or all fp32")
+    a = BlockNormArgs()
+    a.X, a.ldx, a.M, a.K, a.dtype = X.data_ptr(), _ld(X), M, K, code
+    a.param_dtype = types.pop() if types else code
+    if residual is not None:
+        _need(_rows16(residual, "residual") == code and residual.shape == (M, K), "residual must be [M, K] of X's type")
+        a.residual, a.ldr = residual.data_ptr(), _ld(residual)
+    if gate is not None:
+        rows = gate if gate.dim() == 2 else gate[None]
+        _need(gate.dim() in (1, 2) and _here(gate) and rows.shape[1] == K and (K == 1 or rows.stride(1) == 1) and
+              rows.shape[0] >= 1 and M % rows.shape[0] == 0, "gate must be [K], or [G, K] with G dividing M, on the current GPU")
+        a.gate, a.gate_dtype = gate.data_ptr(), _dtype_code(gate.dtype)
+        _need(a.gate_dtype in (code, 2), "gate must be of X's type or fp32")
+        a.gate_tokens, a.ldg = M // rows.shape[0], max(K, rows.stride(0)) if rows.shape[0] > 1 else K
+        _need(rows.shape[0] <= 1 or rows.stride(0) >= K, "the rows of a gate must not overlap")
+    inputs = (X, residual, gate, post_weight, post_bias, weight, bias)
+    if R is None and (post_norm or residual is not None or gate is not None or not pre_norm):
+        R = torch.empty((M, K), dtype=X.dtype, device=X.device)
+    elif R is not None:
+        _need(_rows16(R, "R") == code and R.shape == (M, K), "R must be [M, K] of X's type")
+        _apart(R, "R", *inputs, same=(X, residual))
+    if pre_norm and layer is None and Y is None:
+        Y = torch.empty((M, K), dtype=X.dtype, device=X.device)
+    elif Y is not None:
+        _need(_rows16(Y, "Y") == code and Y.shape == (M, K), "Y must be [M, K] of X's type")
+        _apart(Y, "Y", *inputs, same=(X, residual))
+        _apart(Y, "Y (and R)", R)
+    if layer is not None:
+        _need(layer.K == K, "the layer must take K channels")
+        if A_packed is None or a_scales is None:
+            A, s = layer.activations(M, X.device)
+            A_packed, a_scales = A if A_packed is None else A_packed, s if a_scales is None else a_scales
+        layer.check_activations(A_packed, a_scales, M)
+        a.A_packed, a.a_scales = A_packed.data_ptr(), a_scales.data_ptr()
+    else:
+        _need(A_packed is None and a_scales is None, "A_packed and a_scales need a layer")
+    if R is not None:
+        a.R, a.ldo = R.data_ptr(), _ld(R)
+    if Y is not None:
+        a.Y, a.ldy = Y.data_ptr(), _ld(Y)
+    a.post_weight, a.post_bias, a.weight, a.bias = (v.data_ptr() if v is not None else None
+                                                    for v in (post_weight, post_bias, weight, bias))
+    a.kind, a.post_norm, a.pre_norm = norm, int(post_norm), int(pre_norm)
+    a.eps, a.residual_scale, a.weight_offset = eps, residual_scale, weight_offset
+    _check("fmpq_block_norm", (_lib or load_library()).fmpq_block_norm(ctypes.addressof(a), _on(X)))
+    return BlockNorm(R, Y, A_packed, a_scales)
 
 
 # ---- routing to experts -------------------------------------------------------------------

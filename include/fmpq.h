@@ -495,6 +495,49 @@ FMPQ_API fmpq_status fp8_quantize_gemm(const fp8_layer* layer, const void* X, in
                                        void* Y, int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ======================================================================================
+ * Between two blocks: norms, gate, residual sum, quantizer
+ *
+ *   u = X, or norm(X; post_weight, post_bias) with post_norm = 1      the norm after a block
+ *   r = residual_scale * residual + gate * u                          rounded once, where it is written
+ *   y = norm(r; weight, bias) with pre_norm = 1, of the unrounded r   the norm before the next block
+ *   norm(v; w, b)_k = (v_k - c) / sqrt(mean((v - c)^2) + eps) * (weight_offset + w_k) + b_k,
+ *   c = 0 (FMPQ_NORM_RMS) or mean(v) (FMPQ_NORM_LAYER); no weight: times 1; no bias: + 0
+ * All in FP32. y is written in 16 bits (Y), as the E4M3 codes and scales that fp8_quantize would
+ * make of the FP32 y (A_packed, a_scales), or both. Forward only.
+ * ====================================================================================== */
+
+enum { FMPQ_NORM_RMS = 0, FMPQ_NORM_LAYER = 1 };
+
+typedef struct fmpq_block_norm_args {
+    const void* X;             /* [M][ldx], the block's output, of `dtype` (F16 or BF16), like residual, R and Y */
+    int64_t ldx;
+    const void* residual;      /* [M][ldr], or NULL: r = gate * u */
+    int64_t ldr;
+    const void* gate;          /* row m takes gate row m / gate_tokens, [..][ldg] of K; NULL: 1 */
+    int64_t ldg, gate_tokens;  /* gate_tokens >= M: one gate for every row */
+    const void* post_weight;   /* [K] or NULL, of param_dtype: `dtype` or F32, like the next three */
+    const void* post_bias;
+    const void* weight;
+    const void* bias;
+    void* R;                   /* [M][ldo] or NULL */
+    int64_t ldo;
+    void* Y;                   /* [M][ldy] or NULL */
+    int64_t ldy;
+    void* A_packed;            /* codes and scales as fp8_quantize of a layer with this K makes them, or both NULL */
+    void* a_scales;
+    int64_t M;                 /* 1 .. 2^24 */
+    int32_t K;                 /* 1 .. FP8_MAX_K */
+    int32_t dtype, param_dtype, gate_dtype;
+    int32_t kind, post_norm, pre_norm;
+    float eps;                 /* > 0 */
+    float residual_scale, weight_offset;
+} fmpq_block_norm_args;
+
+/* One launch. R may be residual's or X's buffer, and Y X's or residual's (the same rows: pointer and stride); no
+ * other output may overlap an input. Y and codes need pre_norm; post_weight and post_bias need post_norm. */
+FMPQ_API fmpq_status fmpq_block_norm(const fmpq_block_norm_args* args, void* stream);
+
+/* ======================================================================================
  * Routing to experts, and the experts' products
  * ====================================================================================== */
 
