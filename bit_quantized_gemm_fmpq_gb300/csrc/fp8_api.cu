@@ -6,32 +6,21 @@
 #include <new>
 
 #include "../../include/fmpq.h"
+#include "api_checks.h"
 #include "fp8_internal.h"
 
 namespace {
 
-constexpr int64_t kMaxRows = INT64_C(1) << 24;
+using namespace fmpq::api;
+
 constexpr int kMaxPlanExperts = 1024;
 constexpr int64_t kMaxPairs = INT64_C(1) << 22;
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-template <typename... P>
-bool all_aligned16(const P*... p) { return (aligned16(p) && ...); }
-
-fmpq_status launched(cudaError_t e) { return e == cudaSuccess ? FMPQ_OK : FMPQ_ERR_CUDA; }
 
 fmpq_status check_device(const fp8_layer* L) {
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess) return FMPQ_ERR_CUDA;
     return dev == L->device ? FMPQ_OK : FMPQ_ERR_DEVICE;
 }
-bool sixteen_bits(int32_t dtype) { return dtype == FMPQ_DTYPE_F16 || dtype == FMPQ_DTYPE_BF16; }
-bool any_type(int32_t dtype) { return sixteen_bits(dtype) || dtype == FMPQ_DTYPE_F32; }
-bool element_aligned(const void* p, int32_t dtype) {
-    return (reinterpret_cast<uintptr_t>(p) & (dtype == FMPQ_DTYPE_F32 ? 3u : 1u)) == 0;
-}
-cudaStream_t st(void* stream) { return static_cast<cudaStream_t>(stream); }
-
 // T tokens of k slots over E experts: what the plan and the experts' calls take.
 bool routing_ok(int64_t T, int32_t k, int32_t E) {
     return T >= 1 && k >= 1 && k <= 32 && E >= 1 && E <= kMaxPlanExperts && T <= kMaxPairs && T * k <= kMaxPairs;
@@ -156,23 +145,32 @@ size_t fp8_gemm_workspace_bytes(const fp8_layer* L, int64_t M) {
 }
 
 static fmpq_status gemm_after(const fp8_layer* L, const void* A_packed, const void* a_scales, const void* W_packed,
-                              const void* w_scales, int64_t M, void* Y, int32_t dtype, int64_t ldy, void* workspace,
-                              size_t workspace_bytes, bool pdl, void* stream);
+                              const void* w_scales, int64_t M, const fmpq_epilogue* e, void* Y, int32_t dtype, int64_t ldy,
+                              void* workspace, size_t workspace_bytes, bool pdl, void* stream);
 
 fmpq_status fp8_gemm(const fp8_layer* L, const void* A_packed, const void* a_scales, const void* W_packed,
                      const void* w_scales, int64_t M, void* Y, int32_t dtype, int64_t ldy, void* workspace,
                      size_t workspace_bytes, void* stream) {
-    return gemm_after(L, A_packed, a_scales, W_packed, w_scales, M, Y, dtype, ldy, workspace, workspace_bytes, false, stream);
+    return gemm_after(L, A_packed, a_scales, W_packed, w_scales, M, nullptr, Y, dtype, ldy, workspace, workspace_bytes, false,
+                      stream);
+}
+fmpq_status fp8_gemm_epilogue(const fp8_layer* L, const void* A_packed, const void* a_scales, const void* W_packed,
+                              const void* w_scales, int64_t M, const fmpq_epilogue* epilogue, void* Y, int32_t dtype, int64_t ldy,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+    if (epilogue == nullptr) return FMPQ_ERR_INVALID_ARG;
+    return gemm_after(L, A_packed, a_scales, W_packed, w_scales, M, epilogue, Y, dtype, ldy, workspace, workspace_bytes, false,
+                      stream);
 }
 
 static fmpq_status gemm_after(const fp8_layer* L, const void* A_packed, const void* a_scales, const void* W_packed,
-                              const void* w_scales, int64_t M, void* Y, int32_t dtype, int64_t ldy, void* workspace,
-                              size_t workspace_bytes, bool pdl, void* stream) {
+                              const void* w_scales, int64_t M, const fmpq_epilogue* e, void* Y, int32_t dtype, int64_t ldy,
+                              void* workspace, size_t workspace_bytes, bool pdl, void* stream) {
     if (L == nullptr || A_packed == nullptr || a_scales == nullptr || W_packed == nullptr || w_scales == nullptr ||
         Y == nullptr || !sixteen_bits(dtype) || L->gated || L->experts != 1)
         return FMPQ_ERR_INVALID_ARG;
     if (M < 1 || M > kMaxRows || ldy < L->N) return FMPQ_ERR_UNSUPPORTED_SHAPE;
     if (!all_aligned16(A_packed, a_scales, W_packed, w_scales) || !element_aligned(Y, dtype)) return FMPQ_ERR_MISALIGNED;
+    if (fmpq_status s = epilogue_ok(e, dtype, L->N)) return s;
     const size_t need = fmpq::fp8_gemm_workspace(*L, M);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return FMPQ_ERR_WORKSPACE;
     if (need > 0 && !aligned16(workspace)) return FMPQ_ERR_MISALIGNED;
@@ -187,14 +185,15 @@ static fmpq_status gemm_after(const fp8_layer* L, const void* A_packed, const vo
     a.Y = Y;
     a.dtype = dtype;
     a.ldy = ldy;
+    a.epilogue = epilogue_of(e);
     a.workspace = need > 0 ? workspace : nullptr;
     a.pdl = pdl;
     return launched(fmpq::launch_fp8_gemm(*L, a, st(stream)));
 }
 
-fmpq_status fp8_quantize_gemm(const fp8_layer* L, const void* X, int32_t dtype, int64_t ldx, int64_t M, void* A_packed,
-                              void* a_scales, const void* W_packed, const void* w_scales, void* Y, int64_t ldy,
-                              void* workspace, size_t workspace_bytes, void* stream) {
+static fmpq_status quantize_gemm_with(const fp8_layer* L, const void* X, int32_t dtype, int64_t ldx, int64_t M, void* A_packed,
+                                      void* a_scales, const void* W_packed, const void* w_scales, const fmpq_epilogue* e,
+                                      void* Y, int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
     // both calls' checks first, so that a refusal launches nothing
     if (L == nullptr || X == nullptr || A_packed == nullptr || a_scales == nullptr || W_packed == nullptr ||
         w_scales == nullptr || Y == nullptr || !sixteen_bits(dtype) || L->gated || L->experts != 1)
@@ -202,11 +201,26 @@ fmpq_status fp8_quantize_gemm(const fp8_layer* L, const void* X, int32_t dtype, 
     if (M < 1 || M > kMaxRows || ldx < L->K || ldy < L->N) return FMPQ_ERR_UNSUPPORTED_SHAPE;
     if (!all_aligned16(A_packed, a_scales, W_packed, w_scales) || !element_aligned(X, dtype) || !element_aligned(Y, dtype))
         return FMPQ_ERR_MISALIGNED;
+    if (fmpq_status s = epilogue_ok(e, dtype, L->N)) return s;
     const size_t need = fmpq::fp8_gemm_workspace(*L, M);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return FMPQ_ERR_WORKSPACE;
     if (need > 0 && !aligned16(workspace)) return FMPQ_ERR_MISALIGNED;
     if (fmpq_status s = fp8_quantize(L, X, dtype, ldx, M, A_packed, a_scales, stream)) return s;
-    return gemm_after(L, A_packed, a_scales, W_packed, w_scales, M, Y, dtype, ldy, workspace, workspace_bytes, true, stream);
+    return gemm_after(L, A_packed, a_scales, W_packed, w_scales, M, e, Y, dtype, ldy, workspace, workspace_bytes, true, stream);
+}
+
+fmpq_status fp8_quantize_gemm(const fp8_layer* L, const void* X, int32_t dtype, int64_t ldx, int64_t M, void* A_packed,
+                              void* a_scales, const void* W_packed, const void* w_scales, void* Y, int64_t ldy,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+    return quantize_gemm_with(L, X, dtype, ldx, M, A_packed, a_scales, W_packed, w_scales, nullptr, Y, ldy, workspace,
+                              workspace_bytes, stream);
+}
+fmpq_status fp8_quantize_gemm_epilogue(const fp8_layer* L, const void* X, int32_t dtype, int64_t ldx, int64_t M, void* A_packed,
+                                       void* a_scales, const void* W_packed, const void* w_scales, const fmpq_epilogue* epilogue,
+                                       void* Y, int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
+    if (epilogue == nullptr) return FMPQ_ERR_INVALID_ARG;
+    return quantize_gemm_with(L, X, dtype, ldx, M, A_packed, a_scales, W_packed, w_scales, epilogue, Y, ldy, workspace,
+                              workspace_bytes, stream);
 }
 
 // ---------------------------------------------------------------- between two blocks

@@ -290,7 +290,7 @@ __device__ __forceinline__ bool sum_blocks(Smem& s, uint32_t base, const float* 
 
 // Warp w covers TMEM lanes 32 (w % 4) .. + 31, one packed weight row a thread, and half of the
 // tile's tokens (up to 32): acc[i] holds tokens c0 + 2i and + 1.
-template <bool kGated>
+template <bool kGated, bool kEpi>
 __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank, int warp, int lane, uint32_t tmem,
                                          volatile int* abort_flag) {
     const int units = unit_count<kTokens>(p, s.tables);
@@ -389,6 +389,30 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
             ++nu;
         } else {
             const int n = 256 * t.pair + 128 * static_cast<int>(rank) + 32 * q + lane;
+            // bias, activation and residual of the thread's output channel: all residuals are on their way before the
+            // first is used (read and written by this thread alone, so the residual may be Y)
+            auto store_epilogue = [&]() {
+                const bool bf16 = p.bf16 != 0, mine = ok && n < p.N;
+                uint16_t r[32];
+                if (p.e.residual != nullptr) {
+                    const uint16_t* from = static_cast<const uint16_t*>(p.e.residual) + (t.row0 + c0) * p.e.ldr + n;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (i < own && mine) r[i] = from[i * p.e.ldr];
+                }
+                const float b = mine ? epi::bias_at(p.e, n, bf16) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[i] = make_float2(acc[i].x + b, acc[i].y + b);
+                activate_all(p.e.act, acc);
+                uint16_t* to = static_cast<uint16_t*>(p.Y) + (t.row0 + c0) * p.ldy + n;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    if (i >= own || !mine) continue;
+                    float f = (i & 1) ? acc[i >> 1].y : acc[i >> 1].x;
+                    if (p.e.residual != nullptr) f += epi::value16(r[i], bf16);
+                    to[i * p.ldy] = bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(f)) : __half_as_ushort(__float2half_rn(f));
+                }
+            };
             auto store = [&](auto f32) {   // (FP32 outputs are the experts', whose K is not split)
                 int64_t at = (t.row0 + c0) * p.ldy + n;
 #pragma unroll
@@ -403,7 +427,9 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
                     at += p.ldy;
                 }
             };
-            if (p.splits == 1 && p.f32) {
+            if (kEpi && p.splits == 1) {
+                store_epilogue();
+            } else if (p.splits == 1 && p.f32) {
                 store(std::true_type{});
             } else if (p.splits == 1) {
                 store(std::false_type{});
@@ -446,7 +472,8 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
                                 acc[2 * i + 1].y += f[i].w;
                             }
                     }
-                    store(std::false_type{});
+                    if constexpr (kEpi) store_epilogue();
+                    else store(std::false_type{});
                 }
             }
         }
@@ -457,7 +484,7 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
     }
 }
 
-template <bool kGated>
+template <bool kGated, bool kEpi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 fp8_few_kernel(const Params p, const __grid_constant__ CUtensorMap codes, const __grid_constant__ CUtensorMap scales) {
     extern __shared__ uint8_t smem_raw[];
@@ -508,7 +535,7 @@ fp8_few_kernel(const Params p, const __grid_constant__ CUtensorMap codes, const 
         }
         __syncwarp();
     } else {
-        epilogue<kGated>(p, s, rank, warp, lane, tmem, abort_flag);
+        epilogue<kGated, kEpi>(p, s, rank, warp, lane, tmem, abort_flag);
     }
     dev::tc_fence_before();
     __syncthreads();
@@ -588,6 +615,12 @@ cudaError_t launch_fp8_gemm(const fp8_layer& L, const Fp8GemmArgs& a, cudaStream
     const uintptr_t y = reinterpret_cast<uintptr_t>(a.Y);
     if (p.f32) p.vec = a.ldy % 4 == 0 && (y & 15u) == 0 ? 4 : 1;
     else p.vec = a.ldy % 8 == 0 && (y & 15u) == 0 ? 8 : a.ldy % 4 == 0 && (y & 7u) == 0 ? 4 : 1;
+    p.e = a.epilogue;
+    if (p.e.residual != nullptr) {   // its lines are read as the outputs' are written
+        const uintptr_t r = reinterpret_cast<uintptr_t>(p.e.residual);
+        const int vec = p.e.ldr % 8 == 0 && (r & 15u) == 0 ? 8 : p.e.ldr % 4 == 0 && (r & 7u) == 0 ? 4 : 1;
+        if (vec < p.vec) p.vec = vec;
+    }
     p.H = static_cast<uint8_t*>(a.H);
     p.h_scales = a.h_scales;
     p.M = static_cast<int>(a.rows);
@@ -614,7 +647,7 @@ cudaError_t launch_fp8_gemm(const fp8_layer& L, const Fp8GemmArgs& a, cudaStream
         return cudaErrorInvalidValue;
     const int64_t units = tiles * L.pairs * p.splits;
     const int grid = 2 * static_cast<int>(units < fp8_resident_pairs(L) ? units : fp8_resident_pairs(L));
-    auto fn = L.gated ? fp8::fp8_few_kernel<true> : fp8::fp8_few_kernel<false>;
+    auto fn = L.gated ? fp8::fp8_few_kernel<true, false> : p.e.any() ? fp8::fp8_few_kernel<false, true> : fp8::fp8_few_kernel<false, false>;
     return launch_pairs(fn, grid, fp8::kThreads, fp8::kSmemBytes, a.pdl, stream, p, codes, scales);
 }
 

@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "epilogue.cuh"
 #include "fmpq_device.cuh"
 #include "fmpq_internal.h"
 #include "fp8_internal.h"
@@ -38,6 +39,7 @@ struct Params {
     float* partial;            // split-K: [tile][split][CTA][warp][vector][lane] FP32 sums
     int32_t* arrivals;         // [tile][CTA]
     int32_t* status;
+    Epilogue e;                // (kernels with kEpi)
 };
 
 // The experts' tiles, staged in shared memory: units before each expert's, its first row and tokens.
@@ -185,6 +187,19 @@ __device__ __forceinline__ float max_magnitude(float a, float b) {
 // 19 of 798 us for 4096 tokens through 8 of 128 experts of 4096 x 1024. A rounded division costs 48 more. (Where
 // 1 + e^-g passes 2^126, silu(g) is below 1e-36 in magnitude, the quotient is 0.)
 __device__ __forceinline__ float silu_times(float g, float u) { return __fdividef(g, 1.0f + expf(-g)) * u; }
+
+// v = act(v) for all values of an array of pairs. One branch around the whole loop: only the path taken is fetched.
+template <int kN>
+__device__ __forceinline__ void activate_all(int act, float2 (&v)[kN]) {
+    auto all = [&](auto f) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) v[i] = make_float2(f(v[i].x), f(v[i].y));
+    };
+    if (act == kActRelu) all([](float x) { return epi::activate(kActRelu, x); });
+    else if (act == kActSilu) all([](float x) { return epi::activate(kActSilu, x); });
+    else if (act == kActGelu) all([](float x) { return epi::activate(kActGelu, x); });
+    else if (act == kActGeluTanh) all([](float x) { return epi::activate(kActGeluTanh, x); });
+}
 
 }  // namespace fp8
 

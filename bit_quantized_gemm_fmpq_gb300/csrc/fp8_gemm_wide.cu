@@ -248,6 +248,87 @@ __device__ __forceinline__ void store_tile(const Params& p, uint4* stage, int la
     }
 }
 
+// Bias and activation on a thread's token and 64 columns; then the residual and the rounding, 16 tokens at a time: the
+// residual's lines are read as the outputs' are written, into the stage, where each lane finds its token's and puts the
+// outputs in their place. (The tile is read and written by this warp alone, so the residual may be Y.)
+template <int kW>
+__device__ __forceinline__ void store_tile_epilogue(const Params& p, uint4* stage, int lane, float2 (&acc)[2][16], uint16_t* y,
+                                                    const uint16_t* residual, int n0, int tokens, int columns) {
+    struct alignas(2 * kW) Piece {
+        uint16_t v[kW];
+    };
+    const bool bf16 = p.bf16 != 0;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        if (p.e.bias != nullptr) {
+            const float b = 32 * c + lane < columns ? epi::bias_at(p.e, n0 + 32 * c + lane, bf16) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                acc[c][i].x += __shfl_sync(0xFFFFFFFFu, b, 2 * i);
+                acc[c][i].y += __shfl_sync(0xFFFFFFFFu, b, 2 * i + 1);
+            }
+        }
+        activate_all(p.e.act, acc[c]);
+    }
+    auto slot = [&](int l, int n) { return reinterpret_cast<uint16_t*>(&stage[l * 8 + ((n >> 3) ^ (l & 7))]) + (n & 7); };
+#pragma unroll
+    for (int pass = 0; pass < 2; ++pass) {
+        if (residual != nullptr) {
+#pragma unroll 4
+            for (int j = 0; j < 32 / kW; ++j) {
+                const int l = (32 * j + lane) / (64 / kW), n = (32 * j + lane) % (64 / kW) * kW;
+                if (16 * pass + l >= tokens) continue;
+                const uint16_t* from = residual + (16 * pass + l) * p.e.ldr + n;
+                Piece v{};
+                if (n + kW <= columns) {
+                    v = *reinterpret_cast<const Piece*>(from);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kW; ++i)
+                        if (n + i < columns) v.v[i] = from[i];
+                }
+                *reinterpret_cast<Piece*>(slot(l, n)) = v;
+            }
+            __syncwarp();
+        }
+        if ((lane >> 4) == pass)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                uint4* at = &stage[(lane & 15) * 8 + (k ^ (lane & 7))];
+                float2 f[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = acc[k >> 2][4 * (k & 3) + i];
+                if (residual != nullptr) {
+                    const uint4 r = *at;
+                    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 a = epi::values16(w[i], bf16);
+                        f[i] = make_float2(f[i].x + a.x, f[i].y + a.y);
+                    }
+                }
+                *at = make_uint4(pack16(f[0].x, f[0].y, bf16), pack16(f[1].x, f[1].y, bf16), pack16(f[2].x, f[2].y, bf16),
+                                 pack16(f[3].x, f[3].y, bf16));
+            }
+        __syncwarp();
+#pragma unroll 4
+        for (int j = 0; j < 32 / kW; ++j) {
+            const int l = (32 * j + lane) / (64 / kW), n = (32 * j + lane) % (64 / kW) * kW;
+            const Piece v = *reinterpret_cast<const Piece*>(slot(l, n));
+            if (16 * pass + l >= tokens) continue;
+            uint16_t* to = y + (16 * pass + l) * p.ldy + n;
+            if (n + kW <= columns) {
+                *reinterpret_cast<Piece*>(to) = v;
+            } else {
+#pragma unroll
+                for (int i = 0; i < kW; ++i)
+                    if (n + i < columns) to[i] = v.v[i];
+            }
+        }
+        __syncwarp();
+    }
+}
+
 // The same for FP32 outputs (a routed product whose rows are still to be summed), all 32 tokens and 16 columns at a time
 // (piece k of token l at k ^ (l / 2 % 4)), every lane staging its own token; kW 4 or 1. 8 tokens and whole lines at a
 // time leave three quarters of the lanes idle at the staging: 793 against 772 us for 4096 tokens through 8 of 128
@@ -299,7 +380,7 @@ __device__ __forceinline__ float load_shared(uint32_t address) {
 // a scheduler hide them for each other. The blocks of a unit run straight-line: a TMEM load under a
 // condition makes the compiler move its 32 registers at every join. A wait that gives up is remembered,
 // and the unit's outputs are not stored.
-template <bool kGated>
+template <bool kGated, bool kEpi>
 __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank, int warp, int lane, uint32_t tmem,
                                          volatile int* abort_flag) {
     const int units = unit_count<kT>(p, s.tables);
@@ -402,7 +483,13 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
             const int64_t at = (static_cast<int64_t>(row0) + first) * p.ldy + n0;
             uint16_t* y = static_cast<uint16_t*>(p.Y) + at;
             const int tokens = ok ? n - first : 0, columns = p.N - n0;
-            if (p.f32) {
+            if constexpr (kEpi) {
+                const uint16_t* r = static_cast<const uint16_t*>(p.e.residual);
+                if (r != nullptr) r += (static_cast<int64_t>(row0) + first) * p.e.ldr + n0;
+                if (p.vec == 8) store_tile_epilogue<8>(p, s.out[warp - 4], lane, acc, y, r, n0, tokens, columns);
+                else if (p.vec == 4) store_tile_epilogue<4>(p, s.out[warp - 4], lane, acc, y, r, n0, tokens, columns);
+                else store_tile_epilogue<1>(p, s.out[warp - 4], lane, acc, y, r, n0, tokens, columns);
+            } else if (p.f32) {
                 float* yf = static_cast<float*>(p.Y) + at;
                 if (p.vec == 4) store_tile_f32<4>(p, s.out[warp - 4], lane, acc, weight, yf, tokens, columns);
                 else store_tile_f32<1>(p, s.out[warp - 4], lane, acc, weight, yf, tokens, columns);
@@ -414,7 +501,7 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
     if (!ok && lane == 0) fail(p, abort_flag);
 }
 
-template <bool kGated>
+template <bool kGated, bool kEpi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
 fp8_wide_kernel(const Params p, const __grid_constant__ CUtensorMap scales) {
     extern __shared__ uint8_t smem_raw[];
@@ -465,7 +552,7 @@ fp8_wide_kernel(const Params p, const __grid_constant__ CUtensorMap scales) {
         __syncwarp();
     } else {
         dev::setmaxnreg_inc<112>();   // 128 x 32 + 512 x 112 = the 640 x 96 of the launch
-        epilogue<kGated>(p, s, rank, warp, lane, tmem, abort_flag);
+        epilogue<kGated, kEpi>(p, s, rank, warp, lane, tmem, abort_flag);
     }
     dev::tc_fence_before();
     __syncthreads();
@@ -492,8 +579,8 @@ int fp8_resident_pairs(const fp8_layer& L) {
     cfg.blockDim = dim3(fp8::kWideThreads);
     cfg.dynamicSmemBytes = fp8::kSmemBytes;
     int clusters = 0;
-    if (ensure_smem_limit(reinterpret_cast<const void*>(fp8::fp8_wide_kernel<false>), static_cast<int>(fp8::kSmemBytes)) == cudaSuccess &&
-        cudaOccupancyMaxActiveClusters(&clusters, fp8::fp8_wide_kernel<false>, &cfg) == cudaSuccess && clusters > 0 && clusters < pairs)
+    if (ensure_smem_limit(reinterpret_cast<const void*>(fp8::fp8_wide_kernel<false, false>), static_cast<int>(fp8::kSmemBytes)) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&clusters, fp8::fp8_wide_kernel<false, false>, &cfg) == cudaSuccess && clusters > 0 && clusters < pairs)
         pairs = clusters;
     cudaGetLastError();   // a failed query leaves no error behind
     if (L.device >= 0 && L.device < 64) cached[L.device] = pairs;
@@ -528,7 +615,7 @@ cudaError_t launch_fp8_wide(const fp8_layer& L, const fp8::Params& p, const floa
     if (!encode_scale_map(&map, a_scales, p.sstride, L.nb, 128, fp8::kChunk)) return cudaErrorInvalidValue;
     const int64_t units = tiles * L.pairs;
     const int grid = 2 * static_cast<int>(units < fp8_resident_pairs(L) ? units : fp8_resident_pairs(L));
-    auto fn = L.gated ? fp8::fp8_wide_kernel<true> : fp8::fp8_wide_kernel<false>;
+    auto fn = L.gated ? fp8::fp8_wide_kernel<true, false> : p.e.any() ? fp8::fp8_wide_kernel<false, true> : fp8::fp8_wide_kernel<false, false>;
     return launch_pairs(fn, grid, fp8::kWideThreads, fp8::kSmemBytes, pdl, stream, p, map);
 }
 

@@ -5,6 +5,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "epilogue.h"
+
 struct fp8_layer {
     int32_t K = 0, N = 0, experts = 0;
     int32_t gated = 0;      // N = 2F: F gate rows, then F up rows
@@ -96,6 +98,7 @@ struct Fp8GemmArgs {
     int64_t ldy;
     void* H;                  // gated layer: E4M3 codes [F/128][rows][128] and scales
     float* h_scales;
+    Epilogue epilogue;        // dense, plain layer, 16-bit outputs
     void* workspace;
     // Launched as the programmatic dependent of this library's kernel before it: its prologue, and the
     // weights' stream, start while that one runs; only its codes and scales are waited for. Every kernel

@@ -82,6 +82,8 @@ SIGNATURES = {
     "fp8_gemm_workspace_bytes": (_SZ, [_P, _I64]),
     "fp8_gemm": (_I32, [_P, _P, _P, _P, _P, _I64, _P, _I32, _I64, _P, _SZ, _P]),
     "fp8_quantize_gemm": (_I32, [_P, _P, _I32, _I64, _I64, _P, _P, _P, _P, _P, _I64, _P, _SZ, _P]),
+    "fp8_gemm_epilogue": (_I32, [_P, _P, _P, _P, _P, _I64, _P, _P, _I32, _I64, _P, _SZ, _P]),
+    "fp8_quantize_gemm_epilogue": (_I32, [_P, _P, _I32, _I64, _I64, _P, _P, _P, _P, _P, _P, _I64, _P, _SZ, _P]),
     "fmpq_block_norm": (_I32, [_P, _P]),
     "moe_route": (_I32, [_P, _I32, _I64, _I64, _I32, _I32, _I32, _P, _I32, _I32, _I32, _I32, ctypes.c_float, _P, _P, _P]),
     "moe_rows": (_I64, [_I64, _I32, _I32]),
@@ -666,6 +668,63 @@ def _ld(X) -> int:
     return ld
 
 
+def _extent(t):
+    """First and last byte address of a matrix, exclusive."""
+    at, size = t.data_ptr(), t.element_size()
+    return at, at + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * size
+
+
+def _apart(out, what: str, *inputs, same=()):
+    """Refuse an output that shares memory with an input, unless it is in `same` and has its very rows. Column ranges of
+    one buffer are apart."""
+    lo, hi = _extent(out)
+    for t in inputs:
+        if t is None:
+            continue
+        a, b = _extent(t)
+        if hi <= a or b <= lo:
+            continue
+        rows = out.shape[0] <= 1 or out.stride(0) == t.stride(0)
+        if lo == a and rows and out.dtype == t.dtype and any(t is x for x in same):
+            continue
+        if rows and t.dim() == out.dim() == 2 and out.element_size() == t.element_size() and out.shape[0] > 1:
+            ld = out.stride(0) * out.element_size()
+            gap = (a - lo) % ld     # t's columns start this many bytes behind out's, and end before out's next row
+            if gap >= out.shape[1] * out.element_size() and gap + t.shape[1] * t.element_size() <= ld:
+                continue
+        raise ValueError(f"{what} must not overlap an input")
+
+
+class Epilogue(ctypes.Structure):
+    """fmpq_epilogue of include/fmpq.h."""
+    _fields_ = [("bias", _P), ("residual", _P), ("ldr", _I64), ("bias_dtype", _I32), ("activation", _I32)]
+
+
+ACTIVATIONS = {None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+
+def _epilogue(bias, activation, residual, shape, biases, code: int, Y=None):
+    """The epilogue of a product with outputs of `shape` and the 16-bit type `code`, or None where nothing is asked for.
+    Y: the output that was passed, if one was."""
+    act = ACTIVATIONS.get(activation)
+    _need(act is not None, "activation must be None, 'relu', 'silu', 'gelu' or 'gelu_tanh'")
+    if bias is None and residual is None and act == 0:
+        return None
+    e = Epilogue(activation=act)
+    if bias is not None:
+        _need(tuple(bias.shape) == biases and _here(bias) and bias.is_contiguous(),
+              f"bias must be a contiguous tensor {list(biases)} on the current GPU")
+        e.bias, e.bias_dtype = bias.data_ptr(), _dtype_code(bias.dtype)
+        _need(e.bias_dtype in (code, 2), "bias must be of the output's type or fp32")
+    if residual is not None:
+        _need(_rows16(residual, "residual", fp32=True) == code and residual.shape == shape,
+              "residual must have the output's shape and type")
+        e.residual, e.ldr = residual.data_ptr(), _ld(residual)
+    if Y is not None:
+        _apart(Y, "Y", residual, bias, same=(residual,))
+    return e
+
+
 def _on(X) -> int:
     """torch's current stream for X's device."""
     import torch
@@ -813,9 +872,16 @@ def _workspace_of(layer: Fp8Layer, M: int, workspace):
 
 
 @_on_stream
-def fp8_gemm(layer: Fp8Layer, A_packed, a_scales, W_packed, w_scales, M: int, dtype=None, Y=None, workspace=None):
-    """Y [M, N] (fp16 by default) of quantized activations and packed weights."""
+def fp8_gemm(layer: Fp8Layer, A_packed, a_scales, W_packed, w_scales, M: int, dtype=None, Y=None, workspace=None,
+             bias=None, activation=None, residual=None):
+    """Y [M, N] (fp16 by default) of quantized activations and packed weights: act(product + bias) + residual, rounded
+    once. bias [N] (Y's type or fp32); activation None, "relu", "silu", "gelu" or "gelu_tanh"; residual [M, N] of Y's
+    type, which may be Y."""
     import torch
+    epilogue = None
+    if bias is not None or activation is not None or residual is not None:
+        code = _dtype_code(Y.dtype if Y is not None else dtype or torch.float16)
+        epilogue = _epilogue(bias, activation, residual, (M, layer.N), (layer.N,), code, Y)
     if Y is None:
         Y = torch.empty((M, layer.N), dtype=dtype or torch.float16, device=A_packed.device)
     _rows16(Y, "Y")
@@ -824,6 +890,11 @@ def fp8_gemm(layer: Fp8Layer, A_packed, a_scales, W_packed, w_scales, M: int, dt
         layer.check_weights(W_packed, w_scales)
         layer.check_activations(A_packed, a_scales, M)
     w_ptr, w_bytes = _workspace_of(layer, M, workspace)
+    if epilogue is not None:
+        _check("fp8_gemm", layer._lib.fp8_gemm_epilogue(
+            layer.handle, _ptr(A_packed), _ptr(a_scales), _ptr(W_packed), _ptr(w_scales), M, ctypes.addressof(epilogue), _ptr(Y),
+            _dtype_code(Y.dtype), _ld(Y), w_ptr, w_bytes, _stream(None)))
+        return Y
     _check("fp8_gemm", layer._lib.fp8_gemm(layer.handle, _ptr(A_packed), _ptr(a_scales), _ptr(W_packed), _ptr(w_scales), M,
                                            _ptr(Y), _dtype_code(Y.dtype), _ld(Y), w_ptr, w_bytes,
                                            _stream(None)))
@@ -831,8 +902,10 @@ def fp8_gemm(layer: Fp8Layer, A_packed, a_scales, W_packed, w_scales, M: int, dt
 
 
 @_on_stream
-def fp8_quantize_gemm(layer: Fp8Layer, X, W_packed, w_scales, A_packed=None, a_scales=None, Y=None, workspace=None):
-    """The layer on X (fp16 or bf16 [M, K]) in one call: Y [M, N] of X's type."""
+def fp8_quantize_gemm(layer: Fp8Layer, X, W_packed, w_scales, A_packed=None, a_scales=None, Y=None, workspace=None,
+                      bias=None, activation=None, residual=None):
+    """The layer on X (fp16 or bf16 [M, K]) in one call: Y [M, N] of X's type; bias, activation and residual as
+    fp8_gemm takes them."""
     import torch
     code = _rows16(X, "X")
     M, K = X.shape
@@ -848,11 +921,19 @@ def fp8_quantize_gemm(layer: Fp8Layer, X, W_packed, w_scales, A_packed=None, a_s
         scratch = torch.empty(codes + layer.nb * ((M + 3) // 4 * 16), dtype=torch.uint8, device=X.device)
         a_ptr = scratch.data_ptr()
         s_ptr = a_ptr + codes
+    epilogue = None
+    if bias is not None or activation is not None or residual is not None:
+        epilogue = _epilogue(bias, activation, residual, (M, layer.N), (layer.N,), code, Y)
     if Y is None:
         Y = torch.empty((M, layer.N), dtype=X.dtype, device=X.device)
     else:
         _need(_rows16(Y, "Y") == code and Y.shape == (M, layer.N), "Y must be [M, N] of X's type")
     w_ptr, w_bytes = _workspace_of(layer, M, workspace)
+    if epilogue is not None:
+        _check("fp8_quantize_gemm", layer._lib.fp8_quantize_gemm_epilogue(
+            layer._h, X.data_ptr(), code, _ld(X), M, a_ptr, s_ptr, W_packed.data_ptr(), w_scales.data_ptr(),
+            ctypes.addressof(epilogue), Y.data_ptr(), _ld(Y), w_ptr, w_bytes, _on(X)))
+        return Y
     _check("fp8_quantize_gemm", layer._lib.fp8_quantize_gemm(
         layer._h, X.data_ptr(), code, _ld(X), M, a_ptr, s_ptr, W_packed.data_ptr(), w_scales.data_ptr(), Y.data_ptr(),
         _ld(Y), w_ptr, w_bytes, _on(X)))
@@ -889,33 +970,6 @@ class BlockNorm(NamedTuple):
 
 
 _NORMS = {"rms": 0, "layer": 1}
-
-
-def _extent(t):
-    """First and last byte address of a matrix, exclusive."""
-    at, size = t.data_ptr(), t.element_size()
-    return at, at + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * size
-
-
-def _apart(out, what: str, *inputs, same=()):
-    """Refuse an output that shares memory with an input, unless it is in `same` and has its very rows. Column ranges of
-    one buffer are apart."""
-    lo, hi = _extent(out)
-    for t in inputs:
-        if t is None:
-            continue
-        a, b = _extent(t)
-        if hi <= a or b <= lo:
-            continue
-        rows = out.shape[0] <= 1 or out.stride(0) == t.stride(0)
-        if lo == a and rows and out.dtype == t.dtype and any(t is x for x in same):
-            continue
-        if rows and t.dim() == out.dim() == 2 and out.element_size() == t.element_size() and out.shape[0] > 1:
-            ld = out.stride(0) * out.element_size()
-            gap = (a - lo) % ld     # t's columns start this many bytes behind out's, and end before out's next row
-            if gap >= out.shape[1] * out.element_size() and gap + t.shape[1] * t.element_size() <= ld:
-                continue
-        raise ValueError(f"{what} must not overlap an input")
 
 
 def _vector(v, K: int, what: str):

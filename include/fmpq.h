@@ -494,6 +494,29 @@ FMPQ_API fmpq_status fp8_quantize_gemm(const fp8_layer* layer, const void* X, in
                                        void* A_packed, void* a_scales, const void* W_packed, const void* w_scales,
                                        void* Y, int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
 
+/* What a product may do to its FP32 sums before it rounds them, once: Y = act(sum + bias) + residual.
+ *   bias        per output channel, FP32 or of Y's type (bias_dtype); NULL: 0
+ *   activation  silu(v) = v / (1 + e^-v); gelu(v) = v (1 + erf(v / sqrt 2)) / 2; GELU_TANH: the form with
+ *               tanh(sqrt(2 / pi) (v + 0.044715 v^3)) in place of erf
+ *   residual    [rows][ldr] of Y's type; NULL: 0. It may be Y itself (pointer and stride); it must not overlap Y otherwise. */
+enum { FMPQ_ACT_NONE = 0, FMPQ_ACT_RELU = 1, FMPQ_ACT_SILU = 2, FMPQ_ACT_GELU = 3, FMPQ_ACT_GELU_TANH = 4 };
+typedef struct fmpq_epilogue {
+    const void* bias;
+    const void* residual;
+    int64_t ldr;
+    int32_t bias_dtype;
+    int32_t activation;
+} fmpq_epilogue;
+/* fp8_gemm and fp8_quantize_gemm with an epilogue (not NULL; bias [N]); the same workspace. */
+FMPQ_API fmpq_status fp8_gemm_epilogue(const fp8_layer* layer, const void* A_packed, const void* a_scales,
+                                       const void* W_packed, const void* w_scales, int64_t M, const fmpq_epilogue* epilogue,
+                                       void* Y, int32_t dtype, int64_t ldy, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+FMPQ_API fmpq_status fp8_quantize_gemm_epilogue(const fp8_layer* layer, const void* X, int32_t dtype, int64_t ldx, int64_t M,
+                                                void* A_packed, void* a_scales, const void* W_packed, const void* w_scales,
+                                                const fmpq_epilogue* epilogue, void* Y, int64_t ldy, void* workspace,
+                                                size_t workspace_bytes, void* stream);
+
 /* ======================================================================================
  * Between two blocks: norms, gate, residual sum, quantizer
  *
