@@ -17,7 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libfmpq_gb300.so")
 SOURCES = ["fmpq_api.cu", "fmpq_quantize.cu", "fmpq_gemm.cu", "fmpq_gemm_small.cu", "fmpq_noalloc.cu", "fmpq_calib.cu", "fmpq_outlier.cu",
-           "fp8_api.cu", "fp8_quantize.cu", "fp8_gemm.cu", "fp8_gemm_wide.cu", "block_norm.cu", "moe_route.cu"]
+           "fp8_api.cu", "fp8_quantize.cu", "fp8_gemm.cu", "fp8_gemm_wide.cu", "block_norm.cu", "moe_route.cu",
+           "w16_api.cu", "w16_gemm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden"]
 

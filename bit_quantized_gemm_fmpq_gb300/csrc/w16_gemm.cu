@@ -1,0 +1,736 @@
+// Products with weights kept in 16 bits (sm_103a): a linear layer, or experts whose rows lie one group after another,
+//
+//   Y[r][n] = act(sum_k X[r][k] W_e[n][k] + bias_e[n]) * row_weight[r] + residual[r][n],   e the group of row r,
+//   gated: act(gate sum + bias) * (up sum + bias) in place of act(sum + bias).
+//
+// FP32 sums on the tensor cores (tcgen05 kind::f16, FP32 accumulators in TMEM), one rounding. A pair of CTAs computes 256
+// packed weight rows (128 each, the tensor core's M side, 16 KB a block of 64 channels, laid out beforehand so that a block is
+// one bulk copy) x up to 256 rows of X (the N side, half of them from each CTA, TMA boxes with the 128-byte swizzle).
+// The N side takes any multiple of 32, so a group's rest costs MMAs only for its own rows, and few rows are the same
+// kernel with a narrower tile and more weight blocks in flight: for one row it streams weights, for many it is bound by
+// the tensor pipe.
+//   * A unit's whole K is summed in TMEM; two accumulators, so that a unit's epilogue runs under the next one's MMAs.
+//   * The epilogue turns 16 rows at a time through shared memory in FP32, so that a thread has 8 neighbouring outputs of a row:
+//     bias, activation, residual (16-byte loads, on their way before the sums are there) and one 16-byte store.
+//   * Units too few for the pairs: K is split over the pairs of a cluster; the others leave their sums in the first one's
+//     shared memory, which adds them in order, so results do not depend on timing.
+//
+// Warp roles (384 threads, one CTA per SM, pairs persistent over units):
+//   warp 0      producer of weight blocks and X boxes
+//   warp 1      even CTA of a pair: MMA issuer; odd CTA: reports its operands to the even one
+//   warp 2      allocates and frees TMEM
+//   warp 3      sums up the groups' units
+//   warps 4-11  epilogue: TMEM lane quarter warp % 4; 16-row chunks of the unit in turn
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "epilogue.cuh"
+#include "fmpq_device.cuh"
+#include "fmpq_internal.h"
+#include "w16_internal.h"
+
+namespace fmpq {
+namespace w16 {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kEpiWarps = 8;
+constexpr int kMaxStages = 12;
+constexpr int kMostRows = 256;    // of a unit
+constexpr int kChunk = 16;        // rows of X that the epilogue turns at a time
+constexpr int kStageLd = 132;     // floats of a row there: 128 outputs, and a skew of 16 bytes
+constexpr int kBandTiles = 8;     // dense order: bands of 8 row tiles, weight tiles inside a band
+constexpr int kMaxSplits = 4;
+constexpr int kBigBox = 64, kSmallBox = 16;   // rows of the two TMA boxes
+
+struct Params {
+    const uint8_t* W;
+    const int32_t* start;
+    const int32_t* count;
+    const float* row_weight;
+    Epilogue e;
+    void* Y;
+    int64_t ldy;
+    int bf16, f32;       // operands (and Y, unless f32) are bf16
+    int vec;             // Y and residual take 16-byte accesses of 8 columns
+    int rows, N, out_n;  // out_n: columns of Y (gated: N / 2)
+    int nb, pairs, experts, splits;
+    int tile;            // rows of a unit, at most: a multiple of 32
+    int stages, stage_bytes;
+    int32_t* status;
+};
+
+struct Tables {
+    int32_t first_unit[kMaxFp8Experts + 1], start[kMaxFp8Experts], count[kMaxFp8Experts];
+};
+
+struct __align__(1024) Smem {
+    float turn[2][kChunk][kStageLd];   // a chunk of each half of the epilogue warps
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t acc_full[2], acc_free[2];
+    uint64_t split_full;   // first pair of a cluster: the others' sums are here
+    uint64_t mma_done;
+    uint32_t tmem_base;
+    int abort_flag;
+    Tables tables;
+    // then the ring of operand stages (16 KB of weights, tile / 2 rows of X), and with K split the sums of the other pairs:
+    // [split - 1][chunk][4 vectors][128 weight rows] of 4 floats
+};
+constexpr int kHeadBytes = (sizeof(Smem) + 1023) / 1024 * 1024;
+constexpr int kSmemBytes = 232448;                  // 227 KB: what a CTA may use
+constexpr int kRingBytes = kSmemBytes - 1024 - kHeadBytes;
+
+// `rows` of X for the 256 weight rows `pair` of expert e, blocks [b0, b1).
+struct Unit {
+    int e, pair, rows, row0, b0, b1;
+    __device__ int columns() const { return max(32, (rows + 31) & ~31); }   // of the MMAs
+};
+
+// Rows of a unit where `count` rows are cut evenly into as few units as tiles of p.tile allow.
+__host__ __device__ inline int even_rows(int count, int tile) {
+    const int tiles = (count + tile - 1) / tile;
+    return tiles == 0 ? tile : ((count + tiles - 1) / tiles + 31) / 32 * 32;
+}
+__device__ __forceinline__ int tiles_of(const Params& p, int count) {
+    return count > 0 ? (count + even_rows(count, p.tile) - 1) / even_rows(count, p.tile) : 0;
+}
+
+// Every thread calls it; a barrier must follow. Group bounds outside [0, rows] are cut to it.
+__device__ __forceinline__ void fill_tables(const Params& p, Tables& s, int warp, int lane) {
+    for (int e = threadIdx.x; e < p.experts; e += blockDim.x) {
+        const int64_t from = p.start[e], to = p.count != nullptr ? from + p.count[e] : p.start[e + 1];
+        const int a = static_cast<int>(min(max(from, INT64_C(0)), static_cast<int64_t>(p.rows)));
+        const int b = static_cast<int>(min(max(to, INT64_C(0)), static_cast<int64_t>(p.rows)));
+        s.start[e] = a;
+        s.count[e] = max(0, b - a);
+    }
+    __syncthreads();
+    if (warp != 3) return;
+    const int run = (p.experts + 31) / 32;
+    auto units_of = [&](int e) { return e < p.experts ? tiles_of(p, s.count[e]) * p.pairs : 0; };
+    int sum = 0;
+    for (int i = 0; i < run; ++i) sum += units_of(lane * run + i);
+    int before = sum;
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, before, d);
+        if (lane >= d) before += o;
+    }
+    before -= sum;
+    for (int i = 0; i < run; ++i) {
+        const int e = lane * run + i;
+        if (e <= p.experts) s.first_unit[e] = before;
+        before += units_of(e);
+    }
+    if (lane == 31 && p.experts == 32 * run) s.first_unit[p.experts] = before;
+}
+
+__device__ __forceinline__ int unit_count(const Params& p, const Smem& s) {
+    return p.start != nullptr ? s.tables.first_unit[p.experts] : tiles_of(p, p.rows) * p.pairs;
+}
+
+__device__ __forceinline__ Unit unit_of(const Params& p, const Smem& s, int u, int split) {
+    Unit r;
+    int count = p.rows, first = 0, t, per;
+    r.e = 0;
+    if (p.start != nullptr) {
+        int lo = 0, hi = p.experts;   // the expert with first_unit[e] <= u < first_unit[e + 1]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s.tables.first_unit[mid] <= u) lo = mid;
+            else hi = mid;
+        }
+        r.e = lo;
+        count = s.tables.count[lo];
+        first = s.tables.start[lo];
+        per = even_rows(count, p.tile);
+        const int tiles = (count + per - 1) / per, i = u - s.tables.first_unit[lo];
+        t = i % tiles;
+        r.pair = i / tiles;
+    } else {
+        per = even_rows(count, p.tile);
+        const int tiles = (count + per - 1) / per;
+        const int band = u / (kBandTiles * p.pairs), in_band = u - band * kBandTiles * p.pairs;
+        const int high = min(kBandTiles, tiles - band * kBandTiles);
+        t = band * kBandTiles + in_band % high;
+        r.pair = in_band / high;
+    }
+    r.row0 = first + t * per;
+    r.rows = min(per, count - t * per);
+    r.b0 = static_cast<int>(static_cast<int64_t>(split) * p.nb / p.splits);
+    r.b1 = static_cast<int>(static_cast<int64_t>(split + 1) * p.nb / p.splits);
+    return r;
+}
+
+__device__ __forceinline__ void fail(const Params& p, volatile int* abort_flag) {
+    *abort_flag = 1;
+    dev::report(p.status, dev::kStatusTimeout);
+}
+// true in one lane of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xFFFFFFFF;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
+}
+
+// Where a CTA stands: its number in the cluster, in its pair, the pair's first CTA, the pair's K split, the cluster.
+struct Place {
+    uint32_t cluster_rank, rank, leader;
+    int split, cluster, clusters;
+};
+
+// ---------------------------------------------------------------- producer (warp 0)
+__device__ __forceinline__ void producer(const Params& p, const CUtensorMap* big, const CUtensorMap* small, Smem& s, uint8_t* ring,
+                                         const Place& at, volatile int* abort_flag) {
+    const int units = unit_count(p, s);
+    uint32_t it = 0, st = 0, phase = 1;
+    bool ok = true;
+    for (int u = at.cluster; ok && u < units; u += at.clusters) {
+        const Unit t = unit_of(p, s, u, at.split);
+        const int half = t.columns() >> 1, row = t.row0 + static_cast<int>(at.rank) * half;
+        const uint8_t* w = p.W + (((static_cast<int64_t>(t.e) * p.pairs + t.pair) * 2 + at.rank) * p.nb + t.b0) * kTileBytes;
+        for (int b = t.b0; b < t.b1; ++b, ++it, w += kTileBytes) {
+            ok = __all_sync(0xFFFFFFFFu, dev::mbar_wait(&s.empty[st], phase, abort_flag));
+            if (!ok) break;
+            if (elect_one()) {
+                uint64_t* bar = &s.full[st];
+                uint8_t* to = ring + st * p.stage_bytes;
+                dev::mbar_arrive_expect_tx(bar, kTileBytes + half * 128u);
+                dev::bulk_g2s(to, w, kTileBytes, bar);
+                to += kTileBytes;
+                int i = 0;
+                for (; i + kBigBox <= half; i += kBigBox) dev::tma_load_2d(to + i * 128, big, b * kW16Block, row + i, bar);
+                for (; i < half; i += kSmallBox) dev::tma_load_2d(to + i * 128, small, b * kW16Block, row + i, bar);
+            }
+            __syncwarp();
+            if (++st == static_cast<uint32_t>(p.stages)) {
+                st = 0;
+                phase ^= 1;
+            }
+        }
+    }
+    if (!ok && elect_one()) fail(p, abort_flag);
+    // the copies in flight must land before the CTA's shared memory is given up (after an abort the even CTA's
+    // readiness may never be complete: a short bound, far longer than a copy)
+    const uint32_t stages = p.stages;
+    for (uint32_t k = 0; k < stages && k < it; ++k) {
+        const uint32_t i = it - 1 - k;
+        dev::mbar_wait(&s.full[i % stages], (i / stages) & 1, nullptr, ok ? dev::kMaxPolls : 1u << 16);
+    }
+}
+
+// ---------------------------------------------------------------- MMA (warp 1)
+// kind::f16, A and B both F16 or both BF16, D = F32, both K-major.
+__device__ __forceinline__ uint32_t idesc16(uint32_t M, uint32_t N, uint32_t bf16) {
+    return (1u << 4) | (bf16 << 7) | (bf16 << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n"
+        "}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrive on the barrier at `bar`'s offset in both CTAs of this pair once the MMAs issued so far are done.
+__device__ __forceinline__ void commit_pair(uint64_t* bar, uint32_t leader) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            dev::smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3u << leader))
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_issuer(const Params& p, Smem& s, uint8_t* ring, const Place& at, uint32_t tmem,
+                                           volatile int* abort_flag) {
+    const int units = unit_count(p, s);
+    const uint32_t remote = dev::mapa(&s.full[0], at.leader);
+    const uint64_t w0 = dev::sdesc_k_sw128(dev::smem_u32(ring));
+    uint32_t st = 0, phase = 0, nu = 0;
+    bool ok = true;
+    for (int u = at.cluster; ok && u < units; u += at.clusters, ++nu) {
+        const Unit t = unit_of(p, s, u, at.split);
+        const uint32_t idesc = idesc16(256, static_cast<uint32_t>(t.columns()), static_cast<uint32_t>(p.bf16));
+        const uint32_t acc = nu & 1, d = tmem + acc * kMostRows;
+        if (at.rank == 0) {
+            ok = __all_sync(0xFFFFFFFFu, dev::mbar_wait(&s.acc_free[acc], ((nu >> 1) & 1) ^ 1, abort_flag));
+            if (!ok) break;
+        }
+        for (int b = t.b0; b < t.b1; ++b) {
+            ok = __all_sync(0xFFFFFFFFu, dev::mbar_wait(&s.full[st], phase, abort_flag));
+            if (!ok) break;
+            if (at.rank != 0) {
+                if (elect_one()) dev::mbar_arrive_remote(remote + st * 8u);
+            } else {
+                dev::tc_fence_after();
+                // (a descriptor's address field counts 16 bytes)
+                const uint64_t ad = w0 + st * static_cast<uint32_t>(p.stage_bytes >> 4), bd = ad + kTileBytes / 16;
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) mma_16_pair(d, ad + 2 * k, bd + 2 * k, idesc, b > t.b0 || k > 0 ? 1u : 0u);
+                    commit_pair(&s.empty[st], at.leader);
+                    if (b + 1 == t.b1) commit_pair(&s.acc_full[acc], at.leader);
+                }
+            }
+            __syncwarp();
+            if (++st == static_cast<uint32_t>(p.stages)) {
+                st = 0;
+                phase ^= 1;
+            }
+        }
+    }
+    if (elect_one()) {
+        if (!ok) fail(p, abort_flag);
+        if (at.rank == 0) {   // every MMA must finish before TMEM is released
+            commit_pair(&s.mma_done, at.leader);
+            dev::mbar_wait(&s.mma_done, 0, nullptr);
+        }
+    }
+    __syncwarp();
+}
+
+// ---------------------------------------------------------------- epilogue (warps 4-11)
+
+// Eight neighbouring outputs of a row, from column n on (columns of them exist): 16 bits or FP32.
+__device__ __forceinline__ void store8(const Params& p, int64_t row, int n, int columns, const float (&f)[8]) {
+    if (p.f32) {
+        float* y = static_cast<float*>(p.Y) + row * p.ldy + n;
+        if (p.vec && columns >= 8) {
+            *reinterpret_cast<float4*>(y) = make_float4(f[0], f[1], f[2], f[3]);
+            *reinterpret_cast<float4*>(y + 4) = make_float4(f[4], f[5], f[6], f[7]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < columns) y[i] = f[i];
+        }
+        return;
+    }
+    uint16_t* y = static_cast<uint16_t*>(p.Y) + row * p.ldy + n;
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (p.bf16) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            o[i] = *reinterpret_cast<const uint32_t*>(&v);
+        } else {
+            const __half2 v = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+            o[i] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+    }
+    if (p.vec && columns >= 8) {
+        *reinterpret_cast<uint4*>(y) = make_uint4(o[0], o[1], o[2], o[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < columns) y[i] = static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1)));
+    }
+}
+// The residual there, as it is in memory: 16 bits in raw[0..3], FP32 in all eight.
+__device__ __forceinline__ void load_residual(const Params& p, int64_t row, int n, int columns, uint32_t (&raw)[8]) {
+    if (p.f32) {
+        const uint32_t* r = static_cast<const uint32_t*>(p.e.residual) + row * p.e.ldr + n;
+        if (p.vec && columns >= 8) {
+            const uint4 a = *reinterpret_cast<const uint4*>(r), b = *reinterpret_cast<const uint4*>(r + 4);
+            raw[0] = a.x, raw[1] = a.y, raw[2] = a.z, raw[3] = a.w, raw[4] = b.x, raw[5] = b.y, raw[6] = b.z, raw[7] = b.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) raw[i] = i < columns ? r[i] : 0u;
+        }
+        return;
+    }
+    const uint16_t* r = static_cast<const uint16_t*>(p.e.residual) + row * p.e.ldr + n;
+    if (p.vec && columns >= 8) {
+        const uint4 a = *reinterpret_cast<const uint4*>(r);
+        raw[0] = a.x, raw[1] = a.y, raw[2] = a.z, raw[3] = a.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            raw[i] = (2 * i < columns ? r[2 * i] : 0u) | (2 * i + 1 < columns ? static_cast<uint32_t>(r[2 * i + 1]) << 16 : 0u);
+    }
+}
+__device__ __forceinline__ void add_residual(const Params& p, const uint32_t (&raw)[8], float (&f)[8]) {
+    if (p.f32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] += __uint_as_float(raw[i]);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 a = epi::values16(raw[i], p.bf16 != 0);
+        f[2 * i] += a.x;
+        f[2 * i + 1] += a.y;
+    }
+}
+__device__ __forceinline__ void activate8(int act, float (&f)[8]) {
+    if (act == kActNone) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = epi::activate(act, f[i]);
+}
+// bias[first .. first + 7], 0 past `columns`
+__device__ __forceinline__ void load_bias(const Params& p, int64_t first, int columns, float (&b)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = i < columns ? epi::bias_at(p.e, first + i, p.bf16 != 0) : 0.0f;
+}
+
+// A thread's chunk of sums, rows c * 16 .. + 15 of the unit for one packed weight row, goes through shared memory; then it has the
+// outputs of one piece of 8 columns: of 2 rows, or gated of one, gate and up of 8 hidden channels.
+template <bool kGated>
+__device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* others, const Place& at, int warp, int lane, uint32_t tmem,
+                                         volatile int* abort_flag) {
+    constexpr int kPieces = kGated ? 8 : 16, kRowsAtOnce = 128 / kPieces, kPer = kChunk / kRowsAtOnce;
+    const int units = unit_count(p, s);
+    const int q = warp & 3, g = (warp - 4) >> 2, tid = 32 * q + lane;
+    const int piece = tid % kPieces, sub = tid / kPieces;
+    const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    const uint32_t leader_free = dev::mapa(&s.acc_free[0], at.leader);
+    float (*turn)[kStageLd] = s.turn[g];
+    uint32_t nu = 0;
+    bool ok = true;
+    for (int u = at.cluster; u < units; u += at.clusters, ++nu) {
+        const Unit t = unit_of(p, s, u, at.split);
+        const uint32_t acc = nu & 1;
+        const int n = (kGated ? 128 * t.pair + 64 * static_cast<int>(at.rank) : 256 * t.pair + 128 * static_cast<int>(at.rank)) + 8 * piece;
+        const int columns = p.out_n - n;
+        const int chunks = (t.rows + kChunk - 1) / kChunk;
+        const bool first = at.split == 0;
+        float bias[8], bias_up[kGated ? 8 : 1];
+        if (first && p.e.bias != nullptr) {
+            load_bias(p, static_cast<int64_t>(t.e) * p.N + n, columns, bias);
+            if constexpr (kGated) load_bias(p, static_cast<int64_t>(t.e) * p.N + p.out_n + n, columns, bias_up);
+        }
+        ok = ok && dev::mbar_wait(&s.acc_full[acc], (nu >> 1) & 1, abort_flag);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (first && p.splits > 1 && ok) ok = __all_sync(0xFFFFFFFFu, dev::mbar_wait_cluster(&s.split_full, 0));
+        dev::tc_fence_after();
+        const uint32_t others_at = first ? 0u : dev::mapa(others, at.rank);   // (in the first pair's CTA of this rank)
+        for (int c = g; c < chunks; c += 2) {
+            uint32_t raw[kPer][8];
+            float weight[kPer];
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int r = kChunk * c + sub + kRowsAtOnce * i;
+                weight[i] = 1.0f;
+                if (ok && first && r < t.rows && columns > 0) {
+                    if (p.e.residual != nullptr) load_residual(p, static_cast<int64_t>(t.row0) + r, n, columns, raw[i]);
+                    if (p.row_weight != nullptr) weight[i] = __ldg(p.row_weight + t.row0 + r);
+                }
+            }
+            uint32_t d[16];
+            dev::tmem_ld16(base + acc * kMostRows + kChunk * c, d);
+            dev::tmem_ld_wait16(d);
+            if (!first) {
+                const uint32_t to = others_at + ((((at.split - 1) * (p.tile / kChunk) + c) * 4) * 128 + tid) * 16u;
+                if (ok)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        dev::st_cluster_v4(to + v * 128 * 16u, __uint_as_float(d[4 * v]), __uint_as_float(d[4 * v + 1]),
+                                           __uint_as_float(d[4 * v + 2]), __uint_as_float(d[4 * v + 3]));
+                continue;
+            }
+            float f16[kChunk];
+#pragma unroll
+            for (int j = 0; j < kChunk; ++j) f16[j] = __uint_as_float(d[j]);
+            for (int sp = 1; sp < p.splits; ++sp) {
+                const float4* from = others + (((sp - 1) * (p.tile / kChunk) + c) * 4) * 128 + tid;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const float4 o = from[v * 128];
+                    f16[4 * v] += o.x, f16[4 * v + 1] += o.y, f16[4 * v + 2] += o.z, f16[4 * v + 3] += o.w;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kChunk; ++j) turn[j][tid] = f16[j];
+            dev::named_bar_sync(2 + g, 128);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int j = sub + kRowsAtOnce * i, r = kChunk * c + j;
+                if (!ok || r >= t.rows || columns <= 0) continue;
+                float f[8];
+                // gated: of every 32 packed rows, 16 gates and the ups of the same hidden channels
+                const float* from = &turn[j][kGated ? 32 * (piece >> 1) + 8 * (piece & 1) : 8 * piece];
+                *reinterpret_cast<float4*>(&f[0]) = *reinterpret_cast<const float4*>(from);
+                *reinterpret_cast<float4*>(&f[4]) = *reinterpret_cast<const float4*>(from + 4);
+                if (p.e.bias != nullptr)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) f[k] += bias[k];
+                activate8(p.e.act, f);
+                if constexpr (kGated) {
+                    float up[8];
+                    *reinterpret_cast<float4*>(&up[0]) = *reinterpret_cast<const float4*>(from + 16);
+                    *reinterpret_cast<float4*>(&up[4]) = *reinterpret_cast<const float4*>(from + 20);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) f[k] *= p.e.bias != nullptr ? up[k] + bias_up[k] : up[k];
+                }
+                if (p.row_weight != nullptr)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) f[k] *= weight[i];
+                if (p.e.residual != nullptr) add_residual(p, raw[i], f);
+                store8(p, static_cast<int64_t>(t.row0) + r, n, columns, f);
+            }
+            dev::named_bar_sync(2 + g, 128);   // read before the next chunk comes
+        }
+        // all of it has been read: the accumulator is free
+        dev::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) dev::mbar_arrive_remote(leader_free + acc * 8u);
+        if (!first) {
+            __syncwarp();
+            if (lane == 0 && ok) dev::mbar_arrive_remote_release(dev::mapa(&s.split_full, at.rank));
+        }
+    }
+    if (!ok && lane == 0) fail(p, abort_flag);
+}
+
+template <bool kGated>
+__global__ void __launch_bounds__(kThreads, 1)
+w16_kernel(const Params p, const __grid_constant__ CUtensorMap big, const __grid_constant__ CUtensorMap small) {
+    extern __shared__ uint8_t smem_raw[];
+    // (an offset from the array, so that the compiler still knows the accesses to be shared memory's)
+    uint8_t* head = smem_raw + ((1024u - (dev::smem_u32(smem_raw) & 1023u)) & 1023u);
+    Smem& s = *reinterpret_cast<Smem*>(head);
+    uint8_t* ring = head + kHeadBytes;
+    float4* others = reinterpret_cast<float4*>(ring + p.stages * p.stage_bytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Place at;
+    at.cluster_rank = dev::cluster_ctarank();
+    at.rank = at.cluster_rank & 1;
+    at.leader = at.cluster_rank & ~1u;
+    at.split = static_cast<int>(at.cluster_rank >> 1);
+    at.cluster = static_cast<int>(blockIdx.x) / (2 * p.splits);
+    at.clusters = static_cast<int>(gridDim.x) / (2 * p.splits);
+    if (threadIdx.x == 0) {
+        dev::tma_prefetch_map(&big);
+        dev::tma_prefetch_map(&small);
+        for (int i = 0; i < kMaxStages; ++i) {
+            dev::mbar_init(&s.full[i], at.rank == 0 ? 2 : 1);
+            dev::mbar_init(&s.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            dev::mbar_init(&s.acc_full[i], 1);
+            dev::mbar_init(&s.acc_free[i], 2 * kEpiWarps);
+        }
+        dev::mbar_init(&s.split_full, kEpiWarps * (p.splits > 1 ? p.splits - 1 : 1));
+        dev::mbar_init(&s.mma_done, 1);
+        s.abort_flag = 0;
+        dev::fence_barrier_init();
+    }
+    if (warp == 2) dev::tmem_alloc_pair(&s.tmem_base, 512);
+    if (p.start != nullptr) fill_tables(p, s.tables, warp, lane);
+    dev::tc_fence_before();
+    __syncthreads();
+    dev::cluster_sync();   // every CTA's barriers and TMEM exist before any traffic between them
+    dev::tc_fence_after();
+    const uint32_t tmem = s.tmem_base;
+    volatile int* abort_flag = &s.abort_flag;
+
+    if (warp == 0) {
+        producer(p, &big, &small, s, ring, at, abort_flag);
+    } else if (warp == 1) {
+        mma_issuer(p, s, ring, at, tmem, abort_flag);
+    } else if (warp >= 4) {
+        epilogue<kGated>(p, s, others, at, warp, lane, tmem, abort_flag);
+    }
+    __syncwarp();
+    dev::tc_fence_before();
+    __syncthreads();
+    dev::cluster_sync();   // the other CTAs' MMAs, commits, sums and arrivals on this one are done
+    if (warp == 2) {
+        dev::tc_fence_after();
+        dev::tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------- layout
+
+// W [N] x [K] at strides (ld_n, ld_k) into the packed tiles, 16 bytes (8 channels) a thread.
+__global__ void __launch_bounds__(256) pack_kernel(const uint16_t* __restrict__ W, int64_t ld_n, int64_t ld_k, int K, int N, int gated,
+                                                   int nb, int tiles, uint8_t* __restrict__ Wp) {
+    const int64_t pieces = static_cast<int64_t>(tiles) * nb * 1024;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < pieces; i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int c = static_cast<int>(i & 7), r = static_cast<int>((i >> 3) & 127);
+        const int64_t tb = i >> 10;
+        const int b = static_cast<int>(tb % nb), t = static_cast<int>(tb / nb);
+        const int n = fp8_source_row(t, r, N, gated), k = b * kW16Block + ((c ^ (r & 7)) << 3);
+        uint4 out = make_uint4(0u, 0u, 0u, 0u);
+        if (n >= 0) {
+            const uint16_t* from = W + n * ld_n + k * ld_k;
+            if (ld_k == 1 && k + 8 <= K && (reinterpret_cast<uintptr_t>(from) & 15u) == 0) {
+                out = *reinterpret_cast<const uint4*>(from);
+            } else {
+                uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (k + j < K) w[j >> 1] |= static_cast<uint32_t>(from[j * ld_k]) << (16 * (j & 1));
+                out = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        reinterpret_cast<uint4*>(Wp)[i] = out;
+    }
+}
+
+// Rows of any alignment to rows of ld (a multiple of 8) elements, 8 of them a thread; those past K are not read by anyone.
+__global__ void __launch_bounds__(256) align_kernel(const uint16_t* __restrict__ X, int64_t ldx, int64_t rows, int K, uint4* __restrict__ out,
+                                                    int64_t ld8) {
+    const int64_t pieces = rows * ld8;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < pieces; i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t r = i / ld8;
+        const int k = static_cast<int>(i - r * ld8) * 8;
+        const uint16_t* from = X + r * ldx + k;
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (k + j < K) w[j >> 1] |= static_cast<uint32_t>(from[j]) << (16 * (j & 1));
+        out[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// ---------------------------------------------------------------- launch
+
+bool encode_rows(CUtensorMap* map, const W16Args& a, const w16_layer& L, int box_rows) {
+    const EncodeTiledFn encode = encode_tiled();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(L.K), static_cast<cuuint64_t>(a.rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.ldx) * 2};
+    const cuuint32_t box[2] = {kW16Block, static_cast<cuuint32_t>(box_rows)}, step[2] = {1, 1};
+    return encode(map, L.dtype == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(a.X),
+                  dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaLaunchConfig_t config(int grid, int cluster, size_t smem, cudaStream_t stream, cudaLaunchAttribute* attr) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+// Clusters of `splits` pairs that are resident at once; asked once per device.
+int resident_clusters(const w16_layer& L, int splits) {
+    static int cached[64][kMaxSplits + 1] = {};
+    const bool known = L.device >= 0 && L.device < 64;
+    if (known && cached[L.device][splits] > 0) return cached[L.device][splits];
+    int most = L.num_sms / (2 * splits) > 0 ? L.num_sms / (2 * splits) : 1;
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = config(most * 2 * splits, 2 * splits, kSmemBytes, nullptr, attr);
+    int got = 0;
+    if (ensure_smem_limit(reinterpret_cast<const void*>(w16_kernel<false>), kSmemBytes) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&got, w16_kernel<false>, &cfg) == cudaSuccess && got > 0 && got < most)
+        most = got;
+    cudaGetLastError();   // a failed query leaves no error behind
+    if (known) cached[L.device][splits] = most;
+    return most;
+}
+
+struct Shape {
+    int tile, splits, grid, stages, stage_bytes;
+};
+
+Shape with_ring(int tile, int splits, int64_t units, int clusters) {
+    Shape s{tile, splits, 0, 0, 0};
+    s.grid = static_cast<int>(units < clusters ? units : clusters) * 2 * splits;
+    s.stage_bytes = kTileBytes + tile / 2 * 128;
+    const int others = (splits - 1) * tile * 128 * 4;
+    s.stages = (kRingBytes - others) / s.stage_bytes;
+    if (s.stages > kMaxStages) s.stages = kMaxStages;
+    return s;
+}
+
+// The tile and the K splits. A block of a unit takes the MMAs 2 clk a row of X and the copies no less than that of their
+// 16 KB of weights; an end of a unit about 3000 clk where nothing runs under it.
+Shape shape_of(const w16_layer& L, const W16Args& a) {
+    const int rows = static_cast<int>(a.rows);
+    if (a.start != nullptr) {
+        // the experts' loads are known on the device only: a tile for twice the mean, whose rest is cheap
+        const int used = L.experts < rows ? L.experts : rows, mean = (rows + used - 1) / used;
+        int tile = (2 * mean + 31) / 32 * 32;
+        if (tile > kMostRows) tile = kMostRows;
+        const int64_t most = (static_cast<int64_t>(used) + rows / (tile / 2) + 1) * L.pairs;   // (even_rows cuts no unit below half a tile)
+        return with_ring(tile, 1, most, resident_clusters(L, 1));
+    }
+    Shape best{};
+    double least = 0.0;
+    for (int splits = 1; splits <= kMaxSplits; splits *= 2) {
+        const int clusters = resident_clusters(L, splits);
+        if (splits > 1 && L.nb < 4 * splits) break;
+        for (int tile = 32; tile <= kMostRows; tile += 32) {
+            const int per = even_rows(rows, tile);
+            if (per != tile && tile < kMostRows) continue;
+            const int64_t tiles = (rows + per - 1) / per, units = tiles * L.pairs, rounds = (units + clusters - 1) / clusters;
+            if (splits > 1 && rounds > 1) continue;
+            const Shape s = with_ring(tile, splits, units, clusters);
+            if (s.stages < 4) continue;
+            const double block = 2.0 * per > 600.0 ? 2.0 * per : 600.0;
+            const double time = rounds * ((L.nb + splits - 1) / splits * block + 12.0 * per) + 3000.0 + (splits > 1 ? 1500.0 : 0.0);
+            if (best.grid == 0 || time < least) {
+                best = s;
+                least = time;
+            }
+        }
+    }
+    return best;
+}
+
+}  // namespace
+}  // namespace w16
+
+cudaError_t launch_w16_gemm(const w16_layer& L, const W16Args& a, cudaStream_t stream) {
+    const w16::Shape shape = w16::shape_of(L, a);
+    w16::Params p{};
+    p.W = static_cast<const uint8_t*>(a.W);
+    p.start = a.start;
+    p.count = a.count;
+    p.row_weight = a.row_weight;
+    p.e = a.epilogue;
+    p.Y = a.Y;
+    p.ldy = a.ldy;
+    p.bf16 = L.dtype == kBF16;
+    p.f32 = a.dtype == kF32;
+    const int64_t unit = p.f32 ? 4 : 8;
+    auto whole = [&](const void* v, int64_t ld) { return (reinterpret_cast<uintptr_t>(v) & 15u) == 0 && ld % unit == 0; };
+    p.vec = whole(a.Y, a.ldy) && (p.e.residual == nullptr || whole(p.e.residual, p.e.ldr));
+    p.rows = static_cast<int>(a.rows);
+    p.N = L.N;
+    p.out_n = L.gated ? L.N / 2 : L.N;
+    p.nb = L.nb;
+    p.pairs = L.pairs;
+    p.experts = L.experts;
+    p.splits = shape.splits;
+    p.tile = shape.tile;
+    p.stages = shape.stages;
+    p.stage_bytes = shape.stage_bytes;
+    p.status = L.d_status;
+    CUtensorMap big, small;
+    if (!w16::encode_rows(&big, a, L, w16::kBigBox) || !w16::encode_rows(&small, a, L, w16::kSmallBox)) return cudaErrorInvalidValue;
+    auto fn = L.gated ? w16::w16_kernel<true> : w16::w16_kernel<false>;
+    const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), w16::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = w16::config(shape.grid, 2 * shape.splits, w16::kSmemBytes, stream, attr);
+    return cudaLaunchKernelEx(&cfg, fn, p, big, small);
+}
+
+cudaError_t launch_w16_pack(const w16_layer& L, int expert, const void* W, int64_t ld_n, int64_t ld_k, void* Wp, cudaStream_t stream) {
+    uint8_t* out = static_cast<uint8_t*>(Wp) + static_cast<int64_t>(expert) * L.pairs * 2 * L.nb * kTileBytes;
+    const int64_t ctas = static_cast<int64_t>(L.pairs) * 2 * L.nb * 4;
+    w16::pack_kernel<<<static_cast<int>(ctas < L.num_sms * 32LL ? ctas : L.num_sms * 32LL), 256, 0, stream>>>(
+        static_cast<const uint16_t*>(W), ld_n, ld_k, L.K, L.N, L.gated, L.nb, L.pairs * 2, out);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_w16_align(const void* X, int64_t ldx, int64_t rows, int K, void* out, int64_t ld, int num_sms, cudaStream_t stream) {
+    const int64_t ctas = (rows * (ld / 8) + 255) / 256;
+    w16::align_kernel<<<static_cast<int>(ctas < num_sms * 32LL ? ctas : num_sms * 32LL), 256, 0, stream>>>(
+        static_cast<const uint16_t*>(X), ldx, rows, K, static_cast<uint4*>(out), ld / 8);
+    return cudaGetLastError();
+}
+
+}  // namespace fmpq

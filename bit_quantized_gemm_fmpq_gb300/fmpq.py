@@ -96,6 +96,14 @@ SIGNATURES = {
     "moe_experts": (_I32, [_P, _P, _P, _I32, _I64, _I64, _I32, _P, _P, _P, _P, _P, _P, _P, _I64, _P, _SZ, _P]),
     "moe_combine_f32": (_I32, [_P, _I64, _P, _I64, _I32, _I32, _I32, _P, _I32, _I64, _P]),
     "moe_combine": (_I32, [_P, _I32, _I64, _P, _I64, _I32, _I32, _I32, _P, _I64, _P]),
+    "w16_layer_create": (_I32, [_I32, _I32, _I32, _I32, _I32, ctypes.POINTER(_P)]),
+    "w16_layer_destroy": (None, [_P]),
+    "w16_device_status": (_I32, [_P, ctypes.POINTER(_I32), _I32]),
+    "w16_packed_w_bytes": (_SZ, [_P]),
+    "w16_pack_weights": (_I32, [_P, _I32, _P, _I64, _I64, _P, _P]),
+    "w16_workspace_bytes": (_SZ, [_P, _P, _I64, _I64]),
+    "w16_gemm": (_I32, [_P, _P, _I64, _I64, _P, _P, _P, _I32, _I64, _P, _SZ, _P]),
+    "w16_grouped_gemm": (_I32, [_P, _P, _I64, _I64, _P, _P, _P, _P, _P, _P, _I32, _I64, _P, _SZ, _P]),
     "fmpq_status_string": (ctypes.c_char_p, [_I32]),
     "fmpq_version": (_I32, []),
 }
@@ -1240,3 +1248,129 @@ def moe_experts(up: Fp8Layer, down: Fp8Layer, X, ids, weights, W_up, s_up, W_dow
         s_up.data_ptr(), W_down.data_ptr(), s_down.data_ptr(), Y.data_ptr(), down.N, scratch.data_ptr(), nbytes,
         _on(X)))
     return Y
+
+
+# ---- layers kept in 16 bits ---------------------------------------------------------------
+
+class W16Layer:
+    """Owns a w16_layer*: `experts` weight matrices [N, K] in fp16 or bf16 (one: a linear layer); gated: N = 2F rows, F
+    gate rows then F up rows, and outputs act(gate) * up of F columns."""
+
+    def __init__(self, K: int, N: int, dtype, experts: int = 1, gated: bool = False):
+        lib = load_library()
+        h = ctypes.c_void_p()
+        code = _dtype_code(dtype)
+        _check("w16_layer_create", lib.w16_layer_create(K, N, experts, int(gated), code, ctypes.byref(h)))
+        self._h = h
+        self._lib = lib
+        self.K, self.N, self.experts, self.gated, self.dtype = K, N, experts, bool(gated), dtype
+        self.outputs = N // 2 if gated else N
+        self._code = code
+        self._w_bytes = int(lib.w16_packed_w_bytes(h))
+
+    @property
+    def handle(self):
+        return self._h
+
+    def close(self):
+        if getattr(self, "_h", None) is not None and self._h.value:
+            self._lib.w16_layer_destroy(self._h)
+            self._h = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def packed_w_bytes(self) -> int:
+        return self._w_bytes
+
+
+def w16_device_status(layer: W16Layer, clear: bool = True) -> int:
+    """The layer's status word (0, or 5 after a wait that gave up)."""
+    code = ctypes.c_int32(0)
+    _check("w16_device_status", layer._lib.w16_device_status(layer.handle, ctypes.byref(code), int(clear)))
+    return int(code.value)
+
+
+@_on_stream
+def w16_pack_weights(layer: W16Layer, W):
+    """Lay out W [experts, N, K] (or [N, K]) of the layer's type, of any strides: a checkpoint that holds [K, N] passes its
+    transpose. Returns W_packed u8."""
+    import torch
+    W3 = W if W.dim() == 3 else W[None]
+    _need(W3.shape == (layer.experts, layer.N, layer.K) and W.dtype == layer.dtype and _here(W),
+          "W must be [experts, N, K] (or [N, K]) of the layer's type on the current GPU")
+    strides = [s if n > 1 else 1 for s, n in zip(W3.stride()[1:], W3.shape[1:])]
+    _need(min(strides) >= 1, "W must not be an expanded tensor")
+    Wp = torch.empty(layer.packed_w_bytes(), dtype=torch.uint8, device=W.device)
+    for e in range(layer.experts):
+        _check("w16_pack_weights", layer._lib.w16_pack_weights(layer.handle, e, W3[e].data_ptr(), *strides, Wp.data_ptr(), _on(W)))
+    return Wp
+
+
+def _w16_product(layer, X, groups, W_packed, bias, activation, residual, row_weight, dtype, Y):
+    import torch
+    _need(_rows16(X, "X") == layer._code and X.shape[1] == layer.K, "X must be [rows, K] of the layer's type")
+    _need(_here(W_packed) and W_packed.element_size() == 1 and W_packed.is_contiguous() and W_packed.numel() == layer._w_bytes,
+          "W_packed must be this layer's (w16_pack_weights)")
+    rows, ld = X.shape[0], _ld(X)
+    shape = (rows, layer.outputs)
+    code = layer._code if Y is None and dtype is None else _dtype_code(dtype if Y is None else Y.dtype)
+    _need(code in (layer._code, 2), "the output's type must be the layer's or fp32")
+    epilogue = None
+    if bias is not None or activation is not None or residual is not None:
+        biases = (layer.experts, layer.N)
+        if bias is not None and bias.dim() == 1 and layer.experts == 1:
+            bias = bias[None]
+        epilogue = _epilogue(bias, activation, residual, shape, biases, code, Y)
+    if Y is None:
+        Y = torch.empty(shape, dtype=layer.dtype if dtype is None else dtype, device=X.device)
+    else:
+        _need(_rows16(Y, "Y", fp32=True) == code and Y.shape == shape, "Y must be [rows, N] ([rows, N / 2] of a gated layer)")
+        _apart(Y, "Y", X, row_weight)
+    nbytes = int(layer._lib.w16_workspace_bytes(layer._h, X.data_ptr(), ld, rows)) if ld % 8 or X.data_ptr() % 16 else 0
+    workspace = torch.empty(nbytes, dtype=torch.uint8, device=X.device) if nbytes else None
+    e_ptr = ctypes.addressof(epilogue) if epilogue is not None else None
+    w_ptr = workspace.data_ptr() if nbytes else None
+    if groups is None:
+        _check("w16_gemm", layer._lib.w16_gemm(layer._h, X.data_ptr(), ld, rows, W_packed.data_ptr(), e_ptr, Y.data_ptr(), code,
+                                               _ld(Y), w_ptr, nbytes, _on(X)))
+    else:
+        r_ptr = row_weight.data_ptr() if row_weight is not None else None
+        _check("w16_grouped_gemm", layer._lib.w16_grouped_gemm(
+            layer._h, X.data_ptr(), ld, rows, *groups, W_packed.data_ptr(), e_ptr, r_ptr, Y.data_ptr(), code, _ld(Y), w_ptr,
+            nbytes, _on(X)))
+    return Y
+
+
+@_on_stream
+def w16_gemm(layer: W16Layer, X, W_packed, bias=None, activation=None, residual=None, dtype=None, Y=None):
+    """Y [M, N] (a gated layer: [M, N / 2]) of X [M, K] in the layer's type, or in fp32 (dtype, or a Y that is passed):
+    act(X W^T + bias) + residual; gated: act(gate + bias) * (up + bias) + residual. bias [N] or [1, N], of Y's type or fp32;
+    activation as fp8_gemm takes it; residual of Y's shape and type, which may be Y."""
+    _need(layer.experts == 1, "w16_gemm takes a layer of one matrix (w16_grouped_gemm: experts)")
+    return _w16_product(layer, X, None, W_packed, bias, activation, residual, None, dtype, Y)
+
+
+@_on_stream
+def w16_grouped_gemm(layer: W16Layer, X, groups, W_packed, bias=None, activation=None, residual=None, row_weight=None,
+                     dtype=None, Y=None):
+    """As w16_gemm, the rows of X in groups with a matrix each. groups: int32 offsets [experts + 1] on the GPU (group e is
+    rows offsets[e] to offsets[e + 1] - 1), or a MoePlan, whose rows X and Y then have. bias [experts, N]; row_weight fp32
+    [rows] scales a row's outputs before the residual. Rows of no group are not written."""
+    import torch
+    if isinstance(groups, MoePlan):
+        _need(groups.experts == layer.experts and _here(groups.buffer) and X.shape[0] == groups.rows,
+              "the plan must be of this layer's experts, and X of its rows")
+        at = groups.buffer.data_ptr()
+        pointers = (at, at + 4 * layer.experts)
+    else:
+        _need(_here(groups) and groups.dtype == torch.int32 and groups.shape == (layer.experts + 1,) and groups.is_contiguous(),
+              "groups must be contiguous int32 offsets [experts + 1] on the current GPU, or a MoePlan")
+        pointers = (groups.data_ptr(), None)
+    if row_weight is not None:
+        _need(_here(row_weight) and row_weight.dtype == torch.float32 and row_weight.shape == (X.shape[0],) and
+              row_weight.is_contiguous(), "row_weight must be contiguous fp32 [rows] on the current GPU")
+    return _w16_product(layer, X, pointers, W_packed, bias, activation, residual, row_weight, dtype, Y)

@@ -627,6 +627,51 @@ FMPQ_API fmpq_status moe_experts(const fp8_layer* up, const fp8_layer* down, con
                                  const void* s_up, const void* W_down, const void* s_down, void* Y, int64_t ldy,
                                  void* scratch, size_t scratch_bytes, void* stream);
 
+/* ======================================================================================
+ * Layers kept in 16 bits: a linear layer, or routed experts' matrices with ragged groups of rows
+ *
+ *   Y[r][n] = act(sum_k X[r][k] W_e[n][k] + bias[e][n]) * row_weight[r] + residual[r][n]
+ *   gated (N = 2F: F gate rows, then F up rows), for n < F:
+ *   Y[r][n] = act(gate[r][n] + bias[e][n]) * (up[r][n] + bias[e][F + n]) * row_weight[r] + residual[r][n]
+ * FP16 or BF16 weights and X of that type, FP32 sums on the tensor cores, one rounding. e is the
+ * group that row r lies in. Forward only.
+ * ====================================================================================== */
+
+#define W16_MAX_K 65536
+#define W16_MAX_N 1048576
+
+/* Opaque, library-owned description of a layer of `experts` weight matrices [N][K] of dtype F16 or
+ * BF16. N >= 1, 1 <= K <= W16_MAX_K, 1 <= experts <= 512. Synchronous; allocates a status word. */
+typedef struct w16_layer w16_layer;
+FMPQ_API fmpq_status w16_layer_create(int32_t K, int32_t N, int32_t experts, int32_t gated, int32_t dtype, w16_layer** out);
+FMPQ_API void w16_layer_destroy(w16_layer* layer);
+/* As fmpq_device_status, for this layer's calls. */
+FMPQ_API fmpq_status w16_device_status(const w16_layer* layer, int32_t* status_host, int32_t clear);
+
+/* Bytes of the packed weights of all experts: per expert ceil(N/256) (gated: ceil(F/128)) pairs of tiles of 128 rows, every
+ * tile ceil(K/64) swizzled blocks of 16 KB. The format is implementation-defined. */
+FMPQ_API size_t w16_packed_w_bytes(const w16_layer* layer);
+/* Lay out one expert's weights: element (n, k) at W[n * ld_n + k * ld_k], so a checkpoint may hold [N][K] or [K][N]. */
+FMPQ_API fmpq_status w16_pack_weights(const w16_layer* layer, int32_t expert, const void* W, int64_t ld_n, int64_t ld_k,
+                                      void* W_packed, void* stream);
+/* Bytes of workspace a product needs for these rows of X: 0 where they start on 16-byte boundaries (ldx % 8 = 0 and X
+ * aligned); others are copied there first. Calls that may run at the same time need one each. */
+FMPQ_API size_t w16_workspace_bytes(const w16_layer* layer, const void* X, int64_t ldx, int64_t rows);
+
+/* Y [M][ldy] of a layer with experts = 1. dtype: the layer's, or F32; bias, residual: of that type (the bias also FP32).
+ * epilogue: NULL for none. */
+FMPQ_API fmpq_status w16_gemm(const w16_layer* layer, const void* X, int64_t ldx, int64_t M, const void* W_packed,
+                              const fmpq_epilogue* epilogue, void* Y, int32_t dtype, int64_t ldy, void* workspace,
+                              size_t workspace_bytes, void* stream);
+/* The rows of X [rows][ldx] in groups, one for each expert, in any order and with gaps: expert e has the rows from start[e]
+ * on, count[e] of them; count = NULL: start has experts + 1 entries and the group of e ends at start[e + 1]. Both int32, on
+ * the device, cut to [0, rows]; a group that ends before it starts is empty; groups must not share rows. Rows of no
+ * group are left as they were in Y. row_weight: fp32 [rows] or NULL (1). A plan of moe_plan serves as start and count. */
+FMPQ_API fmpq_status w16_grouped_gemm(const w16_layer* layer, const void* X, int64_t ldx, int64_t rows, const int32_t* start,
+                                      const int32_t* count, const void* W_packed, const fmpq_epilogue* epilogue,
+                                      const float* row_weight, void* Y, int32_t dtype, int64_t ldy, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 FMPQ_API const char* fmpq_status_string(fmpq_status status);
 
