@@ -10,75 +10,97 @@
 // registers of one CTA (8 channels a vector, kV vectors a thread); a layer norm's variance is the mean of the squared
 // differences, a second reduction over those registers.
 #include "fmpq_device.cuh"
+#include "fmpq_internal.h"
 #include "fp8_codes.cuh"
 #include "fp8_internal.h"
 
 namespace fmpq {
 namespace {
 
+// Arithmetic runs on pairs (packed FP32 instructions): a vector of 8 channels is four of them.
+using V8 = float2[4];
+
+// How the vectors of a kernel lie: kWhole: K is a multiple of 8 and rows, weights and outputs are on 16-byte boundaries, so every
+// vector below K is a 16-byte access; kMixed: a row's last vector may be partial; kSingle: elements one by one.
+enum { kWhole = 0, kMixed = 1, kSingle = 2 };
+// Which norm: known to the compiler, or a branch.
+enum { kRms = 0, kLayer = 1, kEither = 2 };
+
+template <int kNorm>
+__device__ __forceinline__ bool is_layer(const BlockNormArgs& p) { return kNorm == kEither ? p.layer_norm != 0 : kNorm == kLayer; }
+
 // ---------------------------------------------------------------- eight values of a row or a vector
 
-template <typename T>
-__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const float2 f = unpack2(w[c], static_cast<const T*>(nullptr));
-        v[2 * c] = f.x;
-        v[2 * c + 1] = f.y;
-    }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+    return *reinterpret_cast<float2*>(&d);
 }
-__device__ __forceinline__ uint32_t pack2(float lo, float hi, const __half*) {
-    const __half2 v = __floats2half2_rn(lo, hi);
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4& u, V8& v) {
+    const T* t = nullptr;
+    v[0] = unpack2(u.x, t);
+    v[1] = unpack2(u.y, t);
+    v[2] = unpack2(u.z, t);
+    v[3] = unpack2(u.w, t);
+}
+__device__ __forceinline__ uint32_t pack2(float2 f, const __half*) {
+    const __half2 v = __floats2half2_rn(f.x, f.y);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ uint32_t pack2(float lo, float hi, const __nv_bfloat16*) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+__device__ __forceinline__ uint32_t pack2(float2 f, const __nv_bfloat16*) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(f.x, f.y);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 __device__ __forceinline__ void store1(__half* p, float v) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ float& at(V8& v, int c) { return (c & 1) ? v[c >> 1].y : v[c >> 1].x; }
+__device__ __forceinline__ float at(const V8& v, int c) { return (c & 1) ? v[c >> 1].y : v[c >> 1].x; }
 
-// Channels k .. k + 7 of a row, those past K as 0.
-template <typename T, bool kVec>
-__device__ __forceinline__ void load8(const T* row, int k, int K, float (&v)[8]) {
-    if (kVec && k + 8 <= K) {
+// Channels k .. k + 7 of a row, those past K as 0 (kWhole: k < K).
+template <typename T, int kLie>
+__device__ __forceinline__ void load8(const T* row, int k, int K, V8& v) {
+    if (kLie == kWhole || (kLie == kMixed && k + 8 <= K)) {
         unpack8<T>(*reinterpret_cast<const uint4*>(row + k), v);
     } else {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] = k + c < K ? load_as_float(row + k + c) : 0.0f;
+        for (int c = 0; c < 8; ++c) at(v, c) = k + c < K ? load_as_float(row + k + c) : 0.0f;
     }
 }
-template <typename T, bool kVec>
-__device__ __forceinline__ void store8(T* row, int k, int K, const float (&v)[8]) {
-    if (kVec && k + 8 <= K) {
+template <typename T, int kLie>
+__device__ __forceinline__ void store8(T* row, int k, int K, const V8& v) {
+    if (kLie == kWhole || (kLie == kMixed && k + 8 <= K)) {
         const T* t = nullptr;
-        *reinterpret_cast<uint4*>(row + k) =
-            make_uint4(pack2(v[0], v[1], t), pack2(v[2], v[3], t), pack2(v[4], v[5], t), pack2(v[6], v[7], t));
+        *reinterpret_cast<uint4*>(row + k) = make_uint4(pack2(v[0], t), pack2(v[1], t), pack2(v[2], t), pack2(v[3], t));
     } else {
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-            if (k + c < K) store1(row + k + c, v[c]);
+            if (k + c < K) store1(row + k + c, at(v, c));
     }
 }
 // The same of a weight, bias or gate: of X's type, or FP32.
-template <typename T, bool kVec>
-__device__ __forceinline__ void param8(const void* p, int fp32, int64_t first, int k, int K, float (&v)[8]) {
+template <typename T, int kLie>
+__device__ __forceinline__ void param8(const void* p, int fp32, int64_t first, int k, int K, V8& v) {
     if (!fp32) {
-        load8<T, kVec>(static_cast<const T*>(p) + first, k, K, v);
+        load8<T, kLie>(static_cast<const T*>(p) + first, k, K, v);
         return;
     }
     const float* f = static_cast<const float*>(p) + first + k;
-    if (kVec && k + 8 <= K) {
+    if (kLie == kWhole || (kLie == kMixed && k + 8 <= K)) {
         const float4 a = *reinterpret_cast<const float4*>(f), b = *reinterpret_cast<const float4*>(f + 4);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        v[0] = make_float2(a.x, a.y), v[1] = make_float2(a.z, a.w), v[2] = make_float2(b.x, b.y), v[3] = make_float2(b.z, b.w);
     } else {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] = k + c < K ? f[c] : 0.0f;
+        for (int c = 0; c < 8; ++c) at(v, c) = k + c < K ? f[c] : 0.0f;
     }
 }
 
 // ---------------------------------------------------------------- sums over a row
+
+constexpr int kMostStages = 4;   // rows in flight a CTA
 
 struct Sums {
     float part[2][32];
@@ -104,55 +126,102 @@ __device__ __forceinline__ float row_sum(float v, Sums& s, int& turn) {
 
 // ---------------------------------------------------------------- one step of a vector of eight
 
-template <typename T, bool kVec>
-__device__ __forceinline__ void scale8(const BlockNormArgs& p, float (&v)[8], float mean, float inv, const void* w,
-                                       const void* b, int k) {
-    float t[8];
+__device__ __forceinline__ void add8(float& sum, const V8& v) {
+    const float2 a = fadd2(fadd2(v[0], v[1]), fadd2(v[2], v[3]));
+    sum += a.x + a.y;
+}
+// sum += (v - mean)^2; a layer norm's values past K do not count (the others are 0 there)
+template <int kLie, int kNorm>
+__device__ __forceinline__ void square8(const BlockNormArgs& p, float2& sum, const V8& v, float mean, int k) {
+    if (!is_layer<kNorm>(p)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum = dev::ffma2(v[i], v[i], sum);
+        return;
+    }
+    if (kLie == kWhole && k >= p.K) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float2 d = fadd2(v[i], both(-mean));
+        if (kLie != kWhole) {
+            if (k + 2 * i >= p.K) d.x = 0.0f;
+            if (k + 2 * i + 1 >= p.K) d.y = 0.0f;
+        }
+        sum = dev::ffma2(d, d, sum);
+    }
+}
+__device__ __forceinline__ float inverse(const BlockNormArgs& p, float mean_square) { return rsqrtf(mean_square + p.eps); }
+
+template <typename T, int kLie, int kNorm>
+__device__ __forceinline__ void scale8(const BlockNormArgs& p, V8& v, float mean, float inv, const void* w, const void* b, int k) {
+    V8 t;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (is_layer<kNorm>(p)) v[i] = fadd2(v[i], both(-mean));
+        v[i] = dev::fmul2(v[i], both(inv));
+    }
     if (w != nullptr) {
-        param8<T, kVec>(w, p.param_f32, 0, k, p.K, t);
+        param8<T, kLie>(w, p.param_f32, 0, k, p.K, t);
+        if (p.weight_offset != 0.0f)
 #pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] = (v[c] - mean) * inv * (p.weight_offset + t[c]);
-    } else {
+            for (int i = 0; i < 4; ++i) t[i] = fadd2(t[i], both(p.weight_offset));
 #pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] = (v[c] - mean) * inv;
+        for (int i = 0; i < 4; ++i) v[i] = dev::fmul2(v[i], t[i]);
     }
     if (b != nullptr) {
-        param8<T, kVec>(b, p.param_f32, 0, k, p.K, t);
+        param8<T, kLie>(b, p.param_f32, 0, k, p.K, t);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] += t[c];
+        for (int i = 0; i < 4; ++i) v[i] = fadd2(v[i], t[i]);
     }
 }
 
 // u to r; residual already read.
-template <typename T, bool kVec>
-__device__ __forceinline__ void join8(const BlockNormArgs& p, float (&v)[8], const float (&res)[8], int64_t gate_row, int k) {
+template <typename T, int kLie>
+__device__ __forceinline__ void join8(const BlockNormArgs& p, V8& v, const V8& res, int64_t gate_row, int k) {
     if (p.gate != nullptr) {
-        float t[8];
-        param8<T, kVec>(p.gate, p.gate_f32, gate_row, k, p.K, t);
+        V8 t;
+        param8<T, kLie>(p.gate, p.gate_f32, gate_row, k, p.K, t);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] *= t[c];
+        for (int i = 0; i < 4; ++i) v[i] = dev::fmul2(v[i], t[i]);
     }
     if (p.residual != nullptr)
 #pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] = fmaf(p.residual_scale, res[c], v[c]);
+        for (int i = 0; i < 4; ++i) v[i] = dev::ffma2(both(p.residual_scale), res[i], v[i]);
+}
+// First element of the gate's row for row m. (M is at most 2^24: 32 bits do.)
+__device__ __forceinline__ int64_t gate_row_of(const BlockNormArgs& p, int64_t m) {
+    if (p.gate == nullptr || p.gate_tokens >= p.M) return 0;
+    return static_cast<int64_t>(static_cast<uint32_t>(m) / static_cast<uint32_t>(p.gate_tokens)) * p.ldg;
 }
 
-// y to memory: 16 bits, and codes (16 lanes of a half warp hold a block of 128; every lane calls it).
-template <typename T, bool kVec>
-__device__ __forceinline__ void put8(const BlockNormArgs& p, int64_t m, int k, const float (&v)[8]) {
-    if (p.Y != nullptr && k < p.K) store8<T, kVec>(static_cast<T*>(p.Y) + m * p.ldy, k, p.K, v);
-    if (p.A == nullptr) return;
-    uint32_t amax = 0u;   // as bits, NaN is above every number
-#pragma unroll
-    for (int c = 0; c < 8; ++c) amax = max(amax, k + c < p.K ? __float_as_uint(fabsf(v[c])) : 0u);
+// The largest of three magnitudes; NaN if one is.
+__device__ __forceinline__ float most3(float a, float b, float c) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// The scale of a block of 128 channels from the vectors of the 16 lanes of a half warp (every lane calls it).
+__device__ __forceinline__ float scale_of(const V8& v) {
+    const float mine = most3(most3(v[0].x, v[0].y, v[1].x), most3(v[1].y, v[2].x, v[2].y), most3(v[3].x, v[3].y, 0.0f));
+    uint32_t amax = __float_as_uint(mine);   // as bits, NaN is above every number
 #pragma unroll
     for (int d = 8; d > 0; d >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+    return __fdiv_rn(__uint_as_float(amax), kQMax);
+}
+
+// y to memory: 16 bits, and codes (16 lanes of a half warp hold a block of 128; every lane calls it, with 0 past K).
+template <typename T, int kLie>
+__device__ __forceinline__ void put8(const BlockNormArgs& p, int64_t m, int k, V8& v) {
+    if (p.Y != nullptr && k < p.K) store8<T, kLie>(static_cast<T*>(p.Y) + m * p.ldy, k, p.K, v);
+    if (p.A == nullptr) return;
+    if (kLie != kWhole && k < p.K && k + 8 > p.K)
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (k + c >= p.K) at(v, c) = 0.0f;
+    const float s = scale_of(v);
     const int b = k >> 7;
     if (b >= p.nb) return;
-    float q[8];
-#pragma unroll
-    for (int c = 0; c < 8; ++c) q[c] = k + c < p.K ? v[c] : 0.0f;
-    const float s = __fdiv_rn(__uint_as_float(amax), kQMax);
+    const float q[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
     const uint2 code = codes_of(q, s);
     const int l = (k >> 3) & 15;
     uint8_t* row = p.A + (static_cast<int64_t>(b) * p.M + m) * 128;
@@ -160,141 +229,280 @@ __device__ __forceinline__ void put8(const BlockNormArgs& p, int64_t m, int k, c
     if (l == 0) p.a_scales[b * p.sstride + m] = s;
 }
 
-// mean and 1 / sqrt(mean square + eps) of the CTA's row from its registers.
-template <int kV>
-__device__ __forceinline__ void statistics(const BlockNormArgs& p, const float (&v)[kV][8], Sums& s, int& turn, float& mean,
-                                           float& inv) {
+// mean and 1 / sqrt(mean square + eps) of the CTA's row from its registers (0 past K).
+template <int kLie, int kNorm, int kV>
+__device__ __forceinline__ void statistics(const BlockNormArgs& p, const V8 (&v)[kV], Sums& s, int& turn, float& mean, float& inv) {
     mean = 0.0f;
-    const float count = static_cast<float>(p.K);
-    if (p.layer_norm) {
+    if (is_layer<kNorm>(p)) {
         float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kV; ++i)
-#pragma unroll
-            for (int c = 0; c < 8; ++c) sum += v[i][c];
-        mean = row_sum(sum, s, turn) / count;
+        for (int i = 0; i < kV; ++i) add8(sum, v[i]);
+        mean = row_sum(sum, s, turn) * p.inv_count;
     }
-    float sq = 0.0f;
+    float2 sq = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < kV; ++i) {
-        const int k = (i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * 8;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            const float d = v[i][c] - mean;   // (values past K are 0, and do not count)
-            if (!p.layer_norm || k + c < p.K) sq = fmaf(d, d, sq);
-        }
-    }
-    inv = __frsqrt_rn(row_sum(sq, s, turn) / count + p.eps);
+    for (int i = 0; i < kV; ++i) square8<kLie, kNorm>(p, sq, v[i], mean, (i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * 8);
+    inv = inverse(p, row_sum(sq.x + sq.y, s, turn) * p.inv_count);
 }
 
+// ---------------------------------------------------------------- kernels
+
 // One CTA a row, kV vectors of 8 channels a thread: blockDim.x * 8 * kV >= nb * 128.
-template <typename T, bool kVec, int kV>
+template <typename T, int kLie, int kV>
 __global__ void __launch_bounds__(kV == 1 ? 1024 : 512) block_norm_kernel(const BlockNormArgs p) {
     __shared__ Sums sums;
     int turn = 0;
     for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
         const T* x = static_cast<const T*>(p.X) + m * p.ldx;
         const T* res = static_cast<const T*>(p.residual) + m * p.ldr;
-        const int64_t gate_row = p.gate != nullptr ? m / p.gate_tokens * p.ldg : 0;
-        float v[kV][8], add[kV][8];
+        const int64_t gate_row = gate_row_of(p, m);
+        V8 v[kV], add[kV];
         auto channel = [&](int i) { return (i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * 8; };
 #pragma unroll
-        for (int i = 0; i < kV; ++i) load8<T, kVec>(x, channel(i), p.K, v[i]);
+        for (int i = 0; i < kV; ++i) load8<T, kLie>(x, channel(i), p.K, v[i]);
         if (p.residual != nullptr)
 #pragma unroll
-            for (int i = 0; i < kV; ++i) load8<T, kVec>(res, channel(i), p.K, add[i]);
+            for (int i = 0; i < kV; ++i) load8<T, kLie>(res, channel(i), p.K, add[i]);
         float mean, inv;
-        if (p.post_norm) {
-            statistics(p, v, sums, turn, mean, inv);
-#pragma unroll
-            for (int i = 0; i < kV; ++i)
-                if (channel(i) < p.K) scale8<T, kVec>(p, v[i], mean, inv, p.post_weight, p.post_bias, channel(i));
-        }
+        if (p.post_norm) statistics<kLie, kEither>(p, v, sums, turn, mean, inv);
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
             if (channel(i) >= p.K) continue;
-            join8<T, kVec>(p, v[i], add[i], gate_row, channel(i));
-            // (past K: a post norm's value of 0 is not 0)
-            if (channel(i) + 8 > p.K)
+            if (p.post_norm) scale8<T, kLie, kEither>(p, v[i], mean, inv, p.post_weight, p.post_bias, channel(i));
+            join8<T, kLie>(p, v[i], add[i], gate_row, channel(i));
+            if (channel(i) + 8 > p.K)   // (a post norm's value of 0 is not 0)
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
-                    if (channel(i) + c >= p.K) v[i][c] = 0.0f;
-            if (p.R != nullptr) store8<T, kVec>(static_cast<T*>(p.R) + m * p.ldo, channel(i), p.K, v[i]);
+                    if (channel(i) + c >= p.K) at(v[i], c) = 0.0f;
+            if (p.R != nullptr) store8<T, kLie>(static_cast<T*>(p.R) + m * p.ldo, channel(i), p.K, v[i]);
         }
         if (!p.pre_norm) continue;
-        statistics(p, v, sums, turn, mean, inv);
+        statistics<kLie, kEither>(p, v, sums, turn, mean, inv);
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
-            if (channel(i) < p.K) scale8<T, kVec>(p, v[i], mean, inv, p.weight, p.bias, channel(i));
-            put8<T, kVec>(p, m, channel(i), v[i]);
+            if (channel(i) < p.K) scale8<T, kLie, kEither>(p, v[i], mean, inv, p.weight, p.bias, channel(i));
+            put8<T, kLie>(p, m, channel(i), v[i]);
         }
     }
 }
 
 // Rows that do not fit the registers: X and residual are read again (from the L2) for each sum and for the outputs. A thread
 // reads a position of X and residual last before it writes there, so that R and Y may be their buffers.
-template <typename T, bool kVec>
+template <typename T, int kLie>
 __global__ void __launch_bounds__(1024) block_norm_long_kernel(const BlockNormArgs p) {
     __shared__ Sums sums;
     int turn = 0;
-    const float count = static_cast<float>(p.K);
     for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
         const T* x = static_cast<const T*>(p.X) + m * p.ldx;
         const T* res = static_cast<const T*>(p.residual) + m * p.ldr;
-        const int64_t gate_row = p.gate != nullptr ? m / p.gate_tokens * p.ldg : 0;
+        const int64_t gate_row = gate_row_of(p, m);
         float mean[2] = {0.0f, 0.0f}, inv[2] = {1.0f, 1.0f};   // of X, of r
-        auto value = [&](int which, int k, float (&v)[8]) {   // X (0) or r (1) at channels k .. k + 7, 0 past K
-            load8<T, kVec>(x, k, p.K, v);
+        auto value = [&](int which, int k, V8& v) {   // X (0) or r (1) at channels k .. k + 7, 0 past K
+            load8<T, kLie>(x, k, p.K, v);
             if (which == 0) return;
-            float add[8];
-            if (p.residual != nullptr) load8<T, kVec>(res, k, p.K, add);
-            if (p.post_norm) scale8<T, kVec>(p, v, mean[0], inv[0], p.post_weight, p.post_bias, k);
-            join8<T, kVec>(p, v, add, gate_row, k);
+            V8 add;
+            if (p.residual != nullptr) load8<T, kLie>(res, k, p.K, add);
+            if (p.post_norm) scale8<T, kLie, kEither>(p, v, mean[0], inv[0], p.post_weight, p.post_bias, k);
+            join8<T, kLie>(p, v, add, gate_row, k);
             if (k + 8 > p.K)
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
-                    if (k + c >= p.K) v[c] = 0.0f;
+                    if (k + c >= p.K) at(v, c) = 0.0f;
         };
+#pragma unroll
         for (int which = 0; which < 2; ++which) {
             if (which == 0 ? !p.post_norm : !p.pre_norm) continue;
             if (p.layer_norm) {
                 float sum = 0.0f;
                 for (int k = static_cast<int>(threadIdx.x) * 8; k < p.K; k += static_cast<int>(blockDim.x) * 8) {
-                    float v[8];
+                    V8 v;
                     value(which, k, v);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) sum += v[c];
+                    add8(sum, v);
                 }
-                mean[which] = row_sum(sum, sums, turn) / count;
+                mean[which] = row_sum(sum, sums, turn) * p.inv_count;
             }
-            float sq = 0.0f;
+            float2 sq = make_float2(0.0f, 0.0f);
             for (int k = static_cast<int>(threadIdx.x) * 8; k < p.K; k += static_cast<int>(blockDim.x) * 8) {
-                float v[8];
+                V8 v;
                 value(which, k, v);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const float d = v[c] - mean[which];
-                    if (!p.layer_norm || k + c < p.K) sq = fmaf(d, d, sq);
-                }
+                square8<kLie, kEither>(p, sq, v, mean[which], k);
             }
-            inv[which] = __frsqrt_rn(row_sum(sq, sums, turn) / count + p.eps);
+            inv[which] = inverse(p, row_sum(sq.x + sq.y, sums, turn) * p.inv_count);
         }
         const int end = p.nb * 128;   // (whole half warps: K is rounded up to a block)
         for (int k0 = 0; k0 < end; k0 += static_cast<int>(blockDim.x) * 8) {
             const int k = k0 + static_cast<int>(threadIdx.x) * 8;
-            float v[8] = {};
+            V8 v = {};
             if (k < p.K) {
                 value(1, k, v);
-                if (p.R != nullptr) store8<T, kVec>(static_cast<T*>(p.R) + m * p.ldo, k, p.K, v);
+                if (p.R != nullptr) store8<T, kLie>(static_cast<T*>(p.R) + m * p.ldo, k, p.K, v);
             }
             if (!p.pre_norm) continue;
-            if (k < p.K) scale8<T, kVec>(p, v, mean[1], inv[1], p.weight, p.bias, k);
-            put8<T, kVec>(p, m, k, v);
+            if (k < p.K) scale8<T, kLie, kEither>(p, v, mean[1], inv[1], p.weight, p.bias, k);
+            put8<T, kLie>(p, m, k, v);
         }
     }
 }
 
-template <typename T, bool kVec>
+// Many rows on 16-byte boundaries: the CTAs stay, and the next rows are on their way into a ring in shared memory (bulk
+// copies) while one is worked on. Two vectors a thread. Its instructions bound it (4096 x 8192 bf16, both norms, a gate, codes: 59 us,
+// 4.0 TB/s, an issue slot used in 73 of 100; one norm and the residual 45; the sum alone 33, the copy rate), so what can be is uniform
+// or made once: a row's addresses are a base for the CTA and 32-bit offsets of a thread, arithmetic is on pairs, P (the weights'
+// type) and the norm are the compiler's. One CTA a row without the ring took 138, four vectors a thread 66, three CTAs of 40
+// registers in place of two 60, the weights in shared memory, which leave the ring two rows, 60.
+template <typename P>
+__device__ __forceinline__ void param_at(const void* p, uint32_t k, V8& v) {
+    if constexpr (sizeof(P) == 2) {
+        unpack8<P>(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + k * 2u)), v);
+    } else {
+        const float4* f = reinterpret_cast<const float4*>(static_cast<const uint8_t*>(p) + k * 4u);
+        const float4 a = __ldg(f), b = __ldg(f + 1);
+        v[0] = make_float2(a.x, a.y), v[1] = make_float2(a.z, a.w), v[2] = make_float2(b.x, b.y), v[3] = make_float2(b.z, b.w);
+    }
+}
+
+template <typename T, typename P, int kNorm>
+__global__ void __launch_bounds__(1024) block_norm_stream_kernel(const BlockNormArgs p, int stages) {
+    constexpr int kV = 2;
+    extern __shared__ __align__(128) uint8_t ring[];   // [stage][X's row, then the residual's]
+    __shared__ Sums sums;
+    __shared__ uint64_t landed[kMostStages];
+    const uint32_t row_bytes = static_cast<uint32_t>(p.K) * 2, slot_bytes = p.residual != nullptr ? 2 * row_bytes : row_bytes;
+    const int rows = static_cast<int>(p.M), step = static_cast<int>(gridDim.x);
+    auto load = [&](int m, int stage) {
+        dev::mbar_arrive_expect_tx(&landed[stage], slot_bytes);
+        dev::bulk_g2s(ring + stage * slot_bytes, static_cast<const T*>(p.X) + m * p.ldx, row_bytes, &landed[stage]);
+        if (p.residual != nullptr)
+            dev::bulk_g2s(ring + stage * slot_bytes + row_bytes, static_cast<const T*>(p.residual) + m * p.ldr, row_bytes, &landed[stage]);
+    };
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i) dev::mbar_init(&landed[i], 1);
+        dev::fence_barrier_init();
+        for (int i = 0; i < stages; ++i)
+            if (blockIdx.x + static_cast<int64_t>(i) * step < rows) load(static_cast<int>(blockIdx.x) + i * step, i);
+    }
+    __syncthreads();
+
+    // this thread's vectors: first channel, whether there is one, places of codes and scale
+    uint32_t k[kV], code_at[kV], scale_at[kV];
+    bool in[kV];
+    const uint32_t l = threadIdx.x & 15u, piece = (l >> 1) << 4;
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+        k[i] = (i * blockDim.x + threadIdx.x) * 8u;
+        in[i] = k[i] < static_cast<uint32_t>(p.K);
+        code_at[i] = (k[i] >> 7) * static_cast<uint32_t>(p.M) * 128u + (l & 1u) * 8u;
+        scale_at[i] = (k[i] >> 7) * static_cast<uint32_t>(p.sstride) * 4u;
+    }
+    const bool single = blockDim.x == 32;
+    int turn = 0, stage = 0;
+    uint32_t phase = 0;
+    for (int m = static_cast<int>(blockIdx.x); m < rows; m += step) {
+        // (a copy that this CTA issued lands; should one not, within about a second, its row comes out NaN)
+        const bool there = dev::mbar_wait(&landed[stage], phase, nullptr);
+        const uint8_t* x = ring + stage * slot_bytes;
+        V8 v[kV];
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[i][c] = both(there ? 0.0f : __int_as_float(0x7FFFFFFF));
+            if (in[i] && there) unpack8<T>(*reinterpret_cast<const uint4*>(x + k[i] * 2u), v[i]);
+        }
+        float mean = 0.0f, inv;
+        // v = (v - mean) * inv * w + b
+        auto scale = [&](const void* w, const void* b) {
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                V8 t;
+                if (kNorm == kLayer)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) v[i][c] = fadd2(v[i][c], both(-mean));
+                if (w != nullptr && in[i]) {
+                    param_at<P>(w, k[i], t);
+                    if (p.weight_offset != 0.0f)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) t[c] = fadd2(t[c], both(p.weight_offset));
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) v[i][c] = dev::fmul2(dev::fmul2(v[i][c], both(inv)), t[c]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) v[i][c] = dev::fmul2(v[i][c], both(inv));
+                }
+                if (b != nullptr && in[i]) {
+                    param_at<P>(b, k[i], t);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) v[i][c] = fadd2(v[i][c], t[c]);
+                }
+                if (kNorm == kLayer && !in[i])
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) v[i][c] = both(0.0f);
+            }
+        };
+        if (p.post_norm) {
+            statistics<kWhole, kNorm>(p, v, sums, turn, mean, inv);
+            scale(p.post_weight, p.post_bias);
+        }
+        if (p.gate != nullptr) {
+            const int64_t gate_row = gate_row_of(p, m);
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                if (!in[i]) continue;
+                V8 t;
+                if (p.gate_f32) param_at<float>(static_cast<const float*>(p.gate) + gate_row, k[i], t);
+                else param_at<T>(static_cast<const T*>(p.gate) + gate_row, k[i], t);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) v[i][c] = dev::fmul2(v[i][c], t[c]);
+            }
+        }
+        if (p.residual != nullptr) {
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                if (!in[i]) continue;
+                V8 t;
+                unpack8<T>(*reinterpret_cast<const uint4*>(x + row_bytes + k[i] * 2u), t);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) v[i][c] = dev::ffma2(both(p.residual_scale), t[c], v[i][c]);
+            }
+        }
+        if (p.R != nullptr) {
+            uint8_t* row = static_cast<uint8_t*>(p.R) + m * p.ldo * 2;
+#pragma unroll
+            for (int i = 0; i < kV; ++i)
+                if (in[i]) store8<T, kWhole>(reinterpret_cast<T*>(row + k[i] * 2u), 0, p.K, v[i]);
+        }
+        if (p.pre_norm) statistics<kWhole, kNorm>(p, v, sums, turn, mean, inv);
+        if (!p.pre_norm || single) __syncthreads();   // (else the statistics' own barrier)
+        // every thread has read the row
+        if (threadIdx.x == 0 && m + static_cast<int64_t>(stages) * step < rows) load(m + stages * step, stage);
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1;
+        }
+        if (!p.pre_norm) continue;
+        scale(p.weight, p.bias);
+        if (p.Y != nullptr) {
+            uint8_t* row = static_cast<uint8_t*>(p.Y) + m * p.ldy * 2;
+#pragma unroll
+            for (int i = 0; i < kV; ++i)
+                if (in[i]) store8<T, kWhole>(reinterpret_cast<T*>(row + k[i] * 2u), 0, p.K, v[i]);
+        }
+        if (p.A != nullptr) {
+            uint8_t* codes = p.A + static_cast<int64_t>(m) * 128;
+            uint8_t* scales = reinterpret_cast<uint8_t*>(p.a_scales + m);
+            const uint32_t swizzled = piece ^ ((m & 7) << 4);
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                const float s = scale_of(v[i]);
+                if (k[i] >= static_cast<uint32_t>(p.nb) * 128u) continue;
+                const float q[8] = {v[i][0].x, v[i][0].y, v[i][1].x, v[i][1].y, v[i][2].x, v[i][2].y, v[i][3].x, v[i][3].y};
+                *reinterpret_cast<uint2*>(codes + (code_at[i] + swizzled)) = codes_of(q, s);
+                if (l == 0) *reinterpret_cast<float*>(scales + scale_at[i]) = s;
+            }
+        }
+    }
+}
+
+template <typename T, int kLie>
 cudaError_t block_norm_as(const BlockNormArgs& p, int num_sms, cudaStream_t stream) {
     const int vectors = p.nb * 16;   // of 8 channels
     const int64_t most = static_cast<int64_t>(num_sms) * 64;
@@ -302,14 +510,27 @@ cudaError_t block_norm_as(const BlockNormArgs& p, int num_sms, cudaStream_t stre
     auto threads_for = [&](int per) { return ((vectors + per - 1) / per + 31) / 32 * 32; };
     // few rows: as many threads a row as there are vectors, for the shortest chain; else 4 vectors a thread
     const bool few = p.M < 2 * num_sms;
-    if (few && threads_for(1) <= 1024) {
-        block_norm_kernel<T, kVec, 1><<<grid, threads_for(1), 0, stream>>>(p);
+    if (kLie == kMixed && !few && p.K % 8 == 0 && p.K >= 512 && threads_for(2) <= 1024 &&
+        p.M * p.nb * 128 < INT64_C(1) << 32) {   // (32-bit offsets of the codes)
+        auto fn = p.param_f32 ? (p.layer_norm ? block_norm_stream_kernel<T, float, kLayer> : block_norm_stream_kernel<T, float, kRms>)
+                              : (p.layer_norm ? block_norm_stream_kernel<T, T, kLayer> : block_norm_stream_kernel<T, T, kRms>);
+        const int threads = threads_for(2), slot = p.K * (p.residual != nullptr ? 4 : 2);
+        int resident = 1024 / threads;   // (64 registers a thread)
+        if (resident > 16) resident = 16;
+        int stages = 200 * 1024 / resident / slot;
+        stages = stages > kMostStages ? kMostStages : stages < 2 ? 2 : stages;
+        const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), 220 * 1024);
+        if (e != cudaSuccess) return e;
+        const int64_t ctas = static_cast<int64_t>(num_sms) * resident;
+        fn<<<static_cast<unsigned>(p.M < ctas ? p.M : ctas), threads, stages * slot, stream>>>(p, stages);
+    } else if (few && threads_for(1) <= 1024) {
+        block_norm_kernel<T, kLie, 1><<<grid, threads_for(1), 0, stream>>>(p);
     } else if (threads_for(4) <= 512) {
-        if (threads_for(4) >= 128) block_norm_kernel<T, kVec, 4><<<grid, threads_for(4), 0, stream>>>(p);
-        else if (threads_for(2) >= 64) block_norm_kernel<T, kVec, 2><<<grid, threads_for(2), 0, stream>>>(p);
-        else block_norm_kernel<T, kVec, 1><<<grid, threads_for(1), 0, stream>>>(p);
+        if (threads_for(4) >= 128) block_norm_kernel<T, kLie, 4><<<grid, threads_for(4), 0, stream>>>(p);
+        else if (threads_for(2) >= 64) block_norm_kernel<T, kLie, 2><<<grid, threads_for(2), 0, stream>>>(p);
+        else block_norm_kernel<T, kLie, 1><<<grid, threads_for(1), 0, stream>>>(p);
     } else {
-        block_norm_long_kernel<T, kVec><<<grid, 1024, 0, stream>>>(p);
+        block_norm_long_kernel<T, kLie><<<grid, 1024, 0, stream>>>(p);
     }
     return cudaGetLastError();
 }
@@ -322,8 +543,8 @@ cudaError_t launch_block_norm(const BlockNormArgs& p, int num_sms, cudaStream_t 
                      aligned(p.Y) && p.ldy % 8 == 0 && aligned(p.gate) && p.ldg % 8 == 0 && aligned(p.weight) && aligned(p.bias) &&
                      aligned(p.post_weight) && aligned(p.post_bias);
     if (p.dtype == kF16)
-        return vec ? block_norm_as<__half, true>(p, num_sms, stream) : block_norm_as<__half, false>(p, num_sms, stream);
-    return vec ? block_norm_as<__nv_bfloat16, true>(p, num_sms, stream) : block_norm_as<__nv_bfloat16, false>(p, num_sms, stream);
+        return vec ? block_norm_as<__half, kMixed>(p, num_sms, stream) : block_norm_as<__half, kSingle>(p, num_sms, stream);
+    return vec ? block_norm_as<__nv_bfloat16, kMixed>(p, num_sms, stream) : block_norm_as<__nv_bfloat16, kSingle>(p, num_sms, stream);
 }
 
 }  // namespace fmpq

@@ -282,6 +282,7 @@ fmpq_status fmpq_block_norm(const fmpq_block_norm_args* args, void* stream) {
     p.eps = a.eps;
     p.residual_scale = a.residual_scale;
     p.weight_offset = a.weight_offset;
+    p.inv_count = 1.0f / static_cast<float>(a.K);
     return launched(fmpq::launch_block_norm(p, sms, st(stream)));
 }
 

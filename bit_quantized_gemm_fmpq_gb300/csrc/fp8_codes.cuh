@@ -4,6 +4,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "fmpq_device.cuh"
+
 namespace fmpq {
 namespace {
 
@@ -30,11 +32,13 @@ __device__ __forceinline__ uint2 codes_of(const float (&v)[8], float s) {
     float inv;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
     const float lo = inv * (1.0f - 4.76837158e-7f), hi = inv * (1.0f + 4.76837158e-7f);
-    uint2 code, other;
-    code.x = e4m3x2(v[0] * lo, v[1] * lo) | (e4m3x2(v[2] * lo, v[3] * lo) << 16);
-    code.y = e4m3x2(v[4] * lo, v[5] * lo) | (e4m3x2(v[6] * lo, v[7] * lo) << 16);
-    other.x = e4m3x2(v[0] * hi, v[1] * hi) | (e4m3x2(v[2] * hi, v[3] * hi) << 16);
-    other.y = e4m3x2(v[4] * hi, v[5] * hi) | (e4m3x2(v[6] * hi, v[7] * hi) << 16);
+    auto codes = [&](float f) {
+        const float2 w = make_float2(f, f);
+        const float2 a = dev::fmul2(make_float2(v[0], v[1]), w), b = dev::fmul2(make_float2(v[2], v[3]), w);
+        const float2 c = dev::fmul2(make_float2(v[4], v[5]), w), d = dev::fmul2(make_float2(v[6], v[7]), w);
+        return make_uint2(e4m3x2(a.x, a.y) | (e4m3x2(b.x, b.y) << 16), e4m3x2(c.x, c.y) | (e4m3x2(d.x, d.y) << 16));
+    };
+    const uint2 code = codes(lo), other = codes(hi);
     if (s >= 1.17549435e-38f && s <= 1e37f && code.x == other.x && code.y == other.y) return code;
     if (!(s > 0.0f)) return make_uint2(0u, 0u);
     float q[8];

@@ -119,7 +119,7 @@ struct BlockNormArgs {
     int64_t ldx, ldr, ldg, ldo, ldy, M, gate_tokens, sstride;
     int K, nb, dtype;
     int layer_norm, post_norm, pre_norm, param_f32, gate_f32;
-    float eps, residual_scale, weight_offset;
+    float eps, residual_scale, weight_offset, inv_count;   // inv_count: 1 / K
 };
 cudaError_t launch_block_norm(const BlockNormArgs& p, int num_sms, cudaStream_t stream);
 
