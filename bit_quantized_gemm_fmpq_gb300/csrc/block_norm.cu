@@ -9,6 +9,8 @@
 // Everything between the reads of X and residual and the writes is FP32. A row is read once and kept in the
 // registers of one CTA (8 channels a vector, kV vectors a thread); a layer norm's variance is the mean of the squared
 // differences, a second reduction over those registers.
+#include <initializer_list>
+
 #include "fmpq_device.cuh"
 #include "fmpq_internal.h"
 #include "fp8_codes.cuh"
@@ -21,8 +23,9 @@ namespace {
 using V8 = float2[4];
 
 // How the vectors of a kernel lie: kWhole: K is a multiple of 8 and rows, weights and outputs are on 16-byte boundaries, so every
-// vector below K is a 16-byte access; kMixed: a row's last vector may be partial; kSingle: elements one by one.
-enum { kWhole = 0, kMixed = 1, kSingle = 2 };
+// vector below K is a 16-byte access; kMixed: a row's last vector may be partial; kHalves: the same on 8-byte boundaries, in two
+// accesses; kSingle: elements one by one. (777 x 2868 fp16, a layer norm: kHalves 9.5 us, kSingle 17.)
+enum { kWhole = 0, kMixed = 1, kHalves = 2, kSingle = 3 };
 // Which norm: known to the compiler, or a branch.
 enum { kRms = 0, kLayer = 1, kEither = 2 };
 
@@ -65,6 +68,9 @@ template <typename T, int kLie>
 __device__ __forceinline__ void load8(const T* row, int k, int K, V8& v) {
     if (kLie == kWhole || (kLie == kMixed && k + 8 <= K)) {
         unpack8<T>(*reinterpret_cast<const uint4*>(row + k), v);
+    } else if (kLie == kHalves && k + 8 <= K) {
+        const uint2 a = *reinterpret_cast<const uint2*>(row + k), b = *reinterpret_cast<const uint2*>(row + k + 4);
+        unpack8<T>(make_uint4(a.x, a.y, b.x, b.y), v);
     } else {
 #pragma unroll
         for (int c = 0; c < 8; ++c) at(v, c) = k + c < K ? load_as_float(row + k + c) : 0.0f;
@@ -75,6 +81,10 @@ __device__ __forceinline__ void store8(T* row, int k, int K, const V8& v) {
     if (kLie == kWhole || (kLie == kMixed && k + 8 <= K)) {
         const T* t = nullptr;
         *reinterpret_cast<uint4*>(row + k) = make_uint4(pack2(v[0], t), pack2(v[1], t), pack2(v[2], t), pack2(v[3], t));
+    } else if (kLie == kHalves && k + 8 <= K) {
+        const T* t = nullptr;
+        *reinterpret_cast<uint2*>(row + k) = make_uint2(pack2(v[0], t), pack2(v[1], t));
+        *reinterpret_cast<uint2*>(row + k + 4) = make_uint2(pack2(v[2], t), pack2(v[3], t));
     } else {
 #pragma unroll
         for (int c = 0; c < 8; ++c)
@@ -92,6 +102,9 @@ __device__ __forceinline__ void param8(const void* p, int fp32, int64_t first, i
     if (kLie == kWhole || (kLie == kMixed && k + 8 <= K)) {
         const float4 a = *reinterpret_cast<const float4*>(f), b = *reinterpret_cast<const float4*>(f + 4);
         v[0] = make_float2(a.x, a.y), v[1] = make_float2(a.z, a.w), v[2] = make_float2(b.x, b.y), v[3] = make_float2(b.z, b.w);
+    } else if (kLie == kHalves && k + 8 <= K) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = reinterpret_cast<const float2*>(f)[i];
     } else {
 #pragma unroll
         for (int c = 0; c < 8; ++c) at(v, c) = k + c < K ? f[c] : 0.0f;
@@ -252,6 +265,8 @@ template <typename T, int kLie, int kV>
 __global__ void __launch_bounds__(kV == 1 ? 1024 : 512) block_norm_kernel(const BlockNormArgs p) {
     __shared__ Sums sums;
     int turn = 0;
+    dev::pdl_wait();
+    dev::pdl_launch_dependents();
     for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
         const T* x = static_cast<const T*>(p.X) + m * p.ldx;
         const T* res = static_cast<const T*>(p.residual) + m * p.ldr;
@@ -292,6 +307,8 @@ template <typename T, int kLie>
 __global__ void __launch_bounds__(1024) block_norm_long_kernel(const BlockNormArgs p) {
     __shared__ Sums sums;
     int turn = 0;
+    dev::pdl_wait();
+    dev::pdl_launch_dependents();
     for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
         const T* x = static_cast<const T*>(p.X) + m * p.ldx;
         const T* res = static_cast<const T*>(p.residual) + m * p.ldr;
@@ -378,6 +395,10 @@ __global__ void __launch_bounds__(1024) block_norm_stream_kernel(const BlockNorm
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i) dev::mbar_init(&landed[i], 1);
         dev::fence_barrier_init();
+    }
+    dev::pdl_wait();
+    dev::pdl_launch_dependents();
+    if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i)
             if (blockIdx.x + static_cast<int64_t>(i) * step < rows) load(static_cast<int>(blockIdx.x) + i * step, i);
     }
@@ -508,7 +529,6 @@ cudaError_t block_norm_as(const BlockNormArgs& p, int num_sms, cudaStream_t stre
     const int64_t most = static_cast<int64_t>(num_sms) * 64;
     const unsigned grid = static_cast<unsigned>(p.M < most ? p.M : most);
     auto threads_for = [&](int per) { return ((vectors + per - 1) / per + 31) / 32 * 32; };
-    // few rows: as many threads a row as there are vectors, for the shortest chain; else 4 vectors a thread
     const bool few = p.M < 2 * num_sms;
     if (kLie == kMixed && !few && p.K % 8 == 0 && p.K >= 512 && threads_for(2) <= 1024 &&
         p.M * p.nb * 128 < INT64_C(1) << 32) {   // (32-bit offsets of the codes)
@@ -522,29 +542,37 @@ cudaError_t block_norm_as(const BlockNormArgs& p, int num_sms, cudaStream_t stre
         const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), 220 * 1024);
         if (e != cudaSuccess) return e;
         const int64_t ctas = static_cast<int64_t>(num_sms) * resident;
-        fn<<<static_cast<unsigned>(p.M < ctas ? p.M : ctas), threads, stages * slot, stream>>>(p, stages);
-    } else if (few && threads_for(1) <= 1024) {
-        block_norm_kernel<T, kLie, 1><<<grid, threads_for(1), 0, stream>>>(p);
-    } else if (threads_for(4) <= 512) {
-        if (threads_for(4) >= 128) block_norm_kernel<T, kLie, 4><<<grid, threads_for(4), 0, stream>>>(p);
-        else if (threads_for(2) >= 64) block_norm_kernel<T, kLie, 2><<<grid, threads_for(2), 0, stream>>>(p);
-        else block_norm_kernel<T, kLie, 1><<<grid, threads_for(1), 0, stream>>>(p);
-    } else {
-        block_norm_long_kernel<T, kLie><<<grid, 1024, 0, stream>>>(p);
+        return launch_after(fn, dim3(static_cast<unsigned>(p.M < ctas ? p.M : ctas)), threads, stages * slot, true, stream, p, stages);
     }
-    return cudaGetLastError();
+    // few rows: as many threads a row as there are vectors, for the shortest chain; else up to 4 vectors a thread
+    auto row_kernel = [&](auto kernel, int per) { return launch_after(kernel, dim3(grid), threads_for(per), 0, true, stream, p); };
+    if (few && threads_for(1) <= 1024) return row_kernel(block_norm_kernel<T, kLie, 1>, 1);
+    if (threads_for(4) > 512) return launch_after(block_norm_long_kernel<T, kLie>, dim3(grid), 1024, 0, true, stream, p);
+    if (threads_for(4) >= 128) return row_kernel(block_norm_kernel<T, kLie, 4>, 4);
+    if (threads_for(2) >= 64) return row_kernel(block_norm_kernel<T, kLie, 2>, 2);
+    return row_kernel(block_norm_kernel<T, kLie, 1>, 1);
+}
+
+template <typename T>
+cudaError_t block_norm_of(const BlockNormArgs& p, int num_sms, cudaStream_t stream) {
+    auto on = [&](int bytes) {   // every pointer and row starts on a boundary of `bytes`
+        uintptr_t all = 0;
+        for (const void* v : {p.X, p.residual, static_cast<const void*>(p.R), static_cast<const void*>(p.Y), p.gate, p.weight, p.bias,
+                              p.post_weight, p.post_bias})
+            all |= reinterpret_cast<uintptr_t>(v);
+        for (int64_t ld : {p.ldx, p.ldr, p.ldo, p.ldy}) all |= static_cast<uintptr_t>(ld) * 2;
+        all |= static_cast<uintptr_t>(p.ldg) * (p.gate_f32 ? 4 : 2);
+        return (all & (bytes - 1)) == 0;
+    };
+    if (on(16)) return block_norm_as<T, kMixed>(p, num_sms, stream);
+    if (on(8)) return block_norm_as<T, kHalves>(p, num_sms, stream);
+    return block_norm_as<T, kSingle>(p, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_block_norm(const BlockNormArgs& p, int num_sms, cudaStream_t stream) {
-    auto aligned = [](const void* v) { return (reinterpret_cast<uintptr_t>(v) & 15u) == 0; };
-    const bool vec = aligned(p.X) && p.ldx % 8 == 0 && aligned(p.residual) && p.ldr % 8 == 0 && aligned(p.R) && p.ldo % 8 == 0 &&
-                     aligned(p.Y) && p.ldy % 8 == 0 && aligned(p.gate) && p.ldg % 8 == 0 && aligned(p.weight) && aligned(p.bias) &&
-                     aligned(p.post_weight) && aligned(p.post_bias);
-    if (p.dtype == kF16)
-        return vec ? block_norm_as<__half, kMixed>(p, num_sms, stream) : block_norm_as<__half, kSingle>(p, num_sms, stream);
-    return vec ? block_norm_as<__nv_bfloat16, kMixed>(p, num_sms, stream) : block_norm_as<__nv_bfloat16, kSingle>(p, num_sms, stream);
+    return p.dtype == kF16 ? block_norm_of<__half>(p, num_sms, stream) : block_norm_of<__nv_bfloat16>(p, num_sms, stream);
 }
 
 }  // namespace fmpq

@@ -228,6 +228,13 @@ __device__ __forceinline__ void bulk_wait_group0() { asm volatile("cp.async.bulk
 __device__ __forceinline__ void cp_async16(uint32_t dst_smem, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst_smem), "l"(src) : "memory");
 }
+// The same of 8 bytes, and of a source that is only there if `there` (zeros otherwise).
+template <int kBytes>
+__device__ __forceinline__ void cp_async_if(uint32_t dst_smem, const void* src, bool there) {
+    static_assert(kBytes == 8 || kBytes == 16, "cp.async copies 4, 8 or 16 bytes");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst_smem), "l"(src), "n"(kBytes), "r"(there ? kBytes : 0)
+                 : "memory");
+}
 // Arrive on `bar` once every cp.async this thread has issued so far has completed (the
 // arrival is not pre-counted: the barrier's expected count includes it).
 __device__ __forceinline__ void cp_async_arrive_noinc(uint64_t* bar) {
@@ -405,6 +412,13 @@ __device__ __forceinline__ void tmem_ld16x256b_x4(uint32_t taddr, uint32_t (&r)[
 // (repetition i in registers 4i..4i+3). Written asynchronously: read only after tmem_ld_wait8.
 __device__ __forceinline__ void tmem_ld16x256b_x2(uint32_t taddr, uint32_t (&r)[8]) {
     asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+
+// Load 8 consecutive 32-bit TMEM columns of this warp's 32-lane quarter. Written asynchronously: read only after tmem_ld_wait8.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr));
 }

@@ -308,6 +308,12 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
         const float* prod0 = &s.prod[0][kGated ? lane >> 4 : 0][c0];
         float weight = 1.0f;   // of token c0 + lane
         if (!kGated && p.pair_weight != nullptr && lane < own) weight = __ldg(p.pair_weight + p.pair_of[t.row0 + c0 + lane]);
+        if (kEpi && p.e.residual != nullptr && lane < own) {   // this warp's 32 channels of its tokens' residuals, to the L2
+            const int n = 256 * t.pair + 128 * static_cast<int>(rank) + 32 * q;
+            const uint16_t* r = static_cast<const uint16_t*>(p.e.residual) + (t.row0 + c0 + lane) * p.e.ldr + n;
+            if (n < p.N) asm volatile("prefetch.global.L2 [%0];" ::"l"(r));
+            if (n < p.N) asm volatile("prefetch.global.L2 [%0];" ::"l"(r + min(31, p.N - 1 - n)));
+        }
         float2 acc[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[i] = make_float2(0.0f, 0.0f);
@@ -389,28 +395,36 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
             ++nu;
         } else {
             const int n = 256 * t.pair + 128 * static_cast<int>(rank) + 32 * q + lane;
-            // bias, activation and residual of the thread's output channel: all residuals are on their way before the
-            // first is used (read and written by this thread alone, so the residual may be Y)
+            // bias, activation and residual of the thread's output channel, 8 tokens' residuals on their way at a time (read and
+            // written by this thread alone, so the residual may be Y)
             auto store_epilogue = [&]() {
                 const bool bf16 = p.bf16 != 0, mine = ok && n < p.N;
-                uint16_t r[32];
-                if (p.e.residual != nullptr) {
-                    const uint16_t* from = static_cast<const uint16_t*>(p.e.residual) + (t.row0 + c0) * p.e.ldr + n;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (i < own && mine) r[i] = from[i * p.e.ldr];
-                }
                 const float b = mine ? epi::bias_at(p.e, n, bf16) : 0.0f;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[i] = make_float2(acc[i].x + b, acc[i].y + b);
                 activate_all(p.e.act, acc);
+                if (!mine) return;
+                const uint16_t* from = static_cast<const uint16_t*>(p.e.residual) + (t.row0 + c0) * p.e.ldr + n;
                 uint16_t* to = static_cast<uint16_t*>(p.Y) + (t.row0 + c0) * p.ldy + n;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    if (i >= own || !mine) continue;
-                    float f = (i & 1) ? acc[i >> 1].y : acc[i >> 1].x;
-                    if (p.e.residual != nullptr) f += epi::value16(r[i], bf16);
-                    to[i * p.ldy] = bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(f)) : __half_as_ushort(__float2half_rn(f));
+                for (int first = 0; first < 32; first += 8) {
+                    if (first >= own) break;
+                    float r[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) r[i] = 0.0f;
+                    if (p.e.residual != nullptr)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (first + i < own) r[i] = __uint_as_float(from[i * p.e.ldr]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (first + i >= own) break;
+                        const float a = (i & 1) ? acc[(first + i) >> 1].y : acc[(first + i) >> 1].x;
+                        const float f = a + epi::value16(static_cast<uint16_t>(__float_as_uint(r[i])), bf16);
+                        to[i * p.ldy] = bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(f)) : __half_as_ushort(__float2half_rn(f));
+                    }
+                    from += 8 * p.e.ldr;
+                    to += 8 * p.ldy;
                 }
             };
             auto store = [&](auto f32) {   // (FP32 outputs are the experts', whose K is not split)

@@ -188,12 +188,17 @@ __device__ __forceinline__ float max_magnitude(float a, float b) {
 // 1 + e^-g passes 2^126, silu(g) is below 1e-36 in magnitude, the quotient is 0.)
 __device__ __forceinline__ float silu_times(float g, float u) { return __fdividef(g, 1.0f + expf(-g)) * u; }
 
-// v = act(v) for all values of an array of pairs. One branch around the whole loop: only the path taken is fetched.
+// v = act(v) for all values of an array of pairs. One branch around the whole loop: only the path taken is fetched. Two pairs at a
+// time (nothing crosses the empty statements): with all of them in flight the compiler spills what else a thread holds.
 template <int kN>
 __device__ __forceinline__ void activate_all(int act, float2 (&v)[kN]) {
     auto all = [&](auto f) {
 #pragma unroll
-        for (int i = 0; i < kN; ++i) v[i] = make_float2(f(v[i].x), f(v[i].y));
+        for (int i = 0; i < kN; i += 2) {
+            asm volatile("" : "+f"(v[i].x), "+f"(v[i].y), "+f"(v[i + 1].x), "+f"(v[i + 1].y));
+            v[i] = make_float2(f(v[i].x), f(v[i].y));
+            v[i + 1] = make_float2(f(v[i + 1].x), f(v[i + 1].y));
+        }
     };
     if (act == kActRelu) all([](float x) { return epi::activate(kActRelu, x); });
     else if (act == kActSilu) all([](float x) { return epi::activate(kActSilu, x); });

@@ -27,21 +27,24 @@ namespace fp8 {
 namespace {
 
 constexpr int kT = 256;      // tokens of a tile, 128 a CTA
-constexpr int kStages = 5;   // operand blocks in flight
 constexpr int kAcc = 2;      // blocks with accumulators, two halves of 128 columns each
 constexpr int kWideEpi = 16; // epilogue warps
 constexpr int kWideThreads = 640;
 constexpr int kChunk = 8;    // blocks of token scales per copy
 constexpr int kSlots = 2;    // chunks of scales, and of factors
 
+// kEpi: one operand block less in flight, for the whole tile of the residual
+template <bool kEpi>
 struct __align__(1024) Smem {
+    static constexpr int kStages = kEpi ? 4 : 5;   // operand blocks in flight
     uint8_t x[kStages][kTileBytes];   // token codes: this CTA's 128 rows
     uint8_t w[kStages][kTileBytes];   // weight block: this CTA's tile, half of the pair's columns
     float sx[kSlots][kChunk][128];        // token scales
     float factor[kSlots][kChunk][2][128]; // times the weight scales: of the pair's two tiles, or gate and up
     union {
         float amax[2][4][128];        // gated: absmax of each quarter of a token's 128 hidden channels (units in turn)
-        uint4 out[kWideEpi][16 * 8];  // of a warp's 32 tokens x 64 columns: 16 tokens of 16-bit outputs, or 16 columns of FP32
+        // of a warp's 32 tokens x 64 columns: 16 tokens of 16-bit outputs (kEpi: all), or 16 columns of FP32
+        uint4 out[kWideEpi][(kEpi ? 32 : 16) * 8];
     };
     // full: a stage's operands have landed (even CTA: in both CTAs). empty: both halves' MMAs have read it.
     uint64_t full[kStages], empty[kStages];
@@ -55,10 +58,13 @@ struct __align__(1024) Smem {
     Tables tables;
 };
 
-__device__ __forceinline__ Unit unit(const Params& p, const Smem& s, int u) { return unit_of<kT>(p, s.tables, u); }
+template <bool kEpi>
+__device__ __forceinline__ Unit unit(const Params& p, const Smem<kEpi>& s, int u) { return unit_of<kT>(p, s.tables, u); }
 
-__device__ __forceinline__ void producer(const Params& p, const CUtensorMap* scales, Smem& s, uint32_t rank,
+template <bool kEpi>
+__device__ __forceinline__ void producer(const Params& p, const CUtensorMap* scales, Smem<kEpi>& s, uint32_t rank,
                                          volatile int* abort_flag) {
+    constexpr uint32_t kStages = Smem<kEpi>::kStages;
     const int units = unit_count<kT>(p, s.tables);
     uint32_t it = 0, ch = 0;
     bool ok = true;
@@ -79,7 +85,7 @@ __device__ __forceinline__ void producer(const Params& p, const CUtensorMap* sca
                 dev::tma_load_2d(s.sx[sl], scales, static_cast<int>(t.row0) + local, b, &s.sc_full[sl]);
                 ++ch;
             }
-            const int st = it % kStages;
+            const uint32_t st = it % kStages;
             ok = dev::mbar_wait(&s.empty[st], ((it / kStages) & 1) ^ 1, abort_flag);
             if (!ok) break;
             uint64_t* bar = &s.full[st];
@@ -105,8 +111,10 @@ __device__ __forceinline__ void producer(const Params& p, const CUtensorMap* sca
 
 // Even CTA: warps 1 and 3 issue the MMAs of one half of the columns each (weight rows 0-63 and 64-127 of both
 // tiles), as its operands and its accumulator allow. Odd CTA: warp 1 reports its operands.
-__device__ __forceinline__ void mma_issuer(const Params& p, Smem& s, uint32_t rank, int half, uint32_t tmem,
+template <bool kEpi>
+__device__ __forceinline__ void mma_issuer(const Params& p, Smem<kEpi>& s, uint32_t rank, int half, uint32_t tmem,
                                            volatile int* abort_flag) {
+    constexpr uint32_t kStages = Smem<kEpi>::kStages;
     const int units = unit_count<kT>(p, s.tables);
     constexpr uint32_t kIdesc = dev::idesc_e4m3_f32(256, 128);
     const uint32_t leader = dev::mapa(&s.full[0], 0);
@@ -152,8 +160,8 @@ __device__ __forceinline__ void mma_issuer(const Params& p, Smem& s, uint32_t ra
 }
 
 // ---------------------------------------------------------------- scaler (warp 2)
-template <bool kGated>
-__device__ __forceinline__ void scaler(const Params& p, Smem& s, int lane, volatile int* abort_flag) {
+template <bool kGated, bool kEpi>
+__device__ __forceinline__ void scaler(const Params& p, Smem<kEpi>& s, int lane, volatile int* abort_flag) {
     const int units = unit_count<kT>(p, s.tables);
     uint32_t ch = 0, nu = 0;
     bool ok = true;
@@ -248,9 +256,27 @@ __device__ __forceinline__ void store_tile(const Params& p, uint4* stage, int la
     }
 }
 
-// Bias and activation on a thread's token and 64 columns; then the residual and the rounding, 16 tokens at a time: the
-// residual's lines are read as the outputs' are written, into the stage, where each lane finds its token's and puts the
-// outputs in their place. (The tile is read and written by this warp alone, so the residual may be Y.)
+// The residual's tile of a warp into its stage (laid out as store_tile's, all 32 tokens): asked for before the tile's blocks,
+// there when they are summed. What lies outside the matrix is 0. kW = 1 reads it only then (1 element is no cp.async).
+template <int kW>
+__device__ __forceinline__ void ask_residual(const Params& p, uint4* stage, int lane, const uint16_t* residual, int tokens, int columns) {
+#pragma unroll 4
+    for (int j = 0; j < 64 / kW; ++j) {
+        const int l = (32 * j + lane) / (64 / kW), n = (32 * j + lane) % (64 / kW) * kW;
+        uint16_t* to = reinterpret_cast<uint16_t*>(&stage[l * 8 + ((n >> 3) ^ (l & 7))]) + (n & 7);
+        const uint16_t* from = residual + l * p.e.ldr + n;
+        if (kW > 1 && (n + kW <= columns || n >= columns || l >= tokens)) {
+            const bool there = l < tokens && n < columns;
+            dev::cp_async_if<kW == 1 ? 8 : 2 * kW>(dev::smem_u32(to), there ? static_cast<const void*>(from) : p.e.residual, there);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kW; ++i) to[i] = l < tokens && n + i < columns ? from[i] : static_cast<uint16_t>(0);
+        }
+    }
+}
+
+// Bias and activation on a thread's token and 64 columns, its residual from the stage, the rounding; the outputs take the
+// residual's place there and go out by whole lines. (The tile is read and written by this warp alone, so the residual may be Y.)
 template <int kW>
 __device__ __forceinline__ void store_tile_epilogue(const Params& p, uint4* stage, int lane, float2 (&acc)[2][16], uint16_t* y,
                                                     const uint16_t* residual, int n0, int tokens, int columns) {
@@ -258,6 +284,7 @@ __device__ __forceinline__ void store_tile_epilogue(const Params& p, uint4* stag
         uint16_t v[kW];
     };
     const bool bf16 = p.bf16 != 0;
+    if (residual != nullptr && kW == 1) ask_residual<1>(p, stage, lane, residual, tokens, columns);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
         if (p.e.bias != nullptr) {
@@ -270,63 +297,42 @@ __device__ __forceinline__ void store_tile_epilogue(const Params& p, uint4* stag
         }
         activate_all(p.e.act, acc[c]);
     }
-    auto slot = [&](int l, int n) { return reinterpret_cast<uint16_t*>(&stage[l * 8 + ((n >> 3) ^ (l & 7))]) + (n & 7); };
+    if (kW > 1) dev::cp_async_wait_all();
+    __syncwarp();
 #pragma unroll
-    for (int pass = 0; pass < 2; ++pass) {
+    for (int k = 0; k < 8; ++k) {
+        uint4* at = &stage[lane * 8 + (k ^ (lane & 7))];
+        float2 f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = acc[k >> 2][4 * (k & 3) + i];
         if (residual != nullptr) {
-#pragma unroll 4
-            for (int j = 0; j < 32 / kW; ++j) {
-                const int l = (32 * j + lane) / (64 / kW), n = (32 * j + lane) % (64 / kW) * kW;
-                if (16 * pass + l >= tokens) continue;
-                const uint16_t* from = residual + (16 * pass + l) * p.e.ldr + n;
-                Piece v{};
-                if (n + kW <= columns) {
-                    v = *reinterpret_cast<const Piece*>(from);
-                } else {
+            const uint4 r = *at;
+            const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-                    for (int i = 0; i < kW; ++i)
-                        if (n + i < columns) v.v[i] = from[i];
-                }
-                *reinterpret_cast<Piece*>(slot(l, n)) = v;
-            }
-            __syncwarp();
-        }
-        if ((lane >> 4) == pass)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                uint4* at = &stage[(lane & 15) * 8 + (k ^ (lane & 7))];
-                float2 f[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) f[i] = acc[k >> 2][4 * (k & 3) + i];
-                if (residual != nullptr) {
-                    const uint4 r = *at;
-                    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 a = epi::values16(w[i], bf16);
-                        f[i] = make_float2(f[i].x + a.x, f[i].y + a.y);
-                    }
-                }
-                *at = make_uint4(pack16(f[0].x, f[0].y, bf16), pack16(f[1].x, f[1].y, bf16), pack16(f[2].x, f[2].y, bf16),
-                                 pack16(f[3].x, f[3].y, bf16));
-            }
-        __syncwarp();
-#pragma unroll 4
-        for (int j = 0; j < 32 / kW; ++j) {
-            const int l = (32 * j + lane) / (64 / kW), n = (32 * j + lane) % (64 / kW) * kW;
-            const Piece v = *reinterpret_cast<const Piece*>(slot(l, n));
-            if (16 * pass + l >= tokens) continue;
-            uint16_t* to = y + (16 * pass + l) * p.ldy + n;
-            if (n + kW <= columns) {
-                *reinterpret_cast<Piece*>(to) = v;
-            } else {
-#pragma unroll
-                for (int i = 0; i < kW; ++i)
-                    if (n + i < columns) to[i] = v.v[i];
+            for (int i = 0; i < 4; ++i) {
+                const float2 a = epi::values16(w[i], bf16);
+                f[i] = make_float2(f[i].x + a.x, f[i].y + a.y);
             }
         }
-        __syncwarp();
+        *at = make_uint4(pack16(f[0].x, f[0].y, bf16), pack16(f[1].x, f[1].y, bf16), pack16(f[2].x, f[2].y, bf16),
+                         pack16(f[3].x, f[3].y, bf16));
     }
+    __syncwarp();
+#pragma unroll 4
+    for (int j = 0; j < 64 / kW; ++j) {
+        const int l = (32 * j + lane) / (64 / kW), n = (32 * j + lane) % (64 / kW) * kW;
+        const Piece v = *reinterpret_cast<const Piece*>(reinterpret_cast<const uint16_t*>(&stage[l * 8 + ((n >> 3) ^ (l & 7))]) + (n & 7));
+        if (l >= tokens) continue;
+        uint16_t* to = y + l * p.ldy + n;
+        if (n + kW <= columns) {
+            *reinterpret_cast<Piece*>(to) = v;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kW; ++i)
+                if (n + i < columns) to[i] = v.v[i];
+        }
+    }
+    __syncwarp();
 }
 
 // The same for FP32 outputs (a routed product whose rows are still to be summed), all 32 tokens and 16 columns at a time
@@ -381,7 +387,7 @@ __device__ __forceinline__ float load_shared(uint32_t address) {
 // condition makes the compiler move its 32 registers at every join. A wait that gives up is remembered,
 // and the unit's outputs are not stored.
 template <bool kGated, bool kEpi>
-__device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank, int warp, int lane, uint32_t tmem,
+__device__ __forceinline__ void epilogue(const Params& p, Smem<kEpi>& s, uint32_t rank, int warp, int lane, uint32_t tmem,
                                          volatile int* abort_flag) {
     const int units = unit_count<kT>(p, s.tables);
     const int q = warp & 3, h = (warp - 4) >> 2;
@@ -403,6 +409,15 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
         const int64_t row = row0 + tok;
         float weight = 1.0f;   // of this thread's token
         if (!kGated && ok && p.pair_weight != nullptr && tok < n) weight = __ldg(p.pair_weight + p.pair_of[row]);
+        // this warp's tile: token of lane 0 (in the unit), first column
+        const int first = static_cast<int>(rank) * 128 + 32 * q, n0 = 256 * pair + 128 * sub + 64 * half;
+        if constexpr (kEpi) {
+            if (p.e.residual != nullptr && ok) {
+                const uint16_t* r = static_cast<const uint16_t*>(p.e.residual) + (static_cast<int64_t>(row0) + first) * p.e.ldr + n0;
+                if (p.vec == 8) ask_residual<8>(p, s.out[warp - 4], lane, r, n - first, p.N - n0);
+                else if (p.vec == 4) ask_residual<4>(p, s.out[warp - 4], lane, r, n - first, p.N - n0);
+            }
+        }
         float2 acc[2][16];
 #pragma unroll
         for (int c = 0; c < 2; ++c)
@@ -478,8 +493,6 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank
                 if (h == 0) p.h_scales[pair * p.sstride + row] = scale;
             }
         } else {
-            const int first = static_cast<int>(rank) * 128 + 32 * q;   // token of the warp's lane 0
-            const int n0 = 256 * pair + 128 * sub + 64 * half;
             const int64_t at = (static_cast<int64_t>(row0) + first) * p.ldy + n0;
             uint16_t* y = static_cast<uint16_t*>(p.Y) + at;
             const int tokens = ok ? n - first : 0, columns = p.N - n0;
@@ -506,12 +519,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
 fp8_wide_kernel(const Params p, const __grid_constant__ CUtensorMap scales) {
     extern __shared__ uint8_t smem_raw[];
     // (an offset from the array, so that the compiler still knows the accesses to be shared memory's)
-    Smem& s = *reinterpret_cast<Smem*>(smem_raw + ((1024u - (dev::smem_u32(smem_raw) & 1023u)) & 1023u));
+    Smem<kEpi>& s = *reinterpret_cast<Smem<kEpi>*>(smem_raw + ((1024u - (dev::smem_u32(smem_raw) & 1023u)) & 1023u));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = dev::cluster_ctarank();
     if (threadIdx.x == 0) {
         dev::tma_prefetch_map(&scales);
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < Smem<kEpi>::kStages; ++i) {
             dev::mbar_init(&s.full[i], rank == 0 ? 2 : 1);
             dev::mbar_init(&s.empty[i], 2);
         }
@@ -563,7 +576,7 @@ fp8_wide_kernel(const Params p, const __grid_constant__ CUtensorMap scales) {
     }
 }
 
-constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
+constexpr size_t kSmemBytes = (sizeof(Smem<false>) > sizeof(Smem<true>) ? sizeof(Smem<false>) : sizeof(Smem<true>)) + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory exceeds the 227 KB a CTA may use");
 
 }  // namespace

@@ -10,17 +10,17 @@
 // kernel with a narrower tile and more weight blocks in flight: for one row it streams weights, for many it is bound by
 // the tensor pipe.
 //   * A unit's whole K is summed in TMEM; two accumulators, so that a unit's epilogue runs under the next one's MMAs.
-//   * The epilogue turns 16 rows at a time through shared memory in FP32, so that a thread has 8 neighbouring outputs of a row:
+//   * The epilogue turns 8 rows at a time through shared memory in FP32, so that a thread has 8 neighbouring outputs of a row:
 //     bias, activation, residual (16-byte loads, on their way before the sums are there) and one 16-byte store.
 //   * Units too few for the pairs: K is split over the pairs of a cluster; the others leave their sums in the first one's
 //     shared memory, which adds them in order, so results do not depend on timing.
 //
-// Warp roles (384 threads, one CTA per SM, pairs persistent over units):
+// Warp roles (640 threads, one CTA per SM, pairs persistent over units):
 //   warp 0      producer of weight blocks and X boxes
 //   warp 1      even CTA of a pair: MMA issuer; odd CTA: reports its operands to the even one
 //   warp 2      allocates and frees TMEM
 //   warp 3      sums up the groups' units
-//   warps 4-11  epilogue: TMEM lane quarter warp % 4; 16-row chunks of the unit in turn
+//   warps 4-19  epilogue: TMEM lane quarter warp % 4; four groups take the unit's 8-row chunks in turn
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -34,11 +34,12 @@ namespace fmpq {
 namespace w16 {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;
+constexpr int kThreads = 32 * (4 + kEpiWarps);
+constexpr int kGroups = kEpiWarps / 4;   // of epilogue warps, one for each TMEM lane quarter, that take the chunks in turn
 constexpr int kMaxStages = 12;
 constexpr int kMostRows = 256;    // of a unit
-constexpr int kChunk = 16;        // rows of X that the epilogue turns at a time
+constexpr int kChunk = 8;         // rows of X that a group turns at a time
 constexpr int kStageLd = 132;     // floats of a row there: 128 outputs, and a skew of 16 bytes
 constexpr int kBandTiles = 8;     // dense order: bands of 8 row tiles, weight tiles inside a band
 constexpr int kMaxSplits = 4;
@@ -53,7 +54,7 @@ struct Params {
     void* Y;
     int64_t ldy;
     int bf16, f32;       // operands (and Y, unless f32) are bf16
-    int vec;             // Y and residual take 16-byte accesses of 8 columns
+    int vec;             // columns that Y and the residual take at once: 8, 4 (16 bits; FP32: 4 and 4), or 1
     int rows, N, out_n;  // out_n: columns of Y (gated: N / 2)
     int nb, pairs, experts, splits;
     int tile;            // rows of a unit, at most: a multiple of 32
@@ -66,7 +67,7 @@ struct Tables {
 };
 
 struct __align__(1024) Smem {
-    float turn[2][kChunk][kStageLd];   // a chunk of each half of the epilogue warps
+    float turn[kGroups][2][kChunk][kStageLd];   // a group's chunks, two in turn
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t acc_full[2], acc_free[2];
     uint64_t split_full;   // first pair of a cluster: the others' sums are here
@@ -75,7 +76,7 @@ struct __align__(1024) Smem {
     int abort_flag;
     Tables tables;
     // then the ring of operand stages (16 KB of weights, tile / 2 rows of X), and with K split the sums of the other pairs:
-    // [split - 1][chunk][4 vectors][128 weight rows] of 4 floats
+    // [split - 1][chunk][2 vectors][128 weight rows] of 4 floats
 };
 constexpr int kHeadBytes = (sizeof(Smem) + 1023) / 1024 * 1024;
 constexpr int kSmemBytes = 232448;                  // 227 KB: what a CTA may use
@@ -291,26 +292,28 @@ __device__ __forceinline__ void mma_issuer(const Params& p, Smem& s, uint8_t* ri
     __syncwarp();
 }
 
-// ---------------------------------------------------------------- epilogue (warps 4-11)
+// ---------------------------------------------------------------- epilogue (warps 4-19)
 
-// Eight neighbouring outputs of a row, from column n on (columns of them exist): 16 bits or FP32.
-__device__ __forceinline__ void store8(const Params& p, int64_t row, int n, int columns, const float (&f)[8]) {
+// kW (8, or 4 of a gated layer) neighbouring outputs of a row, from column n on (columns of them exist): 16 bits or FP32, in
+// accesses of p.vec columns.
+template <int kW>
+__device__ __forceinline__ void store_piece(const Params& p, int64_t row, int n, int columns, const float (&f)[kW]) {
     if (p.f32) {
         float* y = static_cast<float*>(p.Y) + row * p.ldy + n;
-        if (p.vec && columns >= 8) {
-            *reinterpret_cast<float4*>(y) = make_float4(f[0], f[1], f[2], f[3]);
-            *reinterpret_cast<float4*>(y + 4) = make_float4(f[4], f[5], f[6], f[7]);
-        } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < columns) y[i] = f[i];
+        for (int i = 0; i < kW; i += 4) {
+            if (columns >= kW) *reinterpret_cast<float4*>(y + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+            else
+#pragma unroll
+                for (int j = i; j < i + 4; ++j)
+                    if (j < columns) y[j] = f[j];
         }
         return;
     }
     uint16_t* y = static_cast<uint16_t*>(p.Y) + row * p.ldy + n;
-    uint32_t o[4];
+    uint32_t o[kW / 2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kW / 2; ++i) {
         if (p.bf16) {
             const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
             o[i] = *reinterpret_cast<const uint32_t*>(&v);
@@ -319,157 +322,232 @@ __device__ __forceinline__ void store8(const Params& p, int64_t row, int n, int 
             o[i] = *reinterpret_cast<const uint32_t*>(&v);
         }
     }
-    if (p.vec && columns >= 8) {
-        *reinterpret_cast<uint4*>(y) = make_uint4(o[0], o[1], o[2], o[3]);
+    if (columns < kW) {
+#pragma unroll
+        for (int i = 0; i < kW; ++i)
+            if (i < columns) y[i] = static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1)));
+    } else if (kW == 8 && p.vec == 8) {
+        *reinterpret_cast<uint4*>(y) = make_uint4(o[0], o[1], o[kW / 2 - 2], o[kW / 2 - 1]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < columns) y[i] = static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1)));
+        for (int i = 0; i < kW; i += 4) *reinterpret_cast<uint2*>(y + i) = make_uint2(o[i / 2], o[i / 2 + 1]);
     }
 }
-// The residual there, as it is in memory: 16 bits in raw[0..3], FP32 in all eight.
-__device__ __forceinline__ void load_residual(const Params& p, int64_t row, int n, int columns, uint32_t (&raw)[8]) {
+// The residual there, as it is in memory: 16 bits in raw[0 .. kW / 2 - 1], FP32 in all of it.
+template <int kW>
+__device__ __forceinline__ void load_residual(const Params& p, int64_t row, int n, int columns, uint32_t (&raw)[kW]) {
     if (p.f32) {
         const uint32_t* r = static_cast<const uint32_t*>(p.e.residual) + row * p.e.ldr + n;
-        if (p.vec && columns >= 8) {
-            const uint4 a = *reinterpret_cast<const uint4*>(r), b = *reinterpret_cast<const uint4*>(r + 4);
-            raw[0] = a.x, raw[1] = a.y, raw[2] = a.z, raw[3] = a.w, raw[4] = b.x, raw[5] = b.y, raw[6] = b.z, raw[7] = b.w;
-        } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) raw[i] = i < columns ? r[i] : 0u;
+        for (int i = 0; i < kW; i += 4) {
+            if (columns >= kW) {
+                const uint4 a = *reinterpret_cast<const uint4*>(r + i);
+                raw[i] = a.x, raw[i + 1] = a.y, raw[i + 2] = a.z, raw[i + 3] = a.w;
+            } else {
+#pragma unroll
+                for (int j = i; j < i + 4; ++j) raw[j] = j < columns ? r[j] : 0u;
+            }
         }
         return;
     }
     const uint16_t* r = static_cast<const uint16_t*>(p.e.residual) + row * p.e.ldr + n;
-    if (p.vec && columns >= 8) {
+    if (columns < kW) {
+#pragma unroll
+        for (int i = 0; i < kW / 2; ++i)
+            raw[i] = (2 * i < columns ? r[2 * i] : 0u) | (2 * i + 1 < columns ? static_cast<uint32_t>(r[2 * i + 1]) << 16 : 0u);
+    } else if (kW == 8 && p.vec == 8) {
         const uint4 a = *reinterpret_cast<const uint4*>(r);
         raw[0] = a.x, raw[1] = a.y, raw[2] = a.z, raw[3] = a.w;
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            raw[i] = (2 * i < columns ? r[2 * i] : 0u) | (2 * i + 1 < columns ? static_cast<uint32_t>(r[2 * i + 1]) << 16 : 0u);
+        for (int i = 0; i < kW; i += 4) {
+            const uint2 a = *reinterpret_cast<const uint2*>(r + i);
+            raw[i / 2] = a.x, raw[i / 2 + 1] = a.y;
+        }
     }
 }
-__device__ __forceinline__ void add_residual(const Params& p, const uint32_t (&raw)[8], float (&f)[8]) {
+template <int kW>
+__device__ __forceinline__ void add_residual(const Params& p, const uint32_t (&raw)[kW], float (&f)[kW]) {
     if (p.f32) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] += __uint_as_float(raw[i]);
+        for (int i = 0; i < kW; ++i) f[i] += __uint_as_float(raw[i]);
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kW / 2; ++i) {
         const float2 a = epi::values16(raw[i], p.bf16 != 0);
         f[2 * i] += a.x;
         f[2 * i + 1] += a.y;
     }
 }
-__device__ __forceinline__ void activate8(int act, float (&f)[8]) {
-    if (act == kActNone) return;
+template <int kW>
+__device__ __forceinline__ void activate_piece(int act, float (&f)[kW]) {
+    auto all = [&](auto one) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = epi::activate(act, f[i]);
+        for (int i = 0; i < kW; ++i) f[i] = one(f[i]);
+    };
+    if (act == kActRelu) all([](float v) { return epi::activate(kActRelu, v); });
+    else if (act == kActSilu) all([](float v) { return epi::activate(kActSilu, v); });
+    else if (act == kActGelu) all([](float v) { return epi::activate(kActGelu, v); });
+    else if (act == kActGeluTanh) all([](float v) { return epi::activate(kActGeluTanh, v); });
 }
-// bias[first .. first + 7], 0 past `columns`
-__device__ __forceinline__ void load_bias(const Params& p, int64_t first, int columns, float (&b)[8]) {
+// One output, and its residual.
+__device__ __forceinline__ void store1(const Params& p, int64_t row, int n, float f) {
+    const int64_t at = row * p.ldy + n;
+    if (p.f32) static_cast<float*>(p.Y)[at] = f;
+    else static_cast<uint16_t*>(p.Y)[at] = p.bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(f)) : __half_as_ushort(__float2half_rn(f));
+}
+__device__ __forceinline__ uint32_t residual1(const Params& p, int64_t row, int n) {
+    const int64_t at = row * p.e.ldr + n;
+    return p.f32 ? static_cast<const uint32_t*>(p.e.residual)[at] : static_cast<const uint16_t*>(p.e.residual)[at];
+}
+// bias[first] and behind, 0 past `columns`
+template <int kW>
+__device__ __forceinline__ void load_bias(const Params& p, int64_t first, int columns, float (&b)[kW]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = i < columns ? epi::bias_at(p.e, first + i, p.bf16 != 0) : 0.0f;
+    for (int i = 0; i < kW; ++i) b[i] = i < columns ? epi::bias_at(p.e, first + i, p.bf16 != 0) : 0.0f;
+}
+// Where a chunk's sums of another pair begin for a weight row (16 bytes each).
+__device__ __forceinline__ int other_sums(const Params& p, int split, int chunk, int row) {
+    return ((split - 1) * (p.tile / kChunk) + chunk) * (kChunk / 4) * 128 + row;
 }
 
-// A thread's chunk of sums, rows c * 16 .. + 15 of the unit for one packed weight row, goes through shared memory; then it has the
-// outputs of one piece of 8 columns: of 2 rows, or gated of one, gate and up of 8 hidden channels.
+// A thread's sums, a chunk's 8 rows for one packed weight row, go through shared memory; then it has one piece of neighbouring
+// columns of one row: 8, or gate and up of 4 hidden channels. Where rows of Y or of the residual do not start on 8-byte boundaries
+// (FP32: 16) a thread has one column instead, of all 8 rows (gated: of 4), so that a warp's accesses are still neighbours. A chunk's
+// sums leave TMEM while the chunk before is put out.
 template <bool kGated>
 __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* others, const Place& at, int warp, int lane, uint32_t tmem,
                                          volatile int* abort_flag) {
-    constexpr int kPieces = kGated ? 8 : 16, kRowsAtOnce = 128 / kPieces, kPer = kChunk / kRowsAtOnce;
+    constexpr int kCols = kGated ? 64 : 128;              // of this CTA
+    constexpr int kW = kCols * kChunk / 128, kPieces = kCols / kW;
+    constexpr int kColumnRows = 128 / kCols;              // rows that the threads cover at once, a column each
     const int units = unit_count(p, s);
     const int q = warp & 3, g = (warp - 4) >> 2, tid = 32 * q + lane;
-    const int piece = tid % kPieces, sub = tid / kPieces;
+    const bool pieces = p.vec > 1;
+    // column inside the CTA's, first row of a chunk, and the place of the column's gate in a turned row: of every 32 packed rows, 16
+    // are gates and 16 the ups of the same hidden channels
+    const int col = pieces ? tid % kPieces * kW : tid % kCols, sub = pieces ? tid / kPieces : tid / kCols;
+    const int place = kGated ? 32 * (col >> 4) + (col & 15) : col;
     const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const uint32_t leader_free = dev::mapa(&s.acc_free[0], at.leader);
-    float (*turn)[kStageLd] = s.turn[g];
+    const bool first = at.split == 0;
     uint32_t nu = 0;
     bool ok = true;
     for (int u = at.cluster; u < units; u += at.clusters, ++nu) {
         const Unit t = unit_of(p, s, u, at.split);
         const uint32_t acc = nu & 1;
-        const int n = (kGated ? 128 * t.pair + 64 * static_cast<int>(at.rank) : 256 * t.pair + 128 * static_cast<int>(at.rank)) + 8 * piece;
+        const int n = (2 * t.pair + static_cast<int>(at.rank)) * kCols + col;
         const int columns = p.out_n - n;
         const int chunks = (t.rows + kChunk - 1) / kChunk;
-        const bool first = at.split == 0;
-        float bias[8], bias_up[kGated ? 8 : 1];
+        float bias[kW], bias_up[kW];
         if (first && p.e.bias != nullptr) {
-            load_bias(p, static_cast<int64_t>(t.e) * p.N + n, columns, bias);
-            if constexpr (kGated) load_bias(p, static_cast<int64_t>(t.e) * p.N + p.out_n + n, columns, bias_up);
+            load_bias(p, static_cast<int64_t>(t.e) * p.N + n, pieces ? columns : min(columns, 1), bias);
+            if constexpr (kGated) load_bias(p, static_cast<int64_t>(t.e) * p.N + p.out_n + n, pieces ? columns : min(columns, 1), bias_up);
+        }
+        if (first && p.e.residual != nullptr) {   // the unit's lines of the residual to the L2, under its MMAs
+            const int size = p.f32 ? 4 : 2, bytes = min(kCols, p.out_n - (n - col)) * size;
+            for (int r = (warp - 4) * 32 + lane; r < t.rows; r += kEpiWarps * 32) {
+                const uint8_t* line = static_cast<const uint8_t*>(p.e.residual) + ((static_cast<int64_t>(t.row0) + r) * p.e.ldr + (n - col)) * size;
+                for (int b = 0; b < bytes; b += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + b));
+                if (bytes > 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + bytes - 1));
+            }
         }
         ok = ok && dev::mbar_wait(&s.acc_full[acc], (nu >> 1) & 1, abort_flag);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (first && p.splits > 1 && ok) ok = __all_sync(0xFFFFFFFFu, dev::mbar_wait_cluster(&s.split_full, 0));
         dev::tc_fence_after();
-        const uint32_t others_at = first ? 0u : dev::mapa(others, at.rank);   // (in the first pair's CTA of this rank)
-        for (int c = g; c < chunks; c += 2) {
-            uint32_t raw[kPer][8];
-            float weight[kPer];
+        const uint32_t from_tmem = base + acc * kMostRows;
+
+        if (!first) {   // to the first pair's CTA of this rank
+            const uint32_t to = dev::mapa(others, at.rank) + other_sums(p, at.split, 0, tid) * 16u;
+            for (int c = g; c < chunks; c += kGroups) {
+                uint32_t d[kChunk];
+                dev::tmem_ld8(from_tmem + kChunk * c, d);
+                dev::tmem_ld_wait8(d);
+                if (!ok) continue;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int r = kChunk * c + sub + kRowsAtOnce * i;
-                weight[i] = 1.0f;
-                if (ok && first && r < t.rows && columns > 0) {
-                    if (p.e.residual != nullptr) load_residual(p, static_cast<int64_t>(t.row0) + r, n, columns, raw[i]);
-                    if (p.row_weight != nullptr) weight[i] = __ldg(p.row_weight + t.row0 + r);
+                for (int v = 0; v < kChunk / 4; ++v)
+                    dev::st_cluster_v4(to + (c * (kChunk / 4) + v) * 128 * 16u, __uint_as_float(d[4 * v]), __uint_as_float(d[4 * v + 1]),
+                                       __uint_as_float(d[4 * v + 2]), __uint_as_float(d[4 * v + 3]));
+            }
+        } else {
+            const bool mine = ok && columns > 0;
+            // one chunk behind the sums
+            auto put_out = [&](int c, const float (*turn)[kStageLd]) {
+                const int rows = t.rows - kChunk * c;   // of this chunk, and behind
+                const int64_t row0 = static_cast<int64_t>(t.row0) + kChunk * c;
+                if (!mine) return;
+                if (pieces) {
+                    if (sub >= rows) return;
+                    uint32_t raw[kW];
+                    if (p.e.residual != nullptr) load_residual(p, row0 + sub, n, columns, raw);
+                    const float* from = &turn[sub][place];
+                    float f[kW];
+#pragma unroll
+                    for (int i = 0; i < kW; i += 4) *reinterpret_cast<float4*>(&f[i]) = *reinterpret_cast<const float4*>(from + i);
+                    if (p.e.bias != nullptr)
+#pragma unroll
+                        for (int i = 0; i < kW; ++i) f[i] += bias[i];
+                    activate_piece(p.e.act, f);
+                    if constexpr (kGated) {
+                        const float4 v = *reinterpret_cast<const float4*>(from + 16);
+                        const float up[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int i = 0; i < kW; ++i) f[i] *= p.e.bias != nullptr ? up[i] + bias_up[i] : up[i];
+                    }
+                    if (p.row_weight != nullptr) {
+                        const float w = __ldg(p.row_weight + row0 + sub);
+#pragma unroll
+                        for (int i = 0; i < kW; ++i) f[i] *= w;
+                    }
+                    if (p.e.residual != nullptr) add_residual(p, raw, f);
+                    store_piece(p, row0 + sub, n, columns, f);
+                    return;
                 }
-            }
-            uint32_t d[16];
-            dev::tmem_ld16(base + acc * kMostRows + kChunk * c, d);
-            dev::tmem_ld_wait16(d);
-            if (!first) {
-                const uint32_t to = others_at + ((((at.split - 1) * (p.tile / kChunk) + c) * 4) * 128 + tid) * 16u;
-                if (ok)
+                uint32_t raw[kW];
+                if (p.e.residual != nullptr)
 #pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        dev::st_cluster_v4(to + v * 128 * 16u, __uint_as_float(d[4 * v]), __uint_as_float(d[4 * v + 1]),
-                                           __uint_as_float(d[4 * v + 2]), __uint_as_float(d[4 * v + 3]));
-                continue;
-            }
-            float f16[kChunk];
+                    for (int i = 0; i < kW; ++i)
+                        if (sub + kColumnRows * i < rows) raw[i] = residual1(p, row0 + sub + kColumnRows * i, n);
+                float f[kW];
 #pragma unroll
-            for (int j = 0; j < kChunk; ++j) f16[j] = __uint_as_float(d[j]);
-            for (int sp = 1; sp < p.splits; ++sp) {
-                const float4* from = others + (((sp - 1) * (p.tile / kChunk) + c) * 4) * 128 + tid;
+                for (int i = 0; i < kW; ++i) f[i] = turn[sub + kColumnRows * i][place] + (p.e.bias != nullptr ? bias[0] : 0.0f);
+                activate_piece(p.e.act, f);
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const float4 o = from[v * 128];
-                    f16[4 * v] += o.x, f16[4 * v + 1] += o.y, f16[4 * v + 2] += o.z, f16[4 * v + 3] += o.w;
+                for (int i = 0; i < kW; ++i) {
+                    const int j = sub + kColumnRows * i;
+                    if (j >= rows) continue;
+                    if constexpr (kGated) f[i] *= turn[j][place + 16] + (p.e.bias != nullptr ? bias_up[0] : 0.0f);
+                    if (p.row_weight != nullptr) f[i] *= __ldg(p.row_weight + row0 + j);
+                    if (p.e.residual != nullptr) f[i] += p.f32 ? __uint_as_float(raw[i]) : epi::value16(static_cast<uint16_t>(raw[i]), p.bf16 != 0);
+                    store1(p, row0 + j, n, f[i]);
                 }
-            }
+            };
+            int buffer = 0;
+            for (int c = g; c < chunks + kGroups; c += kGroups) {
+                uint32_t d[kChunk];
+                const int here = min(c, chunks - 1);   // (the last turn only puts out: its load is of no use, and not behind a branch)
+                dev::tmem_ld8(from_tmem + kChunk * here, d);
+                if (c >= kGroups) put_out(c - kGroups, s.turn[g][buffer ^ 1]);
+                dev::tmem_ld_wait8(d);
+                float f[kChunk];
 #pragma unroll
-            for (int j = 0; j < kChunk; ++j) turn[j][tid] = f16[j];
-            dev::named_bar_sync(2 + g, 128);
+                for (int j = 0; j < kChunk; ++j) f[j] = __uint_as_float(d[j]);
+                for (int sp = 1; sp < p.splits; ++sp) {
+                    const float4* from = others + other_sums(p, sp, here, tid);
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int j = sub + kRowsAtOnce * i, r = kChunk * c + j;
-                if (!ok || r >= t.rows || columns <= 0) continue;
-                float f[8];
-                // gated: of every 32 packed rows, 16 gates and the ups of the same hidden channels
-                const float* from = &turn[j][kGated ? 32 * (piece >> 1) + 8 * (piece & 1) : 8 * piece];
-                *reinterpret_cast<float4*>(&f[0]) = *reinterpret_cast<const float4*>(from);
-                *reinterpret_cast<float4*>(&f[4]) = *reinterpret_cast<const float4*>(from + 4);
-                if (p.e.bias != nullptr)
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) f[k] += bias[k];
-                activate8(p.e.act, f);
-                if constexpr (kGated) {
-                    float up[8];
-                    *reinterpret_cast<float4*>(&up[0]) = *reinterpret_cast<const float4*>(from + 16);
-                    *reinterpret_cast<float4*>(&up[4]) = *reinterpret_cast<const float4*>(from + 20);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) f[k] *= p.e.bias != nullptr ? up[k] + bias_up[k] : up[k];
+                    for (int v = 0; v < kChunk / 4; ++v) {
+                        const float4 o = from[v * 128];
+                        f[4 * v] += o.x, f[4 * v + 1] += o.y, f[4 * v + 2] += o.z, f[4 * v + 3] += o.w;
+                    }
                 }
-                if (p.row_weight != nullptr)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) f[k] *= weight[i];
-                if (p.e.residual != nullptr) add_residual(p, raw[i], f);
-                store8(p, static_cast<int64_t>(t.row0) + r, n, columns, f);
+                for (int j = 0; j < kChunk; ++j) s.turn[g][buffer][j][tid] = f[j];
+                // (whoever writes this buffer again has passed the next barrier, behind which the others have read it)
+                dev::named_bar_sync(2 + g, 128);
+                buffer ^= 1;
             }
-            dev::named_bar_sync(2 + g, 128);   // read before the next chunk comes
         }
         // all of it has been read: the accumulator is free
         dev::tc_fence_before();
@@ -517,6 +595,9 @@ w16_kernel(const Params p, const __grid_constant__ CUtensorMap big, const __grid
         dev::fence_barrier_init();
     }
     if (warp == 2) dev::tmem_alloc_pair(&s.tmem_base, 512);
+    // (launched as the programmatic dependent of whatever is before it: everything up to here runs under that one's end)
+    dev::pdl_wait();
+    dev::pdl_launch_dependents();
     if (p.start != nullptr) fill_tables(p, s.tables, warp, lane);
     dev::tc_fence_before();
     __syncthreads();
@@ -573,6 +654,8 @@ __global__ void __launch_bounds__(256) pack_kernel(const uint16_t* __restrict__ 
 // Rows of any alignment to rows of ld (a multiple of 8) elements, 8 of them a thread; those past K are not read by anyone.
 __global__ void __launch_bounds__(256) align_kernel(const uint16_t* __restrict__ X, int64_t ldx, int64_t rows, int K, uint4* __restrict__ out,
                                                     int64_t ld8) {
+    dev::pdl_wait();
+    dev::pdl_launch_dependents();
     const int64_t pieces = rows * ld8;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < pieces; i += static_cast<int64_t>(gridDim.x) * 256) {
         const int64_t r = i / ld8;
@@ -608,8 +691,10 @@ cudaLaunchConfig_t config(int grid, int cluster, size_t smem, cudaStream_t strea
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cfg;
 }
 
@@ -619,7 +704,7 @@ int resident_clusters(const w16_layer& L, int splits) {
     const bool known = L.device >= 0 && L.device < 64;
     if (known && cached[L.device][splits] > 0) return cached[L.device][splits];
     int most = L.num_sms / (2 * splits) > 0 ? L.num_sms / (2 * splits) : 1;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = config(most * 2 * splits, 2 * splits, kSmemBytes, nullptr, attr);
     int got = 0;
     if (ensure_smem_limit(reinterpret_cast<const void*>(w16_kernel<false>), kSmemBytes) == cudaSuccess &&
@@ -644,32 +729,35 @@ Shape with_ring(int tile, int splits, int64_t units, int clusters) {
     return s;
 }
 
-// The tile and the K splits. A block of a unit takes the MMAs 2 clk a row of X and the copies no less than that of their
-// 16 KB of weights; an end of a unit about 3000 clk where nothing runs under it.
+// No more units than these, whatever the groups: even_rows cuts none that is not the last of its group below half a tile.
+int64_t most_units(const w16_layer& L, int used, int rows, int tile) {
+    return (static_cast<int64_t>(used) + rows / (tile / 2)) * L.pairs;
+}
+
+// Rows of a unit, and in how many parts K is taken, by the rounds of units over the resident clusters. A block of 64 channels costs
+// a pair about 400 clk and 0.65 more for each row of X (2048 x 4096 -> 12288 in tiles of 64, 128, 192 and 256: 345, 172, 142
+// and 124 us; 777 x 2048 -> 5632: 51, 31, 25 and 29). Units that leave half the pairs idle split K: 1 x 8192 -> 8192 in 1, 2 and 4 parts 33.5,
+// 25.2 and 25.4 us, 16 x 8192 -> 1024 33.2, 20.1 and 13.3, 128 x 8192 -> 8192 35.6 and 31.4; the exchange takes about 1500 clk.
 Shape shape_of(const w16_layer& L, const W16Args& a) {
+    const bool grouped = a.start != nullptr;
     const int rows = static_cast<int>(a.rows);
-    if (a.start != nullptr) {
-        // the experts' loads are known on the device only: a tile for twice the mean, whose rest is cheap
-        const int used = L.experts < rows ? L.experts : rows, mean = (rows + used - 1) / used;
-        int tile = (2 * mean + 31) / 32 * 32;
-        if (tile > kMostRows) tile = kMostRows;
-        const int64_t most = (static_cast<int64_t>(used) + rows / (tile / 2) + 1) * L.pairs;   // (even_rows cuts no unit below half a tile)
-        return with_ring(tile, 1, most, resident_clusters(L, 1));
-    }
+    // the experts' loads are known on the device only: every one in use is taken to have the mean, and a sixth more for the spread. A
+    // tile twice that serves the longer ones, whose weights are then read less often. (1554 rows of 10 uneven experts, 1404 -> 2012, in
+    // tiles of 64, 128, 192 and 256: 37, 28, 32 and 36 us; 32768 of 128, 4096 -> 2048: 1019, 616, 513 and 468 to 490.)
+    const int used = grouped ? (L.experts < rows ? L.experts : rows) : 1, load = grouped ? (7 * rows / used + 5) / 6 : rows;
     Shape best{};
     double least = 0.0;
-    for (int splits = 1; splits <= kMaxSplits; splits *= 2) {
+    for (int splits = 1; splits <= (grouped ? 1 : kMaxSplits); splits *= 2) {
         const int clusters = resident_clusters(L, splits);
         if (splits > 1 && L.nb < 4 * splits) break;
-        for (int tile = 32; tile <= kMostRows; tile += 32) {
-            const int per = even_rows(rows, tile);
-            if (per != tile && tile < kMostRows) continue;
-            const int64_t tiles = (rows + per - 1) / per, units = tiles * L.pairs, rounds = (units + clusters - 1) / clusters;
+        for (int tile = kMostRows; tile >= 32; tile -= 32) {
+            const int per = even_rows(load, tile);
+            if (grouped ? tile > 32 && tile >= 2 * load + 32 : per != tile) continue;
+            const int64_t tiles = (load + per - 1) / per, units = tiles * L.pairs * used, rounds = (units + clusters - 1) / clusters;
             if (splits > 1 && rounds > 1) continue;
-            const Shape s = with_ring(tile, splits, units, clusters);
+            const Shape s = with_ring(tile, splits, grouped ? most_units(L, used, rows, tile) : units, clusters);
             if (s.stages < 4) continue;
-            const double block = 2.0 * per > 600.0 ? 2.0 * per : 600.0;
-            const double time = rounds * ((L.nb + splits - 1) / splits * block + 12.0 * per) + 3000.0 + (splits > 1 ? 1500.0 : 0.0);
+            const double time = rounds * ((L.nb + splits - 1) / splits * (400.0 + 0.65 * per)) + 5.0 * per + (splits > 1 ? 1500.0 : 0.0);
             if (best.grid == 0 || time < least) {
                 best = s;
                 least = time;
@@ -694,9 +782,11 @@ cudaError_t launch_w16_gemm(const w16_layer& L, const W16Args& a, cudaStream_t s
     p.ldy = a.ldy;
     p.bf16 = L.dtype == kBF16;
     p.f32 = a.dtype == kF32;
-    const int64_t unit = p.f32 ? 4 : 8;
-    auto whole = [&](const void* v, int64_t ld) { return (reinterpret_cast<uintptr_t>(v) & 15u) == 0 && ld % unit == 0; };
-    p.vec = whole(a.Y, a.ldy) && (p.e.residual == nullptr || whole(p.e.residual, p.e.ldr));
+    auto takes = [&](const void* v, int64_t ld, int bytes) {
+        return (reinterpret_cast<uintptr_t>(v) & (bytes - 1)) == 0 && ld * (p.f32 ? 4 : 2) % bytes == 0;
+    };
+    auto both = [&](int bytes) { return takes(a.Y, a.ldy, bytes) && (p.e.residual == nullptr || takes(p.e.residual, p.e.ldr, bytes)); };
+    p.vec = both(16) ? 8 : !p.f32 && both(8) ? 4 : 1;
     p.rows = static_cast<int>(a.rows);
     p.N = L.N;
     p.out_n = L.gated ? L.N / 2 : L.N;
@@ -713,7 +803,7 @@ cudaError_t launch_w16_gemm(const w16_layer& L, const W16Args& a, cudaStream_t s
     auto fn = L.gated ? w16::w16_kernel<true> : w16::w16_kernel<false>;
     const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), w16::kSmemBytes);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = w16::config(shape.grid, 2 * shape.splits, w16::kSmemBytes, stream, attr);
     return cudaLaunchKernelEx(&cfg, fn, p, big, small);
 }
@@ -728,9 +818,8 @@ cudaError_t launch_w16_pack(const w16_layer& L, int expert, const void* W, int64
 
 cudaError_t launch_w16_align(const void* X, int64_t ldx, int64_t rows, int K, void* out, int64_t ld, int num_sms, cudaStream_t stream) {
     const int64_t ctas = (rows * (ld / 8) + 255) / 256;
-    w16::align_kernel<<<static_cast<int>(ctas < num_sms * 32LL ? ctas : num_sms * 32LL), 256, 0, stream>>>(
-        static_cast<const uint16_t*>(X), ldx, rows, K, static_cast<uint4*>(out), ld / 8);
-    return cudaGetLastError();
+    return launch_after(w16::align_kernel, dim3(static_cast<unsigned>(ctas < num_sms * 32LL ? ctas : num_sms * 32LL)), 256, 0, true, stream,
+                        static_cast<const uint16_t*>(X), ldx, rows, K, static_cast<uint4*>(out), ld / 8);
 }
 
 }  // namespace fmpq
