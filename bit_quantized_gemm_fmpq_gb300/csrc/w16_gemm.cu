@@ -38,7 +38,8 @@ constexpr int kEpiWarps = 16;
 constexpr int kThreads = 32 * (4 + kEpiWarps);
 constexpr int kGroups = kEpiWarps / 4;   // of epilogue warps, one for each TMEM lane quarter, that take the chunks in turn
 constexpr int kMaxStages = 12;
-constexpr int kMostRows = 256;    // of a unit
+constexpr int kPartRows = 256;    // of a part: the N side of an MMA, and an accumulator's columns
+constexpr int kMostRows = 512;    // of a unit: two parts
 constexpr int kChunk = 8;         // rows of X that a group turns at a time
 constexpr int kStageLd = 132;     // floats of a row there: 128 outputs, and a skew of 16 bytes
 constexpr int kBandTiles = 8;     // dense order: bands of 8 row tiles, weight tiles inside a band
@@ -82,10 +83,15 @@ constexpr int kHeadBytes = (sizeof(Smem) + 1023) / 1024 * 1024;
 constexpr int kSmemBytes = 232448;                  // 227 KB: what a CTA may use
 constexpr int kRingBytes = kSmemBytes - 1024 - kHeadBytes;
 
-// `rows` of X for the 256 weight rows `pair` of expert e, blocks [b0, b1).
+// `rows` of X for the 256 weight rows `pair` of expert e, blocks [b0, b1). More than 256 rows are two parts of about half each, which
+// share the weight blocks and take both accumulators.
 struct Unit {
     int e, pair, rows, row0, b0, b1;
-    __device__ int columns() const { return max(32, (rows + 31) & ~31); }   // of the MMAs
+    __device__ int parts() const { return rows > kPartRows ? 2 : 1; }
+    __device__ int first_rows() const { return rows > kPartRows ? ((rows + 1) / 2 + 31) & ~31 : rows; }
+    __device__ int part_row0(int i) const { return i == 0 ? row0 : row0 + first_rows(); }
+    __device__ int part_rows(int i) const { return i == 0 ? first_rows() : rows - first_rows(); }
+    __device__ int columns(int i) const { return max(32, (part_rows(i) + 31) & ~31); }   // of the MMAs
 };
 
 // Rows of a unit where `count` rows are cut evenly into as few units as tiles of p.tile allow.
@@ -188,7 +194,9 @@ __device__ __forceinline__ void producer(const Params& p, const CUtensorMap* big
     bool ok = true;
     for (int u = at.cluster; ok && u < units; u += at.clusters) {
         const Unit t = unit_of(p, s, u, at.split);
-        const int half = t.columns() >> 1, row = t.row0 + static_cast<int>(at.rank) * half;
+        // this CTA's half of each part's rows
+        const int parts = t.parts(), half0 = t.columns(0) >> 1, half1 = parts > 1 ? t.columns(1) >> 1 : 0;
+        const int from0 = t.part_row0(0) + static_cast<int>(at.rank) * half0, from1 = t.part_row0(1) + static_cast<int>(at.rank) * half1;
         const uint8_t* w = p.W + (((static_cast<int64_t>(t.e) * p.pairs + t.pair) * 2 + at.rank) * p.nb + t.b0) * kTileBytes;
         for (int b = t.b0; b < t.b1; ++b, ++it, w += kTileBytes) {
             ok = __all_sync(0xFFFFFFFFu, dev::mbar_wait(&s.empty[st], phase, abort_flag));
@@ -196,12 +204,17 @@ __device__ __forceinline__ void producer(const Params& p, const CUtensorMap* big
             if (elect_one()) {
                 uint64_t* bar = &s.full[st];
                 uint8_t* to = ring + st * p.stage_bytes;
-                dev::mbar_arrive_expect_tx(bar, kTileBytes + half * 128u);
+                dev::mbar_arrive_expect_tx(bar, kTileBytes + (half0 + half1) * 128u);
                 dev::bulk_g2s(to, w, kTileBytes, bar);
                 to += kTileBytes;
-                int i = 0;
-                for (; i + kBigBox <= half; i += kBigBox) dev::tma_load_2d(to + i * 128, big, b * kW16Block, row + i, bar);
-                for (; i < half; i += kSmallBox) dev::tma_load_2d(to + i * 128, small, b * kW16Block, row + i, bar);
+                auto rows_to = [&](int half, int row) {
+                    int i = 0;
+                    for (; i + kBigBox <= half; i += kBigBox) dev::tma_load_2d(to + i * 128, big, b * kW16Block, row + i, bar);
+                    for (; i < half; i += kSmallBox) dev::tma_load_2d(to + i * 128, small, b * kW16Block, row + i, bar);
+                    to += half * 128;
+                };
+                rows_to(half0, from0);
+                rows_to(half1, from1);
             }
             __syncwarp();
             if (++st == static_cast<uint32_t>(p.stages)) {
@@ -249,14 +262,19 @@ __device__ __forceinline__ void mma_issuer(const Params& p, Smem& s, uint8_t* ri
     const int units = unit_count(p, s);
     const uint32_t remote = dev::mapa(&s.full[0], at.leader);
     const uint64_t w0 = dev::sdesc_k_sw128(dev::smem_u32(ring));
-    uint32_t st = 0, phase = 0, nu = 0;
+    uint32_t st = 0, phase = 0, np = 0;   // np: parts so far; accumulator np & 1 is the next one's
     bool ok = true;
-    for (int u = at.cluster; ok && u < units; u += at.clusters, ++nu) {
+    for (int u = at.cluster; ok && u < units; u += at.clusters) {
         const Unit t = unit_of(p, s, u, at.split);
-        const uint32_t idesc = idesc16(256, static_cast<uint32_t>(t.columns()), static_cast<uint32_t>(p.bf16));
-        const uint32_t acc = nu & 1, d = tmem + acc * kMostRows;
+        const int parts = t.parts();
+        const uint32_t idesc0 = idesc16(256, static_cast<uint32_t>(t.columns(0)), static_cast<uint32_t>(p.bf16));
+        const uint32_t idesc1 = idesc16(256, static_cast<uint32_t>(t.columns(1)), static_cast<uint32_t>(p.bf16));
+        const uint32_t acc = np & 1, d0 = tmem + acc * kPartRows, d1 = tmem + (acc ^ 1) * kPartRows;
+        const uint32_t to1 = static_cast<uint32_t>(t.columns(0)) * 4;   // the second part's rows in a stage, in 16 bytes
         if (at.rank == 0) {
-            ok = __all_sync(0xFFFFFFFFu, dev::mbar_wait(&s.acc_free[acc], ((nu >> 1) & 1) ^ 1, abort_flag));
+            bool free = dev::mbar_wait(&s.acc_free[acc], ((np >> 1) & 1) ^ 1, abort_flag);
+            if (parts > 1) free = free && dev::mbar_wait(&s.acc_free[acc ^ 1], (((np + 1) >> 1) & 1) ^ 1, abort_flag);
+            ok = __all_sync(0xFFFFFFFFu, free);
             if (!ok) break;
         }
         for (int b = t.b0; b < t.b1; ++b) {
@@ -270,9 +288,15 @@ __device__ __forceinline__ void mma_issuer(const Params& p, Smem& s, uint8_t* ri
                 const uint64_t ad = w0 + st * static_cast<uint32_t>(p.stage_bytes >> 4), bd = ad + kTileBytes / 16;
                 if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) mma_16_pair(d, ad + 2 * k, bd + 2 * k, idesc, b > t.b0 || k > 0 ? 1u : 0u);
+                    for (int k = 0; k < 4; ++k) mma_16_pair(d0, ad + 2 * k, bd + 2 * k, idesc0, b > t.b0 || k > 0 ? 1u : 0u);
+                    if (parts > 1)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) mma_16_pair(d1, ad + 2 * k, bd + to1 + 2 * k, idesc1, b > t.b0 || k > 0 ? 1u : 0u);
                     commit_pair(&s.empty[st], at.leader);
-                    if (b + 1 == t.b1) commit_pair(&s.acc_full[acc], at.leader);
+                    if (b + 1 == t.b1) {
+                        commit_pair(&s.acc_full[acc], at.leader);
+                        if (parts > 1) commit_pair(&s.acc_full[acc ^ 1], at.leader);
+                    }
                 }
             }
             __syncwarp();
@@ -281,6 +305,7 @@ __device__ __forceinline__ void mma_issuer(const Params& p, Smem& s, uint8_t* ri
                 phase ^= 1;
             }
         }
+        np += parts;
     }
     if (elect_one()) {
         if (!ok) fail(p, abort_flag);
@@ -432,11 +457,19 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* other
     const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const uint32_t leader_free = dev::mapa(&s.acc_free[0], at.leader);
     const bool first = at.split == 0;
-    uint32_t nu = 0;
+    uint32_t np = 0;   // parts so far
     bool ok = true;
-    for (int u = at.cluster; u < units; u += at.clusters, ++nu) {
-        const Unit t = unit_of(p, s, u, at.split);
-        const uint32_t acc = nu & 1;
+    int part = 0;
+    for (int u = at.cluster; u < units; ++np) {
+        const Unit whole = unit_of(p, s, u, at.split);
+        struct {
+            int e, pair, rows, row0;
+        } const t{whole.e, whole.pair, whole.part_rows(part), whole.part_row0(part)};
+        if (++part == whole.parts()) {
+            part = 0;
+            u += at.clusters;
+        }
+        const uint32_t acc = np & 1;
         const int n = (2 * t.pair + static_cast<int>(at.rank)) * kCols + col;
         const int columns = p.out_n - n;
         const int chunks = (t.rows + kChunk - 1) / kChunk;
@@ -453,11 +486,11 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* other
                 if (bytes > 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + bytes - 1));
             }
         }
-        ok = ok && dev::mbar_wait(&s.acc_full[acc], (nu >> 1) & 1, abort_flag);
+        ok = ok && dev::mbar_wait(&s.acc_full[acc], (np >> 1) & 1, abort_flag);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (first && p.splits > 1 && ok) ok = __all_sync(0xFFFFFFFFu, dev::mbar_wait_cluster(&s.split_full, 0));
         dev::tc_fence_after();
-        const uint32_t from_tmem = base + acc * kMostRows;
+        const uint32_t from_tmem = base + acc * kPartRows;
 
         if (!first) {   // to the first pair's CTA of this rank
             const uint32_t to = dev::mapa(others, at.rank) + other_sums(p, at.split, 0, tid) * 16u;
@@ -735,29 +768,34 @@ int64_t most_units(const w16_layer& L, int used, int rows, int tile) {
 }
 
 // Rows of a unit, and in how many parts K is taken, by the rounds of units over the resident clusters. A block of 64 channels costs
-// a pair about 400 clk and 0.65 more for each row of X (2048 x 4096 -> 12288 in tiles of 64, 128, 192 and 256: 345, 172, 142
-// and 124 us; 777 x 2048 -> 5632: 51, 31, 25 and 29). Units that leave half the pairs idle split K: 1 x 8192 -> 8192 in 1, 2 and 4 parts 33.5,
-// 25.2 and 25.4 us, 16 x 8192 -> 1024 33.2, 20.1 and 13.3, 128 x 8192 -> 8192 35.6 and 31.4; the exchange takes about 1500 clk.
+// a pair about 400 clk and 0.65 more for each row of X: the copies from the L2 bound it, not the MMAs' 2 clk a row (2048 x 4096 -> 12288 in
+// tiles of 64, 128, 192 and 256: 345, 172, 142 and 124 us; 777 x 2048 -> 5632: 51, 31, 25 and 29). Above 256 rows it is the MMAs, and
+// the epilogue, which has no accumulator left to run beside: worth it where it saves a round (777 x 2048 -> 5632 in 320: 22) or where
+// an expert's load is a little above 256 (32768 rows of 128, 4096 -> 2048: 463 us in tiles of 256, 439 in 320).
+// Units that leave half the pairs idle split K: 1 x 8192 -> 8192 in 1, 2 and 4 parts 33.5, 25.2 and 25.4 us, 16 x 8192 -> 1024 33.2,
+// 20.1 and 13.3, 128 x 8192 -> 8192 35.6 and 31.4; the exchange takes about 1500 clk.
 Shape shape_of(const w16_layer& L, const W16Args& a) {
     const bool grouped = a.start != nullptr;
     const int rows = static_cast<int>(a.rows);
-    // the experts' loads are known on the device only: every one in use is taken to have the mean, and a sixth more for the spread. A
-    // tile twice that serves the longer ones, whose weights are then read less often. (1554 rows of 10 uneven experts, 1404 -> 2012, in
-    // tiles of 64, 128, 192 and 256: 37, 28, 32 and 36 us; 32768 of 128, 4096 -> 2048: 1019, 616, 513 and 468 to 490.)
+    // the experts' loads are known on the device only: every one in use is taken to have the mean, and a sixth more for the spread
+    // (1554 rows of 10 uneven experts, 1404 -> 2012, in tiles of 64, 128, 192 and 256: 37, 28, 32 and 36 us)
     const int used = grouped ? (L.experts < rows ? L.experts : rows) : 1, load = grouped ? (7 * rows / used + 5) / 6 : rows;
     Shape best{};
     double least = 0.0;
     for (int splits = 1; splits <= (grouped ? 1 : kMaxSplits); splits *= 2) {
         const int clusters = resident_clusters(L, splits);
         if (splits > 1 && L.nb < 4 * splits) break;
-        for (int tile = kMostRows; tile >= 32; tile -= 32) {
+        for (int tile = 32; tile <= (splits > 1 ? kPartRows : kMostRows); tile += 32) {
             const int per = even_rows(load, tile);
-            if (grouped ? tile > 32 && tile >= 2 * load + 32 : per != tile) continue;
+            if (per != tile) continue;
             const int64_t tiles = (load + per - 1) / per, units = tiles * L.pairs * used, rounds = (units + clusters - 1) / clusters;
             if (splits > 1 && rounds > 1) continue;
             const Shape s = with_ring(tile, splits, grouped ? most_units(L, used, rows, tile) : units, clusters);
             if (s.stages < 4) continue;
-            const double time = rounds * ((L.nb + splits - 1) / splits * (400.0 + 0.65 * per)) + 5.0 * per + (splits > 1 ? 1500.0 : 0.0);
+            const double block = per > kPartRows ? 2.25 * per : 400.0 + 0.65 * per;
+            // what nothing runs under: the last unit's epilogue, two-part units' own, and the exchange
+            const double end = 14.0 * per * (per > kPartRows ? rounds : 1) + (splits > 1 ? 1500.0 : 0.0);
+            const double time = rounds * ((L.nb + splits - 1) / splits * block) + end;
             if (best.grid == 0 || time < least) {
                 best = s;
                 least = time;

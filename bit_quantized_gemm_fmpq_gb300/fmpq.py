@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 import threading
 from typing import NamedTuple
 
@@ -711,26 +712,30 @@ class Epilogue(ctypes.Structure):
 ACTIVATIONS = {None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 
+_pack_epilogue = struct.Struct("@PPqii").pack    # Epilogue, faster than by its fields
+
+
 def _epilogue(bias, activation, residual, shape, biases, code: int, Y=None):
-    """The epilogue of a product with outputs of `shape` and the 16-bit type `code`, or None where nothing is asked for.
+    """The bytes of a product's epilogue with outputs of `shape` and the type `code`, or None where nothing is asked for.
     Y: the output that was passed, if one was."""
     act = ACTIVATIONS.get(activation)
-    _need(act is not None, "activation must be None, 'relu', 'silu', 'gelu' or 'gelu_tanh'")
-    if bias is None and residual is None and act == 0:
-        return None
-    e = Epilogue(activation=act)
+    if act is None:
+        raise ValueError("activation must be None, 'relu', 'silu', 'gelu' or 'gelu_tanh'")
+    b_ptr = b_code = r_ptr = ldr = 0
     if bias is not None:
-        _need(tuple(bias.shape) == biases and _here(bias) and bias.is_contiguous(),
-              f"bias must be a contiguous tensor {list(biases)} on the current GPU")
-        e.bias, e.bias_dtype = bias.data_ptr(), _dtype_code(bias.dtype)
-        _need(e.bias_dtype in (code, 2), "bias must be of the output's type or fp32")
+        if not (bias.shape == biases and _here(bias) and bias.is_contiguous()):
+            raise ValueError(f"bias must be a contiguous tensor {list(biases)} on the current GPU")
+        b_ptr, b_code = bias.data_ptr(), _dtype_code(bias.dtype)
+        _need(b_code == code or b_code == 2, "bias must be of the output's type or fp32")
     if residual is not None:
         _need(_rows16(residual, "residual", fp32=True) == code and residual.shape == shape,
               "residual must have the output's shape and type")
-        e.residual, e.ldr = residual.data_ptr(), _ld(residual)
+        r_ptr, ldr = residual.data_ptr(), _ld(residual)
     if Y is not None:
         _apart(Y, "Y", residual, bias, same=(residual,))
-    return e
+    if b_ptr == 0 and r_ptr == 0 and act == 0:
+        return None
+    return _pack_epilogue(b_ptr, r_ptr, ldr, b_code, act)
 
 
 def _on(X) -> int:
@@ -900,7 +905,7 @@ def fp8_gemm(layer: Fp8Layer, A_packed, a_scales, W_packed, w_scales, M: int, dt
     w_ptr, w_bytes = _workspace_of(layer, M, workspace)
     if epilogue is not None:
         _check("fp8_gemm", layer._lib.fp8_gemm_epilogue(
-            layer.handle, _ptr(A_packed), _ptr(a_scales), _ptr(W_packed), _ptr(w_scales), M, ctypes.addressof(epilogue), _ptr(Y),
+            layer.handle, _ptr(A_packed), _ptr(a_scales), _ptr(W_packed), _ptr(w_scales), M, epilogue, _ptr(Y),
             _dtype_code(Y.dtype), _ld(Y), w_ptr, w_bytes, _stream(None)))
         return Y
     _check("fp8_gemm", layer._lib.fp8_gemm(layer.handle, _ptr(A_packed), _ptr(a_scales), _ptr(W_packed), _ptr(w_scales), M,
@@ -940,7 +945,7 @@ def fp8_quantize_gemm(layer: Fp8Layer, X, W_packed, w_scales, A_packed=None, a_s
     if epilogue is not None:
         _check("fp8_quantize_gemm", layer._lib.fp8_quantize_gemm_epilogue(
             layer._h, X.data_ptr(), code, _ld(X), M, a_ptr, s_ptr, W_packed.data_ptr(), w_scales.data_ptr(),
-            ctypes.addressof(epilogue), Y.data_ptr(), _ld(Y), w_ptr, w_bytes, _on(X)))
+            epilogue, Y.data_ptr(), _ld(Y), w_ptr, w_bytes, _on(X)))
         return Y
     _check("fp8_quantize_gemm", layer._lib.fp8_quantize_gemm(
         layer._h, X.data_ptr(), code, _ld(X), M, a_ptr, s_ptr, W_packed.data_ptr(), w_scales.data_ptr(), Y.data_ptr(),
@@ -980,13 +985,18 @@ class BlockNorm(NamedTuple):
 _NORMS = {"rms": 0, "layer": 1}
 
 
-def _vector(v, K: int, what: str):
-    """A contiguous vector [K] on the current GPU, or None. Returns its dtype code (None without one)."""
-    if v is None:
-        return None
+_pack_block_norm = struct.Struct("@PqPqPqqPPPPPqPqPPqiiiiiiifff").pack    # BlockNormArgs, faster than by its fields
+
+
+def _vector(v, K: int, what: str, code: int, seen):
+    """A contiguous vector [K] on the current GPU, of X's type (code) or fp32, and of the type of those before it (seen).
+    Returns its pointer and dtype code."""
     _need(v.dim() == 1 and v.shape[0] == K and (K == 1 or v.stride(0) == 1) and _here(v),
           f"{what} must be a contiguous tensor [K] on the current GPU")
-    return _dtype_code(v.dtype)
+    mine = _dtype_code(v.dtype)
+    _need((mine == code or mine == 2) and (seen is None or mine == seen),
+          "weights and biases must all be of X's type, or all fp32")
+    return v.data_ptr(), mine
 
 
 @_on_stream
@@ -1010,54 +1020,63 @@ def block_norm(X, residual=None, kind: str = "rms", eps: float = 1e-6, post_norm
     _need(post_norm or (post_weight is None and post_bias is None), "post_weight and post_bias need post_norm")
     _need(pre_norm or (weight is None and bias is None and layer is None and Y is None),
           "weight, bias, layer and Y need pre_norm")
-    params = [_vector(v, K, what) for v, what in ((post_weight, "post_weight"), (post_bias, "post_bias"),
-                                                  (weight, "weight"), (bias, "bias"))]
-    types = {t for t in params if t is not None}
-    _need(len(types) <= 1 and types <= {code, 2}, "weights and biases must all be of X's type, or all fp32")
-    a = BlockNormArgs()
-    a.X, a.ldx, a.M, a.K, a.dtype = X.data_ptr(), _ld(X), M, K, code
-    a.param_dtype = types.pop() if types else code
+    param = None
+    w_ptr = b_ptr = pw_ptr = pb_ptr = 0
+    if weight is not None:
+        w_ptr, param = _vector(weight, K, "weight", code, param)
+    if bias is not None:
+        b_ptr, param = _vector(bias, K, "bias", code, param)
+    if post_weight is not None:
+        pw_ptr, param = _vector(post_weight, K, "post_weight", code, param)
+    if post_bias is not None:
+        pb_ptr, param = _vector(post_bias, K, "post_bias", code, param)
+    res_ptr = ldr = gate_ptr = ldg = gate_tokens = gate_code = 0
     if residual is not None:
-        _need(_rows16(residual, "residual") == code and residual.shape == (M, K), "residual must be [M, K] of X's type")
-        a.residual, a.ldr = residual.data_ptr(), _ld(residual)
+        _need(_rows16(residual, "residual") == code and residual.shape == X.shape, "residual must be [M, K] of X's type")
+        res_ptr, ldr = residual.data_ptr(), _ld(residual)
     if gate is not None:
         rows = gate if gate.dim() == 2 else gate[None]
+        groups = rows.shape[0]
         _need(gate.dim() in (1, 2) and _here(gate) and rows.shape[1] == K and (K == 1 or rows.stride(1) == 1) and
-              rows.shape[0] >= 1 and M % rows.shape[0] == 0, "gate must be [K], or [G, K] with G dividing M, on the current GPU")
-        a.gate, a.gate_dtype = gate.data_ptr(), _dtype_code(gate.dtype)
-        _need(a.gate_dtype in (code, 2), "gate must be of X's type or fp32")
-        a.gate_tokens, a.ldg = M // rows.shape[0], max(K, rows.stride(0)) if rows.shape[0] > 1 else K
-        _need(rows.shape[0] <= 1 or rows.stride(0) >= K, "the rows of a gate must not overlap")
-    inputs = (X, residual, gate, post_weight, post_bias, weight, bias)
-    if R is None and (post_norm or residual is not None or gate is not None or not pre_norm):
+              groups >= 1 and M % groups == 0, "gate must be [K], or [G, K] with G dividing M, on the current GPU")
+        gate_ptr, gate_code = gate.data_ptr(), _dtype_code(gate.dtype)
+        _need(gate_code in (code, 2), "gate must be of X's type or fp32")
+        gate_tokens, ldg = M // groups, rows.stride(0) if groups > 1 else K
+        _need(ldg >= K, "the rows of a gate must not overlap")
+    r_ptr = ldo = y_ptr = ldy = a_ptr = s_ptr = 0
+    if R is not None:
+        _need(_rows16(R, "R") == code and R.shape == X.shape, "R must be [M, K] of X's type")
+        _apart(R, "R", X, residual, gate, post_weight, post_bias, weight, bias, same=(X, residual))
+        r_ptr, ldo = R.data_ptr(), _ld(R)
+    elif post_norm or residual is not None or gate is not None or not pre_norm:
         R = torch.empty((M, K), dtype=X.dtype, device=X.device)
-    elif R is not None:
-        _need(_rows16(R, "R") == code and R.shape == (M, K), "R must be [M, K] of X's type")
-        _apart(R, "R", *inputs, same=(X, residual))
-    if pre_norm and layer is None and Y is None:
-        Y = torch.empty((M, K), dtype=X.dtype, device=X.device)
-    elif Y is not None:
-        _need(_rows16(Y, "Y") == code and Y.shape == (M, K), "Y must be [M, K] of X's type")
-        _apart(Y, "Y", *inputs, same=(X, residual))
+        r_ptr, ldo = R.data_ptr(), K
+    if Y is not None:
+        _need(_rows16(Y, "Y") == code and Y.shape == X.shape, "Y must be [M, K] of X's type")
+        _apart(Y, "Y", X, residual, gate, post_weight, post_bias, weight, bias, same=(X, residual))
         _apart(Y, "Y (and R)", R)
+        y_ptr, ldy = Y.data_ptr(), _ld(Y)
+    elif pre_norm and layer is None:
+        Y = torch.empty((M, K), dtype=X.dtype, device=X.device)
+        y_ptr, ldy = Y.data_ptr(), K
     if layer is not None:
         _need(layer.K == K, "the layer must take K channels")
-        if A_packed is None or a_scales is None:
-            A, s = layer.activations(M, X.device)
-            A_packed, a_scales = A if A_packed is None else A_packed, s if a_scales is None else a_scales
-        layer.check_activations(A_packed, a_scales, M)
-        a.A_packed, a.a_scales = A_packed.data_ptr(), a_scales.data_ptr()
+        if A_packed is None and a_scales is None:
+            A_packed, a_scales = layer.activations(M, X.device)
+        else:
+            if A_packed is None or a_scales is None:
+                A, s = layer.activations(M, X.device)
+                A_packed, a_scales = A if A_packed is None else A_packed, s if a_scales is None else a_scales
+            layer.check_activations(A_packed, a_scales, M)
+            for out, what in ((A_packed, "A_packed"), (a_scales, "a_scales")):
+                _apart(out, what, X, residual, gate, post_weight, post_bias, weight, bias, R, Y)
+        a_ptr, s_ptr = A_packed.data_ptr(), a_scales.data_ptr()
     else:
         _need(A_packed is None and a_scales is None, "A_packed and a_scales need a layer")
-    if R is not None:
-        a.R, a.ldo = R.data_ptr(), _ld(R)
-    if Y is not None:
-        a.Y, a.ldy = Y.data_ptr(), _ld(Y)
-    a.post_weight, a.post_bias, a.weight, a.bias = (v.data_ptr() if v is not None else None
-                                                    for v in (post_weight, post_bias, weight, bias))
-    a.kind, a.post_norm, a.pre_norm = norm, int(post_norm), int(pre_norm)
-    a.eps, a.residual_scale, a.weight_offset = eps, residual_scale, weight_offset
-    _check("fmpq_block_norm", (_lib or load_library()).fmpq_block_norm(ctypes.addressof(a), _on(X)))
+    args = _pack_block_norm(X.data_ptr(), _ld(X), res_ptr, ldr, gate_ptr, ldg, gate_tokens, pw_ptr, pb_ptr, w_ptr, b_ptr, r_ptr,
+                            ldo, y_ptr, ldy, a_ptr, s_ptr, M, K, code, code if param is None else param, gate_code, norm,
+                            bool(post_norm), bool(pre_norm), eps, residual_scale, weight_offset)
+    _check("fmpq_block_norm", (_lib or load_library()).fmpq_block_norm(args, _on(X)))
     return BlockNorm(R, Y, A_packed, a_scales)
 
 
@@ -1332,7 +1351,7 @@ def _w16_product(layer, X, groups, W_packed, bias, activation, residual, row_wei
         _apart(Y, "Y", X, row_weight)
     nbytes = int(layer._lib.w16_workspace_bytes(layer._h, X.data_ptr(), ld, rows)) if ld % 8 or X.data_ptr() % 16 else 0
     workspace = torch.empty(nbytes, dtype=torch.uint8, device=X.device) if nbytes else None
-    e_ptr = ctypes.addressof(epilogue) if epilogue is not None else None
+    e_ptr = epilogue
     w_ptr = workspace.data_ptr() if nbytes else None
     if groups is None:
         _check("w16_gemm", layer._lib.w16_gemm(layer._h, X.data_ptr(), ld, rows, W_packed.data_ptr(), e_ptr, Y.data_ptr(), code,

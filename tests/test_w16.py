@@ -62,7 +62,8 @@ def matrix(rows, K, dtype, seed, pad=0, scale=1.0):
 
 # one row; K split by 4, by 2; several tiles; odd everything; one channel; rows that need aligning; wide
 SIZES = [(1, 2048, 512, 0, 0), (5, 1024, 300, 0, 0), (40, 1536, 4000, 8, 0), (33, 300, 257, 1, 1), (64, 64, 130, 0, 0), (3, 1, 1, 0, 0),
-         (130, 200, 6000, 4, 4), (300, 260, 515, 5, 0), (700, 192, 1028, 3, 4), (1500, 512, 770, 0, 0), (257, 4096, 256, 0, 0)]
+         (130, 200, 6000, 4, 4), (300, 260, 515, 5, 0), (700, 192, 1028, 3, 4), (1500, 512, 770, 0, 0), (257, 4096, 256, 0, 0),
+         (300, 128, 20000, 0, 0), (513, 64, 19999, 0, 0)]
 
 
 @pytest.mark.gpu
@@ -119,13 +120,15 @@ def group_sizes(kind, E):
         return [0] * (E - 1) + [700]
     if kind == "first alone":
         return [300] + [0] * (E - 1)
+    if kind == "above 256":     # units of two parts, and a group that is cut
+        return [257 + 41 * i % 210 for i in range(E - 1)] + [1100]
     if kind == "odd":
         return [(37 * i + 11) % 90 for i in range(E)]
     return (torch.rand(E, generator=g) ** 3 * 900).int().tolist()     # uneven
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("kind", ["one each", "all in one", "first alone", "odd", "uneven"])
+@pytest.mark.parametrize("kind", ["one each", "all in one", "first alone", "above 256", "odd", "uneven"])
 @pytest.mark.parametrize("experts,K,N,gated", [(1, 128, 130, False), (5, 300, 520, False), (9, 256, 256, True), (33, 72, 100, True),
                                                (129, 64, 256, False)])
 def test_groups(fmpq_mod, kind, experts, K, N, gated):  # noqa: F811
