@@ -10,6 +10,7 @@
 // registers of one CTA (8 channels a vector, kV vectors a thread); a layer norm's variance is the mean of the squared
 // differences, a second reduction over those registers.
 #include <initializer_list>
+#include <type_traits>
 
 #include "fmpq_device.cuh"
 #include "fmpq_internal.h"
@@ -206,22 +207,6 @@ __device__ __forceinline__ int64_t gate_row_of(const BlockNormArgs& p, int64_t m
     return static_cast<int64_t>(static_cast<uint32_t>(m) / static_cast<uint32_t>(p.gate_tokens)) * p.ldg;
 }
 
-// The largest of three magnitudes; NaN if one is.
-__device__ __forceinline__ float most3(float a, float b, float c) {
-    float d;
-    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-
-// The scale of a block of 128 channels from the vectors of the 16 lanes of a half warp (every lane calls it).
-__device__ __forceinline__ float scale_of(const V8& v) {
-    const float mine = most3(most3(v[0].x, v[0].y, v[1].x), most3(v[1].y, v[2].x, v[2].y), most3(v[3].x, v[3].y, 0.0f));
-    uint32_t amax = __float_as_uint(mine);   // as bits, NaN is above every number
-#pragma unroll
-    for (int d = 8; d > 0; d >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-    return __fdiv_rn(__uint_as_float(amax), kQMax);
-}
-
 // y to memory: 16 bits, and codes (16 lanes of a half warp hold a block of 128; every lane calls it, with 0 past K).
 template <typename T, int kLie>
 __device__ __forceinline__ void put8(const BlockNormArgs& p, int64_t m, int k, V8& v) {
@@ -231,10 +216,10 @@ __device__ __forceinline__ void put8(const BlockNormArgs& p, int64_t m, int k, V
 #pragma unroll
         for (int c = 0; c < 8; ++c)
             if (k + c >= p.K) at(v, c) = 0.0f;
-    const float s = scale_of(v);
+    const float q[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
+    const float s = scale_of(q);
     const int b = k >> 7;
     if (b >= p.nb) return;
-    const float q[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
     const uint2 code = codes_of(q, s);
     const int l = (k >> 3) & 15;
     uint8_t* row = p.A + (static_cast<int64_t>(b) * p.M + m) * 128;
@@ -362,7 +347,7 @@ __global__ void __launch_bounds__(1024) block_norm_long_kernel(const BlockNormAr
 }
 
 // Many rows on 16-byte boundaries: the CTAs stay, and the next rows are on their way into a ring in shared memory (bulk
-// copies) while one is worked on. Two vectors a thread. Its instructions bound it (4096 x 8192 bf16, both norms, a gate, codes: 59 us,
+// copies) while one is worked on. Two vectors a thread (four where 1024 threads would not do). Its instructions bound it (4096 x 8192 bf16, both norms, a gate, codes: 59 us,
 // 4.0 TB/s, an issue slot used in 73 of 100; one norm and the residual 45; the sum alone 33, the copy rate), so what can be is uniform
 // or made once: a row's addresses are a base for the CTA and 32-bit offsets of a thread, arithmetic is on pairs, P (the weights'
 // type) and the norm are the compiler's. One CTA a row without the ring took 138, four vectors a thread 66, three CTAs of 40
@@ -378,9 +363,8 @@ __device__ __forceinline__ void param_at(const void* p, uint32_t k, V8& v) {
     }
 }
 
-template <typename T, typename P, int kNorm>
+template <typename T, typename P, int kNorm, int kV>
 __global__ void __launch_bounds__(1024) block_norm_stream_kernel(const BlockNormArgs p, int stages) {
-    constexpr int kV = 2;
     extern __shared__ __align__(128) uint8_t ring[];   // [stage][X's row, then the residual's]
     __shared__ Sums sums;
     __shared__ uint64_t landed[kMostStages];
@@ -513,9 +497,9 @@ __global__ void __launch_bounds__(1024) block_norm_stream_kernel(const BlockNorm
             const uint32_t swizzled = piece ^ ((m & 7) << 4);
 #pragma unroll
             for (int i = 0; i < kV; ++i) {
-                const float s = scale_of(v[i]);
-                if (k[i] >= static_cast<uint32_t>(p.nb) * 128u) continue;
                 const float q[8] = {v[i][0].x, v[i][0].y, v[i][1].x, v[i][1].y, v[i][2].x, v[i][2].y, v[i][3].x, v[i][3].y};
+                const float s = scale_of(q);
+                if (k[i] >= static_cast<uint32_t>(p.nb) * 128u) continue;
                 *reinterpret_cast<uint2*>(codes + (code_at[i] + swizzled)) = codes_of(q, s);
                 if (l == 0) *reinterpret_cast<float*>(scales + scale_at[i]) = s;
             }
@@ -530,16 +514,23 @@ cudaError_t block_norm_as(const BlockNormArgs& p, int num_sms, cudaStream_t stre
     const unsigned grid = static_cast<unsigned>(p.M < most ? p.M : most);
     auto threads_for = [&](int per) { return ((vectors + per - 1) / per + 31) / 32 * 32; };
     const bool few = p.M < 2 * num_sms;
-    if (kLie == kMixed && !few && p.K % 8 == 0 && p.K >= 512 && threads_for(2) <= 1024 &&
+    const int slot = p.K * (p.residual != nullptr ? 4 : 2), ring = 224 * 1024, per = threads_for(2) <= 1024 ? 2 : 4;
+    if (kLie == kMixed && !few && p.K % 8 == 0 && p.K >= 512 && threads_for(per) <= 1024 && 2 * slot <= ring &&
         p.M * p.nb * 128 < INT64_C(1) << 32) {   // (32-bit offsets of the codes)
-        auto fn = p.param_f32 ? (p.layer_norm ? block_norm_stream_kernel<T, float, kLayer> : block_norm_stream_kernel<T, float, kRms>)
-                              : (p.layer_norm ? block_norm_stream_kernel<T, T, kLayer> : block_norm_stream_kernel<T, T, kRms>);
-        const int threads = threads_for(2), slot = p.K * (p.residual != nullptr ? 4 : 2);
+        auto of = [&](auto norm, auto v) {
+            return p.param_f32 ? block_norm_stream_kernel<T, float, norm.value, v.value> : block_norm_stream_kernel<T, T, norm.value, v.value>;
+        };
+        using std::integral_constant;
+        auto fn = per == 2 ? (p.layer_norm ? of(integral_constant<int, kLayer>{}, integral_constant<int, 2>{})
+                                           : of(integral_constant<int, kRms>{}, integral_constant<int, 2>{}))
+                           : (p.layer_norm ? of(integral_constant<int, kLayer>{}, integral_constant<int, 4>{})
+                                           : of(integral_constant<int, kRms>{}, integral_constant<int, 4>{}));
+        const int threads = threads_for(per);
         int resident = 1024 / threads;   // (64 registers a thread)
         if (resident > 16) resident = 16;
         int stages = 200 * 1024 / resident / slot;
         stages = stages > kMostStages ? kMostStages : stages < 2 ? 2 : stages;
-        const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), 220 * 1024);
+        const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), ring);
         if (e != cudaSuccess) return e;
         const int64_t ctas = static_cast<int64_t>(num_sms) * resident;
         return launch_after(fn, dim3(static_cast<unsigned>(p.M < ctas ? p.M : ctas)), threads, stages * slot, true, stream, p, stages);

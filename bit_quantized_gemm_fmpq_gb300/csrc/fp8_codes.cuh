@@ -25,6 +25,20 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
+// The largest of three magnitudes; NaN if one is.
+__device__ __forceinline__ float most3(float a, float b, float c) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// The scale of a block of 128 channels from the eight values of each lane of a half warp (every lane calls it): NaN if one is.
+__device__ __forceinline__ float scale_of(const float (&v)[8]) {
+    const float mine = most3(most3(v[0], v[1], v[2]), most3(v[3], v[4], v[5]), most3(v[6], v[7], 0.0f));
+    uint32_t amax = __float_as_uint(mine);   // as bits, NaN is above every number
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+    return __fdiv_rn(__uint_as_float(amax), kQMax);
+}
 // The codes of eight values, e4m3(fl32(v / s)). Products with s's reciprocal, made 2^-21 smaller and larger,
 // enclose the quotient (the reciprocal is good to 2^-23, each product rounds by 2^-24): where both round to the same
 // code it is the quotient's, and elsewhere (one value in 2^17) the division decides.

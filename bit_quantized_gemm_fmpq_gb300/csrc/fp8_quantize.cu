@@ -26,7 +26,7 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
 // row) and scales are contiguous. kRows tokens a warp are in flight. 4096 x 8192 bf16: 29.4 us, 102 MB = 3.5 TB/s, 51%
 // of the copy rate: its instructions bound it. With 8 rounded divisions a lane it took 32.6, with one token in
 // flight or with four 31.3.
-template <typename T, bool kVec, int kRows>
+template <typename T, bool kVec, int kRows, bool kRouted>
 __global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ X, int64_t ldx, int64_t M, int K, int nb,
                                                        const int32_t* __restrict__ positions, int slots, int64_t rows,
                                                        int64_t sstride, uint8_t* __restrict__ A,
@@ -61,21 +61,21 @@ __global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ X, 
 #pragma unroll
                 for (int c = 0; c < 8; ++c) v[c] = k0 + c < K ? load_as_float(x + i * ldx + c) : 0.0f;
             }
-            // as bits, NaN is above every number: a block with one gets the scale NaN
-            uint32_t amax = 0u;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) amax = max(amax, __float_as_uint(fabsf(v[c])));
-#pragma unroll
-            for (int d = 8; d > 0; d >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-            const float s = __fdiv_rn(__uint_as_float(amax), kQMax);
+            const float s = scale_of(v);
             const uint2 code = codes_of(v, s);
             if (b >= nb) continue;
-            for (int j = 0; j < slots; ++j) {
-                const int64_t r = positions != nullptr ? positions[m * slots + j] : m;
-                if (r < 0) continue;
+            auto put = [&](int64_t r) {
                 uint8_t* row = A + (static_cast<int64_t>(b) * rows + r) * 128;
                 *reinterpret_cast<uint2*>(row + (((l >> 1) ^ static_cast<int>(r & 7)) << 4) + (l & 1) * 8) = code;
                 if (l == 0) scales[b * sstride + r] = s;
+            };
+            if constexpr (!kRouted) {
+                put(m);
+            } else {
+                for (int j = 0; j < slots; ++j) {
+                    const int64_t r = positions[m * slots + j];
+                    if (r >= 0) put(r);
+                }
             }
         }
     }
@@ -177,7 +177,8 @@ cudaError_t quantize_as(const void* X, int64_t ldx, int64_t M, int K, const int3
     const bool deep = vec && M * pairs >= num_sms * 128LL;
     const int64_t per = deep ? 8 * 2 : 8, ctas = (M + per - 1) / per, most = (num_sms * 64LL + pairs - 1) / pairs;
     const dim3 grid(static_cast<unsigned>(ctas < most ? ctas : most), static_cast<unsigned>(pairs));
-    auto fn = !vec ? quantize_kernel<T, false, 1> : deep ? quantize_kernel<T, true, 2> : quantize_kernel<T, true, 1>;
+    auto fn = positions != nullptr ? (!vec ? quantize_kernel<T, false, 1, true> : deep ? quantize_kernel<T, true, 2, true> : quantize_kernel<T, true, 1, true>)
+                                   : (!vec ? quantize_kernel<T, false, 1, false> : deep ? quantize_kernel<T, true, 2, false> : quantize_kernel<T, true, 1, false>);
     return launch_after(fn, grid, 256, 0, pdl, stream, static_cast<const T*>(X), ldx, M, K, nb,
                         positions, positions != nullptr ? slots : 1, rows, scale_stride(rows), static_cast<uint8_t*>(A), scales);
 }
