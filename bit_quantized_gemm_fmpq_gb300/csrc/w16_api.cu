@@ -21,40 +21,52 @@ fmpq_status check_device(const w16_layer* L) {
 int64_t aligned_ld(const w16_layer* L) { return (L->K + 7) / 8 * 8; }
 bool rows_aligned(const void* X, int64_t ldx, int64_t rows) { return aligned16(X) && (ldx % 8 == 0 || rows == 1); }
 
-fmpq_status product(const w16_layer* L, const void* X, int64_t ldx, int64_t rows, const int32_t* start, const int32_t* count,
-                    const void* W_packed, const fmpq_epilogue* e, const float* row_weight, void* Y, int32_t dtype, int64_t ldy,
-                    void* workspace, size_t workspace_bytes, void* stream) {
+// What every product checks, but for X and the workspace.
+fmpq_status product_ok(const w16_layer* L, const void* X, int64_t ldx, int64_t rows, const void* W_packed, const fmpq_epilogue* e,
+                       const float* row_weight, const void* Y, int32_t dtype, int64_t ldy) {
     if (L == nullptr || X == nullptr || W_packed == nullptr || Y == nullptr || (dtype != L->dtype && dtype != FMPQ_DTYPE_F32))
         return FMPQ_ERR_INVALID_ARG;
     const int64_t N = L->gated ? L->N / 2 : L->N;
     if (rows < 1 || rows > kMaxRows || ldx < L->K || ldy < N) return FMPQ_ERR_UNSUPPORTED_SHAPE;
-    if (!aligned16(W_packed) || !element_aligned(X, L->dtype) || !element_aligned(Y, dtype) ||
-        !element_aligned(start, FMPQ_DTYPE_F32) || !element_aligned(count, FMPQ_DTYPE_F32) ||
-        !element_aligned(row_weight, FMPQ_DTYPE_F32))
+    if (!aligned16(W_packed) || !element_aligned(X, L->dtype) || !element_aligned(Y, dtype) || !element_aligned(row_weight, FMPQ_DTYPE_F32))
         return FMPQ_ERR_MISALIGNED;
-    if (fmpq_status s = epilogue_ok(e, dtype, N)) return s;
-    const size_t need = w16_workspace_bytes(L, X, ldx, rows);
+    return epilogue_ok(e, dtype, N);
+}
+fmpq_status workspace_ok(size_t need, const void* workspace, size_t workspace_bytes) {
     if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return FMPQ_ERR_WORKSPACE;
-    if (need > 0 && !aligned16(workspace)) return FMPQ_ERR_MISALIGNED;
-    if (fmpq_status s = check_device(L)) return s;
+    return need > 0 && !aligned16(workspace) ? FMPQ_ERR_MISALIGNED : FMPQ_OK;
+}
+fmpq::W16Args args_of(const w16_layer* L, const void* X, int64_t ldx, int64_t rows, const void* W_packed, const fmpq_epilogue* e,
+                      const float* row_weight, void* Y, int32_t dtype, int64_t ldy) {
     fmpq::W16Args a{};
     a.X = X;
-    a.ldx = ldx % 8 == 0 ? ldx : aligned_ld(L);
-    if (need > 0) {
-        a.X = workspace;
-        a.ldx = aligned_ld(L);
-        const cudaError_t c = fmpq::launch_w16_align(X, ldx, rows, L->K, workspace, a.ldx, L->num_sms, st(stream));
-        if (c != cudaSuccess) return launched(c);
-    }
+    a.ldx = ldx % 8 == 0 ? ldx : aligned_ld(L);   // (one row, or replaced by the workspace)
     a.rows = rows;
     a.W = W_packed;
-    a.start = start;
-    a.count = count;
     a.row_weight = row_weight;
     a.epilogue = epilogue_of(e);
     a.Y = Y;
     a.dtype = dtype;
     a.ldy = ldy;
+    return a;
+}
+
+fmpq_status product(const w16_layer* L, const void* X, int64_t ldx, int64_t rows, const int32_t* offsets, const void* W_packed,
+                    const fmpq_epilogue* e, const float* row_weight, void* Y, int32_t dtype, int64_t ldy, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+    if (fmpq_status s = product_ok(L, X, ldx, rows, W_packed, e, row_weight, Y, dtype, ldy)) return s;
+    if (!element_aligned(offsets, FMPQ_DTYPE_F32)) return FMPQ_ERR_MISALIGNED;
+    const size_t need = w16_workspace_bytes(L, X, ldx, rows);
+    if (fmpq_status s = workspace_ok(need, workspace, workspace_bytes)) return s;
+    if (fmpq_status s = check_device(L)) return s;
+    fmpq::W16Args a = args_of(L, X, ldx, rows, W_packed, e, row_weight, Y, dtype, ldy);
+    a.start = offsets;
+    if (need > 0) {
+        a.X = workspace;
+        a.ldx = aligned_ld(L);
+        const cudaError_t c = fmpq::launch_w16_rows(X, ldx, rows, L->K, nullptr, 1, workspace, a.ldx, L->num_sms, st(stream));
+        if (c != cudaSuccess) return launched(c);
+    }
     return launched(fmpq::launch_w16_gemm(*L, a, st(stream)));
 }
 
@@ -135,14 +147,46 @@ size_t w16_workspace_bytes(const w16_layer* L, const void* X, int64_t ldx, int64
 fmpq_status w16_gemm(const w16_layer* L, const void* X, int64_t ldx, int64_t M, const void* W_packed, const fmpq_epilogue* epilogue,
                      void* Y, int32_t dtype, int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
     if (L != nullptr && L->experts != 1) return FMPQ_ERR_INVALID_ARG;
-    return product(L, X, ldx, M, nullptr, nullptr, W_packed, epilogue, nullptr, Y, dtype, ldy, workspace, workspace_bytes, stream);
+    return product(L, X, ldx, M, nullptr, W_packed, epilogue, nullptr, Y, dtype, ldy, workspace, workspace_bytes, stream);
 }
 
-fmpq_status w16_grouped_gemm(const w16_layer* L, const void* X, int64_t ldx, int64_t rows, const int32_t* start, const int32_t* count,
-                             const void* W_packed, const fmpq_epilogue* epilogue, const float* row_weight, void* Y, int32_t dtype,
+fmpq_status w16_grouped_gemm(const w16_layer* L, const void* X, int64_t ldx, int64_t rows, const int32_t* offsets, const void* W_packed,
+                             const fmpq_epilogue* epilogue, const float* row_weight, void* Y, int32_t dtype, int64_t ldy,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+    if (offsets == nullptr) return FMPQ_ERR_INVALID_ARG;
+    return product(L, X, ldx, rows, offsets, W_packed, epilogue, row_weight, Y, dtype, ldy, workspace, workspace_bytes, stream);
+}
+
+size_t w16_experts_workspace_bytes(const w16_layer* L, const void* X, int64_t ldx, int64_t T, int32_t k, int32_t gather) {
+    if (L == nullptr || moe_rows(T, k, L->experts) == 0) return 0;
+    const int64_t rows = moe_rows(T, k, L->experts);
+    if (!gather && rows_aligned(X, ldx, rows)) return 0;
+    return static_cast<size_t>(rows) * static_cast<size_t>(aligned_ld(L)) * 2;
+}
+
+fmpq_status w16_experts_gemm(const w16_layer* L, const void* plan, int64_t T, int32_t k, const void* X, int64_t ldx, int32_t gather,
+                             const void* W_packed, const fmpq_epilogue* epilogue, const float* weights, void* Y, int32_t dtype,
                              int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
-    if (start == nullptr) return FMPQ_ERR_INVALID_ARG;
-    return product(L, X, ldx, rows, start, count, W_packed, epilogue, row_weight, Y, dtype, ldy, workspace, workspace_bytes, stream);
+    if (L == nullptr || plan == nullptr || (gather != 0 && gather != 1)) return FMPQ_ERR_INVALID_ARG;
+    const int64_t rows = moe_rows(T, k, L->experts);
+    if (fmpq_status s = product_ok(L, X, ldx, rows, W_packed, epilogue, weights, Y, dtype, ldy)) return s;   // (no rows: sizes outside the plan's)
+    if (!aligned16(plan)) return FMPQ_ERR_MISALIGNED;
+    const size_t need = w16_experts_workspace_bytes(L, X, ldx, T, k, gather);
+    if (fmpq_status s = workspace_ok(need, workspace, workspace_bytes)) return s;
+    if (fmpq_status s = check_device(L)) return s;
+    const fmpq::MoePlan parts = fmpq::moe_plan_parts(plan, T, k, L->experts);
+    fmpq::W16Args a = args_of(L, X, ldx, rows, W_packed, epilogue, weights, Y, dtype, ldy);
+    a.start = parts.start;
+    a.count = parts.count;
+    a.pair_of = parts.pair_of;
+    if (need > 0) {
+        a.X = workspace;
+        a.ldx = aligned_ld(L);
+        const cudaError_t c = fmpq::launch_w16_rows(X, ldx, gather ? T : rows, L->K, gather ? parts.row_of : nullptr, k, workspace, a.ldx,
+                                                    L->num_sms, st(stream));
+        if (c != cudaSuccess) return launched(c);
+    }
+    return launched(fmpq::launch_w16_gemm(*L, a, st(stream)));
 }
 
 }  // extern "C"

@@ -51,6 +51,7 @@ struct Params {
     const int32_t* start;
     const int32_t* count;
     const float* row_weight;
+    const int32_t* pair_of;
     Epilogue e;
     void* Y;
     int64_t ldy;
@@ -416,6 +417,9 @@ __device__ __forceinline__ void activate_piece(int act, float (&f)[kW]) {
     else if (act == kActGelu) all([](float v) { return epi::activate(kActGelu, v); });
     else if (act == kActGeluTanh) all([](float v) { return epi::activate(kActGeluTanh, v); });
 }
+__device__ __forceinline__ float weight_of(const Params& p, int64_t row) {
+    return __ldg(p.row_weight + (p.pair_of != nullptr ? __ldg(p.pair_of + row) : row));
+}
 // One output, and its residual.
 __device__ __forceinline__ void store1(const Params& p, int64_t row, int n, float f) {
     const int64_t at = row * p.ldy + n;
@@ -530,7 +534,7 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* other
                         for (int i = 0; i < kW; ++i) f[i] *= p.e.bias != nullptr ? up[i] + bias_up[i] : up[i];
                     }
                     if (p.row_weight != nullptr) {
-                        const float w = __ldg(p.row_weight + row0 + sub);
+                        const float w = weight_of(p, row0 + sub);
 #pragma unroll
                         for (int i = 0; i < kW; ++i) f[i] *= w;
                     }
@@ -552,7 +556,7 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* other
                     const int j = sub + kColumnRows * i;
                     if (j >= rows) continue;
                     if constexpr (kGated) f[i] *= turn[j][place + 16] + (p.e.bias != nullptr ? bias_up[0] : 0.0f);
-                    if (p.row_weight != nullptr) f[i] *= __ldg(p.row_weight + row0 + j);
+                    if (p.row_weight != nullptr) f[i] *= weight_of(p, row0 + j);
                     if (p.e.residual != nullptr) f[i] += p.f32 ? __uint_as_float(raw[i]) : epi::value16(static_cast<uint16_t>(raw[i]), p.bf16 != 0);
                     store1(p, row0 + j, n, f[i]);
                 }
@@ -684,21 +688,35 @@ __global__ void __launch_bounds__(256) pack_kernel(const uint16_t* __restrict__ 
     }
 }
 
-// Rows of any alignment to rows of ld (a multiple of 8) elements, 8 of them a thread; those past K are not read by anyone.
-__global__ void __launch_bounds__(256) align_kernel(const uint16_t* __restrict__ X, int64_t ldx, int64_t rows, int K, uint4* __restrict__ out,
-                                                    int64_t ld8) {
+// Rows to rows of ld8 pieces of 8 elements, a piece a thread; elements past K are 0.
+template <bool kVec>
+__global__ void __launch_bounds__(256) rows_kernel(const uint16_t* __restrict__ X, int64_t ldx, int64_t rows, int K,
+                                                   const int32_t* __restrict__ row_of, int slots, uint4* __restrict__ out, int64_t ld8) {
     dev::pdl_wait();
     dev::pdl_launch_dependents();
     const int64_t pieces = rows * ld8;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < pieces; i += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t r = i / ld8;
-        const int k = static_cast<int>(i - r * ld8) * 8;
-        const uint16_t* from = X + r * ldx + k;
-        uint32_t w[4] = {0u, 0u, 0u, 0u};
+        const int64_t m = i / ld8, c = i - m * ld8;
+        const int k = static_cast<int>(c) * 8;
+        const uint16_t* from = X + m * ldx + k;
+        uint4 v;
+        if (kVec && k + 8 <= K) {
+            v = *reinterpret_cast<const uint4*>(from);
+        } else {
+            uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (k + j < K) w[j >> 1] |= static_cast<uint32_t>(from[j]) << (16 * (j & 1));
-        out[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int j = 0; j < 8; ++j)
+                if (k + j < K) w[j >> 1] |= static_cast<uint32_t>(from[j]) << (16 * (j & 1));
+            v = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (row_of == nullptr) {
+            out[i] = v;
+        } else {
+            for (int j = 0; j < slots; ++j) {
+                const int64_t r = row_of[m * slots + j];
+                if (r >= 0) out[r * ld8 + c] = v;
+            }
+        }
     }
 }
 
@@ -815,6 +833,7 @@ cudaError_t launch_w16_gemm(const w16_layer& L, const W16Args& a, cudaStream_t s
     p.start = a.start;
     p.count = a.count;
     p.row_weight = a.row_weight;
+    p.pair_of = a.pair_of;
     p.e = a.epilogue;
     p.Y = a.Y;
     p.ldy = a.ldy;
@@ -854,10 +873,13 @@ cudaError_t launch_w16_pack(const w16_layer& L, int expert, const void* W, int64
     return cudaGetLastError();
 }
 
-cudaError_t launch_w16_align(const void* X, int64_t ldx, int64_t rows, int K, void* out, int64_t ld, int num_sms, cudaStream_t stream) {
+cudaError_t launch_w16_rows(const void* X, int64_t ldx, int64_t rows, int K, const int32_t* row_of, int slots, void* out, int64_t ld,
+                            int num_sms, cudaStream_t stream) {
     const int64_t ctas = (rows * (ld / 8) + 255) / 256;
-    return launch_after(w16::align_kernel, dim3(static_cast<unsigned>(ctas < num_sms * 32LL ? ctas : num_sms * 32LL)), 256, 0, true, stream,
-                        static_cast<const uint16_t*>(X), ldx, rows, K, static_cast<uint4*>(out), ld / 8);
+    const bool vec = (reinterpret_cast<uintptr_t>(X) & 15u) == 0 && ldx % 8 == 0;
+    return launch_after(vec ? w16::rows_kernel<true> : w16::rows_kernel<false>,
+                        dim3(static_cast<unsigned>(ctas < num_sms * 32LL ? ctas : num_sms * 32LL)), 256, 0, true, stream,
+                        static_cast<const uint16_t*>(X), ldx, rows, K, row_of, slots, static_cast<uint4*>(out), ld / 8);
 }
 
 }  // namespace fmpq

@@ -25,6 +25,7 @@ struct W16Args {
     const int32_t* start;       // experts: first row of each, and row counts; nullptr: one group of all rows
     const int32_t* count;       // nullptr: start has experts + 1 entries, each group ending where the next begins
     const float* row_weight;    // scales a row's outputs before the residual (nullptr: 1)
+    const int32_t* pair_of;     // row r has row_weight[pair_of[r]] (nullptr: row_weight[r])
     Epilogue epilogue;          // bias [experts][N]
     void* Y;                    // of type dtype: the layer's, or FP32
     int dtype;
@@ -32,7 +33,9 @@ struct W16Args {
 };
 cudaError_t launch_w16_gemm(const w16_layer& L, const W16Args& a, cudaStream_t stream);
 cudaError_t launch_w16_pack(const w16_layer& L, int expert, const void* W, int64_t ld_n, int64_t ld_k, void* Wp, cudaStream_t stream);
-// X's rows to rows of `ld` elements on 16-byte boundaries.
-cudaError_t launch_w16_align(const void* X, int64_t ldx, int64_t rows, int K, void* out, int64_t ld, int num_sms, cudaStream_t stream);
+// X's rows to rows of `ld` elements (a multiple of 8) on 16-byte boundaries: row m to row m, or to the rows row_of[m * slots ..
+// + slots) that are not negative.
+cudaError_t launch_w16_rows(const void* X, int64_t ldx, int64_t rows, int K, const int32_t* row_of, int slots, void* out, int64_t ld,
+                            int num_sms, cudaStream_t stream);
 
 }  // namespace fmpq

@@ -104,7 +104,9 @@ SIGNATURES = {
     "w16_pack_weights": (_I32, [_P, _I32, _P, _I64, _I64, _P, _P]),
     "w16_workspace_bytes": (_SZ, [_P, _P, _I64, _I64]),
     "w16_gemm": (_I32, [_P, _P, _I64, _I64, _P, _P, _P, _I32, _I64, _P, _SZ, _P]),
-    "w16_grouped_gemm": (_I32, [_P, _P, _I64, _I64, _P, _P, _P, _P, _P, _P, _I32, _I64, _P, _SZ, _P]),
+    "w16_grouped_gemm": (_I32, [_P, _P, _I64, _I64, _P, _P, _P, _P, _P, _I32, _I64, _P, _SZ, _P]),
+    "w16_experts_workspace_bytes": (_SZ, [_P, _P, _I64, _I64, _I32, _I32]),
+    "w16_experts_gemm": (_I32, [_P, _P, _I64, _I32, _P, _I64, _I32, _P, _P, _P, _P, _I32, _I64, _P, _SZ, _P]),
     "fmpq_status_string": (ctypes.c_char_p, [_I32]),
     "fmpq_version": (_I32, []),
 }
@@ -1329,39 +1331,37 @@ def w16_pack_weights(layer: W16Layer, W):
     return Wp
 
 
-def _w16_product(layer, X, groups, W_packed, bias, activation, residual, row_weight, dtype, Y):
+def _w16_product(layer, X, W_packed, rows: int, call, workspace_bytes, bias, activation, residual, dtype, Y, inputs=()):
+    """What the three products share: checks, epilogue, output and workspace; then call(Y's pointer, code and stride, epilogue,
+    workspace's pointer and bytes)."""
     import torch
-    _need(_rows16(X, "X") == layer._code and X.shape[1] == layer.K, "X must be [rows, K] of the layer's type")
     _need(_here(W_packed) and W_packed.element_size() == 1 and W_packed.is_contiguous() and W_packed.numel() == layer._w_bytes,
           "W_packed must be this layer's (w16_pack_weights)")
-    rows, ld = X.shape[0], _ld(X)
     shape = (rows, layer.outputs)
     code = layer._code if Y is None and dtype is None else _dtype_code(dtype if Y is None else Y.dtype)
-    _need(code in (layer._code, 2), "the output's type must be the layer's or fp32")
+    _need(code == layer._code or code == 2, "the output's type must be the layer's or fp32")
     epilogue = None
     if bias is not None or activation is not None or residual is not None:
-        biases = (layer.experts, layer.N)
         if bias is not None and bias.dim() == 1 and layer.experts == 1:
             bias = bias[None]
-        epilogue = _epilogue(bias, activation, residual, shape, biases, code, Y)
+        epilogue = _epilogue(bias, activation, residual, shape, (layer.experts, layer.N), code, Y)
     if Y is None:
         Y = torch.empty(shape, dtype=layer.dtype if dtype is None else dtype, device=X.device)
+        ldy = layer.outputs
     else:
         _need(_rows16(Y, "Y", fp32=True) == code and Y.shape == shape, "Y must be [rows, N] ([rows, N / 2] of a gated layer)")
-        _apart(Y, "Y", X, row_weight)
-    nbytes = int(layer._lib.w16_workspace_bytes(layer._h, X.data_ptr(), ld, rows)) if ld % 8 or X.data_ptr() % 16 else 0
+        _apart(Y, "Y", X, *inputs)
+        ldy = _ld(Y)
+    nbytes = workspace_bytes()
     workspace = torch.empty(nbytes, dtype=torch.uint8, device=X.device) if nbytes else None
-    e_ptr = epilogue
-    w_ptr = workspace.data_ptr() if nbytes else None
-    if groups is None:
-        _check("w16_gemm", layer._lib.w16_gemm(layer._h, X.data_ptr(), ld, rows, W_packed.data_ptr(), e_ptr, Y.data_ptr(), code,
-                                               _ld(Y), w_ptr, nbytes, _on(X)))
-    else:
-        r_ptr = row_weight.data_ptr() if row_weight is not None else None
-        _check("w16_grouped_gemm", layer._lib.w16_grouped_gemm(
-            layer._h, X.data_ptr(), ld, rows, *groups, W_packed.data_ptr(), e_ptr, r_ptr, Y.data_ptr(), code, _ld(Y), w_ptr,
-            nbytes, _on(X)))
+    call(Y.data_ptr(), code, ldy, epilogue, workspace.data_ptr() if nbytes else None, nbytes)
     return Y
+
+
+def _w16_rows(layer, X) -> int:
+    """Row stride of X [rows, K] of the layer's type."""
+    _need(_rows16(X, "X") == layer._code and X.shape[1] == layer.K, "X must be [rows, K] of the layer's type")
+    return _ld(X)
 
 
 @_on_stream
@@ -1369,27 +1369,65 @@ def w16_gemm(layer: W16Layer, X, W_packed, bias=None, activation=None, residual=
     """Y [M, N] (a gated layer: [M, N / 2]) of X [M, K] in the layer's type, or in fp32 (dtype, or a Y that is passed):
     act(X W^T + bias) + residual; gated: act(gate + bias) * (up + bias) + residual. bias [N] or [1, N], of Y's type or fp32;
     activation as fp8_gemm takes it; residual of Y's shape and type, which may be Y."""
-    _need(layer.experts == 1, "w16_gemm takes a layer of one matrix (w16_grouped_gemm: experts)")
-    return _w16_product(layer, X, None, W_packed, bias, activation, residual, None, dtype, Y)
+    _need(layer.experts == 1, "w16_gemm takes a layer of one matrix (w16_grouped_gemm, w16_experts_gemm: experts)")
+    ld, M, lib, x_ptr = _w16_rows(layer, X), X.shape[0], layer._lib, X.data_ptr()
+
+    def call(y_ptr, code, ldy, epilogue, ws, nbytes):
+        _check("w16_gemm", lib.w16_gemm(layer._h, x_ptr, ld, M, W_packed.data_ptr(), epilogue, y_ptr, code, ldy, ws, nbytes, _on(X)))
+
+    return _w16_product(layer, X, W_packed, M, call, lambda: _w16_workspace(layer, x_ptr, ld, M), bias, activation, residual, dtype, Y)
+
+
+def _w16_workspace(layer, x_ptr: int, ld: int, rows: int) -> int:
+    return int(layer._lib.w16_workspace_bytes(layer._h, x_ptr, ld, rows)) if ld % 8 or x_ptr % 16 else 0
 
 
 @_on_stream
-def w16_grouped_gemm(layer: W16Layer, X, groups, W_packed, bias=None, activation=None, residual=None, row_weight=None,
+def w16_grouped_gemm(layer: W16Layer, X, offsets, W_packed, bias=None, activation=None, residual=None, row_weight=None,
                      dtype=None, Y=None):
-    """As w16_gemm, the rows of X in groups with a matrix each. groups: int32 offsets [experts + 1] on the GPU (group e is
-    rows offsets[e] to offsets[e + 1] - 1), or a MoePlan, whose rows X and Y then have. bias [experts, N]; row_weight fp32
-    [rows] scales a row's outputs before the residual. Rows of no group are not written."""
+    """As w16_gemm, the rows of X in groups with a matrix each: group e is rows offsets[e] to offsets[e + 1] - 1 (int32
+    [experts + 1] on the GPU, cut to X's rows). bias [experts, N]; row_weight fp32 [rows] scales a row's outputs before the
+    residual. Rows of no group are not written."""
     import torch
-    if isinstance(groups, MoePlan):
-        _need(groups.experts == layer.experts and _here(groups.buffer) and X.shape[0] == groups.rows,
-              "the plan must be of this layer's experts, and X of its rows")
-        at = groups.buffer.data_ptr()
-        pointers = (at, at + 4 * layer.experts)
-    else:
-        _need(_here(groups) and groups.dtype == torch.int32 and groups.shape == (layer.experts + 1,) and groups.is_contiguous(),
-              "groups must be contiguous int32 offsets [experts + 1] on the current GPU, or a MoePlan")
-        pointers = (groups.data_ptr(), None)
-    if row_weight is not None:
-        _need(_here(row_weight) and row_weight.dtype == torch.float32 and row_weight.shape == (X.shape[0],) and
-              row_weight.is_contiguous(), "row_weight must be contiguous fp32 [rows] on the current GPU")
-    return _w16_product(layer, X, pointers, W_packed, bias, activation, residual, row_weight, dtype, Y)
+    ld, rows, lib, x_ptr = _w16_rows(layer, X), X.shape[0], layer._lib, X.data_ptr()
+    _need(_here(offsets) and offsets.dtype == torch.int32 and offsets.shape == (layer.experts + 1,) and offsets.is_contiguous(),
+          "offsets must be contiguous int32 [experts + 1] on the current GPU")
+    _need(row_weight is None or (_here(row_weight) and row_weight.dtype == torch.float32 and row_weight.shape == (rows,) and
+                                 row_weight.is_contiguous()), "row_weight must be contiguous fp32 [rows] on the current GPU")
+    r_ptr = row_weight.data_ptr() if row_weight is not None else None
+
+    def call(y_ptr, code, ldy, epilogue, ws, nbytes):
+        _check("w16_grouped_gemm", lib.w16_grouped_gemm(layer._h, x_ptr, ld, rows, offsets.data_ptr(), W_packed.data_ptr(), epilogue,
+                                                        r_ptr, y_ptr, code, ldy, ws, nbytes, _on(X)))
+
+    return _w16_product(layer, X, W_packed, rows, call, lambda: _w16_workspace(layer, x_ptr, ld, rows), bias, activation, residual, dtype,
+                        Y, (row_weight,))
+
+
+@_on_stream
+def w16_experts_gemm(layer: W16Layer, plan: MoePlan, X, W_packed, weights=None, bias=None, activation=None, residual=None,
+                     dtype=None, Y=None):
+    """The rows of a plan, each with its expert's matrix: Y [plan.rows, N] ([plan.rows, N / 2] of a gated layer), as
+    w16_grouped_gemm. X [T, K]: each token goes to its experts' rows; or X [plan.rows, K], such a product's output. weights
+    fp32 [T, k] scale each row's outputs by its pair's. Rows of no pair are not written. With dtype=torch.float32 it makes the D
+    that moe_combine sums (into X's type)."""
+    import torch
+    _need(plan.experts == layer.experts and _here(plan.buffer), "the plan must be of this layer's experts, on the current GPU")
+    ld, lib, x_ptr = _w16_rows(layer, X), layer._lib, X.data_ptr()
+    gather = X.shape[0] != plan.rows     # (a plan has more rows than tokens)
+    _need(not gather or X.shape[0] == plan.T, "X must be [T, K] or [plan.rows, K]")
+    _need(weights is None or (_here(weights) and weights.dtype == torch.float32 and weights.shape == (plan.T, plan.k) and
+                              weights.is_contiguous()), "weights must be contiguous fp32 [T, k] on the current GPU")
+    w_ptr = weights.data_ptr() if weights is not None else None
+
+    def need():
+        return int(lib.w16_experts_workspace_bytes(layer._h, x_ptr, ld, plan.T, plan.k, int(gather)))
+
+    def call(y_ptr, code, ldy, epilogue, ws, nbytes):
+        _check("w16_experts_gemm", lib.w16_experts_gemm(
+            layer._h, plan.buffer.data_ptr(), plan.T, plan.k, x_ptr, ld, int(gather), W_packed.data_ptr(), epilogue, w_ptr, y_ptr,
+            code, ldy, ws, nbytes, _on(X)))
+
+    Y = _w16_product(layer, X, W_packed, plan.rows, call, need, bias, activation, residual, dtype, Y, (weights,))
+    plan.dtype = layer.dtype
+    return Y

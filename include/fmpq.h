@@ -663,14 +663,20 @@ FMPQ_API size_t w16_workspace_bytes(const w16_layer* layer, const void* X, int64
 FMPQ_API fmpq_status w16_gemm(const w16_layer* layer, const void* X, int64_t ldx, int64_t M, const void* W_packed,
                               const fmpq_epilogue* epilogue, void* Y, int32_t dtype, int64_t ldy, void* workspace,
                               size_t workspace_bytes, void* stream);
-/* The rows of X [rows][ldx] in groups, one for each expert, in any order and with gaps: expert e has the rows from start[e]
- * on, count[e] of them; count = NULL: start has experts + 1 entries and the group of e ends at start[e + 1]. Both int32, on
- * the device, cut to [0, rows]; a group that ends before it starts is empty; groups must not share rows. Rows of no
- * group are left as they were in Y. row_weight: fp32 [rows] or NULL (1). A plan of moe_plan serves as start and count. */
-FMPQ_API fmpq_status w16_grouped_gemm(const w16_layer* layer, const void* X, int64_t ldx, int64_t rows, const int32_t* start,
-                                      const int32_t* count, const void* W_packed, const fmpq_epilogue* epilogue,
-                                      const float* row_weight, void* Y, int32_t dtype, int64_t ldy, void* workspace,
-                                      size_t workspace_bytes, void* stream);
+/* The rows of X [rows][ldx] in groups, one for each expert: expert e has rows offsets[e] .. offsets[e + 1] - 1 (int32
+ * [experts + 1], on the device; cut to [0, rows]; a group that ends before it starts is empty). Rows of no group are left as they
+ * were in Y. row_weight: fp32 [rows] or NULL (1). */
+FMPQ_API fmpq_status w16_grouped_gemm(const w16_layer* layer, const void* X, int64_t ldx, int64_t rows, const int32_t* offsets,
+                                      const void* W_packed, const fmpq_epilogue* epilogue, const float* row_weight, void* Y,
+                                      int32_t dtype, int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
+/* The rows of a plan (moe_plan of T tokens, k slots and the layer's experts), each with its expert's matrix: Y [moe_rows][ldy], for the
+ * next product or moe_combine(_f32). gather = 1: X is [T][ldx], and each token goes to its experts' rows; 0: X is [moe_rows][ldx].
+ * weights: fp32 [T][k], a row's outputs are scaled by its pair's; NULL: 1. The residual is [moe_rows][ldr]. Rows of no
+ * pair are left as they were. Workspace: w16_experts_workspace_bytes (0 without gather, for rows on 16-byte boundaries). */
+FMPQ_API size_t w16_experts_workspace_bytes(const w16_layer* layer, const void* X, int64_t ldx, int64_t T, int32_t k, int32_t gather);
+FMPQ_API fmpq_status w16_experts_gemm(const w16_layer* layer, const void* plan, int64_t T, int32_t k, const void* X, int64_t ldx,
+                                      int32_t gather, const void* W_packed, const fmpq_epilogue* epilogue, const float* weights,
+                                      void* Y, int32_t dtype, int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Static description of a status code. */
 FMPQ_API const char* fmpq_status_string(fmpq_status status);

@@ -232,15 +232,14 @@ def test_routed_experts_in_16_bits(fmpq_mod, T, k, E, H, F):  # noqa: F811
     Wu, Wd = fmpq_mod.w16_pack_weights(Lu, up), fmpq_mod.w16_pack_weights(Ld, down)
     ids, w = fmpq_mod.moe_route(torch.randn(T, E, generator=g).cuda(), k)
     plan = fmpq_mod.moe_plan(ids, E)
-    rows = plan.row_of.flatten().long()
-    Xp = torch.zeros(plan.rows, H, dtype=X.dtype, device="cuda")
-    Xp[rows] = X.repeat_interleave(k, 0)
-    row_weight = torch.zeros(plan.rows, device="cuda")
-    row_weight[rows] = w.flatten()
-    hidden = fmpq_mod.w16_grouped_gemm(Lu, Xp, plan, Wu, activation="silu")
-    plan.dtype = X.dtype
-    D = fmpq_mod.w16_grouped_gemm(Ld, hidden, plan, Wd, row_weight=row_weight, dtype=torch.float32)
+    buf = torch.full((plan.rows, F + 5), 7.0, dtype=X.dtype, device="cuda")
+    hidden = fmpq_mod.w16_experts_gemm(Lu, plan, X, Wu, activation="silu", Y=buf[:, :F])
+    D = fmpq_mod.w16_experts_gemm(Ld, plan, hidden, Wd, weights=w, dtype=torch.float32)
     Y = fmpq_mod.moe_combine(D, plan)
+    used = torch.zeros(plan.rows, dtype=torch.bool, device="cuda")
+    used[plan.row_of.flatten().long()] = True
+    assert bool((buf[~used] == 7).all()) and bool((buf[:, F:] == 7).all())
+    assert fmpq_mod.w16_device_status(Lu) == 0 and fmpq_mod.w16_device_status(Ld) == 0
     ref = torch.zeros(T, H, dtype=torch.float64)
     for t in range(T):
         for j in range(k):
@@ -256,8 +255,8 @@ def test_routed_experts_in_16_bits(fmpq_mod, T, k, E, H, F):  # noqa: F811
         at = (ids == e).nonzero()
         if at.numel():
             r = plan.row_of[at[:, 0], at[:, 1]].long()
-            check(hidden[r], Xp[r], up[e], "silu", gated=True)
-            check(D[r], hidden[r], down[e], row_weight=row_weight[r])
+            check(hidden[r], X[at[:, 0]], up[e], "silu", gated=True)
+            check(D[r], hidden[r], down[e], row_weight=w[at[:, 0], at[:, 1]])
 
 
 # ---- refusals (no GPU) ------------------------------------------------------------------------
@@ -308,8 +307,13 @@ def test_the_binding_refuses(no_gpu):
         lambda: fmpq.w16_grouped_gemm(three, X, ints(3), W3), lambda: fmpq.w16_grouped_gemm(three, X, ints(4).long(), W3),
         lambda: fmpq.w16_grouped_gemm(three, X, torch.zeros(4, dtype=torch.int32), W3), lambda: fmpq.w16_grouped_gemm(three, X, ints(8)[::2], W3),
         lambda: fmpq.w16_grouped_gemm(three, X, off, W3, bias=half(256)), lambda: fmpq.w16_grouped_gemm(three, X, off, W3, row_weight=f32(5)),
-        lambda: fmpq.w16_grouped_gemm(three, X, off, W3, row_weight=half(6)), lambda: fmpq.w16_grouped_gemm(three, X, plan_of(2, 1, 3, 5), W3),
-        lambda: fmpq.w16_grouped_gemm(three, X, plan_of(2, 1, 4, 6), W3),
+        lambda: fmpq.w16_grouped_gemm(three, X, off, W3, row_weight=half(6)), lambda: fmpq.w16_grouped_gemm(three, X, elsewhere(off), W3),
+        lambda: fmpq.w16_experts_gemm(three, plan_of(5, 1, 3, 40), X, W3), lambda: fmpq.w16_experts_gemm(three, plan_of(6, 1, 4, 40), X, W3),
+        lambda: fmpq.w16_experts_gemm(three, plan_of(6, 1, 3, 40), X, W3, weights=f32(6, 2)),
+        lambda: fmpq.w16_experts_gemm(three, plan_of(6, 1, 3, 40), X, W3, weights=half(6, 1)),
+        lambda: fmpq.w16_experts_gemm(three, plan_of(6, 1, 3, 40), X, W3, Y=half(6, 256)),
+        lambda: fmpq.w16_experts_gemm(three, plan_of(6, 1, 3, 40), X, W3, residual=half(6, 256)),
+        lambda: fmpq.w16_experts_gemm(three, plan_of(6, 1, 3, 40), half(40, 127), W3),
     ]
     for i, call in enumerate(calls):
         with pytest.raises(ValueError):
@@ -328,7 +332,9 @@ def test_layer_sizes_refused(K, N, experts, gated, dtype, code):
     assert lib.w16_layer_create(K, N, experts, gated, dtype, ctypes.byref(out)) == code and not out.value
     assert lib.w16_layer_create(8, 8, 1, 0, 0, None) == 1
     assert lib.w16_gemm(z, z, 8, 1, z, z, z, 0, 8, z, 0, z) == 1
-    assert lib.w16_grouped_gemm(z, z, 8, 1, z, z, z, z, z, z, 0, 8, z, 0, z) == 1
+    assert lib.w16_grouped_gemm(z, z, 8, 1, z, z, z, z, z, 0, 8, z, 0, z) == 1
+    assert lib.w16_experts_gemm(z, z, 1, 1, z, 8, 0, z, z, z, z, 0, 8, z, 0, z) == 1
+    assert lib.w16_experts_workspace_bytes(z, z, 8, 1, 1, 1) == 0
     assert lib.w16_pack_weights(z, 0, z, 8, 1, z, z) == 1 and lib.w16_device_status(z, None, 0) == 1
     assert lib.w16_packed_w_bytes(z) == 0 and lib.w16_workspace_bytes(z, z, 7, 3) == 0
     lib.w16_layer_destroy(z)
