@@ -20,7 +20,8 @@
  * (fmpq_layout_create_select, fmpq_outlier_gemm_fp16), QUIK asymmetric activations
  * (fmpq_quantize_asym, w4ax_gemm_asym) and QoQ progressive group quantization with W4A8
  * GEMMs (qoq_pack_weights, qoq_quantize, qoq_gemm). E4M3 layers with a scale for each block of
- * 128 (fp8_*), and layers of routed experts on them (moe_*).
+ * 128 (fp8_*), with bias, activation and residual in their epilogue, and layers of routed experts on
+ * them (moe_*); the norms between two blocks (fmpq_block_norm); layers and experts kept in 16 bits (w16_*).
  *
  * Conventions for every call:
  *   - Pointers are DEVICE pointers unless the parameter name ends in "_host".
@@ -34,9 +35,10 @@
  *     A CUDA launch failure returns FMPQ_ERR_CUDA. A device-side wait that gives up (a
  *     bounded wait, never a hang) records FMPQ_ERR_TIMEOUT in the layout's device status
  *     word, read by fmpq_device_status. The library never aborts, traps or prints.
- *   - All data buffers must be 16-byte aligned (FMPQ_ERR_MISALIGNED otherwise); the fp8_* and moe_*
- *     calls take their 16-bit and fp32 inputs and outputs at any alignment of an element.
- *   - Inputs must be finite (no NaN/Inf); results for non-finite inputs are unspecified.
+ *   - All data buffers must be 16-byte aligned (FMPQ_ERR_MISALIGNED otherwise); the fp8_*, moe_*, w16_* and
+ *     fmpq_block_norm calls take their 16-bit and fp32 inputs and outputs at any alignment of an element.
+ *   - Inputs must be finite (no NaN/Inf); results for non-finite inputs are unspecified (what the fp8_*, moe_*, w16_* and
+ *     fmpq_block_norm calls make of them is said with each).
  */
 #ifndef FMPQ_H
 #define FMPQ_H
@@ -526,7 +528,8 @@ FMPQ_API fmpq_status fp8_quantize_gemm_epilogue(const fp8_layer* layer, const vo
  *   norm(v; w, b)_k = (v_k - c) / sqrt(mean((v - c)^2) + eps) * (weight_offset + w_k) + b_k,
  *   c = 0 (FMPQ_NORM_RMS) or mean(v) (FMPQ_NORM_LAYER); no weight: times 1; no bias: + 0
  * All in FP32. y is written in 16 bits (Y), as the E4M3 codes and scales that fp8_quantize would
- * make of the FP32 y (A_packed, a_scales), or both. Forward only.
+ * make of the FP32 y (A_packed, a_scales), or both. A NaN or an infinity makes its own row's y NaN; squares past FP32's
+ * range, of rows beyond 1e19, make y 0. Forward only.
  * ====================================================================================== */
 
 enum { FMPQ_NORM_RMS = 0, FMPQ_NORM_LAYER = 1 };
@@ -634,7 +637,8 @@ FMPQ_API fmpq_status moe_experts(const fp8_layer* up, const fp8_layer* down, con
  *   gated (N = 2F: F gate rows, then F up rows), for n < F:
  *   Y[r][n] = act(gate[r][n] + bias[e][n]) * (up[r][n] + bias[e][F + n]) * row_weight[r] + residual[r][n]
  * FP16 or BF16 weights and X of that type, FP32 sums on the tensor cores, one rounding. e is the
- * group that row r lies in. Forward only.
+ * group that row r lies in. NaN and infinity reach the outputs that they take part in, and no others.
+ * Forward only.
  * ====================================================================================== */
 
 #define W16_MAX_K 65536
@@ -664,8 +668,8 @@ FMPQ_API fmpq_status w16_gemm(const w16_layer* layer, const void* X, int64_t ldx
                               const fmpq_epilogue* epilogue, void* Y, int32_t dtype, int64_t ldy, void* workspace,
                               size_t workspace_bytes, void* stream);
 /* The rows of X [rows][ldx] in groups, one for each expert: expert e has rows offsets[e] .. offsets[e + 1] - 1 (int32
- * [experts + 1], on the device; cut to [0, rows]; a group that ends before it starts is empty). Rows of no group are left as they
- * were in Y. row_weight: fp32 [rows] or NULL (1). */
+ * [experts + 1], on the device; cut to [0, rows]; a group that ends before it starts is empty, and a row that offsets which fall back
+ * put into two groups gets the outputs of either). Rows of no group are left as they were in Y. row_weight: fp32 [rows] or NULL (1). */
 FMPQ_API fmpq_status w16_grouped_gemm(const w16_layer* layer, const void* X, int64_t ldx, int64_t rows, const int32_t* offsets,
                                       const void* W_packed, const fmpq_epilogue* epilogue, const float* row_weight, void* Y,
                                       int32_t dtype, int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);

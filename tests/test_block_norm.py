@@ -115,8 +115,8 @@ def test_all_of_it(fmpq_mod, M, K, pad, kind, dtype):  # noqa: F811
     import torch
     dtype = getattr(torch, dtype)
     X, residual = draw(M, K, dtype, M + K, pad, 0.5, 0.3), draw(M, K, dtype, M + K + 1, pad, 2.0)
-    w, b, pw, pb = vectors(K, dtype if K % 2 else torch.float32, K)
-    gate, = vectors(K, dtype, K + 9, 1)
+    w, b, pw, pb = vectors(K, dtype if K % 16 else torch.float32, K)
+    gate, = vectors(K, torch.float32 if K % 3 == 0 else dtype, K + 9, 1)
     if kind == "rms":
         b = pb = None
     layer = fmpq_mod.Fp8Layer(K, 16)
@@ -159,6 +159,33 @@ def test_parts_alone(fmpq_mod, M, K, case):  # noqa: F811
     if out.Y is not None:
         check16(out.Y, y, grown)
     assert out.A_packed is None and out.a_scales is None
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,K", [(2, 1024), (400, 1024), (2, 20000)])
+def test_any_alignment_gives_the_same(fmpq_mod, M, K):  # noqa: F811
+    """Weights, rows and outputs that start 2, 8 and 16 bytes into their buffers."""
+    import torch
+    X, residual = draw(M, K, torch.bfloat16, 1), draw(M, K, torch.bfloat16, 2)
+    w, pw, gate = vectors(K, torch.bfloat16, 3, 3)
+    layer = fmpq_mod.Fp8Layer(K, 16)
+    ref = fmpq_mod.block_norm(X, residual, weight=w, post_norm=True, post_weight=pw, gate=gate, layer=layer)
+
+    def at(v, shift):
+        out = torch.empty(v.numel() + shift, dtype=v.dtype, device="cuda")[shift:].view(v.shape)
+        return out.copy_(v)
+
+    for shift in (1, 4, 8):
+        for moved in range(4):
+            a = [at(v, shift if i == moved else 0) for i, v in enumerate((X, residual, w, gate))]
+            R = at(X, shift if moved == 0 else 0)
+            out = fmpq_mod.block_norm(a[0], a[1], weight=a[2], post_norm=True, post_weight=pw, gate=a[3], layer=layer, R=R)
+            # another kernel sums in another order: both are within 100 e of the same value, so 200 e = 1.2e-5 of each other.
+            # R then differs by a bf16 step (2^-8) where the value is that near to a border, 1.2e-5 / 2^-8 = 0.3% of them: 2.2e-4 in
+            # norm; a code where it is that near to one of E4M3's, at least 2^-4 apart: 2e-4 of them, and as many for the scale
+            assert float((out.R.float() - ref.R.float()).norm()) <= 2.2e-4 * float(ref.R.float().norm())
+            assert float((out.a_scales - ref.a_scales)[:, :M].abs().max()) <= 1.2e-5 * float(ref.a_scales[:, :M].max())
+            assert float((out.A_packed != ref.A_packed).float().mean()) <= 4e-4
 
 
 @pytest.mark.gpu

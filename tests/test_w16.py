@@ -130,7 +130,7 @@ def group_sizes(kind, E):
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["one each", "all in one", "first alone", "above 256", "odd", "uneven"])
 @pytest.mark.parametrize("experts,K,N,gated", [(1, 128, 130, False), (5, 300, 520, False), (9, 256, 256, True), (33, 72, 100, True),
-                                               (129, 64, 256, False)])
+                                               (129, 64, 256, False), (32, 64, 128, False), (512, 72, 64, True)])
 def test_groups(fmpq_mod, kind, experts, K, N, gated):  # noqa: F811
     """Every group with its own matrix; rows before, between and behind the groups left as they were."""
     import torch
@@ -157,6 +157,25 @@ def test_groups(fmpq_mod, kind, experts, K, N, gated):  # noqa: F811
             check(Z[at], X[at], W[e], None, gated=gated)
     for at in (slice(0, before), slice(rows - behind, rows)):
         assert bool((Y[at] == 7).all()) and bool((Z[at] == 7).all())
+
+
+@pytest.mark.gpu
+def test_long_rows_of_a_large_buffer(fmpq_mod):  # noqa: F811
+    """Rows whose offsets pass 32 bits, in X, Y and the residual; only the rows are read and written."""
+    import torch
+    rows, K, N, ld = 70, 64, 128, 1 << 26          # 70 rows 2^26 elements apart: 9.4 GB in 16 bits
+    W = torch.stack([matrix(N, K, torch.bfloat16, e) for e in range(2)])
+    layer = fmpq_mod.W16Layer(K, N, torch.bfloat16, experts=2)
+    Wp = fmpq_mod.w16_pack_weights(layer, W)
+    buf = torch.empty(rows * ld, dtype=torch.bfloat16, device="cuda").view(rows, ld)
+    X, Y = buf[:, :K], buf[:, 256:256 + N]
+    X.copy_(matrix(rows, K, torch.bfloat16, 1))
+    Y.copy_(matrix(rows, N, torch.bfloat16, 2))
+    residual = Y.clone()
+    offsets = torch.tensor([0, 33, 70], dtype=torch.int32, device="cuda")
+    fmpq_mod.w16_grouped_gemm(layer, X, offsets, Wp, residual=Y, Y=Y)
+    check(Y[:33], X[:33], W[0], residual=residual[:33])
+    check(Y[33:], X[33:], W[1], residual=residual[33:])
 
 
 @pytest.mark.gpu
