@@ -791,7 +791,9 @@ int64_t most_units(const w16_layer& L, int used, int rows, int tile) {
 // the epilogue, which has no accumulator left to run beside: worth it where it saves a round (777 x 2048 -> 5632 in 320: 22) or where
 // an expert's load is a little above 256 (32768 rows of 128, 4096 -> 2048: 463 us in tiles of 256, 439 in 320).
 // Units that leave half the pairs idle split K: 1 x 8192 -> 8192 in 1, 2 and 4 parts 33.5, 25.2 and 25.4 us, 16 x 8192 -> 1024 33.2,
-// 20.1 and 13.3, 128 x 8192 -> 8192 35.6 and 31.4; the exchange takes about 1500 clk.
+// 20.1 and 13.3, 128 x 8192 -> 8192 35.6 and 31.4; the exchange takes about 1500 clk. (The last round's blocks cut evenly over all pairs, their
+// sums in global memory and the last to arrive adding them: 31.6 in place of 25.2, 17.2 of 13.3, 64 units of a token's 8 experts 35.8 of 28.3,
+// and 2048 x 4096 -> 12288, 4 units in the last round, no faster.)
 Shape shape_of(const w16_layer& L, const W16Args& a) {
     const bool grouped = a.start != nullptr;
     const int rows = static_cast<int>(a.rows);

@@ -160,6 +160,22 @@ def test_groups(fmpq_mod, kind, experts, K, N, gated):  # noqa: F811
 
 
 @pytest.mark.gpu
+def test_calls_in_turn(fmpq_mod):  # noqa: F811
+    """Products that split K, that copy their rows and that do both, one after another without a wait."""
+    import torch
+    cases = []
+    for i, (M, K, N, pad) in enumerate([(257, 4096, 256, 0), (130, 200, 6000, 4), (1, 8192, 512, 0), (40, 4100, 300, 1), (300, 60, 64, 0), (33, 2048, 520, 8)]):
+        X, W = matrix(M, K, torch.bfloat16, i, pad), matrix(N, K, torch.bfloat16, i + 9, 0, K ** -0.5)
+        layer = fmpq_mod.W16Layer(K, N, torch.bfloat16)
+        cases.append((layer, X, W, fmpq_mod.w16_pack_weights(layer, W)))
+    for turn in range(3):
+        order = cases[::-1] if turn % 2 else cases
+        got = [fmpq_mod.w16_gemm(layer, X, Wp) for layer, X, W, Wp in order]
+        for Y, (layer, X, W, Wp) in zip(got, order):
+            check(Y, X, W)
+
+
+@pytest.mark.gpu
 def test_long_rows_of_a_large_buffer(fmpq_mod):  # noqa: F811
     """Rows whose offsets pass 32 bits, in X, Y and the residual; only the rows are read and written."""
     import torch
