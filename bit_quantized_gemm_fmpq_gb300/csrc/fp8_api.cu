@@ -136,8 +136,9 @@ fmpq_status fp8_quantize(const fp8_layer* L, const void* X, int32_t dtype, int64
     if (M < 1 || M > kMaxRows || ldx < L->K) return FMPQ_ERR_UNSUPPORTED_SHAPE;
     if (!all_aligned16(A_packed, a_scales) || !element_aligned(X, dtype)) return FMPQ_ERR_MISALIGNED;
     if (fmpq_status s = check_device(L)) return s;
+    // (as the programmatic dependent of whatever is before it: the kernel waits for that one's end before it reads X)
     return launched(fmpq::launch_fp8_quantize(X, dtype, ldx, M, L->K, nullptr, 1, M, A_packed,
-                                              static_cast<float*>(a_scales), L->num_sms, false, st(stream)));
+                                              static_cast<float*>(a_scales), L->num_sms, true, st(stream)));
 }
 
 size_t fp8_gemm_workspace_bytes(const fp8_layer* L, int64_t M) {

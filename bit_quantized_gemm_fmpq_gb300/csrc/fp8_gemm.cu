@@ -293,6 +293,7 @@ __device__ __forceinline__ bool sum_blocks(Smem& s, uint32_t base, const float* 
 template <bool kGated, bool kEpi>
 __device__ __forceinline__ void epilogue(const Params& p, Smem& s, uint32_t rank, int warp, int lane, uint32_t tmem,
                                          volatile int* abort_flag) {
+    if (kEpi) dev::pdl_wait();   // bias and residual may come from the kernel before
     const int units = unit_count<kTokens>(p, s.tables);
     const int ew = warp - 4, q = warp & 3, h = ew >> 2;
     const uint32_t leader_ready = dev::mapa(&s.ready[0], 0);

@@ -389,6 +389,7 @@ __device__ __forceinline__ float load_shared(uint32_t address) {
 template <bool kGated, bool kEpi>
 __device__ __forceinline__ void epilogue(const Params& p, Smem<kEpi>& s, uint32_t rank, int warp, int lane, uint32_t tmem,
                                          volatile int* abort_flag) {
+    if (kEpi) dev::pdl_wait();   // bias and residual may come from the kernel before
     const int units = unit_count<kT>(p, s.tables);
     const int q = warp & 3, h = (warp - 4) >> 2;
     const int local = 32 * q + lane;
