@@ -347,11 +347,13 @@ __global__ void __launch_bounds__(1024) block_norm_long_kernel(const BlockNormAr
 }
 
 // Many rows on 16-byte boundaries: the CTAs stay, and the next rows are on their way into a ring in shared memory (bulk
-// copies) while one is worked on. Two vectors a thread (four where 1024 threads would not do). Its instructions bound it (4096 x 8192 bf16, both norms, a gate, codes: 59 us,
-// 4.0 TB/s, an issue slot used in 73 of 100; one norm and the residual 45; the sum alone 33, the copy rate), so what can be is uniform
-// or made once: a row's addresses are a base for the CTA and 32-bit offsets of a thread, arithmetic is on pairs, P (the weights'
-// type) and the norm are the compiler's. One CTA a row without the ring took 138, four vectors a thread 66, three CTAs of 40
-// registers in place of two 60, the weights in shared memory, which leave the ring two rows, 60.
+// copies) while one is worked on. Two vectors a thread (four where 1024 threads would not do). Its instructions and the chain of a row
+// through its barriers bound it (4096 x 8192 bf16, both norms, a gate, codes: 64 us, 236 MB = 3.7 TB/s, an issue slot used in 63 of 100; one
+// norm and the residual 43; the sum alone 30, the copy rate), so what can be is uniform or made once: a row's addresses are a base for the
+// CTA and 32-bit offsets of a thread, arithmetic is on pairs, P (the weights' type) and the norm are the compiler's. One CTA a row
+// without the ring took 138. No faster: four vectors a thread (70), three CTAs of 40 registers in place of two, the weights in shared
+// memory (which leave the ring two rows) or asked for before the sums, all within 1 us; without the codes' stores, the scales' or the
+// reduction of a block's maximum it would still take within 1 us of this.
 template <typename P>
 __device__ __forceinline__ void param_at(const void* p, uint32_t k, V8& v) {
     if constexpr (sizeof(P) == 2) {

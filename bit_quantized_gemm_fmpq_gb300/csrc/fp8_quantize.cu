@@ -23,9 +23,9 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
 
 // A warp takes 256 channels of a token, 16 lanes a block, 8 channels a lane (one 16-byte load, 8 bytes
 // of codes); blockIdx.y chooses the channels, so that a CTA's stores of a block's codes (128 bytes a
-// row) and scales are contiguous. kRows tokens a warp are in flight. 4096 x 8192 bf16: 29.4 us, 102 MB = 3.5 TB/s, 51%
-// of the copy rate: its instructions bound it. With 8 rounded divisions a lane it took 32.6, with one token in
-// flight or with four 31.3.
+// row) and scales are contiguous. kRows tokens a warp are in flight. 4096 x 8192 bf16: 27.4 us, 102 MB = 3.7 TB/s, 55%
+// of the copy rate (4096 x 28672: 83 us, 63%): its instructions bound it. With one form for dense and routed tokens, and maxima of two values,
+// it took 33 on the same day (100), with 8 rounded divisions a lane, one token in flight or four 2 to 3 us more still.
 template <typename T, bool kVec, int kRows, bool kRouted>
 __global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ X, int64_t ldx, int64_t M, int K, int nb,
                                                        const int32_t* __restrict__ positions, int slots, int64_t rows,
