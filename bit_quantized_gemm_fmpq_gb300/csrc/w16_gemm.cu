@@ -60,6 +60,10 @@ struct Params {
     int rows, N, out_n;  // out_n: columns of Y (gated: N / 2)
     int nb, pairs, experts, splits;
     int tile;            // rows of a unit, at most: a multiple of 32
+    int cut, cuts;       // rows of the units that a dense product's rows are cut into, and units of this launch in one of them
+    int first_cut;       // this launch's first
+    int last_launch;     // the rest of a product, behind the launch of its full rounds
+    int units;           // dense: of this launch
     int stages, stage_bytes;
     int32_t* status;
 };
@@ -134,7 +138,7 @@ __device__ __forceinline__ void fill_tables(const Params& p, Tables& s, int warp
 }
 
 __device__ __forceinline__ int unit_count(const Params& p, const Smem& s) {
-    return p.start != nullptr ? s.tables.first_unit[p.experts] : tiles_of(p, p.rows) * p.pairs;
+    return p.start != nullptr ? s.tables.first_unit[p.experts] : p.units;
 }
 
 __device__ __forceinline__ Unit unit_of(const Params& p, const Smem& s, int u, int split) {
@@ -156,15 +160,20 @@ __device__ __forceinline__ Unit unit_of(const Params& p, const Smem& s, int u, i
         t = i % tiles;
         r.pair = i / tiles;
     } else {
-        per = even_rows(count, p.tile);
-        const int tiles = (count + per - 1) / per;
-        const int band = u / (kBandTiles * p.pairs), in_band = u - band * kBandTiles * p.pairs;
+        per = p.cut;
+        const int v = p.first_cut + u / p.cuts, tiles = (count + per - 1) / per;
+        const int band = v / (kBandTiles * p.pairs), in_band = v - band * kBandTiles * p.pairs;
         const int high = min(kBandTiles, tiles - band * kBandTiles);
         t = band * kBandTiles + in_band % high;
         r.pair = in_band / high;
     }
     r.row0 = first + t * per;
     r.rows = min(per, count - t * per);
+    if (p.cuts > 1) {   // (nothing may be left for the last of them)
+        const int skip = u % p.cuts * p.tile;
+        r.row0 += skip;
+        r.rows = max(0, min(p.tile, r.rows - skip));
+    }
     r.b0 = static_cast<int>(static_cast<int64_t>(split) * p.nb / p.splits);
     r.b1 = static_cast<int>(static_cast<int64_t>(split + 1) * p.nb / p.splits);
     return r;
@@ -195,6 +204,7 @@ __device__ __forceinline__ void producer(const Params& p, const CUtensorMap* big
     bool ok = true;
     for (int u = at.cluster; ok && u < units; u += at.clusters) {
         const Unit t = unit_of(p, s, u, at.split);
+        if (t.rows == 0) continue;
         // this CTA's half of each part's rows
         const int parts = t.parts(), half0 = t.columns(0) >> 1, half1 = parts > 1 ? t.columns(1) >> 1 : 0;
         const int from0 = t.part_row0(0) + static_cast<int>(at.rank) * half0, from1 = t.part_row0(1) + static_cast<int>(at.rank) * half1;
@@ -267,6 +277,7 @@ __device__ __forceinline__ void mma_issuer(const Params& p, Smem& s, uint8_t* ri
     bool ok = true;
     for (int u = at.cluster; ok && u < units; u += at.clusters) {
         const Unit t = unit_of(p, s, u, at.split);
+        if (t.rows == 0) continue;
         const int parts = t.parts();
         const uint32_t idesc0 = idesc16(256, static_cast<uint32_t>(t.columns(0)), static_cast<uint32_t>(p.bf16));
         const uint32_t idesc1 = idesc16(256, static_cast<uint32_t>(t.columns(1)), static_cast<uint32_t>(p.bf16));
@@ -466,6 +477,11 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* other
     int part = 0;
     for (int u = at.cluster; u < units; ++np) {
         const Unit whole = unit_of(p, s, u, at.split);
+        if (whole.rows == 0) {
+            u += at.clusters;
+            --np;
+            continue;
+        }
         struct {
             int e, pair, rows, row0;
         } const t{whole.e, whole.pair, whole.part_rows(part), whole.part_row0(part)};
@@ -632,9 +648,15 @@ w16_kernel(const Params p, const __grid_constant__ CUtensorMap big, const __grid
         dev::fence_barrier_init();
     }
     if (warp == 2) dev::tmem_alloc_pair(&s.tmem_base, 512);
-    // (launched as the programmatic dependent of whatever is before it: everything up to here runs under that one's end)
-    dev::pdl_wait();
-    dev::pdl_launch_dependents();
+    // (launched as the programmatic dependent of whatever is before it: everything up to here runs under that one's end. The rest
+    // of a product needs nothing of the launch before it, which lets it start once it has waited for the one before that; it sees
+    // what that one wrote, and ends behind the launch before it.)
+    if (p.last_launch) {
+        __threadfence();
+    } else {
+        dev::pdl_wait();
+        dev::pdl_launch_dependents();
+    }
     if (p.start != nullptr) fill_tables(p, s.tables, warp, lane);
     dev::tc_fence_before();
     __syncthreads();
@@ -654,6 +676,10 @@ w16_kernel(const Params p, const __grid_constant__ CUtensorMap big, const __grid
     dev::tc_fence_before();
     __syncthreads();
     dev::cluster_sync();   // the other CTAs' MMAs, commits, sums and arrivals on this one are done
+    if (p.last_launch) {
+        dev::pdl_wait();
+        dev::pdl_launch_dependents();
+    }
     if (warp == 2) {
         dev::tc_fence_after();
         dev::tmem_dealloc_pair(tmem, 512);
@@ -766,18 +792,43 @@ int resident_clusters(const w16_layer& L, int splits) {
     return most;
 }
 
+// The units that are left of full rounds, in a launch of their own: each cut into `cuts` of `tile` rows, K in `splits` parts.
+struct Rest {
+    int units, tile, cuts, splits;   // units: of the product, 0: there is no such launch
+    double time;
+};
 struct Shape {
     int tile, splits, grid, stages, stage_bytes;
+    Rest rest;
 };
 
 Shape with_ring(int tile, int splits, int64_t units, int clusters) {
-    Shape s{tile, splits, 0, 0, 0};
+    Shape s{tile, splits, 0, 0, 0, {}};
     s.grid = static_cast<int>(units < clusters ? units : clusters) * 2 * splits;
     s.stage_bytes = kTileBytes + tile / 2 * 128;
     const int others = (splits - 1) * tile * 128 * 4;
     s.stages = (kRingBytes - others) / s.stage_bytes;
     if (s.stages > kMaxStages) s.stages = kMaxStages;
     return s;
+}
+
+// The best such launch for `units` of `per` rows, all of it resident at once. It starts under the full rounds' end and still costs about
+// 6000 clk, the exchange 1500 more: 300 x 4096 -> 20480 62 to 55 us, 1 x 8192 -> 28672 82 to 77, 2048 x 4096 -> 12288 127 to 123; counted at
+// 1500, 300 x 1024 -> 20000 lost 3 of 24 and 520 x 4096 -> 11008 3 of 48.
+template <typename F>
+Rest rest_of(const w16_layer& L, int units, int per, const F& block_of) {
+    Rest best{0, 0, 0, 0, 1e30};
+    for (int splits = 1; splits <= kMaxSplits; splits *= 2) {
+        if (splits > 1 && L.nb < 4 * splits) break;
+        const int clusters = resident_clusters(L, splits);
+        for (int tile = 32; tile <= kPartRows && tile <= per; tile += 32) {
+            const int cuts = (per + tile - 1) / tile;
+            if (units * cuts > clusters || with_ring(tile, splits, 1, 1).stages < 4) continue;
+            const double time = (L.nb + splits - 1) / splits * block_of(tile) + (splits > 1 ? 1500.0 : 0.0) + 6000.0 + 14.0 * tile;
+            if (time < best.time) best = Rest{units, tile, cuts, splits, time};
+        }
+    }
+    return best;
 }
 
 // No more units than these, whatever the groups: even_rows cuts none that is not the last of its group below half a tile.
@@ -800,6 +851,7 @@ Shape shape_of(const w16_layer& L, const W16Args& a) {
     // the experts' loads are known on the device only: every one in use is taken to have the mean, and a sixth more for the spread
     // (1554 rows of 10 uneven experts, 1404 -> 2012, in tiles of 64, 128, 192 and 256: 37, 28, 32 and 36 us)
     const int used = grouped ? (L.experts < rows ? L.experts : rows) : 1, load = grouped ? (7 * rows / used + 5) / 6 : rows;
+    const auto block_of = [](int per) { return per > kPartRows ? 2.25 * per : 400.0 + 0.65 * per; };
     Shape best{};
     double least = 0.0;
     for (int splits = 1; splits <= (grouped ? 1 : kMaxSplits); splits *= 2) {
@@ -810,12 +862,17 @@ Shape shape_of(const w16_layer& L, const W16Args& a) {
             if (per != tile) continue;
             const int64_t tiles = (load + per - 1) / per, units = tiles * L.pairs * used, rounds = (units + clusters - 1) / clusters;
             if (splits > 1 && rounds > 1) continue;
-            const Shape s = with_ring(tile, splits, grouped ? most_units(L, used, rows, tile) : units, clusters);
+            Shape s = with_ring(tile, splits, grouped ? most_units(L, used, rows, tile) : units, clusters);
             if (s.stages < 4) continue;
-            const double block = per > kPartRows ? 2.25 * per : 400.0 + 0.65 * per;
-            // what nothing runs under: the last unit's epilogue, two-part units' own, and the exchange
-            const double end = 14.0 * per * (per > kPartRows ? rounds : 1) + (splits > 1 ? 1500.0 : 0.0);
-            const double time = rounds * ((L.nb + splits - 1) / splits * block) + end;
+            const double round = L.nb * block_of(per) + (per > kPartRows ? 14.0 * per : 0.0);
+            double time = splits > 1 ? (L.nb + splits - 1) / splits * block_of(per) + 1500.0 + 14.0 * per : rounds * round + 14.0 * per;
+            if (!grouped && splits == 1 && rounds > 1 && units % clusters != 0) {
+                const Rest r = rest_of(L, static_cast<int>(units % clusters), per, block_of);
+                if (r.time < round) {
+                    s.rest = r;
+                    time += r.time - round;
+                }
+            }
             if (best.grid == 0 || time < least) {
                 best = s;
                 least = time;
@@ -852,19 +909,32 @@ cudaError_t launch_w16_gemm(const w16_layer& L, const W16Args& a, cudaStream_t s
     p.nb = L.nb;
     p.pairs = L.pairs;
     p.experts = L.experts;
-    p.splits = shape.splits;
-    p.tile = shape.tile;
-    p.stages = shape.stages;
-    p.stage_bytes = shape.stage_bytes;
     p.status = L.d_status;
     CUtensorMap big, small;
     if (!w16::encode_rows(&big, a, L, w16::kBigBox) || !w16::encode_rows(&small, a, L, w16::kSmallBox)) return cudaErrorInvalidValue;
     auto fn = L.gated ? w16::w16_kernel<true> : w16::w16_kernel<false>;
     const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), w16::kSmemBytes);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = w16::config(shape.grid, 2 * shape.splits, w16::kSmemBytes, stream, attr);
-    return cudaLaunchKernelEx(&cfg, fn, p, big, small);
+    auto launch = [&](const w16::Shape& s) {
+        p.tile = s.tile;
+        p.splits = s.splits;
+        p.stages = s.stages;
+        p.stage_bytes = s.stage_bytes;
+        cudaLaunchAttribute attr[2];
+        const cudaLaunchConfig_t cfg = w16::config(s.grid, 2 * s.splits, w16::kSmemBytes, stream, attr);
+        return cudaLaunchKernelEx(&cfg, fn, p, big, small);
+    };
+    const w16::Rest& rest = shape.rest;
+    p.cut = shape.tile;
+    p.cuts = 1;
+    p.units = static_cast<int>((a.rows + p.cut - 1) / p.cut * L.pairs - rest.units);   // (experts: not used)
+    const cudaError_t first = launch(shape);
+    if (first != cudaSuccess || rest.units == 0) return first;
+    p.first_cut = p.units;
+    p.cuts = rest.cuts;
+    p.units = rest.units * rest.cuts;
+    p.last_launch = 1;
+    return launch(w16::with_ring(rest.tile, rest.splits, p.units, p.units));
 }
 
 cudaError_t launch_w16_pack(const w16_layer& L, int expert, const void* W, int64_t ld_n, int64_t ld_k, void* Wp, cudaStream_t stream) {

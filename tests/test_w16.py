@@ -63,7 +63,9 @@ def matrix(rows, K, dtype, seed, pad=0, scale=1.0):
 # one row; K split by 4, by 2; several tiles; odd everything; one channel; rows that need aligning; wide
 SIZES = [(1, 2048, 512, 0, 0), (5, 1024, 300, 0, 0), (40, 1536, 4000, 8, 0), (33, 300, 257, 1, 1), (64, 64, 130, 0, 0), (3, 1, 1, 0, 0),
          (130, 200, 6000, 4, 4), (300, 260, 515, 5, 0), (700, 192, 1028, 3, 4), (1500, 512, 770, 0, 0), (257, 4096, 256, 0, 0),
-         (300, 128, 20000, 0, 0), (513, 64, 19999, 0, 0)]
+         (300, 128, 20000, 0, 0), (513, 64, 19999, 0, 0),
+         # full rounds, and a rest in a launch of its own
+         (300, 1024, 20000, 0, 0), (520, 2048, 10000, 8, 0), (1000, 1500, 12345, 0, 1), (2000, 1024, 10240, 0, 0)]
 
 
 @pytest.mark.gpu
@@ -157,6 +159,49 @@ def test_groups(fmpq_mod, kind, experts, K, N, gated):  # noqa: F811
             check(Z[at], X[at], W[e], None, gated=gated)
     for at in (slice(0, before), slice(rows - behind, rows)):
         assert bool((Y[at] == 7).all()) and bool((Z[at] == 7).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,K,N", [(300, 4096, 20480), (1, 8192, 28672), (2048, 2048, 12288)])
+def test_rest_of_a_product_in_a_chain(fmpq_mod, M, K, N):  # noqa: F811
+    """A residual that every product updates in place, and an input that the kernel before writes: products with a launch for their
+    rest, one after another and captured, give what they give with a wait between them."""
+    import torch
+    X, W = matrix(M, K, torch.bfloat16, 1), matrix(N, K, torch.bfloat16, 2, 0, 0.3 * K ** -0.5)
+    layer = fmpq_mod.W16Layer(K, N, torch.bfloat16)
+    Wp = fmpq_mod.w16_pack_weights(layer, W)
+    start = matrix(M, N, torch.bfloat16, 3)
+
+    def chain(r, x, wait=False):
+        for _ in range(6):
+            fmpq_mod.w16_gemm(layer, x, Wp, residual=r, Y=r)
+            if wait:
+                torch.cuda.synchronize()
+            x.copy_(r[:, :K])           # (K <= N)
+            if wait:
+                torch.cuda.synchronize()
+            fmpq_mod.w16_gemm(layer, x, Wp, residual=r, activation="silu", Y=r)
+            if wait:
+                torch.cuda.synchronize()
+            x.mul_(0.5)
+
+    want, x = start.clone(), X.clone()
+    chain(want, x, True)
+    for _ in range(5):
+        got, x = start.clone(), X.clone()
+        chain(got, x)
+        assert torch.equal(got, want)
+    got, x = start.clone(), X.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain(got, x)
+    for _ in range(5):
+        got.copy_(start)
+        x.copy_(X)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    assert bool(torch.isfinite(want).all()) and fmpq_mod.w16_device_status(layer) == 0
 
 
 @pytest.mark.gpu
