@@ -23,10 +23,10 @@ namespace {
 // Arithmetic runs on pairs (packed FP32 instructions): a vector of 8 channels is four of them.
 using V8 = float2[4];
 
-// How the vectors of a kernel lie: kWhole: K is a multiple of 8 and rows, weights and outputs are on 16-byte boundaries, so every
-// vector below K is a 16-byte access; kMixed: a row's last vector may be partial; kHalves: the same on 8-byte boundaries, in two
-// accesses; kSingle: elements one by one. (777 x 2868 fp16, a layer norm: kHalves 9.5 us, kSingle 17.)
-enum { kWhole = 0, kMixed = 1, kHalves = 2, kSingle = 3 };
+// How the vectors of a kernel lie: kWhole: K is a multiple of 8 and weights and outputs are on 16-byte boundaries, so every vector
+// below K is a 16-byte access; kMixed: a row's last vector may be partial; kAny: any alignment of the elements (4481 x 4291, X 2 bytes off:
+// 90 us, by single elements 119; 777 x 2868, rows on 8-byte boundaries: 10.2, 17).
+enum { kWhole = 0, kMixed = 1, kAny = 2 };
 // Which norm: known to the compiler, or a branch.
 enum { kRms = 0, kLayer = 1, kEither = 2 };
 
@@ -64,14 +64,30 @@ __device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float
 __device__ __forceinline__ float& at(V8& v, int c) { return (c & 1) ? v[c >> 1].y : v[c >> 1].x; }
 __device__ __forceinline__ float at(const V8& v, int c) { return (c & 1) ? v[c >> 1].y : v[c >> 1].x; }
 
-// Channels k .. k + 7 of a row, those past K as 0 (kWhole: k < K).
+// Eight elements that begin `off` (1 to 7) elements behind a 16-byte boundary, from the two pieces of 16 bytes that hold them.
+__device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, uint32_t off) {
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = (off & 4) ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = (off & 2) ? w[i + 1] : w[i];
+    const uint32_t by = (off & 1) * 16;
+    return make_uint4(__funnelshift_r(w[0], w[1], by), __funnelshift_r(w[1], w[2], by), __funnelshift_r(w[2], w[3], by),
+                      __funnelshift_r(w[3], w[4], by));
+}
+// Of an address: the boundary before it, and the elements between.
+__device__ __forceinline__ uint32_t elements_past(const void* p) { return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u) >> 1; }
+
+// Channels k .. k + 7 of a row, those past K as 0 (kWhole: k < K). kAny reads whole pieces of 16 bytes, which hold one of the row's
+// elements at least, so they lie in its allocation.
 template <typename T, int kLie>
 __device__ __forceinline__ void load8(const T* row, int k, int K, V8& v) {
     if (kLie == kWhole || (kLie == kMixed && k + 8 <= K)) {
         unpack8<T>(*reinterpret_cast<const uint4*>(row + k), v);
-    } else if (kLie == kHalves && k + 8 <= K) {
-        const uint2 a = *reinterpret_cast<const uint2*>(row + k), b = *reinterpret_cast<const uint2*>(row + k + 4);
-        unpack8<T>(make_uint4(a.x, a.y, b.x, b.y), v);
+    } else if (kLie == kAny && k + 8 <= K) {
+        const uint32_t off = elements_past(row);
+        const uint4* at = reinterpret_cast<const uint4*>(row + k - off);
+        unpack8<T>(off == 0 ? at[0] : shifted(at[0], at[1], off), v);
     } else {
 #pragma unroll
         for (int c = 0; c < 8; ++c) at(v, c) = k + c < K ? load_as_float(row + k + c) : 0.0f;
@@ -82,10 +98,23 @@ __device__ __forceinline__ void store8(T* row, int k, int K, const V8& v) {
     if (kLie == kWhole || (kLie == kMixed && k + 8 <= K)) {
         const T* t = nullptr;
         *reinterpret_cast<uint4*>(row + k) = make_uint4(pack2(v[0], t), pack2(v[1], t), pack2(v[2], t), pack2(v[3], t));
-    } else if (kLie == kHalves && k + 8 <= K) {
+    } else if (kLie == kAny && k + 8 <= K) {   // in the widest accesses that the row's start allows
         const T* t = nullptr;
-        *reinterpret_cast<uint2*>(row + k) = make_uint2(pack2(v[0], t), pack2(v[1], t));
-        *reinterpret_cast<uint2*>(row + k + 4) = make_uint2(pack2(v[2], t), pack2(v[3], t));
+        T* to = row + k;
+        const uint32_t o[4] = {pack2(v[0], t), pack2(v[1], t), pack2(v[2], t), pack2(v[3], t)};
+        const uint32_t past = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) & 7u);
+        if (past == 0) {
+            reinterpret_cast<uint2*>(to)[0] = make_uint2(o[0], o[1]);
+            reinterpret_cast<uint2*>(to)[1] = make_uint2(o[2], o[3]);
+        } else if (past == 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t*>(to)[i] = o[i];
+        } else {
+            *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(o[0]);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) reinterpret_cast<uint32_t*>(to + 1)[i] = __funnelshift_r(o[i], o[i + 1], 16);
+            *reinterpret_cast<uint16_t*>(to + 7) = static_cast<uint16_t>(o[3] >> 16);
+        }
     } else {
 #pragma unroll
         for (int c = 0; c < 8; ++c)
@@ -103,9 +132,6 @@ __device__ __forceinline__ void param8(const void* p, int fp32, int64_t first, i
     if (kLie == kWhole || (kLie == kMixed && k + 8 <= K)) {
         const float4 a = *reinterpret_cast<const float4*>(f), b = *reinterpret_cast<const float4*>(f + 4);
         v[0] = make_float2(a.x, a.y), v[1] = make_float2(a.z, a.w), v[2] = make_float2(b.x, b.y), v[3] = make_float2(b.z, b.w);
-    } else if (kLie == kHalves && k + 8 <= K) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = reinterpret_cast<const float2*>(f)[i];
     } else {
 #pragma unroll
         for (int c = 0; c < 8; ++c) at(v, c) = k + c < K ? f[c] : 0.0f;
@@ -247,7 +273,7 @@ __device__ __forceinline__ void statistics(const BlockNormArgs& p, const V8 (&v)
 
 // One CTA a row, kV vectors of 8 channels a thread: blockDim.x * 8 * kV >= nb * 128.
 template <typename T, int kLie, int kV>
-__global__ void __launch_bounds__(kV == 1 ? 1024 : 512) block_norm_kernel(const BlockNormArgs p) {
+__global__ void __launch_bounds__(kV <= 2 ? 1024 : 512) block_norm_kernel(const BlockNormArgs p) {
     __shared__ Sums sums;
     int turn = 0;
     dev::pdl_wait();
@@ -346,7 +372,8 @@ __global__ void __launch_bounds__(1024) block_norm_long_kernel(const BlockNormAr
     }
 }
 
-// Many rows on 16-byte boundaries: the CTAs stay, and the next rows are on their way into a ring in shared memory (bulk
+// Many rows, weights and outputs on 16-byte boundaries, X and residual anywhere (2325 x 2816 fp16, rows of X and residual 2 bytes off, both
+// norms: 13.6 us, 36 as one CTA a row by single elements): the CTAs stay, and the next rows are on their way into a ring in shared memory (bulk
 // copies) while one is worked on. Two vectors a thread (four where 1024 threads would not do). Its instructions and the chain of a row
 // through its barriers bound it (4096 x 8192 bf16, both norms, a gate, codes: 64 us, 236 MB = 3.7 TB/s, an issue slot used in 63 of 100; one
 // norm and the residual 43; the sum alone 30, the copy rate), so what can be is uniform or made once: a row's addresses are a base for the
@@ -370,13 +397,17 @@ __global__ void __launch_bounds__(1024) block_norm_stream_kernel(const BlockNorm
     extern __shared__ __align__(128) uint8_t ring[];   // [stage][X's row, then the residual's]
     __shared__ Sums sums;
     __shared__ uint64_t landed[kMostStages];
-    const uint32_t row_bytes = static_cast<uint32_t>(p.K) * 2, slot_bytes = p.residual != nullptr ? 2 * row_bytes : row_bytes;
+    // (a row of a slot has room for the piece of 16 bytes more that one not on a boundary takes)
+    const uint32_t row_bytes = static_cast<uint32_t>(p.K) * 2 + 16, slot_bytes = p.residual != nullptr ? 2 * row_bytes : row_bytes;
     const int rows = static_cast<int>(p.M), step = static_cast<int>(gridDim.x);
     auto load = [&](int m, int stage) {
-        dev::mbar_arrive_expect_tx(&landed[stage], slot_bytes);
-        dev::bulk_g2s(ring + stage * slot_bytes, static_cast<const T*>(p.X) + m * p.ldx, row_bytes, &landed[stage]);
-        if (p.residual != nullptr)
-            dev::bulk_g2s(ring + stage * slot_bytes + row_bytes, static_cast<const T*>(p.residual) + m * p.ldr, row_bytes, &landed[stage]);
+        const T* x = static_cast<const T*>(p.X) + m * p.ldx;
+        const T* r = static_cast<const T*>(p.residual) + m * p.ldr;
+        const uint32_t x_off = elements_past(x), r_off = elements_past(r);
+        const uint32_t x_bytes = row_bytes - (x_off == 0 ? 16u : 0u), r_bytes = p.residual != nullptr ? row_bytes - (r_off == 0 ? 16u : 0u) : 0u;
+        dev::mbar_arrive_expect_tx(&landed[stage], x_bytes + r_bytes);
+        dev::bulk_g2s(ring + stage * slot_bytes, x - x_off, x_bytes, &landed[stage]);
+        if (p.residual != nullptr) dev::bulk_g2s(ring + stage * slot_bytes + row_bytes, r - r_off, r_bytes, &landed[stage]);
     };
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i) dev::mbar_init(&landed[i], 1);
@@ -408,12 +439,17 @@ __global__ void __launch_bounds__(1024) block_norm_stream_kernel(const BlockNorm
         // (a copy that this CTA issued lands; should one not, within about a second, its row comes out NaN)
         const bool there = dev::mbar_wait(&landed[stage], phase, nullptr);
         const uint8_t* x = ring + stage * slot_bytes;
+        // a vector of a row in the ring, which begins `off` elements into it
+        auto from_ring = [&](const uint8_t* row, uint32_t off, uint32_t k, V8& v) {
+            const uint4* at = reinterpret_cast<const uint4*>(row + k * 2u);
+            unpack8<T>(off == 0 ? at[0] : shifted(at[0], at[1], off), v);
+        };
         V8 v[kV];
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) v[i][c] = both(there ? 0.0f : __int_as_float(0x7FFFFFFF));
-            if (in[i] && there) unpack8<T>(*reinterpret_cast<const uint4*>(x + k[i] * 2u), v[i]);
+            if (in[i] && there) from_ring(x, elements_past(static_cast<const T*>(p.X) + m * p.ldx), k[i], v[i]);
         }
         float mean = 0.0f, inv;
         // v = (v - mean) * inv * w + b
@@ -466,7 +502,7 @@ __global__ void __launch_bounds__(1024) block_norm_stream_kernel(const BlockNorm
             for (int i = 0; i < kV; ++i) {
                 if (!in[i]) continue;
                 V8 t;
-                unpack8<T>(*reinterpret_cast<const uint4*>(x + row_bytes + k[i] * 2u), t);
+                from_ring(x + row_bytes, elements_past(static_cast<const T*>(p.residual) + m * p.ldr), k[i], t);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) v[i][c] = dev::ffma2(both(p.residual_scale), t[c], v[i][c]);
             }
@@ -509,57 +545,65 @@ __global__ void __launch_bounds__(1024) block_norm_stream_kernel(const BlockNorm
     }
 }
 
+// Threads that a row of nb blocks takes at `per` vectors each.
+int threads_for(int nb, int per) { return ((nb * 16 + per - 1) / per + 31) / 32 * 32; }
+
+constexpr int kRingBytes = 225 * 1024;
+
+// Whether a CTA's ring holds two rows; and the kernel over it.
+bool fits_stream(const BlockNormArgs& p) {
+    return p.K % 8 == 0 && p.K >= 512 && threads_for(p.nb, 4) <= 1024 && 2 * (p.K * 2 + 16) * (p.residual != nullptr ? 2 : 1) <= kRingBytes &&
+           p.M * p.nb * 128 < INT64_C(1) << 32;   // (32-bit offsets of the codes)
+}
+template <typename T>
+cudaError_t block_norm_stream(const BlockNormArgs& p, int num_sms, cudaStream_t stream) {
+    using std::integral_constant;
+    const int per = threads_for(p.nb, 2) <= 1024 ? 2 : 4, threads = threads_for(p.nb, per);
+    auto of = [&](auto norm, auto v) {
+        return p.param_f32 ? block_norm_stream_kernel<T, float, norm.value, v.value> : block_norm_stream_kernel<T, T, norm.value, v.value>;
+    };
+    auto fn = per == 2 ? (p.layer_norm ? of(integral_constant<int, kLayer>{}, integral_constant<int, 2>{})
+                                       : of(integral_constant<int, kRms>{}, integral_constant<int, 2>{}))
+                       : (p.layer_norm ? of(integral_constant<int, kLayer>{}, integral_constant<int, 4>{})
+                                       : of(integral_constant<int, kRms>{}, integral_constant<int, 4>{}));
+    const int slot = (p.K * 2 + 16) * (p.residual != nullptr ? 2 : 1);
+    int resident = 1024 / threads;   // (64 registers a thread)
+    if (resident > 16) resident = 16;
+    int stages = 200 * 1024 / resident / slot;
+    stages = stages > kMostStages ? kMostStages : stages < 2 ? 2 : stages;
+    const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), kRingBytes);
+    if (e != cudaSuccess) return e;
+    const int64_t ctas = static_cast<int64_t>(num_sms) * resident;
+    return launch_after(fn, dim3(static_cast<unsigned>(p.M < ctas ? p.M : ctas)), threads, stages * slot, true, stream, p, stages);
+}
+
+// One CTA a row. Few rows: as many threads a row as there are vectors, for the shortest chain; else up to 4 vectors a thread.
 template <typename T, int kLie>
-cudaError_t block_norm_as(const BlockNormArgs& p, int num_sms, cudaStream_t stream) {
-    const int vectors = p.nb * 16;   // of 8 channels
+cudaError_t block_norm_rows(const BlockNormArgs& p, bool few, int num_sms, cudaStream_t stream) {
     const int64_t most = static_cast<int64_t>(num_sms) * 64;
-    const unsigned grid = static_cast<unsigned>(p.M < most ? p.M : most);
-    auto threads_for = [&](int per) { return ((vectors + per - 1) / per + 31) / 32 * 32; };
-    const bool few = p.M < 2 * num_sms;
-    const int slot = p.K * (p.residual != nullptr ? 4 : 2), ring = 224 * 1024, per = threads_for(2) <= 1024 ? 2 : 4;
-    if (kLie == kMixed && !few && p.K % 8 == 0 && p.K >= 512 && threads_for(per) <= 1024 && 2 * slot <= ring &&
-        p.M * p.nb * 128 < INT64_C(1) << 32) {   // (32-bit offsets of the codes)
-        auto of = [&](auto norm, auto v) {
-            return p.param_f32 ? block_norm_stream_kernel<T, float, norm.value, v.value> : block_norm_stream_kernel<T, T, norm.value, v.value>;
-        };
-        using std::integral_constant;
-        auto fn = per == 2 ? (p.layer_norm ? of(integral_constant<int, kLayer>{}, integral_constant<int, 2>{})
-                                           : of(integral_constant<int, kRms>{}, integral_constant<int, 2>{}))
-                           : (p.layer_norm ? of(integral_constant<int, kLayer>{}, integral_constant<int, 4>{})
-                                           : of(integral_constant<int, kRms>{}, integral_constant<int, 4>{}));
-        const int threads = threads_for(per);
-        int resident = 1024 / threads;   // (64 registers a thread)
-        if (resident > 16) resident = 16;
-        int stages = 200 * 1024 / resident / slot;
-        stages = stages > kMostStages ? kMostStages : stages < 2 ? 2 : stages;
-        const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), ring);
-        if (e != cudaSuccess) return e;
-        const int64_t ctas = static_cast<int64_t>(num_sms) * resident;
-        return launch_after(fn, dim3(static_cast<unsigned>(p.M < ctas ? p.M : ctas)), threads, stages * slot, true, stream, p, stages);
-    }
-    // few rows: as many threads a row as there are vectors, for the shortest chain; else up to 4 vectors a thread
-    auto row_kernel = [&](auto kernel, int per) { return launch_after(kernel, dim3(grid), threads_for(per), 0, true, stream, p); };
-    if (few && threads_for(1) <= 1024) return row_kernel(block_norm_kernel<T, kLie, 1>, 1);
-    if (threads_for(4) > 512) return launch_after(block_norm_long_kernel<T, kLie>, dim3(grid), 1024, 0, true, stream, p);
-    if (threads_for(4) >= 128) return row_kernel(block_norm_kernel<T, kLie, 4>, 4);
-    if (threads_for(2) >= 64) return row_kernel(block_norm_kernel<T, kLie, 2>, 2);
-    return row_kernel(block_norm_kernel<T, kLie, 1>, 1);
+    const dim3 grid(static_cast<unsigned>(p.M < most ? p.M : most));
+    auto launch = [&](auto kernel, int per) { return launch_after(kernel, grid, threads_for(p.nb, per), 0, true, stream, p); };
+    if (few && threads_for(p.nb, 1) <= 1024) return launch(block_norm_kernel<T, kLie, 1>, 1);
+    if (few && threads_for(p.nb, 2) <= 1024) return launch(block_norm_kernel<T, kLie, 2>, 2);
+    if (threads_for(p.nb, 4) > 512) return launch_after(block_norm_long_kernel<T, kLie>, grid, 1024, 0, true, stream, p);
+    if (threads_for(p.nb, 4) >= 128) return launch(block_norm_kernel<T, kLie, 4>, 4);
+    if (threads_for(p.nb, 2) >= 64) return launch(block_norm_kernel<T, kLie, 2>, 2);
+    return launch(block_norm_kernel<T, kLie, 1>, 1);
 }
 
 template <typename T>
 cudaError_t block_norm_of(const BlockNormArgs& p, int num_sms, cudaStream_t stream) {
-    auto on = [&](int bytes) {   // every pointer and row starts on a boundary of `bytes`
-        uintptr_t all = 0;
-        for (const void* v : {p.X, p.residual, static_cast<const void*>(p.R), static_cast<const void*>(p.Y), p.gate, p.weight, p.bias,
-                              p.post_weight, p.post_bias})
-            all |= reinterpret_cast<uintptr_t>(v);
-        for (int64_t ld : {p.ldx, p.ldr, p.ldo, p.ldy}) all |= static_cast<uintptr_t>(ld) * 2;
-        all |= static_cast<uintptr_t>(p.ldg) * (p.gate_f32 ? 4 : 2);
-        return (all & (bytes - 1)) == 0;
-    };
-    if (on(16)) return block_norm_as<T, kMixed>(p, num_sms, stream);
-    if (on(8)) return block_norm_as<T, kHalves>(p, num_sms, stream);
-    return block_norm_as<T, kSingle>(p, num_sms, stream);
+    // bits of the addresses where rows and vectors start
+    uintptr_t in = 0, out = 0;
+    for (const void* v : {p.X, p.residual}) in |= reinterpret_cast<uintptr_t>(v);
+    for (int64_t ld : {p.ldx, p.ldr}) in |= static_cast<uintptr_t>(ld) * 2;
+    for (const void* v : {static_cast<const void*>(p.R), static_cast<const void*>(p.Y), p.gate, p.weight, p.bias, p.post_weight, p.post_bias})
+        out |= reinterpret_cast<uintptr_t>(v);
+    for (int64_t ld : {p.ldo, p.ldy}) out |= static_cast<uintptr_t>(ld) * 2;
+    out |= static_cast<uintptr_t>(p.ldg) * (p.gate_f32 ? 4 : 2);
+    const bool few = p.M < 2 * num_sms;
+    if (!few && (out & 15u) == 0 && fits_stream(p)) return block_norm_stream<T>(p, num_sms, stream);
+    return ((in | out) & 15u) == 0 ? block_norm_rows<T, kMixed>(p, few, num_sms, stream) : block_norm_rows<T, kAny>(p, few, num_sms, stream);
 }
 
 }  // namespace

@@ -108,7 +108,8 @@ __device__ __forceinline__ int tiles_of(const Params& p, int count) {
     return count > 0 ? (count + even_rows(count, p.tile) - 1) / even_rows(count, p.tile) : 0;
 }
 
-// Every thread calls it; a barrier must follow. Group bounds outside [0, rows] are cut to it.
+// Every thread calls it; a barrier must follow. Group bounds outside [0, rows] are cut to it, and a group begins no earlier than those
+// before it end: no row is in two, so there are never more units than the host counts with.
 __device__ __forceinline__ void fill_tables(const Params& p, Tables& s, int warp, int lane) {
     for (int e = threadIdx.x; e < p.experts; e += blockDim.x) {
         const int64_t from = p.start[e], to = p.count != nullptr ? from + p.count[e] : p.start[e + 1];
@@ -119,22 +120,36 @@ __device__ __forceinline__ void fill_tables(const Params& p, Tables& s, int warp
     }
     __syncthreads();
     if (warp != 3) return;
-    const int run = (p.experts + 31) / 32;
-    auto units_of = [&](int e) { return e < p.experts ? tiles_of(p, s.count[e]) * p.pairs : 0; };
+    // lane l: the run of experts [l * run, l * run + run)
+    const int run = (p.experts + 31) / 32, begin = lane * run, end = min(begin + run, p.experts);
+    int last = 0;   // where the groups so far end
+    for (int e = begin; e < end; ++e)
+        if (s.count[e] > 0) last = max(last, s.start[e] + s.count[e]);
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, last, d);
+        if (lane >= d) last = max(last, o);
+    }
+    last = __shfl_up_sync(0xFFFFFFFFu, last, 1);
+    if (lane == 0) last = 0;
     int sum = 0;
-    for (int i = 0; i < run; ++i) sum += units_of(lane * run + i);
+    for (int e = begin; e < end; ++e) {
+        const int cut = min(s.count[e], max(0, last - s.start[e]));
+        s.start[e] += cut;
+        s.count[e] -= cut;
+        if (s.count[e] > 0) last = max(last, s.start[e] + s.count[e]);
+        sum += tiles_of(p, s.count[e]) * p.pairs;
+    }
     int before = sum;
     for (int d = 1; d < 32; d <<= 1) {
         const int o = __shfl_up_sync(0xFFFFFFFFu, before, d);
         if (lane >= d) before += o;
     }
+    if (lane == 31) s.first_unit[p.experts] = before;
     before -= sum;
-    for (int i = 0; i < run; ++i) {
-        const int e = lane * run + i;
-        if (e <= p.experts) s.first_unit[e] = before;
-        before += units_of(e);
+    for (int e = begin; e < end; ++e) {
+        s.first_unit[e] = before;
+        before += tiles_of(p, s.count[e]) * p.pairs;
     }
-    if (lane == 31 && p.experts == 32 * run) s.first_unit[p.experts] = before;
 }
 
 __device__ __forceinline__ int unit_count(const Params& p, const Smem& s) {
@@ -842,7 +857,7 @@ int64_t most_units(const w16_layer& L, int used, int rows, int tile) {
 // the epilogue, which has no accumulator left to run beside: worth it where it saves a round (777 x 2048 -> 5632 in 320: 22) or where
 // an expert's load is a little above 256 (32768 rows of 128, 4096 -> 2048: 463 us in tiles of 256, 439 in 320).
 // Units that leave half the pairs idle split K: 1 x 8192 -> 8192 in 1, 2 and 4 parts 33.5, 25.2 and 25.4 us, 16 x 8192 -> 1024 33.2,
-// 20.1 and 13.3, 128 x 8192 -> 8192 35.6 and 31.4; the exchange takes about 1500 clk. (The last round's blocks cut evenly over all pairs, their
+// 20.1 and 13.3, 128 x 8192 -> 8192 35.6 and 31.4, one row of 65 experts, 6400 -> 512, 29.5 and 14.4 in 4; the exchange takes about 1500 clk. (The last round's blocks cut evenly over all pairs, their
 // sums in global memory and the last to arrive adding them: 31.6 in place of 25.2, 17.2 of 13.3, 64 units of a token's 8 experts 35.8 of 28.3,
 // and 2048 x 4096 -> 12288, 4 units in the last round, no faster.)
 Shape shape_of(const w16_layer& L, const W16Args& a) {
@@ -854,15 +869,16 @@ Shape shape_of(const w16_layer& L, const W16Args& a) {
     const auto block_of = [](int per) { return per > kPartRows ? 2.25 * per : 400.0 + 0.65 * per; };
     Shape best{};
     double least = 0.0;
-    for (int splits = 1; splits <= (grouped ? 1 : kMaxSplits); splits *= 2) {
+    for (int splits = 1; splits <= kMaxSplits; splits *= 2) {
         const int clusters = resident_clusters(L, splits);
         if (splits > 1 && L.nb < 4 * splits) break;
         for (int tile = 32; tile <= (splits > 1 ? kPartRows : kMostRows); tile += 32) {
             const int per = even_rows(load, tile);
             if (per != tile) continue;
             const int64_t tiles = (load + per - 1) / per, units = tiles * L.pairs * used, rounds = (units + clusters - 1) / clusters;
-            if (splits > 1 && rounds > 1) continue;
-            Shape s = with_ring(tile, splits, grouped ? most_units(L, used, rows, tile) : units, clusters);
+            const int64_t most = grouped ? most_units(L, used, rows, tile) : units;
+            if (splits > 1 && most > clusters) continue;   // (a cluster that splits K takes one unit)
+            Shape s = with_ring(tile, splits, most, clusters);
             if (s.stages < 4) continue;
             const double round = L.nb * block_of(per) + (per > kPartRows ? 14.0 * per : 0.0);
             double time = splits > 1 ? (L.nb + splits - 1) / splits * block_of(per) + 1500.0 + 14.0 * per : rounds * round + 14.0 * per;

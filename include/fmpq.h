@@ -669,7 +669,7 @@ FMPQ_API fmpq_status w16_gemm(const w16_layer* layer, const void* X, int64_t ldx
                               size_t workspace_bytes, void* stream);
 /* The rows of X [rows][ldx] in groups, one for each expert: expert e has rows offsets[e] .. offsets[e + 1] - 1 (int32
  * [experts + 1], on the device; cut to [0, rows]; a group that ends before it starts is empty, and a row that offsets which fall back
- * put into two groups gets the outputs of either). Rows of no group are left as they were in Y. row_weight: fp32 [rows] or NULL (1). */
+ * would put into two groups is the first's). Rows of no group are left as they were in Y. row_weight: fp32 [rows] or NULL (1). */
 FMPQ_API fmpq_status w16_grouped_gemm(const w16_layer* layer, const void* X, int64_t ldx, int64_t rows, const int32_t* offsets,
                                       const void* W_packed, const fmpq_epilogue* epilogue, const float* row_weight, void* Y,
                                       int32_t dtype, int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);

@@ -252,9 +252,38 @@ def test_group_bounds_are_cut_to_the_rows(fmpq_mod):  # noqa: F811
     offsets = torch.tensor([-5, 8, 4, 30, 2 ** 31 - 1], dtype=torch.int32, device="cuda")    # 0-7, none, 4-29, 30-39
     fmpq_mod.w16_grouped_gemm(layer, X, offsets, Wp, Y=Y)
     assert bool((buf[:10] == 7).all()) and bool((buf[-10:] == 7).all())
+    check(Y[:8], X[:8], W[0])        # rows 4-7 are the first group's
     check(Y[8:30], X[8:30], W[2])
     check(Y[30:], X[30:], W[3])
-    check(Y[:4], X[:4], W[0])
+    for bad in ([40, 0, 40, 0, 40], [0, 40, 0, 40, 0], [-1] * 5, [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1], [50] * 5):
+        Y.fill_(7)
+        fmpq_mod.w16_grouped_gemm(layer, X, torch.tensor(bad, dtype=torch.int32, device="cuda"), Wp, Y=Y)
+        assert bool((buf[:10] == 7).all()) and bool((buf[-10:] == 7).all())
+        group = next((e for e in range(4) if max(bad[e], 0) < min(bad[e + 1], 40)), None)
+        if group is None:
+            assert bool((Y == 7).all())
+        else:
+            check(Y, X, W[group])
+    assert fmpq_mod.w16_device_status(layer) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,E,K,N,gated", [(1, 65, 6400, 512, False), (3, 7, 4096, 300, True), (9, 2, 2048, 520, False)])
+def test_few_units_of_groups_split_K(fmpq_mod, rows, E, K, N, gated):  # noqa: F811
+    import torch
+    X, W = matrix(rows, K, torch.bfloat16, 1), torch.stack([matrix(N, K, torch.bfloat16, e, 0, K ** -0.5) for e in range(E)])
+    layer = fmpq_mod.W16Layer(K, N, torch.bfloat16, experts=E, gated=gated)
+    Wp = fmpq_mod.w16_pack_weights(layer, W)
+    g = torch.Generator().manual_seed(rows)
+    for turn in range(4):
+        cuts = torch.randint(0, rows + 1, (E - 1,), generator=g).sort().values
+        ends = torch.cat([torch.zeros(1), cuts, torch.full((1,), rows)]).int()
+        Y = fmpq_mod.w16_grouped_gemm(layer, X, ends.cuda(), Wp, activation="silu")
+        for e in range(E):
+            at = slice(int(ends[e]), int(ends[e + 1]))
+            if ends[e] < ends[e + 1]:
+                check(Y[at], X[at], W[e], "silu", gated=gated)
+    assert fmpq_mod.w16_device_status(layer) == 0
 
 
 @pytest.mark.gpu
