@@ -5,15 +5,17 @@
 //
 // FP32 sums on the tensor cores (tcgen05 kind::f16, FP32 accumulators in TMEM), one rounding. A pair of CTAs computes 256
 // packed weight rows (128 each, the tensor core's M side, 16 KB a block of 64 channels, laid out beforehand so that a block is
-// one bulk copy) x up to 256 rows of X (the N side, half of them from each CTA, TMA boxes with the 128-byte swizzle).
+// one bulk copy) x up to 512 rows of X (the N side, 256 an MMA, half of them from each CTA, TMA boxes with the 128-byte swizzle).
 // The N side takes any multiple of 32, so a group's rest costs MMAs only for its own rows, and few rows are the same
 // kernel with a narrower tile and more weight blocks in flight: for one row it streams weights, for many it is bound by
 // the tensor pipe.
-//   * A unit's whole K is summed in TMEM; two accumulators, so that a unit's epilogue runs under the next one's MMAs.
+//   * A unit's whole K is summed in TMEM; two accumulators, so that a unit's epilogue runs under the next one's MMAs (above 256 rows a
+//     unit takes both, and reads its weights once).
 //   * The epilogue turns 8 rows at a time through shared memory in FP32, so that a thread has 8 neighbouring outputs of a row:
 //     bias, activation, residual (16-byte loads, on their way before the sums are there) and one 16-byte store.
 //   * Units too few for the pairs: K is split over the pairs of a cluster; the others leave their sums in the first one's
-//     shared memory, which adds them in order, so results do not depend on timing.
+//     shared memory, which adds them in order, so results do not depend on timing. What a dense product's units leave over of full
+//     rounds has a launch of its own, cut finer and along K, under the first one's end.
 //
 // Warp roles (640 threads, one CTA per SM, pairs persistent over units):
 //   warp 0      producer of weight blocks and X boxes
@@ -857,9 +859,9 @@ int64_t most_units(const w16_layer& L, int used, int rows, int tile) {
 // the epilogue, which has no accumulator left to run beside: worth it where it saves a round (777 x 2048 -> 5632 in 320: 22) or where
 // an expert's load is a little above 256 (32768 rows of 128, 4096 -> 2048: 463 us in tiles of 256, 439 in 320).
 // Units that leave half the pairs idle split K: 1 x 8192 -> 8192 in 1, 2 and 4 parts 33.5, 25.2 and 25.4 us, 16 x 8192 -> 1024 33.2,
-// 20.1 and 13.3, 128 x 8192 -> 8192 35.6 and 31.4, one row of 65 experts, 6400 -> 512, 29.5 and 14.4 in 4; the exchange takes about 1500 clk. (The last round's blocks cut evenly over all pairs, their
-// sums in global memory and the last to arrive adding them: 31.6 in place of 25.2, 17.2 of 13.3, 64 units of a token's 8 experts 35.8 of 28.3,
-// and 2048 x 4096 -> 12288, 4 units in the last round, no faster.)
+// 20.1 and 13.3, 128 x 8192 -> 8192 35.6 and 31.4, one row of 65 experts, 6400 -> 512, 29.5 and 14.4 in 4; the exchange takes about 1500
+// clk. (The last round's blocks cut evenly over all pairs, their sums in global memory and the last to arrive adding them: 31.6 in place of 25.2, 17.2 of 13.3, 64
+// units of a token's 8 experts 35.8 of 28.3, and 2048 x 4096 -> 12288, 4 units in the last round, no faster.)
 Shape shape_of(const w16_layer& L, const W16Args& a) {
     const bool grouped = a.start != nullptr;
     const int rows = static_cast<int>(a.rows);
