@@ -16,6 +16,7 @@
 #include "fmpq_internal.h"
 #include "fp8_codes.cuh"
 #include "fp8_internal.h"
+#include "pieces.cuh"
 
 namespace fmpq {
 namespace {
@@ -64,30 +65,13 @@ __device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float
 __device__ __forceinline__ float& at(V8& v, int c) { return (c & 1) ? v[c >> 1].y : v[c >> 1].x; }
 __device__ __forceinline__ float at(const V8& v, int c) { return (c & 1) ? v[c >> 1].y : v[c >> 1].x; }
 
-// Eight elements that begin `off` (1 to 7) elements behind a 16-byte boundary, from the two pieces of 16 bytes that hold them.
-__device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, uint32_t off) {
-    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = (off & 4) ? w[i + 2] : w[i];
-#pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = (off & 2) ? w[i + 1] : w[i];
-    const uint32_t by = (off & 1) * 16;
-    return make_uint4(__funnelshift_r(w[0], w[1], by), __funnelshift_r(w[1], w[2], by), __funnelshift_r(w[2], w[3], by),
-                      __funnelshift_r(w[3], w[4], by));
-}
-// Of an address: the boundary before it, and the elements between.
-__device__ __forceinline__ uint32_t elements_past(const void* p) { return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u) >> 1; }
-
-// Channels k .. k + 7 of a row, those past K as 0 (kWhole: k < K). kAny reads whole pieces of 16 bytes, which hold one of the row's
-// elements at least, so they lie in its allocation.
+// Channels k .. k + 7 of a row, those past K as 0 (kWhole: k < K).
 template <typename T, int kLie>
 __device__ __forceinline__ void load8(const T* row, int k, int K, V8& v) {
     if (kLie == kWhole || (kLie == kMixed && k + 8 <= K)) {
         unpack8<T>(*reinterpret_cast<const uint4*>(row + k), v);
     } else if (kLie == kAny && k + 8 <= K) {
-        const uint32_t off = elements_past(row);
-        const uint4* at = reinterpret_cast<const uint4*>(row + k - off);
-        unpack8<T>(off == 0 ? at[0] : shifted(at[0], at[1], off), v);
+        unpack8<T>(eight_at(row, k), v);
     } else {
 #pragma unroll
         for (int c = 0; c < 8; ++c) at(v, c) = k + c < K ? load_as_float(row + k + c) : 0.0f;

@@ -30,6 +30,7 @@
 #include "epilogue.cuh"
 #include "fmpq_device.cuh"
 #include "fmpq_internal.h"
+#include "pieces.cuh"
 #include "w16_internal.h"
 
 namespace fmpq {
@@ -743,8 +744,8 @@ __global__ void __launch_bounds__(256) rows_kernel(const uint16_t* __restrict__ 
         const int k = static_cast<int>(c) * 8;
         const uint16_t* from = X + m * ldx + k;
         uint4 v;
-        if (kVec && k + 8 <= K) {
-            v = *reinterpret_cast<const uint4*>(from);
+        if (k + 8 <= K) {
+            v = kVec ? *reinterpret_cast<const uint4*>(from) : eight_at(from, 0);
         } else {
             uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
