@@ -25,8 +25,8 @@ namespace {
 using V8 = float2[4];
 
 // How the vectors of a kernel lie: kWhole: K is a multiple of 8 and weights and outputs are on 16-byte boundaries, so every vector
-// below K is a 16-byte access; kMixed: a row's last vector may be partial; kAny: any alignment of the elements (4481 x 4291, X 2 bytes off:
-// 90 us, by single elements 119; 777 x 2868, rows on 8-byte boundaries: 10.2, 17).
+// below K is a 16-byte access; kMixed: a row's last vector may be partial; kAny: any alignment of the elements (one CTA a row, 4481 x 4291, X 2
+// bytes off: 90 us, by single elements 119; 777 x 2868, rows on 8-byte boundaries: 10.2, 17).
 enum { kWhole = 0, kMixed = 1, kAny = 2 };
 // Which norm: known to the compiler, or a branch.
 enum { kRms = 0, kLayer = 1, kEither = 2 };
@@ -356,15 +356,20 @@ __global__ void __launch_bounds__(1024) block_norm_long_kernel(const BlockNormAr
     }
 }
 
-// Many rows, weights and outputs on 16-byte boundaries, X and residual anywhere (2325 x 2816 fp16, rows of X and residual 2 bytes off, both
-// norms: 13.6 us, 36 as one CTA a row by single elements): the CTAs stay, and the next rows are on their way into a ring in shared memory (bulk
-// copies) while one is worked on. Two vectors a thread (four where 1024 threads would not do). Its instructions and the chain of a row
-// through its barriers bound it (4096 x 8192 bf16, both norms, a gate, codes: 64 us, 236 MB = 3.7 TB/s, an issue slot used in 63 of 100; one
-// norm and the residual 43; the sum alone 30, the copy rate), so what can be is uniform or made once: a row's addresses are a base for the
-// CTA and 32-bit offsets of a thread, arithmetic is on pairs, P (the weights' type) and the norm are the compiler's. One CTA a row
-// without the ring took 138. No faster: four vectors a thread (70), three CTAs of 40 registers in place of two, the weights in shared
-// memory (which leave the ring two rows) or asked for before the sums, all within 1 us; without the codes' stores, the scales' or the
-// reduction of a block's maximum it would still take within 1 us of this.
+// Bytes that a row of K channels takes in the ring, wherever it starts.
+__host__ __device__ inline uint32_t ring_row_bytes(int K) { return ((static_cast<uint32_t>(K) + 7) / 8 * 8 + 8) * 2; }
+
+// Many rows: the CTAs stay, and the next rows are on their way into a ring in shared memory (bulk copies) while one is worked on. Two vectors
+// a thread (three, or four, where 1024 threads would not do: 2048 x 24576 85 us with three, 102 with four). Its instructions and the chain of a row through its barriers bound it (4096 x 8192 bf16,
+// both norms, a gate, codes: 64 us, 236 MB = 3.7 TB/s, an issue slot used in 63 of 100; one norm and the residual 43; the sum alone 30, the
+// copy rate), so what can be is uniform or made once: a row's addresses are a base for the CTA and 32-bit offsets of a thread, arithmetic is
+// on pairs, P (the weights' type) and the norm are the compiler's. One CTA a row without the ring took 138. No faster: four vectors a thread
+// (70), three CTAs of 40 registers in place of two, the weights in shared memory (which leave the ring two rows) or asked for before the sums,
+// all within 1 us; without the codes' stores, the scales' or the reduction of a block's maximum it would still take within 1 us of this.
+// X and residual lie anywhere: the copies begin on the boundary before a row, and vectors are shifted out of the ring (2325 x 2816 fp16, rows
+// 2 bytes off, both norms: 13.6 us, 36 as one CTA a row by single elements). Weights and outputs lie on 16-byte boundaries (kWhole) or K and
+// they are anything (kAny: 7572 x 5913 bf16, rows 2 bytes off, both norms, codes: 117 us, 250 as one CTA a row; its shifts and narrow stores
+// are instructions more; a warp that shuffles its lanes' values into whole pieces for the stores takes 127).
 template <typename P>
 __device__ __forceinline__ void param_at(const void* p, uint32_t k, V8& v) {
     if constexpr (sizeof(P) == 2) {
@@ -376,19 +381,20 @@ __device__ __forceinline__ void param_at(const void* p, uint32_t k, V8& v) {
     }
 }
 
-template <typename T, typename P, int kNorm, int kV>
+template <typename T, typename P, int kNorm, int kV, int kLie>
 __global__ void __launch_bounds__(1024) block_norm_stream_kernel(const BlockNormArgs p, int stages) {
     extern __shared__ __align__(128) uint8_t ring[];   // [stage][X's row, then the residual's]
     __shared__ Sums sums;
     __shared__ uint64_t landed[kMostStages];
-    // (a row of a slot has room for the piece of 16 bytes more that one not on a boundary takes)
-    const uint32_t row_bytes = static_cast<uint32_t>(p.K) * 2 + 16, slot_bytes = p.residual != nullptr ? 2 * row_bytes : row_bytes;
+    // (a row of a slot has room for a row at any place in its pieces, and for the piece behind its last vector's)
+    const uint32_t row_bytes = ring_row_bytes(p.K), slot_bytes = p.residual != nullptr ? 2 * row_bytes : row_bytes;
     const int rows = static_cast<int>(p.M), step = static_cast<int>(gridDim.x);
     auto load = [&](int m, int stage) {
         const T* x = static_cast<const T*>(p.X) + m * p.ldx;
         const T* r = static_cast<const T*>(p.residual) + m * p.ldr;
         const uint32_t x_off = elements_past(x), r_off = elements_past(r);
-        const uint32_t x_bytes = row_bytes - (x_off == 0 ? 16u : 0u), r_bytes = p.residual != nullptr ? row_bytes - (r_off == 0 ? 16u : 0u) : 0u;
+        auto pieces = [&](uint32_t off) { return ((off + static_cast<uint32_t>(p.K)) * 2 + 15u) & ~15u; };
+        const uint32_t x_bytes = pieces(x_off), r_bytes = p.residual != nullptr ? pieces(r_off) : 0u;
         dev::mbar_arrive_expect_tx(&landed[stage], x_bytes + r_bytes);
         dev::bulk_g2s(ring + stage * slot_bytes, x - x_off, x_bytes, &landed[stage]);
         if (p.residual != nullptr) dev::bulk_g2s(ring + stage * slot_bytes + row_bytes, r - r_off, r_bytes, &landed[stage]);
@@ -423,10 +429,22 @@ __global__ void __launch_bounds__(1024) block_norm_stream_kernel(const BlockNorm
         // (a copy that this CTA issued lands; should one not, within about a second, its row comes out NaN)
         const bool there = dev::mbar_wait(&landed[stage], phase, nullptr);
         const uint8_t* x = ring + stage * slot_bytes;
+        // what a row's last vector has past K (kAny) is 0
+        auto cut = [&](uint32_t k, V8& v) {
+            if (kLie == kAny && k + 8 > static_cast<uint32_t>(p.K))
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    if (k + c >= static_cast<uint32_t>(p.K)) at(v, c) = 0.0f;
+        };
         // a vector of a row in the ring, which begins `off` elements into it
         auto from_ring = [&](const uint8_t* row, uint32_t off, uint32_t k, V8& v) {
             const uint4* at = reinterpret_cast<const uint4*>(row + k * 2u);
             unpack8<T>(off == 0 ? at[0] : shifted(at[0], at[1], off), v);
+            cut(k, v);
+        };
+        auto param = [&](const void* w, uint32_t k, V8& t) {
+            if constexpr (kLie == kAny) param8<T, kAny>(w, p.param_f32, 0, static_cast<int>(k), p.K, t);
+            else param_at<P>(w, k, t);
         };
         V8 v[kV];
 #pragma unroll
@@ -445,7 +463,7 @@ __global__ void __launch_bounds__(1024) block_norm_stream_kernel(const BlockNorm
 #pragma unroll
                     for (int c = 0; c < 4; ++c) v[i][c] = fadd2(v[i][c], both(-mean));
                 if (w != nullptr && in[i]) {
-                    param_at<P>(w, k[i], t);
+                    param(w, k[i], t);
                     if (p.weight_offset != 0.0f)
 #pragma unroll
                         for (int c = 0; c < 4; ++c) t[c] = fadd2(t[c], both(p.weight_offset));
@@ -456,17 +474,18 @@ __global__ void __launch_bounds__(1024) block_norm_stream_kernel(const BlockNorm
                     for (int c = 0; c < 4; ++c) v[i][c] = dev::fmul2(v[i][c], both(inv));
                 }
                 if (b != nullptr && in[i]) {
-                    param_at<P>(b, k[i], t);
+                    param(b, k[i], t);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) v[i][c] = fadd2(v[i][c], t[c]);
                 }
                 if (kNorm == kLayer && !in[i])
 #pragma unroll
                     for (int c = 0; c < 4; ++c) v[i][c] = both(0.0f);
+                if (in[i]) cut(k[i], v[i]);   // (its value of 0 is not 0)
             }
         };
         if (p.post_norm) {
-            statistics<kWhole, kNorm>(p, v, sums, turn, mean, inv);
+            statistics<kLie, kNorm>(p, v, sums, turn, mean, inv);
             scale(p.post_weight, p.post_bias);
         }
         if (p.gate != nullptr) {
@@ -475,7 +494,8 @@ __global__ void __launch_bounds__(1024) block_norm_stream_kernel(const BlockNorm
             for (int i = 0; i < kV; ++i) {
                 if (!in[i]) continue;
                 V8 t;
-                if (p.gate_f32) param_at<float>(static_cast<const float*>(p.gate) + gate_row, k[i], t);
+                if constexpr (kLie == kAny) param8<T, kAny>(p.gate, p.gate_f32, gate_row, static_cast<int>(k[i]), p.K, t);
+                else if (p.gate_f32) param_at<float>(static_cast<const float*>(p.gate) + gate_row, k[i], t);
                 else param_at<T>(static_cast<const T*>(p.gate) + gate_row, k[i], t);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) v[i][c] = dev::fmul2(v[i][c], t[c]);
@@ -495,9 +515,9 @@ __global__ void __launch_bounds__(1024) block_norm_stream_kernel(const BlockNorm
             uint8_t* row = static_cast<uint8_t*>(p.R) + m * p.ldo * 2;
 #pragma unroll
             for (int i = 0; i < kV; ++i)
-                if (in[i]) store8<T, kWhole>(reinterpret_cast<T*>(row + k[i] * 2u), 0, p.K, v[i]);
+                if (in[i]) store8<T, kLie>(reinterpret_cast<T*>(row), static_cast<int>(k[i]), p.K, v[i]);
         }
-        if (p.pre_norm) statistics<kWhole, kNorm>(p, v, sums, turn, mean, inv);
+        if (p.pre_norm) statistics<kLie, kNorm>(p, v, sums, turn, mean, inv);
         if (!p.pre_norm || single) __syncthreads();   // (else the statistics' own barrier)
         // every thread has read the row
         if (threadIdx.x == 0 && m + static_cast<int64_t>(stages) * step < rows) load(m + stages * step, stage);
@@ -511,7 +531,7 @@ __global__ void __launch_bounds__(1024) block_norm_stream_kernel(const BlockNorm
             uint8_t* row = static_cast<uint8_t*>(p.Y) + m * p.ldy * 2;
 #pragma unroll
             for (int i = 0; i < kV; ++i)
-                if (in[i]) store8<T, kWhole>(reinterpret_cast<T*>(row + k[i] * 2u), 0, p.K, v[i]);
+                if (in[i]) store8<T, kLie>(reinterpret_cast<T*>(row), static_cast<int>(k[i]), p.K, v[i]);
         }
         if (p.A != nullptr) {
             uint8_t* codes = p.A + static_cast<int64_t>(m) * 128;
@@ -534,28 +554,34 @@ int threads_for(int nb, int per) { return ((nb * 16 + per - 1) / per + 31) / 32 
 
 constexpr int kRingBytes = 225 * 1024;
 
-// Whether a CTA's ring holds two rows; and the kernel over it.
-bool fits_stream(const BlockNormArgs& p) {
-    return p.K % 8 == 0 && p.K >= 512 && threads_for(p.nb, 4) <= 1024 && 2 * (p.K * 2 + 16) * (p.residual != nullptr ? 2 : 1) <= kRingBytes &&
-           p.M * p.nb * 128 < INT64_C(1) << 32;   // (32-bit offsets of the codes)
+// Whether the rows are long enough and a CTA's ring holds two; and the kernel over it. (not `whole`, against one CTA a row: 4096 x 1501 bf16 21.0
+// us to 19.6, 4096 x 2001 23.1 to 25.2, 4481 x 4291 49 to 100)
+bool fits_stream(const BlockNormArgs& p, bool whole) {
+    const int slot = static_cast<int>(ring_row_bytes(p.K)) * (p.residual != nullptr ? 2 : 1);
+    return p.K >= (whole ? 512 : 1792) && threads_for(p.nb, 4) <= 1024 && 2 * slot <= kRingBytes && p.M * p.nb * 128 < INT64_C(1) << 32;   // (32-bit offsets of the codes)
 }
 template <typename T>
-cudaError_t block_norm_stream(const BlockNormArgs& p, int num_sms, cudaStream_t stream) {
+cudaError_t block_norm_stream(const BlockNormArgs& p, bool whole, int num_sms, cudaStream_t stream) {
     using std::integral_constant;
-    const int per = threads_for(p.nb, 2) <= 1024 ? 2 : 4, threads = threads_for(p.nb, per);
+    const int per = threads_for(p.nb, 2) <= 1024 ? 2 : threads_for(p.nb, 3) <= 1024 ? 3 : 4, threads = threads_for(p.nb, per);
     auto of = [&](auto norm, auto v) {
-        return p.param_f32 ? block_norm_stream_kernel<T, float, norm.value, v.value> : block_norm_stream_kernel<T, T, norm.value, v.value>;
+        if (!whole) return block_norm_stream_kernel<T, T, norm.value, v.value, kAny>;
+        return p.param_f32 ? block_norm_stream_kernel<T, float, norm.value, v.value, kWhole> : block_norm_stream_kernel<T, T, norm.value, v.value, kWhole>;
     };
-    auto fn = per == 2 ? (p.layer_norm ? of(integral_constant<int, kLayer>{}, integral_constant<int, 2>{})
-                                       : of(integral_constant<int, kRms>{}, integral_constant<int, 2>{}))
-                       : (p.layer_norm ? of(integral_constant<int, kLayer>{}, integral_constant<int, 4>{})
-                                       : of(integral_constant<int, kRms>{}, integral_constant<int, 4>{}));
-    const int slot = (p.K * 2 + 16) * (p.residual != nullptr ? 2 : 1);
-    int resident = 1024 / threads;   // (64 registers a thread)
+    auto at = [&](auto norm) {
+        return per == 2 ? of(norm, integral_constant<int, 2>{}) : per == 3 ? of(norm, integral_constant<int, 3>{}) : of(norm, integral_constant<int, 4>{});
+    };
+    auto fn = p.layer_norm ? at(integral_constant<int, kLayer>{}) : at(integral_constant<int, kRms>{});
+    const int slot = static_cast<int>(ring_row_bytes(p.K)) * (p.residual != nullptr ? 2 : 1);
+    // CTAs an SM by its registers (4096 x 8960: 55 us, at 64 registers a thread for every kernel 78; 4481 x 4291: 49, 66)
+    cudaFuncAttributes a;
+    cudaError_t e = cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(fn));
+    if (e != cudaSuccess) return e;
+    int resident = 65536 / (((a.numRegs + 7) & ~7) * threads);
     if (resident > 16) resident = 16;
     int stages = 200 * 1024 / resident / slot;
     stages = stages > kMostStages ? kMostStages : stages < 2 ? 2 : stages;
-    const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), kRingBytes);
+    e = ensure_smem_limit(reinterpret_cast<const void*>(fn), kRingBytes);
     if (e != cudaSuccess) return e;
     const int64_t ctas = static_cast<int64_t>(num_sms) * resident;
     return launch_after(fn, dim3(static_cast<unsigned>(p.M < ctas ? p.M : ctas)), threads, stages * slot, true, stream, p, stages);
@@ -586,7 +612,8 @@ cudaError_t block_norm_of(const BlockNormArgs& p, int num_sms, cudaStream_t stre
     for (int64_t ld : {p.ldo, p.ldy}) out |= static_cast<uintptr_t>(ld) * 2;
     out |= static_cast<uintptr_t>(p.ldg) * (p.gate_f32 ? 4 : 2);
     const bool few = p.M < 2 * num_sms;
-    if (!few && (out & 15u) == 0 && fits_stream(p)) return block_norm_stream<T>(p, num_sms, stream);
+    const bool whole = p.K % 8 == 0 && (out & 15u) == 0;
+    if (!few && fits_stream(p, whole)) return block_norm_stream<T>(p, whole, num_sms, stream);
     return ((in | out) & 15u) == 0 ? block_norm_rows<T, kMixed>(p, few, num_sms, stream) : block_norm_rows<T, kAny>(p, few, num_sms, stream);
 }
 

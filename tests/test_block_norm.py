@@ -103,7 +103,7 @@ def vectors(K, dtype, seed, n=4):
 SIZES = [(1, 8192, 0), (1, 1, 0), (3, 5, 1), (2, 127, 1), (5, 128, 0), (7, 129, 8), (400, 64, 0), (310, 250, 0), (33, 4096, 8),
          (350, 1024, 1), (320, 2868, 4), (305, 8192, 0), (305, 12000, 0), (2, 20000, 0), (3, 16385, 1), (1, 65536, 0),
          (1000, 512, 0), (5000, 520, 8), (700, 1000, 0), (2500, 2048, 0), (400, 16384, 0), (310, 28672, 0),
-         (306, 20008, 8)]
+         (306, 20008, 8), (400, 5913, 1), (310, 21703, 3), (1300, 771, 0), (600, 513, 5)]
 
 
 @pytest.mark.gpu
@@ -189,7 +189,7 @@ def test_any_alignment_gives_the_same(fmpq_mod, M, K):  # noqa: F811
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M,K", [(1, 512), (333, 1024), (2, 17000)])
+@pytest.mark.parametrize("M,K", [(1, 512), (333, 1024), (2, 17000), (700, 1003)])
 def test_in_place(fmpq_mod, M, K):  # noqa: F811
     """R in the residual's buffer and Y in X's, or R in X's: the same values as in buffers of their own."""
     import torch
