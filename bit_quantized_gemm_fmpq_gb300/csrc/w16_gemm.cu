@@ -44,7 +44,7 @@ constexpr int kMaxStages = 12;
 constexpr int kPartRows = 256;    // of a part: the N side of an MMA, and an accumulator's columns
 constexpr int kMostRows = 512;    // of a unit: two parts
 constexpr int kChunk = 8;         // rows of X that a group turns at a time
-constexpr int kStageLd = 132;     // floats of a row there: 128 outputs, and a skew of 16 bytes
+constexpr int kStageLd = 136;     // floats of a row there: 128 outputs, and up to 7 in front of them
 constexpr int kBandTiles = 8;     // dense order: bands of 8 row tiles, weight tiles inside a band
 constexpr int kMaxSplits = 4;
 constexpr int kBigBox = 64, kSmallBox = 16;   // rows of the two TMA boxes
@@ -470,11 +470,151 @@ __device__ __forceinline__ int other_sums(const Params& p, int split, int chunk,
     return ((split - 1) * (p.tile / kChunk) + chunk) * (kChunk / 4) * 128 + row;
 }
 
+// Of outputs of 16 bits that rows may hold anywhere (gated: on 8-byte boundaries): where a thread's piece of a row lies. A CTA's row of
+// kCols columns begins `past` elements behind a boundary, and a piece is kW elements between two boundaries; the first thread's is the row's
+// two ends: its last `past` columns and its first kW - past. (Rows kW apart begin at the same place of their pieces, so it is the same in each chunk.)
+template <int kW, int kCols>
+struct Piece {
+    int first, columns;   // the column of its first element (negative: the row's last ones), how many columns there are
+    bool whole;           // all of it exists, in a row
+
+    __device__ __forceinline__ Piece(int i, int past, int columns) : first(kW * i - past), columns(columns), whole(first >= 0 && first + kW <= columns) {}
+    __device__ __forceinline__ int column(int c) const { return first + c < 0 ? first + c + kCols : first + c; }
+    __device__ __forceinline__ bool has(int c) const { return column(c) < columns; }
+};
+// Elements between the 16-byte boundary before a row's outputs and them.
+template <bool kGated>
+__device__ __forceinline__ int row_past(const Params& p, int64_t row) {
+    return kGated ? 0 : static_cast<int>(elements_past(static_cast<const uint16_t*>(p.Y) + row * p.ldy));
+}
+
+// The epilogue's chunks of a part, where p.whole: outputs of 16 bits, K not split. The rows are shifted to their place in memory as they are
+// turned, and the residual of a thread's next row is on its way while it works on one (WHOLE).
+template <bool kGated, int kW, int kCols>
+__device__ __forceinline__ void put_out_whole(const Params& p, float (*turn)[kChunk][kStageLd], uint32_t from_tmem, int g, int tid, int64_t row0, int rows,
+                                              int n0, const Piece<kW, kCols>& piece, const float (&bias)[kW], const float (&bias_up)[kW],
+                                              bool ok, int& buffer) {
+    constexpr int kPieces = kCols / kW;
+    const int chunks = (rows + kChunk - 1) / kChunk, sub = tid / kPieces, i = tid % kPieces;
+    // of every 32 packed rows of a gated layer, 16 are gates and 16 the ups of the same hidden channels
+    const int place = kGated ? 32 * (kW * i >> 4) + (kW * i & 15) : kW * i;
+    int to[kChunk];
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) to[j] = j * kStageLd + tid + row_past<kGated>(p, row0 + j);
+    int64_t row = row0 + kChunk * g + sub;
+    uint16_t* y = static_cast<uint16_t*>(p.Y) + row * p.ldy + n0;
+    const uint16_t* r = static_cast<const uint16_t*>(p.e.residual) + row * p.e.ldr + n0;
+    const int64_t y_step = p.ldy * (kGroups * kChunk), r_step = p.e.ldr * (kGroups * kChunk);
+    int left = ok ? rows - kChunk * g - sub : 0;   // this thread's row of a chunk exists where more than 0 are left
+    uint32_t d[kChunk], raw[kW / 2];
+    // (whole pieces, which hold one of the piece's elements at least)
+    const bool head = max(piece.first, 0) < piece.columns, tail = piece.first < 0 && piece.first + kCols < piece.columns;
+    uint32_t ends[kW / 2];   // the row's last columns, for the first thread
+    auto ask = [&] {
+        if constexpr (kW == 8) {
+            if (head) {
+                const uint4 a = *reinterpret_cast<const uint4*>(r + piece.first);
+                raw[0] = a.x, raw[1] = a.y, raw[2] = a.z, raw[3] = a.w;
+            }
+            if (tail) {
+                const uint4 a = *reinterpret_cast<const uint4*>(r + piece.first + kCols);
+                ends[0] = a.x, ends[1] = a.y, ends[2] = a.z, ends[3] = a.w;
+            }
+        } else if (head) {
+            const uint2 a = *reinterpret_cast<const uint2*>(r + piece.first);
+            raw[0] = a.x, raw[1] = a.y;
+        }
+    };
+    const bool bf16 = p.bf16 != 0, biased = p.e.bias != nullptr, added = p.e.residual != nullptr;
+    dev::tmem_ld8(from_tmem + kChunk * min(g, chunks - 1), d);
+    if (added && left > 0) ask();
+#pragma unroll 1
+    for (int c = g; c < chunks; c += kGroups) {
+        float* here = &turn[buffer][0][0];
+        buffer ^= 1;
+        dev::tmem_ld_wait8(d);
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j) here[to[j]] = __uint_as_float(d[j]);
+        // (whoever writes this buffer again has passed the next barrier, behind which the others have read it)
+        dev::named_bar_sync(2 + g, 128);
+        dev::tmem_ld8(from_tmem + kChunk * min(c + kGroups, chunks - 1), d);
+        r += r_step;
+        if (left > 0) {
+            const float* from = here + sub * kStageLd + place;
+            float f[kW];
+#pragma unroll
+            for (int i = 0; i < kW; i += 4) *reinterpret_cast<float4*>(&f[i]) = *reinterpret_cast<const float4*>(from + i);
+            if (!kGated && piece.first < 0) {
+                float e[kW];
+#pragma unroll
+                for (int i = 0; i < kW; i += 4) *reinterpret_cast<float4*>(&e[i]) = *reinterpret_cast<const float4*>(from + kCols + i);
+#pragma unroll
+                for (int c = 0; c < kW; ++c) f[c] = piece.first + c < 0 ? e[c] : f[c];
+            }
+            if (biased)
+#pragma unroll
+                for (int i = 0; i < kW; ++i) f[i] += bias[i];
+            activate_piece(p.e.act, f);
+            if constexpr (kGated) {
+                const float4 v = *reinterpret_cast<const float4*>(from + 16);
+                const float up[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < kW; ++i) f[i] *= biased ? up[i] + bias_up[i] : up[i];
+            }
+            if (p.row_weight != nullptr) {
+                const float w = weight_of(p, row);
+#pragma unroll
+                for (int i = 0; i < kW; ++i) f[i] *= w;
+            }
+            if (added) {
+#pragma unroll
+                for (int i = 0; i < kW / 2; ++i) {
+                    float2 a = epi::values16(raw[i], bf16);
+                    if (!kGated && piece.first < 0) {
+                        const float2 e = epi::values16(ends[i], bf16);
+                        a = make_float2(piece.first + 2 * i < 0 ? e.x : a.x, piece.first + 2 * i + 1 < 0 ? e.y : a.y);
+                    }
+                    f[2 * i] += a.x;
+                    f[2 * i + 1] += a.y;
+                }
+                if (left > kGroups * kChunk) ask();
+            }
+            uint32_t o[kW / 2];
+#pragma unroll
+            for (int i = 0; i < kW / 2; ++i) {
+                if (bf16) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+                    o[i] = *reinterpret_cast<const uint32_t*>(&h);
+                } else {
+                    const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+                    o[i] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+            }
+            if (!kGated && piece.first == -4 && piece.columns == kCols) {
+                *reinterpret_cast<uint2*>(y) = make_uint2(o[kW / 2 - 2], o[kW / 2 - 1]);
+                *reinterpret_cast<uint2*>(y + kCols - 4) = make_uint2(o[0], o[1]);
+            } else if (!piece.whole) {
+#pragma unroll
+                for (int c = 0; c < kW; ++c)
+                    if (piece.has(c)) y[piece.column(c)] = static_cast<uint16_t>(o[c >> 1] >> (16 * (c & 1)));
+            } else if constexpr (kW == 8) {
+                *reinterpret_cast<uint4*>(y + piece.first) = make_uint4(o[0], o[1], o[2], o[3]);
+            } else {
+                *reinterpret_cast<uint2*>(y + piece.first) = make_uint2(o[0], o[1]);
+            }
+        }
+        y += y_step;
+        row += kGroups * kChunk;
+        left -= kGroups * kChunk;
+    }
+    dev::tmem_ld_wait8(d);   // (the last one's is of no use)
+}
+
 // A thread's sums, a chunk's 8 rows for one packed weight row, go through shared memory; then it has one piece of neighbouring
 // columns of one row: 8, or gate and up of 4 hidden channels. Where rows of Y or of the residual do not start on 8-byte boundaries
 // (FP32: 16) a thread has one column instead, of all 8 rows (gated: of 4), so that a warp's accesses are still neighbours. A chunk's
 // sums leave TMEM while the chunk before is put out.
-template <bool kGated>
+template <bool kGated, bool kWhole>
 __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* others, const Place& at, int warp, int lane, uint32_t tmem,
                                          volatile int* abort_flag) {
     constexpr int kCols = kGated ? 64 : 128;              // of this CTA
@@ -489,10 +629,10 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* other
     const int place = kGated ? 32 * (col >> 4) + (col & 15) : col;
     const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const uint32_t leader_free = dev::mapa(&s.acc_free[0], at.leader);
-    const bool first = at.split == 0;
+    const bool first = kWhole || at.split == 0;
     uint32_t np = 0;   // parts so far
     bool ok = true;
-    int part = 0;
+    int part = 0, buffer = 0;   // (of turn: which a chunk writes)
     for (int u = at.cluster; u < units; ++np) {
         const Unit whole = unit_of(p, s, u, at.split);
         if (whole.rows == 0) {
@@ -508,11 +648,19 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* other
             u += at.clusters;
         }
         const uint32_t acc = np & 1;
-        const int n = (2 * t.pair + static_cast<int>(at.rank)) * kCols + col;
+        const int n0 = (2 * t.pair + static_cast<int>(at.rank)) * kCols, n = n0 + col;
         const int columns = p.out_n - n;
+        const Piece<kW, kCols> piece(tid % kPieces, kWhole ? row_past<kGated>(p, t.row0 + tid / kPieces) : 0, min(kCols, p.out_n - n0));
         const int chunks = (t.rows + kChunk - 1) / kChunk;
         float bias[kW], bias_up[kW];
-        if (first && p.e.bias != nullptr) {
+        if (kWhole && p.e.bias != nullptr) {
+#pragma unroll
+            for (int c = 0; c < kW; ++c) {
+                const int64_t b = static_cast<int64_t>(t.e) * p.N + n0 + piece.column(c);
+                bias[c] = piece.has(c) ? epi::bias_at(p.e, b, p.bf16 != 0) : 0.0f;
+                if (kGated) bias_up[c] = piece.has(c) ? epi::bias_at(p.e, b + p.out_n, p.bf16 != 0) : 0.0f;
+            }
+        } else if (first && p.e.bias != nullptr) {
             load_bias(p, static_cast<int64_t>(t.e) * p.N + n, pieces ? columns : min(columns, 1), bias);
             if constexpr (kGated) load_bias(p, static_cast<int64_t>(t.e) * p.N + p.out_n + n, pieces ? columns : min(columns, 1), bias_up);
         }
@@ -526,11 +674,13 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* other
         }
         ok = ok && dev::mbar_wait(&s.acc_full[acc], (np >> 1) & 1, abort_flag);
         ok = __all_sync(0xFFFFFFFFu, ok);
-        if (first && p.splits > 1 && ok) ok = __all_sync(0xFFFFFFFFu, dev::mbar_wait_cluster(&s.split_full, 0));
+        if (!kWhole && first && p.splits > 1 && ok) ok = __all_sync(0xFFFFFFFFu, dev::mbar_wait_cluster(&s.split_full, 0));
         dev::tc_fence_after();
         const uint32_t from_tmem = base + acc * kPartRows;
 
-        if (!first) {   // to the first pair's CTA of this rank
+        if constexpr (kWhole) {
+            put_out_whole<kGated>(p, s.turn[g], from_tmem, g, tid, t.row0, t.rows, n0, piece, bias, bias_up, ok, buffer);
+        } else if (!first) {   // to the first pair's CTA of this rank
             const uint32_t to = dev::mapa(others, at.rank) + other_sums(p, at.split, 0, tid) * 16u;
             for (int c = g; c < chunks; c += kGroups) {
                 uint32_t d[kChunk];
@@ -595,7 +745,6 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* other
                     store1(p, row0 + j, n, f[i]);
                 }
             };
-            int buffer = 0;
             for (int c = g; c < chunks + kGroups; c += kGroups) {
                 uint32_t d[kChunk];
                 const int here = min(c, chunks - 1);   // (the last turn only puts out: its load is of no use, and not behind a branch)
@@ -632,7 +781,7 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* other
     if (!ok && lane == 0) fail(p, abort_flag);
 }
 
-template <bool kGated>
+template <bool kGated, bool kWhole>
 __global__ void __launch_bounds__(kThreads, 1)
 w16_kernel(const Params p, const __grid_constant__ CUtensorMap big, const __grid_constant__ CUtensorMap small) {
     extern __shared__ uint8_t smem_raw[];
@@ -688,7 +837,7 @@ w16_kernel(const Params p, const __grid_constant__ CUtensorMap big, const __grid
     } else if (warp == 1) {
         mma_issuer(p, s, ring, at, tmem, abort_flag);
     } else if (warp >= 4) {
-        epilogue<kGated>(p, s, others, at, warp, lane, tmem, abort_flag);
+        epilogue<kGated, kWhole>(p, s, others, at, warp, lane, tmem, abort_flag);
     }
     __syncwarp();
     dev::tc_fence_before();
@@ -802,8 +951,8 @@ int resident_clusters(const w16_layer& L, int splits) {
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = config(most * 2 * splits, 2 * splits, kSmemBytes, nullptr, attr);
     int got = 0;
-    if (ensure_smem_limit(reinterpret_cast<const void*>(w16_kernel<false>), kSmemBytes) == cudaSuccess &&
-        cudaOccupancyMaxActiveClusters(&got, w16_kernel<false>, &cfg) == cudaSuccess && got > 0 && got < most)
+    if (ensure_smem_limit(reinterpret_cast<const void*>(w16_kernel<false, false>), kSmemBytes) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&got, w16_kernel<false, false>, &cfg) == cudaSuccess && got > 0 && got < most)
         most = got;
     cudaGetLastError();   // a failed query leaves no error behind
     if (known) cached[L.device][splits] = most;
@@ -931,12 +1080,18 @@ cudaError_t launch_w16_gemm(const w16_layer& L, const W16Args& a, cudaStream_t s
     p.status = L.d_status;
     CUtensorMap big, small;
     if (!w16::encode_rows(&big, a, L, w16::kBigBox) || !w16::encode_rows(&small, a, L, w16::kSmallBox)) return cudaErrorInvalidValue;
-    auto fn = L.gated ? w16::w16_kernel<true> : w16::w16_kernel<false>;
-    const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), w16::kSmemBytes);
-    if (e != cudaSuccess) return e;
     auto launch = [&](const w16::Shape& s) {
         p.tile = s.tile;
         p.splits = s.splits;
+        // (a residual's rows begin at the same place of their 16 bytes as the outputs')
+        const bool whole = !p.f32 && s.splits == 1 &&
+                  (L.gated ? p.vec >= 4
+                           : p.e.residual == nullptr ||
+                                 (((reinterpret_cast<uintptr_t>(a.Y) ^ reinterpret_cast<uintptr_t>(p.e.residual)) & 15u) == 0 && (p.ldy - p.e.ldr) % 8 == 0));
+        auto fn = L.gated ? (whole ? w16::w16_kernel<true, true> : w16::w16_kernel<true, false>)
+                          : (whole ? w16::w16_kernel<false, true> : w16::w16_kernel<false, false>);
+        const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), w16::kSmemBytes);
+        if (e != cudaSuccess) return e;
         p.stages = s.stages;
         p.stage_bytes = s.stage_bytes;
         cudaLaunchAttribute attr[2];
