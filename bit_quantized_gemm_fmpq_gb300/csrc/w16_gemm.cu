@@ -64,6 +64,7 @@ struct Params {
     int nb, pairs, experts, splits;
     int tile;            // rows of a unit, at most: a multiple of 32
     int cut, cuts;       // rows of the units that a dense product's rows are cut into, and units of this launch in one of them
+    int tiles;           // those units, for a pair of weight tiles
     int first_cut;       // this launch's first
     int last_launch;     // the rest of a product, behind the launch of its full rounds
     int units;           // dense: of this launch
@@ -73,6 +74,7 @@ struct Params {
 
 struct Tables {
     int32_t first_unit[kMaxFp8Experts + 1], start[kMaxFp8Experts], count[kMaxFp8Experts];
+    uint16_t per[kMaxFp8Experts];   // rows of its units
 };
 
 struct __align__(1024) Smem {
@@ -107,9 +109,7 @@ __host__ __device__ inline int even_rows(int count, int tile) {
     const int tiles = (count + tile - 1) / tile;
     return tiles == 0 ? tile : ((count + tiles - 1) / tiles + 31) / 32 * 32;
 }
-__device__ __forceinline__ int tiles_of(const Params& p, int count) {
-    return count > 0 ? (count + even_rows(count, p.tile) - 1) / even_rows(count, p.tile) : 0;
-}
+__host__ __device__ inline int tiles_of(int count, int per) { return (count + per - 1) / per; }
 
 // Every thread calls it; a barrier must follow. Group bounds outside [0, rows] are cut to it, and a group begins no earlier than those
 // before it end: no row is in two, so there are never more units than the host counts with.
@@ -140,7 +140,10 @@ __device__ __forceinline__ void fill_tables(const Params& p, Tables& s, int warp
         s.start[e] += cut;
         s.count[e] -= cut;
         if (s.count[e] > 0) last = max(last, s.start[e] + s.count[e]);
-        sum += tiles_of(p, s.count[e]) * p.pairs;
+        s.per[e] = static_cast<uint16_t>(even_rows(s.count[e], p.tile));
+        const int units = tiles_of(s.count[e], s.per[e]) * p.pairs;
+        s.first_unit[e] = sum;   // (of this lane's)
+        sum += units;
     }
     int before = sum;
     for (int d = 1; d < 32; d <<= 1) {
@@ -149,10 +152,7 @@ __device__ __forceinline__ void fill_tables(const Params& p, Tables& s, int warp
     }
     if (lane == 31) s.first_unit[p.experts] = before;
     before -= sum;
-    for (int e = begin; e < end; ++e) {
-        s.first_unit[e] = before;
-        before += tiles_of(p, s.count[e]) * p.pairs;
-    }
+    for (int e = begin; e < end; ++e) s.first_unit[e] += before;
 }
 
 __device__ __forceinline__ int unit_count(const Params& p, const Smem& s) {
@@ -173,17 +173,18 @@ __device__ __forceinline__ Unit unit_of(const Params& p, const Smem& s, int u, i
         r.e = lo;
         count = s.tables.count[lo];
         first = s.tables.start[lo];
-        per = even_rows(count, p.tile);
-        const int tiles = (count + per - 1) / per, i = u - s.tables.first_unit[lo];
-        t = i % tiles;
-        r.pair = i / tiles;
+        per = s.tables.per[lo];
+        const uint32_t tiles = (static_cast<uint32_t>(s.tables.first_unit[lo + 1]) - s.tables.first_unit[lo]) / static_cast<uint32_t>(p.pairs);
+        const uint32_t i = u - s.tables.first_unit[lo];
+        r.pair = static_cast<int>(i / tiles);
+        t = static_cast<int>(i - r.pair * tiles);
     } else {
         per = p.cut;
-        const int v = p.first_cut + u / p.cuts, tiles = (count + per - 1) / per;
-        const int band = v / (kBandTiles * p.pairs), in_band = v - band * kBandTiles * p.pairs;
-        const int high = min(kBandTiles, tiles - band * kBandTiles);
-        t = band * kBandTiles + in_band % high;
-        r.pair = in_band / high;
+        const uint32_t v = p.first_cut + (p.cuts == 1 ? u : u / p.cuts), of_band = kBandTiles * p.pairs;
+        const uint32_t band = v / of_band, in_band = v - band * of_band;
+        const uint32_t high = min(kBandTiles, p.tiles - static_cast<int>(band) * kBandTiles);
+        r.pair = static_cast<int>(high == kBandTiles ? in_band / kBandTiles : in_band / high);
+        t = static_cast<int>(band * kBandTiles + in_band - r.pair * high);
     }
     r.row0 = first + t * per;
     r.rows = min(per, count - t * per);
@@ -192,8 +193,8 @@ __device__ __forceinline__ Unit unit_of(const Params& p, const Smem& s, int u, i
         r.row0 += skip;
         r.rows = max(0, min(p.tile, r.rows - skip));
     }
-    r.b0 = static_cast<int>(static_cast<int64_t>(split) * p.nb / p.splits);
-    r.b1 = static_cast<int>(static_cast<int64_t>(split + 1) * p.nb / p.splits);
+    r.b0 = p.splits == 1 ? 0 : split * p.nb / p.splits;
+    r.b1 = p.splits == 1 ? p.nb : (split + 1) * p.nb / p.splits;
     return r;
 }
 
@@ -485,7 +486,8 @@ struct Piece {
 // Elements between the 16-byte boundary before a row's outputs and them.
 template <bool kGated>
 __device__ __forceinline__ int row_past(const Params& p, int64_t row) {
-    return kGated ? 0 : static_cast<int>(elements_past(static_cast<const uint16_t*>(p.Y) + row * p.ldy));
+    const uint32_t first = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.Y) >> 1) + static_cast<uint32_t>(row) * static_cast<uint32_t>(p.ldy);
+    return kGated ? 0 : static_cast<int>(first & 7u);
 }
 
 // The epilogue's chunks of a part, where p.whole: outputs of 16 bits, K not split. The rows are shifted to their place in memory as they are
@@ -1101,6 +1103,7 @@ cudaError_t launch_w16_gemm(const w16_layer& L, const W16Args& a, cudaStream_t s
     const w16::Rest& rest = shape.rest;
     p.cut = shape.tile;
     p.cuts = 1;
+    p.tiles = w16::tiles_of(p.rows, p.cut);
     p.units = static_cast<int>((a.rows + p.cut - 1) / p.cut * L.pairs - rest.units);   // (experts: not used)
     const cudaError_t first = launch(shape);
     if (first != cudaSuccess || rest.units == 0) return first;
