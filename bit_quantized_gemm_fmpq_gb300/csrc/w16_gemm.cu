@@ -12,7 +12,8 @@
 //   * A unit's whole K is summed in TMEM; two accumulators, so that a unit's epilogue runs under the next one's MMAs (above 256 rows a
 //     unit takes both, and reads its weights once).
 //   * The epilogue turns 8 rows at a time through shared memory in FP32, so that a thread has 8 neighbouring outputs of a row:
-//     bias, activation, residual (16-byte loads, on their way before the sums are there) and one 16-byte store.
+//     activation, residual (16-byte loads, on their way before the sums are there) and one 16-byte store. The bias is added as the sums are
+//     turned, where a thread has one weight row.
 //   * Units too few for the pairs: K is split over the pairs of a cluster; the others leave their sums in the first one's
 //     shared memory, which adds them in order, so results do not depend on timing. What a dense product's units leave over of full
 //     rounds has a launch of its own, cut finer and along K, under the first one's end.
@@ -23,6 +24,8 @@
 //   warp 2      allocates and frees TMEM
 //   warp 3      sums up the groups' units
 //   warps 4-19  epilogue: TMEM lane quarter warp % 4; four groups take the unit's 8-row chunks in turn
+#include <type_traits>
+
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -45,6 +48,10 @@ constexpr int kPartRows = 256;    // of a part: the N side of an MMA, and an acc
 constexpr int kMostRows = 512;    // of a unit: two parts
 constexpr int kChunk = 8;         // rows of X that a group turns at a time
 constexpr int kStageLd = 136;     // floats of a row there: 128 outputs, and up to 7 in front of them
+// Epilogues: any outputs and any split of K; put_out_whole, without a residual and with one.
+enum { kAnyForm, kWholeBare, kWholeAdded };
+constexpr int kAhead = 2;         // chunks of a group whose residual is on its way (put_out_whole), 16 bytes a thread and a row's end
+constexpr int kAheadBytes = kGroups * kAhead * (128 + kChunk) * 16;
 constexpr int kBandTiles = 8;     // dense order: bands of 8 row tiles, weight tiles inside a band
 constexpr int kMaxSplits = 4;
 constexpr int kBigBox = 64, kSmallBox = 16;   // rows of the two TMA boxes
@@ -87,7 +94,7 @@ struct __align__(1024) Smem {
     int abort_flag;
     Tables tables;
     // then the ring of operand stages (16 KB of weights, tile / 2 rows of X), and with K split the sums of the other pairs:
-    // [split - 1][chunk][2 vectors][128 weight rows] of 4 floats
+    // [split - 1][chunk][2 vectors][128 weight rows] of 4 floats, or (K not split) kAheadBytes of the residual
 };
 constexpr int kHeadBytes = (sizeof(Smem) + 1023) / 1024 * 1024;
 constexpr int kSmemBytes = 232448;                  // 227 KB: what a CTA may use
@@ -460,12 +467,6 @@ __device__ __forceinline__ uint32_t residual1(const Params& p, int64_t row, int 
     const int64_t at = row * p.e.ldr + n;
     return p.f32 ? static_cast<const uint32_t*>(p.e.residual)[at] : static_cast<const uint16_t*>(p.e.residual)[at];
 }
-// bias[first] and behind, 0 past `columns`
-template <int kW>
-__device__ __forceinline__ void load_bias(const Params& p, int64_t first, int columns, float (&b)[kW]) {
-#pragma unroll
-    for (int i = 0; i < kW; ++i) b[i] = i < columns ? epi::bias_at(p.e, first + i, p.bf16 != 0) : 0.0f;
-}
 // Where a chunk's sums of another pair begin for a weight row (16 bytes each).
 __device__ __forceinline__ int other_sums(const Params& p, int split, int chunk, int row) {
     return ((split - 1) * (p.tile / kChunk) + chunk) * (kChunk / 4) * 128 + row;
@@ -490,12 +491,11 @@ __device__ __forceinline__ int row_past(const Params& p, int64_t row) {
     return kGated ? 0 : static_cast<int>(first & 7u);
 }
 
-// The epilogue's chunks of a part, where p.whole: outputs of 16 bits, K not split. The rows are shifted to their place in memory as they are
+// The epilogue's chunks of a part: outputs of 16 bits, K not split. The rows are shifted to their place in memory as they are
 // turned, and the residual of a thread's next row is on its way while it works on one (WHOLE).
-template <bool kGated, int kW, int kCols>
-__device__ __forceinline__ void put_out_whole(const Params& p, float (*turn)[kChunk][kStageLd], uint32_t from_tmem, int g, int tid, int64_t row0, int rows,
-                                              int n0, const Piece<kW, kCols>& piece, const float (&bias)[kW], const float (&bias_up)[kW],
-                                              bool ok, int& buffer) {
+template <bool kGated, bool kAdded, int kW, int kCols, typename Wait>
+__device__ __forceinline__ void put_out_whole(const Params& p, float (*turn)[kChunk][kStageLd], uint8_t* residuals, uint32_t from_tmem, int g, int tid, int64_t row0, int rows,
+                                              int n0, const Piece<kW, kCols>& piece, float bias, const Wait& wait, int& buffer) {
     constexpr int kPieces = kCols / kW;
     const int chunks = (rows + kChunk - 1) / kChunk, sub = tid / kPieces, i = tid % kPieces;
     // of every 32 packed rows of a gated layer, 16 are gates and 16 the ups of the same hidden channels
@@ -507,40 +507,38 @@ __device__ __forceinline__ void put_out_whole(const Params& p, float (*turn)[kCh
     uint16_t* y = static_cast<uint16_t*>(p.Y) + row * p.ldy + n0;
     const uint16_t* r = static_cast<const uint16_t*>(p.e.residual) + row * p.e.ldr + n0;
     const int64_t y_step = p.ldy * (kGroups * kChunk), r_step = p.e.ldr * (kGroups * kChunk);
-    int left = ok ? rows - kChunk * g - sub : 0;   // this thread's row of a chunk exists where more than 0 are left
-    uint32_t d[kChunk], raw[kW / 2];
-    // (whole pieces, which hold one of the piece's elements at least)
+    int left = rows - kChunk * g - sub;   // this thread's row of a chunk exists where more than 0 are left
+    uint32_t d[kChunk];
+    // the residual's pieces of this thread's next rows (whole ones, which hold one of the piece's elements at least), and for the first thread
+    // of a row those of its last columns
     const bool head = max(piece.first, 0) < piece.columns, tail = piece.first < 0 && piece.first + kCols < piece.columns;
-    uint32_t ends[kW / 2];   // the row's last columns, for the first thread
-    auto ask = [&] {
-        if constexpr (kW == 8) {
-            if (head) {
-                const uint4 a = *reinterpret_cast<const uint4*>(r + piece.first);
-                raw[0] = a.x, raw[1] = a.y, raw[2] = a.z, raw[3] = a.w;
-            }
-            if (tail) {
-                const uint4 a = *reinterpret_cast<const uint4*>(r + piece.first + kCols);
-                ends[0] = a.x, ends[1] = a.y, ends[2] = a.z, ends[3] = a.w;
-            }
-        } else if (head) {
-            const uint2 a = *reinterpret_cast<const uint2*>(r + piece.first);
-            raw[0] = a.x, raw[1] = a.y;
-        }
+    uint4* slot = reinterpret_cast<uint4*>(residuals) + g * kAhead * 128 + tid;
+    uint4* ends = reinterpret_cast<uint4*>(residuals) + kGroups * kAhead * 128 + g * kAhead * kChunk + sub;
+    auto ask = [&](int i, int left) {
+        if (left > 0 && head) dev::cp_async_if<2 * kW>(dev::smem_u32(slot + i * 128), r + piece.first, true);
+        if (left > 0 && tail) dev::cp_async_if<2 * kW>(dev::smem_u32(ends + i * kChunk), r + piece.first + kCols, true);
+        dev::cp_async_commit();
+        r += r_step;
     };
-    const bool bf16 = p.bf16 != 0, biased = p.e.bias != nullptr, added = p.e.residual != nullptr;
+    const bool bf16 = p.bf16 != 0;
+    if (kAdded)
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) ask(i, left - i * kGroups * kChunk);
+    int turns = 0;   // so far
+    if (!wait()) left = 0;
     dev::tmem_ld8(from_tmem + kChunk * min(g, chunks - 1), d);
-    if (added && left > 0) ask();
 #pragma unroll 1
     for (int c = g; c < chunks; c += kGroups) {
         float* here = &turn[buffer][0][0];
         buffer ^= 1;
         dev::tmem_ld_wait8(d);
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j) here[to[j]] = __uint_as_float(d[j]);
+        for (int j = 0; j < kChunk; ++j) here[to[j]] = __uint_as_float(d[j]) + bias;
         // (whoever writes this buffer again has passed the next barrier, behind which the others have read it)
         dev::named_bar_sync(2 + g, 128);
         dev::tmem_ld8(from_tmem + kChunk * min(c + kGroups, chunks - 1), d);
-        r += r_step;
+        const int held = turns++ % kAhead;   // where this row's residual is
+        if (kAdded) dev::cp_async_wait<kAhead - 1>();
         if (left > 0) {
             const float* from = here + sub * kStageLd + place;
             float f[kW];
@@ -553,33 +551,34 @@ __device__ __forceinline__ void put_out_whole(const Params& p, float (*turn)[kCh
 #pragma unroll
                 for (int c = 0; c < kW; ++c) f[c] = piece.first + c < 0 ? e[c] : f[c];
             }
-            if (biased)
-#pragma unroll
-                for (int i = 0; i < kW; ++i) f[i] += bias[i];
             activate_piece(p.e.act, f);
             if constexpr (kGated) {
                 const float4 v = *reinterpret_cast<const float4*>(from + 16);
                 const float up[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int i = 0; i < kW; ++i) f[i] *= biased ? up[i] + bias_up[i] : up[i];
+                for (int i = 0; i < kW; ++i) f[i] *= up[i];
             }
             if (p.row_weight != nullptr) {
                 const float w = weight_of(p, row);
 #pragma unroll
                 for (int i = 0; i < kW; ++i) f[i] *= w;
             }
-            if (added) {
+            if (kAdded) {
+                const uint4 now = slot[held * 128];
+                uint32_t raw[4] = {now.x, now.y, now.z, now.w};
+                if (!kGated && piece.first < 0) {
+                    const uint4 last = ends[held * kChunk];
+                    const uint32_t e[4] = {last.x, last.y, last.z, last.w};
 #pragma unroll
-                for (int i = 0; i < kW / 2; ++i) {
-                    float2 a = epi::values16(raw[i], bf16);
-                    if (!kGated && piece.first < 0) {
-                        const float2 e = epi::values16(ends[i], bf16);
-                        a = make_float2(piece.first + 2 * i < 0 ? e.x : a.x, piece.first + 2 * i + 1 < 0 ? e.y : a.y);
-                    }
-                    f[2 * i] += a.x;
-                    f[2 * i + 1] += a.y;
+                    for (int c = 0; c < 4; ++c)
+                        raw[c] = (piece.first + 2 * c < 0 ? e[c] & 0xFFFFu : raw[c] & 0xFFFFu) | (piece.first + 2 * c + 1 < 0 ? e[c] & 0xFFFF0000u : raw[c] & 0xFFFF0000u);
                 }
-                if (left > kGroups * kChunk) ask();
+#pragma unroll
+                for (int c = 0; c < kW / 2; ++c) {
+                    const float2 a = epi::values16(raw[c], bf16);
+                    f[2 * c] += a.x;
+                    f[2 * c + 1] += a.y;
+                }
             }
             uint32_t o[kW / 2];
 #pragma unroll
@@ -605,6 +604,7 @@ __device__ __forceinline__ void put_out_whole(const Params& p, float (*turn)[kCh
                 *reinterpret_cast<uint2*>(y + piece.first) = make_uint2(o[0], o[1]);
             }
         }
+        if (kAdded) ask(held, left - kAhead * kGroups * kChunk);
         y += y_step;
         row += kGroups * kChunk;
         left -= kGroups * kChunk;
@@ -616,9 +616,10 @@ __device__ __forceinline__ void put_out_whole(const Params& p, float (*turn)[kCh
 // columns of one row: 8, or gate and up of 4 hidden channels. Where rows of Y or of the residual do not start on 8-byte boundaries
 // (FP32: 16) a thread has one column instead, of all 8 rows (gated: of 4), so that a warp's accesses are still neighbours. A chunk's
 // sums leave TMEM while the chunk before is put out.
-template <bool kGated, bool kWhole>
+template <bool kGated, int kForm>
 __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* others, const Place& at, int warp, int lane, uint32_t tmem,
                                          volatile int* abort_flag) {
+    constexpr bool kWhole = kForm != kAnyForm;
     constexpr int kCols = kGated ? 64 : 128;              // of this CTA
     constexpr int kW = kCols * kChunk / 128, kPieces = kCols / kW;
     constexpr int kColumnRows = 128 / kCols;              // rows that the threads cover at once, a column each
@@ -635,6 +636,17 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* other
     uint32_t np = 0;   // parts so far
     bool ok = true;
     int part = 0, buffer = 0;   // (of turn: which a chunk writes)
+    // a unit's lines of the residual to the L2, under its MMAs
+    auto fetch = [&](int u) {
+        if (!first || p.e.residual == nullptr || u >= units) return;
+        const Unit v = unit_of(p, s, u, 0);
+        const int n0 = (2 * v.pair + static_cast<int>(at.rank)) * kCols, size = p.f32 ? 4 : 2, bytes = min(kCols, p.out_n - n0) * size;
+        for (int r = (warp - 4) * 32 + lane; r < v.rows; r += kEpiWarps * 32) {
+            const uint8_t* line = static_cast<const uint8_t*>(p.e.residual) + ((static_cast<int64_t>(v.row0) + r) * p.e.ldr + n0) * size;
+            for (int b = 0; b < bytes; b += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + b));
+            if (bytes > 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + bytes - 1));
+        }
+    };
     for (int u = at.cluster; u < units; ++np) {
         const Unit whole = unit_of(p, s, u, at.split);
         if (whole.rows == 0) {
@@ -645,6 +657,7 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* other
         struct {
             int e, pair, rows, row0;
         } const t{whole.e, whole.pair, whole.part_rows(part), whole.part_row0(part)};
+        if (part == 0) fetch(u);
         if (++part == whole.parts()) {
             part = 0;
             u += at.clusters;
@@ -654,34 +667,23 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* other
         const int columns = p.out_n - n;
         const Piece<kW, kCols> piece(tid % kPieces, kWhole ? row_past<kGated>(p, t.row0 + tid / kPieces) : 0, min(kCols, p.out_n - n0));
         const int chunks = (t.rows + kChunk - 1) / kChunk;
-        float bias[kW], bias_up[kW];
-        if (kWhole && p.e.bias != nullptr) {
-#pragma unroll
-            for (int c = 0; c < kW; ++c) {
-                const int64_t b = static_cast<int64_t>(t.e) * p.N + n0 + piece.column(c);
-                bias[c] = piece.has(c) ? epi::bias_at(p.e, b, p.bf16 != 0) : 0.0f;
-                if (kGated) bias_up[c] = piece.has(c) ? epi::bias_at(p.e, b + p.out_n, p.bf16 != 0) : 0.0f;
-            }
-        } else if (first && p.e.bias != nullptr) {
-            load_bias(p, static_cast<int64_t>(t.e) * p.N + n, pieces ? columns : min(columns, 1), bias);
-            if constexpr (kGated) load_bias(p, static_cast<int64_t>(t.e) * p.N + p.out_n + n, pieces ? columns : min(columns, 1), bias_up);
+        float bias = -0.0f;   // of this thread's packed row: added to its sums (-0: nothing is)
+        if (first && p.e.bias != nullptr) {
+            const int c = kGated ? n0 + 16 * (tid >> 5) + (tid & 15) : n0 + tid;   // (16 gates, 16 ups)
+            if (c < p.out_n) bias = epi::bias_at(p.e, static_cast<int64_t>(t.e) * p.N + (kGated && (tid & 16) != 0 ? p.out_n : 0) + c, p.bf16 != 0);
         }
-        if (first && p.e.residual != nullptr) {   // the unit's lines of the residual to the L2, under its MMAs
-            const int size = p.f32 ? 4 : 2, bytes = min(kCols, p.out_n - (n - col)) * size;
-            for (int r = (warp - 4) * 32 + lane; r < t.rows; r += kEpiWarps * 32) {
-                const uint8_t* line = static_cast<const uint8_t*>(p.e.residual) + ((static_cast<int64_t>(t.row0) + r) * p.e.ldr + (n - col)) * size;
-                for (int b = 0; b < bytes; b += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + b));
-                if (bytes > 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + bytes - 1));
-            }
-        }
-        ok = ok && dev::mbar_wait(&s.acc_full[acc], (np >> 1) & 1, abort_flag);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!kWhole && first && p.splits > 1 && ok) ok = __all_sync(0xFFFFFFFFu, dev::mbar_wait_cluster(&s.split_full, 0));
-        dev::tc_fence_after();
+        auto wait = [&] {
+            ok = ok && dev::mbar_wait(&s.acc_full[acc], (np >> 1) & 1, abort_flag);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!kWhole && first && p.splits > 1 && ok) ok = __all_sync(0xFFFFFFFFu, dev::mbar_wait_cluster(&s.split_full, 0));
+            dev::tc_fence_after();
+            return ok;
+        };
         const uint32_t from_tmem = base + acc * kPartRows;
+        if (!kWhole) wait();
 
         if constexpr (kWhole) {
-            put_out_whole<kGated>(p, s.turn[g], from_tmem, g, tid, t.row0, t.rows, n0, piece, bias, bias_up, ok, buffer);
+            put_out_whole<kGated, kForm == kWholeAdded>(p, s.turn[g], reinterpret_cast<uint8_t*>(others), from_tmem, g, tid, t.row0, t.rows, n0, piece, bias, wait, buffer);
         } else if (!first) {   // to the first pair's CTA of this rank
             const uint32_t to = dev::mapa(others, at.rank) + other_sums(p, at.split, 0, tid) * 16u;
             for (int c = g; c < chunks; c += kGroups) {
@@ -709,15 +711,12 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* other
                     float f[kW];
 #pragma unroll
                     for (int i = 0; i < kW; i += 4) *reinterpret_cast<float4*>(&f[i]) = *reinterpret_cast<const float4*>(from + i);
-                    if (p.e.bias != nullptr)
-#pragma unroll
-                        for (int i = 0; i < kW; ++i) f[i] += bias[i];
                     activate_piece(p.e.act, f);
                     if constexpr (kGated) {
                         const float4 v = *reinterpret_cast<const float4*>(from + 16);
                         const float up[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                        for (int i = 0; i < kW; ++i) f[i] *= p.e.bias != nullptr ? up[i] + bias_up[i] : up[i];
+                        for (int i = 0; i < kW; ++i) f[i] *= up[i];
                     }
                     if (p.row_weight != nullptr) {
                         const float w = weight_of(p, row0 + sub);
@@ -735,13 +734,13 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* other
                         if (sub + kColumnRows * i < rows) raw[i] = residual1(p, row0 + sub + kColumnRows * i, n);
                 float f[kW];
 #pragma unroll
-                for (int i = 0; i < kW; ++i) f[i] = turn[sub + kColumnRows * i][place] + (p.e.bias != nullptr ? bias[0] : 0.0f);
+                for (int i = 0; i < kW; ++i) f[i] = turn[sub + kColumnRows * i][place];
                 activate_piece(p.e.act, f);
 #pragma unroll
                 for (int i = 0; i < kW; ++i) {
                     const int j = sub + kColumnRows * i;
                     if (j >= rows) continue;
-                    if constexpr (kGated) f[i] *= turn[j][place + 16] + (p.e.bias != nullptr ? bias_up[0] : 0.0f);
+                    if constexpr (kGated) f[i] *= turn[j][place + 16];
                     if (p.row_weight != nullptr) f[i] *= weight_of(p, row0 + j);
                     if (p.e.residual != nullptr) f[i] += p.f32 ? __uint_as_float(raw[i]) : epi::value16(static_cast<uint16_t>(raw[i]), p.bf16 != 0);
                     store1(p, row0 + j, n, f[i]);
@@ -765,7 +764,7 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* other
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < kChunk; ++j) s.turn[g][buffer][j][tid] = f[j];
+                for (int j = 0; j < kChunk; ++j) s.turn[g][buffer][j][tid] = f[j] + bias;
                 // (whoever writes this buffer again has passed the next barrier, behind which the others have read it)
                 dev::named_bar_sync(2 + g, 128);
                 buffer ^= 1;
@@ -783,7 +782,7 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* other
     if (!ok && lane == 0) fail(p, abort_flag);
 }
 
-template <bool kGated, bool kWhole>
+template <bool kGated, int kForm>
 __global__ void __launch_bounds__(kThreads, 1)
 w16_kernel(const Params p, const __grid_constant__ CUtensorMap big, const __grid_constant__ CUtensorMap small) {
     extern __shared__ uint8_t smem_raw[];
@@ -839,7 +838,7 @@ w16_kernel(const Params p, const __grid_constant__ CUtensorMap big, const __grid
     } else if (warp == 1) {
         mma_issuer(p, s, ring, at, tmem, abort_flag);
     } else if (warp >= 4) {
-        epilogue<kGated, kWhole>(p, s, others, at, warp, lane, tmem, abort_flag);
+        epilogue<kGated, kForm>(p, s, others, at, warp, lane, tmem, abort_flag);
     }
     __syncwarp();
     dev::tc_fence_before();
@@ -953,8 +952,8 @@ int resident_clusters(const w16_layer& L, int splits) {
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = config(most * 2 * splits, 2 * splits, kSmemBytes, nullptr, attr);
     int got = 0;
-    if (ensure_smem_limit(reinterpret_cast<const void*>(w16_kernel<false, false>), kSmemBytes) == cudaSuccess &&
-        cudaOccupancyMaxActiveClusters(&got, w16_kernel<false, false>, &cfg) == cudaSuccess && got > 0 && got < most)
+    if (ensure_smem_limit(reinterpret_cast<const void*>(w16_kernel<false, kAnyForm>), kSmemBytes) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&got, w16_kernel<false, kAnyForm>, &cfg) == cudaSuccess && got > 0 && got < most)
         most = got;
     cudaGetLastError();   // a failed query leaves no error behind
     if (known) cached[L.device][splits] = most;
@@ -971,11 +970,12 @@ struct Shape {
     Rest rest;
 };
 
-Shape with_ring(int tile, int splits, int64_t units, int clusters) {
+// (`ahead`: of the residual, where K is not split)
+Shape with_ring(int tile, int splits, int64_t units, int clusters, int ahead) {
     Shape s{tile, splits, 0, 0, 0, {}};
     s.grid = static_cast<int>(units < clusters ? units : clusters) * 2 * splits;
     s.stage_bytes = kTileBytes + tile / 2 * 128;
-    const int others = (splits - 1) * tile * 128 * 4;
+    const int others = splits > 1 ? (splits - 1) * tile * 128 * 4 : ahead;
     s.stages = (kRingBytes - others) / s.stage_bytes;
     if (s.stages > kMaxStages) s.stages = kMaxStages;
     return s;
@@ -985,14 +985,14 @@ Shape with_ring(int tile, int splits, int64_t units, int clusters) {
 // 6000 clk, the exchange 1500 more: 300 x 4096 -> 20480 62 to 55 us, 1 x 8192 -> 28672 82 to 77, 2048 x 4096 -> 12288 127 to 123; counted at
 // 1500, 300 x 1024 -> 20000 lost 3 of 24 and 520 x 4096 -> 11008 3 of 48.
 template <typename F>
-Rest rest_of(const w16_layer& L, int units, int per, const F& block_of) {
+Rest rest_of(const w16_layer& L, int units, int per, int ahead, const F& block_of) {
     Rest best{0, 0, 0, 0, 1e30};
     for (int splits = 1; splits <= kMaxSplits; splits *= 2) {
         if (splits > 1 && L.nb < 4 * splits) break;
         const int clusters = resident_clusters(L, splits);
         for (int tile = 32; tile <= kPartRows && tile <= per; tile += 32) {
             const int cuts = (per + tile - 1) / tile;
-            if (units * cuts > clusters || with_ring(tile, splits, 1, 1).stages < 4) continue;
+            if (units * cuts > clusters || with_ring(tile, splits, 1, 1, ahead).stages < 4) continue;
             const double time = (L.nb + splits - 1) / splits * block_of(tile) + (splits > 1 ? 1500.0 : 0.0) + 6000.0 + 14.0 * tile;
             if (time < best.time) best = Rest{units, tile, cuts, splits, time};
         }
@@ -1014,7 +1014,7 @@ int64_t most_units(const w16_layer& L, int used, int rows, int tile) {
 // 20.1 and 13.3, 128 x 8192 -> 8192 35.6 and 31.4, one row of 65 experts, 6400 -> 512, 29.5 and 14.4 in 4; the exchange takes about 1500
 // clk. (The last round's blocks cut evenly over all pairs, their sums in global memory and the last to arrive adding them: 31.6 in place of 25.2, 17.2 of 13.3, 64
 // units of a token's 8 experts 35.8 of 28.3, and 2048 x 4096 -> 12288, 4 units in the last round, no faster.)
-Shape shape_of(const w16_layer& L, const W16Args& a) {
+Shape shape_of(const w16_layer& L, const W16Args& a, int ahead) {
     const bool grouped = a.start != nullptr;
     const int rows = static_cast<int>(a.rows);
     // the experts' loads are known on the device only: every one in use is taken to have the mean, and a sixth more for the spread
@@ -1032,12 +1032,12 @@ Shape shape_of(const w16_layer& L, const W16Args& a) {
             const int64_t tiles = (load + per - 1) / per, units = tiles * L.pairs * used, rounds = (units + clusters - 1) / clusters;
             const int64_t most = grouped ? most_units(L, used, rows, tile) : units;
             if (splits > 1 && most > clusters) continue;   // (a cluster that splits K takes one unit)
-            Shape s = with_ring(tile, splits, most, clusters);
+            Shape s = with_ring(tile, splits, most, clusters, ahead);
             if (s.stages < 4) continue;
             const double round = L.nb * block_of(per) + (per > kPartRows ? 14.0 * per : 0.0);
             double time = splits > 1 ? (L.nb + splits - 1) / splits * block_of(per) + 1500.0 + 14.0 * per : rounds * round + 14.0 * per;
             if (!grouped && splits == 1 && rounds > 1 && units % clusters != 0) {
-                const Rest r = rest_of(L, static_cast<int>(units % clusters), per, block_of);
+                const Rest r = rest_of(L, static_cast<int>(units % clusters), per, ahead, block_of);
                 if (r.time < round) {
                     s.rest = r;
                     time += r.time - round;
@@ -1056,7 +1056,6 @@ Shape shape_of(const w16_layer& L, const W16Args& a) {
 }  // namespace w16
 
 cudaError_t launch_w16_gemm(const w16_layer& L, const W16Args& a, cudaStream_t stream) {
-    const w16::Shape shape = w16::shape_of(L, a);
     w16::Params p{};
     p.W = static_cast<const uint8_t*>(a.W);
     p.start = a.start;
@@ -1073,6 +1072,13 @@ cudaError_t launch_w16_gemm(const w16_layer& L, const W16Args& a, cudaStream_t s
     };
     auto both = [&](int bytes) { return takes(a.Y, a.ldy, bytes) && (p.e.residual == nullptr || takes(p.e.residual, p.e.ldr, bytes)); };
     p.vec = both(16) ? 8 : !p.f32 && both(8) ? 4 : 1;
+    // put_out_whole does it where K is not split (a residual's rows begin at the same place of their 16 bytes as the outputs')
+    const bool unsplit = !p.f32 && (L.gated ? p.vec >= 4
+                                            : p.e.residual == nullptr ||
+                                                  (((reinterpret_cast<uintptr_t>(a.Y) ^ reinterpret_cast<uintptr_t>(p.e.residual)) & 15u) == 0 &&
+                                                   (p.ldy - p.e.ldr) % 8 == 0));
+    const int ahead = unsplit && p.e.residual != nullptr ? w16::kAheadBytes : 0;
+    const w16::Shape shape = w16::shape_of(L, a, ahead);
     p.rows = static_cast<int>(a.rows);
     p.N = L.N;
     p.out_n = L.gated ? L.N / 2 : L.N;
@@ -1085,13 +1091,12 @@ cudaError_t launch_w16_gemm(const w16_layer& L, const W16Args& a, cudaStream_t s
     auto launch = [&](const w16::Shape& s) {
         p.tile = s.tile;
         p.splits = s.splits;
-        // (a residual's rows begin at the same place of their 16 bytes as the outputs')
-        const bool whole = !p.f32 && s.splits == 1 &&
-                  (L.gated ? p.vec >= 4
-                           : p.e.residual == nullptr ||
-                                 (((reinterpret_cast<uintptr_t>(a.Y) ^ reinterpret_cast<uintptr_t>(p.e.residual)) & 15u) == 0 && (p.ldy - p.e.ldr) % 8 == 0));
-        auto fn = L.gated ? (whole ? w16::w16_kernel<true, true> : w16::w16_kernel<true, false>)
-                          : (whole ? w16::w16_kernel<false, true> : w16::w16_kernel<false, false>);
+        const bool whole = unsplit && s.splits == 1;
+        auto form = [&](auto gated) {
+            return !whole ? w16::w16_kernel<gated.value, w16::kAnyForm>
+                          : p.e.residual == nullptr ? w16::w16_kernel<gated.value, w16::kWholeBare> : w16::w16_kernel<gated.value, w16::kWholeAdded>;
+        };
+        auto fn = L.gated ? form(std::true_type{}) : form(std::false_type{});
         const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), w16::kSmemBytes);
         if (e != cudaSuccess) return e;
         p.stages = s.stages;
@@ -1111,7 +1116,7 @@ cudaError_t launch_w16_gemm(const w16_layer& L, const W16Args& a, cudaStream_t s
     p.cuts = rest.cuts;
     p.units = rest.units * rest.cuts;
     p.last_launch = 1;
-    return launch(w16::with_ring(rest.tile, rest.splits, p.units, p.units));
+    return launch(w16::with_ring(rest.tile, rest.splits, p.units, p.units, ahead));
 }
 
 cudaError_t launch_w16_pack(const w16_layer& L, int expert, const void* W, int64_t ld_n, int64_t ld_k, void* Wp, cudaStream_t stream) {
