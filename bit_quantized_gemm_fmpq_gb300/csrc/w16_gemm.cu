@@ -491,8 +491,12 @@ __device__ __forceinline__ int row_past(const Params& p, int64_t row) {
     return kGated ? 0 : static_cast<int>(first & 7u);
 }
 
-// The epilogue's chunks of a part: outputs of 16 bits, K not split. The rows are shifted to their place in memory as they are
-// turned, and the residual of a thread's next row is on its way while it works on one (WHOLE).
+// The epilogue's chunks of a part: outputs of 16 bits, K not split. What costs time here is a group's chain through a chunk (TMEM, shared
+// memory, barrier, output) and the size of the loop's code, so the rows are shifted to their place in memory as they are turned, the residual
+// of a thread's next two rows is on its way by cp.async (no register waits for it), and this is a kernel of its own, with a residual or
+// without. 8192 x 512 -> 4096 bf16: plain 33 us, with bias, silu and residual 51 (by the form below, with a bias for each of a piece's
+// columns, 49 and 91); 4096 x 1024 -> 4096 31 and 36 (35 and 53), -> 4095 35 and 44 (57 and 88). No faster: the residual 3 or 4
+// rows ahead, or its lines sent for to the L2 before; two chunks a turn of the loop (8192 x 512: 51 and 79); one kernel for both (38 and 55).
 template <bool kGated, bool kAdded, int kW, int kCols, typename Wait>
 __device__ __forceinline__ void put_out_whole(const Params& p, float (*turn)[kChunk][kStageLd], uint8_t* residuals, uint32_t from_tmem, int g, int tid, int64_t row0, int rows,
                                               int n0, const Piece<kW, kCols>& piece, float bias, const Wait& wait, int& buffer) {
@@ -612,7 +616,7 @@ __device__ __forceinline__ void put_out_whole(const Params& p, float (*turn)[kCh
     dev::tmem_ld_wait8(d);   // (the last one's is of no use)
 }
 
-// A thread's sums, a chunk's 8 rows for one packed weight row, go through shared memory; then it has one piece of neighbouring
+// Any outputs, any split of K: a thread's sums, a chunk's 8 rows for one packed weight row, go through shared memory; then it has one piece of neighbouring
 // columns of one row: 8, or gate and up of 4 hidden channels. Where rows of Y or of the residual do not start on 8-byte boundaries
 // (FP32: 16) a thread has one column instead, of all 8 rows (gated: of 4), so that a warp's accesses are still neighbours. A chunk's
 // sums leave TMEM while the chunk before is put out.
@@ -636,17 +640,6 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* other
     uint32_t np = 0;   // parts so far
     bool ok = true;
     int part = 0, buffer = 0;   // (of turn: which a chunk writes)
-    // a unit's lines of the residual to the L2, under its MMAs
-    auto fetch = [&](int u) {
-        if (!first || p.e.residual == nullptr || u >= units) return;
-        const Unit v = unit_of(p, s, u, 0);
-        const int n0 = (2 * v.pair + static_cast<int>(at.rank)) * kCols, size = p.f32 ? 4 : 2, bytes = min(kCols, p.out_n - n0) * size;
-        for (int r = (warp - 4) * 32 + lane; r < v.rows; r += kEpiWarps * 32) {
-            const uint8_t* line = static_cast<const uint8_t*>(p.e.residual) + ((static_cast<int64_t>(v.row0) + r) * p.e.ldr + n0) * size;
-            for (int b = 0; b < bytes; b += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + b));
-            if (bytes > 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + bytes - 1));
-        }
-    };
     for (int u = at.cluster; u < units; ++np) {
         const Unit whole = unit_of(p, s, u, at.split);
         if (whole.rows == 0) {
@@ -657,7 +650,6 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* other
         struct {
             int e, pair, rows, row0;
         } const t{whole.e, whole.pair, whole.part_rows(part), whole.part_row0(part)};
-        if (part == 0) fetch(u);
         if (++part == whole.parts()) {
             part = 0;
             u += at.clusters;
@@ -671,6 +663,14 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* other
         if (first && p.e.bias != nullptr) {
             const int c = kGated ? n0 + 16 * (tid >> 5) + (tid & 15) : n0 + tid;   // (16 gates, 16 ups)
             if (c < p.out_n) bias = epi::bias_at(p.e, static_cast<int64_t>(t.e) * p.N + (kGated && (tid & 16) != 0 ? p.out_n : 0) + c, p.bf16 != 0);
+        }
+        if (!kWhole && first && p.e.residual != nullptr) {   // the part's lines of the residual to the L2, under its MMAs
+            const int size = p.f32 ? 4 : 2, bytes = min(kCols, p.out_n - n0) * size;
+            for (int r = (warp - 4) * 32 + lane; r < t.rows; r += kEpiWarps * 32) {
+                const uint8_t* line = static_cast<const uint8_t*>(p.e.residual) + ((static_cast<int64_t>(t.row0) + r) * p.e.ldr + n0) * size;
+                for (int b = 0; b < bytes; b += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + b));
+                if (bytes > 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + bytes - 1));
+            }
         }
         auto wait = [&] {
             ok = ok && dev::mbar_wait(&s.acc_full[acc], (np >> 1) & 1, abort_flag);

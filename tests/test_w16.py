@@ -111,6 +111,42 @@ def test_gated(fmpq_mod, M, K, F, act):  # noqa: F811
     check(fmpq_mod.w16_gemm(layer, X, Wp, activation=act, bias=bias.float(), dtype=torch.float32), X, W, act, bias, gated=True)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,gated", [(300, 515, False), (67, 128, False), (1030, 260, False), (9, 5, False), (300, 2 * 516, True), (40, 2 * 66, True)])
+def test_rows_of_outputs_lie_anywhere(fmpq_mod, M, N, gated):  # noqa: F811
+    """Every start of the first row and step between rows, the residual in step with them or not: the same values, and nothing around them."""
+    import torch
+    K, dtype = 128, torch.bfloat16    # (K in one part: the sums are the same ones)
+    out_n = N // 2 if gated else N
+    X, W = matrix(M, K, dtype, M), matrix(N, K, dtype, N, 0, 1.5 / K ** 0.5)
+    layer = fmpq_mod.W16Layer(K, N, dtype, gated=gated)
+    Wp = fmpq_mod.w16_pack_weights(layer, W)
+    bias, residual = matrix(1, N, dtype, 5)[0], matrix(M, out_n, dtype, 6)
+    plain = fmpq_mod.w16_gemm(layer, X, Wp, bias=bias, activation="silu")
+    whole = fmpq_mod.w16_gemm(layer, X, Wp, bias=bias, activation="silu", residual=residual)
+    check(whole, X, W, "silu", bias, residual, gated=gated)
+
+    def rows_at(start, step):
+        flat = torch.full((start + M * (out_n + step) + 16,), 7.0, dtype=dtype, device="cuda")
+        return flat, flat[start:start + M * (out_n + step)].view(M, out_n + step)[:, :out_n]
+
+    for start in range(8):
+        for step in range(8):
+            for other in (0, 1, 4):    # the residual begins as many elements further
+                flat, Y = rows_at(start, step)
+                _, r = rows_at((start + other) % 8, step)
+                r.copy_(residual)
+                fmpq_mod.w16_gemm(layer, X, Wp, bias=bias, activation="silu", residual=r, Y=Y)
+                assert torch.equal(Y, whole), (start, step, other)
+                fmpq_mod.w16_gemm(layer, X, Wp, bias=bias, activation="silu", residual=r, Y=r)
+                assert torch.equal(r, whole), (start, step, other)
+                if other == 0:
+                    fmpq_mod.w16_gemm(layer, X, Wp, bias=bias, activation="silu", Y=Y)
+                    assert torch.equal(Y, plain), (start, step)
+                Y.fill_(7.0)
+                assert bool((flat == 7).all()), (start, step, other)
+
+
 # ---- groups -----------------------------------------------------------------------------------
 
 def group_sizes(kind, E):
