@@ -54,6 +54,7 @@ constexpr int kAhead = 2;         // chunks of a group whose residual is on its 
 constexpr int kAheadBytes = kGroups * kAhead * (128 + kChunk) * 16;
 constexpr int kBandTiles = 8;     // dense order: bands of 8 row tiles, weight tiles inside a band
 constexpr int kMaxSplits = 4;
+constexpr int kTileChoices = kMostRows / 32;
 constexpr int kBigBox = 64, kSmallBox = 16;   // rows of the two TMA boxes
 
 struct Params {
@@ -70,18 +71,21 @@ struct Params {
     int rows, N, out_n;  // out_n: columns of Y (gated: N / 2)
     int nb, pairs, experts, splits;
     int tile;            // rows of a unit, at most: a multiple of 32
+    int most_tile;       // groups, K not split: what the device may choose (0: tile)
     int cut, cuts;       // rows of the units that a dense product's rows are cut into, and units of this launch in one of them
     int tiles;           // those units, for a pair of weight tiles
     int first_cut;       // this launch's first
     int last_launch;     // the rest of a product, behind the launch of its full rounds
     int units;           // dense: of this launch
-    int stages, stage_bytes;
+    int others;          // bytes behind the operands' ring
     int32_t* status;
 };
 
 struct Tables {
     int32_t first_unit[kMaxFp8Experts + 1], start[kMaxFp8Experts], count[kMaxFp8Experts];
     uint16_t per[kMaxFp8Experts];   // rows of its units
+    int32_t units[kTileChoices], cost[kTileChoices];   // with tiles of 32, 64, ..
+    int32_t tile, stages, stage_bytes;   // the operands' ring, for units of `tile` rows
 };
 
 struct __align__(1024) Smem {
@@ -111,16 +115,69 @@ struct Unit {
     __device__ int columns(int i) const { return max(32, (part_rows(i) + 31) & ~31); }   // of the MMAs
 };
 
-// Rows of a unit where `count` rows are cut evenly into as few units as tiles of p.tile allow.
+// Rows of a unit where `count` rows are cut evenly into as few units as tiles of `tile` allow.
 __host__ __device__ inline int even_rows(int count, int tile) {
     const int tiles = (count + tile - 1) / tile;
     return tiles == 0 ? tile : ((count + tiles - 1) / tiles + 31) / 32 * 32;
 }
 __host__ __device__ inline int tiles_of(int count, int per) { return (count + per - 1) / per; }
 
+__host__ __device__ inline int stage_bytes_of(int tile) { return kTileBytes + tile / 2 * 128; }
+__host__ __device__ inline int stages_of(int tile, int others) {
+    const int stages = (kRingBytes - others) / stage_bytes_of(tile);
+    return stages < kMaxStages ? stages : kMaxStages;
+}
+__device__ __forceinline__ void set_ring(const Params& p, Tables& s, int tile) {
+    s.tile = tile;
+    s.stage_bytes = stage_bytes_of(tile);
+    s.stages = stages_of(tile, p.others);
+}
+// What a block of 64 channels costs a pair, in clk (shape_of has what it is made of).
+__host__ __device__ inline float block_of(int rows) { return rows > kPartRows ? 2.25f * rows : 400.0f + 0.65f * rows; }
+
+// The tile for the groups as they are (the host knows only their mean): all of a CTA's threads count the units that each tile would make, a
+// choice each and every 40th group; then the one with the least time by shape_of's count. All CTAs find the same. 6436 rows of 39 of 59
+// experts, 896 -> 4608: 115 to 82 us; 23784 of 60 of 66, 256 -> 10624: 225 to 216 (251 with an epilogue's 30 clk a row counted where they are
+// more than the blocks). It takes about 1 us, and few rows an expert gain nothing: 357 of 36 of 55, 1408 -> 128, 12.3 to 13.1.
+__device__ __forceinline__ void count_units(const Params& p, Tables& s, int lane) {
+    const int i = threadIdx.x % kTileChoices, tile = 32 * (i + 1);
+    int units = 0, cost = 0;
+    if (tile <= p.most_tile) {
+        for (int e = threadIdx.x / kTileChoices; e < p.experts; e += blockDim.x / kTileChoices) {
+            const int count = s.count[e];
+            if (count == 0) continue;
+            const int per = even_rows(count, tile), n = tiles_of(count, per);
+            units += n;
+            cost += n * static_cast<int>(block_of(per) + (per > kPartRows ? 14.0f * per / p.nb : 0.0f));
+        }
+    }
+    units += __shfl_xor_sync(0xFFFFFFFFu, units, 16);
+    cost += __shfl_xor_sync(0xFFFFFFFFu, cost, 16);
+    if (lane < kTileChoices) {
+        atomicAdd(&s.units[i], units);
+        atomicAdd(&s.cost[i], cost);
+    }
+}
+__device__ __forceinline__ int best_tile(const Params& p, const Tables& s, int clusters, int lane) {
+    const int i = lane % kTileChoices, tile = 32 * (i + 1), units = s.units[i];
+    float time = 3e38f;
+    if (units > 0) {
+        const int rounds = (units * p.pairs + clusters - 1) / clusters;
+        time = rounds * (static_cast<float>(s.cost[i]) / units) * p.nb + 14.0f * min(tile, kPartRows);
+    }
+    int best = tile;
+    for (int d = 8; d > 0; d >>= 1) {
+        const float t = __shfl_xor_sync(0xFFFFFFFFu, time, d);
+        const int b = __shfl_xor_sync(0xFFFFFFFFu, best, d);
+        if (t < time || (t == time && b < best)) time = t, best = b;
+    }
+    return best;
+}
+
 // Every thread calls it; a barrier must follow. Group bounds outside [0, rows] are cut to it, and a group begins no earlier than those
 // before it end: no row is in two, so there are never more units than the host counts with.
-__device__ __forceinline__ void fill_tables(const Params& p, Tables& s, int warp, int lane) {
+__device__ __forceinline__ void fill_tables(const Params& p, Tables& s, int clusters, int warp, int lane) {
+    if (threadIdx.x < kTileChoices) s.units[threadIdx.x] = 0, s.cost[threadIdx.x] = 0;
     for (int e = threadIdx.x; e < p.experts; e += blockDim.x) {
         const int64_t from = p.start[e], to = p.count != nullptr ? from + p.count[e] : p.start[e + 1];
         const int a = static_cast<int>(min(max(from, INT64_C(0)), static_cast<int64_t>(p.rows)));
@@ -129,7 +186,13 @@ __device__ __forceinline__ void fill_tables(const Params& p, Tables& s, int warp
         s.count[e] = max(0, b - a);
     }
     __syncthreads();
+    if (p.most_tile > 0) {
+        count_units(p, s, lane);
+        __syncthreads();
+    }
     if (warp != 3) return;
+    const int tile = p.most_tile > 0 ? best_tile(p, s, clusters, lane) : p.tile;
+    if (lane == 0) set_ring(p, s, tile);
     // lane l: the run of experts [l * run, l * run + run)
     const int run = (p.experts + 31) / 32, begin = lane * run, end = min(begin + run, p.experts);
     int last = 0;   // where the groups so far end
@@ -147,7 +210,7 @@ __device__ __forceinline__ void fill_tables(const Params& p, Tables& s, int warp
         s.start[e] += cut;
         s.count[e] -= cut;
         if (s.count[e] > 0) last = max(last, s.start[e] + s.count[e]);
-        s.per[e] = static_cast<uint16_t>(even_rows(s.count[e], p.tile));
+        s.per[e] = static_cast<uint16_t>(even_rows(s.count[e], tile));
         const int units = tiles_of(s.count[e], s.per[e]) * p.pairs;
         s.first_unit[e] = sum;   // (of this lane's)
         sum += units;
@@ -226,6 +289,7 @@ struct Place {
 __device__ __forceinline__ void producer(const Params& p, const CUtensorMap* big, const CUtensorMap* small, Smem& s, uint8_t* ring,
                                          const Place& at, volatile int* abort_flag) {
     const int units = unit_count(p, s);
+    const uint32_t stages = s.tables.stages, stage_bytes = s.tables.stage_bytes;
     uint32_t it = 0, st = 0, phase = 1;
     bool ok = true;
     for (int u = at.cluster; ok && u < units; u += at.clusters) {
@@ -240,7 +304,7 @@ __device__ __forceinline__ void producer(const Params& p, const CUtensorMap* big
             if (!ok) break;
             if (elect_one()) {
                 uint64_t* bar = &s.full[st];
-                uint8_t* to = ring + st * p.stage_bytes;
+                uint8_t* to = ring + st * stage_bytes;
                 dev::mbar_arrive_expect_tx(bar, kTileBytes + (half0 + half1) * 128u);
                 dev::bulk_g2s(to, w, kTileBytes, bar);
                 to += kTileBytes;
@@ -254,7 +318,7 @@ __device__ __forceinline__ void producer(const Params& p, const CUtensorMap* big
                 rows_to(half1, from1);
             }
             __syncwarp();
-            if (++st == static_cast<uint32_t>(p.stages)) {
+            if (++st == stages) {
                 st = 0;
                 phase ^= 1;
             }
@@ -263,7 +327,6 @@ __device__ __forceinline__ void producer(const Params& p, const CUtensorMap* big
     if (!ok && elect_one()) fail(p, abort_flag);
     // the copies in flight must land before the CTA's shared memory is given up (after an abort the even CTA's
     // readiness may never be complete: a short bound, far longer than a copy)
-    const uint32_t stages = p.stages;
     for (uint32_t k = 0; k < stages && k < it; ++k) {
         const uint32_t i = it - 1 - k;
         dev::mbar_wait(&s.full[i % stages], (i / stages) & 1, nullptr, ok ? dev::kMaxPolls : 1u << 16);
@@ -296,6 +359,7 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar, uint32_t leader) {
 
 __device__ __forceinline__ void mma_issuer(const Params& p, Smem& s, uint8_t* ring, const Place& at, uint32_t tmem,
                                            volatile int* abort_flag) {
+    const uint32_t stages = s.tables.stages, stage_bytes = s.tables.stage_bytes;
     const int units = unit_count(p, s);
     const uint32_t remote = dev::mapa(&s.full[0], at.leader);
     const uint64_t w0 = dev::sdesc_k_sw128(dev::smem_u32(ring));
@@ -323,7 +387,7 @@ __device__ __forceinline__ void mma_issuer(const Params& p, Smem& s, uint8_t* ri
             } else {
                 dev::tc_fence_after();
                 // (a descriptor's address field counts 16 bytes)
-                const uint64_t ad = w0 + st * static_cast<uint32_t>(p.stage_bytes >> 4), bd = ad + kTileBytes / 16;
+                const uint64_t ad = w0 + st * (stage_bytes >> 4), bd = ad + kTileBytes / 16;
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) mma_16_pair(d0, ad + 2 * k, bd + 2 * k, idesc0, b > t.b0 || k > 0 ? 1u : 0u);
@@ -338,7 +402,7 @@ __device__ __forceinline__ void mma_issuer(const Params& p, Smem& s, uint8_t* ri
                 }
             }
             __syncwarp();
-            if (++st == static_cast<uint32_t>(p.stages)) {
+            if (++st == stages) {
                 st = 0;
                 phase ^= 1;
             }
@@ -790,7 +854,7 @@ w16_kernel(const Params p, const __grid_constant__ CUtensorMap big, const __grid
     uint8_t* head = smem_raw + ((1024u - (dev::smem_u32(smem_raw) & 1023u)) & 1023u);
     Smem& s = *reinterpret_cast<Smem*>(head);
     uint8_t* ring = head + kHeadBytes;
-    float4* others = reinterpret_cast<float4*>(ring + p.stages * p.stage_bytes);
+    float4* others = reinterpret_cast<float4*>(ring + kRingBytes - p.others);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     Place at;
     at.cluster_rank = dev::cluster_ctarank();
@@ -825,7 +889,8 @@ w16_kernel(const Params p, const __grid_constant__ CUtensorMap big, const __grid
         dev::pdl_wait();
         dev::pdl_launch_dependents();
     }
-    if (p.start != nullptr) fill_tables(p, s.tables, warp, lane);
+    if (p.start != nullptr) fill_tables(p, s.tables, at.clusters, warp, lane);
+    else if (threadIdx.x == 0) set_ring(p, s.tables, p.tile);
     dev::tc_fence_before();
     __syncthreads();
     dev::cluster_sync();   // every CTA's barriers and TMEM exist before any traffic between them
@@ -966,26 +1031,23 @@ struct Rest {
     double time;
 };
 struct Shape {
-    int tile, splits, grid, stages, stage_bytes;
+    int tile, splits, grid, stages, others, most_tile;
     Rest rest;
 };
 
 // (`ahead`: of the residual, where K is not split)
 Shape with_ring(int tile, int splits, int64_t units, int clusters, int ahead) {
-    Shape s{tile, splits, 0, 0, 0, {}};
+    Shape s{tile, splits, 0, 0, 0, 0, {}};
     s.grid = static_cast<int>(units < clusters ? units : clusters) * 2 * splits;
-    s.stage_bytes = kTileBytes + tile / 2 * 128;
-    const int others = splits > 1 ? (splits - 1) * tile * 128 * 4 : ahead;
-    s.stages = (kRingBytes - others) / s.stage_bytes;
-    if (s.stages > kMaxStages) s.stages = kMaxStages;
+    s.others = splits > 1 ? (splits - 1) * tile * 128 * 4 : ahead;
+    s.stages = stages_of(tile, s.others);
     return s;
 }
 
 // The best such launch for `units` of `per` rows, all of it resident at once. It starts under the full rounds' end and still costs about
 // 6000 clk, the exchange 1500 more: 300 x 4096 -> 20480 62 to 55 us, 1 x 8192 -> 28672 82 to 77, 2048 x 4096 -> 12288 127 to 123; counted at
 // 1500, 300 x 1024 -> 20000 lost 3 of 24 and 520 x 4096 -> 11008 3 of 48.
-template <typename F>
-Rest rest_of(const w16_layer& L, int units, int per, int ahead, const F& block_of) {
+Rest rest_of(const w16_layer& L, int units, int per, int ahead) {
     Rest best{0, 0, 0, 0, 1e30};
     for (int splits = 1; splits <= kMaxSplits; splits *= 2) {
         if (splits > 1 && L.nb < 4 * splits) break;
@@ -1020,7 +1082,6 @@ Shape shape_of(const w16_layer& L, const W16Args& a, int ahead) {
     // the experts' loads are known on the device only: every one in use is taken to have the mean, and a sixth more for the spread
     // (1554 rows of 10 uneven experts, 1404 -> 2012, in tiles of 64, 128, 192 and 256: 37, 28, 32 and 36 us)
     const int used = grouped ? (L.experts < rows ? L.experts : rows) : 1, load = grouped ? (7 * rows / used + 5) / 6 : rows;
-    const auto block_of = [](int per) { return per > kPartRows ? 2.25 * per : 400.0 + 0.65 * per; };
     Shape best{};
     double least = 0.0;
     for (int splits = 1; splits <= kMaxSplits; splits *= 2) {
@@ -1037,7 +1098,7 @@ Shape shape_of(const w16_layer& L, const W16Args& a, int ahead) {
             const double round = L.nb * block_of(per) + (per > kPartRows ? 14.0 * per : 0.0);
             double time = splits > 1 ? (L.nb + splits - 1) / splits * block_of(per) + 1500.0 + 14.0 * per : rounds * round + 14.0 * per;
             if (!grouped && splits == 1 && rounds > 1 && units % clusters != 0) {
-                const Rest r = rest_of(L, static_cast<int>(units % clusters), per, ahead, block_of);
+                const Rest r = rest_of(L, static_cast<int>(units % clusters), per, ahead);
                 if (r.time < round) {
                     s.rest = r;
                     time += r.time - round;
@@ -1048,6 +1109,12 @@ Shape shape_of(const w16_layer& L, const W16Args& a, int ahead) {
                 least = time;
             }
         }
+    }
+    if (grouped && best.splits == 1 && rows >= 24 * used) {   // the device chooses the tile
+        for (best.most_tile = kMostRows; stages_of(best.most_tile, best.others) < 4;) best.most_tile -= 32;
+        const int64_t most = most_units(L, used, rows, 32);
+        const int clusters = resident_clusters(L, 1);
+        best.grid = static_cast<int>(most < clusters ? most : clusters) * 2;
     }
     return best;
 }
@@ -1090,6 +1157,7 @@ cudaError_t launch_w16_gemm(const w16_layer& L, const W16Args& a, cudaStream_t s
     if (!w16::encode_rows(&big, a, L, w16::kBigBox) || !w16::encode_rows(&small, a, L, w16::kSmallBox)) return cudaErrorInvalidValue;
     auto launch = [&](const w16::Shape& s) {
         p.tile = s.tile;
+        p.most_tile = s.most_tile;
         p.splits = s.splits;
         const bool whole = unsplit && s.splits == 1;
         auto form = [&](auto gated) {
@@ -1099,8 +1167,7 @@ cudaError_t launch_w16_gemm(const w16_layer& L, const W16Args& a, cudaStream_t s
         auto fn = L.gated ? form(std::true_type{}) : form(std::false_type{});
         const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), w16::kSmemBytes);
         if (e != cudaSuccess) return e;
-        p.stages = s.stages;
-        p.stage_bytes = s.stage_bytes;
+        p.others = s.others;
         cudaLaunchAttribute attr[2];
         const cudaLaunchConfig_t cfg = w16::config(s.grid, 2 * s.splits, w16::kSmemBytes, stream, attr);
         return cudaLaunchKernelEx(&cfg, fn, p, big, small);
