@@ -1079,8 +1079,9 @@ int64_t most_units(const w16_layer& L, int used, int rows, int tile) {
 Shape shape_of(const w16_layer& L, const W16Args& a, int ahead) {
     const bool grouped = a.start != nullptr;
     const int rows = static_cast<int>(a.rows);
-    // the experts' loads are known on the device only: every one in use is taken to have the mean, and a sixth more for the spread
-    // (1554 rows of 10 uneven experts, 1404 -> 2012, in tiles of 64, 128, 192 and 256: 37, 28, 32 and 36 us)
+    // the experts' loads are known on the device only: every one in use is taken to have the mean, and a sixth more for the spread. From 24
+    // rows an expert on the device chooses the tile (count_units; 1554 rows of 10 uneven experts, 1404 -> 2012, in tiles of 64, 128, 192 and 256:
+    // 37, 28, 32 and 36 us), and this says only whether K is split.
     const int used = grouped ? (L.experts < rows ? L.experts : rows) : 1, load = grouped ? (7 * rows / used + 5) / 6 : rows;
     Shape best{};
     double least = 0.0;
