@@ -48,8 +48,8 @@ constexpr int kPartRows = 256;    // of a part: the N side of an MMA, and an acc
 constexpr int kMostRows = 512;    // of a unit: two parts
 constexpr int kChunk = 8;         // rows of X that a group turns at a time
 constexpr int kStageLd = 136;     // floats of a row there: 128 outputs, and up to 7 in front of them
-// Epilogues: any outputs and any split of K; put_out_whole, without a residual and with one.
-enum { kAnyForm, kWholeBare, kWholeAdded };
+// Epilogues: any outputs and any split of K; put_out_whole, without a residual, with one, and for FP32.
+enum { kAnyForm, kWholeBare, kWholeAdded, kWholeF32 };
 constexpr int kAhead = 2;         // chunks of a group whose residual is on its way (put_out_whole), 16 bytes a thread and a row's end
 constexpr int kAheadBytes = kGroups * kAhead * (128 + kChunk) * 16;
 constexpr int kBandTiles = 8;     // dense order: bands of 8 row tiles, weight tiles inside a band
@@ -549,30 +549,33 @@ struct Piece {
     __device__ __forceinline__ bool has(int c) const { return column(c) < columns; }
 };
 // Elements between the 16-byte boundary before a row's outputs and them.
-template <bool kGated>
+template <bool kNone>   // the rows are known to start on boundaries
 __device__ __forceinline__ int row_past(const Params& p, int64_t row) {
     const uint32_t first = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.Y) >> 1) + static_cast<uint32_t>(row) * static_cast<uint32_t>(p.ldy);
-    return kGated ? 0 : static_cast<int>(first & 7u);
+    return kNone ? 0 : static_cast<int>(first & 7u);
 }
 
-// The epilogue's chunks of a part: outputs of 16 bits, K not split. What costs time here is a group's chain through a chunk (TMEM, shared
+// The epilogue's chunks of a part: outputs of 16 bits (or FP32), K not split. What costs time here is a group's chain through a chunk (TMEM, shared
 // memory, barrier, output) and the size of the loop's code, so the rows are shifted to their place in memory as they are turned, the residual
 // of a thread's next two rows is on its way by cp.async (no register waits for it), and this is a kernel of its own, with a residual or
 // without. 8192 x 512 -> 4096 bf16: plain 33 us, with bias, silu and residual 51 (by the form below, with a bias for each of a piece's
 // columns, 49 and 91); 4096 x 1024 -> 4096 31 and 36 (35 and 53), -> 4095 35 and 44 (57 and 88). No faster: the residual 3 or 4
 // rows ahead, or its lines sent for to the L2 before; two chunks a turn of the loop (8192 x 512: 51 and 79); one kernel for both (38 and 55).
-template <bool kGated, bool kAdded, int kW, int kCols, typename Wait>
+// FP32 outputs on 16-byte boundaries without a residual go the same way (8192 x 512 -> 4096 52 to 45, 32768 x 512 -> 2000 in 64 groups 104 to 92).
+template <bool kGated, int kForm, int kW, int kCols, typename Wait>
 __device__ __forceinline__ void put_out_whole(const Params& p, float (*turn)[kChunk][kStageLd], uint8_t* residuals, uint32_t from_tmem, int g, int tid, int64_t row0, int rows,
                                               int n0, const Piece<kW, kCols>& piece, float bias, const Wait& wait, int& buffer) {
+    constexpr bool kAdded = kForm == kWholeAdded, kF32 = kForm == kWholeF32;
     constexpr int kPieces = kCols / kW;
     const int chunks = (rows + kChunk - 1) / kChunk, sub = tid / kPieces, i = tid % kPieces;
     // of every 32 packed rows of a gated layer, 16 are gates and 16 the ups of the same hidden channels
     const int place = kGated ? 32 * (kW * i >> 4) + (kW * i & 15) : kW * i;
     int to[kChunk];
 #pragma unroll
-    for (int j = 0; j < kChunk; ++j) to[j] = j * kStageLd + tid + row_past<kGated>(p, row0 + j);
+    for (int j = 0; j < kChunk; ++j) to[j] = j * kStageLd + tid + row_past<kGated || kF32>(p, row0 + j);
     int64_t row = row0 + kChunk * g + sub;
-    uint16_t* y = static_cast<uint16_t*>(p.Y) + row * p.ldy + n0;
+    using Out = std::conditional_t<kF32, float, uint16_t>;
+    Out* y = static_cast<Out*>(p.Y) + row * p.ldy + n0;
     const uint16_t* r = static_cast<const uint16_t*>(p.e.residual) + row * p.e.ldr + n0;
     const int64_t y_step = p.ldy * (kGroups * kChunk), r_step = p.e.ldr * (kGroups * kChunk);
     int left = rows - kChunk * g - sub;   // this thread's row of a chunk exists where more than 0 are left
@@ -648,28 +651,39 @@ __device__ __forceinline__ void put_out_whole(const Params& p, float (*turn)[kCh
                     f[2 * c + 1] += a.y;
                 }
             }
-            uint32_t o[kW / 2];
+            if constexpr (kF32) {
+                if (piece.whole) {
 #pragma unroll
-            for (int i = 0; i < kW / 2; ++i) {
-                if (bf16) {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-                    o[i] = *reinterpret_cast<const uint32_t*>(&h);
+                    for (int i = 0; i < kW; i += 4) *reinterpret_cast<float4*>(y + piece.first + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
                 } else {
-                    const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-                    o[i] = *reinterpret_cast<const uint32_t*>(&h);
-                }
-            }
-            if (!kGated && piece.first == -4 && piece.columns == kCols) {
-                *reinterpret_cast<uint2*>(y) = make_uint2(o[kW / 2 - 2], o[kW / 2 - 1]);
-                *reinterpret_cast<uint2*>(y + kCols - 4) = make_uint2(o[0], o[1]);
-            } else if (!piece.whole) {
 #pragma unroll
-                for (int c = 0; c < kW; ++c)
-                    if (piece.has(c)) y[piece.column(c)] = static_cast<uint16_t>(o[c >> 1] >> (16 * (c & 1)));
-            } else if constexpr (kW == 8) {
-                *reinterpret_cast<uint4*>(y + piece.first) = make_uint4(o[0], o[1], o[2], o[3]);
+                    for (int c = 0; c < kW; ++c)
+                        if (piece.has(c)) y[piece.column(c)] = f[c];
+                }
             } else {
-                *reinterpret_cast<uint2*>(y + piece.first) = make_uint2(o[0], o[1]);
+                uint32_t o[kW / 2];
+#pragma unroll
+                for (int i = 0; i < kW / 2; ++i) {
+                    if (bf16) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+                        o[i] = *reinterpret_cast<const uint32_t*>(&h);
+                    } else {
+                        const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+                        o[i] = *reinterpret_cast<const uint32_t*>(&h);
+                    }
+                }
+                if (!kGated && piece.first == -4 && piece.columns == kCols) {
+                    *reinterpret_cast<uint2*>(y) = make_uint2(o[kW / 2 - 2], o[kW / 2 - 1]);
+                    *reinterpret_cast<uint2*>(y + kCols - 4) = make_uint2(o[0], o[1]);
+                } else if (!piece.whole) {
+#pragma unroll
+                    for (int c = 0; c < kW; ++c)
+                        if (piece.has(c)) y[piece.column(c)] = static_cast<uint16_t>(o[c >> 1] >> (16 * (c & 1)));
+                } else if constexpr (kW == 8) {
+                    *reinterpret_cast<uint4*>(y + piece.first) = make_uint4(o[0], o[1], o[2], o[3]);
+                } else {
+                    *reinterpret_cast<uint2*>(y + piece.first) = make_uint2(o[0], o[1]);
+                }
             }
         }
         if (kAdded) ask(held, left - kAhead * kGroups * kChunk);
@@ -721,7 +735,7 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* other
         const uint32_t acc = np & 1;
         const int n0 = (2 * t.pair + static_cast<int>(at.rank)) * kCols, n = n0 + col;
         const int columns = p.out_n - n;
-        const Piece<kW, kCols> piece(tid % kPieces, kWhole ? row_past<kGated>(p, t.row0 + tid / kPieces) : 0, min(kCols, p.out_n - n0));
+        const Piece<kW, kCols> piece(tid % kPieces, kWhole ? row_past<kGated || kForm == kWholeF32>(p, t.row0 + tid / kPieces) : 0, min(kCols, p.out_n - n0));
         const int chunks = (t.rows + kChunk - 1) / kChunk;
         float bias = -0.0f;   // of this thread's packed row: added to its sums (-0: nothing is)
         if (first && p.e.bias != nullptr) {
@@ -747,7 +761,7 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* other
         if (!kWhole) wait();
 
         if constexpr (kWhole) {
-            put_out_whole<kGated, kForm == kWholeAdded>(p, s.turn[g], reinterpret_cast<uint8_t*>(others), from_tmem, g, tid, t.row0, t.rows, n0, piece, bias, wait, buffer);
+            put_out_whole<kGated, kForm>(p, s.turn[g], reinterpret_cast<uint8_t*>(others), from_tmem, g, tid, t.row0, t.rows, n0, piece, bias, wait, buffer);
         } else if (!first) {   // to the first pair's CTA of this rank
             const uint32_t to = dev::mapa(others, at.rank) + other_sums(p, at.split, 0, tid) * 16u;
             for (int c = g; c < chunks; c += kGroups) {
@@ -1161,8 +1175,10 @@ cudaError_t launch_w16_gemm(const w16_layer& L, const W16Args& a, cudaStream_t s
         p.most_tile = s.most_tile;
         p.splits = s.splits;
         const bool whole = unsplit && s.splits == 1;
+        // (FP32: on 16-byte boundaries)
+        const bool whole32 = p.f32 && s.splits == 1 && p.vec == 8 && p.e.residual == nullptr;
         auto form = [&](auto gated) {
-            return !whole ? w16::w16_kernel<gated.value, w16::kAnyForm>
+            return whole32 ? w16::w16_kernel<gated.value, w16::kWholeF32> : !whole ? w16::w16_kernel<gated.value, w16::kAnyForm>
                           : p.e.residual == nullptr ? w16::w16_kernel<gated.value, w16::kWholeBare> : w16::w16_kernel<gated.value, w16::kWholeAdded>;
         };
         auto fn = L.gated ? form(std::true_type{}) : form(std::false_type{});

@@ -145,6 +145,13 @@ def test_rows_of_outputs_lie_anywhere(fmpq_mod, M, N, gated):  # noqa: F811
                     assert torch.equal(Y, plain), (start, step)
                 Y.fill_(7.0)
                 assert bool((flat == 7).all()), (start, step, other)
+    bias = bias.float()
+    ref = fmpq_mod.w16_gemm(layer, X, Wp, bias=bias, activation="silu", Y=torch.empty(M, out_n + 9, device="cuda")[:, 1:out_n + 1])
+    check(ref, X, W, "silu", bias, gated=gated)
+    for step in range(8):    # FP32
+        flat = torch.full((M, out_n + step), 7.0, device="cuda")
+        assert torch.equal(fmpq_mod.w16_gemm(layer, X, Wp, bias=bias, activation="silu", Y=flat[:, :out_n]), ref), step
+        assert bool((flat[:, out_n:] == 7).all()), step
 
 
 # ---- groups -----------------------------------------------------------------------------------
