@@ -162,7 +162,7 @@ def test_parts_alone(fmpq_mod, M, K, case):  # noqa: F811
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M,K", [(2, 1024), (400, 1024), (2, 20000)])
+@pytest.mark.parametrize("M,K", [(2, 1024), (400, 1024), (2, 20000), (400, 2048), (320, 17000)])
 def test_any_alignment_gives_the_same(fmpq_mod, M, K):  # noqa: F811
     """Weights, rows and outputs that start 2, 8 and 16 bytes into their buffers."""
     import torch
@@ -189,7 +189,7 @@ def test_any_alignment_gives_the_same(fmpq_mod, M, K):  # noqa: F811
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M,K", [(1, 512), (333, 1024), (2, 17000), (700, 1003)])
+@pytest.mark.parametrize("M,K", [(1, 512), (333, 1024), (2, 17000), (700, 1003), (700, 2003), (400, 9001)])
 def test_in_place(fmpq_mod, M, K):  # noqa: F811
     """R in the residual's buffer and Y in X's, or R in X's: the same values as in buffers of their own."""
     import torch
@@ -205,10 +205,9 @@ def test_in_place(fmpq_mod, M, K):  # noqa: F811
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("K", [256, 4096, 17000])
-def test_zeros_nan_and_infinity_stay_in_their_rows(fmpq_mod, K):  # noqa: F811
+@pytest.mark.parametrize("M,K", [(9, 256), (9, 4096), (9, 17000), (400, 4096), (400, 2003), (330, 17003)])
+def test_zeros_nan_and_infinity_stay_in_their_rows(fmpq_mod, M, K):  # noqa: F811
     import torch
-    M = 9
     X, residual = draw(M, K, torch.bfloat16, 1), draw(M, K, torch.bfloat16, 2)
     layer = fmpq_mod.Fp8Layer(K, 16)
     Y = torch.empty_like(X)
@@ -219,7 +218,7 @@ def test_zeros_nan_and_infinity_stay_in_their_rows(fmpq_mod, K):  # noqa: F811
     X[3, K - 1] = float("nan")
     residual[5, 0] = float("inf")
     out = fmpq_mod.block_norm(X, residual, Y=Z, **kw)
-    rest = [0, 2, 4, 6, 7, 8]
+    rest = [m for m in range(M) if m not in (1, 3, 5)]
     assert torch.equal(Z[rest], Y[rest]) and torch.equal(out.R[rest], clean.R[rest])
     assert torch.equal(out.a_scales[:, rest], clean.a_scales[:, rest]) and torch.equal(out.A_packed[:, rest], clean.A_packed[:, rest])
     assert bool((Z[1] == 0).all()) and bool((out.R[1] == 0).all()) and bool((out.a_scales[:, 1] == 0).all())
