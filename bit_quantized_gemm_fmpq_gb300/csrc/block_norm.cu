@@ -173,7 +173,16 @@ __device__ __forceinline__ void square8(const BlockNormArgs& p, float2& sum, con
         sum = dev::ffma2(d, d, sum);
     }
 }
-__device__ __forceinline__ float inverse(const BlockNormArgs& p, float mean_square) { return rsqrtf(mean_square + p.eps); }
+// 1 / sqrt(mean square + eps), rounded once: all of a row's values carry its error, and rsqrtf, off by up to two steps, flips twice as many E4M3
+// codes at their borders. One step of Newton's iteration from rsqrtf's y, y + y / 2 (1 - d y^2), d y in two parts so that the residual is
+// good to 2^-46: the result is within 2^-20 of a step of the nearest value's half step (of all 2^31 positive d, 257 next to a tie go to its other side). Both norms
+// at 4096 x 8192: 66.4 us; with __frsqrt_rn, which has no such exceptions and three times the instructions, 67.4; with rsqrtf alone 65.6.
+__device__ __forceinline__ float inverse(const BlockNormArgs& p, float mean_square) {
+    const float d = mean_square + p.eps, y = rsqrtf(d);
+    const float h = d * y, l = fmaf(d, y, -h);
+    const float rest = fmaf(-l, y, fmaf(-h, y, 1.0f));
+    return d < INFINITY ? fmaf(0.5f * y, rest, y) : y;   // (of infinity 0, of NaN NaN)
+}
 
 template <typename T, int kLie, int kNorm>
 __device__ __forceinline__ void scale8(const BlockNormArgs& p, V8& v, float mean, float inv, const void* w, const void* b, int k) {
