@@ -1013,7 +1013,8 @@ def block_norm(X, residual=None, kind: str = "rms", eps: float = 1e-6, post_norm
 
     Returns (R, Y, A_packed, a_scales). R is r (None where r is X itself and no R is passed). With a layer y comes as the
     codes and scales that fp8_gemm takes for that layer, and as Y only where a Y is passed; without one it comes as Y.
-    R may be residual or X, Y may be X or residual."""
+    R may be residual or X, Y may be X or residual. A NaN makes its row's norm NaN, and so does an infinity in a layer norm; in an RMS norm an
+    infinity's own channel is NaN and the row's others are 0 times their weight, plus their bias."""
     import torch
     code = _rows16(X, "X")
     M, K = X.shape

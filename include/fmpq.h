@@ -528,8 +528,10 @@ FMPQ_API fmpq_status fp8_quantize_gemm_epilogue(const fp8_layer* layer, const vo
  *   norm(v; w, b)_k = (v_k - c) / sqrt(mean((v - c)^2) + eps) * (weight_offset + w_k) + b_k,
  *   c = 0 (FMPQ_NORM_RMS) or mean(v) (FMPQ_NORM_LAYER); no weight: times 1; no bias: + 0
  * All in FP32. y is written in 16 bits (Y), as the E4M3 codes and scales that fp8_quantize would
- * make of the FP32 y (A_packed, a_scales), or both. A NaN or an infinity makes its own row's y NaN; squares past FP32's
- * range, of rows beyond 1e19, make y 0. Forward only.
+ * make of the FP32 y (A_packed, a_scales), or both. A NaN makes its own row's norm NaN, and so does an infinity in a layer
+ * norm. In an RMS norm an infinity makes the mean square infinite, as squares past FP32's range do (of rows beyond 1e19): the infinite
+ * channels, inf / inf, are NaN, and every other channel of the row is 0 times its weight, plus its bias. (A norm of X that does so
+ * leaves NaN in r, which makes y's row NaN.) A block of y with a NaN has the scale NaN. No row reaches another. Forward only.
  * ====================================================================================== */
 
 enum { FMPQ_NORM_RMS = 0, FMPQ_NORM_LAYER = 1 };
