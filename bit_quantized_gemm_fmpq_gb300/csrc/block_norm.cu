@@ -9,6 +9,7 @@
 // Everything between the reads of X and residual and the writes is FP32. A row is read once and kept in the
 // registers of one CTA (8 channels a vector, kV vectors a thread); a layer norm's variance is the mean of the squared
 // differences, a second reduction over those registers.
+#include <climits>
 #include <initializer_list>
 #include <type_traits>
 
@@ -390,11 +391,35 @@ __device__ __forceinline__ void param_at(const void* p, uint32_t k, V8& v) {
     }
 }
 
-template <typename T, typename P, int kNorm, int kV, int kLie>
-__global__ void __launch_bounds__(1024) block_norm_stream_kernel(const BlockNormArgs p, int stages) {
+// The end of a CTA of the kernel below that gave up a row: its rows from there on become NaN, and the copies under way land (a short bound, far longer
+// than a copy). Not inlined: the kernel would take registers for it (777 x 2868, a layer norm: 7.5 us in place of 5.9).
+template <typename T>
+__device__ __noinline__ void give_up(const BlockNormArgs& p, int from, uint64_t* landed, int stages) {
+    const int rows = static_cast<int>(p.M), step = static_cast<int>(gridDim.x);
+    const float nan = __int_as_float(0x7FFFFFFF);
+    for (int64_t m = from; m < rows; m += step) {
+        for (int c = threadIdx.x; c < p.K; c += blockDim.x) {
+            if (p.R != nullptr) store1(static_cast<T*>(p.R) + m * p.ldo + c, nan);
+            if (p.Y != nullptr) store1(static_cast<T*>(p.Y) + m * p.ldy + c, nan);
+            if (p.A != nullptr && c < p.nb) p.a_scales[c * p.sstride + m] = nan;
+        }
+    }
+    if (threadIdx.x != 0) return;
+    int n = (from - static_cast<int>(blockIdx.x)) / step;   // the row's number among the CTA's: its slot, and those behind it
+    for (int i = 0; i < stages && blockIdx.x + static_cast<int64_t>(n) * step < rows; ++i, ++n)
+        dev::mbar_wait(&landed[n % stages], (n / stages) & 1, nullptr, 1u << 16);
+}
+
+// A copy lands, or its wait gives up after about a second, a thread's last wait then. Threads may disagree, so the first row that any of them gave up counts: no
+// slot is filled again from its barrier on, and at the end the CTA's rows from there on are made NaN and the copies under way land.
+// kTest: the row `withheld` gets no copy, and waits end after `polls`.
+template <typename T, typename P, int kNorm, int kV, int kLie, bool kTest = false>
+__global__ void __launch_bounds__(1024) block_norm_stream_kernel(const __grid_constant__ BlockNormArgs p, int stages) {
     extern __shared__ __align__(128) uint8_t ring[];   // [stage][X's row, then the residual's]
     __shared__ Sums sums;
     __shared__ uint64_t landed[kMostStages];
+    __shared__ int given_up;   // the first such row
+    const uint32_t polls = kTest ? p.polls : dev::kMaxPolls;
     // (a row of a slot has room for a row at any place in its pieces, and for the piece behind its last vector's)
     const uint32_t row_bytes = ring_row_bytes(p.K), slot_bytes = p.residual != nullptr ? 2 * row_bytes : row_bytes;
     const int rows = static_cast<int>(p.M), step = static_cast<int>(gridDim.x);
@@ -405,11 +430,12 @@ __global__ void __launch_bounds__(1024) block_norm_stream_kernel(const BlockNorm
         auto pieces = [&](uint32_t off) { return ((off + static_cast<uint32_t>(p.K)) * 2 + 15u) & ~15u; };
         const uint32_t x_bytes = pieces(x_off), r_bytes = p.residual != nullptr ? pieces(r_off) : 0u;
         dev::mbar_arrive_expect_tx(&landed[stage], x_bytes + r_bytes);
-        dev::bulk_g2s(ring + stage * slot_bytes, x - x_off, x_bytes, &landed[stage]);
+        if (!kTest || m != p.withheld) dev::bulk_g2s(ring + stage * slot_bytes, x - x_off, x_bytes, &landed[stage]);
         if (p.residual != nullptr) dev::bulk_g2s(ring + stage * slot_bytes + row_bytes, r - r_off, r_bytes, &landed[stage]);
     };
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i) dev::mbar_init(&landed[i], 1);
+        given_up = INT_MAX;
         dev::fence_barrier_init();
     }
     dev::pdl_wait();
@@ -434,9 +460,12 @@ __global__ void __launch_bounds__(1024) block_norm_stream_kernel(const BlockNorm
     const bool single = blockDim.x == 32;
     int turn = 0, stage = 0;
     uint32_t phase = 0;
+    bool lost = false;   // this thread gave up a row
     for (int m = static_cast<int>(blockIdx.x); m < rows; m += step) {
-        // (a copy that this CTA issued lands; should one not, within about a second, its row comes out NaN)
-        const bool there = dev::mbar_wait(&landed[stage], phase, nullptr);
+        if (!lost && !dev::mbar_wait(&landed[stage], phase, nullptr, polls)) {
+            lost = true;
+            atomicMin(&given_up, m);
+        }
         const uint8_t* x = ring + stage * slot_bytes;
         // what a row's last vector has past K (kAny) is 0
         auto cut = [&](uint32_t k, V8& v) {
@@ -459,8 +488,8 @@ __global__ void __launch_bounds__(1024) block_norm_stream_kernel(const BlockNorm
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) v[i][c] = both(there ? 0.0f : __int_as_float(0x7FFFFFFF));
-            if (in[i] && there) from_ring(x, elements_past(static_cast<const T*>(p.X) + m * p.ldx), k[i], v[i]);
+            for (int c = 0; c < 4; ++c) v[i][c] = both(lost ? __int_as_float(0x7FFFFFFF) : 0.0f);
+            if (in[i] && !lost) from_ring(x, elements_past(static_cast<const T*>(p.X) + m * p.ldx), k[i], v[i]);
         }
         float mean = 0.0f, inv;
         // v = (v - mean) * inv * w + b
@@ -528,8 +557,9 @@ __global__ void __launch_bounds__(1024) block_norm_stream_kernel(const BlockNorm
         }
         if (p.pre_norm) statistics<kLie, kNorm>(p, v, sums, turn, mean, inv);
         if (!p.pre_norm || single) __syncthreads();   // (else the statistics' own barrier)
-        // every thread has read the row
-        if (threadIdx.x == 0 && m + static_cast<int64_t>(stages) * step < rows) load(m + stages * step, stage);
+        // every thread has read the row (or given it up)
+        if (threadIdx.x == 0 && m + static_cast<int64_t>(stages) * step < rows && *static_cast<volatile int*>(&given_up) > m)
+            load(m + stages * step, stage);
         if (++stage == stages) {
             stage = 0;
             phase ^= 1;
@@ -556,6 +586,8 @@ __global__ void __launch_bounds__(1024) block_norm_stream_kernel(const BlockNorm
             }
         }
     }
+    __syncthreads();
+    if (given_up != INT_MAX) give_up<T>(p, given_up, landed, stages);
 }
 
 // Threads that a row of nb blocks takes at `per` vectors each.
@@ -581,6 +613,14 @@ cudaError_t block_norm_stream(const BlockNormArgs& p, bool whole, int num_sms, c
         return per == 2 ? of(norm, integral_constant<int, 2>{}) : per == 3 ? of(norm, integral_constant<int, 3>{}) : of(norm, integral_constant<int, 4>{});
     };
     auto fn = p.layer_norm ? at(integral_constant<int, kLayer>{}) : at(integral_constant<int, kRms>{});
+    if (p.polls != 0) {
+        if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+            if (!whole || p.param_f32 || per != 2) return cudaErrorNotSupported;
+            fn = p.layer_norm ? block_norm_stream_kernel<T, T, kLayer, 2, kWhole, true> : block_norm_stream_kernel<T, T, kRms, 2, kWhole, true>;
+        } else {
+            return cudaErrorNotSupported;
+        }
+    }
     const int slot = static_cast<int>(ring_row_bytes(p.K)) * (p.residual != nullptr ? 2 : 1);
     // CTAs an SM by its registers (4096 x 8960: 55 us, at 64 registers a thread for every kernel 78; 4481 x 4291: 49, 66)
     cudaFuncAttributes a;
@@ -623,6 +663,7 @@ cudaError_t block_norm_of(const BlockNormArgs& p, int num_sms, cudaStream_t stre
     const bool few = p.M < 2 * num_sms;
     const bool whole = p.K % 8 == 0 && (out & 15u) == 0;
     if (!few && fits_stream(p, whole)) return block_norm_stream<T>(p, whole, num_sms, stream);
+    if (p.polls != 0) return cudaErrorNotSupported;
     return ((in | out) & 15u) == 0 ? block_norm_rows<T, kMixed>(p, few, num_sms, stream) : block_norm_rows<T, kAny>(p, few, num_sms, stream);
 }
 

@@ -226,7 +226,7 @@ fmpq_status fp8_quantize_gemm_epilogue(const fp8_layer* L, const void* X, int32_
 
 // ---------------------------------------------------------------- between two blocks
 
-fmpq_status fmpq_block_norm(const fmpq_block_norm_args* args, void* stream) {
+static fmpq_status block_norm_args(const fmpq_block_norm_args* args, fmpq::BlockNormArgs& p) {
     if (args == nullptr) return FMPQ_ERR_INVALID_ARG;
     const fmpq_block_norm_args& a = *args;
     auto flag = [](int32_t v) { return v == 0 || v == 1; };
@@ -249,10 +249,7 @@ fmpq_status fmpq_block_norm(const fmpq_block_norm_args* args, void* stream) {
     for (const void* p : {a.post_weight, a.post_bias, a.weight, a.bias})
         if (!element_aligned(p, a.param_dtype)) return FMPQ_ERR_MISALIGNED;
     if (!element_aligned(a.gate, a.gate_dtype) || !all_aligned16(a.A_packed, a.a_scales)) return FMPQ_ERR_MISALIGNED;
-    int dev = -1, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return FMPQ_ERR_CUDA;
-    fmpq::BlockNormArgs p{};
+    p = fmpq::BlockNormArgs{};
     p.X = a.X;
     p.ldx = a.ldx;
     p.residual = a.residual;
@@ -284,7 +281,33 @@ fmpq_status fmpq_block_norm(const fmpq_block_norm_args* args, void* stream) {
     p.residual_scale = a.residual_scale;
     p.weight_offset = a.weight_offset;
     p.inv_count = 1.0f / static_cast<float>(a.K);
+    return FMPQ_OK;
+}
+static fmpq_status sms_of_device(int& sms) {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return FMPQ_ERR_CUDA;
+    return FMPQ_OK;
+}
+
+fmpq_status fmpq_block_norm(const fmpq_block_norm_args* args, void* stream) {
+    fmpq::BlockNormArgs p;
+    int sms = 0;
+    if (fmpq_status s = block_norm_args(args, p)) return s;
+    if (fmpq_status s = sms_of_device(sms)) return s;
     return launched(fmpq::launch_block_norm(p, sms, st(stream)));
+}
+
+fmpq_status fmpq_block_norm_fault_test(const fmpq_block_norm_args* args, int64_t withhold_row, uint32_t poll_limit, void* stream) {
+    fmpq::BlockNormArgs p;
+    int sms = 0;
+    if (fmpq_status s = block_norm_args(args, p)) return s;
+    if (withhold_row < 0 || withhold_row >= p.M || poll_limit < 1024) return FMPQ_ERR_INVALID_ARG;
+    if (fmpq_status s = sms_of_device(sms)) return s;
+    p.withheld = static_cast<int>(withhold_row);
+    p.polls = poll_limit;
+    const cudaError_t e = fmpq::launch_block_norm(p, sms, st(stream));
+    return e == cudaErrorNotSupported ? FMPQ_ERR_UNSUPPORTED_SHAPE : launched(e);
 }
 
 // ---------------------------------------------------------------- routing and experts

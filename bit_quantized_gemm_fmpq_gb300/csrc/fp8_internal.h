@@ -120,6 +120,8 @@ struct BlockNormArgs {
     int K, nb, dtype;
     int layer_norm, post_norm, pre_norm, param_f32, gate_f32;
     float eps, residual_scale, weight_offset, inv_count;   // inv_count: 1 / K
+    uint32_t polls;   // 0, or the failure-detection test: after how many polls a wait gives up, and the row that gets no copy
+    int withheld;
 };
 cudaError_t launch_block_norm(const BlockNormArgs& p, int num_sms, cudaStream_t stream);
 

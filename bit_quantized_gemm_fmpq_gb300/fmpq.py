@@ -86,6 +86,7 @@ SIGNATURES = {
     "fp8_gemm_epilogue": (_I32, [_P, _P, _P, _P, _P, _I64, _P, _P, _I32, _I64, _P, _SZ, _P]),
     "fp8_quantize_gemm_epilogue": (_I32, [_P, _P, _I32, _I64, _I64, _P, _P, _P, _P, _P, _P, _I64, _P, _SZ, _P]),
     "fmpq_block_norm": (_I32, [_P, _P]),
+    "fmpq_block_norm_fault_test": (_I32, [_P, _I64, ctypes.c_uint32, _P]),
     "moe_route": (_I32, [_P, _I32, _I64, _I64, _I32, _I32, _I32, _P, _I32, _I32, _I32, _I32, ctypes.c_float, _P, _P, _P]),
     "moe_rows": (_I64, [_I64, _I32, _I32]),
     "moe_plan_bytes": (_SZ, [_I64, _I32, _I32]),

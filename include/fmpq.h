@@ -565,6 +565,16 @@ typedef struct fmpq_block_norm_args {
  * other output may overlap an input. Y and codes need pre_norm; post_weight and post_bias need post_norm. */
 FMPQ_API fmpq_status fmpq_block_norm(const fmpq_block_norm_args* args, void* stream);
 
+/* Many rows come through copies that the kernel waits for. The call has no status word: should such a wait give up (within
+ * about a second; FMPQ_ERR_TIMEOUT of the calls that have one), that row and those that its CTA takes after it are NaN in R, Y and
+ * a_scales, and every other row is what it should be.
+ *
+ * Debug/test of that: fmpq_block_norm with the copy of row withhold_row of X left out and every wait bounded by poll_limit
+ * (>= 1024) polls. Nothing faults or hangs; the kernel waits, with a bound, for the copies under way. BF16 with weights of that type, at
+ * least 304 rows of a multiple of 8 channels, 512 to 16384, on 16-byte boundaries; else FMPQ_ERR_UNSUPPORTED_SHAPE. */
+FMPQ_API fmpq_status fmpq_block_norm_fault_test(const fmpq_block_norm_args* args, int64_t withhold_row, uint32_t poll_limit,
+                                                void* stream);
+
 /* ======================================================================================
  * Routing to experts, and the experts' products
  * ====================================================================================== */
