@@ -410,7 +410,7 @@ __device__ __noinline__ void give_up(const BlockNormArgs& p, int from, uint64_t*
         dev::mbar_wait(&landed[n % stages], (n / stages) & 1, nullptr, 1u << 16);
 }
 
-// A copy lands, or its wait gives up after about a second, a thread's last wait then. Threads may disagree, so the first row that any of them gave up counts: no
+// A copy lands, or its wait gives up after seconds, a thread's last wait then. Threads may disagree, so the first row that any of them gave up counts: no
 // slot is filled again from its barrier on, and at the end the CTA's rows from there on are made NaN and the copies under way land.
 // kTest: the row `withheld` gets no copy, and waits end after `polls`.
 template <typename T, typename P, int kNorm, int kV, int kLie, bool kTest = false>

@@ -13,7 +13,7 @@ namespace dev {
 constexpr int kStatusTimeout = 5;
 
 // Upper bound on polls of one mbarrier phase before a wait gives up. A legitimate wait in
-// these kernels lasts microseconds; this allows on the order of a second.
+// these kernels lasts microseconds; this allows about 8 seconds (a failing try_wait of a few warps returns after 2 us; of 32 warps sooner).
 constexpr uint32_t kMaxPolls = 1u << 22;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -46,7 +46,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 
 // Wait for the phase with the given parity to complete. Returns false if it did not
 // complete within max_polls polls, or if *abort (when given) became nonzero meanwhile.
-// Drains of copies in flight pass abort = nullptr so they always wait for completion.
+// Drains of copies in flight pass abort = nullptr so they always wait for completion; where a barrier counts more than its copies, mbar_drain.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const volatile int* abort,
                                           uint32_t max_polls = kMaxPolls) {
     for (uint32_t i = 0; i < max_polls; ++i) {
@@ -54,6 +54,12 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
         if (abort != nullptr && (i & 255u) == 255u && *abort) return false;
     }
     return false;
+}
+
+// Wait for a phase whose copies are in flight before their shared memory is given up. Once the CTA has given up (*abort), what else the barrier counts, an arrival of
+// the pair's other CTA, may never come: then a short bound, far longer than a copy. (With max_polls for each of a ring's barriers, a CTA took 95 s to end.)
+__device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity, const volatile int* abort, uint32_t max_polls = kMaxPolls) {
+    if (!mbar_wait(bar, parity, abort, max_polls)) mbar_wait(bar, parity, nullptr, 1u << 13);
 }
 
 // ---------------------------------------------------------------------------- cluster

@@ -103,11 +103,10 @@ __device__ __forceinline__ void weight_producer(const Params& p, Smem& s, uint32
         }
     }
     if (!ok && elect_one()) fail(p, abort_flag);
-    // the copies in flight must land before the CTA's shared memory is given up (after an abort the
-    // even CTA's readiness may never be complete: a short bound, far longer than a copy)
+    // the copies in flight must land before the CTA's shared memory is given up
     for (uint32_t k = 0; k < kStages && k < it; ++k) {
         const uint32_t i = it - 1 - k;
-        dev::mbar_wait(&s.ready[i % kRing], (i / kRing) & 1, nullptr, ok ? dev::kMaxPolls : 1u << 16);
+        dev::mbar_drain(&s.ready[i % kRing], (i / kRing) & 1, abort_flag);
     }
 }
 

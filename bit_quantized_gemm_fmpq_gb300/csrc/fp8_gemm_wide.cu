@@ -98,11 +98,10 @@ __device__ __forceinline__ void producer(const Params& p, const CUtensorMap* sca
         }
     }
     if (!ok) fail(p, abort_flag);
-    // the copies in flight must land before the CTA's shared memory is given up (after an abort the
-    // even CTA's readiness may never be complete: a short bound, far longer than a copy)
+    // the copies in flight must land before the CTA's shared memory is given up
     for (uint32_t k = 0; k < kStages && k < it; ++k) {
         const uint32_t i = it - 1 - k;
-        dev::mbar_wait(&s.full[i % kStages], (i / kStages) & 1, nullptr, ok ? dev::kMaxPolls : 1u << 16);
+        dev::mbar_drain(&s.full[i % kStages], (i / kStages) & 1, abort_flag);
     }
     for (uint32_t k = 0; k < kSlots && k < ch; ++k) {
         const uint32_t i = ch - 1 - k;

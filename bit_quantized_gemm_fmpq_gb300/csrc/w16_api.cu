@@ -150,6 +150,20 @@ fmpq_status w16_gemm(const w16_layer* L, const void* X, int64_t ldx, int64_t M, 
     return product(L, X, ldx, M, nullptr, W_packed, epilogue, nullptr, Y, dtype, ldy, workspace, workspace_bytes, stream);
 }
 
+fmpq_status w16_gemm_fault_test(const w16_layer* L, const void* X, int64_t ldx, int64_t M, const void* W_packed, void* Y, int64_t ldy,
+                                int32_t withhold_cta, int32_t withhold_copy, uint32_t poll_limit, void* stream) {
+    if (L == nullptr || L->experts != 1 || L->gated) return FMPQ_ERR_INVALID_ARG;
+    if (fmpq_status s = product_ok(L, X, ldx, M, W_packed, nullptr, nullptr, Y, L->dtype, ldy)) return s;
+    if (withhold_cta < 0 || withhold_copy < 0 || poll_limit < 1024) return FMPQ_ERR_INVALID_ARG;
+    if (!rows_aligned(X, ldx, M)) return FMPQ_ERR_MISALIGNED;
+    if (fmpq_status s = check_device(L)) return s;
+    fmpq::W16Args a = args_of(L, X, ldx, M, W_packed, nullptr, nullptr, Y, L->dtype, ldy);
+    a.polls = poll_limit;
+    a.withheld_cta = withhold_cta;
+    a.withheld_copy = withhold_copy;
+    return launched(fmpq::launch_w16_gemm(*L, a, st(stream)));
+}
+
 fmpq_status w16_grouped_gemm(const w16_layer* L, const void* X, int64_t ldx, int64_t rows, const int32_t* offsets, const void* W_packed,
                              const fmpq_epilogue* epilogue, const float* row_weight, void* Y, int32_t dtype, int64_t ldy,
                              void* workspace, size_t workspace_bytes, void* stream) {

@@ -79,6 +79,8 @@ struct Params {
     int units;           // dense: of this launch
     int others;          // bytes behind the operands' ring
     int32_t* status;
+    uint32_t polls;      // (kernels with kTest) after how many polls a wait gives up,
+    int withheld_cta, withheld_copy;   // and the copy of weights, counted from 0, that this CTA leaves out
 };
 
 struct Tables {
@@ -286,8 +288,11 @@ struct Place {
 };
 
 // ---------------------------------------------------------------- producer (warp 0)
+template <bool kTest>
 __device__ __forceinline__ void producer(const Params& p, const CUtensorMap* big, const CUtensorMap* small, Smem& s, uint8_t* ring,
                                          const Place& at, volatile int* abort_flag) {
+    const uint32_t polls = kTest ? p.polls : dev::kMaxPolls;
+    const bool withholds = kTest && static_cast<int>(blockIdx.x) == p.withheld_cta;
     const int units = unit_count(p, s);
     const uint32_t stages = s.tables.stages, stage_bytes = s.tables.stage_bytes;
     uint32_t it = 0, st = 0, phase = 1;
@@ -300,13 +305,13 @@ __device__ __forceinline__ void producer(const Params& p, const CUtensorMap* big
         const int from0 = t.part_row0(0) + static_cast<int>(at.rank) * half0, from1 = t.part_row0(1) + static_cast<int>(at.rank) * half1;
         const uint8_t* w = p.W + (((static_cast<int64_t>(t.e) * p.pairs + t.pair) * 2 + at.rank) * p.nb + t.b0) * kTileBytes;
         for (int b = t.b0; b < t.b1; ++b, ++it, w += kTileBytes) {
-            ok = __all_sync(0xFFFFFFFFu, dev::mbar_wait(&s.empty[st], phase, abort_flag));
+            ok = __all_sync(0xFFFFFFFFu, dev::mbar_wait(&s.empty[st], phase, abort_flag, polls));
             if (!ok) break;
             if (elect_one()) {
                 uint64_t* bar = &s.full[st];
                 uint8_t* to = ring + st * stage_bytes;
                 dev::mbar_arrive_expect_tx(bar, kTileBytes + (half0 + half1) * 128u);
-                dev::bulk_g2s(to, w, kTileBytes, bar);
+                if (!withholds || static_cast<int>(it) != p.withheld_copy) dev::bulk_g2s(to, w, kTileBytes, bar);
                 to += kTileBytes;
                 auto rows_to = [&](int half, int row) {
                     int i = 0;
@@ -325,11 +330,10 @@ __device__ __forceinline__ void producer(const Params& p, const CUtensorMap* big
         }
     }
     if (!ok && elect_one()) fail(p, abort_flag);
-    // the copies in flight must land before the CTA's shared memory is given up (after an abort the even CTA's
-    // readiness may never be complete: a short bound, far longer than a copy)
+    // the copies in flight must land before the CTA's shared memory is given up
     for (uint32_t k = 0; k < stages && k < it; ++k) {
         const uint32_t i = it - 1 - k;
-        dev::mbar_wait(&s.full[i % stages], (i / stages) & 1, nullptr, ok ? dev::kMaxPolls : 1u << 16);
+        dev::mbar_drain(&s.full[i % stages], (i / stages) & 1, abort_flag, polls);
     }
 }
 
@@ -357,8 +361,10 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar, uint32_t leader) {
         : "memory");
 }
 
+template <bool kTest>
 __device__ __forceinline__ void mma_issuer(const Params& p, Smem& s, uint8_t* ring, const Place& at, uint32_t tmem,
                                            volatile int* abort_flag) {
+    const uint32_t polls = kTest ? p.polls : dev::kMaxPolls;
     const uint32_t stages = s.tables.stages, stage_bytes = s.tables.stage_bytes;
     const int units = unit_count(p, s);
     const uint32_t remote = dev::mapa(&s.full[0], at.leader);
@@ -374,13 +380,13 @@ __device__ __forceinline__ void mma_issuer(const Params& p, Smem& s, uint8_t* ri
         const uint32_t acc = np & 1, d0 = tmem + acc * kPartRows, d1 = tmem + (acc ^ 1) * kPartRows;
         const uint32_t to1 = static_cast<uint32_t>(t.columns(0)) * 4;   // the second part's rows in a stage, in 16 bytes
         if (at.rank == 0) {
-            bool free = dev::mbar_wait(&s.acc_free[acc], ((np >> 1) & 1) ^ 1, abort_flag);
-            if (parts > 1) free = free && dev::mbar_wait(&s.acc_free[acc ^ 1], (((np + 1) >> 1) & 1) ^ 1, abort_flag);
+            bool free = dev::mbar_wait(&s.acc_free[acc], ((np >> 1) & 1) ^ 1, abort_flag, polls);
+            if (parts > 1) free = free && dev::mbar_wait(&s.acc_free[acc ^ 1], (((np + 1) >> 1) & 1) ^ 1, abort_flag, polls);
             ok = __all_sync(0xFFFFFFFFu, free);
             if (!ok) break;
         }
         for (int b = t.b0; b < t.b1; ++b) {
-            ok = __all_sync(0xFFFFFFFFu, dev::mbar_wait(&s.full[st], phase, abort_flag));
+            ok = __all_sync(0xFFFFFFFFu, dev::mbar_wait(&s.full[st], phase, abort_flag, polls));
             if (!ok) break;
             if (at.rank != 0) {
                 if (elect_one()) dev::mbar_arrive_remote(remote + st * 8u);
@@ -698,10 +704,11 @@ __device__ __forceinline__ void put_out_whole(const Params& p, float (*turn)[kCh
 // columns of one row: 8, or gate and up of 4 hidden channels. Where rows of Y or of the residual do not start on 8-byte boundaries
 // (FP32: 16) a thread has one column instead, of all 8 rows (gated: of 4), so that a warp's accesses are still neighbours. A chunk's
 // sums leave TMEM while the chunk before is put out.
-template <bool kGated, int kForm>
+template <bool kGated, int kForm, bool kTest>
 __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* others, const Place& at, int warp, int lane, uint32_t tmem,
                                          volatile int* abort_flag) {
     constexpr bool kWhole = kForm != kAnyForm;
+    const uint32_t polls = kTest ? p.polls : dev::kMaxPolls;
     constexpr int kCols = kGated ? 64 : 128;              // of this CTA
     constexpr int kW = kCols * kChunk / 128, kPieces = kCols / kW;
     constexpr int kColumnRows = 128 / kCols;              // rows that the threads cover at once, a column each
@@ -751,9 +758,9 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* other
             }
         }
         auto wait = [&] {
-            ok = ok && dev::mbar_wait(&s.acc_full[acc], (np >> 1) & 1, abort_flag);
+            ok = ok && dev::mbar_wait(&s.acc_full[acc], (np >> 1) & 1, abort_flag, polls);
             ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!kWhole && first && p.splits > 1 && ok) ok = __all_sync(0xFFFFFFFFu, dev::mbar_wait_cluster(&s.split_full, 0));
+            if (!kWhole && first && p.splits > 1 && ok) ok = __all_sync(0xFFFFFFFFu, dev::mbar_wait_cluster(&s.split_full, 0, polls));
             dev::tc_fence_after();
             return ok;
         };
@@ -857,10 +864,12 @@ __device__ __forceinline__ void epilogue(const Params& p, Smem& s, float4* other
             if (lane == 0 && ok) dev::mbar_arrive_remote_release(dev::mapa(&s.split_full, at.rank));
         }
     }
+    if (kForm == kWholeAdded) dev::cp_async_wait_all();   // (none is under way but after a wait that gave up)
     if (!ok && lane == 0) fail(p, abort_flag);
 }
 
-template <bool kGated, int kForm>
+// kTest: the failure-detection test (Params::polls); the others bound every wait by dev::kMaxPolls.
+template <bool kGated, int kForm, bool kTest = false>
 __global__ void __launch_bounds__(kThreads, 1)
 w16_kernel(const Params p, const __grid_constant__ CUtensorMap big, const __grid_constant__ CUtensorMap small) {
     extern __shared__ uint8_t smem_raw[];
@@ -913,11 +922,11 @@ w16_kernel(const Params p, const __grid_constant__ CUtensorMap big, const __grid
     volatile int* abort_flag = &s.abort_flag;
 
     if (warp == 0) {
-        producer(p, &big, &small, s, ring, at, abort_flag);
+        producer<kTest>(p, &big, &small, s, ring, at, abort_flag);
     } else if (warp == 1) {
-        mma_issuer(p, s, ring, at, tmem, abort_flag);
+        mma_issuer<kTest>(p, s, ring, at, tmem, abort_flag);
     } else if (warp >= 4) {
-        epilogue<kGated, kForm>(p, s, others, at, warp, lane, tmem, abort_flag);
+        epilogue<kGated, kForm, kTest>(p, s, others, at, warp, lane, tmem, abort_flag);
     }
     __syncwarp();
     dev::tc_fence_before();
@@ -1168,6 +1177,9 @@ cudaError_t launch_w16_gemm(const w16_layer& L, const W16Args& a, cudaStream_t s
     p.pairs = L.pairs;
     p.experts = L.experts;
     p.status = L.d_status;
+    p.polls = a.polls;
+    p.withheld_cta = a.withheld_cta;
+    p.withheld_copy = a.withheld_copy;
     CUtensorMap big, small;
     if (!w16::encode_rows(&big, a, L, w16::kBigBox) || !w16::encode_rows(&small, a, L, w16::kSmallBox)) return cudaErrorInvalidValue;
     auto launch = [&](const w16::Shape& s) {
@@ -1182,6 +1194,7 @@ cudaError_t launch_w16_gemm(const w16_layer& L, const W16Args& a, cudaStream_t s
                           : p.e.residual == nullptr ? w16::w16_kernel<gated.value, w16::kWholeBare> : w16::w16_kernel<gated.value, w16::kWholeAdded>;
         };
         auto fn = L.gated ? form(std::true_type{}) : form(std::false_type{});
+        if (a.polls != 0) fn = whole ? w16::w16_kernel<false, w16::kWholeBare, true> : w16::w16_kernel<false, w16::kAnyForm, true>;
         const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), w16::kSmemBytes);
         if (e != cudaSuccess) return e;
         p.others = s.others;
@@ -1200,6 +1213,7 @@ cudaError_t launch_w16_gemm(const w16_layer& L, const W16Args& a, cudaStream_t s
     p.cuts = rest.cuts;
     p.units = rest.units * rest.cuts;
     p.last_launch = 1;
+    p.withheld_cta = -1;
     return launch(w16::with_ring(rest.tile, rest.splits, p.units, p.units, ahead));
 }
 

@@ -30,6 +30,9 @@ struct W16Args {
     void* Y;                    // of type dtype: the layer's, or FP32
     int dtype;
     int64_t ldy;
+    // 0, or the failure-detection test (a plain layer without an epilogue): polls before a wait gives up, and the copy of weights that a CTA leaves out
+    uint32_t polls;
+    int withheld_cta, withheld_copy;
 };
 cudaError_t launch_w16_gemm(const w16_layer& L, const W16Args& a, cudaStream_t stream);
 cudaError_t launch_w16_pack(const w16_layer& L, int expert, const void* W, int64_t ld_n, int64_t ld_k, void* Wp, cudaStream_t stream);

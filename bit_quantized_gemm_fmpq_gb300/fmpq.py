@@ -105,6 +105,7 @@ SIGNATURES = {
     "w16_pack_weights": (_I32, [_P, _I32, _P, _I64, _I64, _P, _P]),
     "w16_workspace_bytes": (_SZ, [_P, _P, _I64, _I64]),
     "w16_gemm": (_I32, [_P, _P, _I64, _I64, _P, _P, _P, _I32, _I64, _P, _SZ, _P]),
+    "w16_gemm_fault_test": (_I32, [_P, _P, _I64, _I64, _P, _P, _I64, _I32, _I32, ctypes.c_uint32, _P]),
     "w16_grouped_gemm": (_I32, [_P, _P, _I64, _I64, _P, _P, _P, _P, _P, _I32, _I64, _P, _SZ, _P]),
     "w16_experts_workspace_bytes": (_SZ, [_P, _P, _I64, _I64, _I32, _I32]),
     "w16_experts_gemm": (_I32, [_P, _P, _I64, _I32, _P, _I64, _I32, _P, _P, _P, _P, _I32, _I64, _P, _SZ, _P]),

@@ -565,8 +565,8 @@ typedef struct fmpq_block_norm_args {
  * other output may overlap an input. Y and codes need pre_norm; post_weight and post_bias need post_norm. */
 FMPQ_API fmpq_status fmpq_block_norm(const fmpq_block_norm_args* args, void* stream);
 
-/* Many rows come through copies that the kernel waits for. The call has no status word: should such a wait give up (within
- * about a second; FMPQ_ERR_TIMEOUT of the calls that have one), that row and those that its CTA takes after it are NaN in R, Y and
+/* Many rows come through copies that the kernel waits for. The call has no status word: should such a wait give up (after
+ * seconds; FMPQ_ERR_TIMEOUT of the calls that have one), that row and those that its CTA takes after it are NaN in R, Y and
  * a_scales, and every other row is what it should be.
  *
  * Debug/test of that: fmpq_block_norm with the copy of row withhold_row of X left out and every wait bounded by poll_limit
@@ -679,6 +679,11 @@ FMPQ_API size_t w16_workspace_bytes(const w16_layer* layer, const void* X, int64
 FMPQ_API fmpq_status w16_gemm(const w16_layer* layer, const void* X, int64_t ldx, int64_t M, const void* W_packed,
                               const fmpq_epilogue* epilogue, void* Y, int32_t dtype, int64_t ldy, void* workspace,
                               size_t workspace_bytes, void* stream);
+/* Debug/test of failure detection: w16_gemm of a plain layer, X on 16-byte boundaries, no epilogue, with the copy of weights number withhold_copy of the
+ * thread block withhold_cta left out and every device wait bounded by poll_limit (>= 1024) polls. Waits that depend on it run out, the blocks wait (with a bound)
+ * for the copies they did issue and release TMEM; the call records FMPQ_ERR_TIMEOUT (w16_device_status) and Y is unspecified. Nothing faults or hangs. */
+FMPQ_API fmpq_status w16_gemm_fault_test(const w16_layer* layer, const void* X, int64_t ldx, int64_t M, const void* W_packed, void* Y, int64_t ldy,
+                                         int32_t withhold_cta, int32_t withhold_copy, uint32_t poll_limit, void* stream);
 /* The rows of X [rows][ldx] in groups, one for each expert: expert e has rows offsets[e] .. offsets[e + 1] - 1 (int32
  * [experts + 1], on the device; cut to [0, rows]; a group that ends before it starts is empty, and a row that offsets which fall back
  * would put into two groups is the first's). Rows of no group are left as they were in Y. row_weight: fp32 [rows] or NULL (1). */
