@@ -904,8 +904,10 @@ w16_kernel(const Params p, const __grid_constant__ CUtensorMap big, const __grid
     }
     if (warp == 2) dev::tmem_alloc_pair(&s.tmem_base, 512);
     // (launched as the programmatic dependent of whatever is before it: everything up to here runs under that one's end. The rest
-    // of a product needs nothing of the launch before it, which lets it start once it has waited for the one before that; it sees
-    // what that one wrote, and ends behind the launch before it.)
+    // of a product works before it waits for the launch before it, the full rounds. Two conditions make that sound: every thread of the full rounds
+    // triggers behind its own wait, so that all before them is done and seen when the rest starts; and the rest reads nothing that they write,
+    // and writes other units. Its own wait and trigger come last, so whatever is launched behind it finds both done. A trigger ahead of the wait here, or a rest
+    // that reads an output of the full rounds, would be a race.)
     if (p.last_launch) {
         __threadfence();
     } else {
