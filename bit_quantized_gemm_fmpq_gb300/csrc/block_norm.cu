@@ -174,8 +174,8 @@ __device__ __forceinline__ void square8(const BlockNormArgs& p, float2& sum, con
         sum = dev::ffma2(d, d, sum);
     }
 }
-// 1 / sqrt(mean square + eps), rounded once: all of a row's values carry its error, and rsqrtf, off by up to two steps, flips twice as many E4M3
-// codes at their borders. One step of Newton's iteration from rsqrtf's y, y + y / 2 (1 - d y^2), d y in two parts so that the residual is
+// 1 / sqrt(mean square + eps), rounded once: all of a row's values carry its error. (rsqrtf, off by up to two steps: 45 of 33 million E4M3 codes and 686 of as many
+// bf16 values of r are not those of 64 bits, in the mean of six inputs; this: 39 and 621, as FP32's correctly rounded root and quotient, 42 and 630.) One step of Newton's iteration from rsqrtf's y, y + y / 2 (1 - d y^2), d y in two parts so that the residual is
 // good to 2^-46: the result is within 2^-20 of a step of the nearest value's half step (of all 2^31 positive d, 257 next to a tie go to its other side). Both norms
 // at 4096 x 8192: 66.4 us; with __frsqrt_rn, which has no such exceptions and three times the instructions, 67.4; with rsqrtf alone 65.6.
 __device__ __forceinline__ float inverse(const BlockNormArgs& p, float mean_square) {
@@ -371,8 +371,8 @@ __host__ __device__ inline uint32_t ring_row_bytes(int K) { return ((static_cast
 
 // Many rows: the CTAs stay, and the next rows are on their way into a ring in shared memory (bulk copies) while one is worked on. Two vectors
 // a thread (three, or four, where 1024 threads would not do: 2048 x 24576 85 us with three, 102 with four). Its instructions and the chain of a row through its barriers bound it (4096 x 8192 bf16,
-// both norms, a gate, codes: 64 us, 236 MB = 3.7 TB/s, an issue slot used in 63 of 100; one norm and the residual 43; the sum alone 30, the
-// copy rate), so what can be is uniform or made once: a row's addresses are a base for the CTA and 32-bit offsets of a thread, arithmetic is
+// both norms, a gate, codes: 66.6 us, 236 MB = 3.5 TB/s, an issue slot used in 64 of 100; one norm and the residual 46; the sum alone 32.5,
+// 6.2 TB/s), so what can be is uniform or made once: a row's addresses are a base for the CTA and 32-bit offsets of a thread, arithmetic is
 // on pairs, P (the weights' type) and the norm are the compiler's. One CTA a row without the ring took 138. No faster: four vectors a thread
 // (70), three CTAs of 40 registers in place of two, the weights in shared memory (which leave the ring two rows) or asked for before the sums,
 // all within 1 us; without the codes' stores, the scales' or the reduction of a block's maximum it would still take within 1 us of this.
