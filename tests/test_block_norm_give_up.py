@@ -79,3 +79,19 @@ def test_the_hook_refuses(fmpq_mod):  # noqa: F811
         assert call(**kw) == code, kw
     torch.cuda.synchronize()
     assert bool((R == 7).all()) and bool((Y == 7).all())
+
+
+def test_the_hook_refuses_before_a_device():
+    """(No GPU.) Arguments, the row and the bound of polls."""
+    from bit_quantized_gemm_fmpq_gb300 import build, fmpq
+    build.build()
+    lib = fmpq.load_library()
+    a = fmpq.BlockNormArgs(X=4096, ldx=512, M=400, K=512, Y=8192, ldy=512, eps=1e-6, residual_scale=1.0, pre_norm=1, dtype=1, param_dtype=1)
+    at = ctypes.addressof(a)
+    assert lib.fmpq_block_norm_fault_test(None, 0, 1 << 14, None) == 1
+    for row, polls in [(-1, 1 << 14), (400, 1 << 14), (1 << 40, 1 << 14), (0, 0), (0, 1023)]:
+        assert lib.fmpq_block_norm_fault_test(at, row, polls, None) == 1
+    a.ldx = 511
+    assert lib.fmpq_block_norm_fault_test(at, 0, 1 << 14, None) == 2
+    a.ldx, a.X = 512, 4097
+    assert lib.fmpq_block_norm_fault_test(at, 0, 1 << 14, None) == 3

@@ -52,3 +52,9 @@ def test_the_hook_refuses(fmpq_mod):  # noqa: F811
         assert call(**kw) == code, kw
     torch.cuda.synchronize()
     assert bool((Y == 7).all()) and fmpq_mod.w16_device_status(plain) == 0
+
+
+def test_the_hook_refuses_without_a_layer():
+    from bit_quantized_gemm_fmpq_gb300 import build, fmpq
+    build.build()
+    assert fmpq.load_library().w16_gemm_fault_test(None, 4096, 8, 1, 4096, 4096, 8, 0, 0, 1 << 14, None) == 1
